@@ -311,6 +311,94 @@ int tp_ln_residual_backward(const tpmlp_bf16* dX, const tpmlp_bf16* dres, const 
                             float* dbeta, float* partial, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* LayerNorm without a residual (the final norm)                           */
+/* ---------------------------------------------------------------------- */
+
+/* Element type of the calls that take one. */
+enum tpmlp_dtype { TPMLP_BF16 = 0, TPMLP_FP16 = 1, TPMLP_FP32 = 2 };
+
+/* The norm between the last layer and the output head.  Per row of h values:
+ *   mu = mean(x) ; var = mean((x - mu)^2) (biased)
+ *   y = (x - mu) / sqrt(var + eps) * gamma + beta
+ * In:  x [T,h], gamma, beta [h] of `dtype`, eps > 0.
+ * Out: y [T,h] of `dtype`; mean, rstd [T] float32 (rstd = 1/sqrt(var+eps)),
+ *      saved for the backward pass.
+ * Rules: T >= 0, h >= 1 (any h: rows need not start on 16-byte boundaries;
+ * h % 8 == 0, or h % 4 == 0 in float32, is faster), dtype one of the three.
+ * Statistics are float32 in every type.  x, gamma, beta and y are 16-byte
+ * aligned, mean and rstd 4-byte aligned. */
+int tp_ln_forward(const void* x, const void* gamma, const void* beta, int T, int h, int dtype,
+                  float eps, void* y, float* mean, float* rstd, void* stream);
+
+/* Float32 elements of partial-sum scratch tp_ln_backward needs. */
+size_t tp_ln_backward_workspace_floats(int T, int h, int dtype);
+
+/* Backward pass of tp_ln_forward:
+ *   xhat = (x - mu) rstd ; g = dy * gamma
+ *   dx = rstd (g - mean(g) - xhat mean(g xhat))
+ *   dgamma = sum_rows dy xhat ; dbeta = sum_rows dy   (float32, deterministic)
+ * In:  dy, x [T,h], gamma [h] of `dtype`; mean, rstd [T] from the forward pass.
+ * Out: dx [T,h] of `dtype`; dgamma, dbeta [h] (float32; zeros when T == 0).
+ * `partial` (16-byte aligned) holds tp_ln_backward_workspace_floats(T, h,
+ * dtype) floats, any contents. */
+int tp_ln_backward(const void* dy, const void* x, const void* gamma, const float* mean,
+                   const float* rstd, int T, int h, int dtype, void* dx, float* dgamma,
+                   float* dbeta, float* partial, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Output head: vocabulary projection and softmax cross entropy            */
+/* ---------------------------------------------------------------------- */
+
+/* "Megatron-LM: Tensor Model Parallel" (charles2530.github.io) ends the model
+ * with the projection onto the vocabulary by the embedding matrix, split by
+ * vocabulary rows, and a cross entropy that is fused with it so that no rank
+ * holds or exchanges the logits: each shard contributes its maximum, its sum
+ * of exponentials and the target's logit.  Here the shards are tiles of one
+ * GEMM: with X [T,h] (one row a token), W [V,h] and target y_t,
+ *   z[t,v]  = sum_j X[t,j] W[v,j]
+ *   lse[t]  = log sum_v exp(z[t,v])
+ *   loss[t] = lse[t] - z[t,y_t]
+ * and the logits z are never stored.  loss is computed as
+ * log(1 + sum_{v != y} exp(z[t,v] - z[t,y])), which keeps its relative
+ * precision where the model is sure of the target.
+ * targets [T] (int64): a negative target marks a token that does not count
+ * (loss 0, no gradient; its lse is still written).  A target >= V has no
+ * logit: its loss is NaN, and so are the gradients it reaches.
+ * X and W must be finite (a row of X that does not count included).
+ * Rules: T >= 0, h >= 8, h % 8 == 0, 1 <= V <= 2^30 (any V).  X, W, dX, dW and
+ * the workspace are 16-byte aligned, targets 8-byte, the rest 4-byte. */
+
+/* Bytes of scratch tp_head_loss_forward needs (the row statistics of each
+ * tile of the vocabulary: 16 T ceil(V/256)). */
+size_t tp_head_loss_forward_workspace_bytes(int T, int h, int V);
+
+/* In: X [T,h], W [V,h] (bf16), targets [T].  Out: loss, lse [T] (float32).
+ * The workspace is required; its contents on entry do not matter. */
+int tp_head_loss_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const int64_t* targets, int T,
+                         int h, int V, float* loss, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Scratch of tp_head_loss_backward: what it uses at most, and the least it
+ * runs with.  The backward pass goes through the vocabulary in pieces and
+ * keeps one piece's bf16 logit gradients at a time (at most 512 MiB); a
+ * smaller workspace means narrower pieces, down to 256 columns. */
+size_t tp_head_loss_backward_workspace_bytes(int T, int h, int V);
+size_t tp_head_loss_backward_min_workspace_bytes(int T, int h, int V);
+
+/* Backward pass given dloss [T] (float32), the gradient of each token's loss
+ * (1 / tokens counted, for a mean):
+ *   dz[t,v] = dloss[t] (exp(z[t,v] - lse[t]) - [v == y_t])
+ *   dX = dz W ; dW = dz^T X
+ * The logits are computed again.  dz is rounded to bf16 relative to the
+ * largest |dloss|, which multiplies the float32 sums.
+ * In: dloss, targets, lse [T], X, W.  Out: dX [T,h], dW [V,h] (bf16; dW zeros
+ * when T == 0).  Every sum has a fixed order: results are reproducible. */
+int tp_head_loss_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
+                          const int64_t* targets, const float* lse, int T, int h, int V,
+                          tpmlp_bf16* dX, tpmlp_bf16* dW, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Activation recompute                                                    */
 /* ---------------------------------------------------------------------- */
 

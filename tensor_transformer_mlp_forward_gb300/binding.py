@@ -82,6 +82,14 @@ _SIGNATURES = {
     "tp_ln_residual_forward": ([_P] * 4 + [_I, _I, ctypes.c_float] + [_P] * 4 + [_P], _I),
     "tp_ln_residual_backward_workspace_floats": ([_I, _I], _S),
     "tp_ln_residual_backward": ([_P] * 7 + [_I, _I] + [_P] * 4 + [_P], _I),
+    "tp_ln_forward": ([_P] * 3 + [_I] * 3 + [ctypes.c_float] + [_P] * 3 + [_P], _I),
+    "tp_ln_backward_workspace_floats": ([_I] * 3, _S),
+    "tp_ln_backward": ([_P] * 5 + [_I] * 3 + [_P] * 4 + [_P], _I),
+    "tp_head_loss_forward_workspace_bytes": ([_I] * 3, _S),
+    "tp_head_loss_forward": ([_P] * 3 + [_I] * 3 + [_P] * 2 + [_P, _S, _P], _I),
+    "tp_head_loss_backward_workspace_bytes": ([_I] * 3, _S),
+    "tp_head_loss_backward_min_workspace_bytes": ([_I] * 3, _S),
+    "tp_head_loss_backward": ([_P] * 5 + [_I] * 3 + [_P] * 2 + [_P, _S, _P], _I),
     "tp_attn_qkv": ([_P] * 3 + [_I] * 2 + [_P, _P], _I),
     "tp_attn_core_workspace_bytes": ([_I] * 4, _S),
     "tp_attn_core_forward": ([_P] + [_I] * 4 + [_P] * 2 + [_P, _S, _P], _I),
@@ -602,6 +610,123 @@ def tp_ln_residual_backward(dX, dres, a, r, gamma, mean, rstd, ds=None, dgamma=N
         _ptr(dbeta, "dbeta", (h,), torch.float32), _ptr(partial, "partial", None, torch.float32),
         _stream(stream)))
     return ds, dgamma, dbeta
+
+
+# ------------------------------------- final LayerNorm and the output head
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _one_device(*tensors):
+    """All tensors on the current device: the library launches there."""
+    for x in tensors:
+        if x is not None and x.is_cuda and x.device.index != torch.cuda.current_device():
+            raise ValueError(f"a tensor is on {x.device}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+
+
+def _new(x, shape, like: torch.Tensor, dtype, stream):
+    """The caller's tensor, or a fresh one from the memory pool of the stream
+    that will write it (so that freeing it cannot hand it to another one)."""
+    if x is not None:
+        return x
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _dtype_of(x, name: str) -> int:
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    return _DTYPES[x.dtype]
+
+
+def tp_ln_forward(x, gamma, beta, eps: float = 1e-5, y=None, mean=None, rstd=None, stream=None):
+    """y, mean, rstd of y = LayerNorm(x) * gamma + beta, x [T, h] in bfloat16,
+    float16 or float32 (mean and rstd [T] are float32)."""
+    T, h = x.shape
+    dt = _dtype_of(x, "x")
+    _one_device(x, gamma, beta, y, mean, rstd)
+    y = _new(y, (T, h), x, x.dtype, stream)
+    mean = _new(mean, (T,), x, torch.float32, stream)
+    rstd = _new(rstd, (T,), x, torch.float32, stream)
+    _check("tp_ln_forward", lib().tp_ln_forward(
+        _ptr(x, "x", (T, h), x.dtype), _ptr(gamma, "gamma", (h,), x.dtype),
+        _ptr(beta, "beta", (h,), x.dtype), T, h, dt, eps, _ptr(y, "y", (T, h), x.dtype),
+        _ptr(mean, "mean", (T,), torch.float32), _ptr(rstd, "rstd", (T,), torch.float32),
+        _stream(stream)))
+    return y, mean, rstd
+
+
+def tp_ln_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, partial=None,
+                   stream=None):
+    """dx (of x's type), dgamma, dbeta (float32) of tp_ln_forward."""
+    T, h = x.shape
+    dt = _dtype_of(x, "x")
+    _one_device(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, partial)
+    dx = _new(dx, (T, h), x, x.dtype, stream)
+    dgamma = _new(dgamma, (h,), x, torch.float32, stream)
+    dbeta = _new(dbeta, (h,), x, torch.float32, stream)
+    need = int(lib().tp_ln_backward_workspace_floats(T, h, dt))
+    partial = _new(partial, (max(1, need),), x, torch.float32, stream)
+    if partial.numel() < need:
+        raise ValueError(f"partial holds {partial.numel()} floats, {need} needed")
+    _check("tp_ln_backward", lib().tp_ln_backward(
+        _ptr(dy, "dy", (T, h), x.dtype), _ptr(x, "x", (T, h), x.dtype),
+        _ptr(gamma, "gamma", (h,), x.dtype), _ptr(mean, "mean", (T,), torch.float32),
+        _ptr(rstd, "rstd", (T,), torch.float32), T, h, dt, _ptr(dx, "dx", (T, h), x.dtype),
+        _ptr(dgamma, "dgamma", (h,), torch.float32), _ptr(dbeta, "dbeta", (h,), torch.float32),
+        _ptr(partial, "partial", None, torch.float32), _stream(stream)))
+    return dx, dgamma, dbeta
+
+
+def tp_head_loss_forward(X, W, targets, loss=None, lse=None, workspace=None, stream=None):
+    """loss, lse [T] (float32) of the softmax cross entropy of X W^T against
+    targets [T] (int64; negative: the token does not count).  X [T, h], W [V,
+    h] bfloat16; the logits are not stored."""
+    T, h = X.shape
+    V = W.shape[0]
+    _one_device(X, W, targets, loss, lse, workspace)
+    loss = _new(loss, (T,), X, torch.float32, stream)
+    lse = _new(lse, (T,), X, torch.float32, stream)
+    need = int(lib().tp_head_loss_forward_workspace_bytes(T, h, V))
+    workspace = _new(workspace, (max(need, 16),), X, torch.uint8, stream)
+    _check("tp_head_loss_forward", lib().tp_head_loss_forward(
+        _ptr(X, "X", (T, h)), _ptr(W, "W", (V, h)), _ptr(targets, "targets", (T,), torch.int64),
+        T, h, V, _ptr(loss, "loss", (T,), torch.float32), _ptr(lse, "lse", (T,), torch.float32),
+        _ptr(workspace, "workspace", None, torch.uint8), workspace.numel(), _stream(stream)))
+    return loss, lse
+
+
+def head_loss_backward_workspace_bytes(T: int, h: int, V: int) -> int:
+    return int(lib().tp_head_loss_backward_workspace_bytes(T, h, V))
+
+
+def head_loss_backward_min_workspace_bytes(T: int, h: int, V: int) -> int:
+    """The least workspace tp_head_loss_backward runs with (the vocabulary in
+    pieces of 256 columns)."""
+    return int(lib().tp_head_loss_backward_min_workspace_bytes(T, h, V))
+
+
+def tp_head_loss_backward(dloss, X, W, targets, lse, dX=None, dW=None, workspace=None, stream=None):
+    """dX [T, h], dW [V, h] (bfloat16) of tp_head_loss_forward given dloss [T]
+    (float32) and the forward pass's lse."""
+    T, h = X.shape
+    V = W.shape[0]
+    _one_device(dloss, X, W, targets, lse, dX, dW, workspace)
+    dX = _new(dX, (T, h), X, torch.bfloat16, stream)
+    dW = _new(dW, (V, h), X, torch.bfloat16, stream)
+    workspace = _new(workspace, (max(head_loss_backward_workspace_bytes(T, h, V), 16),), X,
+                     torch.uint8, stream)
+    _check("tp_head_loss_backward", lib().tp_head_loss_backward(
+        _ptr(dloss, "dloss", (T,), torch.float32), _ptr(X, "X", (T, h)), _ptr(W, "W", (V, h)),
+        _ptr(targets, "targets", (T,), torch.int64), _ptr(lse, "lse", (T,), torch.float32),
+        T, h, V, _ptr(dX, "dX", (T, h)), _ptr(dW, "dW", (V, h)),
+        _ptr(workspace, "workspace", None, torch.uint8), workspace.numel(), _stream(stream)))
+    return dX, dW
 
 
 def selftest_bounded_wait(timeout_us: int, stream=None) -> int:

@@ -367,6 +367,7 @@ struct Output {
     void* ptr1;
     long long rows, cols;
     int k_splits;  // > 1: ptr0 is an fp32 [k_splits, rows, cols] partial-sum workspace
+    bool partial = false;  // the same with one split
 };
 
 // ------------------------------------------------------------ tail split
@@ -519,7 +520,7 @@ int run_gemm(Launcher fn, const Operand& a, const Operand& b, const Output& out,
     if (rc) return rc;
     rc = operand_map(&maps.b, fb, f.t, pair ? tile_n / 2 : BN, &g.b_mn4);
     if (rc) return rc;
-    if (out.k_splits > 1)
+    if (out.k_splits > 1 || out.partial)
         rc = make_partial_map(&maps.o0, out.ptr0, out.rows, out.cols, out.k_splits);
     else
         rc = make_map(&maps.o0, out.ptr0, out.rows, out.cols, o_t, g.o_on, 32);
@@ -1648,6 +1649,54 @@ TPMLP_API int tp_ln_residual_backward(const tpmlp_bf16* dX, const tpmlp_bf16* dr
     return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
 }
 
+// ---------------------------------------------- LayerNorm without a residual
+
+static int check_norm(int T, int h, int dtype) {
+    if (T < 0 || h < 1 || dtype < TPMLP_BF16 || dtype > TPMLP_FP32) return TPMLP_ERR_SHAPE;
+    return TPMLP_OK;
+}
+
+TPMLP_API int tp_ln_forward(const void* x, const void* gamma, const void* beta, int T, int h,
+                            int dtype, float eps, void* y, float* mean, float* rstd, void* stream) {
+    TPMLP_PROLOGUE(check_norm(T, h, dtype));
+    if (!(eps > 0.0f)) return TPMLP_ERR_SHAPE;
+    if (any_null(gamma, beta) || (T > 0 && any_null(x, y, mean, rstd))) return TPMLP_ERR_NULL;
+    if (!all_aligned(x, gamma, beta, y)) return TPMLP_ERR_ALIGN;
+    if (T == 0) return TPMLP_OK;
+    DeviceInfo d;
+    if (int rc = enter(d)) return rc;
+    cudaError_t e = launch_norm_forward(dtype, x, gamma, beta, T, h, eps, y, mean, rstd,
+                                        static_cast<cudaStream_t>(stream), &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+TPMLP_API size_t tp_ln_backward_workspace_floats(int T, int h, int dtype) {
+    if (check_norm(T, h, dtype)) return 0;
+    return 2 * static_cast<size_t>(norm_param_chunks(T, h)) * static_cast<size_t>(h);
+}
+
+TPMLP_API int tp_ln_backward(const void* dy, const void* x, const void* gamma, const float* mean,
+                             const float* rstd, int T, int h, int dtype, void* dx, float* dgamma,
+                             float* dbeta, float* partial, void* stream) {
+    TPMLP_PROLOGUE(check_norm(T, h, dtype));
+    if (any_null(gamma, dgamma, dbeta) || (T > 0 && any_null(dy, x, mean, rstd, dx, partial)))
+        return TPMLP_ERR_NULL;
+    if (!all_aligned(dy, x, gamma, dx, dgamma, dbeta, partial)) return TPMLP_ERR_ALIGN;
+    DeviceInfo d;
+    if (int rc = enter(d)) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (T == 0) {
+        if ((e = cudaMemsetAsync(dgamma, 0, sizeof(float) * static_cast<size_t>(h), st)) != cudaSuccess ||
+            (e = cudaMemsetAsync(dbeta, 0, sizeof(float) * static_cast<size_t>(h), st)) != cudaSuccess)
+            return fail_cuda(e);
+        return TPMLP_OK;
+    }
+    e = launch_norm_backward(dtype, dy, x, gamma, mean, rstd, T, h, dx, dgamma, dbeta, partial, st,
+                             &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
 // ---------------------------------------------- head-parallel attention
 
 namespace tpmlp {
@@ -1930,6 +1979,234 @@ TPMLP_API int tp_attn_backward(const tpmlp_bf16* dY, const tpmlp_bf16* X, const 
     // dX = sum_i dQKV_i Wqkv_i^T: the f-operator sum as one accumulation over
     // all 3h columns
     return dx_gemm(dQKV, Wqkv, T, h, 3 * h, 1, dX, ws + L.split, L.total - L.split, st, d);
+}
+
+// ------------------------------------------------------------- output head
+
+namespace tpmlp {
+namespace {
+
+int check_head(int T, int h, int V) {
+    if (T < 0 || h < 8 || h % 8 != 0 || V < 1 || V > (1 << 30)) return TPMLP_ERR_SHAPE;
+    if (cdiv(T, BM) * cdiv(V, BN) >= (1LL << 31)) return TPMLP_ERR_SHAPE;
+    return TPMLP_OK;
+}
+
+// Column parts of the forward's row statistics: one for each epilogue half
+// of each 256-column tile at most.
+size_t head_forward_bytes(int T, int V) {
+    return sizeof(float2) * static_cast<size_t>(2 * cdiv(V, BN)) * static_cast<size_t>(T);
+}
+
+// Bytes of the logits' gradient kept at a time (a piece of the vocabulary).
+constexpr long long kHeadPieceBytes = 512LL << 20;
+constexpr int kHeadMaxSplits = 64;
+
+// Splits of dX's reduction over a piece of total_kb k-blocks: the number
+// with the least estimated time -- rounds of a tile's share at a CTA's (pair's)
+// rate, plus each plane's fp32 write and read at DRAM speed -- as
+// choose_row_splits, but up to 64: one row of tiles over a whole vocabulary
+// is the usual case at few tokens.
+int choose_head_splits(int T, int h, long long total_kb) {
+    const bool pair = cdiv(T, 2 * BM) * cdiv(h, BN) >= kPairMinTiles;
+    const long long tiles = cdiv(T, pair ? 2 * BM : BM) * cdiv(h, BN);
+    const int units = pair ? kSizingPairs : 2 * kSizingPairs;
+    const double tile_ns = 2.0 * 2 * BM * BN * BK * static_cast<double>(total_kb) /
+                           (2.0 * 8192.0 * 2.07 * kSustainedRateRatio);
+    double best = 0.0;
+    int best_s = 1;
+    for (int sp = 1; sp <= kHeadMaxSplits && (sp == 1 || total_kb / sp >= 4); ++sp) {
+        const double c = static_cast<double>(cdiv(tiles * sp, units)) * tile_ns / sp +
+                         (sp > 1 ? 4000.0 + 8.0 * sp * T * static_cast<double>(h) / 6500.0 : 0.0);
+        if (sp == 1 || c < best) {
+            best = c;
+            best_s = sp;
+        }
+    }
+    return best_s;
+}
+
+// The backward pass: the vocabulary in pieces of `width` columns (a multiple
+// of 64), dX over `splits` k ranges of a piece.  With one piece and no split
+// dX is stored by the GEMM; otherwise it is summed in `splits` fp32 planes.
+struct HeadPlan {
+    int width, splits;
+    bool planes;
+    size_t info, scale, plane, dz, total;  // byte offsets, and the whole
+};
+
+HeadPlan head_layout(int T, int h, int V, int width, int splits) {
+    HeadPlan p;
+    p.width = width;
+    p.splits = splits;
+    p.planes = splits > 1 || width < V;
+    p.info = 0;
+    p.scale = align256(sizeof(float4) * static_cast<size_t>(T));
+    p.plane = p.scale + 256;
+    p.dz = align256(p.plane + (p.planes ? sizeof(float) * static_cast<size_t>(splits) * T * h : 0));
+    p.total = align256(p.dz + sizeof(uint16_t) * static_cast<size_t>(T) * width);
+    return p;
+}
+
+int round_up(long long x, long long m) { return static_cast<int>(cdiv(x, m) * m); }
+
+HeadPlan head_plan(int T, int h, int V) {
+    const long long pieces = std::max<long long>(1, cdiv(2LL * T * V, kHeadPieceBytes));
+    const int width = pieces == 1 ? round_up(V, 64) : round_up(cdiv(V, pieces), BN);
+    return head_layout(T, h, V, width, choose_head_splits(T, h, width / BK));
+}
+
+// The narrowest pieces: one column tile at a time.
+HeadPlan head_plan_least(int T, int h, int V) {
+    return head_layout(T, h, V, std::min(round_up(V, 64), BN), 1);
+}
+
+// The plan that fits the caller's workspace: the full one, or else one plane
+// and the widest pieces that fit.
+bool head_plan_for(int T, int h, int V, size_t bytes, HeadPlan& p) {
+    p = head_plan(T, h, V);
+    if (p.total <= bytes) return true;
+    p = head_plan_least(T, h, V);
+    if (p.total > bytes) return false;
+    const long long cols = static_cast<long long>((bytes - p.dz) / (2 * static_cast<size_t>(T)));
+    int width = static_cast<int>(std::min<long long>(round_up(V, 64), cols)) / BN * BN;
+    for (; width > p.width; width -= BN) {
+        const HeadPlan w = head_layout(T, h, V, width, 1);
+        if (w.total <= bytes) {
+            p = w;
+            break;
+        }
+    }
+    return true;
+}
+
+int head_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const long long* targets, int T, int h,
+                 int V, float* loss, float* lse, void* ws, cudaStream_t st, const DeviceInfo& d) {
+    GemmArgs g = blank_args();
+    const GemmShape sh{T, V, h, 1, SHARD_N, 1LL * T * h, 1LL * V * h};
+    g.targets = targets;
+    g.lse_part = static_cast<float2*>(ws);
+    Operand a{X, T, h, ON_NONE, false};
+    Operand b{W, V, h, ON_NONE, false};
+    Output o{const_cast<tpmlp_bf16*>(X), nullptr, T, h, 1};  // a map that nothing is stored through
+    if (int rc = run_gemm(launch_head_lse, a, b, o, g, sh, st, d)) return rc;
+    const int parts = g.n_tiles * (g.epi_warps / 4);
+    cudaError_t e = launch_head_combine(g.lse_part, parts, cb(X), cb(W), targets, T, h, V, loss, lse,
+                                        st, &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
+                  const long long* targets, const float* lse, int T, int h, int V, tpmlp_bf16* dX,
+                  tpmlp_bf16* dW, void* ws, const HeadPlan& p, cudaStream_t st,
+                  const DeviceInfo& d) {
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    float4* info = reinterpret_cast<float4*>(base + p.info);
+    float* scale = reinterpret_cast<float*>(base + p.scale);
+    float* plane = reinterpret_cast<float*>(base + p.plane);
+    tpmlp_bf16* dz = reinterpret_cast<tpmlp_bf16*>(base + p.dz);
+    cudaError_t e = launch_head_prepare(dloss, lse, targets, T, V, info, scale, st, &t_last_launches);
+    if (e != cudaSuccess) return fail_cuda(e);
+    for (long long v = 0; v < V; v += p.width) {
+        const int v0 = static_cast<int>(v);
+        const int cols = std::min(V - v0, p.width);
+        const int width = round_up(cols, 64);  // whole 64-column boxes: zeros behind the vocabulary
+        const tpmlp_bf16* Wp = W + static_cast<long long>(v0) * h;
+        {   // dz = w (softmax - one-hot) of this piece
+            GemmArgs g = blank_args();
+            const GemmShape sh{T, width, h, 1, SHARD_N, 1LL * T * h, 1LL * cols * h};
+            g.row_info = info;
+            g.col0 = v0;
+            g.n_valid = cols;
+            Operand a{X, T, h, ON_NONE, false};
+            Operand b{Wp, cols, h, ON_NONE, false};
+            Output o{dz, nullptr, T, width, 1};
+            if (int rc = run_gemm(launch_head_dlogits, a, b, o, g, sh, st, d)) return rc;
+        }
+        {   // dW's rows v0 .. v0 + cols - 1 = s dz^T X
+            GemmArgs g = blank_args();
+            const GemmShape sh{cols, h, T, 1, SHARD_M, 1LL * T * cols, 1LL * T * h};
+            g.out_scale = scale;
+            Operand a{dz, T, width, ON_NONE, true};
+            Operand b{X, T, h, ON_NONE, true};
+            Output o{dW + static_cast<long long>(v0) * h, nullptr, cols, h, 1};
+            if (int rc = run_gemm(launch_head_dw, a, b, o, g, sh, st, d)) return rc;
+        }
+        {   // dX (+)= dz W over this piece's columns
+            GemmArgs g = blank_args();
+            const GemmShape sh{T, h, width, 1, SHARD_K, 1LL * T * width, 1LL * cols * h};
+            g.out_scale = scale;
+            g.partial_add = v0 > 0;
+            Operand a{dz, T, width, ON_NONE, false};
+            Operand b{Wp, cols, h, ON_NONE, true};
+            if (!p.planes) {
+                Output o{dX, nullptr, T, h, 1};
+                if (int rc = run_gemm(launch_head_dx, a, b, o, g, sh, st, d)) return rc;
+            } else {
+                // a narrow last piece may have fewer k-blocks than splits: the
+                // planes behind them keep what they hold
+                Output o{plane, nullptr, T, h, std::min(p.splits, width / BK), true};
+                if (int rc = run_gemm(launch_row_partial, a, b, o, g, sh, st, d)) return rc;
+            }
+        }
+    }
+    if (!p.planes) return TPMLP_OK;
+    e = launch_head_reduce(plane, p.splits, 1LL * T * h, scale, reinterpret_cast<__nv_bfloat16*>(dX),
+                           st, &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+TPMLP_API size_t tp_head_loss_forward_workspace_bytes(int T, int h, int V) {
+    if (check_head(T, h, V)) return 0;
+    return head_forward_bytes(T, V);
+}
+
+TPMLP_API int tp_head_loss_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const int64_t* targets,
+                                   int T, int h, int V, float* loss, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+    TPMLP_PROLOGUE(check_head(T, h, V));
+    if (T == 0) return TPMLP_OK;
+    if (any_null(X, W, targets, loss, lse)) return TPMLP_ERR_NULL;
+    if (!all_aligned(X, W, workspace)) return TPMLP_ERR_ALIGN;
+    if (workspace == nullptr || workspace_bytes < head_forward_bytes(T, V)) return TPMLP_ERR_WORKSPACE;
+    DeviceInfo d;
+    if (int rc = enter(d)) return rc;
+    return head_forward(X, W, reinterpret_cast<const long long*>(targets), T, h, V, loss, lse, workspace,
+                        static_cast<cudaStream_t>(stream), d);
+}
+
+TPMLP_API size_t tp_head_loss_backward_workspace_bytes(int T, int h, int V) {
+    if (check_head(T, h, V) || T == 0) return 0;
+    return head_plan(T, h, V).total;
+}
+
+TPMLP_API size_t tp_head_loss_backward_min_workspace_bytes(int T, int h, int V) {
+    if (check_head(T, h, V) || T == 0) return 0;
+    return std::min(head_plan(T, h, V).total, head_plan_least(T, h, V).total);
+}
+
+TPMLP_API int tp_head_loss_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
+                                    const int64_t* targets, const float* lse, int T, int h, int V,
+                                    tpmlp_bf16* dX, tpmlp_bf16* dW, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    TPMLP_PROLOGUE(check_head(T, h, V));
+    if (any_null(dW) || (T > 0 && any_null(dloss, X, W, targets, lse, dX))) return TPMLP_ERR_NULL;
+    if (!all_aligned(X, W, dX, dW, workspace)) return TPMLP_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    HeadPlan p{};
+    if (T > 0 && (workspace == nullptr || !head_plan_for(T, h, V, workspace_bytes, p)))
+        return TPMLP_ERR_WORKSPACE;
+    DeviceInfo d;
+    if (int rc = enter(d)) return rc;
+    if (T == 0) {
+        cudaError_t e = cudaMemsetAsync(dW, 0, sizeof(uint16_t) * static_cast<size_t>(V) * h, st);
+        return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+    }
+    return head_backward(dloss, X, W, reinterpret_cast<const long long*>(targets), lse, T, h, V, dX, dW,
+                         workspace, p, st, d);
 }
 
 TPMLP_API const char* tp_mlp_status_string(int status) {

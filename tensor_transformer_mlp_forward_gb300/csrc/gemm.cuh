@@ -100,13 +100,21 @@ enum ShardOn { ON_NONE = 0, ON_CONTIG = 1, ON_ROWS = 2 };
 // EPI_PARTIAL: split reduction -- the fp32 accumulator of k-range split ks is
 // stored as is into plane ks of an fp32 [splits, M, N] workspace.
 // EPI_BIAS: + bias only (the attention block's Q/K/V projection).
+// EPI_LSE: the accumulator is a tile of logits; per row the running maximum
+// and the sum of exponentials over the warp's columns are written, the
+// logits themselves nowhere.
+// EPI_DLOGITS: logits -> their gradient w (softmax - one-hot), stored bf16.
+// EPI_SCALE: the sums times one fp32 factor read from device memory.
 enum Epilogue {
     EPI_BIAS_GELU = 0,
     EPI_BIAS_RESIDUAL = 1,
     EPI_DGELU = 2,
     EPI_STORE = 3,
     EPI_PARTIAL = 4,
-    EPI_BIAS = 5
+    EPI_BIAS = 5,
+    EPI_LSE = 6,
+    EPI_DLOGITS = 7,
+    EPI_SCALE = 8
 };
 
 struct GemmArgs {
@@ -139,6 +147,15 @@ struct GemmArgs {
     // compact [units, TILE_M, BN] fp32 map (tile-local coordinates) instead
     // of split ks of a [splits, M, N] map.
     int partial_compact;
+    // EPI_PARTIAL: 1 = the partial sums are added to what the map holds (a
+    // later piece of a reduction run piece by piece).
+    int partial_add;
+    const long long* targets;  // EPI_LSE: target column of each row (negative: none)
+    float2* lse_part;          // EPI_LSE: {max, sum of exponentials}, [tiles * EW / 4][M]
+    const float4* row_info;    // EPI_DLOGITS: {lse log2(e), weight, target column (int bits), -}
+    int col0;                  // EPI_DLOGITS: vocabulary index of column 0
+    int n_valid;               // EPI_DLOGITS: columns from here to N are stored as 0
+    const float* out_scale;    // EPI_SCALE
     int epi_warps;  // host side: 4 or 8 epilogue warps (the kernel variant launched)
     int dependent_launch;  // host side: launched with programmatic stream serialization
     // 1: the grid holds one CTA (pair) per work unit and a running CTA (pair)
@@ -291,6 +308,10 @@ __device__ __forceinline__ float gelu_tanh_grad(float x) {
     const float w = x * fmaf(1.5f * kGeluC * kGeluA, x2, 0.5f * kGeluC);
     return fmaf(th, fmaf(-w, th, 0.5f), 0.5f + w);
 }
+
+// log2(e): exponentials are taken as 2^(log2(e) x), one multiply-add and one
+// ex2 per value.
+constexpr float kLog2e = 1.4426950408889634f;
 
 // 32 consecutive bf16 values -> float; entries at or beyond `valid` read 0.
 __device__ __forceinline__ void load_bf16x32(const __nv_bfloat16* p, int valid, float (&v)[32]) {
@@ -712,10 +733,83 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
             if constexpr (kBias)  // the same 32 values for every lane (broadcast)
                 load_raw32(p.bias + gcol0 + out_blk(cb0) * 64, min(32, p.N - (tc.n0 + out_blk(cb0) * 64)),
                            bias_cur);
+            // The row's target column relative to this tile, and (EPI_DLOGITS)
+            // its log-sum-exp and weight.
+            int target = -1;
+            float lse2 = 0.0f, weight = 0.0f;
+            if constexpr (EPI == EPI_LSE) {
+                if (row_ok) {
+                    const long long y = __ldg(p.targets + m);
+                    if (y >= tc.n0 && y < p.N) target = static_cast<int>(y) - tc.n0;
+                }
+            }
+            if constexpr (EPI == EPI_DLOGITS) {
+                if (row_ok) {
+                    const float4 info = __ldg(p.row_info + m);
+                    lse2 = info.x;
+                    weight = info.y;
+                    target = __float_as_int(info.z) - p.col0 - tc.n0;
+                }
+            }
+            float scale = 1.0f;
+            if constexpr (EPI == EPI_SCALE) scale = __ldg(p.out_scale);
             if (!warp_wait_bounded<true>(&acc_full[acc], acc_phase, abort_flag, p.status)) break;
             tc_fence_after();
 
-            if constexpr (EPI == EPI_PARTIAL) {
+            if constexpr (EPI == EPI_LSE) {
+                // One pass over the row's columns in blocks of 64: the block's
+                // maximum, the sum so far rescaled to the new maximum, then
+                // the block's exponentials.  The target's column is left out:
+                // the loss is log(1 + sum_{v != y} exp(z_v - z_y)).
+                float mx = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+                for (int cc = 0; cc < NBLK; ++cc) {
+                    const int c = cb0 + cc;
+                    const int valid = p.N - (tc.n0 + c * 64);  // columns left in the vocabulary
+                    uint32_t r2[2][32];
+                    tmem_ld32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + c * 64, r2[0]);
+                    tmem_ld32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + c * 64 + 32,
+                              r2[1]);
+                    tmem_wait_ld();
+                    if (cc == NBLK - 1) {  // the MMA may refill this accumulator
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (PAIR)
+                                mbar_arrive_cluster(release_bar + acc * 8);
+                            else
+                                mbar_arrive(&acc_empty[acc]);
+                        }
+                    }
+                    float v[64];
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r2[i >> 5][i & 31]);
+                    const int t = target - c * 64;
+                    if (valid < 64 || __any_sync(0xFFFFFFFFu, t >= 0 && t < 64)) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i >= valid || i == t) v[i] = -INFINITY;
+                    }
+                    float bm = v[0];
+#pragma unroll
+                    for (int i = 1; i < 64; ++i) bm = fmaxf(bm, v[i]);
+                    const float nm = fmaxf(mx, bm);
+                    // nothing but excluded columns so far: any finite shift
+                    const float shift = nm == -INFINITY ? 0.0f : nm * kLog2e;
+                    float s0 = sum * ex2_approx(fmaf(mx, kLog2e, -shift)), s1 = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        s0 += ex2_approx(fmaf(v[i], kLog2e, -shift));
+                        s1 += ex2_approx(fmaf(v[i + 1], kLog2e, -shift));
+                    }
+                    sum = s0 + s1;
+                    mx = nm;
+                }
+                if (row_ok) {
+                    const long long part = static_cast<long long>(tc.n0 / G::TILE_N) * (EW / 4) + (warp >> 2);
+                    p.lse_part[part * p.M + m] = make_float2(mx, sum);
+                }
+            } else if constexpr (EPI == EPI_PARTIAL) {
                 // fp32 accumulator blocks of 32 rows x 32 columns (128 B rows)
 #pragma unroll 1
                 for (int cc = 0; cc < 2 * NBLK; ++cc) {
@@ -737,6 +831,8 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                         if (lane == 0) {
                             if (p.partial_compact)
                                 tma_store_3d(&tmO0, buf, n - tc.n0, row0 - tc.m0, tc.slot);
+                            else if (p.partial_add)
+                                tma_reduce_add_3d(&tmO0, buf, n, row0, tc.ks);
                             else
                                 tma_store_3d(&tmO0, buf, n, row0, tc.ks);
                             bulk_commit_group();
@@ -877,7 +973,28 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                         if (m_cta < p.M && lane < cvalid)
                             p.colsum[(static_cast<long long>(m_cta / BM) * 4 + q) * p.ld_colsum +
                                      gcol + lane] = cs;
+                    } else if constexpr (EPI == EPI_DLOGITS) {
+                        // w (p - [v == y]) with p = 2^(z log2(e) - lse2)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = weight * ex2_approx(fmaf(v[i], kLog2e, -lse2));
+                        const int t = target - (c * 64 + half * 32);
+                        if (__any_sync(0xFFFFFFFFu, t >= 0 && t < 32)) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i == t) v[i] -= weight;
+                        }
+                        if (p.n_valid - n < 32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i >= p.n_valid - n) v[i] = 0.0f;
+                        }
+                        stage_row(buf0 + my_row, half, swz, v);
                     } else {
+                        if constexpr (EPI == EPI_SCALE) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= scale;
+                        }
                         stage_row(buf0 + my_row, half, swz, v);
                     }
                     if constexpr (kAux) {

@@ -1,0 +1,205 @@
+// head_loss.cu -- the row kernels of the output head's softmax cross entropy
+// (the GEMMs that make the logits and their gradient are in
+// gemm_head_loss.cu).
+//
+// Per token t with logits z_v = X_t . W_v and target y:
+//   others = log sum_{v != y} exp(z_v)
+//   loss   = log(1 + exp(others - z_y))        lse = z_y + loss
+// which is lse - z_y, but keeps its relative precision where the model is
+// sure of the target and lse and z_y are near equals.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kernels.h"
+
+namespace tpmlp {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float dot8(const uint4 a, const uint4 b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        s = fmaf(__uint_as_float(x[j] << 16), __uint_as_float(y[j] << 16), s);
+        s = fmaf(__uint_as_float(x[j] & 0xFFFF0000u), __uint_as_float(y[j] & 0xFFFF0000u), s);
+    }
+    return s;
+}
+
+// {m, s} stands for s 2^(m log2(e)); m = -inf: nothing.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x);
+    const float shift = m == -INFINITY ? 0.0f : m;
+    return make_float2(m, a.y * ex2_approx((a.x - shift) * kLog2e) + b.y * ex2_approx((b.x - shift) * kLog2e));
+}
+
+// A CTA takes `rows` rows (a power of two up to 32), kThreads / rows threads
+// a row: they join the row's column parts and take the dot product of the
+// target's logit in fp32 (a tensor-core accumulator rounds toward zero at
+// every step, which over a long row would cost a large logit its last bits).
+__global__ void __launch_bounds__(kThreads)
+    head_combine_kernel(const float2* __restrict__ parts, int n_parts,
+                        const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
+                        const long long* __restrict__ targets, int T, int h, int V, int rows,
+                        float* __restrict__ loss, float* __restrict__ lse) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // the parts come from the kernel before this one
+    __shared__ float2 warp_part[kThreads / 32];
+    __shared__ float warp_dot[kThreads / 32];
+    const int group = kThreads / rows;  // threads a row, 8..256
+    const int r = threadIdx.x / group, sub = threadIdx.x % group;
+    const int row = blockIdx.x * rows + r;
+    const bool ok = row < T;
+    const long long y = ok ? __ldg(targets + row) : -1;
+    float2 acc = make_float2(-INFINITY, 0.0f);
+    float dot = 0.0f;
+    if (ok) {
+        for (int i = sub; i < n_parts; i += group)
+            acc = join(acc, __ldg(parts + static_cast<long long>(i) * T + row));
+        if (y >= 0 && y < V) {
+            const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<long long>(row) * h);
+            const uint4* w = reinterpret_cast<const uint4*>(W + y * h);
+#pragma unroll 4
+            for (int i = sub; i < (h >> 3); i += group) dot += dot8(__ldg(x + i), __ldg(w + i));
+        }
+    }
+    const int width = min(group, 32);
+    for (int off = width >> 1; off >= 1; off >>= 1) {
+        float2 o;
+        o.x = __shfl_xor_sync(0xFFFFFFFFu, acc.x, off);
+        o.y = __shfl_xor_sync(0xFFFFFFFFu, acc.y, off);
+        acc = join(acc, o);
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+    }
+    if (group > 32) {
+        if ((threadIdx.x & 31) == 0) {
+            warp_part[threadIdx.x >> 5] = acc;
+            warp_dot[threadIdx.x >> 5] = dot;
+        }
+        __syncthreads();
+        if (sub == 0) {
+            for (int w = 1; w < group / 32; ++w) {
+                acc = join(acc, warp_part[(threadIdx.x >> 5) + w]);
+                dot += warp_dot[(threadIdx.x >> 5) + w];
+            }
+        }
+    }
+    if (sub != 0 || !ok) return;
+    const float others = acc.x + logf(acc.y);  // y = 0 (V = 1): -inf
+    if (y < 0) {  // ignored token
+        loss[row] = 0.0f;
+        lse[row] = others;
+    } else if (y >= V) {  // no such class: never silent
+        loss[row] = __int_as_float(0x7FC00000);
+        lse[row] = others;
+    } else {
+        const float d = (acc.y == 0.0f ? -INFINITY : others) - dot;
+        const float l = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
+        loss[row] = d != d ? d : l;
+        lse[row] = dot + loss[row];
+    }
+}
+
+// One CTA: s = max |dloss| over the counted tokens, then every row's info.
+// The weights are divided by s so that in the usual case, one weight for all
+// counted tokens, they are exactly 1 and the bf16 gradient of the logits
+// rounds p - [v == y] itself, not its product with an arbitrary factor; s
+// multiplies the fp32 sums of dX and dW.
+__global__ void __launch_bounds__(1024)
+    head_prepare_kernel(const float* __restrict__ dloss, const float* __restrict__ lse,
+                        const long long* __restrict__ targets, int T, int V,
+                        float4* __restrict__ row_info, float* __restrict__ scale) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // lse may come from the kernel before this one
+    __shared__ float warp_max[32];
+    float s = 0.0f;
+    for (int t = threadIdx.x; t < T; t += blockDim.x)
+        if (__ldg(targets + t) >= 0) s = fmaxf(s, fabsf(__ldg(dloss + t)));
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = warp_max[threadIdx.x & 31];
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
+    if (!(s > 0.0f && s < INFINITY)) s = 1.0f;  // all zero, or a gradient that is not finite
+    if (threadIdx.x == 0) *scale = s;
+    for (int t = threadIdx.x; t < T; t += blockDim.x) {
+        const long long y = __ldg(targets + t);
+        float w = __ldg(dloss + t) / s;
+        float l = __ldg(lse + t) * kLog2e;
+        int target = -1;
+        if (y < 0) {
+            w = 0.0f;
+            l = INFINITY;  // 2^(z - inf) = 0
+        } else if (y >= V) {
+            w = __int_as_float(0x7FC00000);
+        } else {
+            target = static_cast<int>(y);
+        }
+        row_info[t] = make_float4(l, w, __int_as_float(target), 0.0f);
+    }
+}
+
+__global__ void __launch_bounds__(256)
+    head_reduce_kernel(const float* __restrict__ P, int planes, long long count,
+                       const float* __restrict__ scale, __nv_bfloat16* __restrict__ out) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // its inputs come from the kernel before it
+    const long long i = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
+    if (i >= count) return;
+    const float s = __ldg(scale);
+    float a[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < planes; ++k) {
+        const float4* q = reinterpret_cast<const float4*>(P + k * count + i);
+        const float4 x = __ldg(q), y = __ldg(q + 1);
+        a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+        a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+    }
+    uint4 o;
+    o.x = pack_bf16x2(s * a[0], s * a[1]);
+    o.y = pack_bf16x2(s * a[2], s * a[3]);
+    o.z = pack_bf16x2(s * a[4], s * a[5]);
+    o.w = pack_bf16x2(s * a[6], s * a[7]);
+    *reinterpret_cast<uint4*>(out + i) = o;
+}
+
+unsigned blocks_of(long long n, long long per) { return static_cast<unsigned>((n + per - 1) / per); }
+
+}  // namespace
+
+cudaError_t launch_head_combine(const float2* parts, int n_parts, const __nv_bfloat16* X,
+                                const __nv_bfloat16* W, const long long* targets, int T, int h,
+                                int V, float* loss, float* lse, cudaStream_t st, int* launches) {
+    // as many rows a CTA as leave every SM one: few rows get many threads each
+    int rows = 1;
+    while (rows < 32 && T > 152LL * rows) rows *= 2;
+    ++*launches;
+    return launch_dependent(head_combine_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, parts,
+                            n_parts, X, W, targets, T, h, V, rows, loss, lse);
+}
+
+cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long long* targets,
+                                int T, int V, float4* row_info, float* scale, cudaStream_t st,
+                                int* launches) {
+    ++*launches;
+    return launch_dependent(head_prepare_kernel, dim3(1), dim3(1024), 0, st, dloss, lse, targets, T, V,
+                            row_info, scale);
+}
+
+cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,
+                               __nv_bfloat16* out, cudaStream_t st, int* launches) {
+    ++*launches;
+    return launch_dependent(head_reduce_kernel, dim3(blocks_of(count / 8, 256)), dim3(256), 0, st, P,
+                            planes, count, scale, out);
+}
+
+}  // namespace tpmlp

@@ -74,6 +74,32 @@ cudaError_t launch_weight_grad(const GemmMaps& m, const GemmArgs& g,
 cudaError_t launch_weight_grad_partial(const GemmMaps& m, const GemmArgs& g, int grid, bool pair,
                                        cudaStream_t st);
 
+// The output head (X [T, h], W [V, h]; both K-major): row-wise softmax
+// statistics of the logits X W^T, and the logits' gradient.
+cudaError_t launch_head_lse(const GemmMaps& m, const GemmArgs& g, int grid, bool pair,
+                            cudaStream_t st);
+cudaError_t launch_head_dlogits(const GemmMaps& m, const GemmArgs& g, int grid, bool pair,
+                                cudaStream_t st);
+// dX (A K-major, B MN-major) and dW (both MN-major) of the head, scaled.
+cudaError_t launch_head_dx(const GemmMaps& m, const GemmArgs& g, int grid, bool pair,
+                           cudaStream_t st);
+cudaError_t launch_head_dw(const GemmMaps& m, const GemmArgs& g, int grid, bool pair,
+                           cudaStream_t st);
+
+// The head's row kernels (head_loss.cu).  Forward: the `parts` column parts'
+// {max, sum} of each row and the target's logit -> lse and loss.
+cudaError_t launch_head_combine(const float2* parts, int n_parts, const __nv_bfloat16* X,
+                                const __nv_bfloat16* W, const long long* targets, int T, int h,
+                                int V, float* loss, float* lse, cudaStream_t st, int* launches);
+// Backward: row_info[t] = {lse log2(e), dloss[t] / s, target, 0} and *scale =
+// s, the largest |dloss| of the counted tokens.
+cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long long* targets,
+                                int T, int V, float4* row_info, float* scale, cudaStream_t st,
+                                int* launches);
+// out[i] = bf16(*scale * sum_s P[s][i]), P: [planes, count], count % 8 == 0.
+cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,
+                               __nv_bfloat16* out, cudaStream_t st, int* launches);
+
 // out[c * ld_out + r] = in[r * cols + c], bf16, with each output row zeroed
 // from `rows` to the next multiple of 8 (transpose.cu).  cols % 8 == 0,
 // ld_out % 8 == 0, ld_out >= rows rounded up to 8, 16-byte aligned pointers.
@@ -107,6 +133,17 @@ cudaError_t launch_ln_backward(const __nv_bfloat16* dX, const __nv_bfloat16* dre
                                float* partial, cudaStream_t st, int* launches);
 // Row chunks of the dgamma / dbeta partial sums (partial = 2 * chunks * h floats).
 int ln_param_chunks(int T, int h);
+
+// LayerNorm without a residual (layernorm_plain.cu); dtype: TPMLP_BF16 /
+// FP16 / FP32.  `partial` holds 2 * norm_param_chunks(T, h) * h floats.
+cudaError_t launch_norm_forward(int dtype, const void* x, const void* gamma, const void* beta, int T,
+                                int h, float eps, void* y, float* mean, float* rstd,
+                                cudaStream_t st, int* launches);
+cudaError_t launch_norm_backward(int dtype, const void* dy, const void* x, const void* gamma,
+                                 const float* mean, const float* rstd, int T, int h, void* dx,
+                                 float* dgamma, float* dbeta, float* partial, cudaStream_t st,
+                                 int* launches);
+int norm_param_chunks(int T, int h);
 
 // Causal attention of every (sequence, head) (attention.cu).  Head dims
 // d in {64, 96, 128, 160}.  QKV [T, 3h] is read through 3-D tensor maps

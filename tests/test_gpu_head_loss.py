@@ -1,0 +1,272 @@
+"""The output head's softmax cross entropy and its gradients against their
+float64 forms, through the C ABI."""
+
+import numpy as np
+import pytest
+import torch
+
+from tensor_transformer_mlp_forward_gb300 import binding
+from tests import head_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def draw(T, h, V, seed, lean=20.0, skip=0.1):
+    g = torch.Generator().manual_seed(seed)
+    W = (torch.randn(V, h, generator=g) * 0.64 / h ** 0.5).to(torch.bfloat16)
+    y = torch.randint(0, V, (T,), generator=g)
+    Wt = W[y].float()
+    X = torch.randn(T, h, generator=g) + lean * torch.rand(T, 1, generator=g) * Wt / (Wt * Wt).sum(-1, keepdim=True)
+    y = torch.where(torch.rand(T, generator=g) < skip, torch.full_like(y, -100), y)
+    dloss = torch.rand(T, generator=g) / max(1, T)
+    return dict(X=X.to(torch.bfloat16), W=W, y=y, dloss=dloss)
+
+
+def run(c, **kw):
+    loss, lse = binding.tp_head_loss_forward(c["X"], c["W"], c["y"])
+    dX, dW = binding.tp_head_loss_backward(c["dloss"], c["X"], c["W"], c["y"], lse, **kw)
+    return loss, lse, dX, dW
+
+
+def check(c, out):
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    loss, lse, dX, dW = out
+    X, W, dl = (ref.f64(c[k]) for k in ("X", "W", "dloss"))
+    y = c["y"].cpu().numpy()
+    lr, sr, _ = ref.loss_forward(X, W, y)
+    bl, bs = ref.loss_forward_bounds(X, W, y)
+    ref.within(loss, lr, bl, "loss")
+    ref.within(lse, sr, bs, "lse")
+    s = ref.f64(lse)  # the backward pass takes it as given
+    dXr, dWr, _, _ = ref.loss_backward(dl, X, W, y, s)
+    bX, bW = ref.loss_backward_bounds(dl, X, W, y, s)
+    ref.within(dX, dXr, bX, "dX")
+    ref.within(dW, dWr, bW, "dW")
+    assert bool((dX[c["y"].to(dX.device) < 0] == 0).all())
+
+
+# one token, one class, classes below a tile and around its edges, odd
+# vocabularies, hidden sizes of one k-block and ragged ones, pairs and single
+# CTAs, more than one k-block split
+SHAPES = [(1, 8, 1), (1, 64, 2), (3, 16, 5), (2, 1024, 509), (7, 264, 255), (5, 72, 256), (130, 128, 257),
+          (128, 64, 1000), (129, 200, 1003), (300, 1024, 2049), (257, 1032, 777), (33, 2048, 4001),
+          (640, 512, 5000), (1, 4096, 3001), (1100, 256, 3000), (2100, 136, 1031)]
+
+
+@pytest.mark.parametrize("T,h,V", SHAPES)
+def test_against_float64(T, h, V):
+    c = {k: v.cuda() for k, v in draw(T, h, V, T + h + V).items()}
+    check(c, run(c))
+
+
+@pytest.mark.parametrize("lean", [0.0, 40.0])
+def test_unsure_and_sure_tokens(lean):
+    """No preference at all, and targets so sure that the loss is far below
+    the rounding of lse: its relative precision stays."""
+    c = {k: v.cuda() for k, v in draw(200, 256, 1500, 3, lean=lean, skip=0.0).items()}
+    check(c, run(c))
+
+
+def test_large_logits_do_not_overflow():
+    c = draw(90, 128, 700, 5)
+    c["X"] = (c["X"].float() * 40).to(torch.bfloat16)
+    c = {k: v.cuda() for k, v in c.items()}
+    check(c, run(c))
+
+
+def test_no_token_counts():
+    c = {k: v.cuda() for k, v in draw(140, 64, 300, 6, skip=2.0).items()}
+    loss, lse, dX, dW = run(c)
+    assert float(loss.abs().max()) == 0 and float(dX.float().abs().max()) == 0
+    assert float(dW.float().abs().max()) == 0
+    check(c, (loss, lse, dX, dW))
+
+
+def test_ignored_tokens_may_hold_any_dloss_and_lse():
+    """dloss and lse of a token that does not count are not used."""
+    c = {k: v.cuda() for k, v in draw(150, 64, 600, 7, skip=0.4).items()}
+    loss, lse = binding.tp_head_loss_forward(c["X"], c["W"], c["y"])
+    want = binding.tp_head_loss_backward(c["dloss"], c["X"], c["W"], c["y"], lse)
+    off = c["y"] < 0
+    for bad in (float("nan"), float("inf"), -1e30):
+        d2 = torch.where(off, torch.full_like(lse, bad), c["dloss"])
+        l2 = torch.where(off, torch.full_like(lse, bad), lse)
+        got = binding.tp_head_loss_backward(d2, c["X"], c["W"], c["y"], l2)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_target_outside_the_vocabulary_is_nan():
+    c = {k: v.cuda() for k, v in draw(20, 64, 300, 9, skip=0.0).items()}
+    c["y"][3] = 300
+    c["y"][4] = 2 ** 40
+    loss, lse, dX, dW = run(c)
+    assert bool(torch.isnan(loss[3:5]).all()) and not bool(torch.isnan(loss[:3]).any())
+    assert bool(torch.isnan(dX[3:5].float()).all()) and not bool(torch.isnan(dX[5:].float()).any())
+    assert bool(torch.isnan(dW.float()).all())
+
+
+def test_same_target_many_times():
+    """Every token has the same target: dW's row sums them all."""
+    c = {k: v.cuda() for k, v in draw(500, 64, 400, 10, skip=0.0).items()}
+    c["y"].fill_(399)
+    check(c, run(c))
+
+
+@pytest.mark.parametrize("T,h,V", [(70, 128, 2000), (300, 64, 1003), (1, 1024, 5000)])
+def test_narrow_pieces_of_the_vocabulary(T, h, V):
+    """Any workspace from the least to the full one: the same sums in another
+    order, within the same bounds, from a workspace full of NaN."""
+    c = {k: v.cuda() for k, v in draw(T, h, V, 12).items()}
+    least = binding.head_loss_backward_min_workspace_bytes(T, h, V)
+    full = binding.head_loss_backward_workspace_bytes(T, h, V)
+    assert least <= full
+    for size in sorted({least, least + 2 * T * 256 + 8, (least + full) // 2, full, full + 4096}):
+        ws = torch.full((size // 4 * 4 + 16,), 0xFF, dtype=torch.uint8, device="cuda")[:size]
+        check(c, run(c, workspace=ws))
+    with pytest.raises(binding.TpMlpError) as e:
+        run(c, workspace=torch.empty(least - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == binding.TPMLP_ERR_WORKSPACE
+
+
+def test_rows_behind_the_last_stay():
+    T, h, V = 77, 64, 301
+    c = {k: v.cuda() for k, v in draw(T, h, V, 13).items()}
+    n = binding.lib().tp_head_loss_forward_workspace_bytes(T, h, V)
+    stats = [torch.full((T + 5,), 7.0, device="cuda") for _ in range(2)]
+    dX = torch.full((T + 5, h), 7.0, dtype=torch.bfloat16, device="cuda")
+    dW = torch.full((V + 5, h), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((n + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    m = binding.head_loss_backward_workspace_bytes(T, h, V)
+    ws2 = torch.full((m + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    loss, lse = binding.tp_head_loss_forward(c["X"], c["W"], c["y"], loss=stats[0][:T], lse=stats[1][:T],
+                                             workspace=ws[:n])
+    binding.tp_head_loss_backward(c["dloss"], c["X"], c["W"], c["y"], lse, dX=dX[:T], dW=dW[:V],
+                                  workspace=ws2[:m])
+    check(c, (loss, lse, dX[:T], dW[:V]))
+    for t, k in ((stats[0], T), (stats[1], T), (dX, T), (dW, V)):
+        assert bool((t[k:] == 7.0).all())
+    assert bool((ws[n:] == 0x55).all()) and bool((ws2[m:] == 0x55).all())
+
+
+@pytest.mark.parametrize("T,h,V", [(600, 512, 3001), (5, 1024, 4001)])
+def test_deterministic_and_equal_in_every_launch_mode(T, h, V):
+    c = {k: v.cuda() for k, v in draw(T, h, V, 14).items()}
+    want = run(c)
+    for setter, mode in ((binding.set_cta_pair_mode, 0), (binding.set_cta_pair_mode, 2),
+                         (binding.set_tile_scheduler, 0), (binding.set_tile_scheduler, 1),
+                         (binding.set_dependent_launch, 0), (binding.set_wide_tiles, 1), (None, 0)):
+        prev = setter(mode) if setter else None
+        try:
+            got = run(c)
+        finally:
+            if setter:
+                setter(prev)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), (setter, mode)
+    for mode in (4, 8):  # the row statistics' parts are cut otherwise: equal within the bounds
+        prev = binding.set_epilogue_warps(mode)
+        try:
+            check(c, run(c))
+        finally:
+            binding.set_epilogue_warps(prev)
+
+
+def test_empty_batch():
+    W = torch.ones((300, 64), dtype=torch.bfloat16, device="cuda")
+    X = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((0,), dtype=torch.int64, device="cuda")
+    loss, lse = binding.tp_head_loss_forward(X, W, y)
+    dX, dW = binding.tp_head_loss_backward(loss, X, W, y, lse, dW=torch.ones_like(W))
+    torch.cuda.synchronize()
+    assert loss.shape == (0,) and dX.shape == (0, 64) and float(dW.float().abs().max()) == 0.0
+
+
+def test_gradients_against_differences():
+    """<grad, direction> against central differences of the float64 loss."""
+    T, h, V = 60, 64, 500
+    c = {k: v.cuda() for k, v in draw(T, h, V, 15, lean=6.0).items()}
+    _, lse, dX, dW = run(c)
+    X, W, dl = (ref.f64(c[k]) for k in ("X", "W", "dloss"))
+    y = c["y"].cpu().numpy()
+    f = lambda X, W: float((ref.loss_forward(X, W, y)[0] * dl).sum())  # noqa: E731
+    bX, bW = ref.loss_backward_bounds(dl, X, W, y, ref.f64(lse))
+    rng = np.random.default_rng(1)
+    for i, (grad, b) in enumerate(((dX, bX), (dW, bW))):
+        v = rng.standard_normal(b.shape)
+        step = 1e-5
+        up, down = [X, W], [X, W]
+        up[i], down[i] = up[i] + step * v, down[i] - step * v
+        diff = (f(*up) - f(*down)) / (2 * step)
+        # the gradient's own bounds; the differences' error is far below
+        assert abs(float((ref.f64(grad) * v).sum()) - diff) <= float((b * np.abs(v)).sum()) + 1e-7
+
+
+def test_norm_loss_and_back():
+    """The head as it is used: final norm, loss, its backward pass, the
+    norm's, against the float64 chain (bf16 between the steps: a relative
+    error of a few half-steps 2^-8 in the 2-norm)."""
+    T, h, V, eps = 260, 256, 2003, 1e-5
+    c = draw(T, h, V, 16, lean=0.0)
+    g = torch.Generator().manual_seed(2)
+    x = (torch.randn(T, h, generator=g) * 3 + 0.5).to(torch.bfloat16)
+    gam = (1 + 0.1 * torch.randn(h, generator=g)).to(torch.bfloat16)
+    bet = (0.1 * torch.randn(h, generator=g)).to(torch.bfloat16)
+    d = {k: v.cuda() for k, v in dict(c, x=x, gam=gam, bet=bet).items()}
+    X, mean, rstd = binding.tp_ln_forward(d["x"], d["gam"], d["bet"], eps)
+    loss, lse = binding.tp_head_loss_forward(X, d["W"], d["y"])
+    dX, dW = binding.tp_head_loss_backward(d["dloss"], X, d["W"], d["y"], lse)
+    dx, dgam, dbet = binding.tp_ln_backward(dX, d["x"], d["gam"], mean, rstd)
+    torch.cuda.synchronize()
+    f = ref.f64
+    Xr, mr, rr = ref.ln_forward(f(x), f(gam), f(bet), eps)
+    y = c["y"].numpy()
+    lr, sr, _ = ref.loss_forward(Xr, f(c["W"]), y)
+    dXr, dWr, _, _ = ref.loss_backward(f(c["dloss"]), Xr, f(c["W"]), y, sr)
+    dxr, dgr, dbr = ref.ln_backward(dXr, f(x), f(gam), mr, rr)
+    u = 2.0 ** -8
+    for name, got, want, steps in (("loss", loss, lr, 1), ("lse", lse, sr, 1), ("dX", dX, dXr, 3),
+                                   ("dW", dW, dWr, 3), ("dx", dx, dxr, 4), ("dgamma", dgam, dgr, 4),
+                                   ("dbeta", dbet, dbr, 4)):
+        off = np.linalg.norm(f(got) - want) / np.linalg.norm(want)
+        assert off <= steps * u, (name, off)
+
+
+def test_captured_and_beside_another_stream():
+    """Two captured graphs with their own workspaces, replayed on two streams
+    at once and on new inputs, give the eager results."""
+    T, h, V = 200, 256, 3001
+    cs = [{k: v.cuda() for k, v in draw(T, h, V, s).items()} for s in (21, 22)]
+    statics = [{k: v.clone() for k, v in c.items()} for c in cs]
+    run(statics[0])
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for s in statics:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(run(s))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for swap in (0, 1):
+        for i, s in enumerate(statics):
+            for k in s:
+                s[k].copy_(cs[i ^ swap][k])
+        torch.cuda.synchronize()
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for i, s in enumerate(statics):
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], run(cs[i ^ swap])))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    loss, lse = binding.tp_head_loss_forward(cs[0]["X"], cs[0]["W"], cs[0]["y"], stream=side)
+    got = binding.tp_head_loss_backward(cs[0]["dloss"], cs[0]["X"], cs[0]["W"], cs[0]["y"], lse, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((loss, lse, *got), run(cs[0])))
+
+
+def test_more_tokens_than_one_prepare_pass():
+    """A long batch over a small vocabulary, several rows a CTA in the row
+    kernels."""
+    c = {k: v.cuda() for k, v in draw(6001, 64, 130, 17).items()}
+    check(c, run(c))
