@@ -617,69 +617,94 @@ def tp_ln_residual_backward(dX, dres, a, r, gamma, mean, rstd, ds=None, dgamma=N
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _one_device(*tensors):
-    """All tensors on the current device: the library launches there."""
-    for x in tensors:
-        if x is not None and x.is_cuda and x.device.index != torch.cuda.current_device():
-            raise ValueError(f"a tensor is on {x.device}, but the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+def _in(x, name: str, shape, dtype, device: int) -> int:
+    """The address of a contiguous tensor of this shape and type on this
+    device (the current one: the library launches there)."""
+    if (x is None or not x.is_cuda or x.dtype is not dtype or x.shape != shape
+            or not x.is_contiguous()):
+        _ptr(x, name, shape, dtype)  # raises, naming what is wrong
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on {x.device}, but the current device is cuda:{device}")
+    return x.data_ptr()
 
 
-def _new(x, shape, like: torch.Tensor, dtype, stream):
-    """The caller's tensor, or a fresh one from the memory pool of the stream
-    that will write it (so that freeing it cannot hand it to another one)."""
-    if x is not None:
-        return x
+def _stream_of(stream, device: int) -> int:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
+
+
+def _new(shape, dtype, device, stream):
+    """A fresh tensor from the memory pool of the stream that will write it
+    (so that freeing it cannot hand it to another stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(ws, name: str, need: int, dtype, device, index: int, stream):
+    """Address and size of the caller's scratch, or of a fresh one of `need`
+    elements, and the tensor, to be kept until the launch."""
+    if ws is None:
+        ws = _new((max(need, 1),), dtype, device, stream)
+        return ws.data_ptr(), ws.numel(), ws
+    return _in(ws, name, ws.shape, dtype, index), ws.numel(), ws
 
 
 def _dtype_of(x, name: str) -> int:
-    if x.dtype not in _DTYPES:
+    code = _DTYPES.get(x.dtype)
+    if code is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
-    return _DTYPES[x.dtype]
+    return code
+
+
+_F32 = torch.float32
+_BF16 = torch.bfloat16
 
 
 def tp_ln_forward(x, gamma, beta, eps: float = 1e-5, y=None, mean=None, rstd=None, stream=None):
     """y, mean, rstd of y = LayerNorm(x) * gamma + beta, x [T, h] in bfloat16,
     float16 or float32 (mean and rstd [T] are float32)."""
-    T, h = x.shape
-    dt = _dtype_of(x, "x")
-    _one_device(x, gamma, beta, y, mean, rstd)
-    y = _new(y, (T, h), x, x.dtype, stream)
-    mean = _new(mean, (T,), x, torch.float32, stream)
-    rstd = _new(rstd, (T,), x, torch.float32, stream)
+    T, h = shape = x.shape
+    dt = x.dtype
+    code = _dtype_of(x, "x")
+    d = torch.cuda.current_device() if x.is_cuda else -1
+    xp = _in(x, "x", shape, dt, d)
+    gp, bp = _in(gamma, "gamma", (h,), dt, d), _in(beta, "beta", (h,), dt, d)
+    dev = x.device
+    y = _new(shape, dt, dev, stream) if y is None else y
+    mean = _new((T,), _F32, dev, stream) if mean is None else mean
+    rstd = _new((T,), _F32, dev, stream) if rstd is None else rstd
     _check("tp_ln_forward", lib().tp_ln_forward(
-        _ptr(x, "x", (T, h), x.dtype), _ptr(gamma, "gamma", (h,), x.dtype),
-        _ptr(beta, "beta", (h,), x.dtype), T, h, dt, eps, _ptr(y, "y", (T, h), x.dtype),
-        _ptr(mean, "mean", (T,), torch.float32), _ptr(rstd, "rstd", (T,), torch.float32),
-        _stream(stream)))
+        xp, gp, bp, T, h, code, eps, _in(y, "y", shape, dt, d), _in(mean, "mean", (T,), _F32, d),
+        _in(rstd, "rstd", (T,), _F32, d), _stream_of(stream, d)))
     return y, mean, rstd
 
 
 def tp_ln_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, partial=None,
                    stream=None):
     """dx (of x's type), dgamma, dbeta (float32) of tp_ln_forward."""
-    T, h = x.shape
-    dt = _dtype_of(x, "x")
-    _one_device(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, partial)
-    dx = _new(dx, (T, h), x, x.dtype, stream)
-    dgamma = _new(dgamma, (h,), x, torch.float32, stream)
-    dbeta = _new(dbeta, (h,), x, torch.float32, stream)
-    need = int(lib().tp_ln_backward_workspace_floats(T, h, dt))
-    partial = _new(partial, (max(1, need),), x, torch.float32, stream)
-    if partial.numel() < need:
-        raise ValueError(f"partial holds {partial.numel()} floats, {need} needed")
+    T, h = shape = x.shape
+    dt = x.dtype
+    code = _dtype_of(x, "x")
+    d = torch.cuda.current_device() if x.is_cuda else -1
+    xp = _in(x, "x", shape, dt, d)
+    args = (_in(dy, "dy", shape, dt, d), xp, _in(gamma, "gamma", (h,), dt, d),
+            _in(mean, "mean", (T,), _F32, d), _in(rstd, "rstd", (T,), _F32, d))
+    dev = x.device
+    dx = _new(shape, dt, dev, stream) if dx is None else dx
+    dgamma = _new((h,), _F32, dev, stream) if dgamma is None else dgamma
+    dbeta = _new((h,), _F32, dev, stream) if dbeta is None else dbeta
+    need = lib().tp_ln_backward_workspace_floats(T, h, code)
+    pp, pn, partial = _scratch(partial, "partial", need, _F32, dev, d, stream)
+    if pn < need:
+        raise ValueError(f"partial holds {pn} floats, {need} needed")
     _check("tp_ln_backward", lib().tp_ln_backward(
-        _ptr(dy, "dy", (T, h), x.dtype), _ptr(x, "x", (T, h), x.dtype),
-        _ptr(gamma, "gamma", (h,), x.dtype), _ptr(mean, "mean", (T,), torch.float32),
-        _ptr(rstd, "rstd", (T,), torch.float32), T, h, dt, _ptr(dx, "dx", (T, h), x.dtype),
-        _ptr(dgamma, "dgamma", (h,), torch.float32), _ptr(dbeta, "dbeta", (h,), torch.float32),
-        _ptr(partial, "partial", None, torch.float32), _stream(stream)))
+        *args, T, h, code, _in(dx, "dx", shape, dt, d), _in(dgamma, "dgamma", (h,), _F32, d),
+        _in(dbeta, "dbeta", (h,), _F32, d), pp, _stream_of(stream, d)))
     return dx, dgamma, dbeta
 
 
@@ -689,19 +714,22 @@ def tp_head_loss_forward(X, W, targets, loss=None, lse=None, workspace=None, str
     h] bfloat16; the logits are not stored."""
     T, h = X.shape
     V = W.shape[0]
-    _one_device(X, W, targets, loss, lse, workspace)
-    loss = _new(loss, (T,), X, torch.float32, stream)
-    lse = _new(lse, (T,), X, torch.float32, stream)
-    need = int(lib().tp_head_loss_forward_workspace_bytes(T, h, V))
-    workspace = _new(workspace, (max(need, 16),), X, torch.uint8, stream)
+    d = torch.cuda.current_device() if X.is_cuda else -1
+    args = (_in(X, "X", (T, h), _BF16, d), _in(W, "W", (V, h), _BF16, d),
+            _in(targets, "targets", (T,), torch.int64, d))
+    dev = X.device
+    loss = _new((T,), _F32, dev, stream) if loss is None else loss
+    lse = _new((T,), _F32, dev, stream) if lse is None else lse
+    need = lib().tp_head_loss_forward_workspace_bytes(T, h, V)
+    wp, wn, workspace = _scratch(workspace, "workspace", need, torch.uint8, dev, d, stream)
     _check("tp_head_loss_forward", lib().tp_head_loss_forward(
-        _ptr(X, "X", (T, h)), _ptr(W, "W", (V, h)), _ptr(targets, "targets", (T,), torch.int64),
-        T, h, V, _ptr(loss, "loss", (T,), torch.float32), _ptr(lse, "lse", (T,), torch.float32),
-        _ptr(workspace, "workspace", None, torch.uint8), workspace.numel(), _stream(stream)))
+        *args, T, h, V, _in(loss, "loss", (T,), _F32, d), _in(lse, "lse", (T,), _F32, d), wp, wn,
+        _stream_of(stream, d)))
     return loss, lse
 
 
 def head_loss_backward_workspace_bytes(T: int, h: int, V: int) -> int:
+    """Workspace with which tp_head_loss_backward takes its widest pieces."""
     return int(lib().tp_head_loss_backward_workspace_bytes(T, h, V))
 
 
@@ -716,16 +744,18 @@ def tp_head_loss_backward(dloss, X, W, targets, lse, dX=None, dW=None, workspace
     (float32) and the forward pass's lse."""
     T, h = X.shape
     V = W.shape[0]
-    _one_device(dloss, X, W, targets, lse, dX, dW, workspace)
-    dX = _new(dX, (T, h), X, torch.bfloat16, stream)
-    dW = _new(dW, (V, h), X, torch.bfloat16, stream)
-    workspace = _new(workspace, (max(head_loss_backward_workspace_bytes(T, h, V), 16),), X,
-                     torch.uint8, stream)
+    d = torch.cuda.current_device() if X.is_cuda else -1
+    xp = _in(X, "X", (T, h), _BF16, d)
+    args = (_in(dloss, "dloss", (T,), _F32, d), xp, _in(W, "W", (V, h), _BF16, d),
+            _in(targets, "targets", (T,), torch.int64, d), _in(lse, "lse", (T,), _F32, d))
+    dev = X.device
+    dX = _new((T, h), _BF16, dev, stream) if dX is None else dX
+    dW = _new((V, h), _BF16, dev, stream) if dW is None else dW
+    need = lib().tp_head_loss_backward_workspace_bytes(T, h, V) if workspace is None else 0
+    wp, wn, workspace = _scratch(workspace, "workspace", need, torch.uint8, dev, d, stream)
     _check("tp_head_loss_backward", lib().tp_head_loss_backward(
-        _ptr(dloss, "dloss", (T,), torch.float32), _ptr(X, "X", (T, h)), _ptr(W, "W", (V, h)),
-        _ptr(targets, "targets", (T,), torch.int64), _ptr(lse, "lse", (T,), torch.float32),
-        T, h, V, _ptr(dX, "dX", (T, h)), _ptr(dW, "dW", (V, h)),
-        _ptr(workspace, "workspace", None, torch.uint8), workspace.numel(), _stream(stream)))
+        *args, T, h, V, _in(dX, "dX", (T, h), _BF16, d), _in(dW, "dW", (V, h), _BF16, d), wp, wn,
+        _stream_of(stream, d)))
     return dX, dW
 
 

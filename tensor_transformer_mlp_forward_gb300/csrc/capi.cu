@@ -1672,7 +1672,8 @@ TPMLP_API int tp_ln_forward(const void* x, const void* gamma, const void* beta, 
 
 TPMLP_API size_t tp_ln_backward_workspace_floats(int T, int h, int dtype) {
     if (check_norm(T, h, dtype)) return 0;
-    return 2 * static_cast<size_t>(norm_param_chunks(T, h)) * static_cast<size_t>(h);
+    const int elem = dtype == TPMLP_FP32 ? 4 : 2;
+    return 2 * static_cast<size_t>(norm_param_parts(T, h, elem)) * static_cast<size_t>(h);
 }
 
 TPMLP_API int tp_ln_backward(const void* dy, const void* x, const void* gamma, const float* mean,
@@ -1692,8 +1693,8 @@ TPMLP_API int tp_ln_backward(const void* dy, const void* x, const void* gamma, c
             return fail_cuda(e);
         return TPMLP_OK;
     }
-    e = launch_norm_backward(dtype, dy, x, gamma, mean, rstd, T, h, dx, dgamma, dbeta, partial, st,
-                             &t_last_launches);
+    e = launch_norm_backward(dtype, dy, x, gamma, mean, rstd, T, h, dx, dgamma, dbeta, partial,
+                             d.status, st, &t_last_launches);
     return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
 }
 

@@ -135,15 +135,16 @@ cudaError_t launch_ln_backward(const __nv_bfloat16* dX, const __nv_bfloat16* dre
 int ln_param_chunks(int T, int h);
 
 // LayerNorm without a residual (layernorm_plain.cu); dtype: TPMLP_BF16 /
-// FP16 / FP32.  `partial` holds 2 * norm_param_chunks(T, h) * h floats.
+// FP16 / FP32.  `partial` holds 2 * norm_param_parts(T, h, bytes of a value) *
+// h floats; `status` is the device status word.
 cudaError_t launch_norm_forward(int dtype, const void* x, const void* gamma, const void* beta, int T,
                                 int h, float eps, void* y, float* mean, float* rstd,
                                 cudaStream_t st, int* launches);
 cudaError_t launch_norm_backward(int dtype, const void* dy, const void* x, const void* gamma,
                                  const float* mean, const float* rstd, int T, int h, void* dx,
-                                 float* dgamma, float* dbeta, float* partial, cudaStream_t st,
-                                 int* launches);
-int norm_param_chunks(int T, int h);
+                                 float* dgamma, float* dbeta, float* partial, int* status,
+                                 cudaStream_t st, int* launches);
+int norm_param_parts(int T, int h, int elem);
 
 // Causal attention of every (sequence, head) (attention.cu).  Head dims
 // d in {64, 96, 128, 160}.  QKV [T, 3h] is read through 3-D tensor maps

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/tpmlp.h"
 #include "kernels.h"
@@ -33,6 +34,494 @@ template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+constexpr int kNormMaxStages = 6;
+
+// A piece of a row held by one thread: VEC > 1 consecutive values, 16 bytes,
+// or (VEC 1, rows that do not start on 16-byte boundaries) two single values
+// a row's thread count apart.  The arithmetic runs on pairs of fp32 values
+// (one packed instruction for two), and these kernels are close to the
+// issue rate: 37 instructions a value of the backward pass when written one
+// by one, 14 with pairs.
+template <typename T, int VEC>
+struct Piece {
+    static constexpr int N = VEC == 1 ? 2 : VEC;
+    static constexpr int WORDS = N * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[WORDS];
+};
+
+// Column of value j of piece k for thread `sub` of `group`.
+template <int VEC>
+__device__ __forceinline__ int piece_col(int k, int j, int group, int sub) {
+    return VEC == 1 ? (2 * k + j) * group + sub : (k * group + sub) * VEC + j;
+}
+
+// Piece k of the row at p (columns at and beyond h read 0).
+template <typename T, int VEC>
+__device__ __forceinline__ Piece<T, VEC> load_piece(const T* p, int k, int group, int sub, int h) {
+    Piece<T, VEC> r;
+    const int c = piece_col<VEC>(k, 0, group, sub);
+    if constexpr (VEC > 1) {
+        static_assert(sizeof(r) == 16, "a 16-byte piece");
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (c < h) u = *reinterpret_cast<const uint4*>(p + c);
+        r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+    } else if constexpr (sizeof(T) == 4) {
+        r.w[0] = c < h ? reinterpret_cast<const uint32_t*>(p)[c] : 0u;
+        r.w[1] = c + group < h ? reinterpret_cast<const uint32_t*>(p)[c + group] : 0u;
+    } else {
+        const uint32_t lo = c < h ? reinterpret_cast<const uint16_t*>(p)[c] : 0u;
+        const uint32_t hi = c + group < h ? reinterpret_cast<const uint16_t*>(p)[c + group] : 0u;
+        r.w[0] = lo | (hi << 16);
+    }
+    return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_piece(T* p, const Piece<T, VEC>& r, int k, int group, int sub, int h) {
+    const int c = piece_col<VEC>(k, 0, group, sub);
+    if constexpr (VEC > 1) {
+        if (c < h) *reinterpret_cast<uint4*>(p + c) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else if constexpr (sizeof(T) == 4) {
+        if (c < h) reinterpret_cast<uint32_t*>(p)[c] = r.w[0];
+        if (c + group < h) reinterpret_cast<uint32_t*>(p)[c + group] = r.w[1];
+    } else {
+        if (c < h) reinterpret_cast<uint16_t*>(p)[c] = static_cast<uint16_t>(r.w[0]);
+        if (c + group < h) reinterpret_cast<uint16_t*>(p)[c + group] = static_cast<uint16_t>(r.w[0] >> 16);
+    }
+}
+
+// Pair i of a piece as fp32, and back (rounded once).
+template <typename T, int VEC>
+__device__ __forceinline__ float2 pair_of(const Piece<T, VEC>& r, int i) {
+    if constexpr (sizeof(T) == 4) {
+        return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    } else if constexpr (std::is_same_v<T, __half>) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+    } else {
+        return make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void set_pair(Piece<T, VEC>& r, int i, float2 v) {
+    if constexpr (sizeof(T) == 4) {
+        r.w[2 * i] = __float_as_uint(v.x);
+        r.w[2 * i + 1] = __float_as_uint(v.y);
+    } else if constexpr (std::is_same_v<T, __half>) {
+        const __half2 p = __floats2half2_rn(v.x, v.y);
+        r.w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    } else {
+        r.w[i] = pack_bf16x2(v.x, v.y);
+    }
+}
+
+// Packed fp32 arithmetic: each half rounded as the scalar operation.
+__device__ __forceinline__ unsigned long long bits(float2 v) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 halves(unsigned long long b) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
+    return v;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return halves(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return halves(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return halves(r);
+}
+// g = dy gamma.  The packed product may be fused with the subtraction of
+// mean(g) behind it; a row of one value (VEC 1) needs it rounded as it was
+// summed, so that g - mean(g) is 0.
+template <int VEC>
+__device__ __forceinline__ float2 product(float2 a, float2 b) {
+    if constexpr (VEC == 1) return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
+    return mul2(a, b);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The pairs of piece k as fp32 values of a row at p.
+template <int VEC>
+__device__ __forceinline__ void store_pairs(float* p, const float2* v, int k, int group, int sub, int h) {
+    const int c = piece_col<VEC>(k, 0, group, sub);
+    if constexpr (VEC == 1) {
+        if (c < h) p[c] = v[0].x;
+        if (c + group < h) p[c + group] = v[0].y;
+    } else if (c < h) {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; j += 2)
+            *reinterpret_cast<float4*>(p + c + 2 * j) = make_float4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
+    }
+}
+
+// Sum over the W warps of a row's group (W a power of two; warps W g .. W g +
+// W - 1 of the CTA); every thread receives the total, added in the same
+// order in every thread.  `scratch` holds one entry a warp.  All threads of
+// the CTA call it.
+__device__ __forceinline__ float2 group_sum(float2 x, int W, float2* scratch) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, off);
+        x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, off);
+    }
+    if (W == 1) return x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) scratch[warp] = x;
+    __syncthreads();
+    x = scratch[(warp & ~(W - 1)) + (lane & (W - 1))];
+    for (int off = W >> 1; off >= 1; off >>= 1) {
+        x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, off);
+        x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, off);
+    }
+    return x;
+}
+
+// Forward: W warps a row, the row in registers (NV pieces a thread), so all
+// of its loads are in flight at once and x is read once.  The variance is
+// taken from x - mu.
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(1024)
+    norm_forward_reg_kernel(const T* __restrict__ x, const T* __restrict__ gamma,
+                            const T* __restrict__ beta, int rows, int h, int W, float eps,
+                            T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // its inputs may come from the kernel before it
+    __shared__ float2 scratch[2][32];
+    const int group = 32 * W;  // threads a row
+    const int sub = threadIdx.x % group;
+    const int row = blockIdx.x * (blockDim.x / group) + threadIdx.x / group;
+    const bool ok = row < rows;
+    const long long base = static_cast<long long>(row) * h;
+    constexpr int PAIRS = Piece<T, VEC>::N / 2;
+    Piece<T, VEC> in[NV];
+    float2 acc = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) in[k] = load_piece<T, VEC>(x + base, k, group, sub, ok ? h : 0);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) acc = add2(acc, pair_of(in[k], i));
+    const float mu = group_sum(make_float2(acc.x + acc.y, 0.0f), W, scratch[0]).x / static_cast<float>(h);
+    acc = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            float2 c = add2(pair_of(in[k], i), both(-mu));
+            // the zeros behind the row are not its values
+            if (piece_col<VEC>(k, 2 * i, group, sub) >= h) c.x = 0.0f;
+            if (piece_col<VEC>(k, 2 * i + 1, group, sub) >= h) c.y = 0.0f;
+            acc = fma2(c, c, acc);
+        }
+    const float var = group_sum(make_float2(acc.x + acc.y, 0.0f), W, scratch[1]).x / static_cast<float>(h);
+    const float rs = 1.0f / sqrtf(var + eps);
+    if (!ok) return;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const Piece<T, VEC> g = load_piece<T, VEC>(gamma, k, group, sub, h);
+        const Piece<T, VEC> b = load_piece<T, VEC>(beta, k, group, sub, h);
+        Piece<T, VEC> o;
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i)
+            set_pair(o, i, fma2(mul2(add2(pair_of(in[k], i), both(-mu)), both(rs)), pair_of(g, i), pair_of(b, i)));
+        store_piece<T, VEC>(y + base, o, k, group, sub, h);
+    }
+    if (sub == 0) {
+        mean[row] = mu;
+        rstd[row] = rs;
+    }
+}
+
+// Backward in one pass over x and dy.  Blocks of R rows (R = NT / 32 / W, W
+// warps a row) stream through a ring of `stages` buffers in shared memory,
+// one bulk copy a tensor and block (the rows of a block are one contiguous
+// range), so that the loads in flight do not depend on the registers; block
+// b goes to CTA b mod grid.  Every thread keeps the same columns in every
+// row and adds its part of dgamma and dbeta in registers; at the end the
+// CTA's groups meet in shared memory, in group order, and the CTA's sums go
+// to part[0 / 1][CTA][column].
+// The loop is skewed by half a block: it finishes block i (dx from its row
+// sums) and then begins block i + 1 (its row sums), with one CTA barrier
+// between the two, so that a block's latencies overlap the other's work.
+// KEEP: a thread's values of a row stay in registers between the row sums
+// and dx, and gamma with them; else both are read from shared memory again
+// (wide rows, where the accumulators take the registers).
+struct NormBackwardArgs {
+    int rows, h, W, stages;
+    int buf_bytes;  // one tensor's block in the ring, 16-byte multiple
+    int* status;
+};
+
+template <typename T, int VEC, int NV, int NT, int MIN_CTAS, bool KEEP>
+__global__ void __launch_bounds__(NT, MIN_CTAS)
+    norm_backward_ring_kernel(const T* __restrict__ dy, const T* __restrict__ x,
+                              const T* __restrict__ gamma, const float* __restrict__ mean,
+                              const float* __restrict__ rstd, const NormBackwardArgs p,
+                              T* __restrict__ dx, float* __restrict__ part_g,
+                              float* __restrict__ part_b) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kNormMaxStages];
+    __shared__ float2 scratch[2][NT / 32];
+    __shared__ uint32_t abort_flag;
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    const int group = 32 * p.W, R = NT / group;
+    const int g = threadIdx.x / group, sub = threadIdx.x % group;
+    const int h = p.h;
+    const int blocks = (p.rows + R - 1) / R;
+    const long long total = static_cast<long long>(p.rows) * h * sizeof(T);  // bytes of a tensor
+    T* sgamma = reinterpret_cast<T*>(ring + static_cast<size_t>(p.stages) * 2 * p.buf_bytes);  // !KEEP
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0u;
+        fence_mbar_init();
+    }
+    pdl_wait();  // dy may come from the kernel before this one
+    if constexpr (!KEEP)
+        for (int c = threadIdx.x; c < h; c += NT) sgamma[c] = gamma[c];
+    __syncthreads();
+
+    // The block's byte range, and the part of it that is copied: whole
+    // 16-byte granules of the tensor (all but its last few bytes).
+    auto range = [&](int blk, long long& b0, long long& b1, long long& a0, long long& a1) {
+        b0 = static_cast<long long>(blk) * R * h * sizeof(T);
+        const long long rows_end = min(static_cast<long long>(blk + 1) * R, static_cast<long long>(p.rows));
+        b1 = rows_end * h * static_cast<long long>(sizeof(T));
+        a0 = b0 & ~15LL;
+        a1 = min((b1 + 15) & ~15LL, total & ~15LL);
+        if (a1 < a0) a1 = a0;
+    };
+    auto issue = [&](long long blk, int stage) {  // one thread
+        if (blk >= blocks) return;
+        long long b0, b1, a0, a1;
+        range(static_cast<int>(blk), b0, b1, a0, a1);
+        const uint32_t n = static_cast<uint32_t>(a1 - a0);
+        const uint32_t dst = smem_u32(ring) + static_cast<uint32_t>(stage) * 2u * p.buf_bytes;
+        mbar_arrive_expect_tx(&full[stage], 2 * n);
+        if (n) {
+            bulk_load(dst, reinterpret_cast<const uint8_t*>(x) + a0, n, &full[stage]);
+            bulk_load(dst + p.buf_bytes, reinterpret_cast<const uint8_t*>(dy) + a0, n, &full[stage]);
+        }
+    };
+    const long long step = gridDim.x;
+    if (threadIdx.x == 0)
+        for (int s = 0; s < p.stages; ++s) issue(blockIdx.x + s * step, s);
+
+    constexpr int N = Piece<T, VEC>::N, PAIRS = N / 2;
+    float2 acc_g[NV * PAIRS], acc_b[NV * PAIRS];
+    Piece<T, VEC> kx[KEEP ? NV : 1], kdy[KEEP ? NV : 1], kg[KEEP ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV * PAIRS; ++i) acc_g[i] = acc_b[i] = both(0.0f);
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) kg[k] = load_piece<T, VEC>(gamma, k, group, sub, h);
+    }
+    const float inv_h = 1.0f / static_cast<float>(h);
+    // the statistics of this group's row of a block (0 behind the last row)
+    auto row_stats = [&](long long blk) {
+        const long long row = blk * R + g;
+        return row < p.rows ? make_float2(__ldg(mean + row), __ldg(rstd + row)) : make_float2(0.0f, 0.0f);
+    };
+    // this group's row of the block in a stage's buffers
+    auto row_ptr = [&](long long blk, int stage, const T*& sx, const T*& sdy) {
+        long long skip = 0;  // bytes before the block in its first granule
+        if constexpr (VEC == 1) skip = (blk * R * h * static_cast<long long>(sizeof(T))) & 15;
+        const uint8_t* b = ring + static_cast<size_t>(stage) * 2 * p.buf_bytes + skip;
+        sx = reinterpret_cast<const T*>(b) + static_cast<size_t>(g) * h;
+        sdy = reinterpret_cast<const T*>(b + p.buf_bytes) + static_cast<size_t>(g) * h;
+    };
+    // Begins a block: waits for its copies and takes this thread's part of
+    // its row's sums of g and g (x - mu).
+    auto begin = [&](long long blk, int stage, uint32_t phase, float mu) {
+        // A wait that gives up has set the status word; the loop goes on (on
+        // whatever the buffer holds), so that no barrier is left short.
+        warp_wait_bounded(&full[stage], phase, &abort_flag, p.status);
+        if constexpr (VEC == 1) {
+            long long b0, b1, a0, a1;
+            range(static_cast<int>(blk), b0, b1, a0, a1);
+            if (a1 < b1) {  // the tensor's last few bytes: plain loads
+                const long long e = max(a1, b0) / static_cast<long long>(sizeof(T)) + threadIdx.x;
+                const long long o = e * static_cast<long long>(sizeof(T)) - a0;
+                uint8_t* b = ring + static_cast<size_t>(stage) * 2 * p.buf_bytes + o;
+                if (e < b1 / static_cast<long long>(sizeof(T))) {
+                    *reinterpret_cast<T*>(b) = x[e];
+                    *reinterpret_cast<T*>(b + p.buf_bytes) = dy[e];
+                }
+                __syncthreads();
+            }
+        }
+        // columns of this thread's row (none behind the last row: the sums get
+        // zeros, as dy and gamma read 0)
+        const int cols = blk * R + g < p.rows ? h : 0;
+        const T *sx, *sdy;
+        row_ptr(blk, stage, sx, sdy);
+        float2 m = both(0.0f), mx = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Piece<T, VEC> px = load_piece<T, VEC>(sx, k, group, sub, cols);
+            const Piece<T, VEC> pd = load_piece<T, VEC>(sdy, k, group, sub, cols);
+            Piece<T, VEC> pg;
+            if constexpr (KEEP) {
+                kx[k] = px;
+                kdy[k] = pd;
+                pg = kg[k];
+            } else {
+                pg = load_piece<T, VEC>(sgamma, k, group, sub, h);
+            }
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                const float2 gj = product<VEC>(pair_of(pd, i), pair_of(pg, i));
+                m = add2(m, gj);
+                mx = fma2(gj, add2(pair_of(px, i), both(-mu)), mx);
+            }
+        }
+        return make_float2(m.x + m.y, mx.x + mx.y);
+    };
+
+    int stage = 0, parity = 0;
+    uint32_t phase = 0;
+    long long blk = blockIdx.x;
+    float2 st = row_stats(blk), st_next = row_stats(blk + step);
+    float2 m = group_sum(begin(blk, 0, 0, st.x), p.W, scratch[0]);
+    if constexpr (KEEP) {
+        if (p.W == 1) __syncthreads();  // else group_sum's barrier did it
+        if (threadIdx.x == 0) issue(blk + p.stages * step, 0);
+    }
+    while (true) {
+        const long long next = blk + step;
+        const float2 st_after = row_stats(next + step);
+        {  // finish block blk: m = its row's sums
+            const int cols = blk * R + g < p.rows ? h : 0;
+            const float mu = st.x, rs = st.y;
+            const float mg = m.x * inv_h;                   // mean(g)
+            const float k2 = rs * rs * rs * (m.y * inv_h);  // rstd^2 mean(g xhat)
+            const T *sx, *sdy;
+            row_ptr(blk, stage, sx, sdy);
+            const long long base = (blk * R + g) * h;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                Piece<T, VEC> px, pd, pg, o;
+                if constexpr (KEEP) {
+                    px = kx[k];
+                    pd = kdy[k];
+                    pg = kg[k];
+                } else {
+                    px = load_piece<T, VEC>(sx, k, group, sub, cols);
+                    pd = load_piece<T, VEC>(sdy, k, group, sub, cols);
+                    pg = load_piece<T, VEC>(sgamma, k, group, sub, h);
+                }
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    const float2 d = pair_of(pd, i);
+                    const float2 xc = add2(pair_of(px, i), both(-mu));
+                    const float2 gj = product<VEC>(d, pair_of(pg, i));
+                    set_pair(o, i, fma2(both(rs), add2(gj, both(-mg)), mul2(xc, both(-k2))));
+                    acc_g[k * PAIRS + i] = fma2(mul2(d, both(rs)), xc, acc_g[k * PAIRS + i]);
+                    acc_b[k * PAIRS + i] = add2(acc_b[k * PAIRS + i], d);
+                }
+                store_piece<T, VEC>(dx + base, o, k, group, sub, cols);
+            }
+        }
+        if (next >= blocks) break;
+        const int freed = stage;  // !KEEP: read for the last time just now
+        if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        m = begin(next, stage, phase, st_next.x);
+        parity ^= 1;
+        m = group_sum(m, p.W, scratch[parity]);
+        if (p.W == 1) __syncthreads();  // else group_sum's barrier did it
+        if (threadIdx.x == 0) {
+            if constexpr (KEEP)
+                issue(next + p.stages * step, stage);
+            else
+                issue(blk + p.stages * step, freed);
+        }
+        blk = next;
+        st = st_next;
+        st_next = st_after;
+    }
+
+    float* out_g = part_g + static_cast<long long>(blockIdx.x) * h;
+    float* out_b = part_b + static_cast<long long>(blockIdx.x) * h;
+    if (R == 1) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            store_pairs<VEC>(out_g, &acc_g[k * PAIRS], k, group, sub, h);
+            store_pairs<VEC>(out_b, &acc_b[k * PAIRS], k, group, sub, h);
+        }
+        return;
+    }
+    // The ring's buffers are free: every copy has been waited for and read.
+    // Pair i of a thread sits at i group + sub, so that a warp's accesses are
+    // consecutive.
+    float2* sg = reinterpret_cast<float2*>(ring);
+    float2* sb = sg + NV * PAIRS * group;
+    for (int r = 0; r < R; ++r) {
+        __syncthreads();
+        if (g == r) {
+#pragma unroll
+            for (int i = 0; i < NV * PAIRS; ++i) {
+                const int o = i * group + sub;
+                sg[o] = r ? add2(sg[o], acc_g[i]) : acc_g[i];
+                sb[o] = r ? add2(sb[o], acc_b[i]) : acc_b[i];
+            }
+        }
+    }
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                acc_g[k * PAIRS + i] = sg[(k * PAIRS + i) * group + sub];
+                acc_b[k * PAIRS + i] = sb[(k * PAIRS + i) * group + sub];
+            }
+            store_pairs<VEC>(out_g, &acc_g[k * PAIRS], k, group, sub, h);
+            store_pairs<VEC>(out_b, &acc_b[k * PAIRS], k, group, sub, h);
+        }
+    }
+}
+
+// dgamma[c] = sum_i part_g[i][c], dbeta likewise: 32 interleaved chains (a
+// warp each) over i, then the chains in order.
+__global__ void __launch_bounds__(1024)
+    norm_param_reduce_kernel(const float* __restrict__ part_g, const float* __restrict__ part_b,
+                             int n, int h, float* __restrict__ dgamma, float* __restrict__ dbeta) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // the parts come from the kernel before this one
+    __shared__ float chain[32][33];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+    const float* part = blockIdx.y ? part_b : part_g;
+    float s = 0.0f;
+    if (c < h) {
+#pragma unroll 4
+        for (int i = w; i < n; i += 32) s += __ldg(part + static_cast<long long>(i) * h + c);
+    }
+    chain[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < h) {
+        s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s += chain[j][lane];
+        (blockIdx.y ? dbeta : dgamma)[c] = s;
+    }
+}
+
+// ---------------------------------------------------------- any row width
+// Rows beyond what the kernels above hold: one CTA a row, the row read from
+// memory (L2) again for each step.
 
 constexpr int kRowThreads = 256;
 
@@ -139,37 +628,165 @@ __global__ void __launch_bounds__(256)
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
-template <typename T>
-cudaError_t forward(const void* x, const void* gamma, const void* beta, int T_, int h, float eps,
-                    void* y, float* mean, float* rstd, cudaStream_t st, int* launches) {
-    ++*launches;
-    return launch_dependent(norm_forward_kernel<T>, dim3(T_), dim3(kRowThreads), 0, st,
-                            static_cast<const T*>(x), static_cast<const T*>(gamma),
-                            static_cast<const T*>(beta), h, eps, static_cast<T*>(y), mean, rstd);
+constexpr int kSms = 152;
+
+int ceil_pow2(int x) {
+    int p = 1;
+    while (p < x) p *= 2;
+    return p;
+}
+
+template <typename T, int VEC, int NV>
+cudaError_t forward_reg(const T* x, const T* gamma, const T* beta, int T_, int h, int W, float eps, T* y,
+                        float* mean, float* rstd, cudaStream_t st) {
+    const int threads = std::max(256, 32 * W), rows = threads / (32 * W);
+    return launch_dependent(norm_forward_reg_kernel<T, VEC, NV>, dim3(ceil_div(T_, rows)), dim3(threads), 0,
+                            st, x, gamma, beta, T_, h, W, eps, y, mean, rstd);
+}
+
+// W warps a row, 32 values a thread at most.
+template <typename T, int VEC>
+cudaError_t forward_rows(const T* x, const T* gamma, const T* beta, int T_, int h, float eps, T* y,
+                         float* mean, float* rstd, cudaStream_t st) {
+    // 32 values a thread keep the most loads in flight an SM; with few rows
+    // more threads a row, down to 8 values each, fill the SMs instead.
+    // (Single values want more registers each than pieces: 16 a thread.)
+    int per = VEC == 1 && h <= 16 * 1024 ? 16 : 32;
+    while (per > 8 && static_cast<long long>(T_) * ceil_div(h, 32 * per) < 16LL * kSms &&
+           ceil_div(h, 32 * per / 2) <= 32)
+        per /= 2;
+    // rows beyond 16 warps of that: 40 values a thread, so that two rows (two
+    // CTAs of 512 threads) share an SM and one's sums overlap the other's loads
+    if (per == 32 && h > 16 * 1024 && h <= 20 * 1024)
+        return forward_reg<T, VEC, 40 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, 16, eps, y, mean, rstd, st);
+    const int W = ceil_pow2(ceil_div(h, 32 * per));
+    if (per == 32) return forward_reg<T, VEC, 32 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
+    if (per == 16) return forward_reg<T, VEC, 16 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
+    return forward_reg<T, VEC, 8 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
 }
 
 template <typename T>
-cudaError_t backward(const void* dy, const void* x, const void* gamma, const float* mean,
-                     const float* rstd, int T_, int h, void* dx, float* dgamma, float* dbeta,
-                     float* partial, cudaStream_t st, int* launches) {
-    cudaError_t e = launch_dependent(norm_backward_kernel<T>, dim3(T_), dim3(kRowThreads), 0, st,
-                                     static_cast<const T*>(dy), static_cast<const T*>(x),
-                                     static_cast<const T*>(gamma), mean, rstd, h, static_cast<T*>(dx));
-    if (e != cudaSuccess) return e;
+cudaError_t forward(const void* x_, const void* gamma_, const void* beta_, int T_, int h, float eps,
+                    void* y_, float* mean, float* rstd, cudaStream_t st, int* launches) {
+    const T *x = static_cast<const T*>(x_), *gamma = static_cast<const T*>(gamma_),
+            *beta = static_cast<const T*>(beta_);
+    T* y = static_cast<T*>(y_);
     ++*launches;
-    const int chunks = norm_param_chunks(T_, h);
-    e = launch_dependent(norm_param_grad_kernel<T>, dim3(ceil_div(h, 32), chunks), dim3(256), 0, st,
-                         static_cast<const T*>(dy), static_cast<const T*>(x), mean, rstd, T_, h,
-                         ceil_div(T_, chunks), partial);
+    constexpr int VEC = 16 / sizeof(T);
+    if (h <= 32 * 32 * 32) {
+        if (h % VEC == 0) return forward_rows<T, VEC>(x, gamma, beta, T_, h, eps, y, mean, rstd, st);
+        return forward_rows<T, 1>(x, gamma, beta, T_, h, eps, y, mean, rstd, st);
+    }
+    return launch_dependent(norm_forward_kernel<T>, dim3(T_), dim3(kRowThreads), 0, st, x, gamma, beta, h, eps,
+                            y, mean, rstd);
+}
+
+// How a backward call runs: the ring kernel with W warps a row and 16 (narrow)
+// or 40 (wide) values a thread, or, CTAs = 0, the kernels for any width.
+struct NormPlan {
+    int ctas, W, stages, buf_bytes, threads, smem;
+    bool wide;
+};
+
+// CTAs an SM of the 256-thread form: 16 values a thread in 16-bit pieces take
+// 80 registers, in fp32 or one by one up to 128.
+template <typename T, int VEC>
+constexpr int kNormCtas = 2;
+
+constexpr int kSmemMost = 227 * 1024;
+
+NormPlan norm_plan(int T, int h, int elem) {
+    NormPlan p{};
+    p.wide = h > 16 * 512;
+    p.W = p.wide ? 16 : ceil_pow2(ceil_div(h, 32 * 16));
+    p.threads = p.wide || p.W == 16 ? 512 : 256;
+    if (h > 40 * 512) return p;
+    const int R = p.threads / (32 * p.W);
+    // a block of R rows and what its first and last granule hold besides
+    p.buf_bytes = (static_cast<int>((static_cast<long long>(R) * h * elem + 15) / 16) + 1) * 16;
+    const int per_sm = p.threads == 512 ? 1 : 2;
+    const int room = per_sm == 1 ? kSmemMost - 1024 : (kSmemMost / per_sm - 2048) & ~127;
+    const int own = p.wide ? (h * elem + 15) / 16 * 16 : 0;  // gamma
+    p.stages = std::min(kNormMaxStages, (room - own) / (2 * p.buf_bytes));
+    if (p.stages < 2) return p;  // not even two rows fit: fp32 rows beyond 11000 values
+    const int blocks = ceil_div(T, R);
+    p.stages = std::min(p.stages, std::max(2, ceil_div(blocks, kSms * per_sm)));
+    // the meeting place of the groups' sums: 16 values a thread and tensor
+    p.smem = std::max(p.stages * 2 * p.buf_bytes + own, R > 1 ? 2 * 16 * 4 * 32 * p.W : 0);
+    p.ctas = std::min(blocks, kSms * per_sm);
+    return p;
+}
+
+template <typename T, int VEC, int NV, int NT, int MIN_CTAS, bool KEEP>
+cudaError_t backward_ring(const NormPlan& p, const T* dy, const T* x, const T* gamma, const float* mean,
+                          const float* rstd, int T_, int h, T* dx, float* pg, float* pb, int* status,
+                          cudaStream_t st) {
+    auto kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, KEEP>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
-    ++*launches;
-    if ((e = launch_rowsum_f32(partial, chunks, h, dgamma, st, launches)) != cudaSuccess) return e;
-    return launch_rowsum_f32(partial + static_cast<size_t>(chunks) * h, chunks, h, dbeta, st, launches);
+    const NormBackwardArgs a{T_, h, p.W, p.stages, p.buf_bytes, status};
+    return launch_dependent(kern, dim3(p.ctas), dim3(NT), p.smem, st, dy, x, gamma, mean, rstd, a, dx, pg, pb);
+}
+
+template <typename T, int VEC>
+cudaError_t backward_rows(const NormPlan& p, const T* dy, const T* x, const T* gamma, const float* mean,
+                          const float* rstd, int T_, int h, T* dx, float* pg, float* pb, int* status,
+                          cudaStream_t st) {
+    if (p.wide)
+        return backward_ring<T, VEC, 40 / Piece<T, VEC>::N, 512, 1, false>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb,
+                                                              status, st);
+    if (p.threads == 512)
+        return backward_ring<T, VEC, 16 / Piece<T, VEC>::N, 512, 1, true>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb,
+                                                             status, st);
+    return backward_ring<T, VEC, 16 / Piece<T, VEC>::N, 256, kNormCtas<T, VEC>, true>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status,
+                                                         st);
+}
+
+template <typename T>
+cudaError_t backward(const void* dy_, const void* x_, const void* gamma_, const float* mean,
+                     const float* rstd, int T_, int h, void* dx_, float* dgamma, float* dbeta,
+                     float* partial, int* status, cudaStream_t st, int* launches) {
+    const T *dy = static_cast<const T*>(dy_), *x = static_cast<const T*>(x_),
+            *gamma = static_cast<const T*>(gamma_);
+    T* dx = static_cast<T*>(dx_);
+    cudaError_t e;
+    const NormPlan p = norm_plan(T_, h, sizeof(T));
+    if (p.ctas > 0) {
+        constexpr int VEC = 16 / sizeof(T);
+        // one CTA: its sums are the result
+        float* pg = p.ctas == 1 ? dgamma : partial;
+        float* pb = p.ctas == 1 ? dbeta : partial + static_cast<size_t>(p.ctas) * h;
+        if (h % VEC == 0)
+            e = backward_rows<T, VEC>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st);
+        else
+            e = backward_rows<T, 1>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        if (p.ctas == 1) return cudaSuccess;
+        ++*launches;
+        return launch_dependent(norm_param_reduce_kernel, dim3(ceil_div(h, 32), 2), dim3(1024), 0, st,
+                                static_cast<const float*>(pg), static_cast<const float*>(pb), p.ctas, h, dgamma,
+                                dbeta);
+    }
+    e = launch_dependent(norm_backward_kernel<T>, dim3(T_), dim3(kRowThreads), 0, st, dy, x, gamma, mean, rstd,
+                         h, dx);
+    if (e != cudaSuccess) return e;
+    const int chunks = norm_param_parts(T_, h, sizeof(T));
+    float* pb = partial + static_cast<size_t>(chunks) * h;
+    e = launch_dependent(norm_param_grad_kernel<T>, dim3(ceil_div(h, 32), chunks), dim3(256), 0, st, dy, x,
+                         mean, rstd, T_, h, ceil_div(T_, chunks), partial);
+    if (e != cudaSuccess) return e;
+    *launches += 3;
+    return launch_dependent(norm_param_reduce_kernel, dim3(ceil_div(h, 32), 2), dim3(1024), 0, st,
+                            static_cast<const float*>(partial), static_cast<const float*>(pb), chunks, h, dgamma,
+                            dbeta);
 }
 
 }  // namespace
 
-int norm_param_chunks(int T, int h) {
+int norm_param_parts(int T, int h, int elem) {
+    const NormPlan p = norm_plan(T, h, elem);
+    if (p.ctas > 0) return p.ctas;
     const long long col_blocks = (h + 31) / 32;
     return static_cast<int>(std::max(1LL, std::min<long long>((1216 + col_blocks - 1) / col_blocks, (T + 31) / 32)));
 }
@@ -186,15 +803,16 @@ cudaError_t launch_norm_forward(int dtype, const void* x, const void* gamma, con
 
 cudaError_t launch_norm_backward(int dtype, const void* dy, const void* x, const void* gamma,
                                  const float* mean, const float* rstd, int T, int h, void* dx,
-                                 float* dgamma, float* dbeta, float* partial, cudaStream_t st,
+                                 float* dgamma, float* dbeta, float* partial, int* status, cudaStream_t st,
                                  int* launches) {
+    auto run = [&](auto* t) {
+        return backward<std::remove_pointer_t<decltype(t)>>(dy, x, gamma, mean, rstd, T, h, dx, dgamma, dbeta,
+                                                            partial, status, st, launches);
+    };
     switch (dtype) {
-        case TPMLP_BF16:
-            return backward<__nv_bfloat16>(dy, x, gamma, mean, rstd, T, h, dx, dgamma, dbeta, partial, st, launches);
-        case TPMLP_FP16:
-            return backward<__half>(dy, x, gamma, mean, rstd, T, h, dx, dgamma, dbeta, partial, st, launches);
-        default:
-            return backward<float>(dy, x, gamma, mean, rstd, T, h, dx, dgamma, dbeta, partial, st, launches);
+        case TPMLP_BF16: return run(static_cast<__nv_bfloat16*>(nullptr));
+        case TPMLP_FP16: return run(static_cast<__half*>(nullptr));
+        default: return run(static_cast<float*>(nullptr));
     }
 }
 

@@ -150,6 +150,15 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* m, uint32_t bar, 
         : "memory");
 }
 
+// Untiled bulk copy of `bytes` (a multiple of 16) global -> shared, both
+// 16-byte aligned, completion counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // 3-D tiled bulk tensor copy shared (this CTA, address `src`) -> global,
 // tracked by the issuing thread's bulk async-groups.  Parts of the box
 // outside the tensor are not written.
