@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -36,6 +37,10 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 constexpr int kNormMaxStages = 6;
+constexpr int kNormMaxCluster = 8;
+// Blocks begun before the one that is finished.  The ring needs twice as
+// many stages: 16-bit values have six, fp32 three.
+constexpr int norm_ahead(int elem) { return elem == 2 ? 2 : 1; }
 
 // A piece of a row held by one thread: VEC > 1 consecutive values, 16 bytes,
 // or (VEC 1, rows that do not start on 16-byte boundaries) two single values
@@ -72,6 +77,25 @@ __device__ __forceinline__ Piece<T, VEC> load_piece(const T* p, int k, int group
     } else {
         const uint32_t lo = c < h ? reinterpret_cast<const uint16_t*>(p)[c] : 0u;
         const uint32_t hi = c + group < h ? reinterpret_cast<const uint16_t*>(p)[c + group] : 0u;
+        r.w[0] = lo | (hi << 16);
+    }
+    return r;
+}
+
+// The same without a branch: columns behind the row read some value of it.
+template <typename T, int VEC>
+__device__ __forceinline__ Piece<T, VEC> load_piece_any(const T* p, int k, int group, int sub, int h) {
+    Piece<T, VEC> r;
+    const int c = piece_col<VEC>(k, 0, group, sub);
+    if constexpr (VEC > 1) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + min(c, h - VEC));
+        r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+    } else if constexpr (sizeof(T) == 4) {
+        r.w[0] = reinterpret_cast<const uint32_t*>(p)[min(c, h - 1)];
+        r.w[1] = reinterpret_cast<const uint32_t*>(p)[min(c + group, h - 1)];
+    } else {
+        const uint32_t lo = reinterpret_cast<const uint16_t*>(p)[min(c, h - 1)];
+        const uint32_t hi = reinterpret_cast<const uint16_t*>(p)[min(c + group, h - 1)];
         r.w[0] = lo | (hi << 16);
     }
     return r;
@@ -165,16 +189,21 @@ __device__ __forceinline__ void store_pairs(float* p, const float2* v, int k, in
     }
 }
 
-// Sum over the W warps of a row's group (W a power of two; warps W g .. W g +
-// W - 1 of the CTA); every thread receives the total, added in the same
-// order in every thread.  `scratch` holds one entry a warp.  All threads of
-// the CTA call it.
-__device__ __forceinline__ float2 group_sum(float2 x, int W, float2* scratch) {
+__device__ __forceinline__ float2 warp_sum(float2 x) {
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) {
         x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, off);
         x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, off);
     }
+    return x;
+}
+
+// Sum over the W warps of a row's group (W a power of two; warps W g .. W g +
+// W - 1 of the CTA); every thread receives the total, added in the same
+// order in every thread.  `scratch` holds one entry a warp.  All threads of
+// the CTA call it.
+__device__ __forceinline__ float2 group_sum(float2 x, int W, float2* scratch) {
+    x = warp_sum(x);
     if (W == 1) return x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) scratch[warp] = x;
@@ -215,15 +244,16 @@ __global__ void __launch_bounds__(1024)
     const float mu = group_sum(make_float2(acc.x + acc.y, 0.0f), W, scratch[0]).x / static_cast<float>(h);
     acc = both(0.0f);
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        // the zeros behind the row are not its values
+        if (piece_col<VEC>(k, 0, group, sub) >= h) continue;
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
             float2 c = add2(pair_of(in[k], i), both(-mu));
-            // the zeros behind the row are not its values
-            if (piece_col<VEC>(k, 2 * i, group, sub) >= h) c.x = 0.0f;
-            if (piece_col<VEC>(k, 2 * i + 1, group, sub) >= h) c.y = 0.0f;
+            if (VEC == 1 && piece_col<VEC>(k, 1, group, sub) >= h) c.y = 0.0f;
             acc = fma2(c, c, acc);
         }
+    }
     const float var = group_sum(make_float2(acc.x + acc.y, 0.0f), W, scratch[1]).x / static_cast<float>(h);
     const float rs = 1.0f / sqrtf(var + eps);
     if (!ok) return;
@@ -247,214 +277,255 @@ __global__ void __launch_bounds__(1024)
 // warps a row) stream through a ring of `stages` buffers in shared memory,
 // one bulk copy a tensor and block (the rows of a block are one contiguous
 // range), so that the loads in flight do not depend on the registers; block
-// b goes to CTA b mod grid.  Every thread keeps the same columns in every
-// row and adds its part of dgamma and dbeta in registers; at the end the
-// CTA's groups meet in shared memory, in group order, and the CTA's sums go
-// to part[0 / 1][CTA][column].
-// The loop is skewed by half a block: it finishes block i (dx from its row
-// sums) and then begins block i + 1 (its row sums), with one CTA barrier
-// between the two, so that a block's latencies overlap the other's work.
-// KEEP: a thread's values of a row stay in registers between the row sums
-// and dx, and gamma with them; else both are read from shared memory again
-// (wide rows, where the accumulators take the registers).
+// b goes to CTA (or cluster) b mod their number.  Every thread keeps the
+// same columns in every row and adds its part of dgamma and dbeta in
+// registers; at the end the CTA's groups meet in shared memory, in group
+// order, and the sums go to part[0 / 1][CTA or cluster][column].
+// Rows wider than a CTA's registers are cut over the `cl` CTAs of a cluster
+// (one row at a time, `cols` columns each).
+// There is no barrier in the loop.  A warp begins block i + AHEAD (its part of
+// the row sums, which go to the shared memory of every CTA of the row and are
+// counted on an mbarrier there) before it finishes block i
+// (dx, from the sums of all warps, which have long arrived): with a barrier a
+// block, a cluster's exchange of about a microsecond stands in every row.
 struct NormBackwardArgs {
     int rows, h, W, stages;
+    int cl, cols;   // CTAs a row, columns of one
     int buf_bytes;  // one tensor's block in the ring, 16-byte multiple
     int* status;
 };
 
-template <typename T, int VEC, int NV, int NT, int MIN_CTAS, bool KEEP>
+template <typename T, int VEC, int NV, int NT, int MIN_CTAS>
 __global__ void __launch_bounds__(NT, MIN_CTAS)
     norm_backward_ring_kernel(const T* __restrict__ dy, const T* __restrict__ x,
                               const T* __restrict__ gamma, const float* __restrict__ mean,
                               const float* __restrict__ rstd, const NormBackwardArgs p,
                               T* __restrict__ dx, float* __restrict__ part_g,
                               float* __restrict__ part_b) {
+    constexpr int AHEAD = norm_ahead(sizeof(T)), SLOTS = 2 * AHEAD;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kNormMaxStages];
-    __shared__ float2 scratch[2][NT / 32];
+    __shared__ uint64_t sums[SLOTS];  // a block's sums of all warps have arrived
+    __shared__ float2 slots[SLOTS][kNormMaxCluster * (NT / 32)];
     __shared__ uint32_t abort_flag;
     pdl_launch_dependents();  // the next kernel may begin its launch
+    constexpr long long E = sizeof(T);
     const int group = 32 * p.W, R = NT / group;
     const int g = threadIdx.x / group, sub = threadIdx.x % group;
-    const int h = p.h;
+    const int cl = p.cl;
+    const int rank = cl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int unit = cl > 1 ? static_cast<int>(blockIdx.x) / cl : static_cast<int>(blockIdx.x);
+    const int c0 = rank * p.cols;              // this CTA's columns of a row
+    const int h = min(p.cols, p.h - c0);
     const int blocks = (p.rows + R - 1) / R;
-    const long long total = static_cast<long long>(p.rows) * h * sizeof(T);  // bytes of a tensor
-    T* sgamma = reinterpret_cast<T*>(ring + static_cast<size_t>(p.stages) * 2 * p.buf_bytes);  // !KEEP
+    const long long total = E * p.rows * p.h;  // bytes of a tensor
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        // a cluster counts the bytes that its warps send, one CTA its warps
+        for (int s = 0; s < SLOTS; ++s) mbar_init(&sums[s], cl > 1 ? 1 : NT / 32);
         abort_flag = 0u;
         fence_mbar_init();
     }
     pdl_wait();  // dy may come from the kernel before this one
-    if constexpr (!KEEP)
-        for (int c = threadIdx.x; c < h; c += NT) sgamma[c] = gamma[c];
-    __syncthreads();
+    if (cl > 1)
+        cluster_sync();  // the peers run: their shared memory may be written
+    else
+        __syncthreads();
 
-    // The block's byte range, and the part of it that is copied: whole
-    // 16-byte granules of the tensor (all but its last few bytes).
-    auto range = [&](int blk, long long& b0, long long& b1, long long& a0, long long& a1) {
-        b0 = static_cast<long long>(blk) * R * h * sizeof(T);
-        const long long rows_end = min(static_cast<long long>(blk + 1) * R, static_cast<long long>(p.rows));
-        b1 = rows_end * h * static_cast<long long>(sizeof(T));
+    // This CTA's blocks are unit, unit + step, ..., n of them.  Everything a
+    // block needs advances by additions: with divisions and 64-bit addresses
+    // in the loop the overhead was 490 instructions a warp and block against
+    // 200 of arithmetic.
+    const uint32_t step = gridDim.x / cl;
+    const int n = blocks > unit ? static_cast<int>((blocks - unit + step - 1) / step) : 0;
+    const uint32_t rows = p.rows, row_step = step * R;
+    const uint32_t stage_bytes = 2u * p.buf_bytes;
+
+    // Thread 0: copies of the next block not yet issued into the next stage.
+    // Of the block's byte range whole 16-byte granules of the tensor are
+    // copied (all but its last few bytes).
+    const long long first_b0 = E * (static_cast<long long>(unit) * R * p.h + c0);
+    long long issue_b0 = first_b0;
+    const long long issue_step = E * step * R * p.h;
+    const int block_bytes = static_cast<int>(E) * (cl > 1 ? h : R * p.h);
+    int issue_left = n, issue_stage = 0;
+    auto copied = [&](long long b0, long long& a0) {  // first byte, and their number
         a0 = b0 & ~15LL;
-        a1 = min((b1 + 15) & ~15LL, total & ~15LL);
-        if (a1 < a0) a1 = a0;
+        const long long row_end = cl > 1 ? b0 + block_bytes : min(b0 + block_bytes, total);
+        const long long a1 = min((row_end + 15) & ~15LL, total & ~15LL);
+        return a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
     };
-    auto issue = [&](long long blk, int stage) {  // one thread
-        if (blk >= blocks) return;
-        long long b0, b1, a0, a1;
-        range(static_cast<int>(blk), b0, b1, a0, a1);
-        const uint32_t n = static_cast<uint32_t>(a1 - a0);
-        const uint32_t dst = smem_u32(ring) + static_cast<uint32_t>(stage) * 2u * p.buf_bytes;
-        mbar_arrive_expect_tx(&full[stage], 2 * n);
-        if (n) {
-            bulk_load(dst, reinterpret_cast<const uint8_t*>(x) + a0, n, &full[stage]);
-            bulk_load(dst + p.buf_bytes, reinterpret_cast<const uint8_t*>(dy) + a0, n, &full[stage]);
+    auto issue = [&]() {
+        if (issue_left <= 0) return;
+        long long a0;
+        const uint32_t bytes = copied(issue_b0, a0);
+        const uint32_t dst = smem_u32(ring) + issue_stage * stage_bytes;
+        mbar_arrive_expect_tx(&full[issue_stage], 2 * bytes);
+        if (bytes) {
+            bulk_load(dst, reinterpret_cast<const uint8_t*>(x) + a0, bytes, &full[issue_stage]);
+            bulk_load(dst + p.buf_bytes, reinterpret_cast<const uint8_t*>(dy) + a0, bytes, &full[issue_stage]);
         }
+        issue_b0 += issue_step;
+        --issue_left;
+        if (++issue_stage == p.stages) issue_stage = 0;
     };
-    const long long step = gridDim.x;
     if (threadIdx.x == 0)
-        for (int s = 0; s < p.stages; ++s) issue(blockIdx.x + s * step, s);
+        for (int s = 0; s < p.stages; ++s) issue();
 
-    constexpr int N = Piece<T, VEC>::N, PAIRS = N / 2;
+    constexpr int PAIRS = Piece<T, VEC>::N / 2;
     float2 acc_g[NV * PAIRS], acc_b[NV * PAIRS];
-    Piece<T, VEC> kx[KEEP ? NV : 1], kdy[KEEP ? NV : 1], kg[KEEP ? NV : 1];
+    Piece<T, VEC> kg[NV];  // gamma, 0 behind the row: what is read there counts nothing
 #pragma unroll
     for (int i = 0; i < NV * PAIRS; ++i) acc_g[i] = acc_b[i] = both(0.0f);
-    if constexpr (KEEP) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) kg[k] = load_piece<T, VEC>(gamma, k, group, sub, h);
-    }
-    const float inv_h = 1.0f / static_cast<float>(h);
-    // the statistics of this group's row of a block (0 behind the last row)
-    auto row_stats = [&](long long blk) {
-        const long long row = blk * R + g;
-        return row < p.rows ? make_float2(__ldg(mean + row), __ldg(rstd + row)) : make_float2(0.0f, 0.0f);
+    for (int k = 0; k < NV; ++k) kg[k] = load_piece<T, VEC>(gamma + c0, k, group, sub, h);
+    const float inv_h = 1.0f / static_cast<float>(p.h);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the statistics of a row (0 behind the last)
+    auto row_stats = [&](uint32_t row) {
+        return row < rows ? make_float2(__ldg(mean + row), __ldg(rstd + row)) : make_float2(0.0f, 0.0f);
     };
-    // this group's row of the block in a stage's buffers
-    auto row_ptr = [&](long long blk, int stage, const T*& sx, const T*& sdy) {
-        long long skip = 0;  // bytes before the block in its first granule
-        if constexpr (VEC == 1) skip = (blk * R * h * static_cast<long long>(sizeof(T))) & 15;
-        const uint8_t* b = ring + static_cast<size_t>(stage) * 2 * p.buf_bytes + skip;
-        sx = reinterpret_cast<const T*>(b) + static_cast<size_t>(g) * h;
-        sdy = reinterpret_cast<const T*>(b + p.buf_bytes) + static_cast<size_t>(g) * h;
+    // This group's row of a block in a stage's buffers; `skip`: where the block
+    // starts in its first 16-byte granule (rows of VEC 1 only).
+    const uint32_t group_off = static_cast<uint32_t>(E) * g * h;
+    const uint32_t skip0 = VEC == 1 ? static_cast<uint32_t>(first_b0 & 15) : 0u;
+    const uint32_t skip_step = VEC == 1 ? static_cast<uint32_t>(issue_step & 15) : 0u;
+    auto row_at = [&](int stage, uint32_t skip) {
+        return reinterpret_cast<const T*>(ring + (stage * stage_bytes + skip + group_off));
     };
-    // Begins a block: waits for its copies and takes this thread's part of
-    // its row's sums of g and g (x - mu).
-    auto begin = [&](long long blk, int stage, uint32_t phase, float mu) {
-        // A wait that gives up has set the status word; the loop goes on (on
-        // whatever the buffer holds), so that no barrier is left short.
-        warp_wait_bounded(&full[stage], phase, &abort_flag, p.status);
+    // Begins the CTA's i-th block: waits for its copies and sends this warp's
+    // part of its row's sums of g and g (x - mu) to every CTA of the row.
+    // (A wait that gives up has set the status word; the loop goes on, on
+    // whatever the buffers hold.)
+    int b_stage = 0, b_slot = 0;
+    uint32_t b_phase = 0, b_skip = skip0, b_row = static_cast<uint32_t>(unit) * R + g;
+    auto begin = [&](int i, float mu) {
+        warp_wait_polls(&full[b_stage], b_phase, &abort_flag, p.status);
         if constexpr (VEC == 1) {
-            long long b0, b1, a0, a1;
-            range(static_cast<int>(blk), b0, b1, a0, a1);
-            if (a1 < b1) {  // the tensor's last few bytes: plain loads
-                const long long e = max(a1, b0) / static_cast<long long>(sizeof(T)) + threadIdx.x;
-                const long long o = e * static_cast<long long>(sizeof(T)) - a0;
-                uint8_t* b = ring + static_cast<size_t>(stage) * 2 * p.buf_bytes + o;
-                if (e < b1 / static_cast<long long>(sizeof(T))) {
-                    *reinterpret_cast<T*>(b) = x[e];
-                    *reinterpret_cast<T*>(b + p.buf_bytes) = dy[e];
+            if (i == n - 1) {  // the tensor's last few bytes, if they are here: plain loads
+                const long long b0 = first_b0 + i * issue_step;
+                long long a0;
+                const uint32_t bytes = copied(b0, a0);
+                const long long b1 = cl > 1 ? b0 + block_bytes : min(b0 + block_bytes, total);
+                const long long e = max(a0 + bytes, b0) / E + threadIdx.x;
+                if (e < b1 / E) {
+                    uint8_t* d = ring + b_stage * stage_bytes + (e * E - a0);
+                    *reinterpret_cast<T*>(d) = x[e];
+                    *reinterpret_cast<T*>(d + p.buf_bytes) = dy[e];
                 }
                 __syncthreads();
             }
         }
-        // columns of this thread's row (none behind the last row: the sums get
-        // zeros, as dy and gamma read 0)
-        const int cols = blk * R + g < p.rows ? h : 0;
-        const T *sx, *sdy;
-        row_ptr(blk, stage, sx, sdy);
         float2 m = both(0.0f), mx = both(0.0f);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const Piece<T, VEC> px = load_piece<T, VEC>(sx, k, group, sub, cols);
-            const Piece<T, VEC> pd = load_piece<T, VEC>(sdy, k, group, sub, cols);
-            Piece<T, VEC> pg;
-            if constexpr (KEEP) {
-                kx[k] = px;
-                kdy[k] = pd;
-                pg = kg[k];
-            } else {
-                pg = load_piece<T, VEC>(sgamma, k, group, sub, h);
-            }
-#pragma unroll
-            for (int i = 0; i < PAIRS; ++i) {
-                const float2 gj = product<VEC>(pair_of(pd, i), pair_of(pg, i));
-                m = add2(m, gj);
-                mx = fma2(gj, add2(pair_of(px, i), both(-mu)), mx);
-            }
-        }
-        return make_float2(m.x + m.y, mx.x + mx.y);
-    };
-
-    int stage = 0, parity = 0;
-    uint32_t phase = 0;
-    long long blk = blockIdx.x;
-    float2 st = row_stats(blk), st_next = row_stats(blk + step);
-    float2 m = group_sum(begin(blk, 0, 0, st.x), p.W, scratch[0]);
-    if constexpr (KEEP) {
-        if (p.W == 1) __syncthreads();  // else group_sum's barrier did it
-        if (threadIdx.x == 0) issue(blk + p.stages * step, 0);
-    }
-    while (true) {
-        const long long next = blk + step;
-        const float2 st_after = row_stats(next + step);
-        {  // finish block blk: m = its row's sums
-            const int cols = blk * R + g < p.rows ? h : 0;
-            const float mu = st.x, rs = st.y;
-            const float mg = m.x * inv_h;                   // mean(g)
-            const float k2 = rs * rs * rs * (m.y * inv_h);  // rstd^2 mean(g xhat)
-            const T *sx, *sdy;
-            row_ptr(blk, stage, sx, sdy);
-            const long long base = (blk * R + g) * h;
+        if (b_row < rows) {
+            const T* sx = row_at(b_stage, b_skip);
+            const T* sdy = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(sx) + p.buf_bytes);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                Piece<T, VEC> px, pd, pg, o;
-                if constexpr (KEEP) {
-                    px = kx[k];
-                    pd = kdy[k];
-                    pg = kg[k];
-                } else {
-                    px = load_piece<T, VEC>(sx, k, group, sub, cols);
-                    pd = load_piece<T, VEC>(sdy, k, group, sub, cols);
-                    pg = load_piece<T, VEC>(sgamma, k, group, sub, h);
-                }
+                const Piece<T, VEC> px = load_piece_any<T, VEC>(sx, k, group, sub, h);
+                const Piece<T, VEC> pd = load_piece_any<T, VEC>(sdy, k, group, sub, h);
 #pragma unroll
-                for (int i = 0; i < PAIRS; ++i) {
-                    const float2 d = pair_of(pd, i);
-                    const float2 xc = add2(pair_of(px, i), both(-mu));
-                    const float2 gj = product<VEC>(d, pair_of(pg, i));
-                    set_pair(o, i, fma2(both(rs), add2(gj, both(-mg)), mul2(xc, both(-k2))));
-                    acc_g[k * PAIRS + i] = fma2(mul2(d, both(rs)), xc, acc_g[k * PAIRS + i]);
-                    acc_b[k * PAIRS + i] = add2(acc_b[k * PAIRS + i], d);
+                for (int j = 0; j < PAIRS; ++j) {
+                    const float2 gj = product<VEC>(pair_of(pd, j), pair_of(kg[k], j));
+                    m = add2(m, gj);
+                    mx = fma2(gj, add2(pair_of(px, j), both(-mu)), mx);
                 }
-                store_piece<T, VEC>(dx + base, o, k, group, sub, cols);
             }
         }
-        if (next >= blocks) break;
-        const int freed = stage;  // !KEEP: read for the last time just now
-        if (++stage == p.stages) {
-            stage = 0;
+        m = warp_sum(make_float2(m.x + m.y, mx.x + mx.y));
+        uint64_t* bar = &sums[b_slot];
+        float2* slot = &slots[b_slot][rank * (NT / 32) + warp];
+        if (cl == 1) {
+            if (lane == 0) {
+                *slot = m;
+                mbar_arrive(bar);  // releases the slot to the waiting warps
+            }
+        } else {
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * (NT / 32) * sizeof(float2));
+            if (lane < cl)
+                st_async_v2(map_to_cta(smem_u32(slot), lane), m, map_to_cta(smem_u32(bar), lane));
+        }
+        __syncwarp();
+        if (++b_stage == p.stages) {
+            b_stage = 0;
+            b_phase ^= 1u;
+        }
+        b_slot = b_slot + 1 == SLOTS ? 0 : b_slot + 1;
+        b_skip = (b_skip + skip_step) & 15;
+        b_row += row_step;
+    };
+
+    // Slots and stages.  A warp sends block i + AHEAD behind its finish of
+    // block i, for which it had the sums of block i: every warp of the row had
+    // begun block i, so had finished block i - AHEAD and read its slots.  So 2
+    // AHEAD slots are enough; and the buffers of block i - AHEAD are free.
+    uint32_t row = b_row;
+    float2 st[AHEAD], st_next;
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+        st[a] = row_stats(row + a * row_step);
+        if (a < n) begin(a, st[a].x);
+    }
+    st_next = row_stats(row + AHEAD * row_step);
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, skip = skip0;
+    T* out = dx + static_cast<long long>(row) * p.h + c0;
+    const long long out_step = static_cast<long long>(row_step) * p.h;
+    for (int i = 0; i < n; ++i) {
+        const float2 st_after = row_stats(row + (AHEAD + 1) * row_step);
+        warp_wait_polls(&sums[slot], phase, &abort_flag, p.status);
+        if (threadIdx.x == 0 && i >= AHEAD) issue();  // block i - AHEAD is read
+        float2 m = both(0.0f);
+        if (cl > 1) {
+            for (int j = lane; j < cl * (NT / 32); j += 32) m = add2(m, slots[slot][j]);
+            m = warp_sum(m);
+        } else {
+            for (int j = 0; j < p.W; ++j) m = add2(m, slots[slot][g * p.W + j]);
+        }
+        if (row < rows) {
+            const float mu = st[0].x, rs = st[0].y;
+            const float mg = m.x * inv_h;                   // mean(g)
+            const float k2 = rs * rs * rs * (m.y * inv_h);  // rstd^2 mean(g xhat)
+            const T* sx = row_at(stage, skip);
+            const T* sdy = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(sx) + p.buf_bytes);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const Piece<T, VEC> px = load_piece_any<T, VEC>(sx, k, group, sub, h);
+                const Piece<T, VEC> pd = load_piece_any<T, VEC>(sdy, k, group, sub, h);
+                Piece<T, VEC> o;
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) {
+                    const float2 d = pair_of(pd, j);
+                    const float2 xc = add2(pair_of(px, j), both(-mu));
+                    const float2 gj = product<VEC>(d, pair_of(kg[k], j));
+                    set_pair(o, j, fma2(both(rs), add2(gj, both(-mg)), mul2(xc, both(-k2))));
+                    acc_g[k * PAIRS + j] = fma2(mul2(d, both(rs)), xc, acc_g[k * PAIRS + j]);
+                    acc_b[k * PAIRS + j] = add2(acc_b[k * PAIRS + j], d);
+                }
+                store_piece<T, VEC>(out, o, k, group, sub, h);
+            }
+        }
+        if (i + AHEAD < n) begin(i + AHEAD, st_next.x);
+#pragma unroll
+        for (int a = 0; a + 1 < AHEAD; ++a) st[a] = st[a + 1];
+        st[AHEAD - 1] = st_next;
+        st_next = st_after;
+        if (++stage == p.stages) stage = 0;
+        if (++slot == SLOTS) {
+            slot = 0;
             phase ^= 1u;
         }
-        m = begin(next, stage, phase, st_next.x);
-        parity ^= 1;
-        m = group_sum(m, p.W, scratch[parity]);
-        if (p.W == 1) __syncthreads();  // else group_sum's barrier did it
-        if (threadIdx.x == 0) {
-            if constexpr (KEEP)
-                issue(next + p.stages * step, stage);
-            else
-                issue(blk + p.stages * step, freed);
-        }
-        blk = next;
-        st = st_next;
-        st_next = st_after;
+        skip = (skip + skip_step) & 15;
+        row += row_step;
+        out += out_step;
     }
 
-    float* out_g = part_g + static_cast<long long>(blockIdx.x) * h;
-    float* out_b = part_b + static_cast<long long>(blockIdx.x) * h;
+    // No CTA leaves while a value that it has sent is on its way to a peer:
+    // it has itself waited for the last block's sums, to which the peers'
+    // own values of every block belong, but not for their receipt.
+    if (cl > 1) cluster_sync();
+    float* out_g = part_g + static_cast<long long>(unit) * p.h + c0;
+    float* out_b = part_b + static_cast<long long>(unit) * p.h + c0;
     if (R == 1) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -494,29 +565,41 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     }
 }
 
-// dgamma[c] = sum_i part_g[i][c], dbeta likewise: 32 interleaved chains (a
+// dgamma[c] = sum_i part_g[i][c], dbeta likewise: CHAINS interleaved chains (a
 // warp each) over i, then the chains in order.
-__global__ void __launch_bounds__(1024)
+template <int CHAINS>
+__global__ void __launch_bounds__(32 * CHAINS)
     norm_param_reduce_kernel(const float* __restrict__ part_g, const float* __restrict__ part_b,
                              int n, int h, float* __restrict__ dgamma, float* __restrict__ dbeta) {
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // the parts come from the kernel before this one
-    __shared__ float chain[32][33];
+    __shared__ float chain[CHAINS][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
     const float* part = blockIdx.y ? part_b : part_g;
     float s = 0.0f;
     if (c < h) {
-#pragma unroll 4
-        for (int i = w; i < n; i += 32) s += __ldg(part + static_cast<long long>(i) * h + c);
+#pragma unroll 10
+        for (int i = w; i < n; i += CHAINS) s += __ldg(part + static_cast<long long>(i) * h + c);
     }
     chain[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < h) {
         s = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s += chain[j][lane];
+        for (int j = 0; j < CHAINS; ++j) s += chain[j][lane];
         (blockIdx.y ? dbeta : dgamma)[c] = s;
     }
+}
+
+cudaError_t param_reduce(const float* pg, const float* pb, int n, int h, float* dgamma, float* dbeta,
+                         cudaStream_t st, int* launches) {
+    ++*launches;
+    const dim3 grid((h + 31) / 32, 2);
+    // few columns: many warps a column block, so that each adds few rows; many:
+    // the column blocks fill the GPU by themselves
+    if (h <= 4096)
+        return launch_dependent(norm_param_reduce_kernel<32>, grid, dim3(1024), 0, st, pg, pb, n, h, dgamma, dbeta);
+    return launch_dependent(norm_param_reduce_kernel<8>, grid, dim3(256), 0, st, pg, pb, n, h, dgamma, dbeta);
 }
 
 // ---------------------------------------------------------- any row width
@@ -681,65 +764,100 @@ cudaError_t forward(const void* x_, const void* gamma_, const void* beta_, int T
                             y, mean, rstd);
 }
 
-// How a backward call runs: the ring kernel with W warps a row and 16 (narrow)
-// or 40 (wide) values a thread, or, CTAs = 0, the kernels for any width.
+// How a backward call runs: the ring kernel with W warps and `cl` CTAs a
+// row, 16 values a thread, or, units = 0, the kernels for any width.
 struct NormPlan {
-    int ctas, W, stages, buf_bytes, threads, smem;
-    bool wide;
+    int units;  // CTAs, or clusters of `cl` CTAs
+    int W, cl, cols, stages, buf_bytes, threads, smem;
+    int room;  // the most shared memory that a plan of this many threads takes
 };
-
-// CTAs an SM of the 256-thread form: 16 values a thread in 16-bit pieces take
-// 80 registers, in fp32 or one by one up to 128.
-template <typename T, int VEC>
-constexpr int kNormCtas = 2;
 
 constexpr int kSmemMost = 227 * 1024;
 
+// CTAs of 256 threads an SM: 16-bit pieces fit 80 registers a thread, the
+// other forms take up to 128.
+template <int VEC>
+constexpr int kNormCtas = 2;
+
 NormPlan norm_plan(int T, int h, int elem) {
     NormPlan p{};
-    p.wide = h > 16 * 512;
-    p.W = p.wide ? 16 : ceil_pow2(ceil_div(h, 32 * 16));
-    p.threads = p.wide || p.W == 16 ? 512 : 256;
-    if (h > 40 * 512) return p;
+    // 256 threads: two CTAs an SM (128 registers a thread).  Rows beyond eight
+    // such CTAs take eight of 512.
+    p.threads = h <= kNormMaxCluster * 16 * 256 ? 256 : 512;
+    p.cl = ceil_div(h, 16 * p.threads);
+    if (p.cl > kNormMaxCluster) return NormPlan{};
+    p.cols = p.cl == 1 ? h : ceil_div(ceil_div(h, p.cl), 8) * 8;
+    p.W = p.cl > 1 ? p.threads / 32 : ceil_pow2(ceil_div(h, 32 * 16));
     const int R = p.threads / (32 * p.W);
     // a block of R rows and what its first and last granule hold besides
-    p.buf_bytes = (static_cast<int>((static_cast<long long>(R) * h * elem + 15) / 16) + 1) * 16;
-    const int per_sm = p.threads == 512 ? 1 : 2;
-    const int room = per_sm == 1 ? kSmemMost - 1024 : (kSmemMost / per_sm - 2048) & ~127;
-    const int own = p.wide ? (h * elem + 15) / 16 * 16 : 0;  // gamma
-    p.stages = std::min(kNormMaxStages, (room - own) / (2 * p.buf_bytes));
-    if (p.stages < 2) return p;  // not even two rows fit: fp32 rows beyond 11000 values
-    const int blocks = ceil_div(T, R);
-    p.stages = std::min(p.stages, std::max(2, ceil_div(blocks, kSms * per_sm)));
+    p.buf_bytes = (static_cast<int>((static_cast<long long>(R) * p.cols * elem + 15) / 16) + 1) * 16;
+    const int per_sm = p.threads == 512 ? 1 : elem == 2 && h % 8 == 0 ? kNormCtas<8> : kNormCtas<1>;
+    p.room = kSmemMost / per_sm - (per_sm == 1 ? 5120 : 3072);  // beside the static arrays
+    const int blocks = ceil_div(T, R), units = kSms * per_sm / p.cl;
+    // at most 16 bytes a value and thread: six stages of 16-bit values, three
+    // of fp32
+    p.stages = std::min(kNormMaxStages, p.room / (2 * p.buf_bytes));
     // the meeting place of the groups' sums: 16 values a thread and tensor
-    p.smem = std::max(p.stages * 2 * p.buf_bytes + own, R > 1 ? 2 * 16 * 4 * 32 * p.W : 0);
-    p.ctas = std::min(blocks, kSms * per_sm);
+    p.smem = std::max(p.stages * 2 * p.buf_bytes, R > 1 ? 2 * 16 * 4 * 32 * p.W : 0);
+    p.units = std::min(blocks, units);
     return p;
 }
 
-template <typename T, int VEC, int NV, int NT, int MIN_CTAS, bool KEEP>
+// Launches the ring kernel and sets *units to the CTAs or clusters it ran
+// with: no more clusters than can be resident at once (the GPU's parts hold a
+// number of SMs that clusters need not divide; one cluster too many would
+// run alone behind all others).
+template <typename T, int VEC, int NV, int NT, int MIN_CTAS>
 cudaError_t backward_ring(const NormPlan& p, const T* dy, const T* x, const T* gamma, const float* mean,
                           const float* rstd, int T_, int h, T* dx, float* pg, float* pb, int* status,
-                          cudaStream_t st) {
-    auto kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, KEEP>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+                          cudaStream_t st, int* units) {
+    auto kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.room);
     if (e != cudaSuccess) return e;
-    const NormBackwardArgs a{T_, h, p.W, p.stages, p.buf_bytes, status};
-    return launch_dependent(kern, dim3(p.ctas), dim3(NT), p.smem, st, dy, x, gamma, mean, rstd, a, dx, pg, pb);
+    const NormBackwardArgs a{T_, h, p.W, p.stages, p.cl, p.cols, p.buf_bytes, status};
+    if (p.cl == 1) {
+        *units = p.units;
+        return launch_dependent(kern, dim3(p.units), dim3(NT), p.smem, st, dy, x, gamma, mean, rstd, a, dx, pg,
+                                pb);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(NT);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    // clusters of this size that fit with the most shared memory a plan takes
+    static std::atomic<int> fit[kNormMaxCluster + 1];  // the same for every device of this build's target
+    int n = fit[p.cl].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cfg.gridDim = dim3(p.cl);
+        cfg.dynamicSmemBytes = p.room;
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+        n = std::max(n, 1);
+        fit[p.cl].store(n, std::memory_order_relaxed);
+    }
+    *units = std::min(p.units, n);
+    cfg.gridDim = dim3(*units * p.cl);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.numAttrs = dependent_launch() ? 2 : 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, dy, x, gamma, mean, rstd, a, dx, pg, pb)) != cudaSuccess) return e;
+    return cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t backward_rows(const NormPlan& p, const T* dy, const T* x, const T* gamma, const float* mean,
                           const float* rstd, int T_, int h, T* dx, float* pg, float* pb, int* status,
-                          cudaStream_t st) {
-    if (p.wide)
-        return backward_ring<T, VEC, 40 / Piece<T, VEC>::N, 512, 1, false>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb,
-                                                              status, st);
+                          cudaStream_t st, int* units) {
+    constexpr int N = Piece<T, VEC>::N;
     if (p.threads == 512)
-        return backward_ring<T, VEC, 16 / Piece<T, VEC>::N, 512, 1, true>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb,
-                                                             status, st);
-    return backward_ring<T, VEC, 16 / Piece<T, VEC>::N, 256, kNormCtas<T, VEC>, true>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status,
-                                                         st);
+        return backward_ring<T, VEC, 16 / N, 512, 1>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
+    return backward_ring<T, VEC, 16 / N, 256, kNormCtas<VEC>>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
 }
 
 template <typename T>
@@ -751,22 +869,20 @@ cudaError_t backward(const void* dy_, const void* x_, const void* gamma_, const 
     T* dx = static_cast<T*>(dx_);
     cudaError_t e;
     const NormPlan p = norm_plan(T_, h, sizeof(T));
-    if (p.ctas > 0) {
+    if (p.units > 0) {
         constexpr int VEC = 16 / sizeof(T);
-        // one CTA: its sums are the result
-        float* pg = p.ctas == 1 ? dgamma : partial;
-        float* pb = p.ctas == 1 ? dbeta : partial + static_cast<size_t>(p.ctas) * h;
+        // one CTA or cluster: its sums are the result
+        float* pg = p.units == 1 ? dgamma : partial;
+        float* pb = p.units == 1 ? dbeta : partial + static_cast<size_t>(p.units) * h;
+        int units = 0;
         if (h % VEC == 0)
-            e = backward_rows<T, VEC>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st);
+            e = backward_rows<T, VEC>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, &units);
         else
-            e = backward_rows<T, 1>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st);
+            e = backward_rows<T, 1>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, &units);
         if (e != cudaSuccess) return e;
         ++*launches;
-        if (p.ctas == 1) return cudaSuccess;
-        ++*launches;
-        return launch_dependent(norm_param_reduce_kernel, dim3(ceil_div(h, 32), 2), dim3(1024), 0, st,
-                                static_cast<const float*>(pg), static_cast<const float*>(pb), p.ctas, h, dgamma,
-                                dbeta);
+        if (p.units == 1) return cudaSuccess;
+        return param_reduce(pg, pb, units, h, dgamma, dbeta, st, launches);
     }
     e = launch_dependent(norm_backward_kernel<T>, dim3(T_), dim3(kRowThreads), 0, st, dy, x, gamma, mean, rstd,
                          h, dx);
@@ -776,17 +892,15 @@ cudaError_t backward(const void* dy_, const void* x_, const void* gamma_, const 
     e = launch_dependent(norm_param_grad_kernel<T>, dim3(ceil_div(h, 32), chunks), dim3(256), 0, st, dy, x,
                          mean, rstd, T_, h, ceil_div(T_, chunks), partial);
     if (e != cudaSuccess) return e;
-    *launches += 3;
-    return launch_dependent(norm_param_reduce_kernel, dim3(ceil_div(h, 32), 2), dim3(1024), 0, st,
-                            static_cast<const float*>(partial), static_cast<const float*>(pb), chunks, h, dgamma,
-                            dbeta);
+    *launches += 2;
+    return param_reduce(partial, pb, chunks, h, dgamma, dbeta, st, launches);
 }
 
 }  // namespace
 
 int norm_param_parts(int T, int h, int elem) {
     const NormPlan p = norm_plan(T, h, elem);
-    if (p.ctas > 0) return p.ctas;
+    if (p.units > 0) return p.units;
     const long long col_blocks = (h + 31) / 32;
     return static_cast<int>(std::max(1LL, std::min<long long>((1216 + col_blocks - 1) / col_blocks, (T + 31) / 32)));
 }

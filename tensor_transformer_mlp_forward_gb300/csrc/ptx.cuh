@@ -118,6 +118,25 @@ __device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity
     return ok != 0u;
 }
 
+// A wait limited by its number of polls, for waits on a kernel's critical
+// path: the limit of wait_bounded reads the global timer on its first miss,
+// which takes about a microsecond.  A poll suspends the thread until the
+// phase completes or some time of the hardware's own passes, so the limit is
+// seconds.  Called by whole warps; the lanes poll together.
+constexpr int kPollLimit = 1 << 24;
+
+__device__ __forceinline__ void warp_wait_polls(uint64_t* bar, uint32_t parity,
+                                                volatile uint32_t* abort, int* status) {
+    for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if (i >= kPollLimit || *abort) {
+            *abort = 1u;
+            atomicExch(status, kStatusTimeout);
+            break;
+        }
+    }
+    __syncwarp();
+}
+
 // Bounded wait used while draining after an abort: ignores the abort flag.
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, int* status,
                                            int site = 0) {
@@ -357,6 +376,15 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
+}
+
+// Two floats to the shared memory of a CTA of the cluster, 8 bytes counted on
+// that CTA's mbarrier (both shared::cluster addresses, 8-byte aligned).
+__device__ __forceinline__ void st_async_v2(uint32_t addr, float2 v, uint32_t bar) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+        "f"(v.x), "f"(v.y), "r"(bar)
+        : "memory");
 }
 
 // ------------------------------------------------ cluster launch control

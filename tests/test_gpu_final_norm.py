@@ -42,8 +42,8 @@ def check(T, h, dtype, seed=None):
 # one value a row, fewer than a vector, odd widths, whole vectors, the widths
 # where a row takes another number of threads or registers, very long rows;
 # one row, fewer rows than SMs, ragged counts
-SHAPES = [(1, 1), (5, 3), (3, 8), (1, 4096), (37, 200), (130, 255), (300, 1024), (5, 1023),
-          (257, 1032), (64, 2047), (9, 4100), (33, 8192), (70, 8200), (3, 12289), (17, 20480),
+SHAPES = [(1, 1), (5, 3), (3, 8), (1, 4096), (1, 20480), (37, 200), (130, 255), (300, 1024), (5, 1023),
+          (257, 1032), (64, 2047), (9, 4100), (33, 8192), (70, 8200), (200, 9001), (5, 16392), (3, 12289), (17, 20480),
           (2, 24576), (3, 32776), (2, 50001), (1000, 64), (2051, 40)]
 
 
