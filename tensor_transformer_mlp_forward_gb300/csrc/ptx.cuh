@@ -87,7 +87,12 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
 template <bool SLEEP = false>
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
                                              volatile uint32_t* abort, int* status, int site = 0) {
-    if (mbar_try_wait(bar, parity)) return true;
+    // The timer takes about a microsecond to read: polls come first, so that a
+    // wait shorter than theirs (the hardware suspends a poll for a while) does
+    // not pay for it.
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_poll<SLEEP>(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     while (true) {
 #pragma unroll 1
