@@ -369,7 +369,7 @@ int tp_ln_backward(const void* dy, const void* x, const void* gamma, const float
  * the workspace are 16-byte aligned, targets 8-byte, the rest 4-byte. */
 
 /* Bytes of scratch tp_head_loss_forward needs (the row statistics of each
- * tile of the vocabulary: 16 T ceil(V/256)). */
+ * tile of the vocabulary: at most 16 T max(304, ceil(V/256))). */
 size_t tp_head_loss_forward_workspace_bytes(int T, int h, int V);
 
 /* In: X [T,h], W [V,h] (bf16), targets [T].  Out: loss, lse [T] (float32).
@@ -381,7 +381,8 @@ int tp_head_loss_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const int64_t
 /* Scratch of tp_head_loss_backward: what it uses at most, and the least it
  * runs with.  The backward pass goes through the vocabulary in pieces and
  * keeps one piece's bf16 logit gradients at a time (at most 512 MiB); a
- * smaller workspace means narrower pieces, down to 256 columns. */
+ * smaller workspace means narrower pieces, down to 256 columns.  (Up to 16
+ * tokens the whole vocabulary is one piece and the two sizes are the same.) */
 size_t tp_head_loss_backward_workspace_bytes(int T, int h, int V);
 size_t tp_head_loss_backward_min_workspace_bytes(int T, int h, int V);
 

@@ -1994,9 +1994,10 @@ int check_head(int T, int h, int V) {
 }
 
 // Column parts of the forward's row statistics: one for each epilogue half
-// of each 256-column tile at most.
+// of each 256-column tile at most, or one for each CTA of the few-token form.
 size_t head_forward_bytes(int T, int V) {
-    return sizeof(float2) * static_cast<size_t>(2 * cdiv(V, BN)) * static_cast<size_t>(T);
+    const long long parts = head_few(T) ? head_few_parts(V) : 2 * cdiv(V, BN);
+    return sizeof(float2) * static_cast<size_t>(parts) * static_cast<size_t>(T);
 }
 
 // Bytes of the logits' gradient kept at a time (a piece of the vocabulary).
@@ -2051,7 +2052,23 @@ HeadPlan head_layout(int T, int h, int V, int width, int splits) {
 
 int round_up(long long x, long long m) { return static_cast<int>(cdiv(x, m) * m); }
 
+// The few-token form: the whole vocabulary at once, dz in two layouts of 16
+// tokens, dX's planes one for each range of the vocabulary.
+HeadPlan head_plan_few(int T, int h, int V) {
+    HeadPlan p;
+    p.width = head_few_ldz(V);
+    p.splits = head_few_planes(h, V);
+    p.planes = true;
+    p.info = 0;
+    p.scale = 0;
+    p.plane = 256;
+    p.dz = align256(p.plane + sizeof(float) * static_cast<size_t>(p.splits) * T * h);
+    p.total = align256(p.dz + 2 * sizeof(uint16_t) * 16 * static_cast<size_t>(p.width));
+    return p;
+}
+
 HeadPlan head_plan(int T, int h, int V) {
+    if (head_few(T)) return head_plan_few(T, h, V);
     const long long pieces = std::max<long long>(1, cdiv(2LL * T * V, kHeadPieceBytes));
     const int width = pieces == 1 ? round_up(V, 64) : round_up(cdiv(V, pieces), BN);
     return head_layout(T, h, V, width, choose_head_splits(T, h, width / BK));
@@ -2059,6 +2076,7 @@ HeadPlan head_plan(int T, int h, int V) {
 
 // The narrowest pieces: one column tile at a time.
 HeadPlan head_plan_least(int T, int h, int V) {
+    if (head_few(T)) return head_plan_few(T, h, V);
     return head_layout(T, h, V, std::min(round_up(V, 64), BN), 1);
 }
 
@@ -2068,7 +2086,7 @@ bool head_plan_for(int T, int h, int V, size_t bytes, HeadPlan& p) {
     p = head_plan(T, h, V);
     if (p.total <= bytes) return true;
     p = head_plan_least(T, h, V);
-    if (p.total > bytes) return false;
+    if (p.total > bytes || head_few(T)) return false;
     const long long cols = static_cast<long long>((bytes - p.dz) / (2 * static_cast<size_t>(T)));
     int width = static_cast<int>(std::min<long long>(round_up(V, 64), cols)) / BN * BN;
     for (; width > p.width; width -= BN) {
@@ -2083,6 +2101,15 @@ bool head_plan_for(int T, int h, int V, size_t bytes, HeadPlan& p) {
 
 int head_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const long long* targets, int T, int h,
                  int V, float* loss, float* lse, void* ws, cudaStream_t st, const DeviceInfo& d) {
+    cudaError_t e;
+    if (head_few(T)) {
+        float2* parts = static_cast<float2*>(ws);
+        e = launch_head_few_lse(cb(X), cb(W), targets, T, h, V, parts, st, &t_last_launches);
+        if (e == cudaSuccess)
+            e = launch_head_combine(parts, head_few_parts(V), cb(X), cb(W), targets, T, h, V, loss, lse, st,
+                                    &t_last_launches);
+        return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+    }
     GemmArgs g = blank_args();
     const GemmShape sh{T, V, h, 1, SHARD_N, 1LL * T * h, 1LL * V * h};
     g.targets = targets;
@@ -2092,7 +2119,7 @@ int head_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const long long* targ
     Output o{const_cast<tpmlp_bf16*>(X), nullptr, T, h, 1};  // a map that nothing is stored through
     if (int rc = run_gemm(launch_head_lse, a, b, o, g, sh, st, d)) return rc;
     const int parts = g.n_tiles * (g.epi_warps / 4);
-    cudaError_t e = launch_head_combine(g.lse_part, parts, cb(X), cb(W), targets, T, h, V, loss, lse,
+    e = launch_head_combine(g.lse_part, parts, cb(X), cb(W), targets, T, h, V, loss, lse,
                                         st, &t_last_launches);
     return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
 }
@@ -2106,7 +2133,18 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
     float* scale = reinterpret_cast<float*>(base + p.scale);
     float* plane = reinterpret_cast<float*>(base + p.plane);
     tpmlp_bf16* dz = reinterpret_cast<tpmlp_bf16*>(base + p.dz);
-    cudaError_t e = launch_head_prepare(dloss, lse, targets, T, V, info, scale, st, &t_last_launches);
+    cudaError_t e;
+    if (head_few(T)) {
+        __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(dz);
+        e = launch_head_few_backward(dloss, cb(X), cb(W), targets, lse, T, h, V, z,
+                                     z + 16 * static_cast<size_t>(p.width), scale, plane,
+                                     reinterpret_cast<__nv_bfloat16*>(dW), st, &t_last_launches);
+        if (e == cudaSuccess)
+            e = launch_head_reduce(plane, p.splits, 1LL * T * h, scale, reinterpret_cast<__nv_bfloat16*>(dX), st,
+                                   &t_last_launches);
+        return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+    }
+    e = launch_head_prepare(dloss, lse, targets, T, V, info, scale, st, &t_last_launches);
     if (e != cudaSuccess) return fail_cuda(e);
     for (long long v = 0; v < V; v += p.width) {
         const int v0 = static_cast<int>(v);

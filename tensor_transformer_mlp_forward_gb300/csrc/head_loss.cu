@@ -146,24 +146,43 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
+// out[i] = bf16(s sum_k P[k][i]): a CTA takes 256 / chains pieces of 8 values,
+// `chains` threads a piece (1, or 16 for many planes of few values), each
+// adding planes c, c + chains, ... in order; then the chains in order.
 __global__ void __launch_bounds__(256)
-    head_reduce_kernel(const float* __restrict__ P, int planes, long long count,
+    head_reduce_kernel(const float* __restrict__ P, int planes, long long count, int chains,
                        const float* __restrict__ scale, __nv_bfloat16* __restrict__ out) {
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // its inputs come from the kernel before it
-    const long long i = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
-    if (i >= count) return;
-    const float s = __ldg(scale);
+    __shared__ float part[256][9];
+    const int pieces = 256 / chains;
+    const int chain = threadIdx.x / pieces, piece = threadIdx.x % pieces;
+    const long long i = (static_cast<long long>(blockIdx.x) * pieces + piece) * 8;
+    const bool ok = i < count;
     float a[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+    if (ok) {
 #pragma unroll 4
-    for (int k = 0; k < planes; ++k) {
-        const float4* q = reinterpret_cast<const float4*>(P + k * count + i);
-        const float4 x = __ldg(q), y = __ldg(q + 1);
-        a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
-        a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+        for (int k = chain; k < planes; k += chains) {
+            const float4* q = reinterpret_cast<const float4*>(P + k * count + i);
+            const float4 x = __ldg(q), y = __ldg(q + 1);
+            a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+            a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+        }
     }
+    if (chains > 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[threadIdx.x][j] = a[j];
+        __syncthreads();
+        if (chain == 0) {
+            for (int k = 1; k < chains; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[j] += part[k * pieces + piece][j];
+        }
+    }
+    if (chain != 0 || !ok) return;
+    const float s = __ldg(scale);
     uint4 o;
     o.x = pack_bf16x2(s * a[0], s * a[1]);
     o.y = pack_bf16x2(s * a[2], s * a[3]);
@@ -198,8 +217,9 @@ cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long
 cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,
                                __nv_bfloat16* out, cudaStream_t st, int* launches) {
     ++*launches;
-    return launch_dependent(head_reduce_kernel, dim3(blocks_of(count / 8, 256)), dim3(256), 0, st, P,
-                            planes, count, scale, out);
+    const int chains = planes >= 8 ? 16 : 1;
+    return launch_dependent(head_reduce_kernel, dim3(blocks_of(count / 8, 256 / chains)), dim3(256), 0, st, P,
+                            planes, count, chains, scale, out);
 }
 
 }  // namespace tpmlp

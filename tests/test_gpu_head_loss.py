@@ -51,7 +51,12 @@ def check(c, out):
 # CTAs, more than one k-block split
 SHAPES = [(1, 8, 1), (1, 64, 2), (3, 16, 5), (2, 1024, 509), (7, 264, 255), (5, 72, 256), (130, 128, 257),
           (128, 64, 1000), (129, 200, 1003), (300, 1024, 2049), (257, 1032, 777), (33, 2048, 4001),
-          (640, 512, 5000), (1, 4096, 3001), (1100, 256, 3000), (2100, 136, 1031)]
+          (640, 512, 5000), (1, 4096, 3001), (1100, 256, 3000), (2100, 136, 1031),
+          # around the few-token form: its last token count and the next, odd
+          # widths (one 64-column step and a bit, several CTAs of columns),
+          # vocabularies around its 32-row tasks and with more tasks than CTAs
+          (8, 72, 31), (9, 328, 33), (15, 1000, 640), (16, 2056, 1003), (17, 2056, 1003), (4, 8, 20001),
+          (16, 64, 40007)]
 
 
 @pytest.mark.parametrize("T,h,V", SHAPES)
