@@ -30,7 +30,8 @@ constexpr int kWarps = 4;     // of a CTA
 constexpr int kRows = 32;     // vocabulary rows of a task: four n8 tiles
 constexpr int kTiles = kRows / 8;
 constexpr int kKStep = 64;    // columns of a step: 128 bytes of a row
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 4;  // of the logits kernel
+constexpr int kGradCtas = 3;   // of the gradient kernel
 constexpr int kSms = 152;
 constexpr int kColumns = 64;  // columns of W that a warp of the gradient kernel owns
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
 struct FewArgs {
     const __nv_bfloat16 *X, *W;
     const long long* targets;
-    int T, h, V, tasks;
+    int T, h, V;
     float2* parts;  // forward: {max, sum of exponentials}, [CTA][T]
     // backward
     const float *dloss, *lse;
@@ -65,10 +66,12 @@ struct FewArgs {
 };
 
 // Logits of the 16 tokens against tasks of 32 vocabulary rows, CTA b taking
-// tasks b, b + grid, ...  The four warps split k (64 columns each in turn, so
-// that together they read 512 consecutive bytes of a row) and their sums
-// meet in shared memory.  Then thread (token, 4 rows): forward, the running
-// maximum and sum of exponentials; backward, the logits' gradient.
+// tasks b, b + grid, ... (neighbours in memory at the same time).  The four warps split k (64 columns each in turn, so that together
+// they read 512 consecutive bytes of a row) and their sums meet in shared
+// memory.  Then thread (token, 4 rows): forward, the running maximum and sum
+// of exponentials; backward, the logits' gradient.  The loads run one step
+// ahead, across the tasks too: a task has few steps (four a warp at h =
+// 1024), and starting each anew left the memory idle a third of the time.
 template <bool GRAD>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kernel(const FewArgs p) {
     pdl_launch_dependents();  // the next kernel may begin its launch
@@ -99,48 +102,88 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
         }
     }
 
-    int parity = 0;
-    for (int task = blockIdx.x; task < p.tasks; task += gridDim.x, parity ^= 1) {
-        const int v0 = task * kRows;
-        const __nv_bfloat16* w[kTiles];
+    const int row0 = blockIdx.x * kRows, row_step = gridDim.x * kRows;
+    uint4 wb[2][kTiles][2];
+    // One step's loads of W: columns 64 step .. of the task at v0.  Rows behind
+    // the vocabulary read its last.
+    auto load = [&](int v0, int step, int b) {
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)  // rows behind the vocabulary read its last
-            w[i] = p.W + static_cast<long long>(min(v0 + i * 8 + g, p.V - 1)) * p.h + q * 8;
-        float acc[kTiles][4];
+        for (int s = 0; s < 2; ++s) {
+            const int k = step * kKStep + s * 32;  // + q * 8 .. + 7
+            const bool ok = k + q * 8 < p.h;
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+                wb[b][i][s] = ok ? load_stream(p.W + static_cast<long long>(min(v0 + i * 8 + g, p.V - 1)) * p.h + q * 8 + k)
+                                 : z;
+        }
+    };
+    float acc[kTiles][4];
+    // X's share of the step comes from L1 when it is needed: the registers go
+    // to W's loads in flight.
+    auto multiply = [&](int step, int b) {
+        uint4 xa[2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int k = step * kKStep + s * 32;
+            const bool ok = k + q * 8 < p.h;
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            xa[0][s] = ok && lo_ok ? __ldg(reinterpret_cast<const uint4*>(xlo + k)) : z;
+            xa[1][s] = two && ok && hi_ok ? __ldg(reinterpret_cast<const uint4*>(xhi + k)) : z;
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint4 a = xa[0][s], c = xa[1][s];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const uint4 u = wb[b][i][s];
+                mma16816(acc[i], a.x, c.x, a.y, c.y, u.x, u.y);
+                mma16816(acc[i], a.z, c.z, a.w, c.w, u.z, u.w);
+            }
+        }
+    };
+    int parity = 0;
+    int next_v = row0, next_step = warp;  // what the next load takes
+    auto load_next = [&](int b) {
+        if (next_step >= steps) {
+            next_v += row_step;
+            next_step = warp;
+        }
+        if (next_v < p.V && next_step < steps) load(next_v, next_step, b);
+        next_step += kWarps;
+    };
+    const int mine = warp < steps ? (steps - warp + kWarps - 1) / kWarps : 0;  // steps of this warp
+    int buf = 0;
+    if (mine) load_next(0);
+    for (int v0 = row0; v0 < p.V; v0 += row_step, parity ^= 1) {
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-        uint4 wb[2][kTiles][2], xa[2][2][2];
-        auto load = [&](int step, int b) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int k = step * kKStep + s * 32;  // + q * 8 .. + 7
-                const bool ok = k + q * 8 < p.h;
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) wb[b][i][s] = ok ? load_stream(w[i] + k) : z;
-                xa[b][0][s] = ok && lo_ok ? __ldg(reinterpret_cast<const uint4*>(xlo + k)) : z;
-                xa[b][1][s] = two && ok && hi_ok ? __ldg(reinterpret_cast<const uint4*>(xhi + k)) : z;
+        int left = mine, step = warp;
+        // the buffers are named by constants: an odd step first, then pairs
+        auto one = [&](int b) {
+            if (b) {
+                load_next(0);
+                multiply(step, 1);
+            } else {
+                load_next(1);
+                multiply(step, 0);
             }
+            step += kWarps;
         };
-        auto multiply = [&](int b) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const uint4 a = xa[b][0][s], c = xa[b][1][s];
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    const uint4 u = wb[b][i][s];
-                    mma16816(acc[i], a.x, c.x, a.y, c.y, u.x, u.y);
-                    mma16816(acc[i], a.z, c.z, a.w, c.w, u.z, u.w);
-                }
+        if (left & 1) {
+            one(buf);
+            buf ^= 1;
+            --left;
+        }
+        if (buf == 0) {
+            for (; left > 0; left -= 2) {
+                one(0);
+                one(1);
             }
-        };
-        if (warp < steps) load(warp, 0);
-        for (int step = warp; step < steps; step += 2 * kWarps) {  // one step's loads ahead
-            if (step + kWarps < steps) load(step + kWarps, 1);
-            multiply(0);
-            if (step + kWarps < steps) {
-                if (step + 2 * kWarps < steps) load(step + 2 * kWarps, 0);
-                multiply(1);
+        } else {
+            for (; left > 0; left -= 2) {
+                one(1);
+                one(0);
             }
         }
 #pragma unroll
@@ -204,15 +247,29 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
     }
 }
 
-// dX and dW from dz: a warp owns 64 columns and a range of vocabulary rows.
-// Per 16 rows it loads its 16 x 64 block of W once (a lane: 8 columns of
-// rows 2q, 2q + 1, 2q + 8, 2q + 9, byte-permuted into pairs along the rows),
-// adds dz W to its 16 x 64 sums of dX, and multiplies dz^T by its 64 columns
-// of X, which stay in registers, into that block of dW.  Column n of
-// instruction j is column 8 n + j of the 64, so that a lane's eight
-// instructions give it 16 consecutive columns of dW: whole lines are stored.
-// dX's sums of each range go to plane[range][T][h].
-__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm)
+// Both gradients are split alike: a warp owns 64 columns and a range of
+// vocabulary rows, 16 of them at a time.  Column n of instruction j is column
+// 8 n + j of the 64, so that a lane loads 8 consecutive columns (its share of
+// eight instructions) and ends with 16 consecutive columns of a result.
+
+// Eight pairs along k from two rows' 8 values.
+__device__ __forceinline__ void pairs_of(const uint4 a, const uint4 b, uint32_t (&o)[8]) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = __byte_perm(x[i], y[i], 0x5410);
+        o[2 * i + 1] = __byte_perm(x[i], y[i], 0x7632);
+    }
+}
+
+// dX's sums over the range go to plane[range][T][h]; dW = s dz^T X.  Reading W
+// and writing dW in one kernel is what HBM serves best: a kernel that only
+// wrote dW took 29 us for 103 MB, as long as both together here.  A lane loads
+// 8 columns of rows 2q, 2q + 1, 2q + 8 and 2q + 9 and byte-permutes them into
+// pairs along the rows: no transposition through shared memory.  The warp's
+// 64 columns of X stay in registers.  Three steps' loads of W are in flight;
+// dW leaves in whole 128-byte lines.
+__global__ void __launch_bounds__(32 * kWarps, kGradCtas)
     head_few_grad_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
                          const __nv_bfloat16* __restrict__ dz, const __nv_bfloat16* __restrict__ dzt,
                          int ldz, const float* __restrict__ scale, int T, int h, int V,
@@ -222,78 +279,80 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int col0 = (blockIdx.x * kWarps + warp) * kColumns;
     if (col0 >= h) return;
-    const int c = col0 + g * 8;  // columns this lane loads
-    const bool c_ok = c < h;
-    const int row_off[4] = {2 * q, 2 * q + 1, 2 * q + 8, 2 * q + 9};
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    // eight pairs along k from two rows' 8 values
-    auto pairs = [](const uint4 a, const uint4 b, uint32_t (&o)[8]) {
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = __byte_perm(x[i], y[i], 0x5410);
-            o[2 * i + 1] = __byte_perm(x[i], y[i], 0x7632);
-        }
-    };
+    const int c = min(col0 + g * 8, h - 8);  // columns behind the row are not stored
     uint32_t xb[2][8];
     {
         uint4 r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r[i] = c_ok && row_off[i] < T
-                       ? __ldg(reinterpret_cast<const uint4*>(X + static_cast<long long>(row_off[i]) * h + c))
-                       : zero;
-        pairs(r[0], r[1], xb[0]);
-        pairs(r[2], r[3], xb[1]);
+        for (int i = 0; i < 4; ++i) {
+            const int tok = 2 * q + (i & 1) + (i >> 1) * 8;
+            r[i] = tok < T ? __ldg(reinterpret_cast<const uint4*>(X + static_cast<long long>(tok) * h + c))
+                           : make_uint4(0u, 0u, 0u, 0u);
+        }
+        pairs_of(r[0], r[1], xb[0]);
+        pairs_of(r[2], r[3], xb[1]);
     }
     const float s = __ldg(scale);
-    float ax[8][4];
+    float acc[8][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ax[j][0] = ax[j][1] = ax[j][2] = ax[j][3] = 0.0f;
-
+    for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
     const int r0 = blockIdx.y * range_rows, r1 = min(r0 + range_rows, V);
-    uint4 wn[4];
-    uint32_t an[4], tn[4];
-    auto load = [&](int vb) {
+    uint4 w[3][4];
+    uint32_t a[2][4], t[2][4];
+    auto load_w = [&](int vb, int b) {
+        if (vb >= r1) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // rows behind the vocabulary read its last; dz is 0 there
-            wn[i] = c_ok ? load_stream(W + static_cast<long long>(min(vb + row_off[i], V - 1)) * h + c) : zero;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            an[i] = __ldg(reinterpret_cast<const uint32_t*>(dz + static_cast<long long>(g + (i & 1) * 8) * ldz + vb +
-                                                            2 * q + (i >> 1) * 8));
-            tn[i] = __ldg(reinterpret_cast<const uint32_t*>(dzt + static_cast<long long>(vb + g + (i & 1) * 8) * kTokens +
-                                                            2 * q + (i >> 1) * 8));
+        for (int i = 0; i < 4; ++i) {  // rows behind the vocabulary read its last; dz is 0 there
+            const int v = vb + 2 * q + (i & 1) + (i >> 1) * 8;
+            w[b][i] = load_stream(W + static_cast<long long>(min(v, V - 1)) * h + c);
         }
     };
-    if (r0 < r1) load(r0);
-    for (int vb = r0; vb < r1; vb += 16) {
-        uint32_t wb[2][8], a[4], t[4];
-        pairs(wn[0], wn[1], wb[0]);
-        pairs(wn[2], wn[3], wb[1]);
+    auto load_dz = [&](int vb, int b) {
+        if (vb >= r1) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            a[i] = an[i];
-            t[i] = tn[i];
+            a[b][i] = __ldg(reinterpret_cast<const uint32_t*>(dz + static_cast<long long>(g + (i & 1) * 8) * ldz + vb +
+                                                              2 * q + (i >> 1) * 8));
+            t[b][i] = __ldg(reinterpret_cast<const uint32_t*>(dzt + static_cast<long long>(vb + g + (i & 1) * 8) * kTokens +
+                                                              2 * q + (i >> 1) * 8));
         }
-        if (vb + 16 < r1) load(vb + 16);
-        float o[8][4];
+    };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            mma16816(ax[j], a[0], a[1], a[2], a[3], wb[0][j], wb[1][j]);
-            o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-            mma16816(o[j], t[0], t[1], t[2], t[3], xb[0][j], xb[1][j]);
-        }
+    for (int b = 0; b < 3; ++b) load_w(r0 + 16 * b, b);
+    load_dz(r0, 0);
+    for (int vb = r0; vb < r1; vb += 96) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {  // rows g, g + 8
-            const int v = vb + g + 8 * r;
+        for (int u = 0; u < 6; ++u) {
+            const int vr = vb + 16 * u;
+            if (vr >= r1) break;
+            constexpr int kDepth = 3;
+            const int b = u % kDepth, d = u & 1;
+            load_dz(vr + 16, d ^ 1);
+            {
+                uint32_t lo[8], hi[8];
+                pairs_of(w[b][0], w[b][1], lo);
+                pairs_of(w[b][2], w[b][3], hi);
+                load_w(vr + 16 * kDepth, b);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // columns 16 q .., 16 q + 8 ..
-                const int n = col0 + 16 * q + 8 * half, e = 2 * r + half;
-                if (v < V && n < h)
-                    *reinterpret_cast<uint4*>(dW + static_cast<long long>(v) * h + n) =
-                        make_uint4(pack_bf16x2(s * o[0][e], s * o[1][e]), pack_bf16x2(s * o[2][e], s * o[3][e]),
-                                   pack_bf16x2(s * o[4][e], s * o[5][e]), pack_bf16x2(s * o[6][e], s * o[7][e]));
+                for (int j = 0; j < 8; ++j) mma16816(acc[j], a[d][0], a[d][1], a[d][2], a[d][3], lo[j], hi[j]);
+            }
+            float o[8][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+                mma16816(o[j], t[d][0], t[d][1], t[d][2], t[d][3], xb[0][j], xb[1][j]);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {  // rows g, g + 8
+                const int v = vr + g + 8 * r;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // columns 16 q .., 16 q + 8 ..
+                    const int n = col0 + 16 * q + 8 * half, e = 2 * r + half;
+                    if (v < V && n < h)
+                        __stcs(reinterpret_cast<uint4*>(dW + static_cast<long long>(v) * h + n),
+                               make_uint4(pack_bf16x2(s * o[0][e], s * o[1][e]), pack_bf16x2(s * o[2][e], s * o[3][e]),
+                                       pack_bf16x2(s * o[4][e], s * o[5][e]), pack_bf16x2(s * o[6][e], s * o[7][e])));
+                }
             }
         }
     }
@@ -306,8 +365,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm)
             const int n = col0 + 16 * q + 8 * half, e = 2 * r + half;
             if (tok < T && n < h) {
                 float4* d = reinterpret_cast<float4*>(out + static_cast<long long>(tok) * h + n);
-                d[0] = make_float4(ax[0][e], ax[1][e], ax[2][e], ax[3][e]);
-                d[1] = make_float4(ax[4][e], ax[5][e], ax[6][e], ax[7][e]);
+                d[0] = make_float4(acc[0][e], acc[1][e], acc[2][e], acc[3][e]);
+                d[1] = make_float4(acc[4][e], acc[5][e], acc[6][e], acc[7][e]);
             }
         }
     }
@@ -326,14 +385,13 @@ int head_few_ldz(int V) { return ceil_div(V, kRows) * kRows; }
 // Ranges of vocabulary rows, as many as fill the GPU with CTAs of 256 columns.
 int head_few_planes(int h, int V) {
     const int col_ctas = ceil_div(h, kColumns * kWarps);
-    return std::max(1, std::min(kSms * kCtasPerSm / col_ctas, ceil_div(V, 16)));
+    return std::max(1, std::min(kSms * kGradCtas / col_ctas, ceil_div(V, 16)));
 }
 
 cudaError_t launch_head_few_lse(const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets,
                                 int T, int h, int V, float2* parts, cudaStream_t st, int* launches) {
     FewArgs a = {};
     a.X = X; a.W = W; a.targets = targets; a.T = T; a.h = h; a.V = V;
-    a.tasks = ceil_div(V, kRows);
     a.parts = parts;
     ++*launches;
     return launch_dependent(head_few_logits_kernel<false>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0, st, a);
@@ -345,7 +403,6 @@ cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X,
                                      __nv_bfloat16* dW, cudaStream_t st, int* launches) {
     FewArgs a = {};
     a.X = X; a.W = W; a.targets = targets; a.T = T; a.h = h; a.V = V;
-    a.tasks = ceil_div(V, kRows);
     a.dloss = dloss; a.lse = lse; a.dz = dz; a.dzt = dzt; a.ldz = head_few_ldz(V); a.scale = scale;
     ++*launches;
     cudaError_t e = launch_dependent(head_few_logits_kernel<true>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0,

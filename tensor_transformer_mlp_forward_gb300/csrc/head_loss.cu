@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 // out[i] = bf16(s sum_k P[k][i]): a CTA takes 256 / chains pieces of 8 values,
-// `chains` threads a piece (1, or 16 for many planes of few values), each
+// `chains` threads a piece (1, or 16 or 32 for many planes of few values), each
 // adding planes c, c + chains, ... in order; then the chains in order.
 __global__ void __launch_bounds__(256)
     head_reduce_kernel(const float* __restrict__ P, int planes, long long count, int chains,
@@ -217,7 +217,7 @@ cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long
 cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,
                                __nv_bfloat16* out, cudaStream_t st, int* launches) {
     ++*launches;
-    const int chains = planes >= 8 ? 16 : 1;
+    const int chains = planes >= 64 ? 32 : planes >= 8 ? 16 : 1;
     return launch_dependent(head_reduce_kernel, dim3(blocks_of(count / 8, 256 / chains)), dim3(256), 0, st, P,
                             planes, count, chains, scale, out);
 }

@@ -56,7 +56,7 @@ SHAPES = [(1, 8, 1), (1, 64, 2), (3, 16, 5), (2, 1024, 509), (7, 264, 255), (5, 
           # widths (one 64-column step and a bit, several CTAs of columns),
           # vocabularies around its 32-row tasks and with more tasks than CTAs
           (8, 72, 31), (9, 328, 33), (15, 1000, 640), (16, 2056, 1003), (17, 2056, 1003), (4, 8, 20001),
-          (16, 64, 40007)]
+          (16, 64, 40007), (5, 64, 19456), (5, 64, 24360), (3, 128, 32), (3, 128, 40), (3, 128, 24)]
 
 
 @pytest.mark.parametrize("T,h,V", SHAPES)
