@@ -156,6 +156,7 @@ struct GemmArgs {
     int col0;                  // EPI_DLOGITS: vocabulary index of column 0
     int n_valid;               // EPI_DLOGITS: columns from here to N are stored as 0
     const float* out_scale;    // EPI_SCALE
+    int epi_kb;     // host side: most k-blocks for which eight epilogue warps pay (0: 16)
     int epi_warps;  // host side: 4 or 8 epilogue warps (the kernel variant launched)
     int dependent_launch;  // host side: launched with programmatic stream serialization
     // 1: the grid holds one CTA (pair) per work unit and a running CTA (pair)

@@ -198,9 +198,9 @@ unsigned blocks_of(long long n, long long per) { return static_cast<unsigned>((n
 cudaError_t launch_head_combine(const float2* parts, int n_parts, const __nv_bfloat16* X,
                                 const __nv_bfloat16* W, const long long* targets, int T, int h,
                                 int V, float* loss, float* lse, cudaStream_t st, int* launches) {
-    // as many rows a CTA as leave every SM one: few rows get many threads each
+    // as many rows a CTA as leave every SM its eight: few rows get many threads
     int rows = 1;
-    while (rows < 32 && T > 152LL * rows) rows *= 2;
+    while (rows < 32 && T > 8 * 152LL * rows) rows *= 2;
     ++*launches;
     return launch_dependent(head_combine_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, parts,
                             n_parts, X, W, targets, T, h, V, rows, loss, lse);

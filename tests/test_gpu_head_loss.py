@@ -56,7 +56,11 @@ SHAPES = [(1, 8, 1), (1, 64, 2), (3, 16, 5), (2, 1024, 509), (7, 264, 255), (5, 
           # widths (one 64-column step and a bit, several CTAs of columns),
           # vocabularies around its 32-row tasks and with more tasks than CTAs
           (8, 72, 31), (9, 328, 33), (15, 1000, 640), (16, 2056, 1003), (17, 2056, 1003), (4, 8, 20001),
-          (16, 64, 40007), (5, 64, 19456), (5, 64, 24360), (3, 128, 32), (3, 128, 40), (3, 128, 24)]
+          (16, 64, 40007), (5, 64, 19456), (5, 64, 24360), (3, 128, 32), (3, 128, 40), (3, 128, 24),
+          # one and a few tiles of tokens and their edges
+          (31, 264, 999), (33, 512, 1024), (64, 1024, 3001), (96, 72, 255), (97, 72, 257), (224, 328, 2003),
+          (225, 328, 2003), (230, 64, 129), (231, 64, 8000), (257, 2048, 4001), (333, 1024, 5003),
+          (384, 64, 700), (385, 64, 700), (513, 200, 1500), (576, 128, 33), (577, 128, 33), (40, 4096, 40001)]
 
 
 @pytest.mark.parametrize("T,h,V", SHAPES)
