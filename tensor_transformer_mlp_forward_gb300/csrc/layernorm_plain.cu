@@ -38,9 +38,13 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 
 constexpr int kNormMaxStages = 6;
 constexpr int kNormMaxCluster = 8;
-// Blocks begun before the one that is finished.  The ring needs twice as
-// many stages: 16-bit values have six, fp32 three.
-constexpr int norm_ahead(int elem) { return elem == 2 ? 2 : 1; }
+// Rows that a thread of the backward kernel takes together, and the blocks
+// that it begins before the one that it finishes.  The ring needs twice as
+// many stages as the latter.
+template <int VEC>
+constexpr int norm_rows() { return VEC == 8 ? 2 : 1; }
+template <int VEC>
+constexpr int norm_ahead(int elem) { return VEC == 1 && elem == 2 ? 2 : 1; }
 
 // A piece of a row held by one thread: VEC > 1 consecutive values, 16 bytes,
 // or (VEC 1, rows that do not start on 16-byte boundaries) two single values
@@ -295,39 +299,45 @@ struct NormBackwardArgs {
     int* status;
 };
 
-template <typename T, int VEC, int NV, int NT, int MIN_CTAS>
+template <typename T, int VEC, int NV, int NT, int MIN_CTAS, bool CLUSTER>
 __global__ void __launch_bounds__(NT, MIN_CTAS)
     norm_backward_ring_kernel(const T* __restrict__ dy, const T* __restrict__ x,
                               const T* __restrict__ gamma, const float* __restrict__ mean,
                               const float* __restrict__ rstd, const NormBackwardArgs p,
                               T* __restrict__ dx, float* __restrict__ part_g,
                               float* __restrict__ part_b) {
-    constexpr int AHEAD = norm_ahead(sizeof(T)), SLOTS = 2 * AHEAD;
+    // rows of a block that one thread takes together: two share the loop's
+    // overhead and gamma (one where the ring has no room for two, or rows are
+    // misaligned)
+    constexpr int U = norm_rows<VEC>();
+    constexpr int AHEAD = norm_ahead<VEC>(sizeof(T)), SLOTS = 2 * AHEAD;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kNormMaxStages];
     __shared__ uint64_t sums[SLOTS];  // a block's sums of all warps have arrived
-    __shared__ float2 slots[SLOTS][kNormMaxCluster * (NT / 32)];
+    __shared__ float2 slots[SLOTS][(CLUSTER ? kNormMaxCluster : 1) * (NT / 32)][U];
     __shared__ uint32_t abort_flag;
     pdl_launch_dependents();  // the next kernel may begin its launch
     constexpr long long E = sizeof(T);
-    const int group = 32 * p.W, R = NT / group;
-    const int g = threadIdx.x / group, sub = threadIdx.x % group;
-    const int cl = p.cl;
-    const int rank = cl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int unit = cl > 1 ? static_cast<int>(blockIdx.x) / cl : static_cast<int>(blockIdx.x);
+    const int group = CLUSTER ? NT : 32 * p.W, R = NT / group;
+    const int g = CLUSTER ? 0 : threadIdx.x / group, sub = threadIdx.x - g * group;
+    const int cl = CLUSTER ? p.cl : 1;
+    const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
+    const uint32_t unit = CLUSTER ? blockIdx.x / cl : blockIdx.x;
+    const uint32_t step = CLUSTER ? gridDim.x / cl : gridDim.x;
     const int c0 = rank * p.cols;              // this CTA's columns of a row
-    const int h = min(p.cols, p.h - c0);
-    const int blocks = (p.rows + R - 1) / R;
+    const int h = CLUSTER ? min(p.cols, p.h - c0) : p.h;
+    const uint32_t rows = p.rows, block_rows = R * U;
+    const uint32_t blocks = (rows + block_rows - 1) / block_rows;
     const long long total = E * p.rows * p.h;  // bytes of a tensor
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
         // a cluster counts the bytes that its warps send, one CTA its warps
-        for (int s = 0; s < SLOTS; ++s) mbar_init(&sums[s], cl > 1 ? 1 : NT / 32);
+        for (int s = 0; s < SLOTS; ++s) mbar_init(&sums[s], CLUSTER ? 1 : NT / 32);
         abort_flag = 0u;
         fence_mbar_init();
     }
     pdl_wait();  // dy may come from the kernel before this one
-    if (cl > 1)
+    if constexpr (CLUSTER)
         cluster_sync();  // the peers run: their shared memory may be written
     else
         __syncthreads();
@@ -336,36 +346,49 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     // block needs advances by additions: with divisions and 64-bit addresses
     // in the loop the overhead was 490 instructions a warp and block against
     // 200 of arithmetic.
-    const uint32_t step = gridDim.x / cl;
     const int n = blocks > unit ? static_cast<int>((blocks - unit + step - 1) / step) : 0;
-    const uint32_t rows = p.rows, row_step = step * R;
+    const uint32_t row_step = step * block_rows;
     const uint32_t stage_bytes = 2u * p.buf_bytes;
+    const int row_bytes = static_cast<int>(E) * h;
 
     // Thread 0: copies of the next block not yet issued into the next stage.
-    // Of the block's byte range whole 16-byte granules of the tensor are
-    // copied (all but its last few bytes).
-    const long long first_b0 = E * (static_cast<long long>(unit) * R * p.h + c0);
+    // One CTA a row: the block's rows are one contiguous range, of which whole
+    // 16-byte granules of the tensor are copied (all but its last few bytes).
+    // A cluster: each row's columns are copied by themselves.
+    const long long first_b0 = E * (static_cast<long long>(unit) * block_rows * p.h + c0);
+    const long long issue_step = E * row_step * p.h;
     long long issue_b0 = first_b0;
-    const long long issue_step = E * step * R * p.h;
-    const int block_bytes = static_cast<int>(E) * (cl > 1 ? h : R * p.h);
     int issue_left = n, issue_stage = 0;
-    auto copied = [&](long long b0, long long& a0) {  // first byte, and their number
+    uint32_t issue_row = unit * block_rows;
+    auto copied = [&](long long b0, int bytes, long long& a0) {  // first byte, and their number
         a0 = b0 & ~15LL;
-        const long long row_end = cl > 1 ? b0 + block_bytes : min(b0 + block_bytes, total);
-        const long long a1 = min((row_end + 15) & ~15LL, total & ~15LL);
+        const long long a1 = min((min(b0 + bytes, total) + 15) & ~15LL, total & ~15LL);
         return a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
     };
     auto issue = [&]() {
         if (issue_left <= 0) return;
-        long long a0;
-        const uint32_t bytes = copied(issue_b0, a0);
         const uint32_t dst = smem_u32(ring) + issue_stage * stage_bytes;
-        mbar_arrive_expect_tx(&full[issue_stage], 2 * bytes);
-        if (bytes) {
-            bulk_load(dst, reinterpret_cast<const uint8_t*>(x) + a0, bytes, &full[issue_stage]);
-            bulk_load(dst + p.buf_bytes, reinterpret_cast<const uint8_t*>(dy) + a0, bytes, &full[issue_stage]);
+        uint64_t* bar = &full[issue_stage];
+        const uint8_t *px = reinterpret_cast<const uint8_t*>(x), *pd = reinterpret_cast<const uint8_t*>(dy);
+        if (CLUSTER && U > 1) {
+            const int k = min(static_cast<uint32_t>(U), rows - issue_row);
+            mbar_arrive_expect_tx(bar, 2 * k * row_bytes);
+            for (int u = 0; u < k; ++u) {
+                const long long a0 = issue_b0 + u * E * p.h;
+                bulk_load(dst + u * row_bytes, px + a0, row_bytes, bar);
+                bulk_load(dst + u * row_bytes + p.buf_bytes, pd + a0, row_bytes, bar);
+            }
+        } else {
+            long long a0;
+            const uint32_t bytes = copied(issue_b0, CLUSTER ? row_bytes : static_cast<int>(block_rows) * row_bytes, a0);
+            mbar_arrive_expect_tx(bar, 2 * bytes);
+            if (bytes) {
+                bulk_load(dst, px + a0, bytes, bar);
+                bulk_load(dst + p.buf_bytes, pd + a0, bytes, bar);
+            }
         }
         issue_b0 += issue_step;
+        issue_row += row_step;
         --issue_left;
         if (++issue_stage == p.stages) issue_stage = 0;
     };
@@ -381,34 +404,44 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     for (int k = 0; k < NV; ++k) kg[k] = load_piece<T, VEC>(gamma + c0, k, group, sub, h);
     const float inv_h = 1.0f / static_cast<float>(p.h);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the statistics of a row (0 behind the last)
-    auto row_stats = [&](uint32_t row) {
-        return row < rows ? make_float2(__ldg(mean + row), __ldg(rstd + row)) : make_float2(0.0f, 0.0f);
+    struct Stats {
+        float2 v[U];
     };
-    // This group's row of a block in a stage's buffers; `skip`: where the block
-    // starts in its first 16-byte granule (rows of VEC 1 only).
-    const uint32_t group_off = static_cast<uint32_t>(E) * g * h;
+    // the statistics of this thread's rows (0 behind the last)
+    auto row_stats = [&](uint32_t row) {
+        Stats s;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            s.v[u] = row + u < rows ? make_float2(__ldg(mean + row + u), __ldg(rstd + row + u)) : both(0.0f);
+        return s;
+    };
+    // This thread's first row of a block in a stage's buffers; `skip`: where the
+    // block starts in its first 16-byte granule (rows of VEC 1 only).
+    const uint32_t group_off = static_cast<uint32_t>(row_bytes) * (g * U);
     const uint32_t skip0 = VEC == 1 ? static_cast<uint32_t>(first_b0 & 15) : 0u;
     const uint32_t skip_step = VEC == 1 ? static_cast<uint32_t>(issue_step & 15) : 0u;
     auto row_at = [&](int stage, uint32_t skip) {
         return reinterpret_cast<const T*>(ring + (stage * stage_bytes + skip + group_off));
     };
+    auto dy_of = [&](const T* sx) {
+        return reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(sx) + p.buf_bytes);
+    };
     // Begins the CTA's i-th block: waits for its copies and sends this warp's
-    // part of its row's sums of g and g (x - mu) to every CTA of the row.
+    // part of its rows' sums of g and g (x - mu) to every CTA of the row.
     // (A wait that gives up has set the status word; the loop goes on, on
     // whatever the buffers hold.)
     int b_stage = 0, b_slot = 0;
-    uint32_t b_phase = 0, b_skip = skip0, b_row = static_cast<uint32_t>(unit) * R + g;
-    auto begin = [&](int i, float mu) {
+    uint32_t b_phase = 0, b_skip = skip0, b_row = unit * block_rows + g * U;
+    auto begin = [&](int i, const Stats& st) {
         warp_wait_polls(&full[b_stage], b_phase, &abort_flag, p.status);
         if constexpr (VEC == 1) {
             if (i == n - 1) {  // the tensor's last few bytes, if they are here: plain loads
                 const long long b0 = first_b0 + i * issue_step;
+                const int block_bytes = CLUSTER ? row_bytes : static_cast<int>(block_rows) * row_bytes;
                 long long a0;
-                const uint32_t bytes = copied(b0, a0);
-                const long long b1 = cl > 1 ? b0 + block_bytes : min(b0 + block_bytes, total);
+                const uint32_t bytes = copied(b0, block_bytes, a0);
                 const long long e = max(a0 + bytes, b0) / E + threadIdx.x;
-                if (e < b1 / E) {
+                if (e < min(b0 + block_bytes, total) / E) {
                     uint8_t* d = ring + b_stage * stage_bytes + (e * E - a0);
                     *reinterpret_cast<T*>(d) = x[e];
                     *reinterpret_cast<T*>(d + p.buf_bytes) = dy[e];
@@ -416,34 +449,44 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
                 __syncthreads();
             }
         }
-        float2 m = both(0.0f), mx = both(0.0f);
-        if (b_row < rows) {
+        float2 m[U], mx[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) m[u] = mx[u] = both(0.0f);
+        if (b_row < rows) {  // (a second row behind the last reads stale values: its sums go nowhere)
             const T* sx = row_at(b_stage, b_skip);
-            const T* sdy = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(sx) + p.buf_bytes);
+            const T* sdy = dy_of(sx);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const Piece<T, VEC> px = load_piece_any<T, VEC>(sx, k, group, sub, h);
-                const Piece<T, VEC> pd = load_piece_any<T, VEC>(sdy, k, group, sub, h);
 #pragma unroll
-                for (int j = 0; j < PAIRS; ++j) {
-                    const float2 gj = product<VEC>(pair_of(pd, j), pair_of(kg[k], j));
-                    m = add2(m, gj);
-                    mx = fma2(gj, add2(pair_of(px, j), both(-mu)), mx);
+                for (int u = 0; u < U; ++u) {
+                    const Piece<T, VEC> px = load_piece_any<T, VEC>(sx + u * h, k, group, sub, h);
+                    const Piece<T, VEC> pd = load_piece_any<T, VEC>(sdy + u * h, k, group, sub, h);
+#pragma unroll
+                    for (int j = 0; j < PAIRS; ++j) {
+                        const float2 gj = product<VEC>(pair_of(pd, j), pair_of(kg[k], j));
+                        m[u] = add2(m[u], gj);
+                        mx[u] = fma2(gj, add2(pair_of(px, j), both(-st.v[u].x)), mx[u]);
+                    }
                 }
             }
         }
-        m = warp_sum(make_float2(m.x + m.y, mx.x + mx.y));
         uint64_t* bar = &sums[b_slot];
-        float2* slot = &slots[b_slot][rank * (NT / 32) + warp];
-        if (cl == 1) {
+        float2* slot = slots[b_slot][rank * (NT / 32) + warp];
+#pragma unroll
+        for (int u = 0; u < U; ++u) m[u] = warp_sum(make_float2(m[u].x + m[u].y, mx[u].x + mx[u].y));
+        if constexpr (!CLUSTER) {
             if (lane == 0) {
-                *slot = m;
+#pragma unroll
+                for (int u = 0; u < U; ++u) slot[u] = m[u];
                 mbar_arrive(bar);  // releases the slot to the waiting warps
             }
         } else {
-            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * (NT / 32) * sizeof(float2));
-            if (lane < cl)
-                st_async_v2(map_to_cta(smem_u32(slot), lane), m, map_to_cta(smem_u32(bar), lane));
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * (NT / 32) * U * sizeof(float2));
+            if (lane < cl) {
+                const uint32_t peer = map_to_cta(smem_u32(slot), lane), peer_bar = map_to_cta(smem_u32(bar), lane);
+#pragma unroll
+                for (int u = 0; u < U; ++u) st_async_v2(peer + u * sizeof(float2), m[u], peer_bar);
+            }
         }
         __syncwarp();
         if (++b_stage == p.stages) {
@@ -460,11 +503,11 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     // begun block i, so had finished block i - AHEAD and read its slots.  So 2
     // AHEAD slots are enough; and the buffers of block i - AHEAD are free.
     uint32_t row = b_row;
-    float2 st[AHEAD], st_next;
+    Stats st[AHEAD], st_next;
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
         st[a] = row_stats(row + a * row_step);
-        if (a < n) begin(a, st[a].x);
+        if (a < n) begin(a, st[a]);
     }
     st_next = row_stats(row + AHEAD * row_step);
     int stage = 0, slot = 0;
@@ -472,40 +515,55 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     T* out = dx + static_cast<long long>(row) * p.h + c0;
     const long long out_step = static_cast<long long>(row_step) * p.h;
     for (int i = 0; i < n; ++i) {
-        const float2 st_after = row_stats(row + (AHEAD + 1) * row_step);
+        const Stats st_after = row_stats(row + (AHEAD + 1) * row_step);
         warp_wait_polls(&sums[slot], phase, &abort_flag, p.status);
         if (threadIdx.x == 0 && i >= AHEAD) issue();  // block i - AHEAD is read
-        float2 m = both(0.0f);
-        if (cl > 1) {
-            for (int j = lane; j < cl * (NT / 32); j += 32) m = add2(m, slots[slot][j]);
-            m = warp_sum(m);
-        } else {
-            for (int j = 0; j < p.W; ++j) m = add2(m, slots[slot][g * p.W + j]);
-        }
-        if (row < rows) {
-            const float mu = st[0].x, rs = st[0].y;
-            const float mg = m.x * inv_h;                   // mean(g)
-            const float k2 = rs * rs * rs * (m.y * inv_h);  // rstd^2 mean(g xhat)
-            const T* sx = row_at(stage, skip);
-            const T* sdy = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(sx) + p.buf_bytes);
+        float2 m[U];
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const Piece<T, VEC> px = load_piece_any<T, VEC>(sx, k, group, sub, h);
-                const Piece<T, VEC> pd = load_piece_any<T, VEC>(sdy, k, group, sub, h);
-                Piece<T, VEC> o;
-#pragma unroll
-                for (int j = 0; j < PAIRS; ++j) {
-                    const float2 d = pair_of(pd, j);
-                    const float2 xc = add2(pair_of(px, j), both(-mu));
-                    const float2 gj = product<VEC>(d, pair_of(kg[k], j));
-                    set_pair(o, j, fma2(both(rs), add2(gj, both(-mg)), mul2(xc, both(-k2))));
-                    acc_g[k * PAIRS + j] = fma2(mul2(d, both(rs)), xc, acc_g[k * PAIRS + j]);
-                    acc_b[k * PAIRS + j] = add2(acc_b[k * PAIRS + j], d);
-                }
-                store_piece<T, VEC>(out, o, k, group, sub, h);
+        for (int u = 0; u < U; ++u) {
+            m[u] = both(0.0f);
+            if constexpr (CLUSTER) {
+                for (int j = lane; j < cl * (NT / 32); j += 32) m[u] = add2(m[u], slots[slot][j][u]);
+                m[u] = warp_sum(m[u]);
+            } else {
+#pragma unroll 4
+                for (int j = 0; j < p.W; ++j) m[u] = add2(m[u], slots[slot][g * p.W + j][u]);
             }
         }
-        if (i + AHEAD < n) begin(i + AHEAD, st_next.x);
+        if (row < rows) {
+            const bool second = U == 1 || row + 1 < rows;
+            float mg[U], k2[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float rs = st[0].v[u].y;
+                mg[u] = m[u].x * inv_h;                   // mean(g)
+                k2[u] = rs * rs * rs * (m[u].y * inv_h);  // rstd^2 mean(g xhat)
+            }
+            const T* sx = row_at(stage, skip);
+            const T* sdy = dy_of(sx);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u > 0 && !second) break;
+                    const float mu = st[0].v[u].x, rs = st[0].v[u].y;
+                    const Piece<T, VEC> px = load_piece_any<T, VEC>(sx + u * h, k, group, sub, h);
+                    const Piece<T, VEC> pd = load_piece_any<T, VEC>(sdy + u * h, k, group, sub, h);
+                    Piece<T, VEC> o;
+#pragma unroll
+                    for (int j = 0; j < PAIRS; ++j) {
+                        const float2 d = pair_of(pd, j);
+                        const float2 xc = add2(pair_of(px, j), both(-mu));
+                        const float2 gj = product<VEC>(d, pair_of(kg[k], j));
+                        set_pair(o, j, fma2(both(rs), add2(gj, both(-mg[u])), mul2(xc, both(-k2[u]))));
+                        acc_g[k * PAIRS + j] = fma2(mul2(d, both(rs)), xc, acc_g[k * PAIRS + j]);
+                        acc_b[k * PAIRS + j] = add2(acc_b[k * PAIRS + j], d);
+                    }
+                    store_piece<T, VEC>(out + u * p.h, o, k, group, sub, h);
+                }
+            }
+        }
+        if (i + AHEAD < n) begin(i + AHEAD, st_next);
 #pragma unroll
         for (int a = 0; a + 1 < AHEAD; ++a) st[a] = st[a + 1];
         st[AHEAD - 1] = st_next;
@@ -523,7 +581,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     // No CTA leaves while a value that it has sent is on its way to a peer:
     // it has itself waited for the last block's sums, to which the peers'
     // own values of every block belong, but not for their receipt.
-    if (cl > 1) cluster_sync();
+    if constexpr (CLUSTER) cluster_sync();
     float* out_g = part_g + static_cast<long long>(unit) * p.h + c0;
     float* out_b = part_b + static_cast<long long>(unit) * p.h + c0;
     if (R == 1) {
@@ -774,11 +832,6 @@ struct NormPlan {
 
 constexpr int kSmemMost = 227 * 1024;
 
-// CTAs of 256 threads an SM: 16-bit pieces fit 80 registers a thread, the
-// other forms take up to 128.
-template <int VEC>
-constexpr int kNormCtas = 2;
-
 NormPlan norm_plan(int T, int h, int elem) {
     NormPlan p{};
     // 256 threads: two CTAs an SM (128 registers a thread).  Rows beyond eight
@@ -788,14 +841,12 @@ NormPlan norm_plan(int T, int h, int elem) {
     if (p.cl > kNormMaxCluster) return NormPlan{};
     p.cols = p.cl == 1 ? h : ceil_div(ceil_div(h, p.cl), 8) * 8;
     p.W = p.cl > 1 ? p.threads / 32 : ceil_pow2(ceil_div(h, 32 * 16));
-    const int R = p.threads / (32 * p.W);
-    // a block of R rows and what its first and last granule hold besides
-    p.buf_bytes = (static_cast<int>((static_cast<long long>(R) * p.cols * elem + 15) / 16) + 1) * 16;
-    const int per_sm = p.threads == 512 ? 1 : elem == 2 && h % 8 == 0 ? kNormCtas<8> : kNormCtas<1>;
+    const int R = p.threads / (32 * p.W), U = elem == 2 && h % 8 == 0 ? norm_rows<8>() : norm_rows<1>();
+    // a block of rows and what its first and last granule hold besides
+    p.buf_bytes = (static_cast<int>((static_cast<long long>(R) * U * p.cols * elem + 15) / 16) + 1) * 16;
+    const int per_sm = p.threads == 512 ? 1 : 2;
     p.room = kSmemMost / per_sm - (per_sm == 1 ? 5120 : 3072);  // beside the static arrays
-    const int blocks = ceil_div(T, R), units = kSms * per_sm / p.cl;
-    // at most 16 bytes a value and thread: six stages of 16-bit values, three
-    // of fp32
+    const int blocks = ceil_div(T, R * U), units = kSms * per_sm / p.cl;
     p.stages = std::min(kNormMaxStages, p.room / (2 * p.buf_bytes));
     // the meeting place of the groups' sums: 16 values a thread and tensor
     p.smem = std::max(p.stages * 2 * p.buf_bytes, R > 1 ? 2 * 16 * 4 * 32 * p.W : 0);
@@ -811,7 +862,8 @@ template <typename T, int VEC, int NV, int NT, int MIN_CTAS>
 cudaError_t backward_ring(const NormPlan& p, const T* dy, const T* x, const T* gamma, const float* mean,
                           const float* rstd, int T_, int h, T* dx, float* pg, float* pb, int* status,
                           cudaStream_t st, int* units) {
-    auto kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS>;
+    auto kern = p.cl > 1 ? norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, true>
+                         : norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.room);
     if (e != cudaSuccess) return e;
     const NormBackwardArgs a{T_, h, p.W, p.stages, p.cl, p.cols, p.buf_bytes, status};
@@ -857,7 +909,7 @@ cudaError_t backward_rows(const NormPlan& p, const T* dy, const T* x, const T* g
     constexpr int N = Piece<T, VEC>::N;
     if (p.threads == 512)
         return backward_ring<T, VEC, 16 / N, 512, 1>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
-    return backward_ring<T, VEC, 16 / N, 256, kNormCtas<VEC>>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
+    return backward_ring<T, VEC, 16 / N, 256, 2>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
 }
 
 template <typename T>
