@@ -2143,9 +2143,13 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
     cudaError_t e;
     if (head_few(T)) {
         __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(dz);
+        alignas(64) CUtensorMap tm;
+        const int box_rows = head_few_box_rows(h);
+        if (box_rows)
+            if (int rc = make_map(&tm, W, V, h, 1, ON_CONTIG, box_rows)) return rc;
         e = launch_head_few_backward(dloss, cb(X), cb(W), targets, lse, T, h, V, z,
                                      z + 16 * static_cast<size_t>(p.width), scale, plane,
-                                     reinterpret_cast<__nv_bfloat16*>(dW), st, &t_last_launches);
+                                     reinterpret_cast<__nv_bfloat16*>(dW), &tm, d.status, st, &t_last_launches);
         if (e == cudaSuccess)
             e = launch_head_reduce(plane, p.splits, 1LL * T * h, scale, reinterpret_cast<__nv_bfloat16*>(dX), st,
                                    &t_last_launches);

@@ -372,6 +372,218 @@ __global__ void __launch_bounds__(32 * kWarps, kGradCtas)
     }
 }
 
+// The whole backward pass in one reading of W, for rows of up to 1024 values:
+// a CTA takes blocks of 16 vocabulary rows, which the tensor memory
+// accelerator brings to shared memory (boxes of 64 columns, 128-byte swizzle,
+// a ring of kFusedStages blocks).  Warp w owns columns 64 w .. 64 w + 63: its
+// share of the logits' sums, then (dz of the block known) its columns of dX
+// and of the block's dW.  X stays in registers in both operand forms, dX's
+// sums too.  The logits of block i + 1 are begun before block i is finished,
+// so that one pair of barriers a block serves both.
+// Two kernels that read W twice (above) took 63 us where this takes @@ (7
+// tokens, 50257 x 1024).
+constexpr int kFusedWarps = 16;
+constexpr int kFusedThreads = 32 * kFusedWarps;
+constexpr int kFusedStages = 6;
+constexpr int kFusedRows = 16;
+constexpr int kBoxBytes = kFusedRows * 128;
+constexpr int kFusedStageBytes = kFusedWarps * kBoxBytes;
+constexpr int kFusedSmem = 1024 + kFusedStages * kFusedStageBytes;
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 u;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr));
+    return u;
+}
+
+__global__ void __launch_bounds__(kFusedThreads, 1)
+    head_few_fused_kernel(const __grid_constant__ CUtensorMap tmW, const FewArgs p,
+                          __nv_bfloat16* __restrict__ dW, float* __restrict__ plane, int* status) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kFusedStages];
+    __shared__ float red[kFusedWarps][kTokens][kFusedRows + 4];
+    __shared__ __align__(16) __nv_bfloat16 dzs[kTokens][kFusedRows], dzts[kFusedRows][kTokens];
+    __shared__ uint32_t abort_flag;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzle atoms repeat every 1024 bytes
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int boxes = (p.h + 63) / 64;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kFusedStages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0u;
+        fence_mbar_init();
+        prefetch_tmap(&tmW);
+    }
+    __syncthreads();
+    pdl_wait();  // X comes from the kernel before this one
+    const int blocks = (p.V + kFusedRows - 1) / kFusedRows;
+    const int n = blocks > static_cast<int>(blockIdx.x) ? (blocks - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1 : 0;
+    auto issue = [&](int i) {  // thread 0: the CTA's i-th block
+        if (i >= n) return;
+        const int s = i % kFusedStages;
+        const int v0 = (static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x)) * kFusedRows;
+        mbar_arrive_expect_tx(&full[s], boxes * kBoxBytes);
+        for (int b = 0; b < boxes; ++b)
+            tma_load_3d(&tmW, smem_u32(&full[s]), ring + s * kFusedStageBytes + b * kBoxBytes, 64 * b, 0, v0);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < kFusedStages; ++i) issue(i);
+
+    // X as rows (tokens) x k for the logits, as k (tokens) x columns for dW
+    const int col0 = warp * 64;
+    const bool mine = warp < boxes;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 xa[2][2];
+    uint32_t xb[2][8];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int k = col0 + s * 32 + q * 8;
+        xa[0][s] = k < p.h && g < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(g) * p.h + k)) : zero;
+        xa[1][s] = k < p.h && g + 8 < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(g + 8) * p.h + k)) : zero;
+    }
+    {
+        uint4 r[4];
+        const int c = col0 + g * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int tok = 2 * q + (i & 1) + (i >> 1) * 8;
+            r[i] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
+        }
+        pairs_of(r[0], r[1], xb[0]);
+        pairs_of(r[2], r[3], xb[1]);
+    }
+    // thread (token, row of the block) of the logits' meeting
+    const int t = threadIdx.x >> 4, vr = threadIdx.x & 15;
+    long long y = -1;
+    float lse2 = INFINITY, weight = 0.0f, s = 0.0f;
+    for (int i = 0; i < p.T; ++i)
+        if (__ldg(p.targets + i) >= 0) s = fmaxf(s, fabsf(__ldg(p.dloss + i)));
+    if (!(s > 0.0f && s < INFINITY)) s = 1.0f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = s;
+    if (t < p.T) {
+        y = __ldg(p.targets + t);
+        if (y >= 0) {
+            lse2 = __ldg(p.lse + t) * kLog2e;
+            weight = y < p.V ? __ldg(p.dloss + t) / s : __int_as_float(0x7FC00000);
+        }
+    }
+    float acc[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+
+    // The warp's share of block i's logits, to red.  Rows 8 j + g, 16-byte piece
+    // c of row r at position c ^ (r mod 8) of its 128 bytes.
+    auto logits = [&](int i) {
+        const int st = i % kFusedStages;
+        warp_wait_polls(&full[st], static_cast<uint32_t>(i / kFusedStages) & 1u, &abort_flag, status);
+        const uint32_t box = ring + st * kFusedStageBytes + warp * kBoxBytes;
+        float z[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.0f;
+            if (!mine) continue;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 u = ld_shared_v4(box + (8 * j + g) * 128 + (((q + 4 * k) ^ g) << 4));
+                mma16816(z[j], xa[0][k].x, xa[1][k].x, xa[0][k].y, xa[1][k].y, u.x, u.y);
+                mma16816(z[j], xa[0][k].z, xa[1][k].z, xa[0][k].w, xa[1][k].w, u.z, u.w);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            *reinterpret_cast<float2*>(&red[warp][g][8 * j + 2 * q]) = make_float2(z[j][0], z[j][1]);
+            *reinterpret_cast<float2*>(&red[warp][g + 8][8 * j + 2 * q]) = make_float2(z[j][2], z[j][3]);
+        }
+    };
+    // dz of block i from the warps' shares, in both operand forms.
+    auto gradient = [&](int i) {
+        if (threadIdx.x >= kTokens * kFusedRows) return;
+        const int v = (static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x)) * kFusedRows + vr;
+        float z = 0.0f;
+        for (int w = 0; w < boxes; ++w) z += red[w][t][vr];
+        float d = weight * ex2_approx(fmaf(z, kLog2e, -lse2));
+        if (v == y) d -= weight;
+        if (v >= p.V) d = 0.0f;
+        const __nv_bfloat16 b = __float2bfloat16_rn(d);
+        dzs[t][vr] = b;
+        dzts[vr][t] = b;
+    };
+    // dX's sums and dW of block i.
+    auto finish = [&](int i) {
+        if (!mine) return;
+        const uint32_t box = ring + (i % kFusedStages) * kFusedStageBytes + warp * kBoxBytes;
+        const int v0 = (static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x)) * kFusedRows;
+        uint32_t a[4], tt[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = g + (k & 1) * 8, c = 2 * q + (k >> 1) * 8;
+            a[k] = *reinterpret_cast<const uint32_t*>(&dzs[r][c]);
+            tt[k] = *reinterpret_cast<const uint32_t*>(&dzts[r][c]);
+        }
+        {
+            uint4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 2 * q + (k & 1) + (k >> 1) * 8;
+                w[k] = ld_shared_v4(box + r * 128 + ((g ^ (r & 7)) << 4));
+            }
+            uint32_t lo[8], hi[8];
+            pairs_of(w[0], w[1], lo);
+            pairs_of(w[2], w[3], hi);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mma16816(acc[j], a[0], a[1], a[2], a[3], lo[j], hi[j]);
+        }
+        float o[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+            mma16816(o[j], tt[0], tt[1], tt[2], tt[3], xb[0][j], xb[1][j]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // rows g, g + 8
+            const int v = v0 + g + 8 * r;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // columns 16 q .., 16 q + 8 ..
+                const int c = col0 + 16 * q + 8 * half, e = 2 * r + half;
+                if (v < p.V && c < p.h)
+                    __stcs(reinterpret_cast<uint4*>(dW + static_cast<long long>(v) * p.h + c),
+                           make_uint4(pack_bf16x2(s * o[0][e], s * o[1][e]), pack_bf16x2(s * o[2][e], s * o[3][e]),
+                                      pack_bf16x2(s * o[4][e], s * o[5][e]), pack_bf16x2(s * o[6][e], s * o[7][e])));
+            }
+        }
+    };
+
+    if (n > 0) {
+        logits(0);
+        __syncthreads();
+        gradient(0);
+        __syncthreads();
+    }
+    for (int i = 0; i < n; ++i) {
+        if (i + 1 < n) logits(i + 1);
+        finish(i);
+        __syncthreads();  // block i is read, block i + 1's shares are there
+        if (threadIdx.x == 0) issue(i + kFusedStages);
+        if (i + 1 < n) gradient(i + 1);
+        __syncthreads();
+    }
+    if (!mine) return;
+    float* out = plane + static_cast<long long>(blockIdx.x) * p.T * p.h;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int tok = g + 8 * r;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int c = col0 + 16 * q + 8 * half, e = 2 * r + half;
+            if (tok < p.T && c < p.h) {
+                float4* d = reinterpret_cast<float4*>(out + static_cast<long long>(tok) * p.h + c);
+                d[0] = make_float4(acc[0][e], acc[1][e], acc[2][e], acc[3][e]);
+                d[1] = make_float4(acc[4][e], acc[5][e], acc[6][e], acc[7][e]);
+            }
+        }
+    }
+}
+
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 }  // namespace
@@ -382,8 +594,13 @@ int head_few_parts(int V) { return std::min(ceil_div(V, kRows), kSms * kCtasPerS
 
 int head_few_ldz(int V) { return ceil_div(V, kRows) * kRows; }
 
-// Ranges of vocabulary rows, as many as fill the GPU with CTAs of 256 columns.
+// Rows of W that a fused block brings (0: h is too wide for the fused form).
+int head_few_box_rows(int h) { return h <= 64 * kFusedWarps ? kFusedRows : 0; }
+
+// Planes of dX: the fused form's CTAs, or the ranges of vocabulary rows, as many
+// as fill the GPU with CTAs of 256 columns.
 int head_few_planes(int h, int V) {
+    if (head_few_box_rows(h)) return std::min(kSms, ceil_div(V, kFusedRows));
     const int col_ctas = ceil_div(h, kColumns * kWarps);
     return std::max(1, std::min(kSms * kGradCtas / col_ctas, ceil_div(V, 16)));
 }
@@ -400,12 +617,20 @@ cudaError_t launch_head_few_lse(const __nv_bfloat16* X, const __nv_bfloat16* W, 
 cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X, const __nv_bfloat16* W,
                                      const long long* targets, const float* lse, int T, int h, int V,
                                      __nv_bfloat16* dz, __nv_bfloat16* dzt, float* scale, float* plane,
-                                     __nv_bfloat16* dW, cudaStream_t st, int* launches) {
+                                     __nv_bfloat16* dW, const CUtensorMap* tm, int* status, cudaStream_t st,
+                                     int* launches) {
     FewArgs a = {};
     a.X = X; a.W = W; a.targets = targets; a.T = T; a.h = h; a.V = V;
     a.dloss = dloss; a.lse = lse; a.dz = dz; a.dzt = dzt; a.ldz = head_few_ldz(V); a.scale = scale;
     ++*launches;
-    cudaError_t e = launch_dependent(head_few_logits_kernel<true>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0,
+    cudaError_t e;
+    if (head_few_box_rows(h)) {
+        e = cudaFuncSetAttribute(head_few_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(head_few_fused_kernel, dim3(head_few_planes(h, V)), dim3(kFusedThreads), kFusedSmem, st,
+                                *tm, a, dW, plane, status);
+    }
+    e = launch_dependent(head_few_logits_kernel<true>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0,
                                      st, a);
     if (e != cudaSuccess) return e;
     const int planes = head_few_planes(h, V);
