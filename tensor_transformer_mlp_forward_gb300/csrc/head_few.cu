@@ -380,8 +380,10 @@ __global__ void __launch_bounds__(32 * kWarps, kGradCtas)
 // and of the block's dW.  X stays in registers in both operand forms, dX's
 // sums too.  The logits of block i + 1 are begun before block i is finished,
 // so that one pair of barriers a block serves both.
-// Two kernels that read W twice (above) took 63 us where this takes @@ (7
-// tokens, 50257 x 1024).
+// The warp-level matrix instructions are what bounds this kernel (with 16
+// tokens in their rows: 58 us of which the memory alone needs 22 to read and
+// 14 more to write).  So the tokens are their columns, in TT tiles of eight:
+// up to eight tokens take half the instructions.
 constexpr int kFusedWarps = 16;
 constexpr int kFusedThreads = 32 * kFusedWarps;
 constexpr int kFusedStages = 6;
@@ -396,14 +398,22 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     return u;
 }
 
+__device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+
+template <int TT>
 __global__ void __launch_bounds__(kFusedThreads, 1)
     head_few_fused_kernel(const __grid_constant__ CUtensorMap tmW, const FewArgs p,
                           __nv_bfloat16* __restrict__ dW, float* __restrict__ plane, int* status) {
     pdl_launch_dependents();  // the next kernel may begin its launch
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kFusedStages];
-    __shared__ float red[kFusedWarps][kTokens][kFusedRows + 4];
-    __shared__ __align__(16) __nv_bfloat16 dzs[kTokens][kFusedRows], dzts[kFusedRows][kTokens];
+    __shared__ float red[kFusedWarps][kFusedRows][8 * TT + 4];
+    __shared__ __align__(16) __nv_bfloat16 dzs[8 * TT][kFusedRows], dzts[kFusedRows][8 * TT];
     __shared__ uint32_t abort_flag;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzle atoms repeat every 1024 bytes
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -416,44 +426,43 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     }
     __syncthreads();
     pdl_wait();  // X comes from the kernel before this one
+    const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
     const int blocks = (p.V + kFusedRows - 1) / kFusedRows;
-    const int n = blocks > static_cast<int>(blockIdx.x) ? (blocks - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1 : 0;
+    const int n = blocks > first ? (blocks - 1 - first) / step + 1 : 0;
     auto issue = [&](int i) {  // thread 0: the CTA's i-th block
         if (i >= n) return;
         const int s = i % kFusedStages;
-        const int v0 = (static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x)) * kFusedRows;
         mbar_arrive_expect_tx(&full[s], boxes * kBoxBytes);
         for (int b = 0; b < boxes; ++b)
-            tma_load_3d(&tmW, smem_u32(&full[s]), ring + s * kFusedStageBytes + b * kBoxBytes, 64 * b, 0, v0);
+            tma_load_3d(&tmW, smem_u32(&full[s]), ring + s * kFusedStageBytes + b * kBoxBytes, 64 * b, 0,
+                        (first + i * step) * kFusedRows);
     };
     if (threadIdx.x == 0)
         for (int i = 0; i < kFusedStages; ++i) issue(i);
 
-    // X as rows (tokens) x k for the logits, as k (tokens) x columns for dW
+    // X as columns (tokens) x k for the logits, as k (tokens) x columns for dW
     const int col0 = warp * 64;
     const bool mine = warp < boxes;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 xa[2][2];
-    uint32_t xb[2][8];
+    uint4 xa[TT][2];
+    uint32_t xb[TT][8];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int k = col0 + s * 32 + q * 8;
-        xa[0][s] = k < p.h && g < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(g) * p.h + k)) : zero;
-        xa[1][s] = k < p.h && g + 8 < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(g + 8) * p.h + k)) : zero;
-    }
-    {
-        uint4 r[4];
-        const int c = col0 + g * 8;
+    for (int tt = 0; tt < TT; ++tt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tok = 2 * q + (i & 1) + (i >> 1) * 8;
-            r[i] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
+        for (int k = 0; k < 2; ++k) {
+            const int c = col0 + k * 32 + q * 8, tok = g + 8 * tt;
+            xa[tt][k] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
         }
-        pairs_of(r[0], r[1], xb[0]);
-        pairs_of(r[2], r[3], xb[1]);
+        uint4 r[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = col0 + g * 8, tok = 2 * q + k + 8 * tt;
+            r[k] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
+        }
+        pairs_of(r[0], r[1], xb[tt]);
     }
-    // thread (token, row of the block) of the logits' meeting
-    const int t = threadIdx.x >> 4, vr = threadIdx.x & 15;
+    // thread (row of the block, token) of the logits' meeting
+    const int vr = threadIdx.x / (8 * TT), t = threadIdx.x % (8 * TT);
     long long y = -1;
     float lse2 = INFINITY, weight = 0.0f, s = 0.0f;
     for (int i = 0; i < p.T; ++i)
@@ -467,40 +476,45 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             weight = y < p.V ? __ldg(p.dloss + t) / s : __int_as_float(0x7FC00000);
         }
     }
-    float acc[8][4];
+    float acc[TT][4][4];  // [.][m]: columns 8 g + 2 m, + 1 of tokens 2 q, 2 q + 1
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[tt][m][0] = acc[tt][m][1] = acc[tt][m][2] = acc[tt][m][3] = 0.0f;
 
-    // The warp's share of block i's logits, to red.  Rows 8 j + g, 16-byte piece
-    // c of row r at position c ^ (r mod 8) of its 128 bytes.
+    // The warp's share of block i's logits, to red.  16-byte piece c of row r
+    // sits at position c ^ (r mod 8) of its 128 bytes.
     auto logits = [&](int i) {
         const int st = i % kFusedStages;
         warp_wait_polls(&full[st], static_cast<uint32_t>(i / kFusedStages) & 1u, &abort_flag, status);
-        const uint32_t box = ring + st * kFusedStageBytes + warp * kBoxBytes;
-        float z[2][4];
+        if (!mine) return;
+        const uint32_t box = ring + st * kFusedStageBytes + warp * kBoxBytes + g * 128;
+        float z[TT][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.0f;
-            if (!mine) continue;
+        for (int tt = 0; tt < TT; ++tt) z[tt][0] = z[tt][1] = z[tt][2] = z[tt][3] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 u = ld_shared_v4(box + (8 * j + g) * 128 + (((q + 4 * k) ^ g) << 4));
-                mma16816(z[j], xa[0][k].x, xa[1][k].x, xa[0][k].y, xa[1][k].y, u.x, u.y);
-                mma16816(z[j], xa[0][k].z, xa[1][k].z, xa[0][k].w, xa[1][k].w, u.z, u.w);
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t at = box + (((q + 4 * k) ^ g) << 4);
+            const uint4 lo = ld_shared_v4(at), hi = ld_shared_v4(at + 8 * 128);  // rows g, g + 8
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                mma16816(z[tt], lo.x, hi.x, lo.y, hi.y, xa[tt][k].x, xa[tt][k].y);
+                mma16816(z[tt], lo.z, hi.z, lo.w, hi.w, xa[tt][k].z, xa[tt][k].w);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            *reinterpret_cast<float2*>(&red[warp][g][8 * j + 2 * q]) = make_float2(z[j][0], z[j][1]);
-            *reinterpret_cast<float2*>(&red[warp][g + 8][8 * j + 2 * q]) = make_float2(z[j][2], z[j][3]);
+        for (int tt = 0; tt < TT; ++tt) {
+            *reinterpret_cast<float2*>(&red[warp][g][8 * tt + 2 * q]) = make_float2(z[tt][0], z[tt][1]);
+            *reinterpret_cast<float2*>(&red[warp][g + 8][8 * tt + 2 * q]) = make_float2(z[tt][2], z[tt][3]);
         }
     };
     // dz of block i from the warps' shares, in both operand forms.
     auto gradient = [&](int i) {
-        if (threadIdx.x >= kTokens * kFusedRows) return;
-        const int v = (static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x)) * kFusedRows + vr;
+        if (vr >= kFusedRows) return;
+        const int v = (first + i * step) * kFusedRows + vr;
         float z = 0.0f;
-        for (int w = 0; w < boxes; ++w) z += red[w][t][vr];
+#pragma unroll 4
+        for (int w = 0; w < boxes; ++w) z += red[w][vr][t];
         float d = weight * ex2_approx(fmaf(z, kLog2e, -lse2));
         if (v == y) d -= weight;
         if (v >= p.V) d = 0.0f;
@@ -512,14 +526,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     auto finish = [&](int i) {
         if (!mine) return;
         const uint32_t box = ring + (i % kFusedStages) * kFusedStageBytes + warp * kBoxBytes;
-        const int v0 = (static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x)) * kFusedRows;
-        uint32_t a[4], tt[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = g + (k & 1) * 8, c = 2 * q + (k >> 1) * 8;
-            a[k] = *reinterpret_cast<const uint32_t*>(&dzs[r][c]);
-            tt[k] = *reinterpret_cast<const uint32_t*>(&dzts[r][c]);
-        }
+        const int v0 = (first + i * step) * kFusedRows;
         {
             uint4 w[4];
 #pragma unroll
@@ -531,13 +538,26 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             pairs_of(w[0], w[1], lo);
             pairs_of(w[2], w[3], hi);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mma16816(acc[j], a[0], a[1], a[2], a[3], lo[j], hi[j]);
+            for (int tt = 0; tt < TT; ++tt) {
+                const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&dzs[g + 8 * tt][2 * q]);
+                const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&dzs[g + 8 * tt][2 * q + 8]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    mma16816(acc[tt][m], lo[2 * m], lo[2 * m + 1], hi[2 * m], hi[2 * m + 1], b0, b1);
+            }
         }
+        uint32_t a[2 * TT];
+#pragma unroll
+        for (int k = 0; k < 2 * TT; ++k)
+            a[k] = *reinterpret_cast<const uint32_t*>(&dzts[g + (k & 1) * 8][2 * q + (k >> 1) * 8]);
         float o[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-            mma16816(o[j], tt[0], tt[1], tt[2], tt[3], xb[0][j], xb[1][j]);
+            if constexpr (TT == 1)
+                mma1688(o[j], a[0], a[1], xb[0][j]);
+            else
+                mma16816(o[j], a[0], a[1], a[2], a[3], xb[0][j], xb[1][j]);
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {  // rows g, g + 8
@@ -567,21 +587,30 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         if (i + 1 < n) gradient(i + 1);
         __syncthreads();
     }
-    if (!mine) return;
-    float* out = plane + static_cast<long long>(blockIdx.x) * p.T * p.h;
+    const int c = col0 + 8 * g;
+    if (!mine || c >= p.h) return;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int tok = g + 8 * r;
+    for (int tt = 0; tt < TT; ++tt) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int c = col0 + 16 * q + 8 * half, e = 2 * r + half;
-            if (tok < p.T && c < p.h) {
-                float4* d = reinterpret_cast<float4*>(out + static_cast<long long>(tok) * p.h + c);
-                d[0] = make_float4(acc[0][e], acc[1][e], acc[2][e], acc[3][e]);
-                d[1] = make_float4(acc[4][e], acc[5][e], acc[6][e], acc[7][e]);
+        for (int e = 0; e < 2; ++e) {
+            const int tok = 2 * q + e + 8 * tt;
+            if (tok < p.T) {
+                float4* d = reinterpret_cast<float4*>(plane + (static_cast<long long>(blockIdx.x) * p.T + tok) * p.h + c);
+                d[0] = make_float4(acc[tt][0][e], acc[tt][0][2 + e], acc[tt][1][e], acc[tt][1][2 + e]);
+                d[1] = make_float4(acc[tt][2][e], acc[tt][2][2 + e], acc[tt][3][e], acc[tt][3][2 + e]);
             }
         }
     }
+}
+
+template <int TT>
+cudaError_t launch_fused(const CUtensorMap& tm, const FewArgs& a, int ctas, __nv_bfloat16* dW, float* plane,
+                         int* status, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(head_few_fused_kernel<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kFusedSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(head_few_fused_kernel<TT>, dim3(ctas), dim3(kFusedThreads), kFusedSmem, st, tm, a, dW,
+                            plane, status);
 }
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -625,10 +654,9 @@ cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X,
     ++*launches;
     cudaError_t e;
     if (head_few_box_rows(h)) {
-        e = cudaFuncSetAttribute(head_few_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem);
-        if (e != cudaSuccess) return e;
-        return launch_dependent(head_few_fused_kernel, dim3(head_few_planes(h, V)), dim3(kFusedThreads), kFusedSmem, st,
-                                *tm, a, dW, plane, status);
+        const int ctas = head_few_planes(h, V);
+        return T <= 8 ? launch_fused<1>(*tm, a, ctas, dW, plane, status, st)
+                      : launch_fused<2>(*tm, a, ctas, dW, plane, status, st);
     }
     e = launch_dependent(head_few_logits_kernel<true>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0,
                                      st, a);
