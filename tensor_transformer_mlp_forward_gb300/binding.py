@@ -9,6 +9,7 @@ library's kernels; there is no other code path.  A missing library raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -634,24 +635,17 @@ def _stream_of(stream, device: int) -> int:
     return _stream(stream)
 
 
-def _new(shape, dtype, device, stream):
-    """A fresh tensor from the memory pool of the stream that will write it
-    (so that freeing it cannot hand it to another stream)."""
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Context in which fresh tensors come from the memory pool of the stream
+    that will write them (so that freeing one cannot hand it to another)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _HERE_AND_NOW
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _scratch(ws, name: str, need: int, dtype, device, index: int, stream):
-    """Address and size of the caller's scratch, or of a fresh one of `need`
-    elements, and the tensor, to be kept until the launch."""
-    if ws is None:
-        ws = _new((max(need, 1),), dtype, device, stream)
-        return ws.data_ptr(), ws.numel(), ws
-    return _in(ws, name, ws.shape, dtype, index), ws.numel(), ws
+    return torch.cuda.stream(stream)
 
 
 def _dtype_of(x, name: str) -> int:
@@ -663,24 +657,44 @@ def _dtype_of(x, name: str) -> int:
 
 _F32 = torch.float32
 _BF16 = torch.bfloat16
+_I64 = torch.int64
+_U8 = torch.uint8
 
+
+def _device_of(x) -> int:
+    return torch.cuda.current_device() if x.is_cuda else -1  # -1: the first check names x
+
+
+# The calls below are short on the GPU, so they are short here too: a fresh
+# tensor is not checked again, and nothing is looked up twice.
 
 def tp_ln_forward(x, gamma, beta, eps: float = 1e-5, y=None, mean=None, rstd=None, stream=None):
     """y, mean, rstd of y = LayerNorm(x) * gamma + beta, x [T, h] in bfloat16,
     float16 or float32 (mean and rstd [T] are float32)."""
     T, h = shape = x.shape
-    dt = x.dtype
+    dt, d = x.dtype, _device_of(x)
     code = _dtype_of(x, "x")
-    d = torch.cuda.current_device() if x.is_cuda else -1
     xp = _in(x, "x", shape, dt, d)
     gp, bp = _in(gamma, "gamma", (h,), dt, d), _in(beta, "beta", (h,), dt, d)
-    dev = x.device
-    y = _new(shape, dt, dev, stream) if y is None else y
-    mean = _new((T,), _F32, dev, stream) if mean is None else mean
-    rstd = _new((T,), _F32, dev, stream) if rstd is None else rstd
-    _check("tp_ln_forward", lib().tp_ln_forward(
-        xp, gp, bp, T, h, code, eps, _in(y, "y", shape, dt, d), _in(mean, "mean", (T,), _F32, d),
-        _in(rstd, "rstd", (T,), _F32, d), _stream_of(stream, d)))
+    with _on(stream):
+        if y is None:
+            y = torch.empty_like(x)
+            yp = y.data_ptr()
+        else:
+            yp = _in(y, "y", shape, dt, d)
+        if mean is None:
+            mean = torch.empty(T, dtype=_F32, device=x.device)
+            mp = mean.data_ptr()
+        else:
+            mp = _in(mean, "mean", (T,), _F32, d)
+        if rstd is None:
+            rstd = torch.empty_like(mean)
+            rp = rstd.data_ptr()
+        else:
+            rp = _in(rstd, "rstd", (T,), _F32, d)
+    status = lib().tp_ln_forward(xp, gp, bp, T, h, code, eps, yp, mp, rp, _stream_of(stream, d))
+    if status:
+        _check("tp_ln_forward", status)
     return y, mean, rstd
 
 
@@ -688,23 +702,39 @@ def tp_ln_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, p
                    stream=None):
     """dx (of x's type), dgamma, dbeta (float32) of tp_ln_forward."""
     T, h = shape = x.shape
-    dt = x.dtype
+    dt, d = x.dtype, _device_of(x)
     code = _dtype_of(x, "x")
-    d = torch.cuda.current_device() if x.is_cuda else -1
     xp = _in(x, "x", shape, dt, d)
-    args = (_in(dy, "dy", shape, dt, d), xp, _in(gamma, "gamma", (h,), dt, d),
-            _in(mean, "mean", (T,), _F32, d), _in(rstd, "rstd", (T,), _F32, d))
-    dev = x.device
-    dx = _new(shape, dt, dev, stream) if dx is None else dx
-    dgamma = _new((h,), _F32, dev, stream) if dgamma is None else dgamma
-    dbeta = _new((h,), _F32, dev, stream) if dbeta is None else dbeta
+    dyp, gp = _in(dy, "dy", shape, dt, d), _in(gamma, "gamma", (h,), dt, d)
+    mp, rp = _in(mean, "mean", (T,), _F32, d), _in(rstd, "rstd", (T,), _F32, d)
     need = lib().tp_ln_backward_workspace_floats(T, h, code)
-    pp, pn, partial = _scratch(partial, "partial", need, _F32, dev, d, stream)
-    if pn < need:
-        raise ValueError(f"partial holds {pn} floats, {need} needed")
-    _check("tp_ln_backward", lib().tp_ln_backward(
-        *args, T, h, code, _in(dx, "dx", shape, dt, d), _in(dgamma, "dgamma", (h,), _F32, d),
-        _in(dbeta, "dbeta", (h,), _F32, d), pp, _stream_of(stream, d)))
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty_like(x)
+            dxp = dx.data_ptr()
+        else:
+            dxp = _in(dx, "dx", shape, dt, d)
+        if dgamma is None:
+            dgamma = torch.empty(h, dtype=_F32, device=x.device)
+            dgp = dgamma.data_ptr()
+        else:
+            dgp = _in(dgamma, "dgamma", (h,), _F32, d)
+        if dbeta is None:
+            dbeta = torch.empty_like(dgamma)
+            dbp = dbeta.data_ptr()
+        else:
+            dbp = _in(dbeta, "dbeta", (h,), _F32, d)
+        if partial is None:
+            partial = torch.empty(need or 1, dtype=_F32, device=x.device)
+            pp = partial.data_ptr()
+        else:
+            pp = _in(partial, "partial", partial.shape, _F32, d)
+            if partial.numel() < need:
+                raise ValueError(f"partial holds {partial.numel()} floats, {need} needed")
+    status = lib().tp_ln_backward(dyp, xp, gp, mp, rp, T, h, code, dxp, dgp, dbp, pp,
+                                  _stream_of(stream, d))
+    if status:
+        _check("tp_ln_backward", status)
     return dx, dgamma, dbeta
 
 
@@ -713,18 +743,28 @@ def tp_head_loss_forward(X, W, targets, loss=None, lse=None, workspace=None, str
     targets [T] (int64; negative: the token does not count).  X [T, h], W [V,
     h] bfloat16; the logits are not stored."""
     T, h = X.shape
-    V = W.shape[0]
-    d = torch.cuda.current_device() if X.is_cuda else -1
-    args = (_in(X, "X", (T, h), _BF16, d), _in(W, "W", (V, h), _BF16, d),
-            _in(targets, "targets", (T,), torch.int64, d))
-    dev = X.device
-    loss = _new((T,), _F32, dev, stream) if loss is None else loss
-    lse = _new((T,), _F32, dev, stream) if lse is None else lse
-    need = lib().tp_head_loss_forward_workspace_bytes(T, h, V)
-    wp, wn, workspace = _scratch(workspace, "workspace", need, torch.uint8, dev, d, stream)
-    _check("tp_head_loss_forward", lib().tp_head_loss_forward(
-        *args, T, h, V, _in(loss, "loss", (T,), _F32, d), _in(lse, "lse", (T,), _F32, d), wp, wn,
-        _stream_of(stream, d)))
+    V, d = W.shape[0], _device_of(X)
+    xp, wp = _in(X, "X", (T, h), _BF16, d), _in(W, "W", (V, h), _BF16, d)
+    tp = _in(targets, "targets", (T,), _I64, d)
+    with _on(stream):
+        if loss is None:
+            loss = torch.empty(T, dtype=_F32, device=X.device)
+            lp = loss.data_ptr()
+        else:
+            lp = _in(loss, "loss", (T,), _F32, d)
+        if lse is None:
+            lse = torch.empty_like(loss)
+            sp = lse.data_ptr()
+        else:
+            sp = _in(lse, "lse", (T,), _F32, d)
+        if workspace is None:
+            need = lib().tp_head_loss_forward_workspace_bytes(T, h, V)
+            workspace = torch.empty(need or 1, dtype=_U8, device=X.device)
+    status = lib().tp_head_loss_forward(
+        xp, wp, tp, T, h, V, lp, sp, _in(workspace, "workspace", workspace.shape, _U8, d),
+        workspace.numel(), _stream_of(stream, d))
+    if status:
+        _check("tp_head_loss_forward", status)
     return loss, lse
 
 
@@ -743,19 +783,29 @@ def tp_head_loss_backward(dloss, X, W, targets, lse, dX=None, dW=None, workspace
     """dX [T, h], dW [V, h] (bfloat16) of tp_head_loss_forward given dloss [T]
     (float32) and the forward pass's lse."""
     T, h = X.shape
-    V = W.shape[0]
-    d = torch.cuda.current_device() if X.is_cuda else -1
-    xp = _in(X, "X", (T, h), _BF16, d)
-    args = (_in(dloss, "dloss", (T,), _F32, d), xp, _in(W, "W", (V, h), _BF16, d),
-            _in(targets, "targets", (T,), torch.int64, d), _in(lse, "lse", (T,), _F32, d))
-    dev = X.device
-    dX = _new((T, h), _BF16, dev, stream) if dX is None else dX
-    dW = _new((V, h), _BF16, dev, stream) if dW is None else dW
-    need = lib().tp_head_loss_backward_workspace_bytes(T, h, V) if workspace is None else 0
-    wp, wn, workspace = _scratch(workspace, "workspace", need, torch.uint8, dev, d, stream)
-    _check("tp_head_loss_backward", lib().tp_head_loss_backward(
-        *args, T, h, V, _in(dX, "dX", (T, h), _BF16, d), _in(dW, "dW", (V, h), _BF16, d), wp, wn,
-        _stream_of(stream, d)))
+    V, d = W.shape[0], _device_of(X)
+    xp, wp = _in(X, "X", (T, h), _BF16, d), _in(W, "W", (V, h), _BF16, d)
+    dp, tp = _in(dloss, "dloss", (T,), _F32, d), _in(targets, "targets", (T,), _I64, d)
+    sp = _in(lse, "lse", (T,), _F32, d)
+    with _on(stream):
+        if dX is None:
+            dX = torch.empty_like(X)
+            dXp = dX.data_ptr()
+        else:
+            dXp = _in(dX, "dX", (T, h), _BF16, d)
+        if dW is None:
+            dW = torch.empty_like(W)
+            dWp = dW.data_ptr()
+        else:
+            dWp = _in(dW, "dW", (V, h), _BF16, d)
+        if workspace is None:
+            need = lib().tp_head_loss_backward_workspace_bytes(T, h, V)
+            workspace = torch.empty(need or 1, dtype=_U8, device=X.device)
+    status = lib().tp_head_loss_backward(
+        dp, xp, wp, tp, sp, T, h, V, dXp, dWp, _in(workspace, "workspace", workspace.shape, _U8, d),
+        workspace.numel(), _stream_of(stream, d))
+    if status:
+        _check("tp_head_loss_backward", status)
     return dX, dW
 
 
