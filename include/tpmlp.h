@@ -323,7 +323,7 @@ enum tpmlp_dtype { TPMLP_BF16 = 0, TPMLP_FP16 = 1, TPMLP_FP32 = 2 };
  * In:  x [T,h], gamma, beta [h] of `dtype`, eps > 0.
  * Out: y [T,h] of `dtype`; mean, rstd [T] float32 (rstd = 1/sqrt(var+eps)),
  *      saved for the backward pass.
- * Rules: T >= 0, h >= 1 (any h: rows need not start on 16-byte boundaries;
+ * Rules: 0 <= T <= 2^30, 1 <= h <= 2^30 (any h: rows need not start on 16-byte boundaries;
  * h % 8 == 0, or h % 4 == 0 in float32, is faster), dtype one of the three.
  * Statistics are float32 in every type.  x, gamma, beta and y are 16-byte
  * aligned, mean and rstd 4-byte aligned. */
@@ -365,7 +365,7 @@ int tp_ln_backward(const void* dy, const void* x, const void* gamma, const float
  * (loss 0, no gradient; its lse is still written).  A target >= V has no
  * logit: its loss is NaN, and so are the gradients it reaches.
  * X and W must be finite (a row of X that does not count included).
- * Rules: T >= 0, h >= 8, h % 8 == 0, 1 <= V <= 2^30 (any V).  X, W, dX, dW and
+ * Rules: 0 <= T <= 2^30, h >= 8, h % 8 == 0, 1 <= V <= 2^30 (any V).  X, W, dX, dW and
  * the workspace are 16-byte aligned, targets 8-byte, the rest 4-byte. */
 
 /* Bytes of scratch tp_head_loss_forward needs (the row statistics of each

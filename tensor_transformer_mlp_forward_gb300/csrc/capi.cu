@@ -1658,7 +1658,8 @@ TPMLP_API int tp_ln_residual_backward(const tpmlp_bf16* dX, const tpmlp_bf16* dr
 // ---------------------------------------------- LayerNorm without a residual
 
 static int check_norm(int T, int h, int dtype) {
-    if (T < 0 || h < 1 || dtype < TPMLP_BF16 || dtype > TPMLP_FP32) return TPMLP_ERR_SHAPE;
+    if (T < 0 || T > (1 << 30) || h < 1 || h > (1 << 30) || dtype < TPMLP_BF16 || dtype > TPMLP_FP32)
+        return TPMLP_ERR_SHAPE;
     return TPMLP_OK;
 }
 
@@ -1994,7 +1995,7 @@ namespace tpmlp {
 namespace {
 
 int check_head(int T, int h, int V) {
-    if (T < 0 || h < 8 || h % 8 != 0 || V < 1 || V > (1 << 30)) return TPMLP_ERR_SHAPE;
+    if (T < 0 || T > (1 << 30) || h < 8 || h % 8 != 0 || V < 1 || V > (1 << 30)) return TPMLP_ERR_SHAPE;
     if (cdiv(T, BM) * cdiv(V, BN) >= (1LL << 31)) return TPMLP_ERR_SHAPE;
     return TPMLP_OK;
 }
