@@ -793,6 +793,7 @@ cudaError_t forward_rows(const T* x, const T* gamma, const T* beta, int T_, int 
     // more threads a row, down to 8 values each, fill the SMs instead.
     // (Single values want more registers each than pieces: 16 a thread.)
     int per = VEC == 1 && h <= 16 * 1024 ? 16 : 32;
+    while (per > 8 && h <= 32 * per / 2) per /= 2;  // one warp holds the row with fewer
     while (per > 8 && static_cast<long long>(T_) * ceil_div(h, 32 * per) < 16LL * kSms &&
            ceil_div(h, 32 * per / 2) <= 32)
         per /= 2;
@@ -862,8 +863,9 @@ template <typename T, int VEC, int NV, int NT, int MIN_CTAS>
 cudaError_t backward_ring(const NormPlan& p, const T* dy, const T* x, const T* gamma, const float* mean,
                           const float* rstd, int T_, int h, T* dx, float* pg, float* pb, int* status,
                           cudaStream_t st, int* units) {
-    auto kern = p.cl > 1 ? norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, true>
-                         : norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, false>;
+    auto kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, false>;
+    if constexpr (NV * Piece<T, VEC>::N == 16)
+        if (p.cl > 1) kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.room);
     if (e != cudaSuccess) return e;
     const NormBackwardArgs a{T_, h, p.W, p.stages, p.cl, p.cols, p.buf_bytes, status};
@@ -907,6 +909,9 @@ cudaError_t backward_rows(const NormPlan& p, const T* dy, const T* x, const T* g
                           const float* rstd, int T_, int h, T* dx, float* pg, float* pb, int* status,
                           cudaStream_t st, int* units) {
     constexpr int N = Piece<T, VEC>::N;
+    // rows that a warp holds with 8 values a lane (16384 x 256 bf16: 17.6 -> 14.0 us)
+    if (h <= 256)
+        return backward_ring<T, VEC, 8 / N, 256, 2>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
     if (p.threads == 512)
         return backward_ring<T, VEC, 16 / N, 512, 1>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
     return backward_ring<T, VEC, 16 / N, 256, 2>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);

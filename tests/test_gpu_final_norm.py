@@ -173,3 +173,28 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(other, want))
         assert all(torch.equal(p, q) for p, q in zip(raw, want))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 values: a block of rows repeated, whose repeats must all
+    come out alike; dgamma and dbeta are as many times the block's sums."""
+    rows, h, times = 1000, 16384, 140
+    c = draw(rows, h, torch.bfloat16, 12)
+    g = {k: v.cuda() for k, v in c.items()}
+    x, dy = g["x"].repeat(times, 1), g["dy"].repeat(times, 1)
+    y, mean, rstd = binding.tp_ln_forward(x, g["gamma"], g["beta"], EPS)
+    dx, dgamma, dbeta = binding.tp_ln_backward(dy, x, g["gamma"], mean, rstd)
+    for t in (y, mean, rstd, dx):
+        t = t.view(times, rows, -1)
+        for i in range(1, times):
+            assert torch.equal(t[i], t[0]), i
+    d = {k: ref.f64(v) for k, v in c.items()}
+    by, _, _ = ref.ln_forward_bounds(d["x"], d["gamma"], d["beta"], EPS, torch.bfloat16)
+    ref.within(y[-rows:], ref.ln_forward(d["x"], d["gamma"], d["beta"], EPS)[0], by, "y")
+    m, r = ref.f64(mean[:rows]), ref.f64(rstd[:rows])
+    out = ref.ln_backward(d["dy"], d["x"], d["gamma"], m, r)
+    bx, bg, bb = ref.ln_backward_bounds(d["dy"], d["x"], d["gamma"], m, r, torch.bfloat16)
+    ref.within(dx[-rows:], out[0], bx, "dx")
+    chains = (rows * times + 16) / (rows + 16)  # the sums' chains are longer
+    ref.within(dgamma, times * out[1], times * chains * bg, "dgamma")
+    ref.within(dbeta, times * out[2], times * chains * bb, "dbeta")

@@ -279,3 +279,49 @@ def test_more_tokens_than_one_prepare_pass():
     kernels."""
     c = {k: v.cuda() for k, v in draw(6001, 64, 130, 17).items()}
     check(c, run(c))
+
+
+@pytest.mark.parametrize("T", [5, 20])
+def test_offsets_beyond_32_bits(T):
+    """A vocabulary matrix of more than 2^31 values; the float64 reference runs
+    over pieces of it on the GPU, with plain products."""
+    h, V = 32768, 70001
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = torch.randn(V, h, generator=g, device="cuda", dtype=torch.bfloat16).mul_(0.64 / h ** 0.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    y[0] = V - 1
+    X = torch.randn(T, h, generator=g, device="cuda").to(torch.bfloat16)
+    dloss = torch.rand(T, generator=g, device="cuda") / T
+    loss, lse = binding.tp_head_loss_forward(X, W, y)
+    dX, dW = binding.tp_head_loss_backward(dloss, X, W, y, lse)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    X64, step = X.double(), 10000
+    z, size = [], 0.0
+    for v in range(0, V, step):
+        Wv = W[v:v + step].double()
+        z.append(X64 @ Wv.T)
+        size = max(size, float((X64.abs() @ Wv.abs().T).max()))
+    z = torch.cat(z, 1)
+    want = torch.logsumexp(z, 1)
+    bound = (h / 16 + 4) * 2.0 ** -23 * size + 2.0 ** -20 * float(want.max())
+    assert float((lse.double() - want).abs().max()) <= bound
+    want_loss = want - z[torch.arange(T, device="cuda"), y]
+    assert float((loss.double() - want_loss).abs().max()) <= 2 * bound
+    dz = torch.exp(z - lse.double()[:, None])
+    dz[torch.arange(T, device="cuda"), y] -= 1.0
+    dz *= dloss.double()[:, None]
+    dX64 = torch.zeros_like(X64)
+    off = norm = 0.0
+    for v in range(0, V, step):
+        dX64 += dz[:, v:v + step] @ W[v:v + step].double()
+        dWv = dz[:, v:v + step].T @ X64
+        off += float((dW[v:v + step].double() - dWv).square().sum())
+        norm += float(dWv.square().sum())
+    # two roundings to bf16 (dz and the result), each at most 2^-8 and 2^-8 /
+    # sqrt(3) in the mean of squares: twice their sum's
+    limit = 2 * (2 / 3) ** 0.5 * 2.0 ** -8
+    assert (off / norm) ** 0.5 <= limit
+    assert float((dX.double() - dX64).norm() / dX64.norm()) <= limit
+    tail = dz[:, V - 50:].T @ X64  # the rows farthest out
+    assert float((dW[V - 50:].double() - tail).norm() / tail.norm()) <= limit
