@@ -2064,7 +2064,7 @@ int round_up(long long x, long long m) { return static_cast<int>(cdiv(x, m) * m)
 HeadPlan head_plan_few(int T, int h, int V) {
     HeadPlan p;
     p.width = head_few_ldz(V);
-    p.splits = head_few_planes(h, V);
+    p.splits = head_few_planes(T, h, V);
     p.planes = true;
     p.info = 0;
     p.scale = 0;

@@ -375,22 +375,33 @@ __global__ void __launch_bounds__(32 * kWarps, kGradCtas)
 // The whole backward pass in one reading of W, for rows of up to 1024 values:
 // a CTA takes blocks of 16 vocabulary rows, which the tensor memory
 // accelerator brings to shared memory (boxes of 64 columns, 128-byte swizzle,
-// a ring of kFusedStages blocks).  Warp w owns columns 64 w .. 64 w + 63: its
-// share of the logits' sums, then (dz of the block known) its columns of dX
-// and of the block's dW.  X stays in registers in both operand forms, dX's
-// sums too.  The logits of block i + 1 are begun before block i is finished,
+// a ring of blocks).  A warp owns one or two boxes of every block: its share
+// of the logits' sums, then (dz of the block known) its columns of dX and of
+// the block's dW.  X stays in registers in both operand forms, dX's sums too.
+// The logits of block i + 1 are begun before block i is finished,
 // so that one pair of barriers a block serves both.
 // The warp-level matrix instructions are what bounds this kernel (with 16
 // tokens in their rows: 58 us of which the memory alone needs 22 to read and
 // 14 more to write).  So the tokens are their columns, in TT tiles of eight:
 // up to eight tokens take half the instructions.
-constexpr int kFusedWarps = 16;
-constexpr int kFusedThreads = 32 * kFusedWarps;
-constexpr int kFusedStages = 6;
+constexpr int kFusedColumns = 1024;
 constexpr int kFusedRows = 16;
 constexpr int kBoxBytes = kFusedRows * 128;
-constexpr int kFusedStageBytes = kFusedWarps * kBoxBytes;
-constexpr int kFusedSmem = 1024 + kFusedStages * kFusedStageBytes;
+constexpr int kFusedStageBytes = kFusedColumns / 64 * kBoxBytes;
+
+// Up to eight tokens: two CTAs an SM of eight warps with two boxes each, so
+// that one's barriers overlap the other's arithmetic (7 tokens: 57 us with
+// one CTA of 16 warps, 48 with two).  Up to 16: the registers of two boxes
+// would spill (71 us against 66).
+template <int TT>
+struct Fused {
+    static constexpr int BOXES = TT == 1 ? 2 : 1;  // of a warp
+    static constexpr int WARPS = kFusedColumns / 64 / BOXES;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int CTAS = BOXES;  // an SM
+    static constexpr int STAGES = 6 / CTAS;
+    static constexpr int SMEM = 1024 + STAGES * kFusedStageBytes;
+};
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 u;
@@ -406,20 +417,21 @@ __device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 template <int TT>
-__global__ void __launch_bounds__(kFusedThreads, 1)
+__global__ void __launch_bounds__(Fused<TT>::THREADS, Fused<TT>::CTAS)
     head_few_fused_kernel(const __grid_constant__ CUtensorMap tmW, const FewArgs p,
                           __nv_bfloat16* __restrict__ dW, float* __restrict__ plane, int* status) {
+    constexpr int WARPS = Fused<TT>::WARPS, BOXES = Fused<TT>::BOXES, STAGES = Fused<TT>::STAGES;
     pdl_launch_dependents();  // the next kernel may begin its launch
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kFusedStages];
-    __shared__ float red[kFusedWarps][kFusedRows][8 * TT + 4];
+    __shared__ uint64_t full[STAGES];
+    __shared__ float red[WARPS][kFusedRows][8 * TT + 4];
     __shared__ __align__(16) __nv_bfloat16 dzs[8 * TT][kFusedRows], dzts[kFusedRows][8 * TT];
     __shared__ uint32_t abort_flag;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzle atoms repeat every 1024 bytes
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int boxes = (p.h + 63) / 64;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kFusedStages; ++s) mbar_init(&full[s], 1);
+        for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
         abort_flag = 0u;
         fence_mbar_init();
         prefetch_tmap(&tmW);
@@ -431,35 +443,37 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     const int n = blocks > first ? (blocks - 1 - first) / step + 1 : 0;
     auto issue = [&](int i) {  // thread 0: the CTA's i-th block
         if (i >= n) return;
-        const int s = i % kFusedStages;
+        const int s = i % STAGES;
         mbar_arrive_expect_tx(&full[s], boxes * kBoxBytes);
         for (int b = 0; b < boxes; ++b)
             tma_load_3d(&tmW, smem_u32(&full[s]), ring + s * kFusedStageBytes + b * kBoxBytes, 64 * b, 0,
                         (first + i * step) * kFusedRows);
     };
     if (threadIdx.x == 0)
-        for (int i = 0; i < kFusedStages; ++i) issue(i);
+        for (int i = 0; i < STAGES; ++i) issue(i);
 
     // X as columns (tokens) x k for the logits, as k (tokens) x columns for dW
-    const int col0 = warp * 64;
-    const bool mine = warp < boxes;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 xa[TT][2];
-    uint32_t xb[TT][8];
+    uint4 xa[BOXES][TT][2];
+    uint32_t xb[BOXES][TT][8];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
+    for (int b = 0; b < BOXES; ++b) {
+        const int col0 = (warp + b * WARPS) * 64;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = col0 + k * 32 + q * 8, tok = g + 8 * tt;
-            xa[tt][k] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
+        for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = col0 + k * 32 + q * 8, tok = g + 8 * tt;
+                xa[b][tt][k] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
+            }
+            uint4 r[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = col0 + g * 8, tok = 2 * q + k + 8 * tt;
+                r[k] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
+            }
+            pairs_of(r[0], r[1], xb[b][tt]);
         }
-        uint4 r[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = col0 + g * 8, tok = 2 * q + k + 8 * tt;
-            r[k] = c < p.h && tok < p.T ? __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<long long>(tok) * p.h + c)) : zero;
-        }
-        pairs_of(r[0], r[1], xb[tt]);
     }
     // thread (row of the block, token) of the logits' meeting
     const int vr = threadIdx.x / (8 * TT), t = threadIdx.x % (8 * TT);
@@ -476,30 +490,36 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             weight = y < p.V ? __ldg(p.dloss + t) / s : __int_as_float(0x7FC00000);
         }
     }
-    float acc[TT][4][4];  // [.][m]: columns 8 g + 2 m, + 1 of tokens 2 q, 2 q + 1
+    float acc[BOXES][TT][4][4];  // [.][.][m]: columns 8 g + 2 m, + 1 of tokens 2 q, 2 q + 1
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
+    for (int b = 0; b < BOXES; ++b)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) acc[tt][m][0] = acc[tt][m][1] = acc[tt][m][2] = acc[tt][m][3] = 0.0f;
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                acc[b][tt][m][0] = acc[b][tt][m][1] = acc[b][tt][m][2] = acc[b][tt][m][3] = 0.0f;
 
     // The warp's share of block i's logits, to red.  16-byte piece c of row r
     // sits at position c ^ (r mod 8) of its 128 bytes.
     auto logits = [&](int i) {
-        const int st = i % kFusedStages;
-        warp_wait_polls(&full[st], static_cast<uint32_t>(i / kFusedStages) & 1u, &abort_flag, status);
-        if (!mine) return;
-        const uint32_t box = ring + st * kFusedStageBytes + warp * kBoxBytes + g * 128;
+        const int st = i % STAGES;
+        warp_wait_polls(&full[st], static_cast<uint32_t>(i / STAGES) & 1u, &abort_flag, status);
         float z[TT][4];
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) z[tt][0] = z[tt][1] = z[tt][2] = z[tt][3] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t at = box + (((q + 4 * k) ^ g) << 4);
-            const uint4 lo = ld_shared_v4(at), hi = ld_shared_v4(at + 8 * 128);  // rows g, g + 8
+        for (int b = 0; b < BOXES; ++b) {
+            if (warp + b * WARPS >= boxes) break;
+            const uint32_t box = ring + st * kFusedStageBytes + (warp + b * WARPS) * kBoxBytes + g * 128;
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-                mma16816(z[tt], lo.x, hi.x, lo.y, hi.y, xa[tt][k].x, xa[tt][k].y);
-                mma16816(z[tt], lo.z, hi.z, lo.w, hi.w, xa[tt][k].z, xa[tt][k].w);
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t at = box + (((q + 4 * k) ^ g) << 4);
+                const uint4 lo = ld_shared_v4(at), hi = ld_shared_v4(at + 8 * 128);  // rows g, g + 8
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    mma16816(z[tt], lo.x, hi.x, lo.y, hi.y, xa[b][tt][k].x, xa[b][tt][k].y);
+                    mma16816(z[tt], lo.z, hi.z, lo.w, hi.w, xa[b][tt][k].z, xa[b][tt][k].w);
+                }
             }
         }
 #pragma unroll
@@ -514,7 +534,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         const int v = (first + i * step) * kFusedRows + vr;
         float z = 0.0f;
 #pragma unroll 4
-        for (int w = 0; w < boxes; ++w) z += red[w][vr][t];
+        for (int w = 0; w < min(boxes, WARPS); ++w) z += red[w][vr][t];
         float d = weight * ex2_approx(fmaf(z, kLog2e, -lse2));
         if (v == y) d -= weight;
         if (v >= p.V) d = 0.0f;
@@ -524,51 +544,58 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     };
     // dX's sums and dW of block i.
     auto finish = [&](int i) {
-        if (!mine) return;
-        const uint32_t box = ring + (i % kFusedStages) * kFusedStageBytes + warp * kBoxBytes;
         const int v0 = (first + i * step) * kFusedRows;
-        {
-            uint4 w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 2 * q + (k & 1) + (k >> 1) * 8;
-                w[k] = ld_shared_v4(box + r * 128 + ((g ^ (r & 7)) << 4));
-            }
-            uint32_t lo[8], hi[8];
-            pairs_of(w[0], w[1], lo);
-            pairs_of(w[2], w[3], hi);
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-                const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&dzs[g + 8 * tt][2 * q]);
-                const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&dzs[g + 8 * tt][2 * q + 8]);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    mma16816(acc[tt][m], lo[2 * m], lo[2 * m + 1], hi[2 * m], hi[2 * m + 1], b0, b1);
-            }
-        }
-        uint32_t a[2 * TT];
+        uint32_t a[2 * TT], d[TT][2];
 #pragma unroll
         for (int k = 0; k < 2 * TT; ++k)
             a[k] = *reinterpret_cast<const uint32_t*>(&dzts[g + (k & 1) * 8][2 * q + (k >> 1) * 8]);
-        float o[8][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-            if constexpr (TT == 1)
-                mma1688(o[j], a[0], a[1], xb[0][j]);
-            else
-                mma16816(o[j], a[0], a[1], a[2], a[3], xb[0][j], xb[1][j]);
+        for (int tt = 0; tt < TT; ++tt) {
+            d[tt][0] = *reinterpret_cast<const uint32_t*>(&dzs[g + 8 * tt][2 * q]);
+            d[tt][1] = *reinterpret_cast<const uint32_t*>(&dzs[g + 8 * tt][2 * q + 8]);
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {  // rows g, g + 8
-            const int v = v0 + g + 8 * r;
+        for (int b = 0; b < BOXES; ++b) {
+            if (warp + b * WARPS >= boxes) break;
+            const uint32_t box = ring + (i % STAGES) * kFusedStageBytes + (warp + b * WARPS) * kBoxBytes;
+            const int col0 = (warp + b * WARPS) * 64;
+            {
+                uint4 w[4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // columns 16 q .., 16 q + 8 ..
-                const int c = col0 + 16 * q + 8 * half, e = 2 * r + half;
-                if (v < p.V && c < p.h)
-                    __stcs(reinterpret_cast<uint4*>(dW + static_cast<long long>(v) * p.h + c),
-                           make_uint4(pack_bf16x2(s * o[0][e], s * o[1][e]), pack_bf16x2(s * o[2][e], s * o[3][e]),
-                                      pack_bf16x2(s * o[4][e], s * o[5][e]), pack_bf16x2(s * o[6][e], s * o[7][e])));
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 2 * q + (k & 1) + (k >> 1) * 8;
+                    w[k] = ld_shared_v4(box + r * 128 + ((g ^ (r & 7)) << 4));
+                }
+                uint32_t lo[8], hi[8];
+                pairs_of(w[0], w[1], lo);
+                pairs_of(w[2], w[3], hi);
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        mma16816(acc[b][tt][m], lo[2 * m], lo[2 * m + 1], hi[2 * m], hi[2 * m + 1], d[tt][0], d[tt][1]);
+                }
+            }
+            float o[8][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+                if constexpr (TT == 1)
+                    mma1688(o[j], a[0], a[1], xb[b][0][j]);
+                else
+                    mma16816(o[j], a[0], a[1], a[2], a[3], xb[b][0][j], xb[b][1][j]);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {  // rows g, g + 8
+                const int v = v0 + g + 8 * r;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // columns 16 q .., 16 q + 8 ..
+                    const int c = col0 + 16 * q + 8 * half, e = 2 * r + half;
+                    if (v < p.V && c < p.h)
+                        __stcs(reinterpret_cast<uint4*>(dW + static_cast<long long>(v) * p.h + c),
+                               make_uint4(pack_bf16x2(s * o[0][e], s * o[1][e]), pack_bf16x2(s * o[2][e], s * o[3][e]),
+                                          pack_bf16x2(s * o[4][e], s * o[5][e]), pack_bf16x2(s * o[6][e], s * o[7][e])));
+                }
             }
         }
     };
@@ -583,21 +610,25 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         if (i + 1 < n) logits(i + 1);
         finish(i);
         __syncthreads();  // block i is read, block i + 1's shares are there
-        if (threadIdx.x == 0) issue(i + kFusedStages);
+        if (threadIdx.x == 0) issue(i + STAGES);
         if (i + 1 < n) gradient(i + 1);
         __syncthreads();
     }
-    const int c = col0 + 8 * g;
-    if (!mine || c >= p.h) return;
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
+    for (int b = 0; b < BOXES; ++b) {
+        const int c = (warp + b * WARPS) * 64 + 8 * g;
+        if (c >= p.h) break;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int tok = 2 * q + e + 8 * tt;
-            if (tok < p.T) {
-                float4* d = reinterpret_cast<float4*>(plane + (static_cast<long long>(blockIdx.x) * p.T + tok) * p.h + c);
-                d[0] = make_float4(acc[tt][0][e], acc[tt][0][2 + e], acc[tt][1][e], acc[tt][1][2 + e]);
-                d[1] = make_float4(acc[tt][2][e], acc[tt][2][2 + e], acc[tt][3][e], acc[tt][3][2 + e]);
+        for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int tok = 2 * q + e + 8 * tt;
+                if (tok < p.T) {
+                    const float(&r)[4][4] = acc[b][tt];
+                    float4* o = reinterpret_cast<float4*>(plane + (static_cast<long long>(blockIdx.x) * p.T + tok) * p.h + c);
+                    o[0] = make_float4(r[0][e], r[0][2 + e], r[1][e], r[1][2 + e]);
+                    o[1] = make_float4(r[2][e], r[2][2 + e], r[3][e], r[3][2 + e]);
+                }
             }
         }
     }
@@ -607,9 +638,9 @@ template <int TT>
 cudaError_t launch_fused(const CUtensorMap& tm, const FewArgs& a, int ctas, __nv_bfloat16* dW, float* plane,
                          int* status, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(head_few_fused_kernel<TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kFusedSmem);
+                                         Fused<TT>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(head_few_fused_kernel<TT>, dim3(ctas), dim3(kFusedThreads), kFusedSmem, st, tm, a, dW,
+    return launch_dependent(head_few_fused_kernel<TT>, dim3(ctas), dim3(Fused<TT>::THREADS), Fused<TT>::SMEM, st, tm, a, dW,
                             plane, status);
 }
 
@@ -624,12 +655,12 @@ int head_few_parts(int V) { return std::min(ceil_div(V, kRows), kSms * kCtasPerS
 int head_few_ldz(int V) { return ceil_div(V, kRows) * kRows; }
 
 // Rows of W that a fused block brings (0: h is too wide for the fused form).
-int head_few_box_rows(int h) { return h <= 64 * kFusedWarps ? kFusedRows : 0; }
+int head_few_box_rows(int h) { return h <= kFusedColumns ? kFusedRows : 0; }
 
 // Planes of dX: the fused form's CTAs, or the ranges of vocabulary rows, as many
 // as fill the GPU with CTAs of 256 columns.
-int head_few_planes(int h, int V) {
-    if (head_few_box_rows(h)) return std::min(kSms, ceil_div(V, kFusedRows));
+int head_few_planes(int T, int h, int V) {
+    if (head_few_box_rows(h)) return std::min((T <= 8 ? Fused<1>::CTAS : Fused<2>::CTAS) * kSms, ceil_div(V, kFusedRows));
     const int col_ctas = ceil_div(h, kColumns * kWarps);
     return std::max(1, std::min(kSms * kGradCtas / col_ctas, ceil_div(V, 16)));
 }
@@ -654,14 +685,14 @@ cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X,
     ++*launches;
     cudaError_t e;
     if (head_few_box_rows(h)) {
-        const int ctas = head_few_planes(h, V);
+        const int ctas = head_few_planes(T, h, V);
         return T <= 8 ? launch_fused<1>(*tm, a, ctas, dW, plane, status, st)
                       : launch_fused<2>(*tm, a, ctas, dW, plane, status, st);
     }
     e = launch_dependent(head_few_logits_kernel<true>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0,
                                      st, a);
     if (e != cudaSuccess) return e;
-    const int planes = head_few_planes(h, V);
+    const int planes = head_few_planes(T, h, V);
     const int range_rows = ceil_div(ceil_div(V, planes), 16) * 16;
     ++*launches;
     return launch_dependent(head_few_grad_kernel, dim3(ceil_div(h, kColumns * kWarps), planes), dim3(32 * kWarps), 0,

@@ -99,13 +99,13 @@ cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long
 // The head for few tokens (head_few.cu): head_few(T) says whether T are few.
 // Forward: head_few_parts(V) {max, sum} parts a token.  Backward: dz and dzt
 // (16 head_few_ldz(V) values each), *scale, dW, and dX as
-// head_few_planes(h, V) fp32 planes [T, h] of its sum over the vocabulary;
+// head_few_planes(T, h, V) fp32 planes [T, h] of its sum over the vocabulary;
 // with head_few_box_rows(h) > 0 it needs W's tensor map with boxes of that
 // many rows (else null), and dz and dzt are not used.
 bool head_few(int T);
 int head_few_parts(int V);
 int head_few_ldz(int V);
-int head_few_planes(int h, int V);
+int head_few_planes(int T, int h, int V);
 int head_few_box_rows(int h);
 cudaError_t launch_head_few_lse(const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets,
                                 int T, int h, int V, float2* parts, cudaStream_t st, int* launches);
