@@ -6,13 +6,15 @@
 // tcgen05 tile has 128 rows, so here nearly all of its rows would be padding
 // loaded and multiplied for nothing (one token took 41 us that way).  These
 // kernels stream W through registers into warp-level matrix instructions,
-// whose 16 rows are the tokens: m16n8k16, bf16 in, fp32 sums.
+// m16n8k16, bf16 in, fp32 sums.
 //
 // A matrix instruction sums over k in any order as long as both operands use
 // the same one.  So a lane takes 16 consecutive bytes of a row (8 values) as
 // its share of two k16 steps, for W and for X alike, and nothing is staged
 // in shared memory or transposed: a warp's load of 8 rows fills whole
-// sectors.
+// sectors.  A matrix instruction takes 32 clocks or so of a quarter of an SM
+// whatever it multiplies, so the tokens are its columns, eight at a time, and
+// the vocabulary or the columns of W its 16 rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -72,18 +74,17 @@ struct FewArgs {
 // of exponentials; backward, the logits' gradient.  The loads run one step
 // ahead, across the tasks too: a task has few steps (four a warp at h =
 // 1024), and starting each anew left the memory idle a third of the time.
-template <bool GRAD>
+template <bool GRAD, int TT>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kernel(const FewArgs p) {
     pdl_launch_dependents();  // the next kernel may begin its launch
-    __shared__ __align__(16) float red[2][kWarps][kTokens][kRows + 4];
+    __shared__ __align__(16) float red[2][kWarps][8 * TT][kRows + 4];
     __shared__ __align__(16) __nv_bfloat16 tr[2][kRows][kTokens];
     pdl_wait();  // X comes from the kernel before this one
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int steps = (p.h + kKStep - 1) / kKStep;
-    const bool lo_ok = g < p.T, hi_ok = g + 8 < p.T;
-    const __nv_bfloat16* xlo = p.X + static_cast<long long>(lo_ok ? g : 0) * p.h + q * 8;
-    const __nv_bfloat16* xhi = p.X + static_cast<long long>(hi_ok ? g + 8 : 0) * p.h + q * 8;
-    const bool two = p.T > 8;
+    const __nv_bfloat16* x[TT];
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) x[tt] = p.X + static_cast<long long>(g + 8 * tt < p.T ? g + 8 * tt : 0) * p.h + q * 8;
 
     // this thread's token and rows of a task behind the meeting of the sums
     const int t = threadIdx.x / (kRows / 4), vq = threadIdx.x % (kRows / 4) * 4;
@@ -118,27 +119,30 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
                                  : z;
         }
     };
-    float acc[kTiles][4];
+    float acc[kTiles / 2][TT][4];
     // X's share of the step comes from L1 when it is needed: the registers go
     // to W's loads in flight.
     auto multiply = [&](int step, int b) {
-        uint4 xa[2][2];
+        uint4 xa[TT][2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int k = step * kKStep + s * 32;
-            const bool ok = k + q * 8 < p.h;
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            xa[0][s] = ok && lo_ok ? __ldg(reinterpret_cast<const uint4*>(xlo + k)) : z;
-            xa[1][s] = two && ok && hi_ok ? __ldg(reinterpret_cast<const uint4*>(xhi + k)) : z;
+        for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int k = step * kKStep + s * 32;
+                xa[tt][s] = k + q * 8 < p.h && g + 8 * tt < p.T ? __ldg(reinterpret_cast<const uint4*>(x[tt] + k))
+                                                                 : make_uint4(0u, 0u, 0u, 0u);
+            }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint4 a = xa[0][s], c = xa[1][s];
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                const uint4 u = wb[b][i][s];
-                mma16816(acc[i], a.x, c.x, a.y, c.y, u.x, u.y);
-                mma16816(acc[i], a.z, c.z, a.w, c.w, u.z, u.w);
+            for (int i = 0; i < kTiles / 2; ++i) {
+                const uint4 lo = wb[b][2 * i][s], hi = wb[b][2 * i + 1][s];  // rows g, g + 8 of 16
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    mma16816(acc[i][tt], lo.x, hi.x, lo.y, hi.y, xa[tt][s].x, xa[tt][s].y);
+                    mma16816(acc[i][tt], lo.z, hi.z, lo.w, hi.w, xa[tt][s].z, xa[tt][s].w);
+                }
             }
         }
     };
@@ -157,7 +161,9 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
     if (mine) load_next(0);
     for (int v0 = row0; v0 < p.V; v0 += row_step, parity ^= 1) {
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+        for (int i = 0; i < kTiles / 2; ++i)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) acc[i][tt][0] = acc[i][tt][1] = acc[i][tt][2] = acc[i][tt][3] = 0.0f;
         int left = mine, step = warp;
         // the buffers are named by constants: an odd step first, then pairs
         auto one = [&](int b) {
@@ -187,14 +193,17 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
             }
         }
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            *reinterpret_cast<float2*>(&red[parity][warp][g][i * 8 + 2 * q]) = make_float2(acc[i][0], acc[i][1]);
-            *reinterpret_cast<float2*>(&red[parity][warp][g + 8][i * 8 + 2 * q]) = make_float2(acc[i][2], acc[i][3]);
-        }
+        for (int i = 0; i < kTiles / 2; ++i)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    red[parity][warp][8 * tt + 2 * q + (e & 1)][16 * i + g + 8 * (e >> 1)] = acc[i][tt][e];
         __syncthreads();
         float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
+            if (t >= 8 * TT) break;
             const float4 r = *reinterpret_cast<const float4*>(&red[parity][k][t][vq]);
             z[0] += r.x; z[1] += r.y; z[2] += r.z; z[3] += r.w;
         }
@@ -671,7 +680,8 @@ cudaError_t launch_head_few_lse(const __nv_bfloat16* X, const __nv_bfloat16* W, 
     a.X = X; a.W = W; a.targets = targets; a.T = T; a.h = h; a.V = V;
     a.parts = parts;
     ++*launches;
-    return launch_dependent(head_few_logits_kernel<false>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0, st, a);
+    auto kern = T <= 8 ? head_few_logits_kernel<false, 1> : head_few_logits_kernel<false, 2>;
+    return launch_dependent(kern, dim3(head_few_parts(V)), dim3(32 * kWarps), 0, st, a);
 }
 
 cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X, const __nv_bfloat16* W,
@@ -689,7 +699,8 @@ cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X,
         return T <= 8 ? launch_fused<1>(*tm, a, ctas, dW, plane, status, st)
                       : launch_fused<2>(*tm, a, ctas, dW, plane, status, st);
     }
-    e = launch_dependent(head_few_logits_kernel<true>, dim3(head_few_parts(V)), dim3(32 * kWarps), 0,
+    auto kern = T <= 8 ? head_few_logits_kernel<true, 1> : head_few_logits_kernel<true, 2>;
+    e = launch_dependent(kern, dim3(head_few_parts(V)), dim3(32 * kWarps), 0,
                                      st, a);
     if (e != cudaSuccess) return e;
     const int planes = head_few_planes(T, h, V);
