@@ -27,13 +27,13 @@
 namespace tpmlp {
 namespace {
 
-constexpr int kTokens = 16;   // rows of a matrix instruction
+constexpr int kTokens = 16;   // at most
 constexpr int kWarps = 4;     // of a CTA
 constexpr int kRows = 32;     // vocabulary rows of a task: four n8 tiles
 constexpr int kTiles = kRows / 8;
 constexpr int kKStep = 64;    // columns of a step: 128 bytes of a row
 constexpr int kCtasPerSm = 4;  // of the logits kernel
-constexpr int kGradCtas = 3;   // of the gradient kernel
+constexpr int kGradCtas = 4;   // of the gradient kernel
 constexpr int kSms = 152;
 constexpr int kColumns = 64;  // columns of W that a warp of the gradient kernel owns
 
@@ -44,6 +44,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
 }
 
 // A read that nothing will ask for again soon (W is larger than L1).
@@ -256,11 +263,6 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
     }
 }
 
-// Both gradients are split alike: a warp owns 64 columns and a range of
-// vocabulary rows, 16 of them at a time.  Column n of instruction j is column
-// 8 n + j of the 64, so that a lane loads 8 consecutive columns (its share of
-// eight instructions) and ends with 16 consecutive columns of a result.
-
 // Eight pairs along k from two rows' 8 values.
 __device__ __forceinline__ void pairs_of(const uint4 a, const uint4 b, uint32_t (&o)[8]) {
     const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -271,43 +273,53 @@ __device__ __forceinline__ void pairs_of(const uint4 a, const uint4 b, uint32_t 
     }
 }
 
+// Rows of more than 1024 values: dX and dW from dz, W read a second time.  A
+// warp owns 64 columns and a range of vocabulary rows, 16 of them at a time.
 // dX's sums over the range go to plane[range][T][h]; dW = s dz^T X.  Reading W
-// and writing dW in one kernel is what HBM serves best: a kernel that only
-// wrote dW took 29 us for 103 MB, as long as both together here.  A lane loads
-// 8 columns of rows 2q, 2q + 1, 2q + 8 and 2q + 9 and byte-permutes them into
-// pairs along the rows: no transposition through shared memory.  The warp's
-// 64 columns of X stay in registers.  Three steps' loads of W are in flight;
-// dW leaves in whole 128-byte lines.
+// and writing dW in one kernel is what HBM serves best: it fills at 3.9 TB/s
+// and copies at 6.8 (read and write together), and a kernel that only wrote
+// dW took 29 us for 103 MB.  A lane loads 8 columns of rows 2q, 2q + 1, 2q + 8
+// and 2q + 9 and byte-permutes them into pairs along the rows: no
+// transposition through shared memory.  The warp's 64 columns of X stay in
+// registers.  Column n of dW's instruction j is column 8 n + j of the 64, so
+// that a lane ends with 16 consecutive columns and whole 128-byte lines leave.
+// kDepth steps' loads of W are in flight (one token, 51200 x 20480, both
+// kernels: 1158 us with four CTAs an SM and two steps, 1254 with three and
+// three, 1317 with four and three, which spill).
+template <int TT>
 __global__ void __launch_bounds__(32 * kWarps, kGradCtas)
     head_few_grad_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
                          const __nv_bfloat16* __restrict__ dz, const __nv_bfloat16* __restrict__ dzt,
                          int ldz, const float* __restrict__ scale, int T, int h, int V,
                          int range_rows, __nv_bfloat16* __restrict__ dW, float* __restrict__ plane) {
+    constexpr int kDepth = 2;
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // dz comes from the kernel before this one
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int col0 = (blockIdx.x * kWarps + warp) * kColumns;
     if (col0 >= h) return;
     const int c = min(col0 + g * 8, h - 8);  // columns behind the row are not stored
-    uint32_t xb[2][8];
-    {
-        uint4 r[4];
+    uint32_t xb[TT][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tok = 2 * q + (i & 1) + (i >> 1) * 8;
-            r[i] = tok < T ? __ldg(reinterpret_cast<const uint4*>(X + static_cast<long long>(tok) * h + c))
+    for (int tt = 0; tt < TT; ++tt) {
+        uint4 r[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int tok = 2 * q + k + 8 * tt;
+            r[k] = tok < T ? __ldg(reinterpret_cast<const uint4*>(X + static_cast<long long>(tok) * h + c))
                            : make_uint4(0u, 0u, 0u, 0u);
         }
-        pairs_of(r[0], r[1], xb[0]);
-        pairs_of(r[2], r[3], xb[1]);
+        pairs_of(r[0], r[1], xb[tt]);
     }
     const float s = __ldg(scale);
-    float acc[8][4];
+    float acc[TT][4][4];  // [.][m]: columns 8 g + 2 m, + 1 of tokens 2 q, 2 q + 1
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[tt][m][0] = acc[tt][m][1] = acc[tt][m][2] = acc[tt][m][3] = 0.0f;
     const int r0 = blockIdx.y * range_rows, r1 = min(r0 + range_rows, V);
-    uint4 w[3][4];
-    uint32_t a[2][4], t[2][4];
+    uint4 w[kDepth][4];
+    uint32_t d[2][2 * TT], t[2][2 * TT];
     auto load_w = [&](int vb, int b) {
         if (vb >= r1) return;
 #pragma unroll
@@ -319,63 +331,67 @@ __global__ void __launch_bounds__(32 * kWarps, kGradCtas)
     auto load_dz = [&](int vb, int b) {
         if (vb >= r1) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[b][i] = __ldg(reinterpret_cast<const uint32_t*>(dz + static_cast<long long>(g + (i & 1) * 8) * ldz + vb +
-                                                              2 * q + (i >> 1) * 8));
+        for (int i = 0; i < 2 * TT; ++i) {
+            d[b][i] = __ldg(reinterpret_cast<const uint32_t*>(dz + static_cast<long long>(g + (i >> 1) * 8) * ldz + vb +
+                                                              2 * q + (i & 1) * 8));
             t[b][i] = __ldg(reinterpret_cast<const uint32_t*>(dzt + static_cast<long long>(vb + g + (i & 1) * 8) * kTokens +
                                                               2 * q + (i >> 1) * 8));
         }
     };
 #pragma unroll
-    for (int b = 0; b < 3; ++b) load_w(r0 + 16 * b, b);
+    for (int b = 0; b < kDepth; ++b) load_w(r0 + 16 * b, b);
     load_dz(r0, 0);
-    for (int vb = r0; vb < r1; vb += 96) {
+    for (int vb = r0; vb < r1; vb += 32 * kDepth) {
 #pragma unroll
-        for (int u = 0; u < 6; ++u) {
+        for (int u = 0; u < 2 * kDepth; ++u) {
             const int vr = vb + 16 * u;
             if (vr >= r1) break;
-            constexpr int kDepth = 3;
-            const int b = u % kDepth, d = u & 1;
-            load_dz(vr + 16, d ^ 1);
+            const int b = u % kDepth, e = u & 1;
+            load_dz(vr + 16, e ^ 1);
             {
                 uint32_t lo[8], hi[8];
                 pairs_of(w[b][0], w[b][1], lo);
                 pairs_of(w[b][2], w[b][3], hi);
                 load_w(vr + 16 * kDepth, b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mma16816(acc[j], a[d][0], a[d][1], a[d][2], a[d][3], lo[j], hi[j]);
+                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        mma16816(acc[tt][m], lo[2 * m], lo[2 * m + 1], hi[2 * m], hi[2 * m + 1], d[e][2 * tt], d[e][2 * tt + 1]);
             }
             float o[8][4];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-                mma16816(o[j], t[d][0], t[d][1], t[d][2], t[d][3], xb[0][j], xb[1][j]);
+                if constexpr (TT == 1)
+                    mma1688(o[j], t[e][0], t[e][1], xb[0][j]);
+                else
+                    mma16816(o[j], t[e][0], t[e][1], t[e][2], t[e][3], xb[0][j], xb[1][j]);
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {  // rows g, g + 8
                 const int v = vr + g + 8 * r;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {  // columns 16 q .., 16 q + 8 ..
-                    const int n = col0 + 16 * q + 8 * half, e = 2 * r + half;
+                    const int n = col0 + 16 * q + 8 * half, k = 2 * r + half;
                     if (v < V && n < h)
                         __stcs(reinterpret_cast<uint4*>(dW + static_cast<long long>(v) * h + n),
-                               make_uint4(pack_bf16x2(s * o[0][e], s * o[1][e]), pack_bf16x2(s * o[2][e], s * o[3][e]),
-                                       pack_bf16x2(s * o[4][e], s * o[5][e]), pack_bf16x2(s * o[6][e], s * o[7][e])));
+                               make_uint4(pack_bf16x2(s * o[0][k], s * o[1][k]), pack_bf16x2(s * o[2][k], s * o[3][k]),
+                                          pack_bf16x2(s * o[4][k], s * o[5][k]), pack_bf16x2(s * o[6][k], s * o[7][k])));
                 }
             }
         }
     }
-    float* out = plane + static_cast<long long>(blockIdx.y) * T * h;
+    if (col0 + g * 8 >= h) return;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int tok = g + 8 * r;
+    for (int tt = 0; tt < TT; ++tt) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int n = col0 + 16 * q + 8 * half, e = 2 * r + half;
-            if (tok < T && n < h) {
-                float4* d = reinterpret_cast<float4*>(out + static_cast<long long>(tok) * h + n);
-                d[0] = make_float4(acc[0][e], acc[1][e], acc[2][e], acc[3][e]);
-                d[1] = make_float4(acc[4][e], acc[5][e], acc[6][e], acc[7][e]);
+        for (int e = 0; e < 2; ++e) {
+            const int tok = 2 * q + e + 8 * tt;
+            if (tok < T) {
+                float4* o = reinterpret_cast<float4*>(plane + (static_cast<long long>(blockIdx.y) * T + tok) * h + c);
+                o[0] = make_float4(acc[tt][0][e], acc[tt][0][2 + e], acc[tt][1][e], acc[tt][1][2 + e]);
+                o[1] = make_float4(acc[tt][2][e], acc[tt][2][2 + e], acc[tt][3][e], acc[tt][3][2 + e]);
             }
         }
     }
@@ -416,13 +432,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 u;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr));
     return u;
-}
-
-__device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b0));
 }
 
 template <int TT>
@@ -706,7 +715,8 @@ cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X,
     const int planes = head_few_planes(T, h, V);
     const int range_rows = ceil_div(ceil_div(V, planes), 16) * 16;
     ++*launches;
-    return launch_dependent(head_few_grad_kernel, dim3(ceil_div(h, kColumns * kWarps), planes), dim3(32 * kWarps), 0,
+    auto grad = T <= 8 ? head_few_grad_kernel<1> : head_few_grad_kernel<2>;
+    return launch_dependent(grad, dim3(ceil_div(h, kColumns * kWarps), planes), dim3(32 * kWarps), 0,
                             st, X, W, static_cast<const __nv_bfloat16*>(dz), static_cast<const __nv_bfloat16*>(dzt),
                             a.ldz, static_cast<const float*>(scale), T, h, V, range_rows, dW, plane);
 }
