@@ -2149,11 +2149,12 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
         if (box_rows)
             if (int rc = make_map(&tm, W, V, h, 1, ON_CONTIG, box_rows)) return rc;
         e = launch_head_few_backward(dloss, cb(X), cb(W), targets, lse, T, h, V, z,
-                                     z + 16 * static_cast<size_t>(p.width), scale, plane,
+                                     z + 16 * static_cast<size_t>(p.width), scale, scale + 16, plane,
                                      reinterpret_cast<__nv_bfloat16*>(dW), &tm, d.status, st, &t_last_launches);
         if (e == cudaSuccess)
-            e = launch_head_reduce(plane, p.splits, 1LL * T * h, scale, reinterpret_cast<__nv_bfloat16*>(dX), st,
-                                   &t_last_launches);
+            e = launch_head_few_finish(plane, p.splits, scale, scale + 16, dloss, lse, targets, cb(X), cb(W), T, h, V,
+                                       reinterpret_cast<__nv_bfloat16*>(dX), reinterpret_cast<__nv_bfloat16*>(dW),
+                                       st, &t_last_launches);
         return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
     }
     e = launch_head_prepare(dloss, lse, targets, T, V, info, scale, st, &t_last_launches);

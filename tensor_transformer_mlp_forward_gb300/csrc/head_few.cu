@@ -72,6 +72,7 @@ struct FewArgs {
     __nv_bfloat16 *dz, *dzt;  // [16][ldz] and [ldz][16]
     int ldz;
     float* scale;
+    float* err;  // [16]: what each target's dz lost in its rounding (mended at the end)
 };
 
 // Logits of the 16 tokens against tasks of 32 vocabulary rows, CTA b taking
@@ -236,6 +237,10 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
                 if (v + j >= p.V) z[j] = 0.0f;
             }
             const uint2 d = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+            if (y >= v && y < v + 4) {
+                const float own = y == v ? z[0] : y == v + 1 ? z[1] : y == v + 2 ? z[2] : z[3];
+                p.err[t] = own - __bfloat162float(__float2bfloat16_rn(own));
+            }
             *reinterpret_cast<uint2*>(p.dz + static_cast<long long>(t) * p.ldz + v) = d;
             tr[parity][vq][t] = __ushort_as_bfloat16(static_cast<unsigned short>(d.x));
             tr[parity][vq + 1][t] = __ushort_as_bfloat16(static_cast<unsigned short>(d.x >> 16));
@@ -557,6 +562,7 @@ __global__ void __launch_bounds__(Fused<TT>::THREADS, Fused<TT>::CTAS)
         if (v == y) d -= weight;
         if (v >= p.V) d = 0.0f;
         const __nv_bfloat16 b = __float2bfloat16_rn(d);
+        if (v == y) p.err[t] = d - __bfloat162float(b);
         dzs[t][vr] = b;
         dzts[vr][t] = b;
     };
@@ -695,12 +701,12 @@ cudaError_t launch_head_few_lse(const __nv_bfloat16* X, const __nv_bfloat16* W, 
 
 cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X, const __nv_bfloat16* W,
                                      const long long* targets, const float* lse, int T, int h, int V,
-                                     __nv_bfloat16* dz, __nv_bfloat16* dzt, float* scale, float* plane,
+                                     __nv_bfloat16* dz, __nv_bfloat16* dzt, float* scale, float* err, float* plane,
                                      __nv_bfloat16* dW, const CUtensorMap* tm, int* status, cudaStream_t st,
                                      int* launches) {
     FewArgs a = {};
     a.X = X; a.W = W; a.targets = targets; a.T = T; a.h = h; a.V = V;
-    a.dloss = dloss; a.lse = lse; a.dz = dz; a.dzt = dzt; a.ldz = head_few_ldz(V); a.scale = scale;
+    a.dloss = dloss; a.lse = lse; a.dz = dz; a.dzt = dzt; a.ldz = head_few_ldz(V); a.scale = scale; a.err = err;
     ++*launches;
     cudaError_t e;
     if (head_few_box_rows(h)) {

@@ -178,15 +178,15 @@ __global__ void __launch_bounds__(1024)
 }
 
 // out[i] = bf16(s sum_k P[k][i]): a CTA takes 256 / chains pieces of 8 values,
-// `chains` threads a piece (1, or 16 or 32 for many planes of few values), each
-// adding planes c, c + chains, ... in order; then the chains in order.
-__global__ void __launch_bounds__(256)
-    head_reduce_kernel(const float* __restrict__ P, int planes, long long count, int chains,
-                       const float* __restrict__ scale, __nv_bfloat16* __restrict__ out) {
-    pdl_launch_dependents();  // the next kernel may begin its launch
-    pdl_wait();               // its inputs come from the kernel before it
-    __shared__ float part[256][9];
-    const int pieces = 256 / chains;
+// `chains` threads a piece (1, or 16 or 32 for many planes of few values),
+// each adding planes c, c + chains, ... in order; then the chains in order.
+// `mend` adds what the sum lacks to the 8 values at i.
+template <typename Mend>
+__device__ __forceinline__ void reduce_planes(const float* __restrict__ P, int planes, long long count,
+                                              int chains, float s, __nv_bfloat16* __restrict__ out,
+                                              Mend&& mend) {
+    __shared__ float part[kThreads][9];
+    const int pieces = kThreads / chains;
     const int chain = threadIdx.x / pieces, piece = threadIdx.x % pieces;
     const long long i = (static_cast<long long>(blockIdx.x) * pieces + piece) * 8;
     const bool ok = i < count;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(256)
         }
     }
     if (chain != 0 || !ok) return;
-    const float s = __ldg(scale);
+    mend(i, a);
     uint4 o;
     o.x = pack_bf16x2(s * a[0], s * a[1]);
     o.y = pack_bf16x2(s * a[2], s * a[3]);
@@ -221,6 +221,106 @@ __global__ void __launch_bounds__(256)
     o.w = pack_bf16x2(s * a[6], s * a[7]);
     *reinterpret_cast<uint4*>(out + i) = o;
 }
+
+__global__ void __launch_bounds__(kThreads)
+    head_reduce_kernel(const float* __restrict__ P, int planes, long long count, int chains,
+                       const float* __restrict__ scale, __nv_bfloat16* __restrict__ out) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // its inputs come from the kernel before it
+    reduce_planes(P, planes, count, chains, __ldg(scale), out, [](long long, float(&)[8]) {});
+}
+
+__device__ __forceinline__ void add_scaled8(float (&x)[8], float e, const uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = fmaf(e, __uint_as_float(w[i] << 16), x[2 * i]);
+        x[2 * i + 1] = fmaf(e, __uint_as_float(w[i] & 0xFFFF0000u), x[2 * i + 1]);
+    }
+}
+
+// The end of the few-token backward pass (T <= 16).  A target's dz is most of
+// its token's gradient, and with few tokens its one rounding to bf16 would be
+// most of the error: up to half a step of 2^-8, where many tokens average it
+// out.  So CTAs 0 .. reduce_ctas - 1 sum dX's planes and add err[t] W[y_t], what
+// that rounding lost; and CTA reduce_ctas + k computes dW's row of token k's
+// target once more, from fp32 dz: the T logits of that row are dot products of
+// a few rows.  (Mending both where the target's row passes by made the large
+// kernel a fifth slower.)
+__global__ void __launch_bounds__(kThreads)
+    head_few_finish_kernel(const float* __restrict__ P, int planes, int chains, int reduce_ctas,
+                           const float* __restrict__ scale, const float* __restrict__ err,
+                           const float* __restrict__ dloss, const float* __restrict__ lse,
+                           const long long* __restrict__ targets, const __nv_bfloat16* __restrict__ X,
+                           const __nv_bfloat16* __restrict__ W, int T, int h, int V,
+                           __nv_bfloat16* __restrict__ dX, __nv_bfloat16* __restrict__ dW) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // its inputs come from the kernel before it
+    const float s = __ldg(scale);
+    if (static_cast<int>(blockIdx.x) < reduce_ctas) {
+        reduce_planes(P, planes, static_cast<long long>(T) * h, chains, s, dX, [&](long long i, float(&a)[8]) {
+            const int t = static_cast<int>(i / h);
+            const long long y = __ldg(targets + t);
+            if (y >= 0 && y < V)
+                add_scaled8(a, __ldg(err + t), __ldg(reinterpret_cast<const uint4*>(W + y * h + (i - static_cast<long long>(t) * h))));
+        });
+        return;
+    }
+    __shared__ float sums[kThreads / 32][16];
+    __shared__ float dz[16];
+    const int own = static_cast<int>(blockIdx.x) - reduce_ctas;
+    const long long y = __ldg(targets + own);
+    if (y < 0 || y >= V) return;
+    for (int t = 0; t < own; ++t)
+        if (__ldg(targets + t) == y) return;  // an earlier token's CTA does the row
+    const uint4* w = reinterpret_cast<const uint4*>(W + y * h);
+    const int n = h >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float dot[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) dot[t] = 0.0f;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint4 u = __ldg(w + i);
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+            if (t < T) dot[t] += dot8(__ldg(reinterpret_cast<const uint4*>(X + static_cast<long long>(t) * h) + i), u);
+    }
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) dot[t] += __shfl_xor_sync(0xFFFFFFFFu, dot[t], off);
+        if (lane == 0) sums[warp][t] = dot[t];
+    }
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        const int t = threadIdx.x;
+        float z = 0.0f, d = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) z += sums[k][t];
+        const long long yt = t < T ? __ldg(targets + t) : -1;
+        if (yt >= 0) {
+            const float g = yt < V ? __ldg(dloss + t) / s : __int_as_float(0x7FC00000);
+            d = g * ex2_approx(fmaf(z, kLog2e, -__ldg(lse + t) * kLog2e)) - (yt == y ? g : 0.0f);
+        }
+        dz[t] = d;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        float a[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+            if (t < T) add_scaled8(a, dz[t], __ldg(reinterpret_cast<const uint4*>(X + static_cast<long long>(t) * h) + i));
+        uint4 o;
+        o.x = pack_bf16x2(s * a[0], s * a[1]);
+        o.y = pack_bf16x2(s * a[2], s * a[3]);
+        o.z = pack_bf16x2(s * a[4], s * a[5]);
+        o.w = pack_bf16x2(s * a[6], s * a[7]);
+        reinterpret_cast<uint4*>(dW + y * h)[i] = o;
+    }
+}
+
+int chains_for(int planes) { return planes >= 64 ? 32 : planes >= 8 ? 16 : 1; }
 
 unsigned blocks_of(long long n, long long per) { return static_cast<unsigned>((n + per - 1) / per); }
 
@@ -248,9 +348,20 @@ cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long
 cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,
                                __nv_bfloat16* out, cudaStream_t st, int* launches) {
     ++*launches;
-    const int chains = planes >= 64 ? 32 : planes >= 8 ? 16 : 1;
-    return launch_dependent(head_reduce_kernel, dim3(blocks_of(count / 8, 256 / chains)), dim3(256), 0, st, P,
-                            planes, count, chains, scale, out);
+    const int chains = chains_for(planes);
+    return launch_dependent(head_reduce_kernel, dim3(blocks_of(count / 8, kThreads / chains)), dim3(kThreads), 0, st,
+                            P, planes, count, chains, scale, out);
+}
+
+cudaError_t launch_head_few_finish(const float* P, int planes, const float* scale, const float* err,
+                                   const float* dloss, const float* lse, const long long* targets,
+                                   const __nv_bfloat16* X, const __nv_bfloat16* W, int T, int h, int V,
+                                   __nv_bfloat16* dX, __nv_bfloat16* dW, cudaStream_t st, int* launches) {
+    ++*launches;
+    const int chains = chains_for(planes);
+    const int ctas = static_cast<int>(blocks_of(static_cast<long long>(T) * h / 8, kThreads / chains));
+    return launch_dependent(head_few_finish_kernel, dim3(ctas + T), dim3(kThreads), 0, st, P, planes, chains, ctas,
+                            scale, err, dloss, lse, targets, X, W, T, h, V, dX, dW);
 }
 
 }  // namespace tpmlp

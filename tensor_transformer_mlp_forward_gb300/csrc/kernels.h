@@ -98,7 +98,7 @@ cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long
                                 int* launches);
 // The head for few tokens (head_few.cu): head_few(T) says whether T are few.
 // Forward: head_few_parts(V) {max, sum} parts a token.  Backward: dz and dzt
-// (16 head_few_ldz(V) values each), *scale, dW, and dX as
+// (16 head_few_ldz(V) values each), *scale, err (16 values), dW, and dX as
 // head_few_planes(T, h, V) fp32 planes [T, h] of its sum over the vocabulary;
 // with head_few_box_rows(h) > 0 it needs W's tensor map with boxes of that
 // many rows (else null), and dz and dzt are not used.
@@ -111,9 +111,15 @@ cudaError_t launch_head_few_lse(const __nv_bfloat16* X, const __nv_bfloat16* W, 
                                 int T, int h, int V, float2* parts, cudaStream_t st, int* launches);
 cudaError_t launch_head_few_backward(const float* dloss, const __nv_bfloat16* X, const __nv_bfloat16* W,
                                      const long long* targets, const float* lse, int T, int h, int V,
-                                     __nv_bfloat16* dz, __nv_bfloat16* dzt, float* scale, float* plane,
+                                     __nv_bfloat16* dz, __nv_bfloat16* dzt, float* scale, float* err, float* plane,
                                      __nv_bfloat16* dW, const CUtensorMap* tm, int* status, cudaStream_t st,
                                      int* launches);
+// Then launch_head_few_finish (head_loss.cu): dX from its planes, and dW's rows
+// of the targets, with the rounding of the targets' dz mended.
+cudaError_t launch_head_few_finish(const float* P, int planes, const float* scale, const float* err,
+                                   const float* dloss, const float* lse, const long long* targets,
+                                   const __nv_bfloat16* X, const __nv_bfloat16* W, int T, int h, int V,
+                                   __nv_bfloat16* dX, __nv_bfloat16* dW, cudaStream_t st, int* launches);
 // out[i] = bf16(*scale * sum_s P[s][i]), P: [planes, count], count % 8 == 0.
 cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,
                                __nv_bfloat16* out, cudaStream_t st, int* launches);
