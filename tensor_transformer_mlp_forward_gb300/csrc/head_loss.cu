@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads)
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // the parts come from the kernel before this one
     __shared__ float2 warp_part[kThreads / 32];
-    __shared__ float warp_dot[kThreads / 32];
+    __shared__ double warp_dot[kThreads / 32];
     const int group = kThreads / rows;  // threads a row, 8..256
     const int r = threadIdx.x / group, sub = threadIdx.x % group;
     const int row = blockIdx.x * rows + r;
@@ -95,40 +95,48 @@ __global__ void __launch_bounds__(kThreads)
         if (i >= n_parts) break;
         load_parts(i);
     }
+    // The threads' shares of the dot product meet in double: a float holds a
+    // logit of 20 to 1e-6, which would be the relative error of a small loss.
+    double logit = dot;
     const int width = min(group, 32);
     for (int off = width >> 1; off >= 1; off >>= 1) {
         float2 o;
         o.x = __shfl_xor_sync(0xFFFFFFFFu, acc.x, off);
         o.y = __shfl_xor_sync(0xFFFFFFFFu, acc.y, off);
         acc = join(acc, o);
-        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+        logit += __shfl_xor_sync(0xFFFFFFFFu, logit, off);
     }
     if (group > 32) {
         if ((threadIdx.x & 31) == 0) {
             warp_part[threadIdx.x >> 5] = acc;
-            warp_dot[threadIdx.x >> 5] = dot;
+            warp_dot[threadIdx.x >> 5] = logit;
         }
         __syncthreads();
         if (sub == 0) {
             for (int w = 1; w < group / 32; ++w) {
                 acc = join(acc, warp_part[(threadIdx.x >> 5) + w]);
-                dot += warp_dot[(threadIdx.x >> 5) + w];
+                logit += warp_dot[(threadIdx.x >> 5) + w];
             }
         }
     }
     if (sub != 0 || !ok) return;
-    const float others = acc.x + logf(acc.y);  // y = 0 (V = 1): -inf
+    // log of the others' sum (-inf where there are none, V = 1)
+    const double others = acc.y == 0.0f ? -INFINITY : acc.x + log(static_cast<double>(acc.y));
     if (y < 0) {  // ignored token
         loss[row] = 0.0f;
-        lse[row] = others;
+        lse[row] = static_cast<float>(others);
     } else if (y >= V) {  // no such class: never silent
         loss[row] = __int_as_float(0x7FC00000);
-        lse[row] = others;
+        lse[row] = static_cast<float>(others);
     } else {
-        const float d = (acc.y == 0.0f ? -INFINITY : others) - dot;
-        const float l = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
-        loss[row] = d != d ? d : l;
-        lse[row] = dot + loss[row];
+        const double d = others - logit;
+        const float df = static_cast<float>(d);
+        float e = expf(-fabsf(df));
+        // the part of d that its float leaves out
+        if (fabsf(df) < 100.0f) e = fmaf(e, static_cast<float>(df > 0.0f ? df - d : d - df), e);
+        const float l = fmaxf(df, 0.0f) + log1pf(e);
+        loss[row] = df != df ? df : l;
+        lse[row] = static_cast<float>(logit + loss[row]);
     }
 }
 
