@@ -369,7 +369,7 @@ int tp_ln_backward(const void* dy, const void* x, const void* gamma, const float
  * the workspace are 16-byte aligned, targets 8-byte, the rest 4-byte. */
 
 /* Bytes of scratch tp_head_loss_forward needs (the row statistics of each
- * tile of the vocabulary: at most 16 T max(304, ceil(V/256))). */
+ * tile of the vocabulary: at most 18 T max(304, ceil(V/256))). */
 size_t tp_head_loss_forward_workspace_bytes(int T, int h, int V);
 
 /* In: X [T,h], W [V,h] (bf16), targets [T].  Out: loss, lse [T] (float32).

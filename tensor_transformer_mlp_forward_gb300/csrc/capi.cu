@@ -2000,11 +2000,12 @@ int check_head(int T, int h, int V) {
     return TPMLP_OK;
 }
 
-// Column parts of the forward's row statistics: one for each epilogue half
-// of each 256-column tile at most, or one for each CTA of the few-token form.
+// Column parts of the forward's row statistics (and a byte each for where the
+// max is): one for each epilogue half of each 256-column tile at most, or one
+// for each CTA of the few-token form.
 size_t head_forward_bytes(int T, int V) {
-    const long long parts = head_few(T) ? head_few_parts(V) : 2 * cdiv(V, BN);
-    return sizeof(float2) * static_cast<size_t>(parts) * static_cast<size_t>(T);
+    if (head_few(T)) return sizeof(float2) * static_cast<size_t>(head_few_parts(V)) * static_cast<size_t>(T);
+    return (sizeof(float2) + 1) * static_cast<size_t>(2 * cdiv(V, BN)) * static_cast<size_t>(T);
 }
 
 // Bytes of the logits' gradient kept at a time (a piece of the vocabulary).
@@ -2113,8 +2114,8 @@ int head_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const long long* targ
         float2* parts = static_cast<float2*>(ws);
         e = launch_head_few_lse(cb(X), cb(W), targets, T, h, V, parts, st, &t_last_launches);
         if (e == cudaSuccess)
-            e = launch_head_combine(parts, head_few_parts(V), cb(X), cb(W), targets, T, h, V, loss, lse, st,
-                                    &t_last_launches);
+            e = launch_head_combine(parts, nullptr, head_few_parts(V), 0, cb(X), cb(W), targets, T, h, V, loss, lse,
+                                    st, &t_last_launches);
         return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
     }
     GemmArgs g = blank_args();
@@ -2122,13 +2123,14 @@ int head_forward(const tpmlp_bf16* X, const tpmlp_bf16* W, const long long* targ
     g.targets = targets;
     g.epi_kb = kHeadEpiKb;
     g.lse_part = static_cast<float2*>(ws);
+    g.lse_where = reinterpret_cast<uint8_t*>(g.lse_part + static_cast<size_t>(2 * cdiv(V, BN)) * T);
     Operand a{X, T, h, ON_NONE, false};
     Operand b{W, V, h, ON_NONE, false};
     Output o{const_cast<tpmlp_bf16*>(X), nullptr, T, h, 1};  // a map that nothing is stored through
     if (int rc = run_gemm(launch_head_lse, a, b, o, g, sh, st, d)) return rc;
     const int parts = g.n_tiles * (g.epi_warps / 4);
-    e = launch_head_combine(g.lse_part, parts, cb(X), cb(W), targets, T, h, V, loss, lse,
-                                        st, &t_last_launches);
+    e = launch_head_combine(g.lse_part, g.lse_where, parts, BN / (g.epi_warps / 4), cb(X), cb(W), targets, T, h, V,
+                            loss, lse, st, &t_last_launches);
     return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
 }
 

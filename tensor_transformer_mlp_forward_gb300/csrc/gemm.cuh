@@ -152,6 +152,7 @@ struct GemmArgs {
     int partial_add;
     const long long* targets;  // EPI_LSE: target column of each row (negative: none)
     float2* lse_part;          // EPI_LSE: {max, sum of exponentials}, [tiles * EW / 4][M]
+    uint8_t* lse_where;        // EPI_LSE: which 16 of the part's columns hold the max, likewise
     const float4* row_info;    // EPI_DLOGITS: {lse log2(e), weight, target column (int bits), -}
     int col0;                  // EPI_DLOGITS: vocabulary index of column 0
     int n_valid;               // EPI_DLOGITS: columns from here to N are stored as 0
@@ -763,6 +764,7 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                 // the block's exponentials.  The target's column is left out:
                 // the loss is log(1 + sum_{v != y} exp(z_v - z_y)).
                 float mx = -INFINITY, sum = 0.0f;
+                int where = 0;
 #pragma unroll 1
                 for (int cc = 0; cc < NBLK; ++cc) {
                     const int c = cb0 + cc;
@@ -791,9 +793,15 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                         for (int i = 0; i < 64; ++i)
                             if (i >= valid || i == t) v[i] = -INFINITY;
                     }
-                    float bm = v[0];
+                    float q16[4];
 #pragma unroll
-                    for (int i = 1; i < 64; ++i) bm = fmaxf(bm, v[i]);
+                    for (int k = 0; k < 4; ++k) {
+                        q16[k] = v[16 * k];
+#pragma unroll
+                        for (int i = 1; i < 16; ++i) q16[k] = fmaxf(q16[k], v[16 * k + i]);
+                    }
+                    const float lo = fmaxf(q16[0], q16[1]), hi = fmaxf(q16[2], q16[3]), bm = fmaxf(lo, hi);
+                    if (bm > mx) where = 4 * cc + (hi > lo ? (q16[3] > q16[2] ? 3 : 2) : (q16[1] > q16[0] ? 1 : 0));
                     const float nm = fmaxf(mx, bm);
                     // nothing but excluded columns so far: any finite shift
                     const float shift = nm == -INFINITY ? 0.0f : nm * kLog2e;
@@ -809,6 +817,7 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                 if (row_ok) {
                     const long long part = static_cast<long long>(tc.n0 / G::TILE_N) * (EW / 4) + (warp >> 2);
                     p.lse_part[part * p.M + m] = make_float2(mx, sum);
+                    p.lse_where[part * p.M + m] = static_cast<uint8_t>(where);
                 }
             } else if constexpr (EPI == EPI_PARTIAL) {
                 // fp32 accumulator blocks of 32 rows x 32 columns (128 B rows)

@@ -141,16 +141,22 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
                                                                  : make_uint4(0u, 0u, 0u, 0u);
             }
         }
+        // A step's products are summed by themselves and then added: a matrix
+        // instruction cuts its sum towards zero, which over a long row's hundreds
+        // of steps would shrink every logit by some 2^-18.
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int i = 0; i < kTiles / 2; ++i) {
 #pragma unroll
-            for (int i = 0; i < kTiles / 2; ++i) {
-                const uint4 lo = wb[b][2 * i][s], hi = wb[b][2 * i + 1][s];  // rows g, g + 8 of 16
+            for (int tt = 0; tt < TT; ++tt) {
+                float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) {
-                    mma16816(acc[i][tt], lo.x, hi.x, lo.y, hi.y, xa[tt][s].x, xa[tt][s].y);
-                    mma16816(acc[i][tt], lo.z, hi.z, lo.w, hi.w, xa[tt][s].z, xa[tt][s].w);
+                for (int s = 0; s < 2; ++s) {
+                    const uint4 lo = wb[b][2 * i][s], hi = wb[b][2 * i + 1][s];  // rows g, g + 8 of 16
+                    mma16816(z, lo.x, hi.x, lo.y, hi.y, xa[tt][s].x, xa[tt][s].y);
+                    mma16816(z, lo.z, hi.z, lo.w, hi.w, xa[tt][s].z, xa[tt][s].w);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][tt][e] += z[e];
             }
         }
     };

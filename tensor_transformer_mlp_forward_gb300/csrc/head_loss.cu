@@ -38,19 +38,60 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
     return make_float2(m, a.y * ex2_approx((a.x - shift) * kLog2e) + b.y * ex2_approx((b.x - shift) * kLog2e));
 }
 
+// What the loss and lse of a row come from: {m, s} of the classes beside the
+// target, the target's logit, and what to do with them.
+struct Row {
+    float2 others;
+    double logit;
+    long long y;
+};
+
+__device__ __forceinline__ void finish_row(const Row& r, double log_others, int V, float* loss, float* lse) {
+    if (r.y < 0) {  // ignored token
+        *loss = 0.0f;
+        *lse = static_cast<float>(log_others);
+    } else if (r.y >= V) {  // no such class: never silent
+        *loss = __int_as_float(0x7FC00000);
+        *lse = static_cast<float>(log_others);
+    } else {
+        const double d = log_others - r.logit;
+        const float df = static_cast<float>(d);
+        float e = expf(-fabsf(df));
+        // the part of d that its float leaves out
+        if (fabsf(df) < 100.0f) e = fmaf(e, static_cast<float>(df > 0.0f ? df - d : d - df), e);
+        const float l = df != df ? df : fmaxf(df, 0.0f) + log1pf(e);
+        *loss = l;
+        *lse = static_cast<float>(r.logit + l);
+    }
+}
+
+// log(s) in double for s >= 0: the exponent apart, so that the float logarithm
+// is of a number near 1.
+__device__ __forceinline__ double log_of(float s) {
+    if (!(s > 0.0f && s < INFINITY)) return static_cast<double>(logf(s));
+    const int k = ilogbf(s);
+    return k * 0.69314718055994530942 + static_cast<double>(logf(scalbnf(s, -k)));
+}
+
 // A CTA takes `rows` rows (a power of two up to 32), kThreads / rows threads
 // a row: they join the row's column parts and take the dot product of the
-// target's logit in fp32 (a tensor-core accumulator rounds toward zero at
-// every step, which over a long row would cost a large logit its last bits).
+// target's logit in fp32.  (A tensor-core accumulator is cut toward zero at
+// every step of 16: a logit of 20 from a row of 20480 values comes out 5e-4
+// small.)  Where one other class makes most of a row's sum -- a model sure of
+// the wrong token, or a token that does not count -- its logit is taken again
+// like that: the GEMM says which 16 columns hold it.
 __global__ void __launch_bounds__(kThreads)
-    head_combine_kernel(const float2* __restrict__ parts, int n_parts,
-                        const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
+    head_combine_kernel(const float2* __restrict__ parts, const uint8_t* __restrict__ where, int n_parts,
+                        int part_cols, const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
                         const long long* __restrict__ targets, int T, int h, int V, int rows,
                         float* __restrict__ loss, float* __restrict__ lse) {
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // the parts come from the kernel before this one
     __shared__ float2 warp_part[kThreads / 32];
+    __shared__ int warp_from[kThreads / 32];
     __shared__ double warp_dot[kThreads / 32];
+    __shared__ Row again[32];  // rows whose largest logit is taken again
+    __shared__ int again_col[32];
     const int group = kThreads / rows;  // threads a row, 8..256
     const int r = threadIdx.x / group, sub = threadIdx.x % group;
     const int row = blockIdx.x * rows + r;
@@ -58,6 +99,7 @@ __global__ void __launch_bounds__(kThreads)
     const long long y = ok ? __ldg(targets + row) : -1;
     const float2 none = make_float2(-INFINITY, 0.0f);
     float2 acc = none;
+    int from = 0;  // the part that holds the largest logit
     float dot = 0.0f;
     // The loads come in batches, the first parts' before the dot product, whose
     // addresses wait for the target: one latency after the other was 21 us at
@@ -90,7 +132,10 @@ __global__ void __launch_bounds__(kThreads)
     }
     for (int i = sub;;) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) acc = join(acc, batch[j]);
+        for (int j = 0; j < kBatch; ++j) {
+            if (batch[j].x > acc.x) from = i + j * group;
+            acc = join(acc, batch[j]);
+        }
         i += kBatch * group;
         if (i >= n_parts) break;
         load_parts(i);
@@ -103,40 +148,74 @@ __global__ void __launch_bounds__(kThreads)
         float2 o;
         o.x = __shfl_xor_sync(0xFFFFFFFFu, acc.x, off);
         o.y = __shfl_xor_sync(0xFFFFFFFFu, acc.y, off);
+        const int f = __shfl_xor_sync(0xFFFFFFFFu, from, off);
+        if (o.x > acc.x || (o.x == acc.x && f < from)) from = f;
         acc = join(acc, o);
         logit += __shfl_xor_sync(0xFFFFFFFFu, logit, off);
     }
     if (group > 32) {
         if ((threadIdx.x & 31) == 0) {
             warp_part[threadIdx.x >> 5] = acc;
+            warp_from[threadIdx.x >> 5] = from;
             warp_dot[threadIdx.x >> 5] = logit;
         }
         __syncthreads();
         if (sub == 0) {
             for (int w = 1; w < group / 32; ++w) {
-                acc = join(acc, warp_part[(threadIdx.x >> 5) + w]);
+                const float2 o = warp_part[(threadIdx.x >> 5) + w];
+                if (o.x > acc.x) from = warp_from[(threadIdx.x >> 5) + w];
+                acc = join(acc, o);
                 logit += warp_dot[(threadIdx.x >> 5) + w];
             }
         }
     }
-    if (sub != 0 || !ok) return;
-    // log of the others' sum (-inf where there are none, V = 1)
-    const double others = acc.y == 0.0f ? -INFINITY : acc.x + log(static_cast<double>(acc.y));
-    if (y < 0) {  // ignored token
-        loss[row] = 0.0f;
-        lse[row] = static_cast<float>(others);
-    } else if (y >= V) {  // no such class: never silent
-        loss[row] = __int_as_float(0x7FC00000);
-        lse[row] = static_cast<float>(others);
-    } else {
-        const double d = others - logit;
-        const float df = static_cast<float>(d);
-        float e = expf(-fabsf(df));
-        // the part of d that its float leaves out
-        if (fabsf(df) < 100.0f) e = fmaf(e, static_cast<float>(df > 0.0f ? df - d : d - df), e);
-        const float l = fmaxf(df, 0.0f) + log1pf(e);
-        loss[row] = df != df ? df : l;
-        lse[row] = static_cast<float>(logit + loss[row]);
+    bool redo = false;
+    if (sub == 0 && ok) {
+        const Row mine{acc, logit, y};
+        const double others = acc.x + log_of(acc.y);
+        // The error of the largest logit, about h |m| 2^-30, times its share 1 / s
+        // of the sum: taken again where that is more than 2^-20 of lse.  (Not
+        // where the target outweighs the sum, so that it does not matter.)
+        const bool outweighed = y >= 0 && y < V && logit > others + 20.0;
+        redo = where != nullptr && !outweighed && acc.y < 64.0f &&
+               static_cast<float>(h) * fabsf(acc.x) > 1024.0f * acc.y * fmaxf(1.0f, fabsf(static_cast<float>(others)));
+        if (redo) {
+            again[r] = mine;
+            again_col[r] = from * part_cols + 16 * where[static_cast<long long>(from) * T + row];
+        } else {
+            again_col[r] = -1;
+            finish_row(mine, others, V, loss + row, lse + row);
+        }
+    }
+    if (!__syncthreads_or(redo)) return;
+    __shared__ double z[16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int k = 0; k < rows; ++k) {
+        const int at = blockIdx.x * rows + k;
+        if (at >= T || again_col[k] < 0) continue;  // the same in all threads
+        const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<long long>(at) * h);
+        for (int c = warp; c < 16; c += kThreads / 32) {
+            const int v = again_col[k] + c;
+            const bool in = v < V && v != again[k].y;
+            const uint4* w = reinterpret_cast<const uint4*>(W + static_cast<long long>(in ? v : 0) * h);
+            float d = 0.0f;
+#pragma unroll 4
+            for (int i = lane; i < (h >> 3); i += 32) d += dot8(__ldg(x + i), __ldg(w + i));
+            double sum = d;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+            if (lane == 0) z[c] = in ? sum : -INFINITY;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const Row q = again[k];
+            double best = z[0];
+            for (int c = 1; c < 16; ++c) best = fmax(best, z[c]);
+            // its term of the sum was 2^0
+            const float e = expf(static_cast<float>(best - q.others.x));
+            finish_row(q, q.others.x + log_of(fmaxf(q.others.y - 1.0f, 0.0f) + e), V, loss + at, lse + at);
+        }
+        __syncthreads();
     }
 }
 
@@ -334,15 +413,15 @@ unsigned blocks_of(long long n, long long per) { return static_cast<unsigned>((n
 
 }  // namespace
 
-cudaError_t launch_head_combine(const float2* parts, int n_parts, const __nv_bfloat16* X,
-                                const __nv_bfloat16* W, const long long* targets, int T, int h,
-                                int V, float* loss, float* lse, cudaStream_t st, int* launches) {
+cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n_parts, int part_cols,
+                                const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets, int T,
+                                int h, int V, float* loss, float* lse, cudaStream_t st, int* launches) {
     // as many rows a CTA as leave every SM its eight: few rows get many threads
     int rows = 1;
     while (rows < 32 && T > 8 * 152LL * rows) rows *= 2;
     ++*launches;
     return launch_dependent(head_combine_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, parts,
-                            n_parts, X, W, targets, T, h, V, rows, loss, lse);
+                            where, n_parts, part_cols, X, W, targets, T, h, V, rows, loss, lse);
 }
 
 cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long long* targets,

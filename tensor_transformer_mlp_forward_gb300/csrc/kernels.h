@@ -87,10 +87,11 @@ cudaError_t launch_head_dw(const GemmMaps& m, const GemmArgs& g, int grid, bool 
                            cudaStream_t st);
 
 // The head's row kernels (head_loss.cu).  Forward: the `parts` column parts'
-// {max, sum} of each row and the target's logit -> lse and loss.
-cudaError_t launch_head_combine(const float2* parts, int n_parts, const __nv_bfloat16* X,
-                                const __nv_bfloat16* W, const long long* targets, int T, int h,
-                                int V, float* loss, float* lse, cudaStream_t st, int* launches);
+// {max, sum} of each row and the target's logit -> lse and loss.  `where` (may
+// be null) says which 16 of a part's `part_cols` columns hold its max.
+cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n_parts, int part_cols,
+                                const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets, int T,
+                                int h, int V, float* loss, float* lse, cudaStream_t st, int* launches);
 // Backward: row_info[t] = {lse log2(e), dloss[t] / s, target, 0} and *scale =
 // s, the largest |dloss| of the counted tokens.
 cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long long* targets,

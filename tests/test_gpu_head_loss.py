@@ -325,3 +325,30 @@ def test_offsets_beyond_32_bits(T):
     assert float((dX.double() - dX64).norm() / dX64.norm()) <= limit
     tail = dz[:, V - 50:].T @ X64  # the rows farthest out
     assert float((dW[V - 50:].double() - tail).norm() / tail.norm()) <= limit
+
+
+@pytest.mark.parametrize("T,h", [(40, 20480), (700, 8192), (9, 20480)])
+def test_a_long_row_sure_of_the_wrong_class(T, h):
+    """Rows whose largest logit, about 20 from thousands of products, is not
+    the target's (half of them do not count at all).  A tensor-core sum alone
+    would be some 2^-15 small at h = 20480.  The logit is taken again in fp32:
+    n additions a thread of partial sums below 1, errors of at most 2^-25 each
+    that add in squares (n <= 2560: 1.5e-6), over 8 threads or more 5e-6 of a
+    logit of 20 at the worst and the roundings of lse: 2^-21 of it; the others'
+    sums, smaller than that by their share of the probability, shift by 2^-18
+    of their logits' size (1): together below 2^-19 relative."""
+    V = 1500
+    c = draw(T, h, V, 31, lean=0.0, skip=0.0)
+    g = torch.Generator().manual_seed(4)
+    sure = torch.randint(0, V, (T,), generator=g)
+    Wt = c["W"][sure].float()
+    c["X"] = (c["X"].float() + 20.0 * Wt / (Wt * Wt).sum(-1, keepdim=True)).to(torch.bfloat16)
+    c["y"] = torch.where(torch.arange(T) % 2 == 0, (sure + 1) % V, torch.full_like(sure, -1))
+    d = {k: v.cuda() for k, v in c.items()}
+    loss, lse = binding.tp_head_loss_forward(d["X"], d["W"], d["y"])
+    z = d["X"].double() @ d["W"].double().T
+    want = torch.logsumexp(z, 1)
+    counted = d["y"] >= 0
+    want_loss = torch.where(counted, want - z.gather(1, d["y"].clamp(min=0)[:, None])[:, 0], torch.zeros_like(want))
+    assert float(((lse.double() - want) / want).abs().max()) <= 2.0 ** -19
+    assert float((loss.double() - want_loss).abs().max()) <= 2.0 ** -19 * float(want.max())
