@@ -38,39 +38,53 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
     return make_float2(m, a.y * ex2_approx((a.x - shift) * kLog2e) + b.y * ex2_approx((b.x - shift) * kLog2e));
 }
 
+// A number as the sum of two floats, the second below half a step of the
+// first: twice a float's precision for the few values that need it (double
+// precision instructions are rare and slow on this part).
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t)), __fadd_rn(a.lo, b.lo));
+    const float hi = __fadd_rn(s, e);
+    return Two{hi, __fsub_rn(e, __fsub_rn(hi, s))};
+}
+
+// m + log(s), s >= 0: the exponent of s apart, so that the float logarithm is of
+// a number near 1.  ln 2 is cut to 12 bits and a rest: k times the former is
+// exact.
+__device__ __forceinline__ Two log_sum(float m, float s) {
+    if (!(s > 0.0f && s < INFINITY)) return Two{m + logf(s), 0.0f};
+    const int k = ((__float_as_int(s) >> 23) & 0xFF) - 127;  // s is a sum of powers of two near 1: normal
+    const float f = __int_as_float(__float_as_int(s) - (k << 23));
+    constexpr float kLn2Hi = 0.693115234375f, kLn2Lo = 3.194618498e-05f;
+    return add(add(Two{m, 0.0f}, Two{k * kLn2Hi, 0.0f}), Two{fmaf(static_cast<float>(k), kLn2Lo, logf(f)), 0.0f});
+}
+
 // What the loss and lse of a row come from: {m, s} of the classes beside the
 // target, the target's logit, and what to do with them.
 struct Row {
     float2 others;
-    double logit;
-    long long y;
+    Two logit;
+    int y;  // the target, V for one outside the vocabulary
 };
 
-__device__ __forceinline__ void finish_row(const Row& r, double log_others, int V, float* loss, float* lse) {
+__device__ __forceinline__ void finish_row(const Row& r, Two log_others, int V, float* loss, float* lse) {
     if (r.y < 0) {  // ignored token
         *loss = 0.0f;
-        *lse = static_cast<float>(log_others);
+        *lse = log_others.hi;
     } else if (r.y >= V) {  // no such class: never silent
         *loss = __int_as_float(0x7FC00000);
-        *lse = static_cast<float>(log_others);
+        *lse = log_others.hi;
     } else {
-        const double d = log_others - r.logit;
-        const float df = static_cast<float>(d);
-        float e = expf(-fabsf(df));
-        // the part of d that its float leaves out
-        if (fabsf(df) < 100.0f) e = fmaf(e, static_cast<float>(df > 0.0f ? df - d : d - df), e);
-        const float l = df != df ? df : fmaxf(df, 0.0f) + log1pf(e);
+        const Two d = log_others.hi == -INFINITY ? log_others : add(log_others, Two{-r.logit.hi, -r.logit.lo});
+        float e = expf(-fabsf(d.hi));
+        if (fabsf(d.hi) < 100.0f) e = fmaf(e, d.hi > 0.0f ? -d.lo : d.lo, e);
+        const float l = d.hi != d.hi ? d.hi : fmaxf(d.hi, 0.0f) + log1pf(e);
         *loss = l;
-        *lse = static_cast<float>(r.logit + l);
+        *lse = r.logit.hi + (r.logit.lo + l);
     }
-}
-
-// log(s) in double for s >= 0: the exponent apart, so that the float logarithm
-// is of a number near 1.
-__device__ __forceinline__ double log_of(float s) {
-    if (!(s > 0.0f && s < INFINITY)) return static_cast<double>(logf(s));
-    const int k = ilogbf(s);
-    return k * 0.69314718055994530942 + static_cast<double>(logf(scalbnf(s, -k)));
 }
 
 // A CTA takes `rows` rows (a power of two up to 32), kThreads / rows threads
@@ -89,7 +103,7 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();               // the parts come from the kernel before this one
     __shared__ float2 warp_part[kThreads / 32];
     __shared__ int warp_from[kThreads / 32];
-    __shared__ double warp_dot[kThreads / 32];
+    __shared__ Two warp_dot[kThreads / 32];
     __shared__ Row again[32];  // rows whose largest logit is taken again
     __shared__ int again_col[32];
     const int group = kThreads / rows;  // threads a row, 8..256
@@ -140,9 +154,9 @@ __global__ void __launch_bounds__(kThreads)
         if (i >= n_parts) break;
         load_parts(i);
     }
-    // The threads' shares of the dot product meet in double: a float holds a
+    // The threads' shares of the dot product meet as two floats: one holds a
     // logit of 20 to 1e-6, which would be the relative error of a small loss.
-    double logit = dot;
+    Two logit{dot, 0.0f};
     const int width = min(group, 32);
     for (int off = width >> 1; off >= 1; off >>= 1) {
         float2 o;
@@ -151,7 +165,10 @@ __global__ void __launch_bounds__(kThreads)
         const int f = __shfl_xor_sync(0xFFFFFFFFu, from, off);
         if (o.x > acc.x || (o.x == acc.x && f < from)) from = f;
         acc = join(acc, o);
-        logit += __shfl_xor_sync(0xFFFFFFFFu, logit, off);
+        Two l;
+        l.hi = __shfl_xor_sync(0xFFFFFFFFu, logit.hi, off);
+        l.lo = __shfl_xor_sync(0xFFFFFFFFu, logit.lo, off);
+        logit = add(logit, l);
     }
     if (group > 32) {
         if ((threadIdx.x & 31) == 0) {
@@ -165,20 +182,20 @@ __global__ void __launch_bounds__(kThreads)
                 const float2 o = warp_part[(threadIdx.x >> 5) + w];
                 if (o.x > acc.x) from = warp_from[(threadIdx.x >> 5) + w];
                 acc = join(acc, o);
-                logit += warp_dot[(threadIdx.x >> 5) + w];
+                logit = add(logit, warp_dot[(threadIdx.x >> 5) + w]);
             }
         }
     }
     bool redo = false;
     if (sub == 0 && ok) {
-        const Row mine{acc, logit, y};
-        const double others = acc.x + log_of(acc.y);
+        const Row mine{acc, logit, y < 0 ? -1 : static_cast<int>(min(y, static_cast<long long>(V)))};
+        const Two others = log_sum(acc.x, acc.y);
         // The error of the largest logit, about h |m| 2^-30, times its share 1 / s
         // of the sum: taken again where that is more than 2^-20 of lse.  (Not
         // where the target outweighs the sum, so that it does not matter.)
-        const bool outweighed = y >= 0 && y < V && logit > others + 20.0;
+        const bool outweighed = y >= 0 && y < V && logit.hi > others.hi + 20.0f;
         redo = where != nullptr && !outweighed && acc.y < 64.0f &&
-               static_cast<float>(h) * fabsf(acc.x) > 1024.0f * acc.y * fmaxf(1.0f, fabsf(static_cast<float>(others)));
+               static_cast<float>(h) * fabsf(acc.x) > 1024.0f * acc.y * fmaxf(1.0f, fabsf(others.hi));
         if (redo) {
             again[r] = mine;
             again_col[r] = from * part_cols + 16 * where[static_cast<long long>(from) * T + row];
@@ -188,7 +205,7 @@ __global__ void __launch_bounds__(kThreads)
         }
     }
     if (!__syncthreads_or(redo)) return;
-    __shared__ double z[16];
+    __shared__ Two z[16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int k = 0; k < rows; ++k) {
         const int at = blockIdx.x * rows + k;
@@ -201,19 +218,25 @@ __global__ void __launch_bounds__(kThreads)
             float d = 0.0f;
 #pragma unroll 4
             for (int i = lane; i < (h >> 3); i += 32) d += dot8(__ldg(x + i), __ldg(w + i));
-            double sum = d;
+            Two sum{d, 0.0f};
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-            if (lane == 0) z[c] = in ? sum : -INFINITY;
+            for (int off = 16; off >= 1; off >>= 1) {
+                Two o;
+                o.hi = __shfl_xor_sync(0xFFFFFFFFu, sum.hi, off);
+                o.lo = __shfl_xor_sync(0xFFFFFFFFu, sum.lo, off);
+                sum = add(sum, o);
+            }
+            if (lane == 0) z[c] = in ? sum : Two{-INFINITY, 0.0f};
         }
         __syncthreads();
         if (threadIdx.x == 0) {
             const Row q = again[k];
-            double best = z[0];
-            for (int c = 1; c < 16; ++c) best = fmax(best, z[c]);
-            // its term of the sum was 2^0
-            const float e = expf(static_cast<float>(best - q.others.x));
-            finish_row(q, q.others.x + log_of(fmaxf(q.others.y - 1.0f, 0.0f) + e), V, loss + at, lse + at);
+            Two best = z[0];
+            for (int c = 1; c < 16; ++c)
+                if (z[c].hi > best.hi) best = z[c];
+            // its term of the sum was 1
+            const float e = expf((best.hi - q.others.x) + best.lo);
+            finish_row(q, log_sum(q.others.x, fmaxf(q.others.y - 1.0f, 0.0f) + e), V, loss + at, lse + at);
         }
         __syncthreads();
     }
