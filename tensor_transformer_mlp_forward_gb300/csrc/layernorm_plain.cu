@@ -38,6 +38,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 
 constexpr int kNormMaxStages = 6;
 constexpr int kNormMaxCluster = 8;
+constexpr int kNormMaxPerSm = 4;  // CTAs of the backward kernel
 // Rows that a thread of the backward kernel takes together, and the blocks
 // that it begins before the one that it finishes.  The ring needs twice as
 // many stages as the latter.
@@ -202,18 +203,18 @@ __device__ __forceinline__ float2 warp_sum(float2 x) {
     return x;
 }
 
-// Sum over the W warps of a row's group (W a power of two; warps W g .. W g +
-// W - 1 of the CTA); every thread receives the total, added in the same
-// order in every thread.  `scratch` holds one entry a warp.  All threads of
+// Sum over the W warps of a row's group (`first` and the W - 1 behind it);
+// every thread receives the total, added in the same order in every thread.  `scratch` holds one entry a warp.  All threads of
 // the CTA call it.
-__device__ __forceinline__ float2 group_sum(float2 x, int W, float2* scratch) {
+__device__ __forceinline__ float2 group_sum(float2 x, int W, int first, float2* scratch) {
     x = warp_sum(x);
     if (W == 1) return x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) scratch[warp] = x;
     __syncthreads();
-    x = scratch[(warp & ~(W - 1)) + (lane & (W - 1))];
-    for (int off = W >> 1; off >= 1; off >>= 1) {
+    const int lanes = 1 << (32 - __clz(W - 1)), i = lane & (lanes - 1);  // W up to a power of two
+    x = i < W ? scratch[first + i] : both(0.0f);
+    for (int off = lanes >> 1; off >= 1; off >>= 1) {
         x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, off);
         x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, off);
     }
@@ -232,8 +233,8 @@ __global__ void __launch_bounds__(1024)
     pdl_wait();               // its inputs may come from the kernel before it
     __shared__ float2 scratch[2][32];
     const int group = 32 * W;  // threads a row
-    const int sub = threadIdx.x % group;
-    const int row = blockIdx.x * (blockDim.x / group) + threadIdx.x / group;
+    const int g = threadIdx.x / group, sub = threadIdx.x - g * group, first = g * W;
+    const int row = blockIdx.x * (blockDim.x / group) + g;
     const bool ok = row < rows;
     const long long base = static_cast<long long>(row) * h;
     constexpr int PAIRS = Piece<T, VEC>::N / 2;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(1024)
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) acc = add2(acc, pair_of(in[k], i));
-    const float mu = group_sum(make_float2(acc.x + acc.y, 0.0f), W, scratch[0]).x / static_cast<float>(h);
+    const float mu = group_sum(make_float2(acc.x + acc.y, 0.0f), W, first, scratch[0]).x / static_cast<float>(h);
     acc = both(0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(1024)
             acc = fma2(c, c, acc);
         }
     }
-    const float var = group_sum(make_float2(acc.x + acc.y, 0.0f), W, scratch[1]).x / static_cast<float>(h);
+    const float var = group_sum(make_float2(acc.x + acc.y, 0.0f), W, first, scratch[1]).x / static_cast<float>(h);
     const float rs = 1.0f / sqrtf(var + eps);
     if (!ok) return;
 #pragma unroll
@@ -318,7 +319,8 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     __shared__ uint32_t abort_flag;
     pdl_launch_dependents();  // the next kernel may begin its launch
     constexpr long long E = sizeof(T);
-    const int group = CLUSTER ? NT : 32 * p.W, R = NT / group;
+    const int warps = blockDim.x >> 5;  // NT / 32 at most
+    const int group = 32 * p.W, R = warps / p.W;
     const int g = CLUSTER ? 0 : threadIdx.x / group, sub = threadIdx.x - g * group;
     const int cl = CLUSTER ? p.cl : 1;
     const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
         // a cluster counts the bytes that its warps send, one CTA its warps
-        for (int s = 0; s < SLOTS; ++s) mbar_init(&sums[s], CLUSTER ? 1 : NT / 32);
+        for (int s = 0; s < SLOTS; ++s) mbar_init(&sums[s], CLUSTER ? 1 : warps);
         abort_flag = 0u;
         fence_mbar_init();
     }
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
             }
         }
         uint64_t* bar = &sums[b_slot];
-        float2* slot = slots[b_slot][rank * (NT / 32) + warp];
+        float2* slot = slots[b_slot][rank * warps + warp];
 #pragma unroll
         for (int u = 0; u < U; ++u) m[u] = warp_sum(make_float2(m[u].x + m[u].y, mx[u].x + mx[u].y));
         if constexpr (!CLUSTER) {
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
                 mbar_arrive(bar);  // releases the slot to the waiting warps
             }
         } else {
-            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * (NT / 32) * U * sizeof(float2));
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * warps * U * sizeof(float2));
             if (lane < cl) {
                 const uint32_t peer = map_to_cta(smem_u32(slot), lane), peer_bar = map_to_cta(smem_u32(bar), lane);
 #pragma unroll
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         for (int u = 0; u < U; ++u) {
             m[u] = both(0.0f);
             if constexpr (CLUSTER) {
-                for (int j = lane; j < cl * (NT / 32); j += 32) m[u] = add2(m[u], slots[slot][j][u]);
+                for (int j = lane; j < cl * warps; j += 32) m[u] = add2(m[u], slots[slot][j][u]);
                 m[u] = warp_sum(m[u]);
             } else {
 #pragma unroll 4
@@ -780,7 +782,7 @@ int ceil_pow2(int x) {
 template <typename T, int VEC, int NV>
 cudaError_t forward_reg(const T* x, const T* gamma, const T* beta, int T_, int h, int W, float eps, T* y,
                         float* mean, float* rstd, cudaStream_t st) {
-    const int threads = std::max(256, 32 * W), rows = threads / (32 * W);
+    const int rows = std::max(1, 8 / W), threads = rows * 32 * W;
     return launch_dependent(norm_forward_reg_kernel<T, VEC, NV>, dim3(ceil_div(T_, rows)), dim3(threads), 0,
                             st, x, gamma, beta, T_, h, W, eps, y, mean, rstd);
 }
@@ -800,8 +802,8 @@ cudaError_t forward_rows(const T* x, const T* gamma, const T* beta, int T_, int 
     // rows beyond 16 warps of that: 40 values a thread, so that two rows (two
     // CTAs of 512 threads) share an SM and one's sums overlap the other's loads
     if (per == 32 && h > 16 * 1024 && h <= 20 * 1024)
-        return forward_reg<T, VEC, 40 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, 16, eps, y, mean, rstd, st);
-    const int W = ceil_pow2(ceil_div(h, 32 * per));
+        return forward_reg<T, VEC, 40 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, ceil_div(h, 32 * 40), eps, y, mean, rstd, st);
+    const int W = ceil_div(h, 32 * per);
     if (per == 32) return forward_reg<T, VEC, 32 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
     if (per == 16) return forward_reg<T, VEC, 16 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
     return forward_reg<T, VEC, 8 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
@@ -835,18 +837,34 @@ constexpr int kSmemMost = 227 * 1024;
 
 NormPlan norm_plan(int T, int h, int elem) {
     NormPlan p{};
-    // 256 threads: two CTAs an SM (128 registers a thread).  Rows beyond eight
-    // such CTAs take eight of 512.
-    p.threads = h <= kNormMaxCluster * 16 * 256 ? 256 : 512;
-    p.cl = ceil_div(h, 16 * p.threads);
-    if (p.cl > kNormMaxCluster) return NormPlan{};
-    p.cols = p.cl == 1 ? h : ceil_div(ceil_div(h, p.cl), 8) * 8;
-    p.W = p.cl > 1 ? p.threads / 32 : ceil_pow2(ceil_div(h, 32 * 16));
-    const int R = p.threads / (32 * p.W), U = elem == 2 && h % 8 == 0 ? norm_rows<8>() : norm_rows<1>();
+    // 16 values a thread (128 registers): 16 warps an SM.  Rows beyond 8 warps
+    // take a cluster, of an even number of CTAs: SMs come in pairs, and an odd
+    // number leaves places empty (2048 x 20480 bf16: 73 us with five).  Of
+    // those the number whose CTAs fill the SMs' warps best (63 us with six of
+    // seven warps, two an SM; 60 with eight of five, three an SM), the smaller
+    // where the difference is small.
+    // Rows beyond eight CTAs of 8 warps take eight of up to 16.
+    const int warps = h <= kNormMaxCluster * 16 * 256 ? 8 : 16;
+    int most = 0;
+    for (int cl = 1; cl <= kNormMaxCluster; cl += cl == 1 ? 1 : 2) {
+        const int cols = cl == 1 ? h : ceil_div(ceil_div(h, cl), 8) * 8, W = ceil_div(cols, 32 * 16);
+        if (W > warps) continue;
+        const int live = std::min(kNormMaxPerSm, 16 / W) * cols;  // columns at work on an SM
+        if (live <= most + most / 16) continue;
+        most = live;
+        p.cl = cl;
+        p.cols = cols;
+        p.W = W;
+        if (cl == 1) break;
+    }
+    if (p.cl == 0) return NormPlan{};
+    if (p.W < 4 && p.cl == 1) p.W = ceil_pow2(p.W);  // groups that fill 8 warps
+    const int R = p.cl == 1 ? std::max(1, 8 / p.W) : 1, U = elem == 2 && h % 8 == 0 ? norm_rows<8>() : norm_rows<1>();
+    p.threads = 32 * R * p.W;
     // a block of rows and what its first and last granule hold besides
     p.buf_bytes = (static_cast<int>((static_cast<long long>(R) * U * p.cols * elem + 15) / 16) + 1) * 16;
-    const int per_sm = p.threads == 512 ? 1 : 2;
-    p.room = kSmemMost / per_sm - (per_sm == 1 ? 5120 : 3072);  // beside the static arrays
+    const int per_sm = std::min(kNormMaxPerSm, 16 / (R * p.W));
+    p.room = kSmemMost / per_sm - (per_sm == 1 ? 5 : 4) * 1024;  // beside the static arrays
     const int blocks = ceil_div(T, R * U), units = kSms * per_sm / p.cl;
     p.stages = std::min(kNormMaxStages, p.room / (2 * p.buf_bytes));
     // the meeting place of the groups' sums: 16 values a thread and tensor
@@ -871,11 +889,11 @@ cudaError_t backward_ring(const NormPlan& p, const T* dy, const T* x, const T* g
     const NormBackwardArgs a{T_, h, p.W, p.stages, p.cl, p.cols, p.buf_bytes, status};
     if (p.cl == 1) {
         *units = p.units;
-        return launch_dependent(kern, dim3(p.units), dim3(NT), p.smem, st, dy, x, gamma, mean, rstd, a, dx, pg,
+        return launch_dependent(kern, dim3(p.units), dim3(p.threads), p.smem, st, dy, x, gamma, mean, rstd, a, dx, pg,
                                 pb);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(NT);
+    cfg.blockDim = dim3(p.threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -886,15 +904,15 @@ cudaError_t backward_ring(const NormPlan& p, const T* dy, const T* x, const T* g
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     // clusters of this size that fit with the most shared memory a plan takes
-    static std::atomic<int> fit[kNormMaxCluster + 1];  // the same for every device of this build's target
-    int n = fit[p.cl].load(std::memory_order_relaxed);
+    static std::atomic<int> fit[kNormMaxCluster + 1][NT / 32 + 1];  // the same for every device of this build's target
+    int n = fit[p.cl][p.W].load(std::memory_order_relaxed);
     if (n == 0) {
         cfg.gridDim = dim3(p.cl);
         cfg.dynamicSmemBytes = p.room;
         cfg.numAttrs = 1;
         if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
         n = std::max(n, 1);
-        fit[p.cl].store(n, std::memory_order_relaxed);
+        fit[p.cl][p.W].store(n, std::memory_order_relaxed);
     }
     *units = std::min(p.units, n);
     cfg.gridDim = dim3(*units * p.cl);
@@ -912,7 +930,7 @@ cudaError_t backward_rows(const NormPlan& p, const T* dy, const T* x, const T* g
     // rows that a warp holds with 8 values a lane (16384 x 256 bf16: 17.6 -> 14.0 us)
     if (h <= 256)
         return backward_ring<T, VEC, 8 / N, 256, 2>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
-    if (p.threads == 512)
+    if (p.threads > 256)
         return backward_ring<T, VEC, 16 / N, 512, 1>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
     return backward_ring<T, VEC, 16 / N, 256, 2>(p, dy, x, gamma, mean, rstd, T_, h, dx, pg, pb, status, st, units);
 }
