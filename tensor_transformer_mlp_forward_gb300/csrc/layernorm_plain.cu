@@ -288,6 +288,10 @@ __global__ void __launch_bounds__(1024)
 // order, and the sums go to part[0 / 1][CTA or cluster][column].
 // Rows wider than a CTA's registers are cut over the `cl` CTAs of a cluster
 // (one row at a time, `cols` columns each).
+// Measured in bf16: 8192 x 1024 in 18.9 us with the sum of the parts (2.7 TB/s;
+// start, end and the sum's launch are half of it), 40960 x 1024 in 47 us (5.4
+// TB/s), 8192 x 8192 in 75 us (5.3 TB/s), 2048 x 20480 in 60 us (4.2 TB/s);
+// the longest are bound by HBM reading and writing at once.
 // There is no barrier in the loop.  A warp begins block i + AHEAD (its part of
 // the row sums, which go to the shared memory of every CTA of the row and are
 // counted on an mbarrier there) before it finishes block i
@@ -787,7 +791,9 @@ cudaError_t forward_reg(const T* x, const T* gamma, const T* beta, int T_, int h
                             st, x, gamma, beta, T_, h, W, eps, y, mean, rstd);
 }
 
-// W warps a row, 32 values a thread at most.
+// W warps a row.  Measured in bf16: 8192 x 1024 in 7.9 us (4.3 TB/s: launch
+// and first loads are a quarter of it), 8192 x 8192 in 50 us (5.4 TB/s), 2048 x
+// 20480 in 37 us (4.5 TB/s), 1280 x 32768 in 40 us.
 template <typename T, int VEC>
 cudaError_t forward_rows(const T* x, const T* gamma, const T* beta, int T_, int h, float eps, T* y,
                          float* mean, float* rstd, cudaStream_t st) {
@@ -803,6 +809,15 @@ cudaError_t forward_rows(const T* x, const T* gamma, const T* beta, int T_, int 
     // CTAs of 512 threads) share an SM and one's sums overlap the other's loads
     if (per == 32 && h > 16 * 1024 && h <= 20 * 1024)
         return forward_reg<T, VEC, 40 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, ceil_div(h, 32 * 40), eps, y, mean, rstd, st);
+    // the same with 48 and 64 values where a register holds two (1706 x 24576
+    // bf16: 36 us, with 32 values 48; 1024 x 40960: 48 us, row read again from
+    // memory 78)
+    if constexpr (VEC == 8) {
+        if (h > 20 * 1024 && h <= 24 * 1024)
+            return forward_reg<T, VEC, 6>(x, gamma, beta, T_, h, ceil_div(h, 32 * 48), eps, y, mean, rstd, st);
+        if (h > 24 * 1024)
+            return forward_reg<T, VEC, 8>(x, gamma, beta, T_, h, ceil_div(h, 32 * 64), eps, y, mean, rstd, st);
+    }
     const int W = ceil_div(h, 32 * per);
     if (per == 32) return forward_reg<T, VEC, 32 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
     if (per == 16) return forward_reg<T, VEC, 16 / Piece<T, VEC>::N>(x, gamma, beta, T_, h, W, eps, y, mean, rstd, st);
@@ -817,7 +832,7 @@ cudaError_t forward(const void* x_, const void* gamma_, const void* beta_, int T
     T* y = static_cast<T*>(y_);
     ++*launches;
     constexpr int VEC = 16 / sizeof(T);
-    if (h <= 32 * 32 * 32) {
+    if (h <= 32 * 32 * (VEC == 8 && h % VEC == 0 ? 64 : 32)) {
         if (h % VEC == 0) return forward_rows<T, VEC>(x, gamma, beta, T_, h, eps, y, mean, rstd, st);
         return forward_rows<T, 1>(x, gamma, beta, T_, h, eps, y, mean, rstd, st);
     }

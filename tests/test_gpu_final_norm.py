@@ -53,6 +53,18 @@ def test_against_float64(T, h, dtype):
     check(T, h, dtype)
 
 
+# numbers of warps that are no power of two, clusters of each even size with
+# whole and ragged shares, the widest rows in registers and the first beyond
+WIDTHS = [(40, 2560), (12, 3333), (9, 3000), (31, 5120), (31, 6152), (11, 10240), (7, 12296), (5, 14336),
+          (4, 18432), (3, 28680), (2, 40968), (2, 65536), (2, 65544)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,h", WIDTHS)
+def test_warps_and_clusters(T, h, dtype):
+    check(T, h, dtype)
+
+
 @pytest.mark.parametrize("T,h,dtype", [(8192, 1024, torch.bfloat16), (2048, 20480, torch.bfloat16),
                                        (20000, 72, torch.float16), (1031, 4100, torch.float32)])
 def test_training_batches(T, h, dtype):
