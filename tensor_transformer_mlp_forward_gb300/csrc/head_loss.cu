@@ -439,9 +439,10 @@ unsigned blocks_of(long long n, long long per) { return static_cast<unsigned>((n
 cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n_parts, int part_cols,
                                 const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets, int T,
                                 int h, int V, float* loss, float* lse, cudaStream_t st, int* launches) {
-    // as many rows a CTA as leave every SM its eight: few rows get many threads
+    // as many rows a CTA as let all run at once, five an SM: few rows get many
+    // threads (1000 rows with 256 each need a second wave: 9 us more)
     int rows = 1;
-    while (rows < 32 && T > 8 * 152LL * rows) rows *= 2;
+    while (rows < 32 && T > 5 * 152LL * rows) rows *= 2;
     ++*launches;
     return launch_dependent(head_combine_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, parts,
                             where, n_parts, part_cols, X, W, targets, T, h, V, rows, loss, lse);
