@@ -621,12 +621,11 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 def _in(x, name: str, shape, dtype, device: int) -> int:
     """The address of a contiguous tensor of this shape and type on this
     device (the current one: the library launches there)."""
-    if (x is None or not x.is_cuda or x.dtype is not dtype or x.shape != shape
-            or not x.is_contiguous()):
-        _ptr(x, name, shape, dtype)  # raises, naming what is wrong
-    if x.get_device() != device:
-        raise ValueError(f"{name} is on {x.device}, but the current device is cuda:{device}")
-    return x.data_ptr()
+    if (x is not None and x.dtype is dtype and x.shape == shape and x.get_device() == device
+            and device >= 0 and x.is_contiguous()):
+        return x.data_ptr()
+    _ptr(x, name, shape, dtype)  # raises, naming what is wrong
+    raise ValueError(f"{name} is on {x.device}, but the current device is cuda:{device}")
 
 
 def _stream_of(stream, device: int) -> int:
@@ -662,7 +661,7 @@ _U8 = torch.uint8
 
 
 def _device_of(x) -> int:
-    return torch.cuda.current_device() if x.is_cuda else -1  # -1: the first check names x
+    return torch._C._cuda_getDevice() if x.is_cuda else -1  # -1: the first check names x
 
 
 # The calls below are short on the GPU, so they are short here too: a fresh
