@@ -62,6 +62,20 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
     return u;
 }
 
+// The largest |dloss| of the tokens that count, which scales the gradients (1
+// where it is 0 or not finite).  A token a lane: one after the other their
+// loads' latencies added up to some microseconds.  Called by whole warps.
+__device__ __forceinline__ float dloss_scale(const float* dloss, const long long* targets, int T) {
+    const int lane = threadIdx.x & 31;
+    const long long y = lane < T ? __ldg(targets + lane) : -1;
+    const float d = lane < T ? fabsf(__ldg(dloss + lane)) : 0.0f;
+    float s = fmaxf(y >= 0 ? d : 0.0f, 0.0f);  // (a NaN counts as 0)
+#pragma unroll
+    for (int off = kTokens / 2; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
+    s = __shfl_sync(0xFFFFFFFFu, s, 0);
+    return s > 0.0f && s < INFINITY ? s : 1.0f;
+}
+
 struct FewArgs {
     const __nv_bfloat16 *X, *W;
     const long long* targets;
@@ -100,10 +114,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kerne
     float mx = -INFINITY, sum = 0.0f, lse2 = INFINITY, weight = 0.0f;
     if (t < p.T) y = __ldg(p.targets + t);
     if constexpr (GRAD) {
-        float s = 0.0f;
-        for (int i = 0; i < p.T; ++i)
-            if (__ldg(p.targets + i) >= 0) s = fmaxf(s, fabsf(__ldg(p.dloss + i)));
-        if (!(s > 0.0f && s < INFINITY)) s = 1.0f;
+        const float s = dloss_scale(p.dloss, p.targets, p.T);
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = s;
         if (t < p.T && y >= 0) {
             lse2 = __ldg(p.lse + t) * kLog2e;
@@ -427,7 +438,7 @@ constexpr int kFusedStageBytes = kFusedColumns / 64 * kBoxBytes;
 
 // Up to eight tokens: two CTAs an SM of eight warps with two boxes each, so
 // that one's barriers overlap the other's arithmetic (7 tokens: 57 us with
-// one CTA of 16 warps, 48 with two).  Up to 16: the registers of two boxes
+// one CTA of 16 warps, 47 with two).  Up to 16: the registers of two boxes
 // would spill (71 us against 66).
 template <int TT>
 struct Fused {
@@ -507,10 +518,8 @@ __global__ void __launch_bounds__(Fused<TT>::THREADS, Fused<TT>::CTAS)
     // thread (row of the block, token) of the logits' meeting
     const int vr = threadIdx.x / (8 * TT), t = threadIdx.x % (8 * TT);
     long long y = -1;
-    float lse2 = INFINITY, weight = 0.0f, s = 0.0f;
-    for (int i = 0; i < p.T; ++i)
-        if (__ldg(p.targets + i) >= 0) s = fmaxf(s, fabsf(__ldg(p.dloss + i)));
-    if (!(s > 0.0f && s < INFINITY)) s = 1.0f;
+    float lse2 = INFINITY, weight = 0.0f;
+    const float s = dloss_scale(p.dloss, p.targets, p.T);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = s;
     if (t < p.T) {
         y = __ldg(p.targets + t);

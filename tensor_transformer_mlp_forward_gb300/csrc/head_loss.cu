@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(1024)
 // out[i] = bf16(s sum_k P[k][i]): a CTA takes 256 / chains pieces of 8 values,
 // `chains` threads a piece (1, or 16 or 32 for many planes of few values),
 // each adding planes c, c + chains, ... in order; then the chains in order.
-// `mend` adds what the sum lacks to the 8 values at i.
+// `mend`, called before the planes are read, returns what adds the rest that
+// the sum lacks to the 8 values at i.
 template <typename Mend>
 __device__ __forceinline__ void reduce_planes(const float* __restrict__ P, int planes, long long count,
                                               int chains, float s, __nv_bfloat16* __restrict__ out,
@@ -303,6 +304,7 @@ __device__ __forceinline__ void reduce_planes(const float* __restrict__ P, int p
     float a[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+    const auto rest = mend(i, chain == 0 && ok);
     if (ok) {
 #pragma unroll 4
         for (int k = chain; k < planes; k += chains) {
@@ -323,7 +325,7 @@ __device__ __forceinline__ void reduce_planes(const float* __restrict__ P, int p
         }
     }
     if (chain != 0 || !ok) return;
-    mend(i, a);
+    rest(a);
     uint4 o;
     o.x = pack_bf16x2(s * a[0], s * a[1]);
     o.y = pack_bf16x2(s * a[2], s * a[3]);
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kThreads)
                        const float* __restrict__ scale, __nv_bfloat16* __restrict__ out) {
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // its inputs come from the kernel before it
-    reduce_planes(P, planes, count, chains, __ldg(scale), out, [](long long, float(&)[8]) {});
+    reduce_planes(P, planes, count, chains, __ldg(scale), out, [](long long, bool) { return [](float(&)[8]) {}; });
 }
 
 __device__ __forceinline__ void add_scaled8(float (&x)[8], float e, const uint4 u) {
@@ -368,23 +370,32 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();               // its inputs come from the kernel before it
     const float s = __ldg(scale);
     if (static_cast<int>(blockIdx.x) < reduce_ctas) {
-        reduce_planes(P, planes, static_cast<long long>(T) * h, chains, s, dX, [&](long long i, float(&a)[8]) {
-            const int t = static_cast<int>(i / h);
+        reduce_planes(P, planes, static_cast<long long>(T) * h, chains, s, dX, [&](long long i, bool here) {
+            const int t = here ? static_cast<int>(i / h) : 0;
             const long long y = __ldg(targets + t);
-            if (y >= 0 && y < V)
-                add_scaled8(a, __ldg(err + t), __ldg(reinterpret_cast<const uint4*>(W + y * h + (i - static_cast<long long>(t) * h))));
+            const bool in = here && y >= 0 && y < V;
+            const uint4 w = in ? __ldg(reinterpret_cast<const uint4*>(W + y * h + (i - static_cast<long long>(t) * h)))
+                               : make_uint4(0u, 0u, 0u, 0u);
+            const float e = in ? __ldg(err + t) : 0.0f;
+            return [=](float(&a)[8]) {
+                if (in) add_scaled8(a, e, w);
+            };
         });
         return;
     }
     __shared__ float sums[kThreads / 32][16];
     __shared__ float dz[16];
     const int own = static_cast<int>(blockIdx.x) - reduce_ctas;
-    const long long y = __ldg(targets + own);
-    if (y < 0 || y >= V) return;
-    for (int t = 0; t < own; ++t)
-        if (__ldg(targets + t) == y) return;  // an earlier token's CTA does the row
-    const uint4* w = reinterpret_cast<const uint4*>(W + y * h);
+    // A token a lane, all loads at once: one after the other their latencies
+    // would be most of this kernel's time.
     const int n = h >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool token = lane < T;
+    const long long yt = token ? __ldg(targets + lane) : -1;
+    const float gt = token ? __ldg(dloss + lane) : 0.0f, lse_t = token ? __ldg(lse + lane) : 0.0f;
+    const long long y = __shfl_sync(0xFFFFFFFFu, yt, own);
+    if (y < 0 || y >= V) return;
+    if (__any_sync(0xFFFFFFFFu, lane < own && yt == y)) return;  // an earlier token's CTA does the row
+    const uint4* w = reinterpret_cast<const uint4*>(W + y * h);
     float dot[16];
 #pragma unroll
     for (int t = 0; t < 16; ++t) dot[t] = 0.0f;
@@ -406,10 +417,9 @@ __global__ void __launch_bounds__(kThreads)
         float z = 0.0f, d = 0.0f;
 #pragma unroll
         for (int k = 0; k < kThreads / 32; ++k) z += sums[k][t];
-        const long long yt = t < T ? __ldg(targets + t) : -1;
         if (yt >= 0) {
-            const float g = yt < V ? __ldg(dloss + t) / s : __int_as_float(0x7FC00000);
-            d = g * ex2_approx(fmaf(z, kLog2e, -__ldg(lse + t) * kLog2e)) - (yt == y ? g : 0.0f);
+            const float g = yt < V ? gt / s : __int_as_float(0x7FC00000);
+            d = g * ex2_approx(fmaf(z, kLog2e, -lse_t * kLog2e)) - (yt == y ? g : 0.0f);
         }
         dz[t] = d;
     }
