@@ -203,6 +203,23 @@ __device__ __forceinline__ float2 warp_sum(float2 x) {
     return x;
 }
 
+// Sums of four values over the warp: lanes 8 v .. 8 v + 7 receive that of value
+// v.  A lane gives away half of its values at each of the first two steps: 6
+// exchanges instead of 20.
+__device__ __forceinline__ float warp_sum4(float2 a, float2 b) {
+    const int lane = threadIdx.x & 31;
+    const bool second = lane & 16, other = lane & 8;
+    float2 k = second ? b : a;
+    const float2 away = second ? a : b;
+    k.x += __shfl_xor_sync(0xFFFFFFFFu, away.x, 16);
+    k.y += __shfl_xor_sync(0xFFFFFFFFu, away.y, 16);
+    float x = other ? k.y : k.x;
+    x += __shfl_xor_sync(0xFFFFFFFFu, other ? k.x : k.y, 8);
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+    return x;
+}
+
 // Sum over the W warps of a row's group (`first` and the W - 1 behind it);
 // every thread receives the total, added in the same order in every thread.  `scratch` holds one entry a warp.  All threads of
 // the CTA call it.
@@ -479,20 +496,32 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         uint64_t* bar = &sums[b_slot];
         float2* slot = slots[b_slot][rank * warps + warp];
 #pragma unroll
-        for (int u = 0; u < U; ++u) m[u] = warp_sum(make_float2(m[u].x + m[u].y, mx[u].x + mx[u].y));
-        if constexpr (!CLUSTER) {
+        for (int u = 0; u < U; ++u) m[u] = make_float2(m[u].x + m[u].y, mx[u].x + mx[u].y);
+        if constexpr (U == 2) {
+            // value v of the two rows' four lies in lanes 8 v and on: one word
+            // to a place of the slot, and to eight CTAs
+            const float v = warp_sum4(m[0], m[1]);
+            if constexpr (!CLUSTER) {
+                if ((lane & 7) == 0) reinterpret_cast<float*>(slot)[lane >> 3] = v;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);  // releases the slot to the waiting warps
+            } else {
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * warps * U * sizeof(float2));
+                if ((lane & 7) < cl)
+                    st_async_f32(map_to_cta(smem_u32(slot) + 4 * (lane >> 3), lane & 7), v,
+                                 map_to_cta(smem_u32(bar), lane & 7));
+            }
+        } else if constexpr (!CLUSTER) {
+            m[0] = warp_sum(m[0]);
             if (lane == 0) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) slot[u] = m[u];
-                mbar_arrive(bar);  // releases the slot to the waiting warps
+                slot[0] = m[0];
+                mbar_arrive(bar);
             }
         } else {
+            m[0] = warp_sum(m[0]);
             if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * warps * U * sizeof(float2));
-            if (lane < cl) {
-                const uint32_t peer = map_to_cta(smem_u32(slot), lane), peer_bar = map_to_cta(smem_u32(bar), lane);
-#pragma unroll
-                for (int u = 0; u < U; ++u) st_async_v2(peer + u * sizeof(float2), m[u], peer_bar);
-            }
+            if (lane < cl)
+                st_async_v2(map_to_cta(smem_u32(slot), lane), m[0], map_to_cta(smem_u32(bar), lane));
         }
         __syncwarp();
         if (++b_stage == p.stages) {
@@ -525,6 +554,17 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         warp_wait_polls(&sums[slot], phase, &abort_flag, p.status);
         if (threadIdx.x == 0 && i >= AHEAD) issue();  // block i - AHEAD is read
         float2 m[U];
+        if constexpr (CLUSTER && U == 2) {
+            // eight lanes a value, as warp_sum4 leaves them
+            const float* f = reinterpret_cast<const float*>(slots[slot]);
+            float v = 0.0f;
+            for (int j = lane & 7; j < cl * warps; j += 8) v += f[4 * j + (lane >> 3)];
+#pragma unroll
+            for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                m[u] = make_float2(__shfl_sync(0xFFFFFFFFu, v, 16 * u), __shfl_sync(0xFFFFFFFFu, v, 16 * u + 8));
+        } else
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             m[u] = both(0.0f);

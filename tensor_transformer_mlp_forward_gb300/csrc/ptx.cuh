@@ -392,6 +392,13 @@ __device__ __forceinline__ void st_async_v2(uint32_t addr, float2 v, uint32_t ba
         : "memory");
 }
 
+// The same, 4 bytes.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v),
+                 "r"(bar)
+                 : "memory");
+}
+
 // ------------------------------------------------ cluster launch control
 // A running CTA may cancel the launch of a cluster of its own grid that has
 // not started yet and do that cluster's work instead.  The request is
