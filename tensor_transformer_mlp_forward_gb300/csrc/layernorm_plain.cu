@@ -365,6 +365,17 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     else
         __syncthreads();
 
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // where a lane sends its sums: its place of slot 0, and that slot's barrier
+    uint32_t peer_slot = 0, peer_bar = 0;
+    if constexpr (CLUSTER) {
+        const int peer = U == 2 ? lane & 7 : lane;
+        if (peer < cl) {
+            peer_slot = map_to_cta(smem_u32(slots[0][rank * warps + warp]) + (U == 2 ? 4 * (lane >> 3) : 0), peer);
+            peer_bar = map_to_cta(smem_u32(&sums[0]), peer);
+        }
+    }
+
     // This CTA's blocks are unit, unit + step, ..., n of them.  Everything a
     // block needs advances by additions: with divisions and 64-bit addresses
     // in the loop the overhead was 490 instructions a warp and block against
@@ -374,7 +385,8 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     const uint32_t stage_bytes = 2u * p.buf_bytes;
     const int row_bytes = static_cast<int>(E) * h;
 
-    // Thread 0: copies of the next block not yet issued into the next stage.
+    // Warp 0: copies of the next block not yet issued into the next stage, one a
+    // lane.
     // One CTA a row: the block's rows are one contiguous range, of which whole
     // 16-byte granules of the tensor are copied (all but its last few bytes).
     // A cluster: each row's columns are copied by themselves.
@@ -394,28 +406,22 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         uint64_t* bar = &full[issue_stage];
         const uint8_t *px = reinterpret_cast<const uint8_t*>(x), *pd = reinterpret_cast<const uint8_t*>(dy);
         if (CLUSTER && U > 1) {
-            const int k = min(static_cast<uint32_t>(U), rows - issue_row);
-            mbar_arrive_expect_tx(bar, 2 * k * row_bytes);
-            for (int u = 0; u < k; ++u) {
-                const long long a0 = issue_b0 + u * E * p.h;
-                bulk_load(dst + u * row_bytes, px + a0, row_bytes, bar);
-                bulk_load(dst + u * row_bytes + p.buf_bytes, pd + a0, row_bytes, bar);
-            }
+            const int k = min(static_cast<uint32_t>(U), rows - issue_row), u = lane & (U - 1), t = lane / U;
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * k * row_bytes);
+            if (t < 2 && u < k)
+                bulk_load(dst + u * row_bytes + t * p.buf_bytes, (t ? pd : px) + issue_b0 + u * E * p.h, row_bytes, bar);
         } else {
             long long a0;
             const uint32_t bytes = copied(issue_b0, CLUSTER ? row_bytes : static_cast<int>(block_rows) * row_bytes, a0);
-            mbar_arrive_expect_tx(bar, 2 * bytes);
-            if (bytes) {
-                bulk_load(dst, px + a0, bytes, bar);
-                bulk_load(dst + p.buf_bytes, pd + a0, bytes, bar);
-            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
+            if (lane < 2 && bytes) bulk_load(dst + lane * p.buf_bytes, (lane ? pd : px) + a0, bytes, bar);
         }
         issue_b0 += issue_step;
         issue_row += row_step;
         --issue_left;
         if (++issue_stage == p.stages) issue_stage = 0;
     };
-    if (threadIdx.x == 0)
+    if (warp == 0)
         for (int s = 0; s < p.stages; ++s) issue();
 
     constexpr int PAIRS = Piece<T, VEC>::N / 2;
@@ -426,7 +432,6 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
 #pragma unroll
     for (int k = 0; k < NV; ++k) kg[k] = load_piece<T, VEC>(gamma + c0, k, group, sub, h);
     const float inv_h = 1.0f / static_cast<float>(p.h);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     struct Stats {
         float2 v[U];
     };
@@ -508,8 +513,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
             } else {
                 if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * warps * U * sizeof(float2));
                 if ((lane & 7) < cl)
-                    st_async_f32(map_to_cta(smem_u32(slot) + 4 * (lane >> 3), lane & 7), v,
-                                 map_to_cta(smem_u32(bar), lane & 7));
+                    st_async_f32(peer_slot + b_slot * sizeof(slots[0]), v, peer_bar + b_slot * sizeof(sums[0]));
             }
         } else if constexpr (!CLUSTER) {
             m[0] = warp_sum(m[0]);
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
             m[0] = warp_sum(m[0]);
             if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * warps * U * sizeof(float2));
             if (lane < cl)
-                st_async_v2(map_to_cta(smem_u32(slot), lane), m[0], map_to_cta(smem_u32(bar), lane));
+                st_async_v2(peer_slot + b_slot * sizeof(slots[0]), m[0], peer_bar + b_slot * sizeof(sums[0]));
         }
         __syncwarp();
         if (++b_stage == p.stages) {
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     for (int i = 0; i < n; ++i) {
         const Stats st_after = row_stats(row + (AHEAD + 1) * row_step);
         warp_wait_polls(&sums[slot], phase, &abort_flag, p.status);
-        if (threadIdx.x == 0 && i >= AHEAD) issue();  // block i - AHEAD is read
+        if (warp == 0 && i >= AHEAD) issue();  // block i - AHEAD is read
         float2 m[U];
         if constexpr (CLUSTER && U == 2) {
             // eight lanes a value, as warp_sum4 leaves them
