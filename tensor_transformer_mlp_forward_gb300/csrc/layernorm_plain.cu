@@ -203,20 +203,27 @@ __device__ __forceinline__ float2 warp_sum(float2 x) {
     return x;
 }
 
-// Sums of four values over the warp: lanes 8 v .. 8 v + 7 receive that of value
-// v.  A lane gives away half of its values at each of the first two steps: 6
-// exchanges instead of 20.
-__device__ __forceinline__ float warp_sum4(float2 a, float2 b) {
+// Sums over the warp of the U pairs' 2 U values: 32 / (2 U) lanes after one
+// another receive each.  A lane gives away half of its values at each of the
+// first steps: 6 exchanges for four values instead of 20.
+template <int U>
+__device__ __forceinline__ float warp_sums(const float2 (&v)[U]) {
+    static_assert(U == 1 || U == 2, "");
     const int lane = threadIdx.x & 31;
-    const bool second = lane & 16, other = lane & 8;
-    float2 k = second ? b : a;
-    const float2 away = second ? a : b;
-    k.x += __shfl_xor_sync(0xFFFFFFFFu, away.x, 16);
-    k.y += __shfl_xor_sync(0xFFFFFFFFu, away.y, 16);
+    float2 k = v[0];
+    if constexpr (U == 2) {
+        const bool second = lane & 16;
+        const float2 away = second ? v[0] : v[1];
+        if (second) k = v[1];
+        k.x += __shfl_xor_sync(0xFFFFFFFFu, away.x, 16);
+        k.y += __shfl_xor_sync(0xFFFFFFFFu, away.y, 16);
+    }
+    constexpr int HALF = 16 / U;
+    const bool other = lane & HALF;
     float x = other ? k.y : k.x;
-    x += __shfl_xor_sync(0xFFFFFFFFu, other ? k.x : k.y, 8);
+    x += __shfl_xor_sync(0xFFFFFFFFu, other ? k.x : k.y, HALF);
 #pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+    for (int off = HALF / 2; off >= 1; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
     return x;
 }
 
@@ -307,7 +314,7 @@ __global__ void __launch_bounds__(1024)
 // (one row at a time, `cols` columns each).
 // Measured in bf16: 8192 x 1024 in 18.9 us with the sum of the parts (2.7 TB/s;
 // start, end and the sum's launch are half of it), 40960 x 1024 in 47 us (5.4
-// TB/s), 8192 x 8192 in 75 us (5.3 TB/s), 2048 x 20480 in 60 us (4.2 TB/s);
+// TB/s), 8192 x 8192 in 70 us (5.8 TB/s), 2048 x 20480 in 55 us (4.6 TB/s);
 // the longest are bound by HBM reading and writing at once.
 // There is no barrier in the loop.  A warp begins block i + AHEAD (its part of
 // the row sums, which go to the shared memory of every CTA of the row and are
@@ -366,13 +373,16 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         __syncthreads();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // where a lane sends its sums: its place of slot 0, and that slot's barrier
+    // which of a block's 2 U sums a lane holds, and which of its holders it is
+    constexpr int HOLDERS = 16 / U;
+    static_assert(HOLDERS >= kNormMaxCluster, "a holder for each CTA");
+    const int value = lane / HOLDERS, part = lane % HOLDERS;
+    // where it sends it: its place of slot 0, and that slot's barrier
     uint32_t peer_slot = 0, peer_bar = 0;
     if constexpr (CLUSTER) {
-        const int peer = U == 2 ? lane & 7 : lane;
-        if (peer < cl) {
-            peer_slot = map_to_cta(smem_u32(slots[0][rank * warps + warp]) + (U == 2 ? 4 * (lane >> 3) : 0), peer);
-            peer_bar = map_to_cta(smem_u32(&sums[0]), peer);
+        if (part < cl) {
+            peer_slot = map_to_cta(smem_u32(slots[0][rank * warps + warp]) + 4 * value, part);
+            peer_bar = map_to_cta(smem_u32(&sums[0]), part);
         }
     }
 
@@ -502,30 +512,15 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         float2* slot = slots[b_slot][rank * warps + warp];
 #pragma unroll
         for (int u = 0; u < U; ++u) m[u] = make_float2(m[u].x + m[u].y, mx[u].x + mx[u].y);
-        if constexpr (U == 2) {
-            // value v of the two rows' four lies in lanes 8 v and on: one word
-            // to a place of the slot, and to eight CTAs
-            const float v = warp_sum4(m[0], m[1]);
-            if constexpr (!CLUSTER) {
-                if ((lane & 7) == 0) reinterpret_cast<float*>(slot)[lane >> 3] = v;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar);  // releases the slot to the waiting warps
-            } else {
-                if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * warps * U * sizeof(float2));
-                if ((lane & 7) < cl)
-                    st_async_f32(peer_slot + b_slot * sizeof(slots[0]), v, peer_bar + b_slot * sizeof(sums[0]));
-            }
-        } else if constexpr (!CLUSTER) {
-            m[0] = warp_sum(m[0]);
-            if (lane == 0) {
-                slot[0] = m[0];
-                mbar_arrive(bar);
-            }
+        const float v = warp_sums<U>(m);
+        if constexpr (!CLUSTER) {
+            if (part == 0) reinterpret_cast<float*>(slot)[value] = v;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);  // releases the slot to the waiting warps
         } else {
-            m[0] = warp_sum(m[0]);
             if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, cl * warps * U * sizeof(float2));
-            if (lane < cl)
-                st_async_v2(peer_slot + b_slot * sizeof(slots[0]), m[0], peer_bar + b_slot * sizeof(sums[0]));
+            if (part < cl)
+                st_async_f32(peer_slot + b_slot * sizeof(slots[0]), v, peer_bar + b_slot * sizeof(sums[0]));
         }
         __syncwarp();
         if (++b_stage == p.stages) {
@@ -558,24 +553,20 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         warp_wait_polls(&sums[slot], phase, &abort_flag, p.status);
         if (warp == 0 && i >= AHEAD) issue();  // block i - AHEAD is read
         float2 m[U];
-        if constexpr (CLUSTER && U == 2) {
-            // eight lanes a value, as warp_sum4 leaves them
+        if constexpr (CLUSTER) {
             const float* f = reinterpret_cast<const float*>(slots[slot]);
             float v = 0.0f;
-            for (int j = lane & 7; j < cl * warps; j += 8) v += f[4 * j + (lane >> 3)];
+            for (int j = part; j < cl * warps; j += HOLDERS) v += f[2 * U * j + value];
 #pragma unroll
-            for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+            for (int off = HOLDERS / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                m[u] = make_float2(__shfl_sync(0xFFFFFFFFu, v, 16 * u), __shfl_sync(0xFFFFFFFFu, v, 16 * u + 8));
-        } else
+                m[u] = make_float2(__shfl_sync(0xFFFFFFFFu, v, 2 * u * HOLDERS),
+                                   __shfl_sync(0xFFFFFFFFu, v, (2 * u + 1) * HOLDERS));
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            m[u] = both(0.0f);
-            if constexpr (CLUSTER) {
-                for (int j = lane; j < cl * warps; j += 32) m[u] = add2(m[u], slots[slot][j][u]);
-                m[u] = warp_sum(m[u]);
-            } else {
+            for (int u = 0; u < U; ++u) {
+                m[u] = both(0.0f);
 #pragma unroll 4
                 for (int j = 0; j < p.W; ++j) m[u] = add2(m[u], slots[slot][g * p.W + j][u]);
             }
@@ -900,8 +891,8 @@ NormPlan norm_plan(int T, int h, int elem) {
     // take a cluster, of an even number of CTAs: SMs come in pairs, and an odd
     // number leaves places empty (2048 x 20480 bf16: 73 us with five).  Of
     // those the number whose CTAs fill the SMs' warps best (63 us with six of
-    // seven warps, two an SM; 60 with eight of five, three an SM), the smaller
-    // where the difference is small.
+    // seven warps, two an SM; 60, now 55, with eight of five, three an SM), the
+    // smaller where the difference is small.
     // Rows beyond eight CTAs of 8 warps take eight of up to 16.
     const int warps = h <= kNormMaxCluster * 16 * 256 ? 8 : 16;
     int most = 0;

@@ -383,16 +383,8 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t rank) {
     return r;
 }
 
-// Two floats to the shared memory of a CTA of the cluster, 8 bytes counted on
-// that CTA's mbarrier (both shared::cluster addresses, 8-byte aligned).
-__device__ __forceinline__ void st_async_v2(uint32_t addr, float2 v, uint32_t bar) {
-    asm volatile(
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
-        "f"(v.x), "f"(v.y), "r"(bar)
-        : "memory");
-}
-
-// The same, 4 bytes.
+// A float to the shared memory of a CTA of the cluster, 4 bytes counted on
+// that CTA's mbarrier (both shared::cluster addresses).
 __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v),
                  "r"(bar)
