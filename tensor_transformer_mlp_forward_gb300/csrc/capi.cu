@@ -2042,7 +2042,7 @@ int choose_head_splits(int T, int h, long long total_kb) {
 struct HeadPlan {
     int width, splits;
     bool planes;
-    size_t info, scale, plane, dz, total;  // byte offsets, and the whole
+    size_t scale, plane, dz, total;  // byte offsets, and the whole
 };
 
 HeadPlan head_layout(int T, int h, int V, int width, int splits) {
@@ -2050,9 +2050,8 @@ HeadPlan head_layout(int T, int h, int V, int width, int splits) {
     p.width = width;
     p.splits = splits;
     p.planes = splits > 1 || width < V;
-    p.info = 0;
-    p.scale = align256(sizeof(float4) * static_cast<size_t>(T));
-    p.plane = p.scale + 256;
+    p.scale = 0;
+    p.plane = 256;
     p.dz = align256(p.plane + (p.planes ? sizeof(float) * static_cast<size_t>(splits) * T * h : 0));
     p.total = align256(p.dz + sizeof(uint16_t) * static_cast<size_t>(T) * width);
     return p;
@@ -2067,7 +2066,6 @@ HeadPlan head_plan_few(int T, int h, int V) {
     p.width = head_few_ldz(V);
     p.splits = head_few_planes(T, h, V);
     p.planes = true;
-    p.info = 0;
     p.scale = 0;
     p.plane = 256;
     p.dz = align256(p.plane + sizeof(float) * static_cast<size_t>(p.splits) * T * h);
@@ -2139,7 +2137,6 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
                   tpmlp_bf16* dW, void* ws, const HeadPlan& p, cudaStream_t st,
                   const DeviceInfo& d) {
     uint8_t* base = static_cast<uint8_t*>(ws);
-    float4* info = reinterpret_cast<float4*>(base + p.info);
     float* scale = reinterpret_cast<float*>(base + p.scale);
     float* plane = reinterpret_cast<float*>(base + p.plane);
     tpmlp_bf16* dz = reinterpret_cast<tpmlp_bf16*>(base + p.dz);
@@ -2159,8 +2156,6 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
                                        st, &t_last_launches);
         return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
     }
-    e = launch_head_prepare(dloss, lse, targets, T, V, info, scale, st, &t_last_launches);
-    if (e != cudaSuccess) return fail_cuda(e);
     for (long long v = 0; v < V; v += p.width) {
         const int v0 = static_cast<int>(v);
         const int cols = std::min(V - v0, p.width);
@@ -2169,7 +2164,12 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
         {   // dz = w (softmax - one-hot) of this piece
             GemmArgs g = blank_args();
             const GemmShape sh{T, width, h, 1, SHARD_N, 1LL * T * h, 1LL * cols * h};
-            g.row_info = info;
+            g.dloss = dloss;
+            g.lse = lse;
+            g.targets = targets;
+            g.vocab = V;
+            g.scale_out = v0 == 0 ? scale : nullptr;
+            g.out_scale = scale;
             g.col0 = v0;
             g.epi_kb = kHeadEpiKb;
             g.n_valid = cols;

@@ -153,10 +153,12 @@ struct GemmArgs {
     const long long* targets;  // EPI_LSE: target column of each row (negative: none)
     float2* lse_part;          // EPI_LSE: {max, sum of exponentials}, [tiles * EW / 4][M]
     uint8_t* lse_where;        // EPI_LSE: which 16 of the part's columns hold the max, likewise
-    const float4* row_info;    // EPI_DLOGITS: {lse log2(e), weight, target column (int bits), -}
+    const float *dloss, *lse;  // EPI_DLOGITS, [M]
+    int vocab;                 // EPI_DLOGITS: classes in all (a target behind them has no logit)
+    float* scale_out;          // EPI_DLOGITS: receives the largest |dloss|; null: *out_scale holds it
     int col0;                  // EPI_DLOGITS: vocabulary index of column 0
     int n_valid;               // EPI_DLOGITS: columns from here to N are stored as 0
-    const float* out_scale;    // EPI_SCALE
+    const float* out_scale;    // EPI_SCALE, EPI_DLOGITS
     int epi_kb;     // host side: most k-blocks for which eight epilogue warps pay (0: 16)
     int epi_warps;  // host side: 4 or 8 epilogue warps (the kernel variant launched)
     int dependent_launch;  // host side: launched with programmatic stream serialization
@@ -314,6 +316,44 @@ __device__ __forceinline__ float gelu_tanh_grad(float x) {
 // log2(e): exponentials are taken as 2^(log2(e) x), one multiply-add and one
 // ex2 per value.
 constexpr float kLog2e = 1.4426950408889634f;
+
+// The largest |dloss| of the tokens that count (1 where that is 0 or not
+// finite), taken by the `warps` epilogue warps of every CTA over all of them
+// while the first tile's products run (`place` + warp * `stride`: a float of
+// shared memory that is the warp's own).  The logits' gradients are divided by it, so that in
+// the usual case, one weight for all counted tokens, the weights are exactly 1
+// and the bf16 gradient rounds p - [v == y] itself, not its product with an
+// arbitrary factor; it multiplies the fp32 sums of dX and dW.
+__device__ __forceinline__ float head_scale(const float* dloss, const long long* targets, int T, int warps,
+                                            uint8_t* place, int stride) {
+    constexpr int kBatch = 32;  // a lane's loads in flight
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool share = T > 32 * kBatch;  // else each warp takes all by itself
+    const int first = share ? warp : 0, step = share ? warps : 1;
+    float s = 0.0f;
+    for (long long t0 = first * (32 * kBatch) + lane; t0 < T; t0 += step * (32 * kBatch)) {
+        float d[kBatch];
+        int sign[kBatch];  // the targets' upper halves
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const bool in = t0 + 32 * j < T;
+            d[j] = in ? __ldg(dloss + t0 + 32 * j) : 0.0f;
+            sign[j] = in ? __ldg(reinterpret_cast<const int*>(targets) + 2 * (t0 + 32 * j) + 1) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (sign[j] >= 0) s = fmaxf(s, fabsf(d[j]));
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
+    if (share) {
+        if (lane == 0) *reinterpret_cast<volatile float*>(place + warp * stride) = s;
+        named_bar_sync(1, 32 * warps);
+        for (int w = 0; w < warps; ++w) s = fmaxf(s, *reinterpret_cast<volatile float*>(place + w * stride));
+        named_bar_sync(1, 32 * warps);
+    }
+    return s > 0.0f && s < INFINITY ? s : 1.0f;
+}
 
 // 32 consecutive bf16 values -> float; entries at or beyond `valid` read 0.
 __device__ __forceinline__ void load_bf16x32(const __nv_bfloat16* p, int valid, float (&v)[32]) {
@@ -708,6 +748,15 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
         const uint32_t swz = static_cast<uint32_t>(lane & 7);
         uint32_t seq = 0;  // stores committed so far: selects the buffer
         int count = 0;
+        float dloss_max = 1.0f;
+        if constexpr (EPI == EPI_DLOGITS) {
+            if (p.scale_out == nullptr) {
+                dloss_max = __ldg(p.out_scale);
+            } else {
+                dloss_max = head_scale(p.dloss, p.targets, p.M, EW, staging, 2 * EPI_BUF_BYTES);
+                if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale_out = dloss_max;
+            }
+        }
         for (int tile = unit; tile >= 0; ++count) {
             const TileCoord tc = decode_tile<G::TILE_M, G::TILE_N>(tile, p);
             const int acc = G::ACCS == 2 ? (count & 1) : 0;
@@ -747,10 +796,11 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
             }
             if constexpr (EPI == EPI_DLOGITS) {
                 if (row_ok) {
-                    const float4 info = __ldg(p.row_info + m);
-                    lse2 = info.x;
-                    weight = info.y;
-                    target = __float_as_int(info.z) - p.col0 - tc.n0;
+                    const long long y = __ldg(p.targets + m);
+                    const bool known = y < p.vocab;
+                    weight = y < 0 ? 0.0f : known ? __ldg(p.dloss + m) / dloss_max : __int_as_float(0x7FC00000);
+                    lse2 = y < 0 ? INFINITY : __ldg(p.lse + m) * kLog2e;  // 2^(z - inf) = 0
+                    if (known && y >= 0) target = static_cast<int>(y) - p.col0 - tc.n0;
                 }
             }
             float scale = 1.0f;

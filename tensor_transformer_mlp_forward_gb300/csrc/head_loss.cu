@@ -242,51 +242,6 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// s = max |dloss| over the counted tokens (every CTA takes it over all of them
-// itself, so that one launch is enough), then the info of the CTA's 1024 rows.
-// The weights are divided by s so that in the usual case, one weight for all
-// counted tokens, they are exactly 1 and the bf16 gradient of the logits
-// rounds p - [v == y] itself, not its product with an arbitrary factor; s
-// multiplies the fp32 sums of dX and dW.
-__global__ void __launch_bounds__(1024)
-    head_prepare_kernel(const float* __restrict__ dloss, const float* __restrict__ lse,
-                        const long long* __restrict__ targets, int T, int V,
-                        float4* __restrict__ row_info, float* __restrict__ scale) {
-    pdl_launch_dependents();  // the next kernel may begin its launch
-    pdl_wait();               // lse may come from the kernel before this one
-    __shared__ float warp_max[32];
-    float s = 0.0f;
-#pragma unroll 8
-    for (int t = threadIdx.x; t < T; t += 1024) {
-        const float d = fabsf(__ldg(dloss + t));
-        if (__ldg(targets + t) >= 0) s = fmaxf(s, d);
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = warp_max[threadIdx.x & 31];
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
-    if (!(s > 0.0f && s < INFINITY)) s = 1.0f;  // all zero, or a gradient that is not finite
-    if (blockIdx.x == 0 && threadIdx.x == 0) *scale = s;
-    const long long t = static_cast<long long>(blockIdx.x) * 1024 + threadIdx.x;
-    if (t >= T) return;
-    const long long y = __ldg(targets + t);
-    float w = __ldg(dloss + t) / s;
-    float l = __ldg(lse + t) * kLog2e;
-    int target = -1;
-    if (y < 0) {
-        w = 0.0f;
-        l = INFINITY;  // 2^(z - inf) = 0
-    } else if (y >= V) {
-        w = __int_as_float(0x7FC00000);
-    } else {
-        target = static_cast<int>(y);
-    }
-    row_info[t] = make_float4(l, w, __int_as_float(target), 0.0f);
-}
-
 // out[i] = bf16(s sum_k P[k][i]): a CTA takes 256 / chains pieces of 8 values,
 // `chains` threads a piece (1, or 16 or 32 for many planes of few values),
 // each adding planes c, c + chains, ... in order; then the chains in order.
@@ -456,14 +411,6 @@ cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n
     ++*launches;
     return launch_dependent(head_combine_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, parts,
                             where, n_parts, part_cols, X, W, targets, T, h, V, rows, loss, lse);
-}
-
-cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long long* targets,
-                                int T, int V, float4* row_info, float* scale, cudaStream_t st,
-                                int* launches) {
-    ++*launches;
-    return launch_dependent(head_prepare_kernel, dim3(blocks_of(T, 1024)), dim3(1024), 0, st, dloss, lse, targets, T, V,
-                            row_info, scale);
 }
 
 cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,

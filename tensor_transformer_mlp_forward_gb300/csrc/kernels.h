@@ -92,11 +92,6 @@ cudaError_t launch_head_dw(const GemmMaps& m, const GemmArgs& g, int grid, bool 
 cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n_parts, int part_cols,
                                 const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets, int T,
                                 int h, int V, float* loss, float* lse, cudaStream_t st, int* launches);
-// Backward: row_info[t] = {lse log2(e), dloss[t] / s, target, 0} and *scale =
-// s, the largest |dloss| of the counted tokens.
-cudaError_t launch_head_prepare(const float* dloss, const float* lse, const long long* targets,
-                                int T, int V, float4* row_info, float* scale, cudaStream_t st,
-                                int* launches);
 // The head for few tokens (head_few.cu): head_few(T) says whether T are few.
 // Forward: head_few_parts(V) {max, sum} parts a token.  Backward: dz and dzt
 // (16 head_few_ldz(V) values each), *scale, err (16 values), dW, and dX as
