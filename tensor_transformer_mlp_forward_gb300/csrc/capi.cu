@@ -2042,7 +2042,7 @@ int choose_head_splits(int T, int h, long long total_kb) {
 struct HeadPlan {
     int width, splits;
     bool planes;
-    size_t scale, plane, dz, total;  // byte offsets, and the whole
+    size_t scale, target, plane, dz, total;  // byte offsets, and the whole
 };
 
 HeadPlan head_layout(int T, int h, int V, int width, int splits) {
@@ -2051,7 +2051,8 @@ HeadPlan head_layout(int T, int h, int V, int width, int splits) {
     p.splits = splits;
     p.planes = splits > 1 || width < V;
     p.scale = 0;
-    p.plane = 256;
+    p.target = 256;
+    p.plane = align256(p.target + sizeof(float) * static_cast<size_t>(T));
     p.dz = align256(p.plane + (p.planes ? sizeof(float) * static_cast<size_t>(splits) * T * h : 0));
     p.total = align256(p.dz + sizeof(uint16_t) * static_cast<size_t>(T) * width);
     return p;
@@ -2066,7 +2067,7 @@ HeadPlan head_plan_few(int T, int h, int V) {
     p.width = head_few_ldz(V);
     p.splits = head_few_planes(T, h, V);
     p.planes = true;
-    p.scale = 0;
+    p.scale = p.target = 0;  // no target_q: the kernels mend the target's dz themselves
     p.plane = 256;
     p.dz = align256(p.plane + sizeof(float) * static_cast<size_t>(p.splits) * T * h);
     p.total = align256(p.dz + 2 * sizeof(uint16_t) * 16 * static_cast<size_t>(p.width));
@@ -2156,6 +2157,9 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
                                        st, &t_last_launches);
         return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
     }
+    float* target_q = reinterpret_cast<float*>(base + p.target);
+    e = launch_head_target(cb(X), cb(W), targets, lse, T, h, V, target_q, st, &t_last_launches);
+    if (e != cudaSuccess) return fail_cuda(e);
     for (long long v = 0; v < V; v += p.width) {
         const int v0 = static_cast<int>(v);
         const int cols = std::min(V - v0, p.width);
@@ -2166,6 +2170,7 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
             const GemmShape sh{T, width, h, 1, SHARD_N, 1LL * T * h, 1LL * cols * h};
             g.dloss = dloss;
             g.lse = lse;
+            g.target_q = target_q;
             g.targets = targets;
             g.vocab = V;
             g.scale_out = v0 == 0 ? scale : nullptr;

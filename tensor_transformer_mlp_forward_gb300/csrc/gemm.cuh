@@ -154,6 +154,7 @@ struct GemmArgs {
     float2* lse_part;          // EPI_LSE: {max, sum of exponentials}, [tiles * EW / 4][M]
     uint8_t* lse_where;        // EPI_LSE: which 16 of the part's columns hold the max, likewise
     const float *dloss, *lse;  // EPI_DLOGITS, [M]
+    const float* target_q;     // EPI_DLOGITS, [M]: softmax - 1 at the row's target, from its fp32 logit
     int vocab;                 // EPI_DLOGITS: classes in all (a target behind them has no logit)
     float* scale_out;          // EPI_DLOGITS: receives the largest |dloss|; null: *out_scale holds it
     int col0;                  // EPI_DLOGITS: vocabulary index of column 0
@@ -785,9 +786,9 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                 load_raw32(p.bias + gcol0 + out_blk(cb0) * 64, min(32, p.N - (tc.n0 + out_blk(cb0) * 64)),
                            bias_cur);
             // The row's target column relative to this tile, and (EPI_DLOGITS)
-            // its log-sum-exp and weight.
+            // its log-sum-exp, weight and gradient at the target.
             int target = -1;
-            float lse2 = 0.0f, weight = 0.0f;
+            float lse2 = 0.0f, weight = 0.0f, target_dz = 0.0f;
             if constexpr (EPI == EPI_LSE) {
                 if (row_ok) {
                     const long long y = __ldg(p.targets + m);
@@ -800,7 +801,10 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                     const bool known = y < p.vocab;
                     weight = y < 0 ? 0.0f : known ? __ldg(p.dloss + m) / dloss_max : __int_as_float(0x7FC00000);
                     lse2 = y < 0 ? INFINITY : __ldg(p.lse + m) * kLog2e;  // 2^(z - inf) = 0
-                    if (known && y >= 0) target = static_cast<int>(y) - p.col0 - tc.n0;
+                    if (known && y >= 0) {
+                        target = static_cast<int>(y) - p.col0 - tc.n0;
+                        if (target >= 0 && target < G::TILE_N) target_dz = weight * __ldg(p.target_q + m);
+                    }
                 }
             }
             float scale = 1.0f;
@@ -1042,7 +1046,7 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                         if (__any_sync(0xFFFFFFFFu, t >= 0 && t < 32)) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (i == t) v[i] -= weight;
+                                if (i == t) v[i] = target_dz;  // this accumulator is too coarse for p - 1
                         }
                         if (p.n_valid - n < 32) {
 #pragma unroll

@@ -31,6 +31,27 @@ __device__ __forceinline__ float dot8(const uint4 a, const uint4 b) {
     return s;
 }
 
+// Thread `sub` of `group`'s share of the dot product of two rows of n pieces of
+// 8 values, loads in batches.
+__device__ __forceinline__ float dot_rows(const __nv_bfloat16* a_row, const __nv_bfloat16* b_row, int n, int sub,
+                                          int group) {
+    const uint4* x = reinterpret_cast<const uint4*>(a_row);
+    const uint4* w = reinterpret_cast<const uint4*>(b_row);
+    float dot = 0.0f;
+    for (int i = sub; i < n; i += 4 * group) {
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = i + j * group < n;
+            a[j] = in ? __ldg(x + i + j * group) : make_uint4(0u, 0u, 0u, 0u);
+            b[j] = in ? __ldg(w + i + j * group) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dot += dot8(a[j], b[j]);
+    }
+    return dot;
+}
+
 // {m, s} stands for s 2^(m log2(e)); m = -inf: nothing.
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x);
@@ -128,22 +149,8 @@ __global__ void __launch_bounds__(kThreads)
         }
     };
     load_parts(sub);
-    if (ok && y >= 0 && y < V) {
-        const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<long long>(row) * h);
-        const uint4* w = reinterpret_cast<const uint4*>(W + y * h);
-        const int n = h >> 3;
-        for (int i = sub; i < n; i += 4 * group) {
-            uint4 a[4], b[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = i + j * group < n;
-                a[j] = in ? __ldg(x + i + j * group) : make_uint4(0u, 0u, 0u, 0u);
-                b[j] = in ? __ldg(w + i + j * group) : make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dot += dot8(a[j], b[j]);
-        }
-    }
+    if (ok && y >= 0 && y < V)
+        dot = dot_rows(X + static_cast<long long>(row) * h, W + y * h, h >> 3, sub, group);
     for (int i = sub;;) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -240,6 +247,44 @@ __global__ void __launch_bounds__(kThreads)
         }
         __syncthreads();
     }
+}
+
+// q[t] = exp(z - lse[t]) - 1 for the logit z of token t's target, 0 where there
+// is none: what the backward pass has of it beside the other classes'
+// probabilities.  With the model sure of the target, z and lse are near equals,
+// and z as the GEMM has it -- cut toward zero at every step, 5e-4 small at a
+// logit of 20 from 20480 products -- would leave nothing of their difference
+// (the gradient of such a token came out some hundred times too large).  So z
+// is taken in fp32, as forward, and only the difference is rounded.
+// `rows` rows a CTA as in head_combine_kernel.
+__global__ void __launch_bounds__(kThreads)
+    head_target_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
+                       const long long* __restrict__ targets, const float* __restrict__ lse, int T, int h, int V,
+                       int rows, float* __restrict__ q) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    pdl_wait();               // X comes from the kernel before this one
+    __shared__ Two warp_dot[kThreads / 32];
+    const int group = kThreads / rows;  // threads a row, 8..256
+    const int r = threadIdx.x / group, sub = threadIdx.x % group;
+    const int row = blockIdx.x * rows + r;
+    const bool ok = row < T;
+    const long long y = ok ? __ldg(targets + row) : -1;
+    const bool in = y >= 0 && y < V;
+    const float l = ok ? __ldg(lse + row) : 0.0f;
+    Two z{in ? dot_rows(X + static_cast<long long>(row) * h, W + y * h, h >> 3, sub, group) : 0.0f, 0.0f};
+    for (int off = min(group, 32) >> 1; off >= 1; off >>= 1) {
+        Two o;
+        o.hi = __shfl_xor_sync(0xFFFFFFFFu, z.hi, off);
+        o.lo = __shfl_xor_sync(0xFFFFFFFFu, z.lo, off);
+        z = add(z, o);
+    }
+    if (group > 32) {
+        if ((threadIdx.x & 31) == 0) warp_dot[threadIdx.x >> 5] = z;
+        __syncthreads();
+        if (sub == 0)
+            for (int w = 1; w < group / 32; ++w) z = add(z, warp_dot[(threadIdx.x >> 5) + w]);
+    }
+    if (sub == 0 && ok) q[row] = in ? expm1f((z.hi - l) + z.lo) : 0.0f;
 }
 
 // out[i] = bf16(s sum_k P[k][i]): a CTA takes 256 / chains pieces of 8 values,
@@ -399,18 +444,31 @@ int chains_for(int planes) { return planes >= 64 ? 32 : planes >= 8 ? 16 : 1; }
 
 unsigned blocks_of(long long n, long long per) { return static_cast<unsigned>((n + per - 1) / per); }
 
+// As many rows a CTA of the row kernels as let all run at once, five an SM: few
+// rows get many threads (1000 rows with 256 each need a second wave: 9 us more).
+int rows_a_cta(int T) {
+    int rows = 1;
+    while (rows < 32 && T > 5 * 152LL * rows) rows *= 2;
+    return rows;
+}
+
 }  // namespace
 
 cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n_parts, int part_cols,
                                 const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets, int T,
                                 int h, int V, float* loss, float* lse, cudaStream_t st, int* launches) {
-    // as many rows a CTA as let all run at once, five an SM: few rows get many
-    // threads (1000 rows with 256 each need a second wave: 9 us more)
-    int rows = 1;
-    while (rows < 32 && T > 5 * 152LL * rows) rows *= 2;
+    const int rows = rows_a_cta(T);
     ++*launches;
     return launch_dependent(head_combine_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, parts,
                             where, n_parts, part_cols, X, W, targets, T, h, V, rows, loss, lse);
+}
+
+cudaError_t launch_head_target(const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets,
+                               const float* lse, int T, int h, int V, float* q, cudaStream_t st, int* launches) {
+    const int rows = rows_a_cta(T);
+    ++*launches;
+    return launch_dependent(head_target_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, X, W, targets, lse,
+                            T, h, V, rows, q);
 }
 
 cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,
