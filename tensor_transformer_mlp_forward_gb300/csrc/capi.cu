@@ -2158,7 +2158,7 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
         return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
     }
     float* target_q = reinterpret_cast<float*>(base + p.target);
-    e = launch_head_target(cb(X), cb(W), targets, lse, T, h, V, target_q, st, &t_last_launches);
+    e = launch_head_target(dloss, cb(X), cb(W), targets, lse, T, h, V, target_q, scale, st, &t_last_launches);
     if (e != cudaSuccess) return fail_cuda(e);
     for (long long v = 0; v < V; v += p.width) {
         const int v0 = static_cast<int>(v);
@@ -2173,7 +2173,6 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
             g.target_q = target_q;
             g.targets = targets;
             g.vocab = V;
-            g.scale_out = v0 == 0 ? scale : nullptr;
             g.out_scale = scale;
             g.col0 = v0;
             g.epi_kb = kHeadEpiKb;

@@ -156,7 +156,6 @@ struct GemmArgs {
     const float *dloss, *lse;  // EPI_DLOGITS, [M]
     const float* target_q;     // EPI_DLOGITS, [M]: softmax - 1 at the row's target, from its fp32 logit
     int vocab;                 // EPI_DLOGITS: classes in all (a target behind them has no logit)
-    float* scale_out;          // EPI_DLOGITS: receives the largest |dloss|; null: *out_scale holds it
     int col0;                  // EPI_DLOGITS: vocabulary index of column 0
     int n_valid;               // EPI_DLOGITS: columns from here to N are stored as 0
     const float* out_scale;    // EPI_SCALE, EPI_DLOGITS
@@ -317,44 +316,6 @@ __device__ __forceinline__ float gelu_tanh_grad(float x) {
 // log2(e): exponentials are taken as 2^(log2(e) x), one multiply-add and one
 // ex2 per value.
 constexpr float kLog2e = 1.4426950408889634f;
-
-// The largest |dloss| of the tokens that count (1 where that is 0 or not
-// finite), taken by the `warps` epilogue warps of every CTA over all of them
-// while the first tile's products run (`place` + warp * `stride`: a float of
-// shared memory that is the warp's own).  The logits' gradients are divided by it, so that in
-// the usual case, one weight for all counted tokens, the weights are exactly 1
-// and the bf16 gradient rounds p - [v == y] itself, not its product with an
-// arbitrary factor; it multiplies the fp32 sums of dX and dW.
-__device__ __forceinline__ float head_scale(const float* dloss, const long long* targets, int T, int warps,
-                                            uint8_t* place, int stride) {
-    constexpr int kBatch = 32;  // a lane's loads in flight
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool share = T > 32 * kBatch;  // else each warp takes all by itself
-    const int first = share ? warp : 0, step = share ? warps : 1;
-    float s = 0.0f;
-    for (long long t0 = first * (32 * kBatch) + lane; t0 < T; t0 += step * (32 * kBatch)) {
-        float d[kBatch];
-        int sign[kBatch];  // the targets' upper halves
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const bool in = t0 + 32 * j < T;
-            d[j] = in ? __ldg(dloss + t0 + 32 * j) : 0.0f;
-            sign[j] = in ? __ldg(reinterpret_cast<const int*>(targets) + 2 * (t0 + 32 * j) + 1) : -1;
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (sign[j] >= 0) s = fmaxf(s, fabsf(d[j]));
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
-    if (share) {
-        if (lane == 0) *reinterpret_cast<volatile float*>(place + warp * stride) = s;
-        named_bar_sync(1, 32 * warps);
-        for (int w = 0; w < warps; ++w) s = fmaxf(s, *reinterpret_cast<volatile float*>(place + w * stride));
-        named_bar_sync(1, 32 * warps);
-    }
-    return s > 0.0f && s < INFINITY ? s : 1.0f;
-}
 
 // 32 consecutive bf16 values -> float; entries at or beyond `valid` read 0.
 __device__ __forceinline__ void load_bf16x32(const __nv_bfloat16* p, int valid, float (&v)[32]) {
@@ -750,14 +711,7 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
         uint32_t seq = 0;  // stores committed so far: selects the buffer
         int count = 0;
         float dloss_max = 1.0f;
-        if constexpr (EPI == EPI_DLOGITS) {
-            if (p.scale_out == nullptr) {
-                dloss_max = __ldg(p.out_scale);
-            } else {
-                dloss_max = head_scale(p.dloss, p.targets, p.M, EW, staging, 2 * EPI_BUF_BYTES);
-                if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale_out = dloss_max;
-            }
-        }
+        if constexpr (EPI == EPI_DLOGITS) dloss_max = __ldg(p.out_scale);
         for (int tile = unit; tile >= 0; ++count) {
             const TileCoord tc = decode_tile<G::TILE_M, G::TILE_N>(tile, p);
             const int acc = G::ACCS == 2 ? (count & 1) : 0;

@@ -249,6 +249,38 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// The largest |dloss| of the tokens that count (1 where that is 0 or not
+// finite), taken by one CTA over all of them.  The logits' gradients are
+// divided by it, so that in the usual case, one weight for all counted tokens,
+// the weights are exactly 1 and the bf16 gradient rounds p - [v == y] itself,
+// not its product with an arbitrary factor; it multiplies the fp32 sums of dX
+// and dW.
+__device__ __forceinline__ float dloss_scale(const float* __restrict__ dloss, const long long* __restrict__ targets,
+                                             int T) {
+    __shared__ float most[kThreads / 32];
+    constexpr int kBatch = 8;  // a thread's loads in flight
+    float s = 0.0f;
+    for (long long t0 = threadIdx.x; t0 < T; t0 += kBatch * kThreads) {
+        float d[kBatch];
+        int sign[kBatch];  // the targets' upper halves
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const long long t = t0 + j * kThreads;
+            d[j] = t < T ? __ldg(dloss + t) : 0.0f;
+            sign[j] = t < T ? __ldg(reinterpret_cast<const int*>(targets) + 2 * t + 1) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (sign[j] >= 0) s = fmaxf(s, fabsf(d[j]));  // (a NaN counts as 0)
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = s;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) s = fmaxf(s, most[w]);
+    return s > 0.0f && s < INFINITY ? s : 1.0f;
+}
+
 // q[t] = exp(z - lse[t]) - 1 for the logit z of token t's target, 0 where there
 // is none: what the backward pass has of it beside the other classes'
 // probabilities.  With the model sure of the target, z and lse are near equals,
@@ -256,17 +288,23 @@ __global__ void __launch_bounds__(kThreads)
 // logit of 20 from 20480 products -- would leave nothing of their difference
 // (the gradient of such a token came out some hundred times too large).  So z
 // is taken in fp32, as forward, and only the difference is rounded.
-// `rows` rows a CTA as in head_combine_kernel.
+// `rows` rows a CTA as in head_combine_kernel; CTA 0 takes the largest |dloss|.
 __global__ void __launch_bounds__(kThreads)
-    head_target_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
-                       const long long* __restrict__ targets, const float* __restrict__ lse, int T, int h, int V,
-                       int rows, float* __restrict__ q) {
+    head_target_kernel(const float* __restrict__ dloss, const __nv_bfloat16* __restrict__ X,
+                       const __nv_bfloat16* __restrict__ W, const long long* __restrict__ targets,
+                       const float* __restrict__ lse, int T, int h, int V, int rows, float* __restrict__ q,
+                       float* __restrict__ scale) {
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // X comes from the kernel before this one
+    if (blockIdx.x == 0) {
+        const float s = dloss_scale(dloss, targets, T);
+        if (threadIdx.x == 0) *scale = s;
+        return;
+    }
     __shared__ Two warp_dot[kThreads / 32];
     const int group = kThreads / rows;  // threads a row, 8..256
     const int r = threadIdx.x / group, sub = threadIdx.x % group;
-    const int row = blockIdx.x * rows + r;
+    const int row = (blockIdx.x - 1) * rows + r;
     const bool ok = row < T;
     const long long y = ok ? __ldg(targets + row) : -1;
     const bool in = y >= 0 && y < V;
@@ -463,12 +501,13 @@ cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n
                             where, n_parts, part_cols, X, W, targets, T, h, V, rows, loss, lse);
 }
 
-cudaError_t launch_head_target(const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets,
-                               const float* lse, int T, int h, int V, float* q, cudaStream_t st, int* launches) {
+cudaError_t launch_head_target(const float* dloss, const __nv_bfloat16* X, const __nv_bfloat16* W,
+                               const long long* targets, const float* lse, int T, int h, int V, float* q,
+                               float* scale, cudaStream_t st, int* launches) {
     const int rows = rows_a_cta(T);
     ++*launches;
-    return launch_dependent(head_target_kernel, dim3(blocks_of(T, rows)), dim3(kThreads), 0, st, X, W, targets, lse,
-                            T, h, V, rows, q);
+    return launch_dependent(head_target_kernel, dim3(1 + blocks_of(T, rows)), dim3(kThreads), 0, st, dloss, X, W,
+                            targets, lse, T, h, V, rows, q, scale);
 }
 
 cudaError_t launch_head_reduce(const float* P, int planes, long long count, const float* scale,

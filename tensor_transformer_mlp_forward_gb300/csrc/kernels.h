@@ -93,9 +93,10 @@ cudaError_t launch_head_combine(const float2* parts, const uint8_t* where, int n
                                 const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets, int T,
                                 int h, int V, float* loss, float* lse, cudaStream_t st, int* launches);
 // Backward: q[t] = exp(z - lse[t]) - 1 of token t's target (0 without one), from
-// its logit in fp32.
-cudaError_t launch_head_target(const __nv_bfloat16* X, const __nv_bfloat16* W, const long long* targets,
-                               const float* lse, int T, int h, int V, float* q, cudaStream_t st, int* launches);
+// its logit in fp32; *scale, the largest |dloss| of the tokens that count.
+cudaError_t launch_head_target(const float* dloss, const __nv_bfloat16* X, const __nv_bfloat16* W,
+                               const long long* targets, const float* lse, int T, int h, int V, float* q,
+                               float* scale, cudaStream_t st, int* launches);
 // The head for few tokens (head_few.cu): head_few(T) says whether T are few.
 // Forward: head_few_parts(V) {max, sum} parts a token.  Backward: dz and dzt
 // (16 head_few_ldz(V) values each), *scale, err (16 values), dW, and dX as

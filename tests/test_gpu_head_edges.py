@@ -60,3 +60,45 @@ def test_gradients_of_sure_tokens(T, h, V):
                                              (dW, e.T @ np.abs(X), a.T @ np.abs(X), dz.T @ X, T, "dW")):
         bound = (1 + u) * (ez_out + (n / 16 + 80) * 2.0 ** -23 * sums) + u * np.abs(want) + 1e-37
         ref.within(got, want, bound, name)
+
+
+def test_two_calls_at_once_from_dirty_workspaces():
+    """Rows wide enough for grids whose CTAs take one another's tiles over
+    (12288 values and more), two calls side by side on two streams with
+    workspaces full of NaN: the largest weight and every other intermediate
+    come from the call itself, whichever of its CTAs run first."""
+    T, h, V = 300, 12296, 6001
+    cs = [{k: v.cuda() for k, v in lean_on(T, h, V, s, 4.0).items()} for s in (1, 2)]
+    lses = [binding.tp_head_loss_forward(c["X"], c["W"], c["y"])[1] for c in cs]
+    want = [binding.tp_head_loss_backward(c["dloss"], c["X"], c["W"], c["y"], s) for c, s in zip(cs, lses)]
+    n = binding.head_loss_backward_workspace_bytes(T, h, V)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        ws = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _ in cs]
+        torch.cuda.synchronize()
+        got = [binding.tp_head_loss_backward(c["dloss"], c["X"], c["W"], c["y"], s, workspace=w, stream=st)
+               for c, s, w, st in zip(cs, lses, ws, streams)]
+        torch.cuda.synchronize()
+        assert binding.device_status() == 0
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("T", [17, 257, 2049, 9000])
+def test_the_largest_weight_may_be_any_token_s(T):
+    """One weight far above the others, at the first, last or a middle token,
+    and a larger one at a token that does not count: the same gradients as
+    with all weights and results scaled by a power of two, bit for bit."""
+    h, V = 64, 300
+    c = {k: v.cuda() for k, v in lean_on(T, h, V, T, 4.0).items()}
+    _, lse = binding.tp_head_loss_forward(c["X"], c["W"], c["y"])
+    for at in (0, T // 2, T - 1):
+        y = c["y"].clone()
+        y[at] = 7
+        y[(at + 5) % T] = -1
+        dl = c["dloss"].clone()
+        dl[at], dl[(at + 5) % T] = 2.0, 1e9
+        want = binding.tp_head_loss_backward(dl, c["X"], c["W"], y, lse)
+        got = binding.tp_head_loss_backward(dl * 1024.0, c["X"], c["W"], y, lse)
+        for a, b in zip(got, want):
+            assert torch.equal(a.float(), 1024.0 * b.float()) and bool(a.float().abs().max() > 0)
