@@ -880,10 +880,11 @@ cudaError_t forward(const void* x_, const void* gamma_, const void* beta_, int T
 struct NormPlan {
     int units;  // CTAs, or clusters of `cl` CTAs
     int W, cl, cols, stages, buf_bytes, threads, smem;
-    int room;  // the most shared memory that a plan of this many threads takes
+    int room;  // the most shared memory that a plan of this many CTAs an SM takes
 };
 
-constexpr int kSmemMost = 227 * 1024;
+// A CTA's share of an SM's shared memory beside the static arrays.
+constexpr int norm_room(int per_sm) { return 227 * 1024 / per_sm - (per_sm == 1 ? 5 : 4) * 1024; }
 
 NormPlan norm_plan(int T, int h, int elem) {
     NormPlan p{};
@@ -914,7 +915,7 @@ NormPlan norm_plan(int T, int h, int elem) {
     // a block of rows and what its first and last granule hold besides
     p.buf_bytes = (static_cast<int>((static_cast<long long>(R) * U * p.cols * elem + 15) / 16) + 1) * 16;
     const int per_sm = std::min(kNormMaxPerSm, 16 / (R * p.W));
-    p.room = kSmemMost / per_sm - (per_sm == 1 ? 5 : 4) * 1024;  // beside the static arrays
+    p.room = norm_room(per_sm);
     const int blocks = ceil_div(T, R * U), units = kSms * per_sm / p.cl;
     p.stages = std::min(kNormMaxStages, p.room / (2 * p.buf_bytes));
     // the meeting place of the groups' sums: 16 values a thread and tensor
@@ -934,7 +935,11 @@ cudaError_t backward_ring(const NormPlan& p, const T* dy, const T* x, const T* g
     auto kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, false>;
     if constexpr (NV * Piece<T, VEC>::N == 16)
         if (p.cl > 1) kern = norm_backward_ring_kernel<T, VEC, NV, NT, MIN_CTAS, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.room);
+    // The attribute is the kernel's, not the launch's: the same from every call (the
+    // most that any plan of this kernel takes), so that a call of another
+    // width in another thread takes nothing from this one.
+    static_assert(MIN_CTAS * (NT / 32) == 16, "a plan has at least MIN_CTAS of these CTAs an SM");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, norm_room(MIN_CTAS));
     if (e != cudaSuccess) return e;
     const NormBackwardArgs a{T_, h, p.W, p.stages, p.cl, p.cols, p.buf_bytes, status};
     if (p.cl == 1) {
