@@ -1599,9 +1599,6 @@ TPMLP_API int tp_mlp_backward_dropout(const tpmlp_bf16* dY, const tpmlp_bf16* X,
 
 // ----------------------------------------------- residual add + LayerNorm
 
-// LayerNorm rows are staged in shared memory as fp32.
-constexpr int kLnMaxHidden = 49152;
-
 static int check_ln(int T, int h, float eps) {
     if (T < 0 || h < 8 || h % 8 != 0 || h > kLnMaxHidden || !(eps > 0.0f)) return TPMLP_ERR_SHAPE;
     return TPMLP_OK;

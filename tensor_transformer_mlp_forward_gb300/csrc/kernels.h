@@ -145,8 +145,10 @@ cudaError_t launch_colsum(const __nv_bfloat16* G, int T, int n, float* db, float
 cudaError_t launch_rowsum_f32(const float* P, int rows, int n, float* out, cudaStream_t st,
                               int* launches);
 
-// Residual add + LayerNorm (layernorm.cu).  `launches` is incremented per
-// kernel launched.
+// Residual add + LayerNorm (layernorm.cu), rows of at most kLnMaxHidden values
+// (staged in shared memory as fp32).  `launches` is incremented per kernel
+// launched.
+constexpr int kLnMaxHidden = 49152;
 cudaError_t launch_ln_forward(const __nv_bfloat16* a, const __nv_bfloat16* r,
                               const __nv_bfloat16* gamma, const __nv_bfloat16* beta, int T, int h,
                               float eps, __nv_bfloat16* X, __nv_bfloat16* s, float* mean,

@@ -335,9 +335,11 @@ cudaError_t launch_ln_forward(const __nv_bfloat16* a, const __nv_bfloat16* r,
         });
     }
     const size_t smem = sizeof(float) * static_cast<size_t>(h);
+    // the kernel's limit, the same from every call: another thread's call of
+    // another width must not lower it between this line and the launch
     cudaError_t e = cudaFuncSetAttribute(ln_forward_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(sizeof(float)) * kLnMaxHidden);
     if (e != cudaSuccess) return e;
     ln_forward_kernel<<<T, ln_threads(h), smem, st>>>(a, r, gamma, beta, h, eps, X, s, mean, rstd);
     return cudaGetLastError();

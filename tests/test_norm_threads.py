@@ -41,3 +41,10 @@ def test_rejects_bad_arguments(exe):
 def test_two_threads_of_other_widths(exe, widths):
     r = subprocess.run([exe, "backward", "100000", *map(str, widths)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.gpu
+def test_two_threads_of_residual_norms(exe):
+    # rows staged in shared memory, of different sizes
+    r = subprocess.run([exe, "residual", "100000", "32776", "49152"], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
