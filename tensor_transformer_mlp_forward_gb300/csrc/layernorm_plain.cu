@@ -573,12 +573,11 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
         }
         if (row < rows) {
             const bool second = U == 1 || row + 1 < rows;
-            float mg[U], k2[U];
+            float mg[U], mgx[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float rs = st[0].v[u].y;
-                mg[u] = m[u].x * inv_h;                   // mean(g)
-                k2[u] = rs * rs * rs * (m[u].y * inv_h);  // rstd^2 mean(g xhat)
+                mg[u] = m[u].x * inv_h;                  // mean(g)
+                mgx[u] = m[u].y * inv_h * st[0].v[u].y;  // mean(g xhat)
             }
             const T* sx = row_at(stage, skip);
             const T* sdy = dy_of(sx);
@@ -594,10 +593,12 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
 #pragma unroll
                     for (int j = 0; j < PAIRS; ++j) {
                         const float2 d = pair_of(pd, j);
-                        const float2 xc = add2(pair_of(px, j), both(-mu));
+                        // one rstd a factor: its powers leave the range of fp32 (rows of
+                        // 1e13, or eps below 1e-25) where the products do not
+                        const float2 xhat = mul2(add2(pair_of(px, j), both(-mu)), both(rs));
                         const float2 gj = product<VEC>(d, pair_of(kg[k], j));
-                        set_pair(o, j, fma2(both(rs), add2(gj, both(-mg[u])), mul2(xc, both(-k2[u]))));
-                        acc_g[k * PAIRS + j] = fma2(mul2(d, both(rs)), xc, acc_g[k * PAIRS + j]);
+                        set_pair(o, j, mul2(both(rs), fma2(xhat, both(-mgx[u]), add2(gj, both(-mg[u])))));
+                        acc_g[k * PAIRS + j] = fma2(d, xhat, acc_g[k * PAIRS + j]);
                         acc_b[k * PAIRS + j] = add2(acc_b[k * PAIRS + j], d);
                     }
                     store_piece<T, VEC>(out + u * p.h, o, k, group, sub, h);
