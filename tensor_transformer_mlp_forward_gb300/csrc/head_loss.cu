@@ -108,13 +108,23 @@ __device__ __forceinline__ void finish_row(const Row& r, Two log_others, int V, 
     }
 }
 
+// A class whose share of a row's sum is w / s (w: its term beside the
+// largest's, s: the sum, log s: near enough `log_others`) puts that share of its
+// logit's error into lse.  A tensor-core logit is off by about h |z| 2^-30:
+// whether that is more than 2^-20 of lse.
+__device__ __forceinline__ bool too_coarse(float z, float w, float s, float log_others, int h) {
+    return static_cast<float>(h) * fabsf(z) * w > 1024.0f * s * fmaxf(1.0f, fabsf(log_others));
+}
+
 // A CTA takes `rows` rows (a power of two up to 32), kThreads / rows threads
 // a row: they join the row's column parts and take the dot product of the
 // target's logit in fp32.  (A tensor-core accumulator is cut toward zero at
 // every step of 16: a logit of 20 from a row of 20480 values comes out 5e-4
-// small.)  Where one other class makes most of a row's sum -- a model sure of
-// the wrong token, or a token that does not count -- its logit is taken again
-// like that: the GEMM says which 16 columns hold it.
+// small.)  Where other classes make much of a row's sum -- a model sure of
+// the wrong token or torn between a few, or a token that does not count --
+// their logits are taken again like that, the largest of each column part that
+// has one: the GEMM says which 16 columns hold it.  (A second large class in
+// the same part keeps its accumulator's error, that share of h |z| 2^-30.)
 __global__ void __launch_bounds__(kThreads)
     head_combine_kernel(const float2* __restrict__ parts, const uint8_t* __restrict__ where, int n_parts,
                         int part_cols, const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
@@ -123,10 +133,9 @@ __global__ void __launch_bounds__(kThreads)
     pdl_launch_dependents();  // the next kernel may begin its launch
     pdl_wait();               // the parts come from the kernel before this one
     __shared__ float2 warp_part[kThreads / 32];
-    __shared__ int warp_from[kThreads / 32];
     __shared__ Two warp_dot[kThreads / 32];
-    __shared__ Row again[32];  // rows whose largest logit is taken again
-    __shared__ int again_col[32];
+    __shared__ Row again[32];  // rows whose largest logits are taken again
+    __shared__ bool is_again[32];
     const int group = kThreads / rows;  // threads a row, 8..256
     const int r = threadIdx.x / group, sub = threadIdx.x % group;
     const int row = blockIdx.x * rows + r;
@@ -134,7 +143,6 @@ __global__ void __launch_bounds__(kThreads)
     const long long y = ok ? __ldg(targets + row) : -1;
     const float2 none = make_float2(-INFINITY, 0.0f);
     float2 acc = none;
-    int from = 0;  // the part that holds the largest logit
     float dot = 0.0f;
     // The loads come in batches, the first parts' before the dot product, whose
     // addresses wait for the target: one latency after the other was 21 us at
@@ -153,10 +161,7 @@ __global__ void __launch_bounds__(kThreads)
         dot = dot_rows(X + static_cast<long long>(row) * h, W + y * h, h >> 3, sub, group);
     for (int i = sub;;) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (batch[j].x > acc.x) from = i + j * group;
-            acc = join(acc, batch[j]);
-        }
+        for (int j = 0; j < kBatch; ++j) acc = join(acc, batch[j]);
         i += kBatch * group;
         if (i >= n_parts) break;
         load_parts(i);
@@ -169,8 +174,6 @@ __global__ void __launch_bounds__(kThreads)
         float2 o;
         o.x = __shfl_xor_sync(0xFFFFFFFFu, acc.x, off);
         o.y = __shfl_xor_sync(0xFFFFFFFFu, acc.y, off);
-        const int f = __shfl_xor_sync(0xFFFFFFFFu, from, off);
-        if (o.x > acc.x || (o.x == acc.x && f < from)) from = f;
         acc = join(acc, o);
         Two l;
         l.hi = __shfl_xor_sync(0xFFFFFFFFu, logit.hi, off);
@@ -180,15 +183,12 @@ __global__ void __launch_bounds__(kThreads)
     if (group > 32) {
         if ((threadIdx.x & 31) == 0) {
             warp_part[threadIdx.x >> 5] = acc;
-            warp_from[threadIdx.x >> 5] = from;
             warp_dot[threadIdx.x >> 5] = logit;
         }
         __syncthreads();
         if (sub == 0) {
             for (int w = 1; w < group / 32; ++w) {
-                const float2 o = warp_part[(threadIdx.x >> 5) + w];
-                if (o.x > acc.x) from = warp_from[(threadIdx.x >> 5) + w];
-                acc = join(acc, o);
+                acc = join(acc, warp_part[(threadIdx.x >> 5) + w]);
                 logit = add(logit, warp_dot[(threadIdx.x >> 5) + w]);
             }
         }
@@ -197,55 +197,70 @@ __global__ void __launch_bounds__(kThreads)
     if (sub == 0 && ok) {
         const Row mine{acc, logit, y < 0 ? -1 : static_cast<int>(min(y, static_cast<long long>(V)))};
         const Two others = log_sum(acc.x, acc.y);
-        // The error of the largest logit, about h |m| 2^-30, times its share 1 / s
-        // of the sum: taken again where that is more than 2^-20 of lse.  (Not
-        // where the target outweighs the sum, so that it does not matter.)
+        // (Not where the target outweighs the sum, so that it does not matter.)
         const bool outweighed = y >= 0 && y < V && logit.hi > others.hi + 20.0f;
-        redo = where != nullptr && !outweighed && acc.y < 64.0f &&
-               static_cast<float>(h) * fabsf(acc.x) > 1024.0f * acc.y * fmaxf(1.0f, fabsf(others.hi));
-        if (redo) {
+        redo = where != nullptr && !outweighed && acc.y < 64.0f && too_coarse(acc.x, 1.0f, acc.y, others.hi, h);
+        if (redo)
             again[r] = mine;
-            again_col[r] = from * part_cols + 16 * where[static_cast<long long>(from) * T + row];
-        } else {
-            again_col[r] = -1;
+        else
             finish_row(mine, others, V, loss + row, lse + row);
-        }
     }
+    if (sub == 0) is_again[r] = redo;
     if (!__syncthreads_or(redo)) return;
     __shared__ Two z[16];
+    __shared__ unsigned coarse[kThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int k = 0; k < rows; ++k) {
+        if (!is_again[k]) continue;  // the same in all threads
         const int at = blockIdx.x * rows + k;
-        if (at >= T || again_col[k] < 0) continue;  // the same in all threads
+        const Row q = again[k];
+        const Two log_others = log_sum(q.others.x, q.others.y);
         const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<long long>(at) * h);
-        for (int c = warp; c < 16; c += kThreads / 32) {
-            const int v = again_col[k] + c;
-            const bool in = v < V && v != again[k].y;
-            const uint4* w = reinterpret_cast<const uint4*>(W + static_cast<long long>(in ? v : 0) * h);
-            float d = 0.0f;
+        float more = 0.0f;  // thread 0: what the sum lacks, part by part
+        for (int first = 0; first < n_parts; first += kThreads) {
+            const int mine = first + threadIdx.x;
+            const float m = mine < n_parts ? __ldg(parts + static_cast<long long>(mine) * T + at).x : -INFINITY;
+            const float w = ex2_approx((m - q.others.x) * kLog2e);
+            const unsigned bits = __ballot_sync(0xFFFFFFFFu, m > -INFINITY && too_coarse(m, w, q.others.y, log_others.hi, h));
+            if (lane == 0) coarse[warp] = bits;
+            __syncthreads();
+            for (int i = 0; i < kThreads / 32; ++i) {
+                for (unsigned left = coarse[i]; left != 0; left &= left - 1) {
+                    const int part = first + 32 * i + __ffs(left) - 1;
+                    const long long p = static_cast<long long>(part) * T + at;
+                    const float was = __ldg(parts + p).x;
+                    const int col = part * part_cols + 16 * __ldg(where + p);
+                    for (int c = warp; c < 16; c += kThreads / 32) {
+                        const int v = col + c;
+                        const bool in = v < V && v != q.y;
+                        const uint4* w8 = reinterpret_cast<const uint4*>(W + static_cast<long long>(in ? v : 0) * h);
+                        float d = 0.0f;
 #pragma unroll 4
-            for (int i = lane; i < (h >> 3); i += 32) d += dot8(__ldg(x + i), __ldg(w + i));
-            Two sum{d, 0.0f};
+                        for (int j = lane; j < (h >> 3); j += 32) d += dot8(__ldg(x + j), __ldg(w8 + j));
+                        Two sum{d, 0.0f};
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) {
-                Two o;
-                o.hi = __shfl_xor_sync(0xFFFFFFFFu, sum.hi, off);
-                o.lo = __shfl_xor_sync(0xFFFFFFFFu, sum.lo, off);
-                sum = add(sum, o);
+                        for (int off = 16; off >= 1; off >>= 1) {
+                            Two o;
+                            o.hi = __shfl_xor_sync(0xFFFFFFFFu, sum.hi, off);
+                            o.lo = __shfl_xor_sync(0xFFFFFFFFu, sum.lo, off);
+                            sum = add(sum, o);
+                        }
+                        if (lane == 0) z[c] = in ? sum : Two{-INFINITY, 0.0f};
+                    }
+                    __syncthreads();
+                    if (threadIdx.x == 0) {
+                        Two best = z[0];
+                        for (int c = 1; c < 16; ++c)
+                            if (z[c].hi > best.hi) best = z[c];
+                        more += ex2_approx((was - q.others.x) * kLog2e) * expm1f((best.hi - was) + best.lo);
+                    }
+                    __syncthreads();
+                }
             }
-            if (lane == 0) z[c] = in ? sum : Two{-INFINITY, 0.0f};
+            __syncthreads();  // coarse[] is read
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const Row q = again[k];
-            Two best = z[0];
-            for (int c = 1; c < 16; ++c)
-                if (z[c].hi > best.hi) best = z[c];
-            // its term of the sum was 1
-            const float e = expf((best.hi - q.others.x) + best.lo);
-            finish_row(q, log_sum(q.others.x, fmaxf(q.others.y - 1.0f, 0.0f) + e), V, loss + at, lse + at);
-        }
-        __syncthreads();
+        if (threadIdx.x == 0)
+            finish_row(q, log_sum(q.others.x, q.others.y + more), V, loss + at, lse + at);
     }
 }
 

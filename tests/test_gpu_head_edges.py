@@ -102,3 +102,48 @@ def test_the_largest_weight_may_be_any_token_s(T):
         got = binding.tp_head_loss_backward(dl * 1024.0, c["X"], c["W"], y, lse)
         for a, b in zip(got, want):
             assert torch.equal(a.float(), 1024.0 * b.float()) and bool(a.float().abs().max() > 0)
+
+
+@pytest.mark.parametrize("T,h,V,classes", [(40, 20480, 1500, (0, 700)), (90, 20480, 1500, (0, 300, 900)),
+                                           (700, 8192, 1501, (0, 520)), (6200, 4096, 600, (0, 300)),
+                                           (12300, 4096, 600, (0,)), (12200, 2048, 1027, (5,))])
+def test_rows_torn_between_classes(T, h, V, classes):
+    """Rows with equal logits of about 20 at a few classes far apart, none of
+    them the target (every third row counts, every third counts for one of
+    them); up to 32 rows a CTA.  All of these logits are taken again in fp32.
+
+    A lane adds at most 9 h / 256 rounded terms to partial sums below 1 (20 of
+    32 lanes and the noise): at most 720 roundings of 2^-25 in 32 lanes, in
+    squares 2.6e-6 for h = 20480, six times that is 1.6e-5 or 2^-20.3 of a
+    logit of 20.  lse's own roundings and the 2^x of the sum: 2^-21 of it.  The
+    others' logits shift by less than 2^-18 of their size, 1, times their share,
+    below 2^-8: together below 2^-19 relative."""
+    g = torch.Generator().manual_seed(T + h)
+    W = (torch.randn(V, h, generator=g) * 0.64 / h ** 0.5).to(torch.bfloat16)
+    base = torch.randint(0, V - max(classes) - 1, (T,), generator=g)
+    # W's rows are nearly orthogonal: their pseudo-inverse gives each its logit
+    cols = base[:, None] + torch.tensor(classes)
+    S = W[cols].float()  # [T, classes, h]
+    gram = S @ S.transpose(1, 2)
+    X = torch.randn(T, h, generator=g)
+    X = X + (torch.linalg.solve(gram, 20.0 - (S @ X[:, :, None])).transpose(1, 2) @ S)[:, 0]
+    kind = torch.arange(T) % 3
+    y = torch.where(kind == 0, torch.full_like(base, -1), torch.where(kind == 1, base, base + max(classes) + 1))
+    d = [t.cuda() for t in (X.to(torch.bfloat16), W, y)]
+    loss, lse = binding.tp_head_loss_forward(*d)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    z = d[0].double() @ d[1].double().T
+    want = torch.logsumexp(z, 1)
+    # the share of the classes: nothing else matters
+    assert float(torch.exp(z.gather(1, cols.cuda()) - want[:, None]).sum(1).min()) > 1 - 2.0 ** -8
+    off = float(((lse.double() - want) / want).abs().max())
+    assert off <= 2.0 ** -19, off
+    rest = z.clone()
+    counted = d[2] >= 0
+    at = d[2].clamp(min=0)[:, None]
+    zt = z.gather(1, at)[:, 0]
+    rest.scatter_(1, at, torch.where(counted, torch.full_like(zt, -torch.inf), zt)[:, None])
+    want_loss = torch.where(counted, torch.nn.functional.softplus(torch.logsumexp(rest, 1) - zt), torch.zeros_like(zt))
+    off = float((loss.double() - want_loss).abs().max() / want.max())
+    assert off <= 2.0 ** -19, off
