@@ -2057,8 +2057,9 @@ HeadPlan head_layout(int T, int h, int V, int width, int splits) {
 
 int round_up(long long x, long long m) { return static_cast<int>(cdiv(x, m) * m); }
 
-// The few-token form: the whole vocabulary at once, dz in two layouts of 16
-// tokens, dX's planes one for each range of the vocabulary.
+// The few-token form: the whole vocabulary at once, dX's planes one for each
+// range of it; rows too wide for the fused kernel also keep dz, in two layouts
+// of 16 tokens.
 HeadPlan head_plan_few(int T, int h, int V) {
     HeadPlan p;
     p.width = head_few_ldz(V);
@@ -2067,7 +2068,8 @@ HeadPlan head_plan_few(int T, int h, int V) {
     p.scale = p.target = 0;  // no target_q: the kernels mend the target's dz themselves
     p.plane = 256;
     p.dz = align256(p.plane + sizeof(float) * static_cast<size_t>(p.splits) * T * h);
-    p.total = align256(p.dz + 2 * sizeof(uint16_t) * 16 * static_cast<size_t>(p.width));
+    const size_t dz_values = head_few_box_rows(h) ? 0 : 2 * 16 * static_cast<size_t>(p.width);
+    p.total = align256(p.dz + sizeof(uint16_t) * dz_values);
     return p;
 }
 
@@ -2147,7 +2149,8 @@ int head_backward(const float* dloss, const tpmlp_bf16* X, const tpmlp_bf16* W,
             if (int rc = make_map(&tm, W, V, h, 1, ON_CONTIG, box_rows)) return rc;
         e = launch_head_few_backward(dloss, cb(X), cb(W), targets, lse, T, h, V, z,
                                      z + 16 * static_cast<size_t>(p.width), scale, scale + 16, plane,
-                                     reinterpret_cast<__nv_bfloat16*>(dW), &tm, d.status, st, &t_last_launches);
+                                     reinterpret_cast<__nv_bfloat16*>(dW), box_rows ? &tm : nullptr, d.status, st,
+                                     &t_last_launches);
         if (e == cudaSuccess)
             e = launch_head_few_finish(plane, p.splits, scale, scale + 16, dloss, lse, targets, cb(X), cb(W), T, h, V,
                                        reinterpret_cast<__nv_bfloat16*>(dX), reinterpret_cast<__nv_bfloat16*>(dW),
