@@ -654,6 +654,13 @@ def _dtype_of(x, name: str) -> int:
     return code
 
 
+_MOST = 1 << 30  # rows, columns and classes of the calls below; ctypes would cut a larger int to 32 bits
+
+
+def _too_large(**sizes):
+    raise ValueError(f"at most 2^30 each: {', '.join(f'{k} = {v}' for k, v in sizes.items())}")
+
+
 _F32 = torch.float32
 _BF16 = torch.bfloat16
 _I64 = torch.int64
@@ -671,6 +678,8 @@ def tp_ln_forward(x, gamma, beta, eps: float = 1e-5, y=None, mean=None, rstd=Non
     """y, mean, rstd of y = LayerNorm(x) * gamma + beta, x [T, h] in bfloat16,
     float16 or float32 (mean and rstd [T] are float32)."""
     T, h = shape = x.shape
+    if T > _MOST or h > _MOST:
+        _too_large(T=T, h=h)
     dt, d = x.dtype, _device_of(x)
     code = _dtype_of(x, "x")
     xp = _in(x, "x", shape, dt, d)
@@ -701,6 +710,8 @@ def tp_ln_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, p
                    stream=None):
     """dx (of x's type), dgamma, dbeta (float32) of tp_ln_forward."""
     T, h = shape = x.shape
+    if T > _MOST or h > _MOST:
+        _too_large(T=T, h=h)
     dt, d = x.dtype, _device_of(x)
     code = _dtype_of(x, "x")
     xp = _in(x, "x", shape, dt, d)
@@ -743,6 +754,8 @@ def tp_head_loss_forward(X, W, targets, loss=None, lse=None, workspace=None, str
     h] bfloat16; the logits are not stored."""
     T, h = X.shape
     V, d = W.shape[0], _device_of(X)
+    if T > _MOST or h > _MOST or V > _MOST:
+        _too_large(T=T, h=h, V=V)
     xp, wp = _in(X, "X", (T, h), _BF16, d), _in(W, "W", (V, h), _BF16, d)
     tp = _in(targets, "targets", (T,), _I64, d)
     with _on(stream):
@@ -769,12 +782,16 @@ def tp_head_loss_forward(X, W, targets, loss=None, lse=None, workspace=None, str
 
 def head_loss_backward_workspace_bytes(T: int, h: int, V: int) -> int:
     """Workspace with which tp_head_loss_backward takes its widest pieces."""
+    if T > _MOST or h > _MOST or V > _MOST:
+        _too_large(T=T, h=h, V=V)
     return int(lib().tp_head_loss_backward_workspace_bytes(T, h, V))
 
 
 def head_loss_backward_min_workspace_bytes(T: int, h: int, V: int) -> int:
     """The least workspace tp_head_loss_backward runs with (the vocabulary in
     pieces of 256 columns)."""
+    if T > _MOST or h > _MOST or V > _MOST:
+        _too_large(T=T, h=h, V=V)
     return int(lib().tp_head_loss_backward_min_workspace_bytes(T, h, V))
 
 
@@ -783,6 +800,8 @@ def tp_head_loss_backward(dloss, X, W, targets, lse, dX=None, dW=None, workspace
     (float32) and the forward pass's lse."""
     T, h = X.shape
     V, d = W.shape[0], _device_of(X)
+    if T > _MOST or h > _MOST or V > _MOST:
+        _too_large(T=T, h=h, V=V)
     xp, wp = _in(X, "X", (T, h), _BF16, d), _in(W, "W", (V, h), _BF16, d)
     dp, tp = _in(dloss, "dloss", (T,), _F32, d), _in(targets, "targets", (T,), _I64, d)
     sp = _in(lse, "lse", (T,), _F32, d)

@@ -2,6 +2,7 @@
 of their ranges, on a host without a GPU."""
 
 import pytest
+import torch
 
 from tensor_transformer_mlp_forward_gb300 import binding, build
 
@@ -23,3 +24,25 @@ def test_few_tokens_keep_no_logits_where_one_kernel_does_all(L, T):
         assert L.tp_head_loss_backward_min_workspace_bytes(T, h, 50257) == sizes[50257]
     # wider rows keep the logits' gradient of 16 tokens twice
     assert L.tp_head_loss_backward_workspace_bytes(T, 1032, 50257) >= 2 * 2 * 16 * 50257
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """A row count that 32 bits cut to another (2^32 + 4 to 4) is no call of four
+    rows.  Tensors without memory: their shapes are answered first."""
+    n = (1 << 32) + 4
+    m = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    for T, h in ((n, 1), (1 << 31, 1), ((1 << 30) + 1, 1), (1, n)):
+        x, p, stat = m(T, h), m(h), m(T, dtype=torch.float32)
+        with pytest.raises(ValueError, match="at most 2.30"):
+            binding.tp_ln_forward(x, p, p)
+        with pytest.raises(ValueError, match="at most 2.30"):
+            binding.tp_ln_backward(x, x, p, stat, stat)
+    for T, h, V in ((n, 8, 5), (4, n + 4, 5), (4, 8, n)):
+        X, W, y, f = m(T, h), m(V, h), m(T, dtype=torch.int64), m(T, dtype=torch.float32)
+        with pytest.raises(ValueError, match="at most 2.30"):
+            binding.tp_head_loss_forward(X, W, y)
+        with pytest.raises(ValueError, match="at most 2.30"):
+            binding.tp_head_loss_backward(f, X, W, y, f)
+        for size in (binding.head_loss_backward_workspace_bytes, binding.head_loss_backward_min_workspace_bytes):
+            with pytest.raises(ValueError, match="at most 2.30"):
+                size(T, h, V)
