@@ -365,8 +365,8 @@ int tp_ln_backward(const void* dy, const void* x, const void* gamma, const float
  * (loss 0, no gradient; its lse is still written).  A target >= V has no
  * logit: its loss is NaN, and so are the gradients it reaches.
  * X and W must be finite (a row of X that does not count included).
- * Rules: 0 <= T <= 2^30, h >= 8, h % 8 == 0, 1 <= V <= 2^30 (any V).  X, W, dX, dW and
- * the workspace are 16-byte aligned, targets 8-byte, the rest 4-byte. */
+ * Rules: 0 <= T <= 2^30, 8 <= h <= 2^30, h % 8 == 0, 1 <= V <= 2^30 (any V).  X, W, dX,
+ * dW and the workspace are 16-byte aligned, targets 8-byte, the rest 4-byte. */
 
 /* Bytes of scratch tp_head_loss_forward needs (the row statistics of each
  * tile of the vocabulary: at most 18 T max(304, ceil(V/256))). */

@@ -1992,7 +1992,8 @@ namespace tpmlp {
 namespace {
 
 int check_head(int T, int h, int V) {
-    if (T < 0 || T > (1 << 30) || h < 8 || h % 8 != 0 || V < 1 || V > (1 << 30)) return TPMLP_ERR_SHAPE;
+    if (T < 0 || T > (1 << 30) || h < 8 || h > (1 << 30) || h % 8 != 0 || V < 1 || V > (1 << 30))
+        return TPMLP_ERR_SHAPE;
     if (cdiv(T, BM) * cdiv(V, BN) >= (1LL << 31)) return TPMLP_ERR_SHAPE;
     return TPMLP_OK;
 }

@@ -26,6 +26,22 @@ def test_few_tokens_keep_no_logits_where_one_kernel_does_all(L, T):
     assert L.tp_head_loss_backward_workspace_bytes(T, 1032, 50257) >= 2 * 2 * 16 * 50257
 
 
+def test_rows_wider_than_the_kernels_count(L):
+    """h = 2^31 - 8: a column counter behind the row's end would pass 2^31 (the
+    few-token kernels would see no column at all).  2^30 is the widest."""
+    import ctypes
+
+    P, N = ctypes.c_void_p(0x10000), None
+    big = ctypes.c_size_t(1 << 62)
+    for h in ((1 << 31) - 8, (1 << 30) + 8):
+        assert L.tp_head_loss_forward(P, P, P, 1, h, 5, P, P, P, big, N) == binding.TPMLP_ERR_SHAPE
+        assert L.tp_head_loss_backward(P, P, P, P, P, 1, h, 5, P, P, P, big, N) == binding.TPMLP_ERR_SHAPE
+        assert L.tp_head_loss_forward_workspace_bytes(1, h, 5) == 0
+        assert L.tp_head_loss_backward_workspace_bytes(1, h, 5) == 0
+    assert L.tp_head_loss_forward_workspace_bytes(1, 1 << 30, 5) > 0
+    assert L.tp_head_loss_backward_workspace_bytes(1, 1 << 30, 5) > 0
+
+
 def test_sizes_beyond_32_bits_are_refused():
     """A row count that 32 bits cut to another (2^32 + 4 to 4) is no call of four
     rows.  Tensors without memory: their shapes are answered first."""
