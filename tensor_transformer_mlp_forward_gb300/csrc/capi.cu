@@ -1041,23 +1041,31 @@ int bias_grad(const tpmlp_bf16* G, int T, int n, float* db, float* partial, cuda
 
 // ------------------------------------------------------ bounded-wait check
 
+// Nothing ever arrives on `bar`: each of the kernels' waits must give up by
+// itself, after its time or its number of polls, and one whose neighbour has
+// given up must see that.  The status word is written when all three have.
 __global__ void wait_selftest_kernel(int* status, unsigned long long limit_ns) {
     __shared__ uint64_t bar;
+    __shared__ uint32_t abort_flag[2];
+    __shared__ int code[2];
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
+        abort_flag[0] = abort_flag[1] = 0u;
+        code[0] = code[1] = 0;
         fence_mbar_init();
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        // Nothing ever arrives on `bar`: the wait must give up by itself.
-        const unsigned long long t0 = global_ns();
-        while (!mbar_try_wait(&bar, 0)) {
-            if (global_ns() - t0 > limit_ns) {
-                atomicExch(status, kStatusTimeout);
-                break;
-            }
-        }
-    }
+    const int warp = threadIdx.x >> 5;
+    bool ok = true;
+    if (warp == 0)
+        ok = warp_wait_bounded(&bar, 0, &abort_flag[0], &code[0], 0, limit_ns);
+    else if (warp == 1)
+        ok = warp_wait_bounded<true>(&bar, 0, &abort_flag[0], &code[0]);
+    else
+        warp_wait_polls(&bar, 0, &abort_flag[1], &code[1], [&] { ok = false; }, static_cast<int>(limit_ns / kPollNs));
+    const bool none = !__syncthreads_or(ok);
+    if (threadIdx.x == 0 && none && code[0] == kStatusTimeout && code[1] == kStatusTimeout)
+        atomicExch(status, kStatusTimeout);
 }
 
 size_t dgelu_partial_floats(int T, int F) {
@@ -2346,7 +2354,7 @@ TPMLP_API int tpmlp_selftest_bounded_wait(int timeout_us, void* stream) {
     if (timeout_us < 1 || timeout_us > 1000000) return TPMLP_ERR_SHAPE;
     DeviceInfo d;
     if (int rc = device_info(d)) return rc;
-    wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
+    wait_selftest_kernel<<<1, 96, 0, static_cast<cudaStream_t>(stream)>>>(
         d.status, 1000ull * static_cast<unsigned long long>(timeout_us));
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail_cuda(e);

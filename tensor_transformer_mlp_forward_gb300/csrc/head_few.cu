@@ -481,8 +481,11 @@ __global__ void __launch_bounds__(Fused<TT>::THREADS, Fused<TT>::CTAS)
     const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
     const int blocks = (p.V + kFusedRows - 1) / kFusedRows;
     const int n = blocks > first ? (blocks - 1 - first) / step + 1 : 0;
+    // Blocks that are copied: all n, or those issued when a wait gave up (the
+    // status word is set; the loop goes on, on whatever the buffers hold).
+    int to_issue = n;
     auto issue = [&](int i) {  // thread 0: the CTA's i-th block
-        if (i >= n) return;
+        if (i >= to_issue) return;
         const int s = i % STAGES;
         mbar_arrive_expect_tx(&full[s], boxes * kBoxBytes);
         for (int b = 0; b < boxes; ++b)
@@ -541,7 +544,8 @@ __global__ void __launch_bounds__(Fused<TT>::THREADS, Fused<TT>::CTAS)
     // sits at position c ^ (r mod 8) of its 128 bytes.
     auto logits = [&](int i) {
         const int st = i % STAGES;
-        warp_wait_polls(&full[st], static_cast<uint32_t>(i / STAGES) & 1u, &abort_flag, status);
+        warp_wait_polls(&full[st], static_cast<uint32_t>(i / STAGES) & 1u, &abort_flag, status,
+                        [&] { to_issue = min(to_issue, max(i - 1, 0) + STAGES); });
         float z[TT][4];
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) z[tt][0] = z[tt][1] = z[tt][2] = z[tt][3] = 0.0f;
@@ -653,6 +657,10 @@ __global__ void __launch_bounds__(Fused<TT>::THREADS, Fused<TT>::CTAS)
         if (i + 1 < n) gradient(i + 1);
         __syncthreads();
     }
+    // copies that a wait has given up on land before the CTA may leave
+    if (threadIdx.x == 0 && *static_cast<volatile uint32_t*>(&abort_flag))
+        for (int s = 0; s < min(STAGES, to_issue); ++s)
+            wait_drain(&full[s], static_cast<uint32_t>((to_issue - 1 - s) / STAGES) & 1u, status);
 #pragma unroll
     for (int b = 0; b < BOXES; ++b) {
         const int c = (warp + b * WARPS) * 64 + 8 * g;

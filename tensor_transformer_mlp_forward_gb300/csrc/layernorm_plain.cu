@@ -464,14 +464,27 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     auto dy_of = [&](const T* sx) {
         return reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(sx) + p.buf_bytes);
     };
+    // A wait that gives up: the copies issued so far (the last of each stage; the
+    // earlier ones were waited for) land, and so does what peers have sent,
+    // before the CTA is gone.
+    auto give_up = [&] {
+        if (threadIdx.x == 0) {
+            const int issued = n - issue_left;
+            for (int s = 0; s < p.stages && s < issued; ++s)
+                wait_drain(&full[s], static_cast<uint32_t>((issued - 1 - s) / p.stages) & 1u, p.status);
+        }
+        if constexpr (CLUSTER) {
+            for (int i = 0; i < 100; ++i) __nanosleep(10000);
+            cluster_sync_thread();
+        }
+        exit_thread();
+    };
     // Begins the CTA's i-th block: waits for its copies and sends this warp's
     // part of its rows' sums of g and g (x - mu) to every CTA of the row.
-    // (A wait that gives up has set the status word; the loop goes on, on
-    // whatever the buffers hold.)
     int b_stage = 0, b_slot = 0;
     uint32_t b_phase = 0, b_skip = skip0, b_row = unit * block_rows + g * U;
     auto begin = [&](int i, const Stats& st) {
-        warp_wait_polls(&full[b_stage], b_phase, &abort_flag, p.status);
+        warp_wait_polls(&full[b_stage], b_phase, &abort_flag, p.status, give_up);
         if constexpr (VEC == 1) {
             if (i == n - 1) {  // the tensor's last few bytes, if they are here: plain loads
                 const long long b0 = first_b0 + i * issue_step;
@@ -550,7 +563,7 @@ __global__ void __launch_bounds__(NT, MIN_CTAS)
     const long long out_step = static_cast<long long>(row_step) * p.h;
     for (int i = 0; i < n; ++i) {
         const Stats st_after = row_stats(row + (AHEAD + 1) * row_step);
-        warp_wait_polls(&sums[slot], phase, &abort_flag, p.status);
+        warp_wait_polls(&sums[slot], phase, &abort_flag, p.status, give_up);
         if (warp == 0 && i >= AHEAD) issue();  // block i - AHEAD is read
         float2 m[U];
         if constexpr (CLUSTER) {

@@ -78,7 +78,7 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
 }
 
 // Waits for the phase of `bar` with the given parity to complete.  Gives up
-// after kWaitLimitNs, or as soon as another role of the CTA has given up
+// after limit_ns, or as soon as another role of the CTA has given up
 // (*abort != 0): on its own timeout it raises *abort, writes the timeout
 // code to the device status word status[0] and, when `site` is nonzero and
 // no earlier wait has done so, records `site` in status[1] so that the host
@@ -86,10 +86,11 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
 // SLEEP selects the suspending try_wait (see mbar_try_wait_sleep).
 template <bool SLEEP = false>
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
-                                             volatile uint32_t* abort, int* status, int site = 0) {
+                                             volatile uint32_t* abort, int* status, int site = 0,
+                                             unsigned long long limit_ns = kWaitLimitNs) {
     // The timer takes about a microsecond to read: polls come first, so that a
-    // wait shorter than theirs (the hardware suspends a poll for a while) does
-    // not pay for it.
+    // wait shorter than theirs does not pay for it.  (A poll that fails suspends
+    // the thread for 4 us, whatever the hint: 64 are a quarter of a millisecond.)
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
         if (mbar_poll<SLEEP>(bar, parity)) return true;
@@ -99,7 +100,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
         for (int i = 0; i < 64; ++i)
             if (mbar_poll<SLEEP>(bar, parity)) return true;
         if (*abort) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
+        if (global_ns() - t0 > limit_ns) {
             *abort = 1u;
             atomicExch(status, kStatusTimeout);
             if (site) atomicCAS(status + 1, 0, site);
@@ -115,32 +116,41 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
 template <bool SLEEP = false>
 __device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity,
                                                   volatile uint32_t* abort, int* status,
-                                                  int site = 0) {
+                                                  int site = 0,
+                                                  unsigned long long limit_ns = kWaitLimitNs) {
     uint32_t ok = 1u;
-    if ((threadIdx.x & 31) == 0) ok = wait_bounded<SLEEP>(bar, parity, abort, status, site) ? 1u : 0u;
+    if ((threadIdx.x & 31) == 0)
+        ok = wait_bounded<SLEEP>(bar, parity, abort, status, site, limit_ns) ? 1u : 0u;
     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
     __syncwarp();
     return ok != 0u;
 }
 
-// A wait limited by its number of polls, for waits on a kernel's critical
-// path: the limit of wait_bounded reads the global timer on its first miss,
-// which takes about a microsecond.  A poll suspends the thread until the
-// phase completes or some time of the hardware's own passes, so the limit is
-// seconds.  Called by whole warps; the lanes poll together.
-constexpr int kPollLimit = 1 << 24;
+// The same limited by its number of polls, for waits on a kernel's critical
+// path: no timer, whose first read takes about a microsecond and whose 64-bit
+// arithmetic takes registers.  A poll that fails takes 3.97 us (measured, 64 to
+// 8192 polls), so the limit is 2 s.  Called by whole warps; the lanes poll
+// together.  A lane that gives up raises *abort, sets the status word and calls
+// give_up(), behind the loop's own test, so that the way of a wait that succeeds
+// has no test more (one flag read a block cost the few-token kernel 1.4 us of 47).
+constexpr int kPollNs = 3970, kPollLimit = static_cast<int>(kWaitLimitNs / kPollNs);
 
-__device__ __forceinline__ void warp_wait_polls(uint64_t* bar, uint32_t parity,
-                                                volatile uint32_t* abort, int* status) {
+template <typename GiveUp>
+__device__ __forceinline__ void warp_wait_polls(uint64_t* bar, uint32_t parity, volatile uint32_t* abort,
+                                                int* status, GiveUp&& give_up, int limit = kPollLimit) {
     for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
-        if (i >= kPollLimit || *abort) {
+        if (i >= limit || *abort) {
             *abort = 1u;
             atomicExch(status, kStatusTimeout);
+            give_up();
             break;
         }
     }
     __syncwarp();
 }
+
+// Ends the calling thread.  Barriers wait for the threads that have not exited.
+__device__ __forceinline__ void exit_thread() { asm volatile("exit;"); }
 
 // Bounded wait used while draining after an abort: ignores the abort flag.
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, int* status,
@@ -389,6 +399,13 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v),
                  "r"(bar)
                  : "memory");
+}
+
+// cluster_sync for a thread on its own way.
+__device__ __forceinline__ void cluster_sync_thread() {
+    asm volatile(
+        "barrier.cluster.arrive.release;\n\t"
+        "barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ------------------------------------------------ cluster launch control
