@@ -750,15 +750,14 @@ __global__ void __launch_bounds__(32 * (EW + 2), 1)
                 }
             }
             if constexpr (EPI == EPI_DLOGITS) {
-                if (row_ok) {
+                if (row_ok) {  // all four loads at once
                     const long long y = __ldg(p.targets + m);
+                    const float d = __ldg(p.dloss + m), l = __ldg(p.lse + m), tq = __ldg(p.target_q + m);
                     const bool known = y < p.vocab;
-                    weight = y < 0 ? 0.0f : known ? __ldg(p.dloss + m) / dloss_max : __int_as_float(0x7FC00000);
-                    lse2 = y < 0 ? INFINITY : __ldg(p.lse + m) * kLog2e;  // 2^(z - inf) = 0
-                    if (known && y >= 0) {
-                        target = static_cast<int>(y) - p.col0 - tc.n0;
-                        if (target >= 0 && target < G::TILE_N) target_dz = weight * __ldg(p.target_q + m);
-                    }
+                    weight = y < 0 ? 0.0f : known ? d / dloss_max : __int_as_float(0x7FC00000);
+                    lse2 = y < 0 ? INFINITY : l * kLog2e;  // 2^(z - inf) = 0
+                    if (known && y >= 0) target = static_cast<int>(y) - p.col0 - tc.n0;
+                    target_dz = weight * tq;
                 }
             }
             float scale = 1.0f;
