@@ -147,3 +147,25 @@ def test_rows_torn_between_classes(T, h, V, classes):
     want_loss = torch.where(counted, torch.nn.functional.softplus(torch.logsumexp(rest, 1) - zt), torch.zeros_like(zt))
     off = float((loss.double() - want_loss).abs().max() / want.max())
     assert off <= 2.0 ** -19, off
+
+
+@pytest.mark.parametrize("T,h,V", [(9, 264, 999), (9, 2056, 999), (150, 264, 999), (300, 64, 5003)])
+def test_a_bad_token_stays_by_itself(T, h, V):
+    """A counted token's row of NaN, its weight of infinity: its own loss, lse and
+    dX are NaN, the other tokens' bit for bit as without it.  (dW's rows sum all
+    tokens: NaN.)"""
+    c = {k: v.cuda() for k, v in lean_on(T, h, V, T, 4.0).items()}
+    c["y"][3] = 5
+    loss0, lse0 = binding.tp_head_loss_forward(c["X"], c["W"], c["y"])
+    X = c["X"].clone()
+    X[3] = float("nan")
+    loss, lse = binding.tp_head_loss_forward(X, c["W"], c["y"])
+    ok = torch.arange(T, device="cuda") != 3
+    assert torch.equal(loss[ok], loss0[ok]) and torch.equal(lse[ok], lse0[ok])
+    assert bool(torch.isnan(loss[3])) and bool(torch.isnan(lse[3]))
+    dX0, _ = binding.tp_head_loss_backward(c["dloss"], c["X"], c["W"], c["y"], lse0)
+    dX, dW = binding.tp_head_loss_backward(c["dloss"], X, c["W"], c["y"], lse)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    assert torch.equal(dX[ok], dX0[ok]) and bool(torch.isnan(dX[3].float()).all())
+    assert bool(torch.isnan(dW.float()).all())
