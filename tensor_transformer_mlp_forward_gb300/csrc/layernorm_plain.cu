@@ -228,8 +228,8 @@ __device__ __forceinline__ float warp_sums(const float2 (&v)[U]) {
 }
 
 // Sum over the W warps of a row's group (`first` and the W - 1 behind it);
-// every thread receives the total, added in the same order in every thread.  `scratch` holds one entry a warp.  All threads of
-// the CTA call it.
+// every thread receives the total, added in the same order in every thread.
+// `scratch` holds one entry a warp.  All threads of the CTA call it.
 __device__ __forceinline__ float2 group_sum(float2 x, int W, int first, float2* scratch) {
     x = warp_sum(x);
     if (W == 1) return x;
