@@ -689,10 +689,11 @@ int tpmlp_device_wait_site(void);
  * launched (for launch accounting). */
 int tpmlp_last_launch_count(void);
 
-/* Self-test of the bounded device wait: launches one small kernel whose
- * thread waits on a barrier that nothing ever completes, with a limit of
- * `timeout_us` microseconds (1..1000000).  Returns TPMLP_OK after the launch;
- * tpmlp_device_status() then reports TPMLP_ERR_DEVICE_TIMEOUT. */
+/* Self-test of the bounded device waits: launches one small kernel whose
+ * warps wait on a barrier that nothing ever completes, in each of the ways the
+ * kernels wait, with a limit of `timeout_us` microseconds (1..1000000).
+ * Returns TPMLP_OK after the launch; when all have given up,
+ * tpmlp_device_status() reports TPMLP_ERR_DEVICE_TIMEOUT. */
 int tpmlp_selftest_bounded_wait(int timeout_us, void* stream);
 
 #ifdef __cplusplus
