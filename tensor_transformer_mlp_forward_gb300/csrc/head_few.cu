@@ -92,10 +92,11 @@ struct FewArgs {
 // Logits of the 16 tokens against tasks of 32 vocabulary rows, CTA b taking
 // tasks b, b + grid, ... (neighbours in memory at the same time).  The four
 // warps split k (64 columns each in turn, so that together they read 512
-// consecutive bytes of a row) and their sums meet in shared memory.  Then thread (token, 4 rows): forward, the running maximum and sum
-// of exponentials; backward, the logits' gradient.  The loads run one step
-// ahead, across the tasks too: a task has few steps (four a warp at h =
-// 1024), and starting each anew left the memory idle a third of the time.
+// consecutive bytes of a row) and their sums meet in shared memory.  Then
+// thread (token, 4 rows): forward, the running maximum and sum of
+// exponentials; backward, the logits' gradient.  The loads run one step ahead,
+// across the tasks too: a task has few steps (four a warp at h = 1024), and
+// starting each anew left the memory idle a third of the time.
 template <bool GRAD, int TT>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) head_few_logits_kernel(const FewArgs p) {
     pdl_launch_dependents();  // the next kernel may begin its launch

@@ -199,7 +199,9 @@ __global__ void __launch_bounds__(kThreads)
     if (sub == 0 && ok) {
         const Row mine{acc, logit, y < 0 ? -1 : static_cast<int>(min(y, static_cast<long long>(V)))};
         const Two others = log_sum(acc.x, acc.y);
-        // (Not where the target outweighs the sum, so that it does not matter.)
+        // (Not where the target outweighs the sum, so that it does not matter; nor
+        // where 64 classes' worth share the sum, which up to h = 65536 the test itself
+        // excludes: beyond, it would be a second product of the row with most of W.)
         const bool outweighed = y >= 0 && y < V && logit.hi > others.hi + 20.0f;
         redo = where != nullptr && !outweighed && acc.y < 64.0f && too_coarse(acc.x, 1.0f, acc.y, others.hi, h);
         if (redo)
@@ -223,7 +225,8 @@ __global__ void __launch_bounds__(kThreads)
             const int mine = first + threadIdx.x;
             const float m = mine < n_parts ? __ldg(parts + static_cast<long long>(mine) * T + at).x : -INFINITY;
             const float w = ex2_approx((m - q.others.x) * kLog2e);
-            const unsigned bits = __ballot_sync(0xFFFFFFFFu, m > -INFINITY && too_coarse(m, w, q.others.y, log_others.hi, h));
+            const bool again_here = m > -INFINITY && too_coarse(m, w, q.others.y, log_others.hi, h);
+            const unsigned bits = __ballot_sync(0xFFFFFFFFu, again_here);
             if (lane == 0) coarse[warp] = bits;
             __syncthreads();
             for (int i = 0; i < kThreads / 32; ++i) {
