@@ -596,6 +596,127 @@ int tp_attn_backward(const tpmlp_bf16* dY, const tpmlp_bf16* X, const tpmlp_bf16
                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Packed attention with grouped key/value heads                           */
+/* ---------------------------------------------------------------------- */
+
+/* Causal attention of a batch whose sequences have lengths of their own, one
+ * behind another in T rows of tokens, with nkv key/value heads that nh query
+ * heads share:
+ *
+ *   sequence i: rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1
+ *   query head j reads key/value head j / (nh / nkv)
+ *   S = scale Q K^T (keys up to the query, of its own sequence),
+ *   P = softmax over each row, O = P V
+ *
+ * Layout: Q, dQ [T, nh, d], K, V, dK, dV [T, nkv, d] bf16, head by head, whose
+ * tokens lie ld* values apart (ld* >= heads * d, a multiple of 8), so that they
+ * may be parts of one [T, (nh + 2 nkv) d] projection; O, dO [T, nh, d] dense;
+ * lse float32 [nh, T], in the log2 domain as in tp_attn_core_forward;
+ * cu_seqlens int32 [nb + 1] in device memory (4-byte aligned): read on the
+ * device, so a captured call takes the lengths of the replay.  A sequence may be
+ * empty.  Rows in no sequence (before cu_seqlens[0], behind cu_seqlens[nb]) are
+ * neither used nor written.  Offsets that fall or leave [0, T] make the call
+ * write nothing and set the device status word to TPMLP_ERR_SHAPE.
+ *
+ * Rules (else TPMLP_ERR_SHAPE): 0 <= nb, T <= 2^30, nh >= 1, nkv >= 1,
+ * nh % nkv == 0, d in {64, 96, 128, 160}, scale finite and > 0 (1/sqrt(d) as a
+ * rule), (T / 128 + nb) nh < 2^31, T nh <= 2^36.  nb == 0 or T == 0 does nothing.
+ * A token's infinities and NaN reach no other sequence; within its own they may
+ * reach earlier tokens of its block of 128. */
+
+/* Bytes of scratch tp_attn_packed_forward needs (contents on entry do not
+ * matter): the list of work items that the call makes on its stream. */
+size_t tp_attn_packed_forward_workspace_bytes(int nb, int T, int nh, int nkv, int d);
+
+int tp_attn_packed_forward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16* K, long long ldk,
+                           const tpmlp_bf16* V, long long ldv, const int* cu_seqlens, int nb, int T,
+                           int nh, int nkv, int d, float scale, tpmlp_bf16* O, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of scratch tp_attn_packed_backward needs. */
+size_t tp_attn_packed_backward_workspace_bytes(int nb, int T, int nh, int nkv, int d);
+
+/* Gradients of tp_attn_packed_forward given dO, from the forward's O and lse:
+ * dK and dV are summed over the query heads that share them.  Every gradient is
+ * summed in fp32 in a fixed order and written once. */
+int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16* K, long long ldk,
+                            const tpmlp_bf16* V, long long ldv, const tpmlp_bf16* O,
+                            const float* lse, const tpmlp_bf16* dO, const int* cu_seqlens, int nb,
+                            int T, int nh, int nkv, int d, float scale, tpmlp_bf16* dQ,
+                            long long lddq, tpmlp_bf16* dK, long long lddk, tpmlp_bf16* dV,
+                            long long lddv, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Norms and rotation of queries and keys                                  */
+/* ---------------------------------------------------------------------- */
+
+/* Each head's d values x of token t, p = positions[t]:
+ *
+ *   rstd = 1 / sqrt(mean(x^2) + eps) ; u = x rstd gamma
+ *   y_i           = u_i cos(a_i) - u_{i + rot/2} sin(a_i)
+ *   y_{i + rot/2} = u_{i + rot/2} cos(a_i) + u_i sin(a_i)    i < rot / 2
+ *   y_j = u_j                                                j >= rot
+ *   a_i = p theta^(-2 i / rot)
+ *
+ * Q, Qo [T, nh, d] and K, Ko [T, nkv, d] of type `dtype` (tpmlp_dtype) with
+ * tokens ld* values apart (ld* >= heads * d, whole 16-byte pieces); gamma_q,
+ * gamma_k [d] of that type, shared by the heads; positions int32 [T] (4-byte
+ * aligned, any values); rstd float32 [T, nh + nkv] (queries first), saved for
+ * the backward pass.  Statistics and rotation are fp32, angles exact to fp32 at
+ * any position.  Rules (else TPMLP_ERR_SHAPE): 0 <= T <= 2^30, nh, nkv >= 1,
+ * d % 16 == 0, 32 <= d <= 256, rot % 16 == 0, 0 <= rot <= d, 0 < theta <= 1e300,
+ * eps finite and > 0, T (nh + nkv) <= 2^36. */
+int tp_qk_norm_rope_forward(const void* Q, long long ldq, const void* K, long long ldk,
+                            const void* gamma_q, const void* gamma_k, const int* positions, int T,
+                            int nh, int nkv, int d, int rot, double theta, float eps, int dtype,
+                            void* Qo, long long ldqo, void* Ko, long long ldko, float* rstd,
+                            void* stream);
+
+/* Floats of scratch (`partial`) tp_qk_norm_rope_backward needs. */
+size_t tp_qk_norm_rope_backward_workspace_floats(int T, int nh, int nkv, int d);
+
+/* With g = dy turned back by its position's angles and xhat = x rstd:
+ *   dgamma = sum over tokens and heads of g xhat (float32 [d] each)
+ *   dx = rstd (g gamma - xhat mean(g gamma xhat))
+ * dQo, dKo: gradients at Qo, Ko; Q, K, rstd: the forward's.  Sums run in a fixed
+ * order.  T == 0 zeroes dgamma_q and dgamma_k. */
+int tp_qk_norm_rope_backward(const void* dQo, long long lddqo, const void* dKo, long long lddko,
+                             const void* Q, long long ldq, const void* K, long long ldk,
+                             const void* gamma_q, const void* gamma_k, const int* positions,
+                             const float* rstd, int T, int nh, int nkv, int d, int rot,
+                             double theta, int dtype, void* dQ, long long lddq, void* dK,
+                             long long lddk, float* dgamma_q, float* dgamma_k, float* partial,
+                             void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Global gradient norm and clipping                                       */
+/* ---------------------------------------------------------------------- */
+
+/* n tensors (n <= 2^20): grads[i] points to sizes[i] dense values (0 <= sizes[i]
+ * <= 2^40) of type dtypes[i] (tpmlp_dtype) in device memory, aligned to its type
+ * only (tensors on 16-byte boundaries are the fast ones); the three arrays are
+ * host memory and free once the call returns.
+ *
+ *   norm = sqrt(sum over all tensors and values of g^2)     (float32, device)
+ *
+ * The sum runs in a fixed order.  Squares above the float32 range are kept in
+ * range; a norm below 2^-63 may read as less than it is.  An infinite or NaN
+ * gradient gives an infinite or NaN norm.  workspace: tp_grad_workspace_bytes(n)
+ * bytes, 16-byte aligned. */
+size_t tp_grad_workspace_bytes(int n);
+int tp_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes, int n,
+                 float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norm, and out_i = grads_i * min(1, max_norm / (norm + 1e-6)) in the same
+ * types.  out[i] may be grads[i] (clipped in place); otherwise no output may
+ * share memory with another tensor (TPMLP_ERR_SHAPE, as max_norm that is not
+ * > 0).  A NaN norm makes every output NaN; an infinite one zeroes the finite
+ * values. */
+int tp_grad_clip(const void* const* grads, void* const* out, const long long* sizes,
+                 const int* dtypes, int n, float max_norm, float* norm, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Status                                                                  */
 /* ---------------------------------------------------------------------- */
 
@@ -673,15 +794,16 @@ const char* tpmlp_status_string(int status);
 int tpmlp_last_cuda_error(void);
 
 /* Reads and clears the device status word of the current device: TPMLP_OK,
- * or TPMLP_ERR_DEVICE_TIMEOUT if a bounded wait in a kernel gave up since the
- * last read.  Synchronises the device. Returns TPMLP_ERR_LAUNCH if the read
+ * TPMLP_ERR_DEVICE_TIMEOUT if a bounded wait in a kernel gave up since the last
+ * read, or TPMLP_ERR_SHAPE if the offsets of a packed batch were out of order or
+ * range.  Synchronises the device. Returns TPMLP_ERR_LAUNCH if the read
  * itself fails. */
 int tpmlp_device_status(void);
 
 /* Reads and clears the site code of the first bounded wait that gave up on
  * the current device since the last read: 0 if none; otherwise a code that
  * names the kernel and the wait (0x1nn attention forward, 0x2nn attention dQ,
- * 0x3nn attention dK/dV; the GEMM kernels record none).  Synchronises the
+ * 0x3nn attention dK/dV, 0x4nn, 0x5nn and 0x6nn the same of packed attention; the GEMM kernels record none).  Synchronises the
  * device.  A failed read returns minus the status code. */
 int tpmlp_device_wait_site(void);
 

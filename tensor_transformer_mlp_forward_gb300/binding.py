@@ -44,6 +44,8 @@ _I = ctypes.c_int
 _S = ctypes.c_size_t
 _D = ctypes.c_double
 _U64 = ctypes.c_uint64
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "tp_mlp_split_workspace_bytes": ([_I] * 4, _S),
@@ -99,6 +101,16 @@ _SIGNATURES = {
     "tp_attn_forward": ([_P] * 6 + [_I] * 5 + [_P] * 4 + [_P, _S, _P], _I),
     "tp_attn_backward_workspace_bytes": ([_I] * 5, _S),
     "tp_attn_backward": ([_P] * 7 + [_I] * 5 + [_P] * 5 + [_P, _S, _P], _I),
+    "tp_attn_packed_forward_workspace_bytes": ([_I] * 5, _S),
+    "tp_attn_packed_forward": ([_P, _L] * 3 + [_P] + [_I] * 5 + [_F] + [_P] * 2 + [_P, _S, _P], _I),
+    "tp_attn_packed_backward_workspace_bytes": ([_I] * 5, _S),
+    "tp_attn_packed_backward": ([_P, _L] * 3 + [_P] * 4 + [_I] * 5 + [_F] + [_P, _L] * 3 + [_P, _S, _P], _I),
+    "tp_qk_norm_rope_forward": ([_P, _L] * 2 + [_P] * 3 + [_I] * 5 + [_D, _F, _I] + [_P, _L] * 2 + [_P] * 2, _I),
+    "tp_qk_norm_rope_backward_workspace_floats": ([_I] * 4, _S),
+    "tp_qk_norm_rope_backward": ([_P, _L] * 4 + [_P] * 4 + [_I] * 5 + [_D, _I] + [_P, _L] * 2 + [_P] * 4, _I),
+    "tp_grad_workspace_bytes": ([_I], _S),
+    "tp_grad_norm": ([_P] * 3 + [_I] + [_P] * 2 + [_S, _P], _I),
+    "tp_grad_clip": ([_P] * 4 + [_I, _F] + [_P] * 2 + [_S, _P], _I),
     "tp_mlp_status_string": ([_I], ctypes.c_char_p),
     "tpmlp_status_string": ([_I], ctypes.c_char_p),
     "tpmlp_last_cuda_error": ([], _I),
@@ -931,3 +943,244 @@ def tp_attn_backward(dY, X, Wqkv, Wo, QKV, O, lse, nb: int, nh: int, t: int, dX=
         _ptr(dbo, "dbo", (h,), torch.float32),
         _ptr(workspace, "workspace", None, torch.uint8), workspace.numel(), _stream(stream)))
     return dX, dWqkv, dbqkv, dWo, dbo
+
+
+# ------------------------------- packed attention with grouped heads
+
+_I32 = torch.int32
+
+
+def _heads(x, name: str, shape, dtype, device: int):
+    """The address of x [T, heads, d] whose tokens may lie apart (a part of a
+    projection's rows), and how far."""
+    T, n, d = shape
+    if x is not None and x.dtype is dtype and x.shape == shape and x.get_device() == device and device >= 0:
+        a, b, c = x.stride()
+        if T == 0 or n == 0 or ((c == 1 or d == 1) and (b == d or n == 1)):
+            if T < 2:
+                return x.data_ptr(), n * d
+            if a >= n * d:
+                return x.data_ptr(), a
+        raise ValueError(f"{name} has strides {tuple(x.stride())}: a token's {n} heads of {d} values must lie "
+                         "one behind another, and tokens may not overlap")
+    if x is not None and tuple(x.shape) == tuple(shape) and x.is_cuda and x.dtype == dtype:
+        raise ValueError(f"{name} is on {x.device}, but the current device is cuda:{device}")
+    _ptr(x.contiguous() if x is not None and x.is_cuda else x, name, shape, dtype)  # raises, naming what is wrong
+    raise ValueError(f"{name} cannot be used")
+
+
+def _packed_shape(Q, K):
+    T, nh, d = Q.shape
+    nkv = K.shape[1]
+    if T > _MOST or nh > _MOST or nkv > _MOST:
+        _too_large(T=T, nh=nh, nkv=nkv)
+    return T, nh, nkv, d
+
+
+def tp_attn_packed_forward(Q, K, V, cu_seqlens, scale=None, O=None, lse=None, workspace=None, stream=None):
+    """O [T, nh, d] (bf16) and lse [nh, T] (float32, log2 domain) of causal
+    attention over packed sequences: sequence i owns tokens cu_seqlens[i] to
+    cu_seqlens[i + 1] - 1 (int32, on the device).  Q [T, nh, d], K, V [T, nkv,
+    d] may be parts of one projection's rows; query head j reads head j // (nh
+    // nkv) of K and V.  scale: 1 / sqrt(d) unless given.  Tokens in no
+    sequence are left as they are (in a fresh O: uninitialised)."""
+    T, nh, nkv, d = _packed_shape(Q, K)
+    dev = _device_of(Q)
+    qp, ldq = _heads(Q, "Q", (T, nh, d), _BF16, dev)
+    kp, ldk = _heads(K, "K", (T, nkv, d), _BF16, dev)
+    vp, ldv = _heads(V, "V", (T, nkv, d), _BF16, dev)
+    nb = cu_seqlens.numel() - 1
+    cp = _in(cu_seqlens, "cu_seqlens", (nb + 1,), _I32, dev)
+    L = lib()
+    with _on(stream):
+        if O is None:
+            O = torch.empty((T, nh, d), dtype=_BF16, device=Q.device)
+            op = O.data_ptr()
+        else:
+            op = _in(O, "O", (T, nh, d), _BF16, dev)
+        if lse is None:
+            lse = torch.empty((nh, T), dtype=_F32, device=Q.device)
+            lp = lse.data_ptr()
+        else:
+            lp = _in(lse, "lse", (nh, T), _F32, dev)
+        if workspace is None:
+            need = L.tp_attn_packed_forward_workspace_bytes(nb, T, nh, nkv, d)
+            workspace = torch.empty(need or 1, dtype=_U8, device=Q.device)
+    status = L.tp_attn_packed_forward(
+        qp, ldq, kp, ldk, vp, ldv, cp, nb, T, nh, nkv, d, d ** -0.5 if scale is None else scale, op, lp,
+        _in(workspace, "workspace", workspace.shape, _U8, dev), workspace.numel(), _stream_of(stream, dev))
+    if status:
+        _check("tp_attn_packed_forward", status)
+    return O, lse
+
+
+def tp_attn_packed_backward(Q, K, V, O, lse, dO, cu_seqlens, scale=None, dQ=None, dK=None, dV=None,
+                            workspace=None, stream=None):
+    """dQ [T, nh, d], dK, dV [T, nkv, d] (bf16) of tp_attn_packed_forward given
+    dO; dK and dV are summed over the query heads that share them.  dQ, dK and
+    dV may be parts of one gradient's rows.  Tokens in no sequence are left as
+    they are (in fresh outputs: uninitialised)."""
+    T, nh, nkv, d = _packed_shape(Q, K)
+    dev = _device_of(Q)
+    qs, ks = (T, nh, d), (T, nkv, d)
+    qp, ldq = _heads(Q, "Q", qs, _BF16, dev)
+    kp, ldk = _heads(K, "K", ks, _BF16, dev)
+    vp, ldv = _heads(V, "V", ks, _BF16, dev)
+    op, dop = _in(O, "O", qs, _BF16, dev), _in(dO, "dO", qs, _BF16, dev)
+    lp = _in(lse, "lse", (nh, T), _F32, dev)
+    nb = cu_seqlens.numel() - 1
+    cp = _in(cu_seqlens, "cu_seqlens", (nb + 1,), _I32, dev)
+    L = lib()
+    with _on(stream):
+        dQ = torch.empty(qs, dtype=_BF16, device=Q.device) if dQ is None else dQ
+        dK = torch.empty(ks, dtype=_BF16, device=Q.device) if dK is None else dK
+        dV = torch.empty(ks, dtype=_BF16, device=Q.device) if dV is None else dV
+        if workspace is None:
+            need = L.tp_attn_packed_backward_workspace_bytes(nb, T, nh, nkv, d)
+            workspace = torch.empty(need or 1, dtype=_U8, device=Q.device)
+    dqp, lddq = _heads(dQ, "dQ", qs, _BF16, dev)
+    dkp, lddk = _heads(dK, "dK", ks, _BF16, dev)
+    dvp, lddv = _heads(dV, "dV", ks, _BF16, dev)
+    status = L.tp_attn_packed_backward(
+        qp, ldq, kp, ldk, vp, ldv, op, lp, dop, cp, nb, T, nh, nkv, d, d ** -0.5 if scale is None else scale,
+        dqp, lddq, dkp, lddk, dvp, lddv, _in(workspace, "workspace", workspace.shape, _U8, dev), workspace.numel(),
+        _stream_of(stream, dev))
+    if status:
+        _check("tp_attn_packed_backward", status)
+    return dQ, dK, dV
+
+
+# ------------------------------- norms and rotation of queries and keys
+
+def tp_qk_norm_rope_forward(Q, K, gamma_q, gamma_k, positions, rot=None, theta: float = 10000.0, eps: float = 1e-5,
+                            Qo=None, Ko=None, rstd=None, stream=None):
+    """Qo, Ko, rstd: each head of Q [T, nh, d] and K [T, nkv, d] divided by its
+    root mean square, times gamma [d], with its first `rot` values (all unless
+    given) turned by the angles of positions [T] (int32).  bfloat16, float16 or
+    float32; Q and K may be parts of one projection's rows.  rstd [T, nh + nkv]
+    (float32) is for the backward pass."""
+    T, nh, nkv, d = _packed_shape(Q, K)
+    dt, dev = Q.dtype, _device_of(Q)
+    code = _dtype_of(Q, "Q")
+    qs, ks = (T, nh, d), (T, nkv, d)
+    qp, ldq = _heads(Q, "Q", qs, dt, dev)
+    kp, ldk = _heads(K, "K", ks, dt, dev)
+    gq, gk = _in(gamma_q, "gamma_q", (d,), dt, dev), _in(gamma_k, "gamma_k", (d,), dt, dev)
+    pp = _in(positions, "positions", (T,), _I32, dev)
+    with _on(stream):
+        Qo = torch.empty(qs, dtype=dt, device=Q.device) if Qo is None else Qo
+        Ko = torch.empty(ks, dtype=dt, device=Q.device) if Ko is None else Ko
+        if rstd is None:
+            rstd = torch.empty((T, nh + nkv), dtype=_F32, device=Q.device)
+    qop, ldqo = _heads(Qo, "Qo", qs, dt, dev)
+    kop, ldko = _heads(Ko, "Ko", ks, dt, dev)
+    status = lib().tp_qk_norm_rope_forward(
+        qp, ldq, kp, ldk, gq, gk, pp, T, nh, nkv, d, d if rot is None else rot, theta, eps, code, qop, ldqo, kop, ldko,
+        _in(rstd, "rstd", (T, nh + nkv), _F32, dev), _stream_of(stream, dev))
+    if status:
+        _check("tp_qk_norm_rope_forward", status)
+    return Qo, Ko, rstd
+
+
+def tp_qk_norm_rope_backward(dQo, dKo, Q, K, gamma_q, gamma_k, positions, rstd, rot=None, theta: float = 10000.0,
+                             dQ=None, dK=None, dgamma_q=None, dgamma_k=None, partial=None, stream=None):
+    """dQ, dK (of Q's type), dgamma_q, dgamma_k (float32 [d]) of
+    tp_qk_norm_rope_forward given the gradients dQo and dKo of its outputs."""
+    T, nh, nkv, d = _packed_shape(Q, K)
+    dt, dev = Q.dtype, _device_of(Q)
+    code = _dtype_of(Q, "Q")
+    qs, ks = (T, nh, d), (T, nkv, d)
+    yq, ldyq = _heads(dQo, "dQo", qs, dt, dev)
+    yk, ldyk = _heads(dKo, "dKo", ks, dt, dev)
+    qp, ldq = _heads(Q, "Q", qs, dt, dev)
+    kp, ldk = _heads(K, "K", ks, dt, dev)
+    gq, gk = _in(gamma_q, "gamma_q", (d,), dt, dev), _in(gamma_k, "gamma_k", (d,), dt, dev)
+    pp = _in(positions, "positions", (T,), _I32, dev)
+    rp = _in(rstd, "rstd", (T, nh + nkv), _F32, dev)
+    L = lib()
+    need = L.tp_qk_norm_rope_backward_workspace_floats(T, nh, nkv, d)
+    with _on(stream):
+        dQ = torch.empty(qs, dtype=dt, device=Q.device) if dQ is None else dQ
+        dK = torch.empty(ks, dtype=dt, device=Q.device) if dK is None else dK
+        dgamma_q = torch.empty(d, dtype=_F32, device=Q.device) if dgamma_q is None else dgamma_q
+        dgamma_k = torch.empty(d, dtype=_F32, device=Q.device) if dgamma_k is None else dgamma_k
+        if partial is None:
+            partial = torch.empty(need or 1, dtype=_F32, device=Q.device)
+    if partial.numel() < need:
+        raise ValueError(f"partial holds {partial.numel()} floats, {need} needed")
+    dqp, lddq = _heads(dQ, "dQ", qs, dt, dev)
+    dkp, lddk = _heads(dK, "dK", ks, dt, dev)
+    status = L.tp_qk_norm_rope_backward(
+        yq, ldyq, yk, ldyk, qp, ldq, kp, ldk, gq, gk, pp, rp, T, nh, nkv, d, d if rot is None else rot, theta, code,
+        dqp, lddq, dkp, lddk, _in(dgamma_q, "dgamma_q", (d,), _F32, dev), _in(dgamma_k, "dgamma_k", (d,), _F32, dev),
+        _in(partial, "partial", partial.shape, _F32, dev), _stream_of(stream, dev))
+    if status:
+        _check("tp_qk_norm_rope_backward", status)
+    return dQ, dK, dgamma_q, dgamma_k
+
+
+# ------------------------------- global gradient norm and clipping
+
+def _tensors(xs, name: str, device: int):
+    """Addresses, sizes and type codes of a list of dense tensors."""
+    for i, x in enumerate(xs):
+        if x.get_device() != device or device < 0:
+            raise ValueError(f"{name}[{i}] is on {x.device}, but the current device is cuda:{device}")
+        if x.dtype not in _DTYPES:
+            _dtype_of(x, f"{name}[{i}]")
+        if not x.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+    n = len(xs)
+    return ((_P * n)(*[x.data_ptr() for x in xs]), (_L * n)(*[x.numel() for x in xs]),
+            (_I * n)(*[_DTYPES[x.dtype] for x in xs]))
+
+
+def _norm_scratch(n: int, norm, workspace, device: int, stream):
+    with _on(stream):
+        where = torch.device("cuda", device)
+        if norm is None:
+            norm = torch.empty((), dtype=_F32, device=where)
+        if workspace is None:
+            workspace = torch.empty(lib().tp_grad_workspace_bytes(n), dtype=_U8, device=where)
+    return (norm, workspace, _in(norm, "norm", (), _F32, device),
+            _in(workspace, "workspace", workspace.shape, _U8, device))
+
+
+def _list_device(grads) -> int:
+    if grads:
+        return _device_of(grads[0])
+    return torch._C._cuda_getDevice() if torch.cuda.is_available() else -1
+
+
+def tp_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The norm (float32, no dimensions) of all values of a list of tensors
+    (bfloat16, float16, float32, mixed) together."""
+    grads = list(grads)
+    dev = _list_device(grads)
+    gp, sizes, types = _tensors(grads, "grads", dev)
+    norm, workspace, np_, wp = _norm_scratch(len(grads), norm, workspace, dev, stream)
+    status = lib().tp_grad_norm(gp, sizes, types, len(grads), np_, wp, workspace.numel(), _stream_of(stream, dev))
+    if status:
+        _check("tp_grad_norm", status)
+    return norm
+
+
+def tp_grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None, stream=None):
+    """norm, out: the norm of all gradients together, and every gradient times
+    min(1, max_norm / (norm + 1e-6)), into the tensors of `out` (the gradients
+    themselves unless given)."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    dev = _list_device(grads)
+    gp, sizes, types = _tensors(grads, "grads", dev)
+    op = gp
+    if out is not grads:
+        if [(x.dtype, x.shape) for x in out] != [(x.dtype, x.shape) for x in grads]:
+            raise ValueError("out must have the types and shapes of grads")
+        op, _, _ = _tensors(out, "out", dev)
+    norm, workspace, np_, wp = _norm_scratch(len(grads), norm, workspace, dev, stream)
+    status = lib().tp_grad_clip(gp, op, sizes, types, len(grads), max_norm, np_, wp, workspace.numel(),
+                                _stream_of(stream, dev))
+    if status:
+        _check("tp_grad_clip", status)
+    return norm, out

@@ -1,0 +1,531 @@
+// attention_packed.cu -- causal softmax attention of a packed batch with grouped
+// key/value heads, forward.
+//
+// Query head j of nh reads key/value head j / (nh / nkv).  Per sequence (rows
+// cu_seqlens[i] .. cu_seqlens[i + 1] - 1) and head:
+//
+//   S = scale Q K^T (keys up to the query) ; P = softmax_rows(S) ; O = P V
+//
+// in one pass over the keys with a running maximum and sum, in the log2 domain
+// (u = scale log2(e) q.k, P = 2^(u - m) / l, lse = m + log2(l)).  S, l and O are
+// fp32; P is rounded to bf16 where it becomes an operand of P V, which the
+// rounding of O to bf16 covers.
+//
+// The kernel is that of attention.cu (two 128-query tiles A and B in ping-pong,
+// S and O in tensor memory, P written back over S as the A operand of P V) with
+// other work: items come from a list of the sequences' tiles, tiles of a sequence
+// are read by row coordinates, and A and B are, where the heads of a group come
+// in pairs, two heads' tiles of the same queries, so that both share every K/V
+// tile, need the same number of them, and a sequence of 128 tokens or fewer keeps
+// both busy; else two adjacent tiles of one head.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_packed.cuh"
+#include "kernels.h"
+
+namespace tpmlp {
+namespace {
+
+struct FwdArgs {
+    const int4* entries;  // the plan's tiles
+    unsigned* plan;       // its header words
+    int nh, group;        // query heads, query heads per key/value head
+    int units;            // items per entry (heads, or pairs of heads)
+    int pair_heads;
+    long long T;
+    float scale2;         // scale * log2(e)
+    __nv_bfloat16* O;     // [T, nh, D]
+    float* lse;           // [nh, T]
+    int* status;
+};
+
+__global__ void __launch_bounds__(1024) packed_plan_kernel(const int* cu, int nb, int T, int tile, int4* entries,
+                                                           unsigned* head, int* ranks, int* status) {
+    pdl_launch_dependents();
+    pdl_wait();
+    plan_block(cu, nb, T, tile, entries, head, ranks, status);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,  // 128-row boxes
+                      const __grid_constant__ CUtensorMap tm_k,  // BKV-row boxes
+                      const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
+    pdl_launch_dependents();  // the next kernel may begin its launch
+    using C = FwdCfg<D>;
+    constexpr int S = C::STAGES;
+    constexpr int BKV = C::BKV;
+    constexpr int SCH = BKV / 32;  // 32-key chunks of S per key tile
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t* sQ = smem;                   // Q_A, Q_B
+    uint8_t* ring = smem + 2 * C::QTILE;  // K_0, V_0, K_1, V_1, ... of every item in turn
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S * C::KVTILE);
+    uint64_t* q_full = bars;              // the item's Q tiles have landed
+    uint64_t* q_empty = bars + 1;         // the item's last S MMAs have read them
+    uint64_t* kv_full = bars + 2;
+    uint64_t* kv_empty = kv_full + S;
+    uint64_t* s_full = kv_empty + S;      // [tile]
+    uint64_t* p_full = s_full + 2;        // [tile]
+    uint64_t* pv_done = p_full + 2;       // [tile]
+    uint64_t* o_free = pv_done + 2;       // [tile] the softmax warps have read O_x out
+    uint64_t* item_full = o_free + 2;     // [2]
+    uint64_t* item_empty = item_full + 2; // [2]
+    uint64_t* drain = item_empty + 2;
+    int* items = reinterpret_cast<int*>(drain + 1);  // [2] x {first row, length, tile, head}
+    uint32_t* misc = reinterpret_cast<uint32_t*>(items + 8);
+    volatile uint32_t* abort_flag = misc + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    struct Item {
+        int row0, len, n_kv;
+        int q0[2], head[2];
+        bool has_b;
+        int last[2];  // last key tile each query tile sees
+    };
+    auto decode = [&](int slot) {
+        const volatile int* p = items + 4 * slot;
+        Item it;
+        it.row0 = p[0];
+        it.len = p[1];
+        it.head[0] = p[3];
+        if (a.pair_heads) {
+            it.q0[0] = it.q0[1] = p[2] * 128;
+            it.head[1] = it.head[0] + 1;
+            it.has_b = true;
+        } else {
+            it.q0[0] = p[2] * 256;
+            it.q0[1] = it.q0[0] + 128;
+            it.head[1] = it.head[0];
+            it.has_b = it.q0[1] < it.len;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) it.last[x] = (min(it.q0[x] + 128, it.len) - 1) / BKV;
+        it.n_kv = it.has_b ? it.last[1] + 1 : it.last[0] + 1;
+        return it;
+    };
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], 4);  // one arrival per warp of the tile's warpgroup
+            mbar_init(&pv_done[x], 1);
+            mbar_init(&o_free[x], 4);
+            mbar_init(&item_full[x], 1);
+            mbar_init(&item_empty[x], 9);  // the MMA thread and the 8 softmax warps
+        }
+        mbar_init(drain, 1);
+        misc[1] = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&misc[0], 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    pdl_wait();  // the plan, and whatever wrote the inputs, is done
+
+    if (warp == 8) {
+        // ------------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+            const unsigned units = static_cast<unsigned>(a.units);
+            const unsigned total = a.plan[kPlanCount] * units;
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_phase = 0;
+            int q_loads = 0;
+            bool ok = true;
+            for (int k = 0;; ++k) {
+                const int slot = k & 1;
+                if (k >= 2 && !wait_bounded(&item_empty[slot], static_cast<uint32_t>((k - 2) >> 1) & 1u,
+                                            abort_flag, a.status, 0x411))
+                    ok = false;
+                unsigned item = total;
+                if (ok) item = atomicAdd(&a.plan[kPlanWork0], 1u);
+                if (item >= total) {
+                    items[4 * slot + 1] = 0;  // no sequence: the end
+                    mbar_arrive(&item_full[slot]);
+                    break;
+                }
+                {
+                    const int4 e = a.entries[item / units];
+                    items[4 * slot] = e.x;
+                    items[4 * slot + 1] = e.y;
+                    items[4 * slot + 2] = e.z;
+                    items[4 * slot + 3] = static_cast<int>(item % units) * (a.pair_heads ? 2 : 1);
+                }
+                mbar_arrive(&item_full[slot]);
+                const Item it = decode(slot);
+                const int kcol = it.head[0] / a.group * D;
+                // the previous item's S MMAs are done with the Q tiles
+                if (k >= 1 && !wait_bounded(q_empty, static_cast<uint32_t>(k - 1) & 1u, abort_flag,
+                                            a.status, 0x412))
+                    break;
+                mbar_arrive_expect_tx(q_full, (it.has_b ? 2 : 1) * C::QTILE);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    for (int b = 0; b < C::NB && (x == 0 || it.has_b); ++b)
+                        tma_load_3d(&tm_q, smem_u32(q_full),
+                                    smem_u32(sQ) + x * C::QTILE + b * 128 * kRowBytes,
+                                    it.head[x] * D + 64 * b, it.row0 + it.q0[x], 0);
+                ++q_loads;
+                for (int idx = 0; idx < 2 * it.n_kv; ++idx) {  // K_j = 2j, V_j = 2j + 1
+                    if (!wait_bounded(&kv_empty[stage], phase ^ 1u, abort_flag, a.status, 0x401)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&kv_full[stage], C::KVTILE);
+                    const uint32_t dst = smem_u32(ring) + stage * C::KVTILE;
+                    for (int b = 0; b < C::NB; ++b)
+                        tma_load_3d((idx & 1) ? &tm_v : &tm_k, smem_u32(&kv_full[stage]),
+                                    dst + b * BKV * kRowBytes, kcol + 64 * b, it.row0 + (idx >> 1) * BKV, 0);
+                    issued |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+            }
+            if (q_loads > 0) wait_drain(q_full, static_cast<uint32_t>(q_loads - 1) & 1u, a.status, 0x402);
+            for (int i = 0; i < S; ++i)
+                if (issued & (1u << i)) wait_drain(&kv_full[i], (issued_phase >> i) & 1u, a.status, 0x403);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_bf16_f32(128, BKV, false, false);
+            bool ok = true;
+            int rstage = 0;  // ring entries are taken in order, across items
+            uint32_t rphase = 0;
+            int gx[2] = {0, 0};  // S / P V MMAs of each tile over the items so far
+            int cx[2] = {0, 0};  // items each tile has taken part in
+            // wait for the next ring entry; returns its stage
+            auto acquire = [&](int site) -> int {
+                const int stage = rstage;
+                if (ok && !wait_bounded(&kv_full[stage], rphase, abort_flag, a.status, site)) ok = false;
+                tc_fence_after();
+                if (++rstage == S) {
+                    rstage = 0;
+                    rphase ^= 1u;
+                }
+                return stage;
+            };
+            int s_left = 0;  // S MMAs of the item still to issue
+            auto issue_s = [&](int x, int stage) {  // S_x = Q_x K^T
+                const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ) + x * C::QTILE, 16, 1024);
+                const uint64_t kdesc = smem_desc_sw128(smem_u32(ring) + stage * C::KVTILE, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma_f16(tmem + C::s_col(x), desc_add(qdesc, kmajor_step<128>(kk)),
+                               desc_add(kdesc, kmajor_step<BKV>(kk)), id_s, kk > 0 ? 1u : 0u);
+                tc_commit(&s_full[x]);
+                // the item's last S: once done, the Q tiles may be replaced
+                if (--s_left == 0) tc_commit(q_empty);
+            };
+            auto issue_pv = [&](int x, int j, int stage) {  // O_x (+)= P_x V
+                // the first P V of an item overwrites the previous item's O_x
+                if (ok && j == 0 && cx[x] >= 1 &&
+                    !wait_bounded(&o_free[x], static_cast<uint32_t>(cx[x] - 1) & 1u, abort_flag, a.status,
+                                  0x413 + x))
+                    ok = false;
+                if (ok && !wait_bounded(&p_full[x], static_cast<uint32_t>(gx[x] + j) & 1u, abort_flag,
+                                        a.status, 0x405 + x))
+                    ok = false;
+                if (!ok) return;
+                tc_fence_after();
+                // O_x (+)= P_x V: A = P_x from TMEM (packed over S_x's first
+                // columns), B = V (MN-major: d along the rows, keys down the box)
+                const uint64_t vdesc =
+                    smem_desc_sw128(smem_u32(ring) + stage * C::KVTILE, BKV * kRowBytes, 1024);
+                mma_ts_n_is_d<D, BKV / 16>(tmem + C::o_col(x), tmem + C::s_col(x), vdesc,
+                                           BKV * kRowBytes, j > 0, tmem + C::o_tail(x));
+                tc_commit(&pv_done[x]);
+            };
+            for (int k = 0; ok; ++k) {
+                const int slot = k & 1;
+                if (!wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag,
+                                  a.status, 0x415))
+                    break;
+                const Item it = decode(slot);
+                mbar_arrive(&item_empty[slot]);
+                if (it.len == 0) break;
+                if (!wait_bounded(q_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x404)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                s_left = it.last[0] + 1 + (it.has_b ? it.last[1] + 1 : 0);
+                // S of both tiles for key tile 0
+                int ks = acquire(0x407);
+                if (ok) {
+                    issue_s(0, ks);
+                    if (it.has_b) issue_s(1, ks);
+                    tc_commit(&kv_empty[ks]);
+                }
+                for (int j = 0; j < it.n_kv && ok; ++j) {
+                    const int vs = acquire(0x408);
+                    const bool more = j + 1 < it.n_kv;
+                    int kn = -1;
+                    if (j <= it.last[0]) {
+                        issue_pv(0, j, vs);
+                        if (ok && j + 1 <= it.last[0]) {
+                            kn = acquire(0x409);
+                            if (ok) issue_s(0, kn);
+                        }
+                    }
+                    if (it.has_b && ok) {
+                        issue_pv(1, j, vs);
+                        if (ok) tc_commit(&kv_empty[vs]);
+                        if (ok && more) {
+                            if (kn < 0) kn = acquire(0x40A);
+                            if (ok) issue_s(1, kn);
+                        }
+                    } else if (ok) {
+                        tc_commit(&kv_empty[vs]);
+                    }
+                    if (ok && kn >= 0) tc_commit(&kv_empty[kn]);
+                }
+                gx[0] += it.last[0] + 1;
+                cx[0] += 1;
+                if (it.has_b) {
+                    gx[1] += it.last[1] + 1;
+                    cx[1] += 1;
+                }
+            }
+            tc_commit(drain);
+            wait_drain(drain, 0, a.status, 0x40B);
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------- softmax warps
+        const int x = warp >> 2;               // tile: 0 = A, 1 = B
+        const int r = threadIdx.x & 127;       // row of the tile = TMEM lane
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t s_addr = lane_addr + C::s_col(x);
+        int gxl = 0;  // this tile's S / P V MMAs over the items so far
+        unsigned ring_at = 0;  // ring entries of the items so far
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const int slot = k & 1;
+            if (!warp_wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag,
+                                   a.status, 0x416))
+                break;
+            const Item it = decode(slot);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[slot]);
+            if (it.len == 0) break;
+            const unsigned ring0 = ring_at;  // ring entry of the item's K_0
+            ring_at += 2u * static_cast<unsigned>(it.n_kv);
+            if (x == 1 && !it.has_b) continue;  // no B tile in this item
+            const int q = (x ? it.q0[1] : it.q0[0]) + r;
+            const int head = x ? it.head[1] : it.head[0];
+            const int jl = x ? it.last[1] : it.last[0];
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j <= jl; ++j) {
+                if (!warp_wait_bounded(&s_full[x], static_cast<uint32_t>(gxl + j) & 1u, abort_flag,
+                                       a.status, 0x40C + x)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t v[SCH][32];
+#pragma unroll
+                for (int c = 0; c < SCH; ++c) tmem_ld32(s_addr + c * 32, v[c]);
+                tmem_wait_ld();
+                // causal mask where this key tile reaches past the row's query
+                const int k0 = j * BKV;
+                if (k0 + BKV - 1 > q) {
+#pragma unroll
+                    for (int c = 0; c < SCH; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (k0 + c * 32 + i > q) v[c][i] = __float_as_uint(-INFINITY);
+                }
+                // eight independent max / sum chains: the row is one thread's
+                // work, so its reductions must not be one serial chain
+                float mx8[8];
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) mx8[kk] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < SCH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx8[i & 7] = fmaxf(mx8[i & 7], __uint_as_float(v[c][i]));
+                const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                // the reference max only moves when the row max outgrows it by
+                // more than 2^8, so the O rescale below is rare.  A row whose
+                // keys in this tile are all masked (rows past the sequence end
+                // in a 64-key tile) keeps its reference.
+                const float m_new = fmaxf(m, mx * a.scale2);
+                const bool move = (j == 0 && m_new > -INFINITY) || m_new > m + kRescaleLog2;
+                const float alpha = move ? ex2(m - m_new) : 1.0f;
+                if (move) m = m_new;
+                uint64_t rs2[4];
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) rs2[kk] = 0ull;  // (0.0f, 0.0f)
+                const uint64_t scale2 = f32x2(a.scale2, a.scale2), neg_m = f32x2(-m, -m);
+                uint32_t pk[SCH][16];
+#pragma unroll
+                for (int c = 0; c < SCH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        // masked scores are -inf: 2^-inf = 0
+                        float x0, x1;
+                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
+                                              scale2, neg_m), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        rs2[i & 3] = add_f32x2(rs2[i & 3], f32x2(p0, p1));
+                        pk[c][i] = pack_bf16x2(p0, p1);
+                    }
+                float rsv[8];
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) f32x2_split(rs2[kk], rsv[2 * kk], rsv[2 * kk + 1]);
+                const float rs = ((rsv[0] + rsv[1]) + (rsv[2] + rsv[3])) + ((rsv[4] + rsv[5]) + (rsv[6] + rsv[7]));
+                l = fmaf(l, alpha, rs);
+                // S_x(j) was issued after P_x V of the previous key tile, and the
+                // commit that signalled S_x covers every earlier MMA: that P V
+                // has finished, so O_x is final and P_x's columns are free
+                if (j >= 1) {
+                    if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_addr + C::o_chunk(x, c), o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(lane_addr + C::o_chunk(x, c), o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // V rows behind the sequence's end
+                if (k0 + BKV > it.len) {
+                    const unsigned v_at = ring0 + 2u * static_cast<unsigned>(j) + 1u;
+                    const int vs = static_cast<int>(v_at % S);
+                    if (!warp_wait_bounded(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
+                        ok = false;
+                        break;
+                    }
+                    zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - k0, r, 128);
+                }
+                // P_x, packed bf16, over the first columns of S_x (already read)
+#pragma unroll
+                for (int c = 0; c < SCH; ++c) tmem_st16(s_addr + 16 * c, pk[c]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            if (!ok || !warp_wait_bounded(&pv_done[x], static_cast<uint32_t>(gxl + jl) & 1u, abort_flag,
+                                          a.status, 0x410 + x)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float inv = 1.0f / l;
+            const bool q_ok = q < it.len;
+            const long long tok = static_cast<long long>(it.row0) + q;
+            uint4* dst = reinterpret_cast<uint4*>(a.O + (tok * a.nh + head) * D);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(lane_addr + C::o_chunk(x, c), o);  // every lane: warp-collective
+                tmem_wait_ld();
+                if (q_ok) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 u;
+                        u.x = pack_bf16x2(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
+                        u.y = pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
+                        u.z = pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
+                        u.w = pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+                        dst[c * 4 + i] = u;
+                    }
+                }
+            }
+            if (q_ok) a.lse[head * a.T + tok] = m + lg2(l);
+            // O_x is in registers or on its way to memory: the MMA may reuse it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[x]);
+            gxl += jl + 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// CTAs of a persistent kernel: one per SM at most.
+unsigned persistent_grid(long long items, int sms) {
+    return static_cast<unsigned>(items < sms ? items : sms);
+}
+
+template <int D>
+cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& a,
+                       unsigned grid, cudaStream_t st) {
+    auto kern = packed_fwd_kernel<D>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(grid), dim3(kFwdThreads), FwdCfg<D>::SMEM, st, q, k, v, a);
+}
+
+}  // namespace
+
+int packed_attn_kv_rows(int d) { return d <= 128 ? 128 : 64; }
+
+cudaError_t launch_packed_forward(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, int d,
+                                  const PackedAttn& p, cudaStream_t st, int* launches) {
+    FwdArgs a{};
+    a.nh = p.nh;
+    a.group = p.nh / p.nkv;
+    a.pair_heads = a.group % 2 == 0;
+    a.units = a.pair_heads ? p.nh / 2 : p.nh;
+    a.T = p.T;
+    a.scale2 = 1.4426950408889634f * p.scale;
+    a.O = p.O;
+    a.lse = p.lse;
+    a.plan = p.plan;
+    a.entries = p.entries;
+    a.status = p.status;
+    const int tile = a.pair_heads ? 128 : 256;
+    cudaError_t e = launch_dependent(packed_plan_kernel, dim3(1), dim3(1024), 0, st, p.cu_seqlens, p.nb, p.T, tile,
+                                     p.entries, p.plan, p.ranks, p.status);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    const unsigned grid = persistent_grid((static_cast<long long>(p.T) / tile + p.nb) * a.units, p.sms);
+    switch (d) {
+        case 64: e = launch_fwd<64>(q, k, v, a, grid, st); break;
+        case 96: e = launch_fwd<96>(q, k, v, a, grid, st); break;
+        case 128: e = launch_fwd<128>(q, k, v, a, grid, st); break;
+        default: e = launch_fwd<160>(q, k, v, a, grid, st); break;
+    }
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+}  // namespace tpmlp

@@ -1,0 +1,126 @@
+// attn_packed.cuh -- work items of the packed attention kernels.
+//
+// A packed batch is a [T, heads, d] matrix of tokens in which sequence i owns
+// rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1.  The kernels' work is cut into
+// tiles of `tile` tokens of one sequence; the list of tiles is made on the
+// device, because the offsets live there: a sequence of n tiles has entries of
+// rank 1 .. n (rank = how many of the sequence's tiles a causal forward tile
+// sees, or how many see a key tile), and the list holds the highest ranks
+// first, so that the persistent kernels take the heaviest items first.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace tpmlp {
+namespace {
+
+constexpr int kPlanShared = 4096;  // ranks that one CTA counts in shared memory
+constexpr int kStatusShape = 2;    // TPMLP_ERR_SHAPE
+
+// The header words of a plan: item counters of the kernels that take its
+// items, and the number of entries.
+enum { kPlanWork0 = 0, kPlanWork1 = 1, kPlanCount = 2 };
+
+// Inclusive prefix sum over the CTA's threads; *total is the sum of all.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();  // the last call's sums have been read
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+        const int s = warp_sums[w];
+        before += w < warp ? s : 0;
+        all += s;
+    }
+    *total = all;
+    return v + before;
+}
+
+// One CTA (whole warps).  entries: {first row, length, rank - 1, tiles of the
+// sequence}; `ranks` holds T / tile + 2 words, used beyond kPlanShared ranks.
+// Offsets that leave [0, T] or fall make an empty list and set the device
+// status word.
+__device__ __forceinline__ void plan_block(const int* __restrict__ cu, int nb, int T, int tile,
+                                           int4* __restrict__ entries, unsigned* __restrict__ head,
+                                           int* __restrict__ ranks, int* status) {
+    __shared__ int s_count[kPlanShared + 1];
+    __shared__ int s_sums[32];
+    __shared__ int s_most, s_bad;
+    const int tid = threadIdx.x, nt = blockDim.x;
+    const int most = T / tile + 1;  // a sequence has at most this many tiles
+    int* count = most <= kPlanShared ? s_count : ranks;
+    for (int r = tid; r <= most; r += nt) count[r] = 0;
+    if (tid == 0) s_most = s_bad = 0;
+    __syncthreads();
+    for (int i = tid; i < nb; i += nt) {
+        const int a = cu[i], b = cu[i + 1];
+        if (a < 0 || b < a || b > T) {
+            s_bad = 1;
+        } else if (b > a) {
+            const int n = (b - a + tile - 1) / tile;
+            atomicAdd(&count[n], 1);
+            atomicMax(&s_most, n);
+        }
+    }
+    __syncthreads();
+    if (s_bad) {
+        if (tid == 0) {
+            head[kPlanWork0] = head[kPlanWork1] = head[kPlanCount] = 0u;
+            atomicExch(status, kStatusShape);
+        }
+        return;
+    }
+    // first[r]: entries of higher rank, i.e. over r' > r of sequences with >= r' tiles
+    int longer = 0, above = 0;
+    for (int top = s_most; top >= 1; top -= nt) {
+        const int r = top - tid;
+        int all;
+        const int c = longer + block_scan(r >= 1 ? count[r] : 0, s_sums, &all);
+        longer += all;
+        const int mine = r >= 1 ? c : 0;
+        const int upto = above + block_scan(mine, s_sums, &all);
+        above += all;
+        if (r >= 1) count[r] = upto - mine;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        head[kPlanWork0] = head[kPlanWork1] = 0u;
+        head[kPlanCount] = static_cast<unsigned>(above);
+    }
+    // a warp per sequence, or the whole CTA where there are fewer sequences
+    const int team = nb < nt / 32 ? nt : 32;
+    for (int i = tid / team; i < nb; i += nt / team) {
+        const int a = cu[i], len = cu[i + 1] - a, n = (len + tile - 1) / tile;
+        for (int r = 1 + tid % team; r <= n; r += team)
+            entries[atomicAdd(&count[r], 1)] = make_int4(a, len, r - 1, n);
+    }
+}
+
+// Zeroes rows first .. rows - 1 of an operand tile of NB 64-column boxes in
+// shared memory (a box row is 128 bytes whatever the swizzle does within it),
+// by `threads` threads, and makes the zeros visible to the tensor cores.
+// Rows behind a sequence's end belong to the next sequence: their weights are
+// exact zeros, but zero times an infinity or NaN of theirs would be NaN.
+template <int NB>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int rows, int first, int tid, int threads) {
+    const int chunks = (rows - first) * 8;  // 16-byte chunks of a box
+    for (int i = tid; i < NB * chunks; i += threads) {
+        const int b = i / chunks, c = i - b * chunks;
+        st_shared_v4(tile + static_cast<uint32_t>((b * rows + first) * kRowBytes + c * 16), 0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+}
+
+// The rounding of a pair of fp32 values times `f` to packed bf16.
+__device__ __forceinline__ uint32_t pack_scaled(uint32_t lo, uint32_t hi, float f) {
+    return pack_bf16x2(__uint_as_float(lo) * f, __uint_as_float(hi) * f);
+}
+
+}  // namespace
+}  // namespace tpmlp

@@ -14,6 +14,8 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "../../include/tpmlp.h"
 #include "kernels.h"
@@ -2277,6 +2279,324 @@ TPMLP_API int tp_head_loss_backward(const float* dloss, const tpmlp_bf16* X, con
     }
     return head_backward(dloss, X, W, reinterpret_cast<const long long*>(targets), lse, T, h, V, dX, dW,
                          workspace, p, st, d);
+}
+
+// ------------------------------- packed attention with grouped heads
+
+namespace tpmlp {
+namespace {
+
+constexpr long long kMostTokens = 1LL << 30;
+
+int check_packed(int nb, int T, int nh, int nkv, int d, float scale) {
+    if (nb < 0 || T < 0 || nb > kMostTokens || T > kMostTokens || nh < 1 || nkv < 1 || nh % nkv != 0 ||
+        !attn_head_dim_ok(d) || !(scale > 0.0f) || scale > 3.0e38f)
+        return TPMLP_ERR_SHAPE;
+    if (1LL * nh * d >= (1LL << 31) || (T / 128 + 1LL * nb) * nh >= (1LL << 31) || 1LL * T * nh > (1LL << 36))
+        return TPMLP_ERR_SHAPE;
+    return TPMLP_OK;
+}
+
+bool row_stride_ok(long long ld, long long cols, int multiple) { return ld >= cols && ld % multiple == 0; }
+
+// Header words, entries, ranks; behind them the backward pass's delta.
+struct PackedLayout {
+    size_t entries, ranks, delta, total;
+};
+
+PackedLayout packed_layout(int nb, int T, int nh, bool backward) {
+    const size_t tiles = static_cast<size_t>(T) / 128;
+    PackedLayout L;
+    L.entries = 256;
+    L.ranks = align256(L.entries + sizeof(int4) * (tiles + nb));
+    L.delta = align256(L.ranks + sizeof(int) * (tiles + 2));
+    L.total = backward ? align256(L.delta + sizeof(float) * static_cast<size_t>(T) * nh) : L.delta;
+    return L;
+}
+
+PackedAttn packed_params(const int* cu, int nb, int T, int nh, int nkv, float scale, void* workspace,
+                         const PackedLayout& L, const DeviceInfo& d) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PackedAttn p{};
+    p.cu_seqlens = cu;
+    p.nb = nb; p.T = T; p.nh = nh; p.nkv = nkv; p.sms = d.sms;
+    p.scale = scale;
+    p.plan = reinterpret_cast<unsigned*>(ws);
+    p.entries = reinterpret_cast<int4*>(ws + L.entries);
+    p.ranks = reinterpret_cast<int*>(ws + L.ranks);
+    p.status = d.status;
+    return p;
+}
+
+int token_map(CUtensorMap* m, const tpmlp_bf16* x, int T, int heads, int d, long long ld, int box_rows) {
+    return make_map(m, x, T, 1LL * heads * d, 1, ON_NONE, box_rows, ld);
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+TPMLP_API size_t tp_attn_packed_forward_workspace_bytes(int nb, int T, int nh, int nkv, int d) {
+    if (check_packed(nb, T, nh, nkv, d, 1.0f)) return 0;
+    return packed_layout(nb, T, nh, false).total;
+}
+
+TPMLP_API int tp_attn_packed_forward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16* K, long long ldk,
+                                     const tpmlp_bf16* V, long long ldv, const int* cu_seqlens, int nb, int T, int nh,
+                                     int nkv, int d, float scale, tpmlp_bf16* O, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    TPMLP_PROLOGUE(check_packed(nb, T, nh, nkv, d, scale));
+    if (!row_stride_ok(ldq, 1LL * nh * d, 8) || !row_stride_ok(ldk, 1LL * nkv * d, 8) ||
+        !row_stride_ok(ldv, 1LL * nkv * d, 8))
+        return TPMLP_ERR_SHAPE;
+    if (nb == 0 || T == 0) return TPMLP_OK;
+    if (any_null(Q, K, V, O, cu_seqlens, lse)) return TPMLP_ERR_NULL;
+    const PackedLayout L = packed_layout(nb, T, nh, false);
+    if (workspace == nullptr || workspace_bytes < L.total) return TPMLP_ERR_WORKSPACE;
+    if (!all_aligned(Q, K, V, O, lse, workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+        return TPMLP_ERR_ALIGN;
+    DeviceInfo dev;
+    if (int rc = enter(dev)) return rc;
+    CUtensorMap mq, mk, mv;
+    const int rows = packed_attn_kv_rows(d);
+    if (int rc = token_map(&mq, Q, T, nh, d, ldq, 128)) return rc;
+    if (int rc = token_map(&mk, K, T, nkv, d, ldk, rows)) return rc;
+    if (int rc = token_map(&mv, V, T, nkv, d, ldv, rows)) return rc;
+    PackedAttn p = packed_params(cu_seqlens, nb, T, nh, nkv, scale, workspace, L, dev);
+    p.O = reinterpret_cast<__nv_bfloat16*>(O);
+    p.lse = lse;
+    const cudaError_t e =
+        launch_packed_forward(mq, mk, mv, d, p, static_cast<cudaStream_t>(stream), &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+TPMLP_API size_t tp_attn_packed_backward_workspace_bytes(int nb, int T, int nh, int nkv, int d) {
+    if (check_packed(nb, T, nh, nkv, d, 1.0f)) return 0;
+    return packed_layout(nb, T, nh, true).total;
+}
+
+TPMLP_API int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16* K, long long ldk,
+                                      const tpmlp_bf16* V, long long ldv, const tpmlp_bf16* O, const float* lse,
+                                      const tpmlp_bf16* dO, const int* cu_seqlens, int nb, int T, int nh, int nkv,
+                                      int d, float scale, tpmlp_bf16* dQ, long long lddq, tpmlp_bf16* dK,
+                                      long long lddk, tpmlp_bf16* dV, long long lddv, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    TPMLP_PROLOGUE(check_packed(nb, T, nh, nkv, d, scale));
+    const long long qc = 1LL * nh * d, kc = 1LL * nkv * d;
+    if (!row_stride_ok(ldq, qc, 8) || !row_stride_ok(ldk, kc, 8) || !row_stride_ok(ldv, kc, 8) ||
+        !row_stride_ok(lddq, qc, 8) || !row_stride_ok(lddk, kc, 8) || !row_stride_ok(lddv, kc, 8))
+        return TPMLP_ERR_SHAPE;
+    if (nb == 0 || T == 0) return TPMLP_OK;
+    if (any_null(Q, K, V, O, dO, dQ, dK, dV, cu_seqlens, lse)) return TPMLP_ERR_NULL;
+    const PackedLayout L = packed_layout(nb, T, nh, true);
+    if (workspace == nullptr || workspace_bytes < L.total) return TPMLP_ERR_WORKSPACE;
+    if (!all_aligned(Q, K, V, O, dO, dQ, dK, dV, lse, workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+        return TPMLP_ERR_ALIGN;
+    DeviceInfo dev;
+    if (int rc = enter(dev)) return rc;
+    CUtensorMap q128, do128, k128, v128, qs, dos, ks, vs;
+    const int rows = packed_attn_stream_rows(d);
+    if (int rc = token_map(&q128, Q, T, nh, d, ldq, 128)) return rc;
+    if (int rc = token_map(&do128, dO, T, nh, d, qc, 128)) return rc;
+    if (int rc = token_map(&k128, K, T, nkv, d, ldk, 128)) return rc;
+    if (int rc = token_map(&v128, V, T, nkv, d, ldv, 128)) return rc;
+    qs = q128; dos = do128; ks = k128; vs = v128;
+    if (rows != 128) {
+        if (int rc = token_map(&qs, Q, T, nh, d, ldq, rows)) return rc;
+        if (int rc = token_map(&dos, dO, T, nh, d, qc, rows)) return rc;
+        if (int rc = token_map(&ks, K, T, nkv, d, ldk, rows)) return rc;
+        if (int rc = token_map(&vs, V, T, nkv, d, ldv, rows)) return rc;
+    }
+    PackedAttn p = packed_params(cu_seqlens, nb, T, nh, nkv, scale, workspace, L, dev);
+    p.O_in = cb(O);
+    p.lse_in = lse;
+    p.dO = cb(dO);
+    p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.delta);
+    p.dQ = reinterpret_cast<__nv_bfloat16*>(dQ);
+    p.dK = reinterpret_cast<__nv_bfloat16*>(dK);
+    p.dV = reinterpret_cast<__nv_bfloat16*>(dV);
+    p.ldq = lddq; p.ldk = lddk; p.ldv = lddv;
+    const cudaError_t e = launch_packed_backward(q128, do128, k128, v128, qs, dos, ks, vs, d, p,
+                                                 static_cast<cudaStream_t>(stream), &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+// ------------------------------- norms and rotation of queries and keys
+
+namespace tpmlp {
+namespace {
+
+int check_qk(int T, int nh, int nkv, int d, int rot, double theta, int dtype) {
+    if (T < 0 || T > kMostTokens || nh < 1 || nkv < 1 || d < 32 || d > 256 || d % 16 != 0 || rot < 0 || rot > d ||
+        rot % 16 != 0 || !(theta > 0.0) || theta > 1e300 || (dtype != TPMLP_BF16 && dtype != TPMLP_FP16 && dtype != TPMLP_FP32))
+        return TPMLP_ERR_SHAPE;
+    if ((1LL * nh + nkv) * d >= (1LL << 31) || 1LL * T * (1LL * nh + nkv) > (1LL << 36)) return TPMLP_ERR_SHAPE;
+    return TPMLP_OK;
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+TPMLP_API int tp_qk_norm_rope_forward(const void* Q, long long ldq, const void* K, long long ldk, const void* gamma_q,
+                                      const void* gamma_k, const int* positions, int T, int nh, int nkv, int d, int rot,
+                                      double theta, float eps, int dtype, void* Qo, long long ldqo, void* Ko,
+                                      long long ldko, float* rstd, void* stream) {
+    TPMLP_PROLOGUE(check_qk(T, nh, nkv, d, rot, theta, dtype));
+    if (!(eps > 0.0f) || eps > 3.0e38f) return TPMLP_ERR_SHAPE;
+    const int per16 = dtype == TPMLP_FP32 ? 4 : 8;
+    const long long qc = 1LL * nh * d, kc = 1LL * nkv * d;
+    if (!row_stride_ok(ldq, qc, per16) || !row_stride_ok(ldk, kc, per16) || !row_stride_ok(ldqo, qc, per16) ||
+        !row_stride_ok(ldko, kc, per16))
+        return TPMLP_ERR_SHAPE;
+    if (T == 0) return TPMLP_OK;
+    if (any_null(Q, K, gamma_q, gamma_k, positions, rstd, Qo, Ko)) return TPMLP_ERR_NULL;
+    if (!all_aligned(Q, K, gamma_q, gamma_k, Qo, Ko, rstd) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+        return TPMLP_ERR_ALIGN;
+    DeviceInfo dev;
+    if (int rc = enter(dev)) return rc;
+    QkNormRope p{};
+    p.dtype = dtype; p.T = T; p.nh = nh; p.nkv = nkv; p.d = d; p.rot = rot;
+    p.theta = theta; p.eps = eps;
+    p.q = Q; p.k = K; p.gamma_q = gamma_q; p.gamma_k = gamma_k; p.positions = positions;
+    p.out_q = Qo; p.out_k = Ko; p.rstd = rstd;
+    p.ldq = ldq; p.ldk = ldk; p.ldoq = ldqo; p.ldok = ldko;
+    const cudaError_t e = launch_qk_norm_rope_forward(p, static_cast<cudaStream_t>(stream), &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+TPMLP_API size_t tp_qk_norm_rope_backward_workspace_floats(int T, int nh, int nkv, int d) {
+    if (check_qk(T, nh, nkv, d, 0, 1.0, TPMLP_BF16) || T == 0) return 0;
+    return static_cast<size_t>(qk_norm_parts(T, nh + nkv, d)) * 2 * d;
+}
+
+TPMLP_API int tp_qk_norm_rope_backward(const void* dQo, long long lddqo, const void* dKo, long long lddko,
+                                       const void* Q, long long ldq, const void* K, long long ldk, const void* gamma_q,
+                                       const void* gamma_k, const int* positions, const float* rstd, int T, int nh,
+                                       int nkv, int d, int rot, double theta, int dtype, void* dQ, long long lddq,
+                                       void* dK, long long lddk, float* dgamma_q, float* dgamma_k, float* partial,
+                                       void* stream) {
+    TPMLP_PROLOGUE(check_qk(T, nh, nkv, d, rot, theta, dtype));
+    const int per16 = dtype == TPMLP_FP32 ? 4 : 8;
+    const long long qc = 1LL * nh * d, kc = 1LL * nkv * d;
+    if (!row_stride_ok(ldq, qc, per16) || !row_stride_ok(ldk, kc, per16) || !row_stride_ok(lddqo, qc, per16) ||
+        !row_stride_ok(lddko, kc, per16) || !row_stride_ok(lddq, qc, per16) || !row_stride_ok(lddk, kc, per16))
+        return TPMLP_ERR_SHAPE;
+    if (any_null(dgamma_q, dgamma_k) ||
+        (T > 0 && any_null(dQo, dKo, Q, K, gamma_q, gamma_k, positions, rstd, dQ, dK, partial)))
+        return TPMLP_ERR_NULL;
+    if (!all_aligned(dQo, dKo, Q, K, gamma_q, gamma_k, rstd, dQ, dK, dgamma_q, dgamma_k, partial) ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u))
+        return TPMLP_ERR_ALIGN;
+    DeviceInfo dev;
+    if (int rc = enter(dev)) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        cudaError_t e;
+        if ((e = cudaMemsetAsync(dgamma_q, 0, sizeof(float) * static_cast<size_t>(d), st)) != cudaSuccess ||
+            (e = cudaMemsetAsync(dgamma_k, 0, sizeof(float) * static_cast<size_t>(d), st)) != cudaSuccess)
+            return fail_cuda(e);
+        return TPMLP_OK;
+    }
+    QkNormRope p{};
+    p.dtype = dtype; p.T = T; p.nh = nh; p.nkv = nkv; p.d = d; p.rot = rot;
+    p.theta = theta;
+    p.q = Q; p.k = K; p.dy_q = dQo; p.dy_k = dKo;
+    p.gamma_q = gamma_q; p.gamma_k = gamma_k; p.positions = positions;
+    p.out_q = dQ; p.out_k = dK; p.rstd = const_cast<float*>(rstd); p.partial = partial;
+    p.ldq = ldq; p.ldk = ldk; p.ldyq = lddqo; p.ldyk = lddko; p.ldoq = lddq; p.ldok = lddk;
+    const cudaError_t e = launch_qk_norm_rope_backward(p, dgamma_q, dgamma_k, st, &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+// ------------------------------- global gradient norm and clipping
+
+namespace tpmlp {
+namespace {
+
+constexpr int kMostGrads = 1 << 20;
+
+int check_grads(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes, int n,
+                bool clip) {
+    if (n < 0 || n > kMostGrads) return TPMLP_ERR_SHAPE;
+    if (n > 0 && (any_null(grads, sizes, dtypes) || (clip && out == nullptr))) return TPMLP_ERR_NULL;
+    for (int i = 0; i < n; ++i) {
+        if (sizes[i] < 0 || sizes[i] > (1LL << 40) ||
+            (dtypes[i] != TPMLP_BF16 && dtypes[i] != TPMLP_FP16 && dtypes[i] != TPMLP_FP32))
+            return TPMLP_ERR_SHAPE;
+        if (sizes[i] == 0) continue;
+        if (grads[i] == nullptr || (clip && out[i] == nullptr)) return TPMLP_ERR_NULL;
+        const uintptr_t mask = dtypes[i] == TPMLP_FP32 ? 3u : 1u;
+        if ((reinterpret_cast<uintptr_t>(grads[i]) & mask) || (clip && (reinterpret_cast<uintptr_t>(out[i]) & mask)))
+            return TPMLP_ERR_ALIGN;
+    }
+    return TPMLP_OK;
+}
+
+// No output may share memory with another output or with another tensor's
+// gradient; it may be its own gradient.
+int check_outputs_apart(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes,
+                        int n) {
+    struct Span {
+        uintptr_t begin, end;
+        int owner;
+        bool written;
+    };
+    try {
+        std::vector<Span> spans;
+        spans.reserve(2 * static_cast<size_t>(n));
+        for (int i = 0; i < n; ++i) {
+            if (sizes[i] == 0) continue;
+            const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * (dtypes[i] == TPMLP_FP32 ? 4u : 2u);
+            const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(out[i]);
+            spans.push_back({o, o + bytes, i, true});
+            if (g != o) spans.push_back({g, g + bytes, i, false});
+        }
+        std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+        // the furthest end so far of a written span, and of any span
+        uintptr_t written_end = 0, any_end = 0;
+        for (const Span& s : spans) {
+            if (s.begin < (s.written ? any_end : written_end)) return TPMLP_ERR_SHAPE;
+            any_end = std::max(any_end, s.end);
+            if (s.written) written_end = std::max(written_end, s.end);
+        }
+    } catch (const std::bad_alloc&) {
+        return TPMLP_ERR_WORKSPACE;
+    }
+    return TPMLP_OK;
+}
+
+int grad_clip(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes, int n,
+              float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+    if (any_null(norm)) return TPMLP_ERR_NULL;
+    if (workspace == nullptr || workspace_bytes < sizeof(float2) * static_cast<size_t>(grad_partials(n)))
+        return TPMLP_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(norm) & 3u) || !aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    DeviceInfo dev;
+    if (int rc = enter(dev)) return rc;
+    const cudaError_t e = launch_grad_clip(grads, out, sizes, dtypes, n, max_norm, norm, static_cast<float2*>(workspace),
+                                           static_cast<cudaStream_t>(stream), &t_last_launches);
+    return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+TPMLP_API size_t tp_grad_workspace_bytes(int n) {
+    if (n < 0 || n > kMostGrads) return 0;
+    return sizeof(float2) * static_cast<size_t>(grad_partials(n));
+}
+
+TPMLP_API int tp_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes, int n, float* norm,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    TPMLP_PROLOGUE(check_grads(grads, nullptr, sizes, dtypes, n, false));
+    return grad_clip(grads, nullptr, sizes, dtypes, n, 0.0f, norm, workspace, workspace_bytes, stream);
+}
+
+TPMLP_API int tp_grad_clip(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes, int n,
+                           float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+    TPMLP_PROLOGUE(check_grads(grads, out, sizes, dtypes, n, true));
+    if (!(max_norm > 0.0f)) return TPMLP_ERR_SHAPE;
+    if (int rc = check_outputs_apart(grads, out, sizes, dtypes, n)) return rc;
+    return grad_clip(grads, out, sizes, dtypes, n, max_norm, norm, workspace, workspace_bytes, stream);
 }
 
 TPMLP_API const char* tp_mlp_status_string(int status) {

@@ -196,6 +196,65 @@ cudaError_t launch_attn_backward(const CUtensorMap& tm_qkv128, const CUtensorMap
                                  const CUtensorMap& tm_do128, const CUtensorMap& tm_do64, int d,
                                  const AttnParams& p, cudaStream_t st, int* launches);
 
+// Packed causal attention with grouped heads (attention_packed.cu,
+// attention_packed_backward.cu): Q [T, nh, d], K, V [T, nkv, d] through 3-D maps
+// {columns, T, 1} with 64-column boxes.  Head dims 64, 96, 128, 160.
+struct PackedAttn {
+    const int* cu_seqlens;       // [nb + 1], device
+    int nb, T, nh, nkv, sms;
+    float scale;
+    int4* entries;               // scratch: the plan (packed_attn_entries(nb, T, .) int4,
+    unsigned* plan;              // 4 header words, T / 128 + 2 ranks)
+    int* ranks;
+    __nv_bfloat16* O;            // forward: [T, nh, d]
+    float* lse;                  // forward: [nh, T], log2 domain
+    const __nv_bfloat16* O_in;   // backward: the forward's O and lse, and dO [T, nh, d]
+    const float* lse_in;
+    const __nv_bfloat16* dO;
+    float* delta;                // backward: scratch [nh, T]
+    __nv_bfloat16 *dQ, *dK, *dV; // backward: outputs, rows ldq, ldk, ldv values apart
+    long long ldq, ldk, ldv;
+    int* status;
+};
+// Rows of the forward's K and V boxes (its Q boxes have 128).
+int packed_attn_kv_rows(int d);
+cudaError_t launch_packed_forward(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, int d,
+                                  const PackedAttn& p, cudaStream_t st, int* launches);
+// Rows of the backward's streamed boxes: K and V in the dQ kernel, Q and dO in
+// the dK/dV kernel (the other operands' boxes have 128).
+int packed_attn_stream_rows(int d);
+cudaError_t launch_packed_backward(const CUtensorMap& q128, const CUtensorMap& do128, const CUtensorMap& k128,
+                                   const CUtensorMap& v128, const CUtensorMap& q_stream,
+                                   const CUtensorMap& do_stream, const CUtensorMap& k_stream,
+                                   const CUtensorMap& v_stream, int d, const PackedAttn& p, cudaStream_t st,
+                                   int* launches);
+
+// Norms of queries and keys per head with the rotary rotation (qk_norm_rope.cu).
+// dtype: TPMLP_BF16 / FP16 / FP32.  Tokens of each matrix are ld* values apart.
+struct QkNormRope {
+    int dtype, T, nh, nkv, d, rot;
+    double theta;
+    float eps;
+    const void *q, *k, *dy_q, *dy_k, *gamma_q, *gamma_k;
+    const int* positions;
+    void *out_q, *out_k;  // forward: y; backward: dx
+    float* rstd;          // [T, nh + nkv]
+    float* partial;       // backward: qk_norm_parts(T, nh + nkv, d) * 2 d floats
+    long long ldq, ldk, ldyq, ldyk, ldoq, ldok;
+};
+constexpr int kQkMaxParts = 608;  // CTAs of the backward kernel: 4 on each of 152 SMs
+int qk_norm_parts(int T, int heads, int d);
+cudaError_t launch_qk_norm_rope_forward(const QkNormRope& p, cudaStream_t st, int* launches);
+cudaError_t launch_qk_norm_rope_backward(const QkNormRope& p, float* dgamma_q, float* dgamma_k, cudaStream_t st,
+                                         int* launches);
+
+// Global gradient norm, and clipping where `out` is given (grad_clip.cu).  The
+// arrays are host memory; `partial` holds grad_partials(n) float2.
+constexpr int kClipCtas = 912;  // CTAs of a launch: 6 on each of 152 SMs
+long long grad_partials(int n);
+cudaError_t launch_grad_clip(const void* const* in, void* const* out, const long long* sizes, const int* dtypes, int n,
+                             float max_norm, float* norm, float2* partial, cudaStream_t st, int* launches);
+
 // `grid` is the number of work units wanted (CTAs, or CTA pairs when PAIR).
 // With static units it is clipped to what can be resident at once, so the
 // persistent loop never waits for a second wave of CTAs; with dynamic units
