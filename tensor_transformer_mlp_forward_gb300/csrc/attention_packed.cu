@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             bool ok = true;
             for (int k = 0;; ++k) {
                 const int slot = k & 1;
-                if (k >= 2 && !wait_bounded(&item_empty[slot], static_cast<uint32_t>((k - 2) >> 1) & 1u,
+                if (k >= 2 && !thread_wait(&item_empty[slot], static_cast<uint32_t>((k - 2) >> 1) & 1u,
                                             abort_flag, a.status, 0x411))
                     ok = false;
                 unsigned item = total;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const Item it = decode(slot);
                 const int kcol = it.head[0] / a.group * D;
                 // the previous item's S MMAs are done with the Q tiles
-                if (k >= 1 && !wait_bounded(q_empty, static_cast<uint32_t>(k - 1) & 1u, abort_flag,
+                if (k >= 1 && !thread_wait(q_empty, static_cast<uint32_t>(k - 1) & 1u, abort_flag,
                                             a.status, 0x412))
                     break;
                 mbar_arrive_expect_tx(q_full, (it.has_b ? 2 : 1) * C::QTILE);
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                     it.head[x] * D + 64 * b, it.row0 + it.q0[x], 0);
                 ++q_loads;
                 for (int idx = 0; idx < 2 * it.n_kv; ++idx) {  // K_j = 2j, V_j = 2j + 1
-                    if (!wait_bounded(&kv_empty[stage], phase ^ 1u, abort_flag, a.status, 0x401)) {
+                    if (!thread_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.status, 0x401)) {
                         ok = false;
                         break;
                     }
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // wait for the next ring entry; returns its stage
             auto acquire = [&](int site) -> int {
                 const int stage = rstage;
-                if (ok && !wait_bounded(&kv_full[stage], rphase, abort_flag, a.status, site)) ok = false;
+                if (ok && !thread_wait(&kv_full[stage], rphase, abort_flag, a.status, site)) ok = false;
                 tc_fence_after();
                 if (++rstage == S) {
                     rstage = 0;
@@ -243,10 +243,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             auto issue_pv = [&](int x, int j, int stage) {  // O_x (+)= P_x V
                 // the first P V of an item overwrites the previous item's O_x
                 if (ok && j == 0 && cx[x] >= 1 &&
-                    !wait_bounded(&o_free[x], static_cast<uint32_t>(cx[x] - 1) & 1u, abort_flag, a.status,
+                    !thread_wait(&o_free[x], static_cast<uint32_t>(cx[x] - 1) & 1u, abort_flag, a.status,
                                   0x413 + x))
                     ok = false;
-                if (ok && !wait_bounded(&p_full[x], static_cast<uint32_t>(gx[x] + j) & 1u, abort_flag,
+                if (ok && !thread_wait(&p_full[x], static_cast<uint32_t>(gx[x] + j) & 1u, abort_flag,
                                         a.status, 0x405 + x))
                     ok = false;
                 if (!ok) return;
@@ -261,13 +261,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             };
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
-                if (!wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag,
+                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag,
                                   a.status, 0x415))
                     break;
                 const Item it = decode(slot);
                 mbar_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
-                if (!wait_bounded(q_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x404)) {
+                if (!thread_wait(q_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x404)) {
                     ok = false;
                     break;
                 }
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int slot = k & 1;
-            if (!warp_wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag,
+            if (!warp_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag,
                                    a.status, 0x416))
                 break;
             const Item it = decode(slot);
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int jl = x ? it.last[1] : it.last[0];
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j <= jl; ++j) {
-                if (!warp_wait_bounded(&s_full[x], static_cast<uint32_t>(gxl + j) & 1u, abort_flag,
+                if (!warp_wait(&s_full[x], static_cast<uint32_t>(gxl + j) & 1u, abort_flag,
                                        a.status, 0x40C + x)) {
                     ok = false;
                     break;
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (k0 + BKV > it.len) {
                     const unsigned v_at = ring0 + 2u * static_cast<unsigned>(j) + 1u;
                     const int vs = static_cast<int>(v_at % S);
-                    if (!warp_wait_bounded(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
+                    if (!warp_wait(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
                         ok = false;
                         break;
                     }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
-            if (!ok || !warp_wait_bounded(&pv_done[x], static_cast<uint32_t>(gxl + jl) & 1u, abort_flag,
+            if (!ok || !warp_wait(&pv_done[x], static_cast<uint32_t>(gxl + jl) & 1u, abort_flag,
                                           a.status, 0x410 + x)) {
                 ok = false;
                 break;

@@ -42,23 +42,34 @@ struct BwdCfg {
     static constexpr int HALF = BS / 2;                     // columns of a tile a softmax warp owns
     static constexpr int OWN = NB * 128 * kRowBytes;        // a resident operand: 128 rows
     static constexpr int STREAM = NB * BS * kRowBytes;      // a streamed operand
-    static constexpr int STATS = 8 * 2 * HALF * 4;          // lse and delta of each warp's columns
+    static constexpr int STATS = 2 * 2 * 2 * HALF * 4;      // two tiles' lse and delta, by halves
     static constexpr int BARS = 512;
-    static constexpr int FIXED = 2 * OWN + STATS + BARS;
-    static constexpr int FIT = (226 * 1024 - FIXED) / (2 * STREAM);
-    static constexpr int STAGES = FIT > 4 ? 4 : FIT;
-    static constexpr int SMEM = 1024 + FIXED + STAGES * 2 * STREAM;
-    static_assert(STAGES >= 2, "two stages at least");
-    // Tensor memory.  Tiles: S (or S^T) at 0, dP (or dP^T) at BS.  The packed
-    // P or dS of softmax half w overlays the first columns of that half's fp32
-    // columns, at HALF w.  Accumulators of N >= 128 start on multiples of 128,
-    // with the 32-column tails of d = 160 at 384 and 416 (dK/dV) or 256 and 288 (dQ).
-    static constexpr uint32_t kS = 0, kP = BS;
+    // Rings of the streamed operands: FAR holds the one whose last use is a tile behind
+    // its first (K for dQ, Q for dK), NEAR the other.  Three and two slots for d = 96
+    // and 128 are all that fits, and what keeps a load a tile ahead of its use.
+    static constexpr int FIT = (227 * 1024 - 2 * OWN - STATS - BARS) / STREAM;
+    static constexpr int NEAR = FIT / 2 > 4 ? 4 : FIT / 2;
+    static constexpr int FAR = FIT - NEAR > 4 ? 4 : FIT - NEAR;
+    static constexpr int SMEM = 2 * OWN + (FAR + NEAR) * STREAM + STATS + BARS;
+    static_assert(NEAR >= 2 && FAR >= 3, "slots");
+    // Tensor memory.  Packed P or dS of softmax half w overlays the first columns of
+    // that half's fp32 columns, at HALF w.  Accumulators of N >= 128 start on
+    // multiples of 128.  dQ kernel: S, two dP, dQ; dK/dV kernel: S^T, dP^T, dV, dK.
+    static constexpr uint32_t kS = 0;
+    static constexpr uint32_t dp(int b) { return BS * (1u + b); }
+    static constexpr uint32_t kDQ = D <= 128 ? 384 : 256;
+    static constexpr uint32_t kDQTail = D <= 128 ? kDQ + (D / 64) * 64 : 384;
     static constexpr uint32_t acc(int x) { return D <= 128 ? 256u + 128u * x : 128u + 128u * x; }
     static constexpr uint32_t acc_tail(int x) { return D <= 128 ? acc(x) + (D / 64) * 64 : 384u + 32u * x; }
-    static constexpr uint32_t dq(int x) { return D <= 128 ? 256u + 128u * x : 128u + 256u * x; }
-    static constexpr uint32_t dq_tail(int x) { return D <= 128 ? dq(x) + (D / 64) * 64 : 256u + 32u * x; }
 };
+
+// The kernels' tiles start on 1024-byte boundaries (the swizzle's period), and their
+// shared memory leaves no room to look for one.
+__device__ __forceinline__ bool tiles_aligned(const uint8_t* smem, int* status) {
+    if ((smem_u32(smem) & 1023u) == 0) return true;
+    if (threadIdx.x == 0) atomicExch(status, kStatusTimeout);
+    return false;
+}
 
 struct BwdArgs {
     const int4* entries;
@@ -71,6 +82,29 @@ struct BwdArgs {
     __nv_bfloat16 *dQ, *dK, *dV;
     long long ldq, ldk, ldv;
     int* status;
+};
+
+// A role's place in a ring of N slots.
+template <int N>
+struct RingSlot {
+    int at = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+    // the producer's: remembers the copy it has started
+    __device__ __forceinline__ void issue() {
+        issued |= 1u << at;
+        issued_phase = (issued_phase & ~(1u << at)) | (phase << at);
+        next();
+    }
+    __device__ __forceinline__ void drain(uint64_t* full, int* status, int site) {
+        for (int i = 0; i < N; ++i)
+            if (issued & (1u << i)) wait_drain(&full[i], (issued_phase >> i) & 1u, status, site);
+    }
 };
 
 // D (+)= A B^T with A the packed bf16 halves of a tile in tensor memory (half w at
@@ -110,6 +144,62 @@ __device__ __forceinline__ void tmem_ld_half(uint32_t addr, uint32_t (&v)[HALF /
 #pragma unroll
     for (int c = 0; c < HALF / 32; ++c) tmem_ld32(addr + 32 * c, v[c]);
     tmem_wait_ld();
+}
+
+// The same value, or the columns' own (in shared memory, the same for every lane), as
+// pairs for columns 4 i .. 4 i + 3.
+struct OneValue {
+    uint64_t v;
+    __device__ __forceinline__ ulonglong2 operator()(int) const { return make_ulonglong2(v, v); }
+};
+struct ColumnValues {
+    const float* p;
+    __device__ __forceinline__ ulonglong2 operator()(int i) const {
+        return reinterpret_cast<const ulonglong2*>(p)[i];
+    }
+};
+
+__device__ __forceinline__ uint64_t pair_of(const uint32_t (&v)[32], int i) {
+    return f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+}
+
+// x = scale2 s + neg_lse, p = 2^x of 32 columns of a row.  With MASK, columns c, c + 1,
+// ... outside [lo, hi) give an exact zero whatever s holds.
+template <bool MASK, typename Lse>
+__device__ __forceinline__ void weights(const uint32_t (&v)[32], uint64_t scale2, Lse neg_lse, int c, int lo, int hi,
+                                        float (&p)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const ulonglong2 l = neg_lse(i / 4);
+        float x[4];
+        f32x2_split(fma_f32x2(pair_of(v, i), scale2, l.x), x[0], x[1]);
+        f32x2_split(fma_f32x2(pair_of(v, i + 2), scale2, l.y), x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (MASK && (c + i + e < lo || c + i + e >= hi)) x[e] = -INFINITY;
+            p[i + e] = ex2(x[e]);
+        }
+    }
+}
+
+// dS = p (dP + neg_delta), packed; masked columns are exact zeros here too.
+template <bool MASK, typename Delta>
+__device__ __forceinline__ void score_grads(const uint32_t (&v)[32], const float (&p)[32], Delta neg_dlt, int c, int lo,
+                                            int hi, uint32_t (&dd)[16]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const ulonglong2 l = neg_dlt(i / 4);
+        float x[4];
+        f32x2_split(mul_f32x2(f32x2(p[i], p[i + 1]), add_f32x2(pair_of(v, i), l.x)), x[0], x[1]);
+        f32x2_split(mul_f32x2(f32x2(p[i + 2], p[i + 3]), add_f32x2(pair_of(v, i + 2), l.y)), x[2], x[3]);
+        if (MASK) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + i + e < lo || c + i + e >= hi) x[e] = 0.0f;
+        }
+        dd[i / 2] = pack_bf16x2(x[0], x[1]);
+        dd[i / 2 + 1] = pack_bf16x2(x[2], x[3]);
+    }
 }
 
 // Reads chunks [c0, c1) of 32 accumulator columns of this thread's row, scales and
@@ -155,33 +245,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                      const BwdArgs a) {
     pdl_launch_dependents();
     using C = BwdCfg<D>;
-    constexpr int S = C::STAGES, BS = C::BS, HALF = C::HALF;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    constexpr int FAR = C::FAR, NEAR = C::NEAR, BS = C::BS, HALF = C::HALF;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (!tiles_aligned(smem, a.status)) return;
     uint8_t* sQ = smem;
     uint8_t* sdO = sQ + C::OWN;
-    uint8_t* ring = sdO + C::OWN;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S * 2 * C::STREAM + C::STATS);
+    uint8_t* sK = sdO + C::OWN;           // [FAR]
+    uint8_t* sV = sK + FAR * C::STREAM;   // [NEAR]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NEAR * C::STREAM + C::STATS);
     uint64_t* q_full = bars;              // the item's Q has landed
     uint64_t* q_empty = bars + 1;         // its last S has read it
     uint64_t* do_full = bars + 2;         // the same for dO and dP
     uint64_t* do_empty = bars + 3;
     uint64_t* s_full = bars + 4;          // S is complete
     uint64_t* s_read = bars + 5;          // the softmax warps have read it
-    uint64_t* dp_full = bars + 6;         // dP is complete
-    uint64_t* ds_full = bars + 7;         // dS is in its place
-    uint64_t* dq_done = bars + 8;         // [2] the item's dQ is complete
-    uint64_t* dq_free = bars + 10;        // [2] the softmax warps have read it out
+    uint64_t* dq_done = bars + 6;         // the item's dQ is complete
+    uint64_t* dq_free = bars + 7;         // the softmax warps have read it out
+    uint64_t* dp_full = bars + 8;         // [2] dP is complete
+    uint64_t* ds_full = bars + 10;        // [2] dS is in its place
     uint64_t* item_full = bars + 12;      // [2]
     uint64_t* item_empty = bars + 14;     // [2]
     uint64_t* drain = bars + 16;
-    uint64_t* kv_full = bars + 17;        // [S]
-    uint64_t* kv_empty = kv_full + S;     // [S]
-    int* items = reinterpret_cast<int*>(bars + 17 + 2 * 4);  // [2] x {first row, length, tile, head}
+    uint64_t* k_full = bars + 17;         // [FAR]
+    uint64_t* k_empty = bars + 21;
+    uint64_t* v_full = bars + 25;         // [NEAR]
+    uint64_t* v_empty = bars + 29;
+    int* items = reinterpret_cast<int*>(bars + 33);  // [2] x {first row, length, tile, head}
     uint32_t* misc = reinterpret_cast<uint32_t*>(items + 8);
     volatile uint32_t* abort_flag = misc + 1;
-    static_assert((17 + 8) * 8 + 8 * 4 + 8 <= C::BARS, "barrier space");
+    static_assert(33 * 8 + 8 * 4 + 8 <= C::BARS && FAR <= 4 && NEAR <= 4, "barrier space");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     struct Item {
@@ -205,17 +297,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_init(do_empty, 1);
         mbar_init(s_full, 1);
         mbar_init(s_read, 8);
-        mbar_init(dp_full, 1);
-        mbar_init(ds_full, 8);
+        mbar_init(dq_done, 1);
+        mbar_init(dq_free, 8);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&dq_done[b], 1);
-            mbar_init(&dq_free[b], 8);
+            mbar_init(&dp_full[b], 1);
+            mbar_init(&ds_full[b], 8);
             mbar_init(&item_full[b], 1);
             mbar_init(&item_empty[b], 9);  // the MMA thread and the 8 softmax warps
         }
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+        for (int i = 0; i < FAR; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < NEAR; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
         mbar_init(drain, 1);
         misc[1] = 0u;
@@ -239,13 +335,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
             const unsigned total = a.plan[kPlanCount] * static_cast<unsigned>(a.nh);
-            int stage = 0;
-            uint32_t phase = 0, issued = 0, issued_phase = 0;
+            RingSlot<FAR> ks;
+            RingSlot<NEAR> vs;
             int q_loads = 0, do_loads = 0;
             bool ok = true;
             for (int k = 0;; ++k) {
                 const int slot = k & 1;
-                if (k >= 2 && !wait_bounded(&item_empty[slot], static_cast<uint32_t>((k - 2) >> 1) & 1u, abort_flag,
+                if (k >= 2 && !thread_wait(&item_empty[slot], static_cast<uint32_t>((k - 2) >> 1) & 1u, abort_flag,
                                             a.status, 0x511))
                     ok = false;
                 unsigned item = total;
@@ -267,32 +363,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const int qcol = it.head * D, kcol = it.head / a.group * D, row = it.row0 + it.q0;
                 const uint32_t before = static_cast<uint32_t>(k - 1) & 1u;
                 // Q goes first: the next S needs it while dP still needs the last dO
-                if (k >= 1 && !wait_bounded(q_empty, before, abort_flag, a.status, 0x512)) break;
+                if (k >= 1 && !thread_wait(q_empty, before, abort_flag, a.status, 0x512)) break;
                 mbar_arrive_expect_tx(q_full, C::OWN);
                 for (int b = 0; b < C::NB; ++b)
                     tma_load_3d(&tm_q, smem_u32(q_full), smem_u32(sQ) + b * 128 * kRowBytes, qcol + 64 * b, row, 0);
                 ++q_loads;
                 for (int j = 0; j < it.n_kv; ++j) {
-                    if (!wait_bounded(&kv_empty[stage], phase ^ 1u, abort_flag, a.status, 0x501)) {
+                    if (!thread_wait(&k_empty[ks.at], ks.phase ^ 1u, abort_flag, a.status, 0x501)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&kv_full[stage], 2 * C::STREAM);
-                    const uint32_t dst = smem_u32(ring) + stage * 2 * C::STREAM;
-                    for (int b = 0; b < C::NB; ++b) {
-                        tma_load_3d(&tm_k, smem_u32(&kv_full[stage]), dst + b * BS * kRowBytes, kcol + 64 * b,
+                    mbar_arrive_expect_tx(&k_full[ks.at], C::STREAM);
+                    for (int b = 0; b < C::NB; ++b)
+                        tma_load_3d(&tm_k, smem_u32(&k_full[ks.at]),
+                                    smem_u32(sK) + ks.at * C::STREAM + b * BS * kRowBytes, kcol + 64 * b,
                                     it.row0 + j * BS, 0);
-                        tma_load_3d(&tm_v, smem_u32(&kv_full[stage]), dst + C::STREAM + b * BS * kRowBytes,
-                                    kcol + 64 * b, it.row0 + j * BS, 0);
-                    }
-                    issued |= 1u << stage;
-                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    ks.issue();
                     if (j == 0) {
-                        if (k >= 1 && !wait_bounded(do_empty, before, abort_flag, a.status, 0x513)) {
+                        if (k >= 1 && !thread_wait(do_empty, before, abort_flag, a.status, 0x513)) {
                             ok = false;
                             break;
                         }
@@ -302,14 +390,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                         row, 0);
                         ++do_loads;
                     }
+                    if (!thread_wait(&v_empty[vs.at], vs.phase ^ 1u, abort_flag, a.status, 0x517)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&v_full[vs.at], C::STREAM);
+                    for (int b = 0; b < C::NB; ++b)
+                        tma_load_3d(&tm_v, smem_u32(&v_full[vs.at]),
+                                    smem_u32(sV) + vs.at * C::STREAM + b * BS * kRowBytes, kcol + 64 * b,
+                                    it.row0 + j * BS, 0);
+                    vs.issue();
                 }
                 if (!ok) break;
             }
             // every copy this thread started lands before the CTA may exit
             if (q_loads > 0) wait_drain(q_full, static_cast<uint32_t>(q_loads - 1) & 1u, a.status, 0x502);
             if (do_loads > 0) wait_drain(do_full, static_cast<uint32_t>(do_loads - 1) & 1u, a.status, 0x503);
-            for (int i = 0; i < S; ++i)
-                if (issued & (1u << i)) wait_drain(&kv_full[i], (issued_phase >> i) & 1u, a.status, 0x504);
+            ks.drain(k_full, a.status, 0x504);
+            vs.drain(v_full, a.status, 0x518);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -317,79 +415,77 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (lane == 0) {
             const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t dodesc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
-            int stage = 0, g = 0;  // g: tiles so far
-            uint32_t phase = 0;
+            int g = 0;  // tiles so far
+            RingSlot<FAR> ks;
+            RingSlot<NEAR> vs;
             bool ok = true;
             // the tile whose dQ product is still to be issued
-            int last_stage = 0, last_k = -1;
+            int last_slot = 0, last_k = -1;
             bool last_first = false, last_final = false;
-            auto issue_dq = [&]() {  // dQ += dS K of tile g - 1
+            auto issue_dq = [&](int tile) {  // dQ += dS K
                 if (last_k < 0 || !ok) return;
-                const int x = last_k & 1;
-                if (last_first && last_k >= 2 &&
-                    !wait_bounded(&dq_free[x], static_cast<uint32_t>((last_k - 2) >> 1) & 1u, abort_flag, a.status,
-                                  0x514)) {
-                    ok = false;
-                    return;
-                }
-                if (!wait_bounded(ds_full, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x505)) {
+                const int b = tile & 1;
+                // the first product of an item overwrites the last item's dQ
+                if ((last_first && last_k >= 1 &&
+                     !thread_wait(dq_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x514)) ||
+                    !thread_wait(&ds_full[b], static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, a.status, 0x505)) {
                     ok = false;
                     return;
                 }
                 tc_fence_after();
-                const uint64_t kdesc =
-                    smem_desc_sw128(smem_u32(ring) + last_stage * 2 * C::STREAM, BS * kRowBytes, 1024);
-                mma_halves<D>(tmem + C::dq(x), tmem + C::dq_tail(x), tmem + C::kP, kdesc, !last_first);
-                tc_commit(&kv_empty[last_stage]);
-                if (last_final) tc_commit(&dq_done[x]);
+                mma_halves<D>(tmem + C::kDQ, tmem + C::kDQTail, tmem + C::dp(b),
+                              smem_desc_sw128(smem_u32(sK) + last_slot * C::STREAM, BS * kRowBytes, 1024),
+                              !last_first);
+                tc_commit(&k_empty[last_slot]);
+                if (last_final) tc_commit(dq_done);
                 last_k = -1;
             };
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
-                if (!wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x515))
+                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x515))
                     break;
                 const Item it = decode(slot);
                 mbar_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
                 for (int j = 0; j < it.n_kv && ok; ++j) {
+                    const uint32_t item_parity = static_cast<uint32_t>(k) & 1u;
                     // where the next item's Q is still on its way, the last dQ goes first
-                    if (j == 0 && !mbar_test(q_full, static_cast<uint32_t>(k) & 1u)) issue_dq();
+                    if (j == 0 && !mbar_test(q_full, item_parity)) issue_dq(g - 1);
                     if (!ok) break;
-                    if ((j == 0 && !wait_bounded(q_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x506)) ||
-                        !wait_bounded(&kv_full[stage], phase, abort_flag, a.status, 0x507) ||
+                    if ((j == 0 && !thread_wait(q_full, item_parity, abort_flag, a.status, 0x506)) ||
+                        !thread_wait(&k_full[ks.at], ks.phase, abort_flag, a.status, 0x507) ||
                         (g > 0 &&
-                         !wait_bounded(s_read, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x508))) {
+                         !thread_wait(s_read, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x508))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t kv = smem_u32(ring) + stage * 2 * C::STREAM;
-                    mma_scores<D>(tmem + C::kS, qdesc, smem_desc_sw128(kv, 16, 1024));
+                    mma_scores<D>(tmem + C::kS, qdesc, smem_desc_sw128(smem_u32(sK) + ks.at * C::STREAM, 16, 1024));
                     tc_commit(s_full);
                     if (j == it.n_kv - 1) tc_commit(q_empty);
-                    issue_dq();  // reads dS, which lies over the last dP
-                    if (!ok) break;
-                    if (j == 0 &&
-                        !wait_bounded(do_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x509)) {
+                    if ((j == 0 && !thread_wait(do_full, item_parity, abort_flag, a.status, 0x509)) ||
+                        !thread_wait(&v_full[vs.at], vs.phase, abort_flag, a.status, 0x519)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    mma_scores<D>(tmem + C::kP, dodesc, smem_desc_sw128(kv + C::STREAM, 16, 1024));
-                    tc_commit(dp_full);
+                    // over the dS of the tile before the last, whose dQ has been issued
+                    mma_scores<D>(tmem + C::dp(g & 1), dodesc,
+                                  smem_desc_sw128(smem_u32(sV) + vs.at * C::STREAM, 16, 1024));
+                    tc_commit(&dp_full[g & 1]);
+                    tc_commit(&v_empty[vs.at]);
                     if (j == it.n_kv - 1) tc_commit(do_empty);
-                    last_stage = stage;
+                    issue_dq(g - 1);
+                    last_slot = ks.at;
                     last_k = k;
                     last_first = j == 0;
                     last_final = j == it.n_kv - 1;
+                    ks.next();
+                    vs.next();
                     ++g;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
             }
-            issue_dq();
+            issue_dq(g - 1);
             tc_commit(drain);
             wait_drain(drain, 0, a.status, 0x50A);
         }
@@ -401,7 +497,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         constexpr int CH = D / 32, MID = (CH + 1) / 2;  // dQ chunks of half 0: [0, MID)
         bool ok = true;
-        int g = 0, stage = 0;
+        int g = 0, k_slot = 0;
         struct Pending {
             int k, head;
             bool q_ok;
@@ -409,21 +505,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         };
         Pending pend{-1, 0, false, 0};
         auto readout = [&]() -> bool {
-            const int x = pend.k & 1;
-            if (!warp_wait_bounded(&dq_done[x], static_cast<uint32_t>(pend.k >> 1) & 1u, abort_flag, a.status, 0x50B))
+            if (!warp_wait(dq_done, static_cast<uint32_t>(pend.k) & 1u, abort_flag, a.status, 0x50B))
                 return false;
             tc_fence_after();
-            read_out<D>(lane_addr + C::dq(x), lane_addr + C::dq_tail(x), w ? MID : 0, w ? CH : MID, a.scale, pend.q_ok,
+            read_out<D>(lane_addr + C::kDQ, lane_addr + C::kDQTail, w ? MID : 0, w ? CH : MID, a.scale, pend.q_ok,
                         a.dQ + pend.tok * a.ldq + pend.head * D);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&dq_free[x]);
+            if (lane == 0) mbar_arrive(dq_free);
             pend.k = -1;
             return true;
         };
         for (int k = 0; ok; ++k) {
             const int slot = k & 1;
-            if (!warp_wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x516))
+            if (!warp_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x516))
                 break;
             const Item it = decode(slot);
             __syncwarp();
@@ -434,11 +529,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const long long tok = static_cast<long long>(it.row0) + q;
             const float lse = q_ok ? __ldg(a.lse + it.head * a.T + tok) : 0.0f;
             const float dlt = q_ok ? __ldg(a.delta + it.head * a.T + tok) : 0.0f;
+            const OneValue neg_lse{f32x2(-lse, -lse)}, neg_dlt{f32x2(-dlt, -dlt)};
+            const uint64_t scale2 = f32x2(a.scale2, a.scale2);
             for (int j = 0; j < it.n_kv; ++j, ++g) {
-                const uint32_t parity = static_cast<uint32_t>(g) & 1u;
-                const int key0 = j * BS + w * HALF;  // first key of this half
+                const int b = g & 1, key0 = j * BS + w * HALF;  // first key of this half
+                // keys after the warp's first query (keys behind the sequence's end are)
                 const bool masked = key0 + HALF - 1 > it.q0 + (warp & 3) * 32;
-                if (!warp_wait_bounded(s_full, parity, abort_flag, a.status, 0x50C)) {
+                if (!warp_wait(s_full, static_cast<uint32_t>(g) & 1u, abort_flag, a.status, 0x50C)) {
                     ok = false;
                     break;
                 }
@@ -449,52 +546,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read);
                 float p[HALF / 32][32];
-                const uint64_t scale2 = f32x2(a.scale2, a.scale2), neg_lse = f32x2(-lse, -lse);
 #pragma unroll
-                for (int c = 0; c < HALF / 32; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x0, x1;
-                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
-                                              scale2, neg_lse), x0, x1);
-                        p[c][2 * i] = ex2(x0);
-                        p[c][2 * i + 1] = ex2(x1);
-                    }
-                if (!warp_wait_bounded(dp_full, parity, abort_flag, a.status, 0x50D)) {
+                for (int c = 0; c < HALF / 32; ++c) weights<false>(v[c], scale2, neg_lse, 0, 0, 0, p[c]);
+                if (!warp_wait(&dp_full[b], static_cast<uint32_t>(g >> 1) & 1u, abort_flag, a.status, 0x50D)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                tmem_ld_half<HALF>(lane_addr + C::kP + w * HALF, v);
-                const uint64_t neg_dlt = f32x2(-dlt, -dlt);
+                const uint32_t dp = lane_addr + C::dp(b) + w * HALF;
+                tmem_ld_half<HALF>(dp, v);
 #pragma unroll
                 for (int c = 0; c < HALF / 32; ++c) {
                     uint32_t dd[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float d0, d1;
-                        f32x2_split(mul_f32x2(f32x2(p[c][2 * i], p[c][2 * i + 1]),
-                                              add_f32x2(f32x2(__uint_as_float(v[c][2 * i]),
-                                                              __uint_as_float(v[c][2 * i + 1])), neg_dlt)), d0, d1);
-                        // an exact zero whatever the masked scores and values hold
-                        if (masked) {
-                            if (key0 + 32 * c + 2 * i > q) d0 = 0.0f;
-                            if (key0 + 32 * c + 2 * i + 1 > q) d1 = 0.0f;
-                        }
-                        dd[i] = pack_bf16x2(d0, d1);
-                    }
-                    tmem_st16(lane_addr + C::kP + w * HALF + 16 * c, dd);
+                    if (masked)
+                        score_grads<true>(v[c], p[c], neg_dlt, key0 + 32 * c, 0, q + 1, dd);
+                    else
+                        score_grads<false>(v[c], p[c], neg_dlt, 0, 0, 0, dd);
+                    tmem_st16(dp + 16 * c, dd);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 // K rows behind the sequence's end (S, their first use, is done)
                 if ((j + 1) * BS > it.len)
-                    zero_rows<C::NB>(smem_u32(ring) + stage * 2 * C::STREAM, BS, it.len - j * BS, threadIdx.x, 256);
+                    zero_rows<C::NB>(smem_u32(sK) + k_slot * C::STREAM, BS, it.len - j * BS, threadIdx.x, 256);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ds_full);
-                if (++stage == S) stage = 0;
-                // the last item's dQ, once this item's first tiles keep the tensor cores busy
-                if (pend.k >= 0 && j == (it.n_kv > 1 ? 1 : 0) && !readout()) {
+                if (lane == 0) mbar_arrive(&ds_full[b]);
+                if (++k_slot == FAR) k_slot = 0;
+                // the last item's dQ, while the tensor cores have this item's next tile
+                if (pend.k >= 0 && !readout()) {
                     ok = false;
                     break;
                 }
@@ -522,15 +601,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                        const BwdArgs a) {
     pdl_launch_dependents();
     using C = BwdCfg<D>;
-    constexpr int S = C::STAGES, BS = C::BS, HALF = C::HALF;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    constexpr int FAR = C::FAR, NEAR = C::NEAR, BS = C::BS, HALF = C::HALF;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (!tiles_aligned(smem, a.status)) return;
     uint8_t* sK = smem;
     uint8_t* sV = sK + C::OWN;
-    uint8_t* ring = sV + C::OWN;
-    float* stats = reinterpret_cast<float*>(ring + S * 2 * C::STREAM);  // [warp][lse, delta][HALF], negated
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S * 2 * C::STREAM + C::STATS);
+    uint8_t* sQ = sV + C::OWN;            // [FAR]
+    uint8_t* sdO = sQ + FAR * C::STREAM;  // [NEAR]
+    float* stats = reinterpret_cast<float*>(sdO + NEAR * C::STREAM);  // [tile & 1][half][lse, delta][HALF], negated
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sdO + NEAR * C::STREAM + C::STATS);
     uint64_t* k_full = bars;              // the item's K has landed
     uint64_t* k_empty = bars + 1;         // its last S^T has read it
     uint64_t* v_full = bars + 2;          // the same for V and dP^T
@@ -544,9 +623,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint64_t* item_full = bars + 10;      // [2]
     uint64_t* item_empty = bars + 12;     // [2]
     uint64_t* drain = bars + 14;
-    uint64_t* q_full = bars + 15;         // [S]
-    uint64_t* q_empty = q_full + S;       // [S]
-    int* items = reinterpret_cast<int*>(bars + 15 + 2 * 4);  // [2] x {first row, length, key tile, head}
+    uint64_t* q_full = bars + 15;         // [FAR]
+    uint64_t* q_empty = bars + 19;
+    uint64_t* do_full = bars + 23;        // [NEAR]
+    uint64_t* do_empty = bars + 27;
+    uint64_t* stat_full = bars + 31;      // [2] the half's lse and delta of the tile are there
+    int* items = reinterpret_cast<int*>(bars + 33);  // [2] x {first row, length, key tile, head}
     uint32_t* misc = reinterpret_cast<uint32_t*>(items + 8);
     volatile uint32_t* abort_flag = misc + 1;
 
@@ -581,10 +663,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&item_full[b], 1);
             mbar_init(&item_empty[b], 9);  // the MMA thread and the 8 softmax warps
+            mbar_init(&stat_full[b], 4);
         }
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < FAR; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
+        }
+        for (int i = 0; i < NEAR; ++i) {
+            mbar_init(&do_full[i], 1);
+            mbar_init(&do_empty[i], 1);
         }
         mbar_init(drain, 1);
         misc[1] = 0u;
@@ -608,13 +695,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_do);
             const unsigned total = a.plan[kPlanCount] * static_cast<unsigned>(a.nkv);
-            int stage = 0;
-            uint32_t phase = 0, issued = 0, issued_phase = 0;
+            RingSlot<FAR> qs;
+            RingSlot<NEAR> os;
             int k_loads = 0, v_loads = 0;
             bool ok = true;
             for (int k = 0;; ++k) {
                 const int slot = k & 1;
-                if (k >= 2 && !wait_bounded(&item_empty[slot], static_cast<uint32_t>((k - 2) >> 1) & 1u, abort_flag,
+                if (k >= 2 && !thread_wait(&item_empty[slot], static_cast<uint32_t>((k - 2) >> 1) & 1u, abort_flag,
                                             a.status, 0x611))
                     ok = false;
                 unsigned item = total;
@@ -635,38 +722,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const Item it = decode(slot);
                 const int kcol = it.kv_head * D, row = it.row0 + it.k0;
                 const uint32_t before = static_cast<uint32_t>(k - 1) & 1u;
-                if (k >= 1 && !wait_bounded(k_empty, before, abort_flag, a.status, 0x612)) break;
+                if (k >= 1 && !thread_wait(k_empty, before, abort_flag, a.status, 0x612)) break;
                 mbar_arrive_expect_tx(k_full, C::OWN);
                 for (int b = 0; b < C::NB; ++b)
                     tma_load_3d(&tm_k, smem_u32(k_full), smem_u32(sK) + b * 128 * kRowBytes, kcol + 64 * b, row, 0);
                 ++k_loads;
                 int head = it.kv_head * a.group, i = 0;
                 for (int n = 0; n < it.tiles; ++n) {
-                    if (!wait_bounded(&q_empty[stage], phase ^ 1u, abort_flag, a.status, 0x601)) {
+                    const int qrow = it.row0 + (it.i0 + i) * BS;
+                    if (!thread_wait(&q_empty[qs.at], qs.phase ^ 1u, abort_flag, a.status, 0x601)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&q_full[stage], 2 * C::STREAM);
-                    const uint32_t dst = smem_u32(ring) + stage * 2 * C::STREAM;
-                    const int qrow = it.row0 + (it.i0 + i) * BS;
-                    for (int b = 0; b < C::NB; ++b) {
-                        tma_load_3d(&tm_q, smem_u32(&q_full[stage]), dst + b * BS * kRowBytes, head * D + 64 * b, qrow,
-                                    0);
-                        tma_load_3d(&tm_do, smem_u32(&q_full[stage]), dst + C::STREAM + b * BS * kRowBytes,
-                                    head * D + 64 * b, qrow, 0);
-                    }
-                    issued |= 1u << stage;
-                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    if (++i == it.nq) {
-                        i = 0;
-                        ++head;
-                    }
+                    mbar_arrive_expect_tx(&q_full[qs.at], C::STREAM);
+                    for (int b = 0; b < C::NB; ++b)
+                        tma_load_3d(&tm_q, smem_u32(&q_full[qs.at]),
+                                    smem_u32(sQ) + qs.at * C::STREAM + b * BS * kRowBytes, head * D + 64 * b, qrow, 0);
+                    qs.issue();
                     if (n == 0) {
-                        if (k >= 1 && !wait_bounded(v_empty, before, abort_flag, a.status, 0x613)) {
+                        if (k >= 1 && !thread_wait(v_empty, before, abort_flag, a.status, 0x613)) {
                             ok = false;
                             break;
                         }
@@ -676,14 +750,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                         0);
                         ++v_loads;
                     }
+                    if (!thread_wait(&do_empty[os.at], os.phase ^ 1u, abort_flag, a.status, 0x617)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&do_full[os.at], C::STREAM);
+                    for (int b = 0; b < C::NB; ++b)
+                        tma_load_3d(&tm_do, smem_u32(&do_full[os.at]),
+                                    smem_u32(sdO) + os.at * C::STREAM + b * BS * kRowBytes, head * D + 64 * b, qrow,
+                                    0);
+                    os.issue();
+                    if (++i == it.nq) {
+                        i = 0;
+                        ++head;
+                    }
                 }
                 if (!ok) break;
             }
             // every copy this thread started lands before the CTA may exit
             if (k_loads > 0) wait_drain(k_full, static_cast<uint32_t>(k_loads - 1) & 1u, a.status, 0x602);
             if (v_loads > 0) wait_drain(v_full, static_cast<uint32_t>(v_loads - 1) & 1u, a.status, 0x603);
-            for (int i = 0; i < S; ++i)
-                if (issued & (1u << i)) wait_drain(&q_full[i], (issued_phase >> i) & 1u, a.status, 0x604);
+            qs.drain(q_full, a.status, 0x604);
+            os.drain(do_full, a.status, 0x618);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -691,44 +779,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (lane == 0) {
             const uint64_t kdesc = smem_desc_sw128(smem_u32(sK), 16, 1024);
             const uint64_t vdesc = smem_desc_sw128(smem_u32(sV), 16, 1024);
-            int stage = 0, g = 0;  // g: tiles so far
-            uint32_t phase = 0;
+            int g = 0;  // tiles so far
+            RingSlot<FAR> qs;
+            RingSlot<NEAR> os;
             bool ok = true;
             // the tile whose dV and dK products are still to be issued
-            int last_stage = 0, last_k = -1;
+            int last_q = 0, last_o = 0, last_k = -1;
             bool last_first = false, last_final = false, dv_issued = false;
             auto issue_dv = [&]() {  // dV += P^T dO of tile g - 1
                 if (last_k < 0 || dv_issued || !ok) return;
                 // the first products of an item overwrite the last item's gradients
                 if ((last_first && last_k >= 1 &&
-                     !wait_bounded(grad_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x614)) ||
-                    !wait_bounded(p_full, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x605)) {
+                     !thread_wait(grad_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x614)) ||
+                    !thread_wait(p_full, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x605)) {
                     ok = false;
                     return;
                 }
                 tc_fence_after();
                 mma_halves<D>(tmem + C::acc(0), tmem + C::acc_tail(0), tmem + C::kS,
-                              smem_desc_sw128(smem_u32(ring) + last_stage * 2 * C::STREAM + C::STREAM, BS * kRowBytes,
-                                              1024), !last_first);
+                              smem_desc_sw128(smem_u32(sdO) + last_o * C::STREAM, BS * kRowBytes, 1024),
+                              !last_first);
+                tc_commit(&do_empty[last_o]);
                 dv_issued = true;
             };
             auto issue_dk = [&]() {  // dK += dS^T Q of tile g - 1
                 if (last_k < 0 || !ok) return;
-                if (!wait_bounded(ds_full, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x606)) {
+                if (!thread_wait(ds_full, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x606)) {
                     ok = false;
                     return;
                 }
                 tc_fence_after();
-                mma_halves<D>(tmem + C::acc(1), tmem + C::acc_tail(1), tmem + C::kP,
-                              smem_desc_sw128(smem_u32(ring) + last_stage * 2 * C::STREAM, BS * kRowBytes, 1024),
-                              !last_first);
-                tc_commit(&q_empty[last_stage]);
+                mma_halves<D>(tmem + C::acc(1), tmem + C::acc_tail(1), tmem + C::dp(0),
+                              smem_desc_sw128(smem_u32(sQ) + last_q * C::STREAM, BS * kRowBytes, 1024), !last_first);
+                tc_commit(&q_empty[last_q]);
                 if (last_final) tc_commit(grad_done);
                 last_k = -1;
             };
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
-                if (!wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x615))
+                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x615))
                     break;
                 const Item it = decode(slot);
                 mbar_arrive(&item_empty[slot]);
@@ -738,36 +827,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     // where the next item's K is still on its way, the last dK goes first
                     if (n == 0 && ok && !mbar_test(k_full, static_cast<uint32_t>(k) & 1u)) issue_dk();
                     if (!ok) break;
-                    if ((n == 0 && !wait_bounded(k_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x607)) ||
-                        !wait_bounded(&q_full[stage], phase, abort_flag, a.status, 0x608)) {
+                    if ((n == 0 && !thread_wait(k_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x607)) ||
+                        !thread_wait(&q_full[qs.at], qs.phase, abort_flag, a.status, 0x608)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t qd = smem_u32(ring) + stage * 2 * C::STREAM;
-                    mma_scores<D>(tmem + C::kS, kdesc, smem_desc_sw128(qd, 16, 1024));
+                    mma_scores<D>(tmem + C::kS, kdesc, smem_desc_sw128(smem_u32(sQ) + qs.at * C::STREAM, 16, 1024));
                     tc_commit(s_full);
                     if (n == it.tiles - 1) tc_commit(k_empty);
                     issue_dk();  // reads dS^T, which lies over the last dP^T
                     if (!ok) break;
-                    if (n == 0 && !wait_bounded(v_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x609)) {
+                    if ((n == 0 && !thread_wait(v_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x609)) ||
+                        !thread_wait(&do_full[os.at], os.phase, abort_flag, a.status, 0x619)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    mma_scores<D>(tmem + C::kP, vdesc, smem_desc_sw128(qd + C::STREAM, 16, 1024));
+                    mma_scores<D>(tmem + C::dp(0), vdesc, smem_desc_sw128(smem_u32(sdO) + os.at * C::STREAM, 16, 1024));
                     tc_commit(dp_full);
                     if (n == it.tiles - 1) tc_commit(v_empty);
-                    last_stage = stage;
+                    last_q = qs.at;
+                    last_o = os.at;
                     last_k = k;
                     last_first = n == 0;
                     last_final = n == it.tiles - 1;
                     dv_issued = false;
                     ++g;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    qs.next();
+                    os.next();
                 }
             }
             issue_dv();
@@ -781,29 +869,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int w = warp >> 2;            // which half of a tile's columns (queries)
         const int r = threadIdx.x & 127;    // key row = TMEM lane
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        float* neg_lse = stats + warp * 2 * HALF;
-        float* neg_dlt = neg_lse + HALF;
+        const uint64_t scale2 = f32x2(a.scale2, a.scale2);
         bool ok = true;
-        int g = 0, stage = 0;
+        int g = 0;
+        RingSlot<FAR> qs;
+        RingSlot<NEAR> os;
         for (int k = 0; ok; ++k) {
             const int slot = k & 1;
-            if (!warp_wait_bounded(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x616))
+            if (!warp_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x616))
                 break;
             const Item it = decode(slot);
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             if (it.len == 0) break;
             const int key = it.k0 + r;
-            // lse and delta of the tile's queries, loaded a tile ahead
-            float lse_n[HALF / 32], dlt_n[HALF / 32];
+            // a value of the tile's lse or delta per thread, loaded a tile ahead
+            float stat_n = 0.0f;
             auto fetch = [&](int head, int i) {
-                const long long at = head * a.T + it.row0;
-#pragma unroll
-                for (int c = 0; c < HALF / 32; ++c) {
-                    const int qq = (it.i0 + i) * BS + w * HALF + 32 * c + lane;
-                    const bool in = qq < it.len;
-                    lse_n[c] = in ? -__ldg(a.lse + at + qq) : 0.0f;
-                    dlt_n[c] = in ? -__ldg(a.delta + at + qq) : 0.0f;
+                if (r < 2 * HALF) {
+                    const int qq = (it.i0 + i) * BS + w * HALF + r % HALF;
+                    stat_n = qq < it.len ? -__ldg((r < HALF ? a.lse : a.delta) + head * a.T + it.row0 + qq) : 0.0f;
                 }
             };
             int head = it.kv_head * a.group, i = 0;
@@ -811,104 +896,80 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int n = 0; n < it.tiles; ++n, ++g) {
                 const uint32_t parity = static_cast<uint32_t>(g) & 1u;
                 const int q0 = (it.i0 + i) * BS + w * HALF;  // first query of this half
-                const bool masked = q0 < it.k0 + (warp & 3) * 32 + 31 || q0 + HALF > it.len;
-                const bool tail = (it.i0 + i + 1) * BS > it.len;
                 const int valid = it.len - (it.i0 + i) * BS;  // queries of the tile inside the sequence
-                __syncwarp();  // the last tile's values have been read
-#pragma unroll
-                for (int c = 0; c < HALF / 32; ++c) {
-                    neg_lse[32 * c + lane] = lse_n[c];
-                    neg_dlt[32 * c + lane] = dlt_n[c];
-                }
+                const bool tail = valid < BS;
+                // queries before the warp's last key, or behind the sequence's end
+                const bool masked = q0 < it.k0 + (warp & 3) * 32 + 31 || q0 + HALF > it.len;
+                float* stat = stats + ((g & 1) * 2 + w) * 2 * HALF;
+                if (r < 2 * HALF) stat[r] = stat_n;
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&stat_full[w]);
                 if (++i == it.nq) {
                     i = 0;
                     ++head;
                 }
                 if (n + 1 < it.tiles) fetch(head, i);
-                if (!warp_wait_bounded(s_full, parity, abort_flag, a.status, 0x60B)) {
+                // (a warp that passes has left the tile before the last, whose place this was)
+                if (!warp_wait(&stat_full[w], parity, abort_flag, a.status, 0x61B) ||
+                    !warp_wait(s_full, parity, abort_flag, a.status, 0x60B)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t v[HALF / 32][32];
-                tmem_ld_half<HALF>(lane_addr + C::kS + w * HALF, v);
                 float p[HALF / 32][32];
-                const uint64_t scale2 = f32x2(a.scale2, a.scale2);
 #pragma unroll
                 for (int c = 0; c < HALF / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_addr + C::kS + w * HALF + 32 * c, v);
+                    tmem_wait_ld();
+                    const ColumnValues neg_lse{stat + 32 * c};
+                    if (masked)
+                        weights<true>(v, scale2, neg_lse, q0 + 32 * c, key, it.len, p[c]);
+                    else
+                        weights<false>(v, scale2, neg_lse, 0, 0, 0, p[c]);
                     uint32_t pp[16];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float4 l4 = *reinterpret_cast<const float4*>(neg_lse + 32 * c + 4 * u);
-                        float x[4];
-                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c][4 * u]), __uint_as_float(v[c][4 * u + 1])),
-                                              scale2, f32x2(l4.x, l4.y)), x[0], x[1]);
-                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c][4 * u + 2]), __uint_as_float(v[c][4 * u + 3])),
-                                              scale2, f32x2(l4.z, l4.w)), x[2], x[3]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float pe = ex2(x[e]);
-                            // keys after the query, and queries behind the sequence's end
-                            if (masked) {
-                                const int qq = q0 + 32 * c + 4 * u + e;
-                                if (qq < key || qq >= it.len) pe = 0.0f;
-                            }
-                            p[c][4 * u + e] = pe;
-                        }
-                        pp[2 * u] = pack_bf16x2(p[c][4 * u], p[c][4 * u + 1]);
-                        pp[2 * u + 1] = pack_bf16x2(p[c][4 * u + 2], p[c][4 * u + 3]);
-                    }
+                    for (int e = 0; e < 16; ++e) pp[e] = pack_bf16x2(p[c][2 * e], p[c][2 * e + 1]);
                     tmem_st16(lane_addr + C::kS + w * HALF + 16 * c, pp);
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                const uint32_t qd = smem_u32(ring) + stage * 2 * C::STREAM;
-                // dO rows behind the end: S^T is there, so Q and dO have landed
-                if (tail) zero_rows<C::NB>(qd + C::STREAM, BS, valid, threadIdx.x, 256);
+                if (tail) {  // dO rows behind the end
+                    if (!warp_wait(&do_full[os.at], os.phase, abort_flag, a.status, 0x61A)) {
+                        ok = false;
+                        break;
+                    }
+                    zero_rows<C::NB>(smem_u32(sdO) + os.at * C::STREAM, BS, valid, threadIdx.x, 256);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
-                if (!warp_wait_bounded(dp_full, parity, abort_flag, a.status, 0x60C)) {
+                if (!warp_wait(dp_full, parity, abort_flag, a.status, 0x60C)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                tmem_ld_half<HALF>(lane_addr + C::kP + w * HALF, v);
 #pragma unroll
                 for (int c = 0; c < HALF / 32; ++c) {
-                    uint32_t dd[16];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float4 d4 = *reinterpret_cast<const float4*>(neg_dlt + 32 * c + 4 * u);
-                        float x[4];
-                        f32x2_split(mul_f32x2(f32x2(p[c][4 * u], p[c][4 * u + 1]),
-                                              add_f32x2(f32x2(__uint_as_float(v[c][4 * u]),
-                                                              __uint_as_float(v[c][4 * u + 1])), f32x2(d4.x, d4.y))),
-                                    x[0], x[1]);
-                        f32x2_split(mul_f32x2(f32x2(p[c][4 * u + 2], p[c][4 * u + 3]),
-                                              add_f32x2(f32x2(__uint_as_float(v[c][4 * u + 2]),
-                                                              __uint_as_float(v[c][4 * u + 3])), f32x2(d4.z, d4.w))),
-                                    x[2], x[3]);
-                        if (masked) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int qq = q0 + 32 * c + 4 * u + e;
-                                if (qq < key || qq >= it.len) x[e] = 0.0f;
-                            }
-                        }
-                        dd[2 * u] = pack_bf16x2(x[0], x[1]);
-                        dd[2 * u + 1] = pack_bf16x2(x[2], x[3]);
-                    }
-                    tmem_st16(lane_addr + C::kP + w * HALF + 16 * c, dd);
+                    uint32_t v[32], dd[16];
+                    tmem_ld32(lane_addr + C::dp(0) + w * HALF + 32 * c, v);
+                    tmem_wait_ld();
+                    const ColumnValues neg_dlt{stat + HALF + 32 * c};
+                    if (masked)
+                        score_grads<true>(v, p[c], neg_dlt, q0 + 32 * c, key, it.len, dd);
+                    else
+                        score_grads<false>(v, p[c], neg_dlt, 0, 0, 0, dd);
+                    tmem_st16(lane_addr + C::dp(0) + w * HALF + 16 * c, dd);
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                if (tail) zero_rows<C::NB>(qd, BS, valid, threadIdx.x, 256);  // Q rows
+                // Q rows behind the end (S^T, their first use, is done)
+                if (tail) zero_rows<C::NB>(smem_u32(sQ) + qs.at * C::STREAM, BS, valid, threadIdx.x, 256);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ds_full);
-                if (++stage == S) stage = 0;
+                qs.next();
+                os.next();
             }
-            if (!ok || !warp_wait_bounded(grad_done, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x60D)) {
+            if (!ok || !warp_wait(grad_done, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x60D)) {
                 ok = false;
                 break;
             }

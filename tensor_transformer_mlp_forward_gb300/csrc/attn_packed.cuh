@@ -102,6 +102,43 @@ __device__ __forceinline__ void plan_block(const int* __restrict__ cu, int nb, i
     }
 }
 
+// Waits of these kernels' roles, by polls (a failing one sleeps 4 us, so the limit is
+// that of the timed waits).  The roles run different code on one SM and push each
+// other's out of the instruction caches: a wait that inlines the timed loops took
+// 250 clocks when its phase was complete, this one takes 64.
+__device__ __noinline__ void give_up(volatile uint32_t* abort, int* status, int site) {
+    *abort = 1u;
+    atomicExch(status, kStatusTimeout);
+    atomicCAS(status + 1, 0, site);
+}
+
+// One thread.
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, int* status,
+                                            int site) {
+#pragma unroll 1
+    for (int i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if (*abort) return false;
+        if (i >= kPollLimit) {
+            give_up(abort, status, site);
+            return false;
+        }
+    }
+    return true;
+}
+
+// A whole warp, whose lanes poll and leave together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, int* status,
+                                          int site) {
+#pragma unroll 1
+    for (int i = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {
+        if (__any_sync(0xFFFFFFFFu, *abort != 0u || i >= kPollLimit)) {
+            if (i >= kPollLimit) give_up(abort, status, site);
+            return false;
+        }
+    }
+    return true;
+}
+
 // Zeroes rows first .. rows - 1 of an operand tile of NB 64-column boxes in
 // shared memory (a box row is 128 bytes whatever the swizzle does within it),
 // by `threads` threads, and makes the zeros visible to the tensor cores.
