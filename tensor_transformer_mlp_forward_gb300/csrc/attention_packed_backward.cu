@@ -33,7 +33,13 @@
 namespace tpmlp {
 namespace {
 
-constexpr int kBwdThreads = 320;  // 8 softmax warps, producer, MMA
+// 8 softmax warps, the producer's, and those that issue the MMAs: one warp for each
+// chain of products, because a lone thread spends 55 clocks on an MMA that takes 64
+// and some 240 on each barrier, ready or not, while the MMAs load shared memory.
+// With one warp for all, the issuer and not the tensor cores set the pace (3400 to
+// 4400 clocks a tile against 1536 and 2048 of MMAs).
+constexpr int kDqThreads = 384;    // S, dP and dQ
+constexpr int kDkvThreads = 352;   // dV with S^T, and dK with dP^T, in each other's place
 
 template <int D>
 struct BwdCfg {
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kDeltaThreads)
 // ------------------------------------------------------------- dQ
 
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kDqThreads, 1)
     packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,  // 128 rows
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,   // BS rows
                      const BwdArgs a) {
@@ -270,10 +276,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint64_t* k_empty = bars + 21;
     uint64_t* v_full = bars + 25;         // [NEAR]
     uint64_t* v_empty = bars + 29;
-    int* items = reinterpret_cast<int*>(bars + 33);  // [2] x {first row, length, tile, head}
+    uint64_t* ds_used = bars + 33;        // [2] dQ has read dS
+    int* items = reinterpret_cast<int*>(bars + 35);  // [2] x {first row, length, tile, head}
     uint32_t* misc = reinterpret_cast<uint32_t*>(items + 8);
     volatile uint32_t* abort_flag = misc + 1;
-    static_assert(33 * 8 + 8 * 4 + 8 <= C::BARS && FAR <= 4 && NEAR <= 4, "barrier space");
+    static_assert(35 * 8 + 8 * 4 + 8 <= C::BARS && FAR <= 4 && NEAR <= 4, "barrier space");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     struct Item {
@@ -303,7 +310,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mbar_init(&dp_full[b], 1);
             mbar_init(&ds_full[b], 8);
             mbar_init(&item_full[b], 1);
-            mbar_init(&item_empty[b], 9);  // the MMA thread and the 8 softmax warps
+            mbar_init(&ds_used[b], 1);
+            mbar_init(&item_empty[b], 11);  // the 3 MMA threads and the 8 softmax warps
         }
         for (int i = 0; i < FAR; ++i) {
             mbar_init(&k_full[i], 1);
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, 3);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -410,36 +418,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             vs.drain(v_full, a.status, 0x518);
         }
         __syncwarp();
-    } else if (warp == 9) {
-        // ------------------------------------------------------ MMA issuer
+    } else if (warp >= 9) {
+        // ----------------------- MMA issuers: S (warp 9), dP (warp 10), dQ (warp 11)
         if (lane == 0) {
-            const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t dodesc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
             int g = 0;  // tiles so far
             RingSlot<FAR> ks;
             RingSlot<NEAR> vs;
             bool ok = true;
-            // the tile whose dQ product is still to be issued
-            int last_slot = 0, last_k = -1;
-            bool last_first = false, last_final = false;
-            auto issue_dq = [&](int tile) {  // dQ += dS K
-                if (last_k < 0 || !ok) return;
-                const int b = tile & 1;
-                // the first product of an item overwrites the last item's dQ
-                if ((last_first && last_k >= 1 &&
-                     !thread_wait(dq_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x514)) ||
-                    !thread_wait(&ds_full[b], static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, a.status, 0x505)) {
-                    ok = false;
-                    return;
-                }
-                tc_fence_after();
-                mma_halves<D>(tmem + C::kDQ, tmem + C::kDQTail, tmem + C::dp(b),
-                              smem_desc_sw128(smem_u32(sK) + last_slot * C::STREAM, BS * kRowBytes, 1024),
-                              !last_first);
-                tc_commit(&k_empty[last_slot]);
-                if (last_final) tc_commit(dq_done);
-                last_k = -1;
-            };
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
                 if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x515))
@@ -447,45 +432,54 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const Item it = decode(slot);
                 mbar_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
-                for (int j = 0; j < it.n_kv && ok; ++j) {
-                    const uint32_t item_parity = static_cast<uint32_t>(k) & 1u;
-                    // where the next item's Q is still on its way, the last dQ goes first
-                    if (j == 0 && !mbar_test(q_full, item_parity)) issue_dq(g - 1);
-                    if (!ok) break;
-                    if ((j == 0 && !thread_wait(q_full, item_parity, abort_flag, a.status, 0x506)) ||
-                        !thread_wait(&k_full[ks.at], ks.phase, abort_flag, a.status, 0x507) ||
-                        (g > 0 &&
-                         !thread_wait(s_read, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x508))) {
-                        ok = false;
-                        break;
+                const uint32_t item_parity = static_cast<uint32_t>(k) & 1u;
+                if (warp == 9) {
+                    const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+                    ok = thread_wait(q_full, item_parity, abort_flag, a.status, 0x506);
+                    for (int j = 0; j < it.n_kv && ok; ++j, ++g, ks.next()) {
+                        if (!(ok = thread_wait(&k_full[ks.at], ks.phase, abort_flag, a.status, 0x507) &&
+                                   (g == 0 || thread_wait(s_read, static_cast<uint32_t>(g - 1) & 1u, abort_flag,
+                                                          a.status, 0x508))))
+                            break;
+                        tc_fence_after();
+                        mma_scores<D>(tmem + C::kS, qdesc, smem_desc_sw128(smem_u32(sK) + ks.at * C::STREAM, 16, 1024));
+                        tc_commit(s_full);
                     }
-                    tc_fence_after();
-                    mma_scores<D>(tmem + C::kS, qdesc, smem_desc_sw128(smem_u32(sK) + ks.at * C::STREAM, 16, 1024));
-                    tc_commit(s_full);
-                    if (j == it.n_kv - 1) tc_commit(q_empty);
-                    if ((j == 0 && !thread_wait(do_full, item_parity, abort_flag, a.status, 0x509)) ||
-                        !thread_wait(&v_full[vs.at], vs.phase, abort_flag, a.status, 0x519)) {
-                        ok = false;
-                        break;
+                    if (ok) tc_commit(q_empty);
+                } else if (warp == 10) {
+                    const uint64_t dodesc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
+                    ok = thread_wait(do_full, item_parity, abort_flag, a.status, 0x509);
+                    for (int j = 0; j < it.n_kv && ok; ++j, ++g, vs.next()) {
+                        const int b = g & 1;
+                        // over the dS of the tile before the last, which its dQ has read
+                        if (!(ok = thread_wait(&v_full[vs.at], vs.phase, abort_flag, a.status, 0x519) &&
+                                   (g < 2 || thread_wait(&ds_used[b], static_cast<uint32_t>((g - 2) >> 1) & 1u,
+                                                         abort_flag, a.status, 0x51A))))
+                            break;
+                        tc_fence_after();
+                        mma_scores<D>(tmem + C::dp(b), dodesc,
+                                      smem_desc_sw128(smem_u32(sV) + vs.at * C::STREAM, 16, 1024));
+                        tc_commit(&dp_full[b]);
+                        tc_commit(&v_empty[vs.at]);
                     }
-                    tc_fence_after();
-                    // over the dS of the tile before the last, whose dQ has been issued
-                    mma_scores<D>(tmem + C::dp(g & 1), dodesc,
-                                  smem_desc_sw128(smem_u32(sV) + vs.at * C::STREAM, 16, 1024));
-                    tc_commit(&dp_full[g & 1]);
-                    tc_commit(&v_empty[vs.at]);
-                    if (j == it.n_kv - 1) tc_commit(do_empty);
-                    issue_dq(g - 1);
-                    last_slot = ks.at;
-                    last_k = k;
-                    last_first = j == 0;
-                    last_final = j == it.n_kv - 1;
-                    ks.next();
-                    vs.next();
-                    ++g;
+                    if (ok) tc_commit(do_empty);
+                } else {
+                    // the first product of an item overwrites the last item's dQ
+                    ok = k == 0 || thread_wait(dq_free, static_cast<uint32_t>(k - 1) & 1u, abort_flag, a.status, 0x514);
+                    for (int j = 0; j < it.n_kv && ok; ++j, ++g, ks.next()) {
+                        const int b = g & 1;
+                        if (!(ok = thread_wait(&ds_full[b], static_cast<uint32_t>(g >> 1) & 1u, abort_flag, a.status,
+                                               0x505)))
+                            break;
+                        tc_fence_after();
+                        mma_halves<D>(tmem + C::kDQ, tmem + C::kDQTail, tmem + C::dp(b),
+                                      smem_desc_sw128(smem_u32(sK) + ks.at * C::STREAM, BS * kRowBytes, 1024), j > 0);
+                        tc_commit(&ds_used[b]);
+                        tc_commit(&k_empty[ks.at]);
+                    }
+                    if (ok) tc_commit(dq_done);
                 }
             }
-            issue_dq(g - 1);
             tc_commit(drain);
             wait_drain(drain, 0, a.status, 0x50A);
         }
@@ -595,7 +589,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------- dK, dV
 
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
     packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,   // 128 rows
                        const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,  // BS rows
                        const BwdArgs a) {
@@ -658,11 +652,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_init(p_full, 8);
         mbar_init(dp_full, 1);
         mbar_init(ds_full, 8);
-        mbar_init(grad_done, 1);
+        mbar_init(grad_done, 2);
         mbar_init(grad_free, 8);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&item_full[b], 1);
-            mbar_init(&item_empty[b], 9);  // the MMA thread and the 8 softmax warps
+            mbar_init(&item_empty[b], 10);  // the 2 MMA threads and the 8 softmax warps
             mbar_init(&stat_full[b], 4);
         }
         for (int i = 0; i < FAR; ++i) {
@@ -671,9 +665,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         for (int i = 0; i < NEAR; ++i) {
             mbar_init(&do_full[i], 1);
-            mbar_init(&do_empty[i], 1);
+            mbar_init(&do_empty[i], 2);  // read for dP^T and dV
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, 2);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -774,44 +768,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             os.drain(do_full, a.status, 0x618);
         }
         __syncwarp();
-    } else if (warp == 9) {
-        // ------------------------------------------------------ MMA issuer
+    } else if (warp >= 9) {
+        // -------- MMA issuers: dV and S^T (warp 9), dK and dP^T (warp 10).  The product
+        // of a tile that reads P^T (dS^T) goes before the next tile's S^T (dP^T), which
+        // overwrites it: MMAs of one thread run in order.
         if (lane == 0) {
-            const uint64_t kdesc = smem_desc_sw128(smem_u32(sK), 16, 1024);
-            const uint64_t vdesc = smem_desc_sw128(smem_u32(sV), 16, 1024);
+            const bool first = warp == 9;
+            const uint64_t own = smem_desc_sw128(smem_u32(first ? sK : sV), 16, 1024);
+            const uint32_t tile = tmem + (first ? C::kS : C::dp(0));
+            const uint32_t acc = tmem + (first ? C::acc(0) : C::acc(1));
+            const uint32_t tail = tmem + (first ? C::acc_tail(0) : C::acc_tail(1));
             int g = 0;  // tiles so far
             RingSlot<FAR> qs;
             RingSlot<NEAR> os;
             bool ok = true;
-            // the tile whose dV and dK products are still to be issued
+            // the tile whose gradient product is still to be issued
             int last_q = 0, last_o = 0, last_k = -1;
-            bool last_first = false, last_final = false, dv_issued = false;
-            auto issue_dv = [&]() {  // dV += P^T dO of tile g - 1
-                if (last_k < 0 || dv_issued || !ok) return;
-                // the first products of an item overwrite the last item's gradients
-                if ((last_first && last_k >= 1 &&
-                     !thread_wait(grad_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x614)) ||
-                    !thread_wait(p_full, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x605)) {
-                    ok = false;
-                    return;
-                }
-                tc_fence_after();
-                mma_halves<D>(tmem + C::acc(0), tmem + C::acc_tail(0), tmem + C::kS,
-                              smem_desc_sw128(smem_u32(sdO) + last_o * C::STREAM, BS * kRowBytes, 1024),
-                              !last_first);
-                tc_commit(&do_empty[last_o]);
-                dv_issued = true;
-            };
-            auto issue_dk = [&]() {  // dK += dS^T Q of tile g - 1
+            uint32_t last_o_phase = 0;
+            bool last_first = false, last_final = false;
+            auto issue_grad = [&]() {
                 if (last_k < 0 || !ok) return;
-                if (!thread_wait(ds_full, static_cast<uint32_t>(g - 1) & 1u, abort_flag, a.status, 0x606)) {
-                    ok = false;
-                    return;
-                }
+                const uint32_t parity = static_cast<uint32_t>(g - 1) & 1u;
+                // the first products of an item overwrite the last item's gradients
+                if (last_first && last_k >= 1)
+                    ok = thread_wait(grad_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x614);
+                if (first)
+                    ok = ok && thread_wait(&do_full[last_o], last_o_phase, abort_flag, a.status, 0x605) &&
+                         thread_wait(p_full, parity, abort_flag, a.status, 0x606);
+                else
+                    ok = ok && thread_wait(ds_full, parity, abort_flag, a.status, 0x60E);
+                if (!ok) return;
                 tc_fence_after();
-                mma_halves<D>(tmem + C::acc(1), tmem + C::acc_tail(1), tmem + C::dp(0),
-                              smem_desc_sw128(smem_u32(sQ) + last_q * C::STREAM, BS * kRowBytes, 1024), !last_first);
-                tc_commit(&q_empty[last_q]);
+                // dV += P^T dO, dK += dS^T Q
+                const uint32_t rows = first ? smem_u32(sdO) + last_o * C::STREAM : smem_u32(sQ) + last_q * C::STREAM;
+                mma_halves<D>(acc, tail, tile, smem_desc_sw128(rows, BS * kRowBytes, 1024), !last_first);
+                tc_commit(first ? &do_empty[last_o] : &q_empty[last_q]);
                 if (last_final) tc_commit(grad_done);
                 last_k = -1;
             };
@@ -822,44 +813,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const Item it = decode(slot);
                 mbar_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
-                for (int n = 0; n < it.tiles && ok; ++n) {
-                    issue_dv();  // reads P^T, which lies over the last S^T
-                    // where the next item's K is still on its way, the last dK goes first
-                    if (n == 0 && ok && !mbar_test(k_full, static_cast<uint32_t>(k) & 1u)) issue_dk();
+                for (int n = 0; n < it.tiles; ++n) {
+                    issue_grad();
+                    if (n == 0)
+                        ok = ok && thread_wait(first ? k_full : v_full, static_cast<uint32_t>(k) & 1u, abort_flag,
+                                               a.status, 0x607);
+                    ok = ok && (first ? thread_wait(&q_full[qs.at], qs.phase, abort_flag, a.status, 0x608)
+                                      : thread_wait(&do_full[os.at], os.phase, abort_flag, a.status, 0x609));
                     if (!ok) break;
-                    if ((n == 0 && !thread_wait(k_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x607)) ||
-                        !thread_wait(&q_full[qs.at], qs.phase, abort_flag, a.status, 0x608)) {
-                        ok = false;
-                        break;
-                    }
                     tc_fence_after();
-                    mma_scores<D>(tmem + C::kS, kdesc, smem_desc_sw128(smem_u32(sQ) + qs.at * C::STREAM, 16, 1024));
-                    tc_commit(s_full);
-                    if (n == it.tiles - 1) tc_commit(k_empty);
-                    issue_dk();  // reads dS^T, which lies over the last dP^T
-                    if (!ok) break;
-                    if ((n == 0 && !thread_wait(v_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x609)) ||
-                        !thread_wait(&do_full[os.at], os.phase, abort_flag, a.status, 0x619)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    mma_scores<D>(tmem + C::dp(0), vdesc, smem_desc_sw128(smem_u32(sdO) + os.at * C::STREAM, 16, 1024));
-                    tc_commit(dp_full);
-                    if (n == it.tiles - 1) tc_commit(v_empty);
+                    // S^T = K Q^T, dP^T = V dO^T
+                    const uint32_t rows = first ? smem_u32(sQ) + qs.at * C::STREAM : smem_u32(sdO) + os.at * C::STREAM;
+                    mma_scores<D>(tile, own, smem_desc_sw128(rows, 16, 1024));
+                    tc_commit(first ? s_full : dp_full);
+                    if (!first) tc_commit(&do_empty[os.at]);
+                    if (n == it.tiles - 1) tc_commit(first ? k_empty : v_empty);
                     last_q = qs.at;
                     last_o = os.at;
+                    last_o_phase = os.phase;
                     last_k = k;
                     last_first = n == 0;
                     last_final = n == it.tiles - 1;
-                    dv_issued = false;
                     ++g;
                     qs.next();
                     os.next();
                 }
             }
-            issue_dv();
-            issue_dk();
+            issue_grad();
             tc_commit(drain);
             wait_drain(drain, 0, a.status, 0x60A);
         }
@@ -1018,10 +998,10 @@ cudaError_t launch_bwd(const CUtensorMap& q128, const CUtensorMap& do128, const 
     auto kk = packed_dkdv_kernel<D>;
     if ((e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
-        (e = launch_dependent(kq, grid(p.nh), dim3(kBwdThreads), smem, st, q128, do128, k_s, v_s, a)) != cudaSuccess)
+        (e = launch_dependent(kq, grid(p.nh), dim3(kDqThreads), smem, st, q128, do128, k_s, v_s, a)) != cudaSuccess)
         return e;
     ++*launches;
-    e = launch_dependent(kk, grid(p.nkv), dim3(kBwdThreads), smem, st, k128, v128, q_s, do_s, a);
+    e = launch_dependent(kk, grid(p.nkv), dim3(kDkvThreads), smem, st, k128, v128, q_s, do_s, a);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
