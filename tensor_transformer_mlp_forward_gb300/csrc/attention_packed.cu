@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t* kv_empty = kv_full + S;
     uint64_t* s_full = kv_empty + S;      // [tile]
     uint64_t* p_full = s_full + 2;        // [tile]
-    uint64_t* pv_done = p_full + 2;       // [tile]
-    uint64_t* o_free = pv_done + 2;       // [tile] the softmax warps have read O_x out
+    uint64_t* o_full = p_full + 2;       // [tile]
+    uint64_t* o_free = o_full + 2;       // [tile] the softmax warps have read O_x out
     uint64_t* item_full = o_free + 2;     // [2]
     uint64_t* item_empty = item_full + 2; // [2]
     uint64_t* drain = item_empty + 2;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
             mbar_init(&p_full[x], 4);  // one arrival per warp of the tile's warpgroup
-            mbar_init(&pv_done[x], 1);
+            mbar_init(&o_full[x], 1);
             mbar_init(&o_free[x], 4);
             mbar_init(&item_full[x], 1);
             mbar_init(&item_empty[x], 9);  // the MMA thread and the 8 softmax warps
@@ -217,16 +217,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             uint32_t rphase = 0;
             int gx[2] = {0, 0};  // S / P V MMAs of each tile over the items so far
             int cx[2] = {0, 0};  // items each tile has taken part in
-            // wait for the next ring entry; returns its stage
-            auto acquire = [&](int site) -> int {
-                const int stage = rstage;
-                if (ok && !thread_wait(&kv_full[stage], rphase, abort_flag, a.status, site)) ok = false;
-                tc_fence_after();
+            auto next = [&]() {
                 if (++rstage == S) {
                     rstage = 0;
                     rphase ^= 1u;
                 }
-                return stage;
             };
             int s_left = 0;  // S MMAs of the item still to issue
             auto issue_s = [&](int x, int stage) {  // S_x = Q_x K^T
@@ -240,68 +235,69 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // the item's last S: once done, the Q tiles may be replaced
                 if (--s_left == 0) tc_commit(q_empty);
             };
-            auto issue_pv = [&](int x, int j, int stage) {  // O_x (+)= P_x V
-                // the first P V of an item overwrites the previous item's O_x
-                if (ok && j == 0 && cx[x] >= 1 &&
-                    !thread_wait(&o_free[x], static_cast<uint32_t>(cx[x] - 1) & 1u, abort_flag, a.status,
-                                  0x413 + x))
-                    ok = false;
-                if (ok && !thread_wait(&p_full[x], static_cast<uint32_t>(gx[x] + j) & 1u, abort_flag,
-                                        a.status, 0x405 + x))
-                    ok = false;
-                if (!ok) return;
+            // O_x (+)= P_x V: A = P_x from TMEM (packed over S_x's first columns), B = V
+            // (MN-major: d along the rows, keys down the box)
+            auto issue_pv = [&](int x, int j, int stage, bool final) {
+                mma_ts_n_is_d<D, BKV / 16>(
+                    tmem + C::o_col(x), tmem + C::s_col(x),
+                    smem_desc_sw128(smem_u32(ring) + stage * C::KVTILE, BKV * kRowBytes, 1024), BKV * kRowBytes, j > 0,
+                    tmem + C::o_tail(x));
+                if (final) tc_commit(&o_full[x]);
+            };
+            // P_x of key tile j is there, and (j == 0) O_x of the last item is read out
+            auto wait_p = [&](int x, int j) {
+                if (j == 0 && cx[x] >= 1)
+                    ok = ok && thread_wait(&o_free[x], static_cast<uint32_t>(cx[x] - 1) & 1u, abort_flag, a.status,
+                                           0x413 + x);
+                ok = ok && thread_wait(&p_full[x], static_cast<uint32_t>(gx[x] + j) & 1u, abort_flag, a.status,
+                                       0x405 + x);
                 tc_fence_after();
-                // O_x (+)= P_x V: A = P_x from TMEM (packed over S_x's first
-                // columns), B = V (MN-major: d along the rows, keys down the box)
-                const uint64_t vdesc =
-                    smem_desc_sw128(smem_u32(ring) + stage * C::KVTILE, BKV * kRowBytes, 1024);
-                mma_ts_n_is_d<D, BKV / 16>(tmem + C::o_col(x), tmem + C::s_col(x), vdesc,
-                                           BKV * kRowBytes, j > 0, tmem + C::o_tail(x));
-                tc_commit(&pv_done[x]);
             };
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
-                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag,
-                                  a.status, 0x415))
+                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x415))
                     break;
                 const Item it = decode(slot);
                 mbar_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
-                if (!thread_wait(q_full, static_cast<uint32_t>(k) & 1u, abort_flag, a.status, 0x404)) {
-                    ok = false;
+                if (!thread_wait_both(q_full, static_cast<uint32_t>(k) & 1u, &kv_full[rstage], rphase, abort_flag,
+                                      a.status, 0x404))
                     break;
-                }
                 tc_fence_after();
                 s_left = it.last[0] + 1 + (it.has_b ? it.last[1] + 1 : 0);
                 // S of both tiles for key tile 0
-                int ks = acquire(0x407);
-                if (ok) {
-                    issue_s(0, ks);
-                    if (it.has_b) issue_s(1, ks);
-                    tc_commit(&kv_empty[ks]);
-                }
+                issue_s(0, rstage);
+                if (it.has_b) issue_s(1, rstage);
+                tc_commit(&kv_empty[rstage]);
+                next();
                 for (int j = 0; j < it.n_kv && ok; ++j) {
-                    const int vs = acquire(0x408);
+                    // V of this key tile and K of the next: by now both have landed as a
+                    // rule, and one wait for the two is spent while tile A's softmax runs
+                    const int vs = rstage;
+                    const uint32_t vp = rphase;
+                    next();
                     const bool more = j + 1 < it.n_kv;
-                    int kn = -1;
+                    const int kn = rstage;
+                    ok = more ? thread_wait_both(&kv_full[vs], vp, &kv_full[kn], rphase, abort_flag, a.status, 0x408)
+                              : thread_wait(&kv_full[vs], vp, abort_flag, a.status, 0x409);
+                    if (more) next();
+                    if (!ok) break;
                     if (j <= it.last[0]) {
-                        issue_pv(0, j, vs);
-                        if (ok && j + 1 <= it.last[0]) {
-                            kn = acquire(0x409);
-                            if (ok) issue_s(0, kn);
-                        }
+                        wait_p(0, j);
+                        if (!ok) break;
+                        issue_pv(0, j, vs, j == it.last[0]);
+                        if (j + 1 <= it.last[0]) issue_s(0, kn);
                     }
-                    if (it.has_b && ok) {
-                        issue_pv(1, j, vs);
-                        if (ok) tc_commit(&kv_empty[vs]);
-                        if (ok && more) {
-                            if (kn < 0) kn = acquire(0x40A);
-                            if (ok) issue_s(1, kn);
-                        }
-                    } else if (ok) {
+                    if (it.has_b) {
+                        wait_p(1, j);
+                        if (!ok) break;
+                        issue_pv(1, j, vs, j == it.last[1]);
+                        tc_commit(&kv_empty[vs]);
+                        if (more) issue_s(1, kn);
+                    } else {
                         tc_commit(&kv_empty[vs]);
                     }
-                    if (ok && kn >= 0) tc_commit(&kv_empty[kn]);
+                    if (more) tc_commit(&kv_empty[kn]);
                 }
                 gx[0] += it.last[0] + 1;
                 cx[0] += 1;
@@ -321,6 +317,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t s_addr = lane_addr + C::s_col(x);
         int gxl = 0;  // this tile's S / P V MMAs over the items so far
+        int taken = 0;         // items this tile has taken part in
         unsigned ring_at = 0;  // ring entries of the items so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -435,7 +432,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
-            if (!ok || !warp_wait(&pv_done[x], static_cast<uint32_t>(gxl + jl) & 1u, abort_flag,
+            if (!ok || !warp_wait(&o_full[x], static_cast<uint32_t>(taken) & 1u, abort_flag,
                                           a.status, 0x410 + x)) {
                 ok = false;
                 break;
@@ -468,6 +465,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_free[x]);
             gxl += jl + 1;
+            ++taken;
         }
     }
 

@@ -126,11 +126,52 @@ __device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, vola
     return true;
 }
 
+// Whether both phases are complete (or sleeps on one of them): the two polls are on
+// their way together, so that a wait for two costs little more than a wait for one.
+__device__ __forceinline__ bool mbar_try_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool thread_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                                 volatile uint32_t* abort, int* status, int site) {
+#pragma unroll 1
+    for (int i = 0; !mbar_try_wait_both(a, pa, b, pb); ++i) {
+        if (*abort) return false;
+        if (i >= kPollLimit) {
+            give_up(abort, status, site);
+            return false;
+        }
+    }
+    return true;
+}
+
 // A whole warp, whose lanes poll and leave together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, int* status,
                                           int site) {
 #pragma unroll 1
     for (int i = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {
+        if (__any_sync(0xFFFFFFFFu, *abort != 0u || i >= kPollLimit)) {
+            if (i >= kPollLimit) give_up(abort, status, site);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool warp_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                               volatile uint32_t* abort, int* status, int site) {
+#pragma unroll 1
+    for (int i = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait_both(a, pa, b, pb)); ++i) {
         if (__any_sync(0xFFFFFFFFu, *abort != 0u || i >= kPollLimit)) {
             if (i >= kPollLimit) give_up(abort, status, site);
             return false;
