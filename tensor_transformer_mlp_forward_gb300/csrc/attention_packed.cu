@@ -210,8 +210,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
     } else if (warp == 9) {
         // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_bf16_f32(128, BKV, false, false);
+        {
             bool ok = true;
             int rstage = 0;  // ring entries are taken in order, across items
             uint32_t rphase = 0;
@@ -225,42 +224,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             };
             int s_left = 0;  // S MMAs of the item still to issue
             auto issue_s = [&](int x, int stage) {  // S_x = Q_x K^T
-                const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ) + x * C::QTILE, 16, 1024);
-                const uint64_t kdesc = smem_desc_sw128(smem_u32(ring) + stage * C::KVTILE, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_f16(tmem + C::s_col(x), desc_add(qdesc, kmajor_step<128>(kk)),
-                               desc_add(kdesc, kmajor_step<BKV>(kk)), id_s, kk > 0 ? 1u : 0u);
-                tc_commit(&s_full[x]);
+                warp_mma_scores<D, BKV>(tmem + C::s_col(x), desc_low(smem_u32(sQ) + x * C::QTILE, 16),
+                                        desc_low(smem_u32(ring) + stage * C::KVTILE, 16));
+                warp_commit(&s_full[x]);
                 // the item's last S: once done, the Q tiles may be replaced
-                if (--s_left == 0) tc_commit(q_empty);
+                if (--s_left == 0) warp_commit(q_empty);
             };
             // O_x (+)= P_x V: A = P_x from TMEM (packed over S_x's first columns), B = V
             // (MN-major: d along the rows, keys down the box)
             auto issue_pv = [&](int x, int j, int stage, bool final) {
-                mma_ts_n_is_d<D, BKV / 16>(
-                    tmem + C::o_col(x), tmem + C::s_col(x),
-                    smem_desc_sw128(smem_u32(ring) + stage * C::KVTILE, BKV * kRowBytes, 1024), BKV * kRowBytes, j > 0,
-                    tmem + C::o_tail(x));
-                if (final) tc_commit(&o_full[x]);
+                warp_mma_values<D, BKV, BKV / 4>(tmem + C::o_col(x), tmem + C::o_tail(x), tmem + C::s_col(x),
+                                                 desc_low(smem_u32(ring) + stage * C::KVTILE, BKV * kRowBytes), j > 0);
+                if (final) warp_commit(&o_full[x]);
             };
             // P_x of key tile j is there, and (j == 0) O_x of the last item is read out
             auto wait_p = [&](int x, int j) {
                 if (j == 0 && cx[x] >= 1)
-                    ok = ok && thread_wait(&o_free[x], static_cast<uint32_t>(cx[x] - 1) & 1u, abort_flag, a.status,
+                    ok = ok && warp_wait(&o_free[x], static_cast<uint32_t>(cx[x] - 1) & 1u, abort_flag, a.status,
                                            0x413 + x);
-                ok = ok && thread_wait(&p_full[x], static_cast<uint32_t>(gx[x] + j) & 1u, abort_flag, a.status,
+                ok = ok && warp_wait(&p_full[x], static_cast<uint32_t>(gx[x] + j) & 1u, abort_flag, a.status,
                                        0x405 + x);
                 tc_fence_after();
             };
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
-                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x415))
+                if (!warp_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x415))
                     break;
                 const Item it = decode(slot);
-                mbar_arrive(&item_empty[slot]);
+                __syncwarp();
+                warp_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
-                if (!thread_wait_both(q_full, static_cast<uint32_t>(k) & 1u, &kv_full[rstage], rphase, abort_flag,
+                if (!warp_wait_both(q_full, static_cast<uint32_t>(k) & 1u, &kv_full[rstage], rphase, abort_flag,
                                       a.status, 0x404))
                     break;
                 tc_fence_after();
@@ -268,7 +262,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // S of both tiles for key tile 0
                 issue_s(0, rstage);
                 if (it.has_b) issue_s(1, rstage);
-                tc_commit(&kv_empty[rstage]);
+                warp_commit(&kv_empty[rstage]);
                 next();
                 for (int j = 0; j < it.n_kv && ok; ++j) {
                     // V of this key tile and K of the next: by now both have landed as a
@@ -278,8 +272,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     next();
                     const bool more = j + 1 < it.n_kv;
                     const int kn = rstage;
-                    ok = more ? thread_wait_both(&kv_full[vs], vp, &kv_full[kn], rphase, abort_flag, a.status, 0x408)
-                              : thread_wait(&kv_full[vs], vp, abort_flag, a.status, 0x409);
+                    ok = more ? warp_wait_both(&kv_full[vs], vp, &kv_full[kn], rphase, abort_flag, a.status, 0x408)
+                              : warp_wait(&kv_full[vs], vp, abort_flag, a.status, 0x409);
                     if (more) next();
                     if (!ok) break;
                     if (j <= it.last[0]) {
@@ -292,12 +286,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         wait_p(1, j);
                         if (!ok) break;
                         issue_pv(1, j, vs, j == it.last[1]);
-                        tc_commit(&kv_empty[vs]);
+                        warp_commit(&kv_empty[vs]);
                         if (more) issue_s(1, kn);
                     } else {
-                        tc_commit(&kv_empty[vs]);
+                        warp_commit(&kv_empty[vs]);
                     }
-                    if (more) tc_commit(&kv_empty[kn]);
+                    if (more) warp_commit(&kv_empty[kn]);
                 }
                 gx[0] += it.last[0] + 1;
                 cx[0] += 1;
@@ -306,8 +300,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     cx[1] += 1;
                 }
             }
-            tc_commit(drain);
-            wait_drain(drain, 0, a.status, 0x40B);
+            warp_commit(drain);
+            if (lane == 0) wait_drain(drain, 0, a.status, 0x40B);
         }
         __syncwarp();
     } else {

@@ -113,37 +113,6 @@ struct RingSlot {
     }
 };
 
-// D (+)= A B^T with A the packed bf16 halves of a tile in tensor memory (half w at
-// a_tmem + HALF w, 8 columns a k-step) and B MN-major along d in shared memory: N in
-// whole 64-wide swizzle atoms, then a 32-wide tail.
-template <int D>
-__device__ __forceinline__ void mma_halves(uint32_t acc, uint32_t tail, uint32_t a_tmem, uint64_t b_desc,
-                                           bool accumulate) {
-    using C = BwdCfg<D>;
-    constexpr int N1 = (D / 64) * 64, N2 = D - N1, STEPS = C::BS / 16;
-    constexpr uint32_t id1 = idesc_bf16_f32(128, N1, false, true);
-    constexpr uint32_t id2 = idesc_bf16_f32(128, N2 > 0 ? N2 : 32, false, true);
-#pragma unroll
-    for (int kk = 0; kk < STEPS; ++kk) {
-        const uint32_t on = (accumulate || kk > 0) ? 1u : 0u;
-        const uint32_t at = a_tmem + (kk / (STEPS / 2)) * C::HALF + (kk % (STEPS / 2)) * 8;
-        const uint64_t bd = desc_add(b_desc, mnmajor_step(kk));
-        tc_mma_f16_ts(acc, at, bd, id1, on);
-        if constexpr (N2 > 0) tc_mma_f16_ts(tail, at, desc_add(bd, (N1 / 64) * C::BS * kRowBytes), id2, on);
-    }
-}
-
-// D = A B^T over the head dim, A 128 rows and B BS rows, both K-major.
-template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc) {
-    using C = BwdCfg<D>;
-    constexpr uint32_t id = idesc_bf16_f32(128, C::BS, false, false);
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-        tc_mma_f16(d_tmem, desc_add(a_desc, kmajor_step<128>(kk)), desc_add(b_desc, kmajor_step<C::BS>(kk)), id,
-                   kk > 0 ? 1u : 0u);
-}
-
 // HALF consecutive 32-bit columns of this thread's lane.
 template <int HALF>
 __device__ __forceinline__ void tmem_ld_half(uint32_t addr, uint32_t (&v)[HALF / 32][32]) {
@@ -420,68 +389,69 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         __syncwarp();
     } else if (warp >= 9) {
         // ----------------------- MMA issuers: S (warp 9), dP (warp 10), dQ (warp 11)
-        if (lane == 0) {
+        {
             int g = 0;  // tiles so far
             RingSlot<FAR> ks;
             RingSlot<NEAR> vs;
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
-                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x515))
+                if (!warp_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x515))
                     break;
                 const Item it = decode(slot);
-                mbar_arrive(&item_empty[slot]);
+                __syncwarp();
+                warp_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
                 const uint32_t item_parity = static_cast<uint32_t>(k) & 1u;
                 if (warp == 9) {
-                    const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-                    ok = thread_wait(q_full, item_parity, abort_flag, a.status, 0x506);
+                    const uint32_t qdesc = desc_low(smem_u32(sQ), 16);
+                    ok = warp_wait(q_full, item_parity, abort_flag, a.status, 0x506);
                     for (int j = 0; j < it.n_kv && ok; ++j, ++g, ks.next()) {
-                        if (!(ok = thread_wait(&k_full[ks.at], ks.phase, abort_flag, a.status, 0x507) &&
-                                   (g == 0 || thread_wait(s_read, static_cast<uint32_t>(g - 1) & 1u, abort_flag,
+                        if (!(ok = warp_wait(&k_full[ks.at], ks.phase, abort_flag, a.status, 0x507) &&
+                                   (g == 0 || warp_wait(s_read, static_cast<uint32_t>(g - 1) & 1u, abort_flag,
                                                           a.status, 0x508))))
                             break;
                         tc_fence_after();
-                        mma_scores<D>(tmem + C::kS, qdesc, smem_desc_sw128(smem_u32(sK) + ks.at * C::STREAM, 16, 1024));
-                        tc_commit(s_full);
+                        warp_mma_scores<D, BS>(tmem + C::kS, qdesc, desc_low(smem_u32(sK) + ks.at * C::STREAM, 16));
+                        warp_commit(s_full);
                     }
-                    if (ok) tc_commit(q_empty);
+                    if (ok) warp_commit(q_empty);
                 } else if (warp == 10) {
-                    const uint64_t dodesc = smem_desc_sw128(smem_u32(sdO), 16, 1024);
-                    ok = thread_wait(do_full, item_parity, abort_flag, a.status, 0x509);
+                    const uint32_t dodesc = desc_low(smem_u32(sdO), 16);
+                    ok = warp_wait(do_full, item_parity, abort_flag, a.status, 0x509);
                     for (int j = 0; j < it.n_kv && ok; ++j, ++g, vs.next()) {
                         const int b = g & 1;
                         // over the dS of the tile before the last, which its dQ has read
-                        if (!(ok = thread_wait(&v_full[vs.at], vs.phase, abort_flag, a.status, 0x519) &&
-                                   (g < 2 || thread_wait(&ds_used[b], static_cast<uint32_t>((g - 2) >> 1) & 1u,
+                        if (!(ok = warp_wait(&v_full[vs.at], vs.phase, abort_flag, a.status, 0x519) &&
+                                   (g < 2 || warp_wait(&ds_used[b], static_cast<uint32_t>((g - 2) >> 1) & 1u,
                                                          abort_flag, a.status, 0x51A))))
                             break;
                         tc_fence_after();
-                        mma_scores<D>(tmem + C::dp(b), dodesc,
-                                      smem_desc_sw128(smem_u32(sV) + vs.at * C::STREAM, 16, 1024));
-                        tc_commit(&dp_full[b]);
-                        tc_commit(&v_empty[vs.at]);
+                        warp_mma_scores<D, BS>(tmem + C::dp(b), dodesc,
+                                      desc_low(smem_u32(sV) + vs.at * C::STREAM, 16));
+                        warp_commit(&dp_full[b]);
+                        warp_commit(&v_empty[vs.at]);
                     }
-                    if (ok) tc_commit(do_empty);
+                    if (ok) warp_commit(do_empty);
                 } else {
                     // the first product of an item overwrites the last item's dQ
-                    ok = k == 0 || thread_wait(dq_free, static_cast<uint32_t>(k - 1) & 1u, abort_flag, a.status, 0x514);
+                    ok = k == 0 || warp_wait(dq_free, static_cast<uint32_t>(k - 1) & 1u, abort_flag, a.status, 0x514);
                     for (int j = 0; j < it.n_kv && ok; ++j, ++g, ks.next()) {
                         const int b = g & 1;
-                        if (!(ok = thread_wait(&ds_full[b], static_cast<uint32_t>(g >> 1) & 1u, abort_flag, a.status,
+                        if (!(ok = warp_wait(&ds_full[b], static_cast<uint32_t>(g >> 1) & 1u, abort_flag, a.status,
                                                0x505)))
                             break;
                         tc_fence_after();
-                        mma_halves<D>(tmem + C::kDQ, tmem + C::kDQTail, tmem + C::dp(b),
-                                      smem_desc_sw128(smem_u32(sK) + ks.at * C::STREAM, BS * kRowBytes, 1024), j > 0);
-                        tc_commit(&ds_used[b]);
-                        tc_commit(&k_empty[ks.at]);
+                        warp_mma_values<D, BS, HALF>(tmem + C::kDQ, tmem + C::kDQTail, tmem + C::dp(b),
+                                      desc_low(smem_u32(sK) + ks.at * C::STREAM, BS * kRowBytes), j > 0);
+                        warp_commit(&ds_used[b]);
+                        warp_commit(&k_empty[ks.at]);
                     }
-                    if (ok) tc_commit(dq_done);
+                    if (ok) warp_commit(dq_done);
                 }
             }
-            tc_commit(drain);
-            wait_drain(drain, 0, a.status, 0x50A);
+            warp_commit(drain);
+            if (lane == 0) wait_drain(drain, 0, a.status, 0x50A);
         }
         __syncwarp();
     } else {
@@ -772,9 +742,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         // -------- MMA issuers: dV and S^T (warp 9), dK and dP^T (warp 10).  The product
         // of a tile that reads P^T (dS^T) goes before the next tile's S^T (dP^T), which
         // overwrites it: MMAs of one thread run in order.
-        if (lane == 0) {
+        {
             const bool first = warp == 9;
-            const uint64_t own = smem_desc_sw128(smem_u32(first ? sK : sV), 16, 1024);
+            const uint32_t own = desc_low(smem_u32(first ? sK : sV), 16);
             const uint32_t tile = tmem + (first ? C::kS : C::dp(0));
             const uint32_t acc = tmem + (first ? C::acc(0) : C::acc(1));
             const uint32_t tail = tmem + (first ? C::acc_tail(0) : C::acc_tail(1));
@@ -791,43 +761,44 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 const uint32_t parity = static_cast<uint32_t>(g - 1) & 1u;
                 // the first products of an item overwrite the last item's gradients
                 if (last_first && last_k >= 1)
-                    ok = thread_wait(grad_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x614);
+                    ok = warp_wait(grad_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x614);
                 if (first)
-                    ok = ok && thread_wait(&do_full[last_o], last_o_phase, abort_flag, a.status, 0x605) &&
-                         thread_wait(p_full, parity, abort_flag, a.status, 0x606);
+                    ok = ok && warp_wait(&do_full[last_o], last_o_phase, abort_flag, a.status, 0x605) &&
+                         warp_wait(p_full, parity, abort_flag, a.status, 0x606);
                 else
-                    ok = ok && thread_wait(ds_full, parity, abort_flag, a.status, 0x60E);
+                    ok = ok && warp_wait(ds_full, parity, abort_flag, a.status, 0x60E);
                 if (!ok) return;
                 tc_fence_after();
                 // dV += P^T dO, dK += dS^T Q
                 const uint32_t rows = first ? smem_u32(sdO) + last_o * C::STREAM : smem_u32(sQ) + last_q * C::STREAM;
-                mma_halves<D>(acc, tail, tile, smem_desc_sw128(rows, BS * kRowBytes, 1024), !last_first);
-                tc_commit(first ? &do_empty[last_o] : &q_empty[last_q]);
-                if (last_final) tc_commit(grad_done);
+                warp_mma_values<D, BS, HALF>(acc, tail, tile, desc_low(rows, BS * kRowBytes), !last_first);
+                warp_commit(first ? &do_empty[last_o] : &q_empty[last_q]);
+                if (last_final) warp_commit(grad_done);
                 last_k = -1;
             };
             for (int k = 0; ok; ++k) {
                 const int slot = k & 1;
-                if (!thread_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x615))
+                if (!warp_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x615))
                     break;
                 const Item it = decode(slot);
-                mbar_arrive(&item_empty[slot]);
+                __syncwarp();
+                warp_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
                 for (int n = 0; n < it.tiles; ++n) {
                     issue_grad();
                     if (n == 0)
-                        ok = ok && thread_wait(first ? k_full : v_full, static_cast<uint32_t>(k) & 1u, abort_flag,
+                        ok = ok && warp_wait(first ? k_full : v_full, static_cast<uint32_t>(k) & 1u, abort_flag,
                                                a.status, 0x607);
-                    ok = ok && (first ? thread_wait(&q_full[qs.at], qs.phase, abort_flag, a.status, 0x608)
-                                      : thread_wait(&do_full[os.at], os.phase, abort_flag, a.status, 0x609));
+                    ok = ok && (first ? warp_wait(&q_full[qs.at], qs.phase, abort_flag, a.status, 0x608)
+                                      : warp_wait(&do_full[os.at], os.phase, abort_flag, a.status, 0x609));
                     if (!ok) break;
                     tc_fence_after();
                     // S^T = K Q^T, dP^T = V dO^T
                     const uint32_t rows = first ? smem_u32(sQ) + qs.at * C::STREAM : smem_u32(sdO) + os.at * C::STREAM;
-                    mma_scores<D>(tile, own, smem_desc_sw128(rows, 16, 1024));
-                    tc_commit(first ? s_full : dp_full);
-                    if (!first) tc_commit(&do_empty[os.at]);
-                    if (n == it.tiles - 1) tc_commit(first ? k_empty : v_empty);
+                    warp_mma_scores<D, BS>(tile, own, desc_low(rows, 16));
+                    warp_commit(first ? s_full : dp_full);
+                    if (!first) warp_commit(&do_empty[os.at]);
+                    if (n == it.tiles - 1) warp_commit(first ? k_empty : v_empty);
                     last_q = qs.at;
                     last_o = os.at;
                     last_o_phase = os.phase;
@@ -840,8 +811,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 }
             }
             issue_grad();
-            tc_commit(drain);
-            wait_drain(drain, 0, a.status, 0x60A);
+            warp_commit(drain);
+            if (lane == 0) wait_drain(drain, 0, a.status, 0x60A);
         }
         __syncwarp();
     } else {

@@ -142,19 +142,6 @@ __device__ __forceinline__ bool mbar_try_wait_both(uint64_t* a, uint32_t pa, uin
     return ok != 0;
 }
 
-__device__ __forceinline__ bool thread_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
-                                                 volatile uint32_t* abort, int* status, int site) {
-#pragma unroll 1
-    for (int i = 0; !mbar_try_wait_both(a, pa, b, pb); ++i) {
-        if (*abort) return false;
-        if (i >= kPollLimit) {
-            give_up(abort, status, site);
-            return false;
-        }
-    }
-    return true;
-}
-
 // A whole warp, whose lanes poll and leave together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort, int* status,
                                           int site) {
@@ -178,6 +165,88 @@ __device__ __forceinline__ bool warp_wait_both(uint64_t* a, uint32_t pa, uint64_
         }
     }
     return true;
+}
+
+// MMAs and commits issued by a converged warp, one elected lane doing it (the same one
+// each time, so that they run in order).  Operands of an MMA live in uniform registers:
+// in a branch that a single lane takes the compiler moves each of them there one by
+// one, 63 to 67 clocks an MMA, more than the 64 that a 128 x 128 x 16 one runs; a warp
+// that stays together spends 40.
+// Descriptors: low word {address, leading offset}, high word as below (rows of 128
+// bytes, swizzled, 8 rows = 1024 bytes apart).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+
+__device__ __forceinline__ void warp_mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%1, %4};\n\t"
+        "mov.b64 db, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void warp_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 db, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void warp_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// D = A B^T over the head dim: A 128 rows, B N rows, both K-major boxes.
+template <int D, int N>
+__device__ __forceinline__ void warp_mma_scores(uint32_t d_tmem, uint32_t a_low, uint32_t b_low) {
+    constexpr uint32_t id = idesc_bf16_f32(128, N, false, false);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        warp_mma_ss(d_tmem, a_low + (kmajor_step<128>(kk) >> 4), b_low + (kmajor_step<N>(kk) >> 4), id, kk > 0 ? 1u : 0u);
+}
+
+// D (+)= A B^T with A packed bf16 in tensor memory (K columns; k-steps of 8 columns,
+// those of the second half of K from a_tmem + HALF on) and B a tile of K rows, MN-major
+// along the head dim: N in whole 64-wide swizzle atoms, then a 32-wide tail.
+template <int D, int K, int HALF>
+__device__ __forceinline__ void warp_mma_values(uint32_t acc, uint32_t tail, uint32_t a_tmem, uint32_t b_low,
+                                                bool accumulate) {
+    constexpr int N1 = (D / 64) * 64, N2 = D - N1, STEPS = K / 16;
+    constexpr uint32_t id1 = idesc_bf16_f32(128, N1, false, true);
+    constexpr uint32_t id2 = idesc_bf16_f32(128, N2 > 0 ? N2 : 32, false, true);
+#pragma unroll
+    for (int kk = 0; kk < STEPS; ++kk) {
+        const uint32_t on = (accumulate || kk > 0) ? 1u : 0u;
+        const uint32_t at = a_tmem + (kk / (STEPS / 2)) * HALF + (kk % (STEPS / 2)) * 8;
+        const uint32_t bl = b_low + (mnmajor_step(kk) >> 4);
+        warp_mma_ts(acc, at, bl, id1, on);
+        if constexpr (N2 > 0) warp_mma_ts(tail, at, bl + (N1 / 64) * (K * kRowBytes >> 4), id2, on);
+    }
 }
 
 // Zeroes rows first .. rows - 1 of an operand tile of NB 64-column boxes in
