@@ -49,6 +49,25 @@ __global__ void __launch_bounds__(1024) packed_plan_kernel(const int* cu, int nb
     plan_block(cu, nb, T, tile, entries, head, ranks, status);
 }
 
+__device__ __forceinline__ void row_max(const uint32_t (&v)[32], float (&mx)[8]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) mx[i & 7] = fmaxf(mx[i & 7], __uint_as_float(v[i]));
+}
+
+// p = 2^(scale2 s - m) of 32 scores (masked ones are -inf: 2^-inf = 0), packed bf16, and
+// their sums in fp32.
+__device__ __forceinline__ void row_weights(const uint32_t (&v)[32], uint64_t scale2, uint64_t neg_m, uint32_t (&pk)[16],
+                                            uint64_t (&sum)[4]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x0, x1;
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2, neg_m), x0, x1);
+        const float p0 = ex2(x0), p1 = ex2(x1);
+        sum[i & 3] = add_f32x2(sum[i & 3], f32x2(p0, p1));
+        pk[i] = pack_bf16x2(p0, p1);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,  // 128-row boxes
@@ -326,7 +345,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const unsigned ring0 = ring_at;  // ring entry of the item's K_0
             ring_at += 2u * static_cast<unsigned>(it.n_kv);
             if (x == 1 && !it.has_b) continue;  // no B tile in this item
-            const int q = (x ? it.q0[1] : it.q0[0]) + r;
+            const int first_q = (x ? it.q0[1] : it.q0[0]) + (warp & 3) * 32;  // the warp's
+            const int q = first_q + lane;
             const int head = x ? it.head[1] : it.head[0];
             const int jl = x ? it.last[1] : it.last[0];
             float m = -INFINITY, l = 0.0f;
@@ -341,30 +361,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                 for (int c = 0; c < SCH; ++c) tmem_ld32(s_addr + c * 32, v[c]);
                 tmem_wait_ld();
-                // causal mask where this key tile reaches past the row's query
+                // chunks of 32 keys: the warp's queries see the first `live`, the last of
+                // those up to the diagonal if that is in this key tile; the rest holds
+                // nothing for any of them
                 const int k0 = j * BKV;
-                if (k0 + BKV - 1 > q) {
-#pragma unroll
-                    for (int c = 0; c < SCH; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (k0 + c * 32 + i > q) v[c][i] = __float_as_uint(-INFINITY);
-                }
+                const int live = ((first_q - k0) >> 5) + 1;
                 // eight independent max / sum chains: the row is one thread's
                 // work, so its reductions must not be one serial chain
                 float mx8[8];
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) mx8[kk] = -INFINITY;
+                if (live > SCH) {
 #pragma unroll
-                for (int c = 0; c < SCH; ++c)
+                    for (int c = 0; c < SCH; ++c) row_max(v[c], mx8);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx8[i & 7] = fmaxf(mx8[i & 7], __uint_as_float(v[c][i]));
+                    for (int c = 0; c < SCH; ++c) {
+                        if (c == live - 1) {
+#pragma unroll
+                            for (int i = 1; i < 32; ++i)
+                                if (i > lane) v[c][i] = __float_as_uint(-INFINITY);
+                        }
+                        if (c < live) row_max(v[c], mx8);
+                    }
+                }
                 const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                        fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
                 // the reference max only moves when the row max outgrows it by
                 // more than 2^8, so the O rescale below is rare.  A row whose
-                // keys in this tile are all masked (rows past the sequence end
-                // in a 64-key tile) keeps its reference.
+                // keys in this tile are all masked keeps its reference.
                 const float m_new = fmaxf(m, mx * a.scale2);
                 const bool move = (j == 0 && m_new > -INFINITY) || m_new > m + kRescaleLog2;
                 const float alpha = move ? ex2(m - m_new) : 1.0f;
@@ -373,19 +398,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) rs2[kk] = 0ull;  // (0.0f, 0.0f)
                 const uint64_t scale2 = f32x2(a.scale2, a.scale2), neg_m = f32x2(-m, -m);
-                uint32_t pk[SCH][16];
+                // P_x, packed bf16, over the first columns of S_x (already read)
+                if (live > SCH) {
 #pragma unroll
-                for (int c = 0; c < SCH; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        // masked scores are -inf: 2^-inf = 0
-                        float x0, x1;
-                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
-                                              scale2, neg_m), x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        rs2[i & 3] = add_f32x2(rs2[i & 3], f32x2(p0, p1));
-                        pk[c][i] = pack_bf16x2(p0, p1);
+                    for (int c = 0; c < SCH; ++c) {
+                        uint32_t pk[16];
+                        row_weights(v[c], scale2, neg_m, pk, rs2);
+                        tmem_st16(s_addr + 16 * c, pk);
                     }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < SCH; ++c) {
+                        uint32_t pk[16];
+                        if (c < live) {
+                            row_weights(v[c], scale2, neg_m, pk, rs2);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                        }
+                        tmem_st16(s_addr + 16 * c, pk);
+                    }
+                }
                 float rsv[8];
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) f32x2_split(rs2[kk], rsv[2 * kk], rsv[2 * kk + 1]);
@@ -418,9 +451,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                     zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - k0, r, 128);
                 }
-                // P_x, packed bf16, over the first columns of S_x (already read)
-#pragma unroll
-                for (int c = 0; c < SCH; ++c) tmem_st16(s_addr + 16 * c, pk[c]);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -435,24 +465,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float inv = 1.0f / l;
             const bool q_ok = q < it.len;
             const long long tok = static_cast<long long>(it.row0) + q;
-            uint4* dst = reinterpret_cast<uint4*>(a.O + (tok * a.nh + head) * D);
+            const RowsOut out(a.O, static_cast<long long>(a.nh) * D, static_cast<long long>(it.row0) + first_q, head * D,
+                              it.len - first_q);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(lane_addr + C::o_chunk(x, c), o);  // every lane: warp-collective
-                tmem_wait_ld();
-                if (q_ok) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 u;
-                        u.x = pack_bf16x2(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
-                        u.y = pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
-                        u.z = pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
-                        u.w = pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
-                        dst[c * 4 + i] = u;
-                    }
-                }
-            }
+            for (int c = 0; c < D / 32; ++c) read_out(out, c, lane_addr + C::o_chunk(x, c), inv);
             if (q_ok) a.lse[head * a.T + tok] = m + lg2(l);
             // O_x is in registers or on its way to memory: the MMA may reuse it
             tc_fence_before();

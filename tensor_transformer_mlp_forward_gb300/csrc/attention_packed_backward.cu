@@ -138,10 +138,10 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t (&v)[32], int i) {
     return f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
 }
 
-// x = scale2 s + neg_lse, p = 2^x of 32 columns of a row.  With MASK, columns c, c + 1,
-// ... outside [lo, hi) give an exact zero whatever s holds.
+// x = scale2 s + neg_lse, p = 2^x of 32 columns of a row.  With MASK, columns outside
+// [lo, hi) give an exact zero whatever s holds.
 template <bool MASK, typename Lse>
-__device__ __forceinline__ void weights(const uint32_t (&v)[32], uint64_t scale2, Lse neg_lse, int c, int lo, int hi,
+__device__ __forceinline__ void weights(const uint32_t (&v)[32], uint64_t scale2, Lse neg_lse, int lo, int hi,
                                         float (&p)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -151,7 +151,7 @@ __device__ __forceinline__ void weights(const uint32_t (&v)[32], uint64_t scale2
         f32x2_split(fma_f32x2(pair_of(v, i + 2), scale2, l.y), x[2], x[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if (MASK && (c + i + e < lo || c + i + e >= hi)) x[e] = -INFINITY;
+            if (MASK && (i + e < lo || i + e >= hi)) x[e] = -INFINITY;
             p[i + e] = ex2(x[e]);
         }
     }
@@ -159,8 +159,8 @@ __device__ __forceinline__ void weights(const uint32_t (&v)[32], uint64_t scale2
 
 // dS = p (dP + neg_delta), packed; masked columns are exact zeros here too.
 template <bool MASK, typename Delta>
-__device__ __forceinline__ void score_grads(const uint32_t (&v)[32], const float (&p)[32], Delta neg_dlt, int c, int lo,
-                                            int hi, uint32_t (&dd)[16]) {
+__device__ __forceinline__ void score_grads(const uint32_t (&v)[32], const float (&p)[32], Delta neg_dlt, int lo, int hi,
+                                            uint32_t (&dd)[16]) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
         const ulonglong2 l = neg_dlt(i / 4);
@@ -170,35 +170,14 @@ __device__ __forceinline__ void score_grads(const uint32_t (&v)[32], const float
         if (MASK) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (c + i + e < lo || c + i + e >= hi) x[e] = 0.0f;
+                if (i + e < lo || i + e >= hi) x[e] = 0.0f;
         }
         dd[i / 2] = pack_bf16x2(x[0], x[1]);
         dd[i / 2 + 1] = pack_bf16x2(x[2], x[3]);
     }
 }
 
-// Reads chunks [c0, c1) of 32 accumulator columns of this thread's row, scales and
-// rounds them, and stores them at dst (a row of D values) when `store`.
-template <int D>
-__device__ __forceinline__ void read_out(uint32_t acc, uint32_t tail, int c0, int c1, float f, bool store,
-                                         __nv_bfloat16* row) {
-    uint4* dst = reinterpret_cast<uint4*>(row);
-    for (int c = c0; c < c1; ++c) {
-        uint32_t v[32];
-        // tcgen05.ld is warp-collective: every lane loads
-        tmem_ld32(c < (D / 64) * 2 ? acc + 32 * c : tail + 32 * (c - (D / 64) * 2), v);
-        tmem_wait_ld();
-        if (store) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dst[c * 4 + i] = make_uint4(pack_scaled(v[8 * i], v[8 * i + 1], f), pack_scaled(v[8 * i + 2], v[8 * i + 3], f),
-                                            pack_scaled(v[8 * i + 4], v[8 * i + 5], f),
-                                            pack_scaled(v[8 * i + 6], v[8 * i + 7], f));
-        }
-    }
-}
-
-// delta = rowsum(dO O) of every token and head; the last CTA makes the plan.
+// delta = rowsum(dO O) of every token and head; the first CTA makes the plan.
 template <int D>
 __global__ void __launch_bounds__(kDeltaThreads)
     packed_prepare_kernel(const __nv_bfloat16* dO, const __nv_bfloat16* O, long long T, int nh, float* delta,
@@ -463,17 +442,18 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         bool ok = true;
         int g = 0, k_slot = 0;
         struct Pending {
-            int k, head;
-            bool q_ok;
-            long long tok;
+            int k, head, valid;
+            long long row;
         };
-        Pending pend{-1, 0, false, 0};
+        Pending pend{-1, 0, 0, 0};
         auto readout = [&]() -> bool {
             if (!warp_wait(dq_done, static_cast<uint32_t>(pend.k) & 1u, abort_flag, a.status, 0x50B))
                 return false;
             tc_fence_after();
-            read_out<D>(lane_addr + C::kDQ, lane_addr + C::kDQTail, w ? MID : 0, w ? CH : MID, a.scale, pend.q_ok,
-                        a.dQ + pend.tok * a.ldq + pend.head * D);
+            const RowsOut out(a.dQ, a.ldq, pend.row, pend.head * D, pend.valid);
+            for (int c = w ? MID : 0; c < (w ? CH : MID); ++c)
+                read_out(out, c, lane_addr + (c < (D / 64) * 2 ? C::kDQ + 32 * c : C::kDQTail + 32 * (c - (D / 64) * 2)),
+                         a.scale);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(dq_free);
@@ -488,7 +468,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             if (it.len == 0) break;
-            const int q = it.q0 + r;
+            const int first_q = it.q0 + (warp & 3) * 32, q = it.q0 + r;  // the warp's first, this lane's
             const bool q_ok = q < it.len;
             const long long tok = static_cast<long long>(it.row0) + q;
             const float lse = q_ok ? __ldg(a.lse + it.head * a.T + tok) : 0.0f;
@@ -497,8 +477,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             const uint64_t scale2 = f32x2(a.scale2, a.scale2);
             for (int j = 0; j < it.n_kv; ++j, ++g) {
                 const int b = g & 1, key0 = j * BS + w * HALF;  // first key of this half
-                // keys after the warp's first query (keys behind the sequence's end are)
-                const bool masked = key0 + HALF - 1 > it.q0 + (warp & 3) * 32;
+                // chunks of 32 keys: the warp's queries see the first `live`, the last of
+                // those up to the diagonal if that is in this half (keys behind the
+                // sequence's end come after its last query)
+                const int live = ((first_q - key0) >> 5) + 1;
                 if (!warp_wait(s_full, static_cast<uint32_t>(g) & 1u, abort_flag, a.status, 0x50C)) {
                     ok = false;
                     break;
@@ -511,7 +493,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 if (lane == 0) mbar_arrive(s_read);
                 float p[HALF / 32][32];
 #pragma unroll
-                for (int c = 0; c < HALF / 32; ++c) weights<false>(v[c], scale2, neg_lse, 0, 0, 0, p[c]);
+                for (int c = 0; c < HALF / 32; ++c)
+                    if (c < live) weights<false>(v[c], scale2, neg_lse, 0, 0, p[c]);
                 if (!warp_wait(&dp_full[b], static_cast<uint32_t>(g >> 1) & 1u, abort_flag, a.status, 0x50D)) {
                     ok = false;
                     break;
@@ -522,10 +505,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
                 for (int c = 0; c < HALF / 32; ++c) {
                     uint32_t dd[16];
-                    if (masked)
-                        score_grads<true>(v[c], p[c], neg_dlt, key0 + 32 * c, 0, q + 1, dd);
-                    else
-                        score_grads<false>(v[c], p[c], neg_dlt, 0, 0, 0, dd);
+                    if (c >= live) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) dd[i] = 0u;
+                    } else if (c == live - 1) {
+                        score_grads<true>(v[c], p[c], neg_dlt, 0, lane + 1, dd);
+                    } else {
+                        score_grads<false>(v[c], p[c], neg_dlt, 0, 0, dd);
+                    }
                     tmem_st16(dp + 16 * c, dd);
                 }
                 tmem_wait_st();
@@ -543,7 +530,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 }
             }
             if (!ok) break;
-            pend = Pending{k, it.head, q_ok, tok};
+            pend = Pending{k, it.head, it.len - first_q, static_cast<long long>(it.row0) + first_q};
         }
         if (ok && pend.k >= 0) readout();
     }
@@ -833,7 +820,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             if (it.len == 0) break;
-            const int key = it.k0 + r;
+            const int first_key = it.k0 + (warp & 3) * 32;  // the warp's
             // a value of the tile's lse or delta per thread, loaded a tile ahead
             float stat_n = 0.0f;
             auto fetch = [&](int head, int i) {
@@ -849,8 +836,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 const int q0 = (it.i0 + i) * BS + w * HALF;  // first query of this half
                 const int valid = it.len - (it.i0 + i) * BS;  // queries of the tile inside the sequence
                 const bool tail = valid < BS;
-                // queries before the warp's last key, or behind the sequence's end
-                const bool masked = q0 < it.k0 + (warp & 3) * 32 + 31 || q0 + HALF > it.len;
+                // chunks of 32 queries: all of them see the warp's keys (full), none does or
+                // none is inside the sequence (dead), or those in [lo, hi)
+                auto full = [&](int c) { return q0 + 32 * c > first_key && q0 + 32 * c + 32 <= it.len; };
+                auto dead = [&](int c) { return q0 + 32 * c < first_key || q0 + 32 * c >= it.len; };
+                auto lo = [&](int c) { return q0 + 32 * c == first_key ? lane : 0; };
+                auto hi = [&](int c) { return it.len - q0 - 32 * c; };
                 float* stat = stats + ((g & 1) * 2 + w) * 2 * HALF;
                 if (r < 2 * HALF) stat[r] = stat_n;
                 __syncwarp();
@@ -874,10 +865,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                     tmem_ld32(lane_addr + C::kS + w * HALF + 32 * c, v);
                     tmem_wait_ld();
                     const ColumnValues neg_lse{stat + 32 * c};
-                    if (masked)
-                        weights<true>(v, scale2, neg_lse, q0 + 32 * c, key, it.len, p[c]);
-                    else
-                        weights<false>(v, scale2, neg_lse, 0, 0, 0, p[c]);
+                    if (full(c)) {
+                        weights<false>(v, scale2, neg_lse, 0, 0, p[c]);
+                    } else if (dead(c)) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) p[c][e] = 0.0f;
+                    } else {
+                        weights<true>(v, scale2, neg_lse, lo(c), hi(c), p[c]);
+                    }
                     uint32_t pp[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) pp[e] = pack_bf16x2(p[c][2 * e], p[c][2 * e + 1]);
@@ -905,10 +900,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                     tmem_ld32(lane_addr + C::dp(0) + w * HALF + 32 * c, v);
                     tmem_wait_ld();
                     const ColumnValues neg_dlt{stat + HALF + 32 * c};
-                    if (masked)
-                        score_grads<true>(v, p[c], neg_dlt, q0 + 32 * c, key, it.len, dd);
-                    else
-                        score_grads<false>(v, p[c], neg_dlt, 0, 0, 0, dd);
+                    if (full(c)) {
+                        score_grads<false>(v, p[c], neg_dlt, 0, 0, dd);
+                    } else if (dead(c)) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) dd[e] = 0u;
+                    } else {
+                        score_grads<true>(v, p[c], neg_dlt, lo(c), hi(c), dd);
+                    }
                     tmem_st16(lane_addr + C::dp(0) + w * HALF + 16 * c, dd);
                 }
                 tmem_wait_st();
@@ -926,14 +925,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             }
             tc_fence_after();
             // half 0 reads dV out, half 1 dK
-            const long long tok = static_cast<long long>(it.row0) + key;
-            const bool key_ok = key < it.len;
-            if (w == 0)
-                read_out<D>(lane_addr + C::acc(0), lane_addr + C::acc_tail(0), 0, D / 32, 1.0f, key_ok,
-                            a.dV + tok * a.ldv + it.kv_head * D);
-            else
-                read_out<D>(lane_addr + C::acc(1), lane_addr + C::acc_tail(1), 0, D / 32, a.scale, key_ok,
-                            a.dK + tok * a.ldk + it.kv_head * D);
+            const RowsOut out(w ? a.dK : a.dV, w ? a.ldk : a.ldv, static_cast<long long>(it.row0) + first_key,
+                              it.kv_head * D, it.len - first_key);
+            for (int c = 0; c < D / 32; ++c)
+                read_out(out, c, lane_addr + (c < (D / 64) * 2 ? C::acc(w) + 32 * c
+                                                               : C::acc_tail(w) + 32 * (c - (D / 64) * 2)),
+                         w ? a.scale : 1.0f);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(grad_free);

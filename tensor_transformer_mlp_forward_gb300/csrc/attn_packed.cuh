@@ -269,5 +269,60 @@ __device__ __forceinline__ uint32_t pack_scaled(uint32_t lo, uint32_t hi, float 
     return pack_bf16x2(__uint_as_float(lo) * f, __uint_as_float(hi) * f);
 }
 
+// 32 bytes, to an address on a 32-byte boundary (wide) or a 16-byte one.
+__device__ __forceinline__ void store_32(void* p, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Where a warp's 32 accumulator rows go: rows of a matrix one after another, `ld`
+// values apart, the first `valid` of them.
+struct RowsOut {
+    __nv_bfloat16* row;  // this lane's
+    long long ld;
+    int valid;           // rows from this warp's first row on
+    bool wide;           // rows start on 32-byte boundaries
+
+    __device__ __forceinline__ RowsOut(__nv_bfloat16* base, long long ld_, long long first_row, int col, int valid_)
+        : row(base + (first_row + (threadIdx.x & 31)) * ld_ + col), ld(ld_), valid(valid_),
+          wide(((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(ld_ * 2)) & 31u) == 0) {}
+
+    // Columns [32 c, 32 c + 32) of this lane's row, 16 packed words.  A lane's stores
+    // to its own row alone would touch 32 lines an instruction (a read-out of 128
+    // columns took 3600 clocks): neighbours exchange half a chunk, so that two lanes
+    // write 64 bytes of one row, in 32-byte stores.
+    __device__ __forceinline__ void store(int c, const uint32_t (&w)[16]) const {
+        const int lane = threadIdx.x & 31;
+        const bool odd = lane & 1;
+        uint32_t even_row[8], odd_row[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[i] : w[8 + i], 1);
+            even_row[i] = odd ? got : w[i];
+            odd_row[i] = odd ? w[8 + i] : got;
+        }
+        const int even = lane & ~1;
+        __nv_bfloat16* at = row + 32 * c + (odd ? 16 : 0);
+        if (even < valid) store_32(odd ? at - ld : at, even_row, wide);
+        if (even + 1 < valid) store_32(odd ? at : at + ld, odd_row, wide);
+    }
+};
+
+// Scales and rounds accumulator chunk c (32 columns from `addr` on) and stores it.
+__device__ __forceinline__ void read_out(const RowsOut& out, int c, uint32_t addr, float f) {
+    uint32_t v[32], w[16];
+    tmem_ld32(addr, v);  // warp-collective: every lane loads
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_scaled(v[2 * i], v[2 * i + 1], f);
+    out.store(c, w);
+}
+
 }  // namespace
 }  // namespace tpmlp
