@@ -386,9 +386,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                     const uint32_t qdesc = desc_low(smem_u32(sQ), 16);
                     ok = warp_wait(q_full, item_parity, abort_flag, a.status, 0x506);
                     for (int j = 0; j < it.n_kv && ok; ++j, ++g, ks.next()) {
-                        if (!(ok = warp_wait(&k_full[ks.at], ks.phase, abort_flag, a.status, 0x507) &&
-                                   (g == 0 || warp_wait(s_read, static_cast<uint32_t>(g - 1) & 1u, abort_flag,
-                                                          a.status, 0x508))))
+                        // (parity 1 of a barrier that has seen no phase counts as complete)
+                        if (!(ok = warp_wait_both(&k_full[ks.at], ks.phase, s_read, static_cast<uint32_t>(g + 1) & 1u,
+                                                  abort_flag, a.status, 0x507)))
                             break;
                         tc_fence_after();
                         warp_mma_scores<D, BS>(tmem + C::kS, qdesc, desc_low(smem_u32(sK) + ks.at * C::STREAM, 16));
@@ -401,9 +401,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                     for (int j = 0; j < it.n_kv && ok; ++j, ++g, vs.next()) {
                         const int b = g & 1;
                         // over the dS of the tile before the last, which its dQ has read
-                        if (!(ok = warp_wait(&v_full[vs.at], vs.phase, abort_flag, a.status, 0x519) &&
-                                   (g < 2 || warp_wait(&ds_used[b], static_cast<uint32_t>((g - 2) >> 1) & 1u,
-                                                         abort_flag, a.status, 0x51A))))
+                        if (!(ok = warp_wait_both(&v_full[vs.at], vs.phase, &ds_used[b],
+                                                  static_cast<uint32_t>((g >> 1) + 1) & 1u, abort_flag, a.status, 0x519)))
                             break;
                         tc_fence_after();
                         warp_mma_scores<D, BS>(tmem + C::dp(b), dodesc,
@@ -749,11 +748,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 // the first products of an item overwrite the last item's gradients
                 if (last_first && last_k >= 1)
                     ok = warp_wait(grad_free, static_cast<uint32_t>(last_k - 1) & 1u, abort_flag, a.status, 0x614);
-                if (first)
-                    ok = ok && warp_wait(&do_full[last_o], last_o_phase, abort_flag, a.status, 0x605) &&
-                         warp_wait(p_full, parity, abort_flag, a.status, 0x606);
-                else
-                    ok = ok && warp_wait(ds_full, parity, abort_flag, a.status, 0x60E);
+                ok = ok && (first ? warp_wait_both(&do_full[last_o], last_o_phase, p_full, parity, abort_flag, a.status,
+                                                   0x605)
+                                  : warp_wait(ds_full, parity, abort_flag, a.status, 0x60E));
                 if (!ok) return;
                 tc_fence_after();
                 // dV += P^T dO, dK += dS^T Q
@@ -772,12 +769,17 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 warp_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
                 for (int n = 0; n < it.tiles; ++n) {
-                    issue_grad();
-                    if (n == 0)
-                        ok = ok && warp_wait(first ? k_full : v_full, static_cast<uint32_t>(k) & 1u, abort_flag,
-                                               a.status, 0x607);
-                    ok = ok && (first ? warp_wait(&q_full[qs.at], qs.phase, abort_flag, a.status, 0x608)
-                                      : warp_wait(&do_full[os.at], os.phase, abort_flag, a.status, 0x609));
+                    uint64_t* full = first ? &q_full[qs.at] : &do_full[os.at];
+                    const uint32_t phase = first ? qs.phase : os.phase;
+                    if (n == 0) {
+                        issue_grad();
+                        ok = ok && warp_wait_both(first ? k_full : v_full, static_cast<uint32_t>(k) & 1u, full, phase,
+                                                  abort_flag, a.status, 0x607);
+                    } else {
+                        // landed by now as a rule: the wait is over before the softmax is
+                        ok = warp_wait(full, phase, abort_flag, a.status, 0x608);
+                        issue_grad();
+                    }
                     if (!ok) break;
                     tc_fence_after();
                     // S^T = K Q^T, dP^T = V dO^T
@@ -852,8 +854,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 }
                 if (n + 1 < it.tiles) fetch(head, i);
                 // (a warp that passes has left the tile before the last, whose place this was)
-                if (!warp_wait(&stat_full[w], parity, abort_flag, a.status, 0x61B) ||
-                    !warp_wait(s_full, parity, abort_flag, a.status, 0x60B)) {
+                if (!warp_wait_both(&stat_full[w], parity, s_full, parity, abort_flag, a.status, 0x60B)) {
                     ok = false;
                     break;
                 }
