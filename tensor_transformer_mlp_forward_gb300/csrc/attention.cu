@@ -497,12 +497,67 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 // ------------------------------------------------------------ delta
 
+// delta[head, tok] = sum_c dO[tok, head*d + c] * O[tok, head*d + c], fp32.
+// The (token, head) segments of d elements lie end to end in dO and O, d/8
+// 16-byte chunks each.  A CTA takes kDeltaSegs(d) whole segments (at most
+// 2048 chunks): its 256 threads read the chunks coalesced (chunk base + tid +
+// 256 k, all loads issued before any product), each chunk's 8 products are
+// summed and parked in shared memory, and one thread per segment adds its
+// chunks in order.
+constexpr int kDeltaChunks = 2048;
+constexpr int kDeltaThreads = 256;
+template <int D>
+constexpr int delta_segs() { return kDeltaChunks / (D / 8); }
+
 template <int D>
 __global__ void __launch_bounds__(kDeltaThreads)
     attn_delta_kernel(const __nv_bfloat16* __restrict__ dO, const __nv_bfloat16* __restrict__ O,
                       long long T, int nh, float* __restrict__ delta) {
     pdl_launch_dependents();  // the next kernel may begin its launch
-    attn_delta_block<D>(dO, O, T, nh, delta, blockIdx.x);
+    constexpr int CH = D / 8;                 // chunks per segment
+    constexpr int SEGS = delta_segs<D>();     // segments per CTA
+    constexpr int PER = (SEGS * CH + kDeltaThreads - 1) / kDeltaThreads;
+    __shared__ float part[SEGS * CH];
+    const long long seg0 = static_cast<long long>(blockIdx.x) * SEGS;
+    const long long segs_total = T * nh;
+    const int segs = static_cast<int>(segs_total - seg0 < SEGS ? segs_total - seg0 : SEGS);
+    const int chunks = segs * CH;
+    const uint4* g = reinterpret_cast<const uint4*>(dO) + seg0 * CH;
+    const uint4* o = reinterpret_cast<const uint4*>(O) + seg0 * CH;
+    uint4 gu[PER], ou[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = threadIdx.x + k * kDeltaThreads;
+        if (c < chunks) {
+            gu[k] = __ldg(g + c);
+            ou[k] = __ldg(o + c);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = threadIdx.x + k * kDeltaThreads;
+        if (c < chunks) {
+            const uint32_t gw[4] = {gu[k].x, gu[k].y, gu[k].z, gu[k].w};
+            const uint32_t ow[4] = {ou[k].x, ou[k].y, ou[k].z, ou[k].w};
+            float acc = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc = fmaf(__uint_as_float(gw[j] << 16), __uint_as_float(ow[j] << 16), acc);
+                acc = fmaf(__uint_as_float(gw[j] & 0xFFFF0000u), __uint_as_float(ow[j] & 0xFFFF0000u), acc);
+            }
+            part[c] = acc;
+        }
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < segs; t += kDeltaThreads) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) sum += part[t * CH + i];
+        const long long sg = seg0 + t;
+        const long long tok = sg / nh;
+        const long long head = sg - tok * nh;
+        delta[head * T + tok] = sum;
+    }
 }
 
 // ------------------------------------------------------------- dQ

@@ -81,6 +81,8 @@ struct BwdArgs {
     const int4* entries;
     unsigned* plan;
     int nh, nkv, group;
+    int split;           // parts of a group's heads (dK/dV kernel)
+    float* parts;        // [split][T][nkv][dV, dK][d] where split > 1
     long long T;
     float scale, scale2;
     const float* lse;    // [nh, T]
@@ -177,17 +179,52 @@ __device__ __forceinline__ void score_grads(const uint32_t (&v)[32], const float
     }
 }
 
-// delta = rowsum(dO O) of every token and head; the first CTA makes the plan.
+// delta = rowsum(dO O) of every token and head; the first CTA makes the plan.  A warp
+// takes a head of 8 tokens, all of their loads at once, a row to as many lanes as it has
+// 16-byte pieces; the next warp the next head, whose rows lie behind.
+constexpr int kPrepareThreads = 256, kPrepareTokens = 8;
+
 template <int D>
-__global__ void __launch_bounds__(kDeltaThreads)
+__global__ void __launch_bounds__(kPrepareThreads)
     packed_prepare_kernel(const __nv_bfloat16* dO, const __nv_bfloat16* O, long long T, int nh, float* delta,
                           const int* cu, int nb, int4* entries, unsigned* plan, int* ranks, int* status) {
     pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0) {
         plan_block(cu, nb, static_cast<int>(T), 128, entries, plan, ranks, status);
-    else
-        attn_delta_block<D>(dO, O, T, nh, delta, blockIdx.x - 1);
+        return;
+    }
+    constexpr int PIECES = D / 8, LANES = PIECES <= 8 ? 8 : PIECES <= 16 ? 16 : 32;
+    constexpr int ROWS = 32 / LANES, PASSES = kPrepareTokens / ROWS;
+    const int lane = threadIdx.x & 31, sub = lane % LANES;
+    const long long unit = static_cast<long long>(blockIdx.x - 1) * (kPrepareThreads / 32) + threadIdx.x / 32;
+    const long long tok0 = unit / nh * kPrepareTokens + lane / LANES;
+    const long long head = unit % nh;
+    uint4 g[PASSES], o[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const long long tok = tok0 + i * ROWS;
+        g[i] = o[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (tok < T && sub < PIECES) {
+            const long long at = (tok * nh + head) * PIECES + sub;
+            g[i] = __ldg(reinterpret_cast<const uint4*>(dO) + at);
+            o[i] = __ldg(reinterpret_cast<const uint4*>(O) + at);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w}, ow[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            sum = fmaf(__uint_as_float(gw[k] << 16), __uint_as_float(ow[k] << 16), sum);
+            sum = fmaf(__uint_as_float(gw[k] & 0xFFFF0000u), __uint_as_float(ow[k] & 0xFFFF0000u), sum);
+        }
+#pragma unroll
+        for (int x = LANES / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        const long long tok = tok0 + i * ROWS;
+        if (sub == 0 && tok < T) delta[head * T + tok] = sum;
+    }
 }
 
 // ------------------------------------------------------------- dQ
@@ -197,7 +234,6 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,  // 128 rows
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,   // BS rows
                      const BwdArgs a) {
-    pdl_launch_dependents();
     using C = BwdCfg<D>;
     constexpr int FAR = C::FAR, NEAR = C::NEAR, BS = C::BS, HALF = C::HALF;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -282,6 +318,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tc_fence_after();
     const uint32_t tmem = misc[0];
     pdl_wait();  // the plan and delta are there
+    pdl_launch_dependents();  // the dK/dV kernel needs nothing else
 
     if (warp == 8) {
         // ------------------------------------------------------ producer
@@ -549,7 +586,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     packed_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,   // 128 rows
                        const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,  // BS rows
                        const BwdArgs a) {
-    pdl_launch_dependents();
     using C = BwdCfg<D>;
     constexpr int FAR = C::FAR, NEAR = C::NEAR, BS = C::BS, HALF = C::HALF;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -584,7 +620,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     struct Item {
-        int row0, len, k0, kv_head, i0, nq, tiles;
+        int row0, len, k0, kv_head, part, head, i0, nq, tiles;
     };
     auto decode = [&](int slot) {
         const volatile int* p = items + 4 * slot;
@@ -592,10 +628,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         it.row0 = p[0];
         it.len = p[1];
         it.k0 = p[2] * 128;
-        it.kv_head = p[3];
+        it.kv_head = p[3] / a.split;
+        it.part = p[3] - it.kv_head * a.split;
+        it.head = it.kv_head * a.group + it.part * (a.group / a.split);
         it.i0 = it.k0 / BS;                         // first query tile that sees the keys
         it.nq = (it.len + BS - 1) / BS - it.i0;     // query tiles of each head
-        it.tiles = it.nq * a.group;
+        it.tiles = it.nq * (a.group / a.split);
         return it;
     };
 
@@ -635,7 +673,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    pdl_wait();  // the plan and delta are there
+    // No pdl_wait() here: the dQ kernel lets this one begin once the plan and delta are
+    // complete, and where its CTAs run out of items this one's take the SMs over.  What
+    // was written since (plan, delta) is read past the first-level cache.
 
     if (warp == 8) {
         // ------------------------------------------------------ producer
@@ -644,7 +684,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             prefetch_tmap(&tm_v);
             prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_do);
-            const unsigned total = a.plan[kPlanCount] * static_cast<unsigned>(a.nkv);
+            const unsigned units = static_cast<unsigned>(a.nkv * a.split);
+            const unsigned total = __ldcg(&a.plan[kPlanCount]) * units;
             RingSlot<FAR> qs;
             RingSlot<NEAR> os;
             int k_loads = 0, v_loads = 0;
@@ -662,11 +703,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                     break;
                 }
                 {
-                    const int4 e = a.entries[item / a.nkv];
+                    const int4 e = __ldcg(&a.entries[item / units]);
                     items[4 * slot] = e.x;
                     items[4 * slot + 1] = e.y;
                     items[4 * slot + 2] = e.w - 1 - e.z;  // the highest rank is the first key tile
-                    items[4 * slot + 3] = static_cast<int>(item % a.nkv);
+                    items[4 * slot + 3] = static_cast<int>(item % units);
                 }
                 mbar_arrive(&item_full[slot]);
                 const Item it = decode(slot);
@@ -677,7 +718,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 for (int b = 0; b < C::NB; ++b)
                     tma_load_3d(&tm_k, smem_u32(k_full), smem_u32(sK) + b * 128 * kRowBytes, kcol + 64 * b, row, 0);
                 ++k_loads;
-                int head = it.kv_head * a.group, i = 0;
+                int head = it.head, i = 0;
                 for (int n = 0; n < it.tiles; ++n) {
                     const int qrow = it.row0 + (it.i0 + i) * BS;
                     if (!thread_wait(&q_empty[qs.at], qs.phase ^ 1u, abort_flag, a.status, 0x601)) {
@@ -828,10 +869,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             auto fetch = [&](int head, int i) {
                 if (r < 2 * HALF) {
                     const int qq = (it.i0 + i) * BS + w * HALF + r % HALF;
-                    stat_n = qq < it.len ? -__ldg((r < HALF ? a.lse : a.delta) + head * a.T + it.row0 + qq) : 0.0f;
+                    stat_n = qq < it.len ? -__ldcg((r < HALF ? a.lse : a.delta) + head * a.T + it.row0 + qq) : 0.0f;
                 }
             };
-            int head = it.kv_head * a.group, i = 0;
+            int head = it.head, i = 0;
             fetch(head, 0);
             for (int n = 0; n < it.tiles; ++n, ++g) {
                 const uint32_t parity = static_cast<uint32_t>(g) & 1u;
@@ -926,12 +967,30 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             }
             tc_fence_after();
             // half 0 reads dV out, half 1 dK
-            const RowsOut out(w ? a.dK : a.dV, w ? a.ldk : a.ldv, static_cast<long long>(it.row0) + first_key,
-                              it.kv_head * D, it.len - first_key);
-            for (int c = 0; c < D / 32; ++c)
-                read_out(out, c, lane_addr + (c < (D / 64) * 2 ? C::acc(w) + 32 * c
-                                                               : C::acc_tail(w) + 32 * (c - (D / 64) * 2)),
-                         w ? a.scale : 1.0f);
+            auto chunk = [&](int c) {
+                return lane_addr + (c < (D / 64) * 2 ? C::acc(w) + 32 * c : C::acc_tail(w) + 32 * (c - (D / 64) * 2));
+            };
+            const long long first_row = static_cast<long long>(it.row0) + first_key;
+            if (a.split == 1) {
+                const RowsOut out(w ? a.dK : a.dV, w ? a.ldk : a.ldv, first_row, it.kv_head * D, it.len - first_key);
+                for (int c = 0; c < D / 32; ++c) read_out(out, c, chunk(c), w ? a.scale : 1.0f);
+            } else {
+                // a part of the group's heads: its fp32 sum
+                float* row = a.parts + (((it.part * a.T + first_row + lane) * a.nkv + it.kv_head) * 2 + w) * D;
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(chunk(c), v);
+                    tmem_wait_ld();
+                    if (lane < it.len - first_key)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t u[8];
+#pragma unroll
+                            for (int f = 0; f < 8; ++f) u[f] = v[8 * e + f];
+                            store_32(row + 32 * c + 8 * e, u, true);
+                        }
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(grad_free);
@@ -944,6 +1003,35 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    pdl_wait();  // what follows this kernel follows the dQ kernel too
+    pdl_launch_dependents();
+}
+
+// dK and dV from the parts' sums, added in order: 8 values a thread, of the tokens that
+// are in sequences.
+__global__ void __launch_bounds__(256)
+    packed_parts_kernel(const BwdArgs a, int d, const int* cu, int nb) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int pieces = d / 8;
+    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;  // [token][kv head][dV, dK][piece]
+    const long long tok = i / (2 * pieces * a.nkv);
+    if (a.plan[kPlanCount] == 0u || tok < cu[0] || tok >= cu[nb]) return;
+    const int rest = static_cast<int>(i - tok * (2 * pieces * a.nkv));
+    const int head = rest / (2 * pieces), x = rest / pieces & 1, c = rest % pieces * 8;
+    const long long plane = a.T * a.nkv * 2 * d;
+    const float* p = a.parts + i * 8;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < a.split; ++s) {
+        const float4 lo = *reinterpret_cast<const float4*>(p + s * plane);
+        const float4 hi = *reinterpret_cast<const float4*>(p + s * plane + 4);
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    }
+    const float f = x ? a.scale : 1.0f;
+    __nv_bfloat16* out = (x ? a.dK + tok * a.ldk : a.dV + tok * a.ldv) + head * d + c;
+    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
+                                                pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
 }
 
 template <int D>
@@ -951,9 +1039,9 @@ cudaError_t launch_bwd(const CUtensorMap& q128, const CUtensorMap& do128, const 
                        const CUtensorMap& v128, const CUtensorMap& q_s, const CUtensorMap& do_s,
                        const CUtensorMap& k_s, const CUtensorMap& v_s, const PackedAttn& p, const BwdArgs& a,
                        cudaStream_t st, int* launches) {
-    const long long segs = static_cast<long long>(p.T) * p.nh;
-    const unsigned blocks = static_cast<unsigned>((segs + delta_segs<D>() - 1) / delta_segs<D>());
-    cudaError_t e = launch_dependent(packed_prepare_kernel<D>, dim3(blocks + 1), dim3(kDeltaThreads), 0, st, p.dO,
+    const long long warps = (static_cast<long long>(p.T) + kPrepareTokens - 1) / kPrepareTokens * p.nh;
+    const unsigned blocks = static_cast<unsigned>((warps + kPrepareThreads / 32 - 1) / (kPrepareThreads / 32));
+    cudaError_t e = launch_dependent(packed_prepare_kernel<D>, dim3(blocks + 1), dim3(kPrepareThreads), 0, st, p.dO,
                                      p.O_in, static_cast<long long>(p.T), p.nh, p.delta, p.cu_seqlens, p.nb, p.entries,
                                      p.plan, p.ranks, p.status);
     if (e != cudaSuccess) return e;
@@ -970,12 +1058,35 @@ cudaError_t launch_bwd(const CUtensorMap& q128, const CUtensorMap& do128, const 
         (e = launch_dependent(kq, grid(p.nh), dim3(kDqThreads), smem, st, q128, do128, k_s, v_s, a)) != cudaSuccess)
         return e;
     ++*launches;
-    e = launch_dependent(kk, grid(p.nkv), dim3(kDkvThreads), smem, st, k128, v128, q_s, do_s, a);
-    if (e == cudaSuccess) ++*launches;
+    if ((e = launch_dependent(kk, grid(static_cast<long long>(p.nkv) * a.split), dim3(kDkvThreads), smem, st, k128, v128,
+                              q_s, do_s, a)) != cudaSuccess)
+        return e;
+    ++*launches;
+    if (a.split > 1) {
+        const long long pieces = static_cast<long long>(p.T) * p.nkv * 2 * (D / 8);
+        e = launch_dependent(packed_parts_kernel, dim3(static_cast<unsigned>((pieces + 255) / 256)), dim3(256), 0, st, a,
+                             D, p.cu_seqlens, p.nb);
+        if (e == cudaSuccess) ++*launches;
+    }
     return e;
 }
 
 }  // namespace
+
+// Parts that a group's heads are dealt to in the dK/dV kernel: one where key tiles and
+// key/value heads make an item and a half for each SM, else the fewest that do.  Whole
+// groups of 16 heads of 128 on one key/value head took 250 us (8 x 1024 tokens) and
+// 1688 us (one sequence of 8192), in parts 144 and 585; two parts where the items were
+// 256 cost 15 % at 8 x 1024 tokens (their sums go through memory) and gained 5 % at 8192.
+// The sums are at most some 100 MB, whatever T.
+int packed_attn_split(int nb, int T, int nh, int nkv) {
+    constexpr long long wanted = 3 * 152 / 2;
+    const int group = nh / nkv;
+    const long long items = ((static_cast<long long>(T) + 127) / 128 + nb / 2) * nkv;  // half a tile each lost to ends
+    for (int s = 1; s < group; ++s)
+        if (group % s == 0 && items * s >= wanted) return s;
+    return group;
+}
 
 int packed_attn_stream_rows(int d) { return d <= 128 ? 128 : 64; }
 
@@ -994,6 +1105,8 @@ cudaError_t launch_packed_backward(const CUtensorMap& q128, const CUtensorMap& d
     a.scale2 = 1.4426950408889634f * p.scale;
     a.lse = p.lse_in;
     a.delta = p.delta;
+    a.split = packed_attn_split(p.nb, p.T, p.nh, p.nkv);
+    a.parts = p.parts;
     a.dQ = p.dQ;
     a.dK = p.dK;
     a.dV = p.dV;

@@ -2299,18 +2299,25 @@ int check_packed(int nb, int T, int nh, int nkv, int d, float scale) {
 
 bool row_stride_ok(long long ld, long long cols, int multiple) { return ld >= cols && ld % multiple == 0; }
 
-// Header words, entries, ranks; behind them the backward pass's delta.
+// Header words, entries, ranks; behind them the backward pass's delta and the sums of
+// parts of a group's heads.
 struct PackedLayout {
-    size_t entries, ranks, delta, total;
+    size_t entries, ranks, delta, parts, total;
 };
 
-PackedLayout packed_layout(int nb, int T, int nh, bool backward) {
+PackedLayout packed_layout(int nb, int T, int nh, int nkv, int d, bool backward) {
     const size_t tiles = static_cast<size_t>(T) / 128;
     PackedLayout L;
     L.entries = 256;
     L.ranks = align256(L.entries + sizeof(int4) * (tiles + nb));
     L.delta = align256(L.ranks + sizeof(int) * (tiles + 2));
-    L.total = backward ? align256(L.delta + sizeof(float) * static_cast<size_t>(T) * nh) : L.delta;
+    if (!backward) {
+        L.total = L.delta;
+        return L;
+    }
+    const size_t split = static_cast<size_t>(packed_attn_split(nb, T, nh, nkv));
+    L.parts = align256(L.delta + sizeof(float) * static_cast<size_t>(T) * nh);
+    L.total = L.parts + (split > 1 ? align256(sizeof(float) * split * T * nkv * 2 * d) : 0);
     return L;
 }
 
@@ -2337,7 +2344,7 @@ int token_map(CUtensorMap* m, const tpmlp_bf16* x, int T, int heads, int d, long
 
 TPMLP_API size_t tp_attn_packed_forward_workspace_bytes(int nb, int T, int nh, int nkv, int d) {
     if (check_packed(nb, T, nh, nkv, d, 1.0f)) return 0;
-    return packed_layout(nb, T, nh, false).total;
+    return packed_layout(nb, T, nh, nkv, d, false).total;
 }
 
 TPMLP_API int tp_attn_packed_forward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16* K, long long ldk,
@@ -2350,7 +2357,7 @@ TPMLP_API int tp_attn_packed_forward(const tpmlp_bf16* Q, long long ldq, const t
         return TPMLP_ERR_SHAPE;
     if (nb == 0 || T == 0) return TPMLP_OK;
     if (any_null(Q, K, V, O, cu_seqlens, lse)) return TPMLP_ERR_NULL;
-    const PackedLayout L = packed_layout(nb, T, nh, false);
+    const PackedLayout L = packed_layout(nb, T, nh, nkv, d, false);
     if (workspace == nullptr || workspace_bytes < L.total) return TPMLP_ERR_WORKSPACE;
     if (!all_aligned(Q, K, V, O, lse, workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
         return TPMLP_ERR_ALIGN;
@@ -2371,7 +2378,7 @@ TPMLP_API int tp_attn_packed_forward(const tpmlp_bf16* Q, long long ldq, const t
 
 TPMLP_API size_t tp_attn_packed_backward_workspace_bytes(int nb, int T, int nh, int nkv, int d) {
     if (check_packed(nb, T, nh, nkv, d, 1.0f)) return 0;
-    return packed_layout(nb, T, nh, true).total;
+    return packed_layout(nb, T, nh, nkv, d, true).total;
 }
 
 TPMLP_API int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16* K, long long ldk,
@@ -2387,7 +2394,7 @@ TPMLP_API int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const 
         return TPMLP_ERR_SHAPE;
     if (nb == 0 || T == 0) return TPMLP_OK;
     if (any_null(Q, K, V, O, dO, dQ, dK, dV, cu_seqlens, lse)) return TPMLP_ERR_NULL;
-    const PackedLayout L = packed_layout(nb, T, nh, true);
+    const PackedLayout L = packed_layout(nb, T, nh, nkv, d, true);
     if (workspace == nullptr || workspace_bytes < L.total) return TPMLP_ERR_WORKSPACE;
     if (!all_aligned(Q, K, V, O, dO, dQ, dK, dV, lse, workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
         return TPMLP_ERR_ALIGN;
@@ -2411,6 +2418,7 @@ TPMLP_API int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const 
     p.lse_in = lse;
     p.dO = cb(dO);
     p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.delta);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.parts);
     p.dQ = reinterpret_cast<__nv_bfloat16*>(dQ);
     p.dK = reinterpret_cast<__nv_bfloat16*>(dK);
     p.dV = reinterpret_cast<__nv_bfloat16*>(dV);

@@ -212,6 +212,7 @@ struct PackedAttn {
     const float* lse_in;
     const __nv_bfloat16* dO;
     float* delta;                // backward: scratch [nh, T]
+    float* parts;                // backward: scratch, packed_attn_split() x [T, nkv, 2, d] if that is > 1
     __nv_bfloat16 *dQ, *dK, *dV; // backward: outputs, rows ldq, ldk, ldv values apart
     long long ldq, ldk, ldv;
     int* status;
@@ -223,6 +224,7 @@ cudaError_t launch_packed_forward(const CUtensorMap& q, const CUtensorMap& k, co
 // Rows of the backward's streamed boxes: K and V in the dQ kernel, Q and dO in
 // the dK/dV kernel (the other operands' boxes have 128).
 int packed_attn_stream_rows(int d);
+int packed_attn_split(int nb, int T, int nh, int nkv);
 cudaError_t launch_packed_backward(const CUtensorMap& q128, const CUtensorMap& do128, const CUtensorMap& k128,
                                    const CUtensorMap& v128, const CUtensorMap& q_stream,
                                    const CUtensorMap& do_stream, const CUtensorMap& k_stream,
