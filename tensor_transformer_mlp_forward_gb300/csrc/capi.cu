@@ -2297,7 +2297,9 @@ int check_packed(int nb, int T, int nh, int nkv, int d, float scale) {
     return TPMLP_OK;
 }
 
-bool row_stride_ok(long long ld, long long cols, int multiple) { return ld >= cols && ld % multiple == 0; }
+bool row_stride_ok(long long ld, long long cols, int multiple) {
+    return ld >= cols && ld < (1LL << 31) && ld % multiple == 0;
+}
 
 // Header words, entries, ranks; behind them the backward pass's delta and the sums of
 // parts of a group's heads.
@@ -2473,7 +2475,7 @@ TPMLP_API int tp_qk_norm_rope_forward(const void* Q, long long ldq, const void* 
 
 TPMLP_API size_t tp_qk_norm_rope_backward_workspace_floats(int T, int nh, int nkv, int d) {
     if (check_qk(T, nh, nkv, d, 0, 1.0, TPMLP_BF16) || T == 0) return 0;
-    return static_cast<size_t>(qk_norm_parts(T, nh + nkv, d)) * 2 * d;
+    return static_cast<size_t>(qk_norm_parts(T, nh, nkv, d)) * d;
 }
 
 TPMLP_API int tp_qk_norm_rope_backward(const void* dQo, long long lddqo, const void* dKo, long long lddko,

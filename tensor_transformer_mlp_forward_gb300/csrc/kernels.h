@@ -241,11 +241,11 @@ struct QkNormRope {
     const int* positions;
     void *out_q, *out_k;  // forward: y; backward: dx
     float* rstd;          // [T, nh + nkv]
-    float* partial;       // backward: qk_norm_parts(T, nh + nkv, d) * 2 d floats
+    float* partial;       // backward: qk_norm_parts(T, nh, nkv, d) * d floats
     long long ldq, ldk, ldyq, ldyk, ldoq, ldok;
 };
-constexpr int kQkMaxParts = 608;  // CTAs of the backward kernel: 4 on each of 152 SMs
-int qk_norm_parts(int T, int heads, int d);
+constexpr int kQkSms = 152;  // what the CTAs are dealt to: the order of sums depends on the sizes alone
+int qk_norm_parts(int T, int nh, int nkv, int d);
 cudaError_t launch_qk_norm_rope_forward(const QkNormRope& p, cudaStream_t st, int* launches);
 cudaError_t launch_qk_norm_rope_backward(const QkNormRope& p, float* dgamma_q, float* dgamma_k, cudaStream_t st,
                                          int* launches);

@@ -17,11 +17,15 @@
 // quarter turn comes off as an integer, and the rest (at most an eighth of a turn)
 // is rounded to fp32 once.
 //
-// A few operations per value: bound by HBM.  A thread holds two pieces of 8 values
-// of a head, the two that the rotation mixes, so the rotation is its own business
-// and the head's sums cross d / 16 lanes.  A CTA takes a run of (token, head) pairs
-// and computes the sines and cosines of its few tokens once, in shared memory, while
-// its loads are on their way; every thread has UNITS heads in flight.
+// A few operations per value: bound by HBM, and not far from the issue rate, so the
+// arithmetic runs on pairs of fp32 values.  A thread holds two pieces of 8 values of a
+// head, the two that the rotation mixes, so the rotation is its own business and the
+// head's sums cross d / 16 lanes.  A CTA takes runs of (token, head) pairs, and computes
+// the sines and cosines of a run's few tokens once, in shared memory, while its values are
+// on their way.  Forward, a CTA takes one run: CTAs that come and go keep more loads in
+// flight than resident ones that fetch a run ahead.  Backward, resident CTAs on queries or
+// on keys carry the sums of one dgamma from run to run, the next run's values on their way
+// while one is computed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -41,17 +45,24 @@ struct QkTurns {
     unsigned long long f[128];  // per pair: turns a position, times 2^64
 };
 
+// Queries or keys.
+struct QkJob {
+    const void *x, *dy;      // [T, heads, d], tokens ldx, lddy values apart
+    void* out;               // y or dx
+    const void* gamma;       // [d]
+    int ldx, lddy, ldo;
+    int heads, first;        // first: the matrix's first column of rstd
+    int step_t, step_h;      // (tokens, heads) from one run of a CTA to its next
+    int group_t, group_h;    // and from one unit of a thread to the next
+};
+
 struct QkArgs {
-    const void *q, *k;       // [T, nh, d], [T, nkv, d], tokens ldq, ldk values apart
-    const void *dy_q, *dy_k;
-    void *out_q, *out_k;     // y or dx
-    const void *gamma_q, *gamma_k;  // [d]
+    QkJob job[2];            // queries, keys
+    int ctas[2];             // CTAs of each
     const int* positions;    // [T]
-    float* rstd;             // [T, nh + nkv]: forward output, backward input
-    float* partial;          // backward: [CTA][2][d] of dgamma_q, dgamma_k
-    long long ldq, ldk, ldyq, ldyk, ldoq, ldok;
-    long long total;         // T (nh + nkv)
-    int T, nh, heads, d, rot;
+    float* rstd;             // [T, all heads]: forward output, backward input
+    float* partial;          // backward: [CTA][d] of dgamma
+    int T, all_heads, d, rot;
     float eps, inv_d;
 };
 
@@ -77,47 +88,79 @@ __device__ __forceinline__ Raw<T> zero8() {
     return r;
 }
 
-__device__ __forceinline__ float2 widen(uint32_t w, __nv_bfloat16) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+// Pairs of fp32 values, one instruction for two.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ float2 widen(uint32_t w, __half) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+__device__ __forceinline__ float2 apart(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
-__device__ __forceinline__ uint32_t narrow(float a, float b, __nv_bfloat16) { return pack_bf16x2(a, b); }
-__device__ __forceinline__ uint32_t narrow(float a, float b, __half) {
-    const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t widen(uint32_t w, __nv_bfloat16) {
+    return two(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint64_t widen(uint32_t w, __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return two(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t narrow(uint64_t v, __nv_bfloat16) {
+    const float2 f = apart(v);
+    return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t narrow(uint64_t v, __half) {
+    const float2 f = apart(v);
+    const __half2 h = __floats2half2_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack8(const Raw<T>& r, float (&v)[8]) {
+__device__ __forceinline__ void unpack8(const Raw<T>& r, uint64_t (&v)[4]) {
     if constexpr (sizeof(T) == 4) {
         const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        for (int i = 0; i < 4; ++i) v[i] = two(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else {
         const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = widen(w[i], T{});
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
+        for (int i = 0; i < 4; ++i) v[i] = widen(w[i], T{});
     }
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* p, const uint64_t (&v)[4]) {
     if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        const float2 a = apart(v[0]), b = apart(v[1]), c = apart(v[2]), d = apart(v[3]);
+        reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+        reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
     } else {
-        *reinterpret_cast<uint4*>(p) = make_uint4(narrow(v[0], v[1], T{}), narrow(v[2], v[3], T{}),
-                                                  narrow(v[4], v[5], T{}), narrow(v[6], v[7], T{}));
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(narrow(v[0], T{}), narrow(v[1], T{}), narrow(v[2], T{}), narrow(v[3], T{}));
     }
 }
 
 // cos and sin of 2 pi (p f / 2^64 mod 1).
+// In the 16-bit types by the fast sine and cosine, whose error on an eighth of a turn
+// (2^-21) is nothing beside the rounding of the result.
+template <bool FAST>
 __device__ __forceinline__ float2 turn(int p, unsigned long long f) {
     const unsigned long long a = static_cast<unsigned long long>(static_cast<long long>(p)) * f;
     const unsigned long long quarter = (a + (1ull << 61)) >> 62;  // nearest quarter turn, modulo 4
@@ -125,7 +168,10 @@ __device__ __forceinline__ float2 turn(int p, unsigned long long f) {
     // in half turns, for cospi and sinpi
     const float x = static_cast<float>(static_cast<int>(rest >> 31)) * 4.656612873077393e-10f * 0.5f;
     float s, c;
-    sincospif(x, &s, &c);
+    if constexpr (FAST)
+        __sincosf(x * 3.14159265358979f, &s, &c);
+    else
+        sincospif(x, &s, &c);
     const bool swap = quarter & 1ull;
     const float cc = swap ? s : c, ss = swap ? c : s;
     const unsigned q = static_cast<unsigned>(quarter) & 3u;
@@ -147,34 +193,44 @@ __device__ __forceinline__ Place place_of(int u, int d, int rot) {
     return p;
 }
 
-// cos and sin of the tokens [t0, t0 + tokens) into shared memory, [token][2][rot / 2].
-__device__ __forceinline__ void fill_turns(float* table, const QkArgs& a, const QkTurns& turns, long long t0,
-                                           int tokens) {
-    const int half = a.rot / 2;
-    for (int i = threadIdx.x; i < tokens * half; i += kQkThreads) {
-        const int t = i / half, j = i - t * half;
-        const float2 cs = turn(__ldg(a.positions + t0 + t), turns.f[j]);
-        table[(2 * t) * half + j] = cs.x;
-        table[(2 * t + 1) * half + j] = cs.y;
+// A thread's share of the sines and cosines: pair j of every per'th token of a run.
+struct TurnsOf {
+    int tok, j, per;
+    unsigned long long f;
+    __device__ __forceinline__ TurnsOf(const QkTurns& turns, int half) {
+        per = half > 0 ? kQkThreads / half : 0;
+        tok = half > 0 ? threadIdx.x / half : 0;
+        j = half > 0 ? threadIdx.x - tok * half : 0;
+        f = half > 0 ? turns.f[j] : 0ull;
+        if (tok >= per) tok = 1 << 30;  // beyond every run
     }
-}
+    // cos and sin of the tokens [t0, t0 + tokens) into shared memory, [token][2][rot / 2]
+    template <bool FAST>
+    __device__ __forceinline__ void fill(float* table, const int* positions, int t0, int tokens, int rot) const {
+        for (int t = tok; t < tokens; t += per) {
+            const float2 cs = turn<FAST>(__ldg(positions + t0 + t), f);
+            table[t * rot + j] = cs.x;
+            table[t * rot + rot / 2 + j] = cs.y;
+        }
+    }
+};
 
-__device__ __forceinline__ void load_f8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-// (a, b) turned by the angle whose cos and sin are given; sign -1 turns back.
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float* table, int half, int u, float sign) {
-    float c[8], s[8];
-    load_f8(table + 8 * u, c);
-    load_f8(table + half + 8 * u, s);
+// (a, b) turned by the angle whose cos and sin are given, or (sign -1) back.
+__device__ __forceinline__ void rotate(uint64_t (&a)[4], uint64_t (&b)[4], const float* table, int half, int u,
+                                       float sign) {
+    const ulonglong2* c = reinterpret_cast<const ulonglong2*>(table + 8 * u);
+    const ulonglong2* s = reinterpret_cast<const ulonglong2*>(table + half + 8 * u);
+    const uint64_t plus = two(sign, sign), minus = two(-sign, -sign);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float si = sign * s[i], x = a[i], y = b[i];
-        a[i] = x * c[i] - y * si;
-        b[i] = y * c[i] + x * si;
+    for (int i = 0; i < 4; i += 2) {
+        const ulonglong2 cc = c[i / 2], ss = s[i / 2];
+        const uint64_t c2[2] = {cc.x, cc.y}, s2[2] = {ss.x, ss.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint64_t x = a[i + k], y = b[i + k];
+            a[i + k] = fma2(y, mul2(s2[k], minus), mul2(x, c2[k]));
+            b[i + k] = fma2(x, mul2(s2[k], plus), mul2(y, c2[k]));
+        }
     }
 }
 
@@ -185,192 +241,245 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// A run of UNITS x kQkThreads / LANES (token, head) pairs.
-template <typename T, int LANES, int UNITS>
-__global__ void __launch_bounds__(kQkThreads)
+__device__ __forceinline__ float sum4(const uint64_t (&v)[2]) {
+    const float2 f = apart(add2(v[0], v[1]));
+    return f.x + f.y;
+}
+
+// A (token, head) pair, moved without a division.
+struct Pair {
+    int t, h;
+    __device__ __forceinline__ void move(int dt, int dh, int heads) {
+        t += dt;
+        h += dh;
+        if (h >= heads) {
+            h -= heads;
+            ++t;
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ const T* row_of(const void* p, int ld, Pair at, int d) {
+    return static_cast<const T*>(p) + (static_cast<long long>(at.t) * ld + at.h * d);
+}
+
+// One run: pairs of a token's queries and keys, queries first.
+template <typename T, int LANES, int UNITS, int PER_SM>
+__global__ void __launch_bounds__(kQkThreads, PER_SM)
     qk_forward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkTurns turns) {
     pdl_launch_dependents();
     pdl_wait();
-    extern __shared__ float table[];
-    constexpr int GROUPS = kQkThreads / LANES;
-    const long long first = static_cast<long long>(blockIdx.x) * (GROUPS * UNITS);
-    const int count = static_cast<int>(a.total - first < GROUPS * UNITS ? a.total - first : GROUPS * UNITS);
-    const long long t0 = first / a.heads;
-    const int h0 = static_cast<int>(first - t0 * a.heads);
+    extern __shared__ __align__(16) float table[];
+    constexpr int GROUPS = kQkThreads / LANES, RUN = GROUPS * UNITS;
+    constexpr bool FAST = sizeof(T) == 2;
+    const int heads = a.all_heads, nh = a.job[0].heads, d = a.d;
     const int u = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-    const Place pl = place_of(u, a.d, a.rot);
+    const Place pl = place_of(u, d, a.rot);
+    const TurnsOf mine(turns, a.rot / 2);
+    const long long first = static_cast<long long>(blockIdx.x) * RUN, whole = first / heads;
+    const int t0 = static_cast<int>(whole), h0 = static_cast<int>(first - whole * heads);
+    Pair at;
+    at.t = t0 + (h0 + grp) / heads;
+    at.h = (h0 + grp) % heads;
+    const int group_t = GROUPS / heads, group_h = GROUPS % heads;
     Raw<T> xa[UNITS], xb[UNITS];
-    int tok[UNITS], head[UNITS];
+    Pair from = at;
 #pragma unroll
     for (int n = 0; n < UNITS; ++n) {
-        const int i = n * GROUPS + grp;
-        tok[n] = (h0 + i) / a.heads;
-        head[n] = h0 + i - tok[n] * a.heads;
-        xa[n] = zero8<T>();
-        xb[n] = zero8<T>();
-        if (i < count && pl.on) {
-            const long long t = t0 + tok[n];
-            const T* x = head[n] < a.nh ? static_cast<const T*>(a.q) + t * a.ldq + head[n] * a.d
-                                        : static_cast<const T*>(a.k) + t * a.ldk + (head[n] - a.nh) * a.d;
+        xa[n] = xb[n] = zero8<T>();
+        if (from.t < a.T && pl.on) {
+            const T* x = from.h < nh ? row_of<T>(a.job[0].x, a.job[0].ldx, from, d)
+                                     : row_of<T>(a.job[1].x, a.job[1].ldx, Pair{from.t, from.h - nh}, d);
             xa[n] = load8(x + pl.a);
             xb[n] = load8(x + pl.b);
         }
+        from.move(group_t, group_h, heads);
     }
-    fill_turns(table, a, turns, t0, (h0 + count - 1) / a.heads + 1);
+    mine.fill<FAST>(table, a.positions, t0, min(t0 + (h0 + RUN - 1) / heads, a.T - 1) - t0 + 1, a.rot);
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < UNITS; ++n) {
-        const int i = n * GROUPS + grp;
-        float va[8], vb[8];
+        const bool on = at.t < a.T && pl.on, isq = at.h < nh;
+        uint64_t va[4], vb[4], sum[2] = {0ull, 0ull};
         unpack8(xa[n], va);
         unpack8(xb[n], vb);
-        float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(va[e], va[e], fmaf(vb[e], vb[e], sum));
-        const float r = __frsqrt_rn(group_sum<LANES>(sum) * a.inv_d + a.eps);
-        if (i >= count || !pl.on) continue;
-        const bool isq = head[n] < a.nh;
-        const T* gamma = static_cast<const T*>(isq ? a.gamma_q : a.gamma_k);
-        float ga[8], gb[8];
-        unpack8(load8(gamma + pl.a), ga);
-        unpack8(load8(gamma + pl.b), gb);
+        for (int e = 0; e < 4; ++e) sum[e & 1] = fma2(va[e], va[e], fma2(vb[e], vb[e], sum[e & 1]));
+        const float r = rsqrtf(group_sum<LANES>(sum4(sum)) * a.inv_d + a.eps);
+        if (on) {
+            const T* gamma = static_cast<const T*>(isq ? a.job[0].gamma : a.job[1].gamma);
+            const uint64_t rr = two(r, r);
+            uint64_t wa[4], wb[4];
+            unpack8(load8(gamma + pl.a), wa);
+            unpack8(load8(gamma + pl.b), wb);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            va[e] = va[e] * r * ga[e];
-            vb[e] = vb[e] * r * gb[e];
+            for (int e = 0; e < 4; ++e) {
+                va[e] = mul2(mul2(va[e], rr), wa[e]);
+                vb[e] = mul2(mul2(vb[e], rr), wb[e]);
+            }
+            if (pl.turns) rotate(va, vb, table + (at.t - t0) * a.rot, a.rot / 2, u, 1.0f);
+            T* out = const_cast<T*>(isq ? row_of<T>(a.job[0].out, a.job[0].ldo, at, d)
+                                        : row_of<T>(a.job[1].out, a.job[1].ldo, Pair{at.t, at.h - nh}, d));
+            store8(out + pl.a, va);
+            store8(out + pl.b, vb);
+            if (u == 0) a.rstd[static_cast<long long>(at.t) * heads + at.h] = r;
         }
-        if (pl.turns) rotate(va, vb, table + tok[n] * a.rot, a.rot / 2, u, 1.0f);
-        const long long t = t0 + tok[n];
-        T* y = isq ? static_cast<T*>(a.out_q) + t * a.ldoq + head[n] * a.d
-                   : static_cast<T*>(a.out_k) + t * a.ldok + (head[n] - a.nh) * a.d;
-        store8(y + pl.a, va);
-        store8(y + pl.b, vb);
-        if (u == 0) a.rstd[t * a.heads + head[n]] = r;
+        at.move(group_t, group_h, heads);
     }
 }
 
-// Runs of pairs, CTA by CTA in a fixed order: each thread keeps its 16 columns' sums
-// of dgamma_q and dgamma_k, which the CTA adds up at the end.
-template <typename T, int LANES, int UNITS>
-__global__ void __launch_bounds__(kQkThreads)
-    qk_backward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkTurns turns) {
+// CTAs [0, ctas[0]) take the queries' runs in turn, the others the keys'.
+template <typename T, int LANES, int UNITS, int PER_SM>
+__global__ void __launch_bounds__(kQkThreads, PER_SM)
+    qk_backward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkTurns turns, int table_floats) {
     pdl_launch_dependents();
     pdl_wait();
-    extern __shared__ float table[];
-    constexpr int GROUPS = kQkThreads / LANES, RUN = GROUPS * UNITS, WARPS = kQkThreads / 32;
+    extern __shared__ __align__(16) float tables[];
+    constexpr int GROUPS = kQkThreads / LANES, RUN = GROUPS * UNITS;
+    constexpr bool FAST = sizeof(T) == 2;
+    const bool keys = static_cast<int>(blockIdx.x) >= a.ctas[0];
+    const QkJob& j = a.job[keys];
+    const int heads = j.heads, d = a.d;
     const int u = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-    const Place pl = place_of(u, a.d, a.rot);
-    float acc[2][16];
+    const Place pl = place_of(u, d, a.rot);
+    const TurnsOf mine(turns, a.rot / 2);
+    // gamma's two pieces, for every run
+    uint64_t wa[4], wb[4];
+    {
+        const T* gamma = static_cast<const T*>(j.gamma);
+        unpack8(pl.on ? load8(gamma + pl.a) : zero8<T>(), wa);
+        unpack8(pl.on ? load8(gamma + pl.b) : zero8<T>(), wb);
+    }
+    uint64_t acc[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = 0.0f;
-    for (long long first = static_cast<long long>(blockIdx.x) * RUN; first < a.total;
-         first += static_cast<long long>(gridDim.x) * RUN) {
-        const int count = static_cast<int>(a.total - first < RUN ? a.total - first : RUN);
-        const long long t0 = first / a.heads;
-        const int h0 = static_cast<int>(first - t0 * a.heads);
-        Raw<T> xa[UNITS], xb[UNITS], ya[UNITS], yb[UNITS];
-        int tok[UNITS], head[UNITS];
-        float rstd[UNITS];
+    for (int e = 0; e < 8; ++e) acc[e] = 0ull;
+    // the run's first pair, its last one's token, and this thread's first pair
+    Pair at0, last, at;
+    {
+        const long long first = static_cast<long long>(blockIdx.x - (keys ? a.ctas[0] : 0)) * RUN;
+        const long long t0 = first / heads;
+        at0.t = static_cast<int>(t0);
+        at0.h = static_cast<int>(first - t0 * heads);
+        last.t = at0.t + (at0.h + RUN - 1) / heads;
+        last.h = (at0.h + RUN - 1) % heads;
+        at.t = at0.t + (at0.h + grp) / heads;
+        at.h = (at0.h + grp) % heads;
+    }
+    Raw<T> xa[UNITS], xb[UNITS], ya[UNITS], yb[UNITS];
+    float rstd[UNITS];
+    auto load = [&](Pair from) {
 #pragma unroll
         for (int n = 0; n < UNITS; ++n) {
-            const int i = n * GROUPS + grp;
-            tok[n] = (h0 + i) / a.heads;
-            head[n] = h0 + i - tok[n] * a.heads;
             xa[n] = xb[n] = ya[n] = yb[n] = zero8<T>();
             rstd[n] = 0.0f;
-            if (i < count && pl.on) {
-                const long long t = t0 + tok[n];
-                const bool isq = head[n] < a.nh;
-                const int col = (isq ? head[n] : head[n] - a.nh) * a.d;
-                const T* x = (isq ? static_cast<const T*>(a.q) + t * a.ldq : static_cast<const T*>(a.k) + t * a.ldk) + col;
-                const T* y =
-                    (isq ? static_cast<const T*>(a.dy_q) + t * a.ldyq : static_cast<const T*>(a.dy_k) + t * a.ldyk) + col;
+            if (from.t < a.T && pl.on) {
+                const T* x = row_of<T>(j.x, j.ldx, from, d);
                 xa[n] = load8(x + pl.a);
                 xb[n] = load8(x + pl.b);
+                const T* y = row_of<T>(j.dy, j.lddy, from, d);
                 ya[n] = load8(y + pl.a);
                 yb[n] = load8(y + pl.b);
-                rstd[n] = __ldg(a.rstd + t * a.heads + head[n]);
+                rstd[n] = __ldg(a.rstd + static_cast<long long>(from.t) * a.all_heads + j.first + from.h);
             }
+            from.move(j.group_t, j.group_h, heads);
         }
-        __syncthreads();  // the last run's sines have been read
-        fill_turns(table, a, turns, t0, (h0 + count - 1) / a.heads + 1);
-        __syncthreads();
+    };
+    auto fill = [&](int k) {
+        mine.fill<FAST>(tables + (k & 1) * table_floats, a.positions, at0.t, min(last.t, a.T - 1) - at0.t + 1, a.rot);
+    };
+    load(at);
+    fill(0);
+    __syncthreads();
+    for (int k = 0; at0.t < a.T; ++k) {
+        const float* table = tables + (k & 1) * table_floats;
+        const int t0 = at0.t;
+        uint64_t va[UNITS][4], vb[UNITS][4], ga[UNITS][4], gb[UNITS][4];
+        float r[UNITS];
 #pragma unroll
         for (int n = 0; n < UNITS; ++n) {
-            const int i = n * GROUPS + grp;
-            const bool on = i < count && pl.on, isq = head[n] < a.nh;
-            float va[8], vb[8], ga[8], gb[8];
-            unpack8(xa[n], va);
-            unpack8(xb[n], vb);
-            unpack8(ya[n], ga);
-            unpack8(yb[n], gb);
-            if (on && pl.turns) rotate(ga, gb, table + tok[n] * a.rot, a.rot / 2, u, -1.0f);
-            float wa[8], wb[8];
-            float sum = 0.0f;
+            unpack8(xa[n], va[n]);
+            unpack8(xb[n], vb[n]);
+            unpack8(ya[n], ga[n]);
+            unpack8(yb[n], gb[n]);
+            r[n] = rstd[n];
+        }
+        // the next run's values, and its tokens' turns, while this one is computed
+        Pair here = at;
+        at0.move(j.step_t, j.step_h, heads);
+        last.move(j.step_t, j.step_h, heads);
+        at.move(j.step_t, j.step_h, heads);
+        load(at);
+        fill(k + 1);
+#pragma unroll
+        for (int n = 0; n < UNITS; ++n) {
+            const bool on = here.t < a.T && pl.on;
+            const float* turned = table + (here.t - t0) * a.rot;
+            uint64_t sum[2] = {0ull, 0ull};
+            if (on && pl.turns) rotate(ga[n], gb[n], turned, a.rot / 2, u, -1.0f);
+            const uint64_t rr = two(r[n], r[n]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // (a pair beyond the end is all zeros)
+                va[n][e] = mul2(va[n][e], rr);
+                vb[n][e] = mul2(vb[n][e], rr);
+                const uint64_t pa = mul2(ga[n][e], va[n][e]), pb = mul2(gb[n][e], vb[n][e]);
+                acc[e] = add2(acc[e], pa);
+                acc[4 + e] = add2(acc[4 + e], pb);
+                sum[e & 1] = fma2(pa, wa[e], fma2(pb, wb[e], sum[e & 1]));
+            }
+            const float m = -group_sum<LANES>(sum4(sum)) * a.inv_d;
+            const uint64_t mm = two(m, m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                va[n][e] = mul2(rr, fma2(va[n][e], mm, mul2(ga[n][e], wa[e])));
+                vb[n][e] = mul2(rr, fma2(vb[n][e], mm, mul2(gb[n][e], wb[e])));
+            }
             if (on) {
-                const T* gamma = static_cast<const T*>(isq ? a.gamma_q : a.gamma_k);
-                unpack8(load8(gamma + pl.a), wa);
-                unpack8(load8(gamma + pl.b), wb);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    va[e] *= rstd[n];
-                    vb[e] *= rstd[n];
-                    const float pa = ga[e] * va[e], pb = gb[e] * vb[e];
-                    if (isq) {
-                        acc[0][e] += pa;
-                        acc[0][8 + e] += pb;
-                    } else {
-                        acc[1][e] += pa;
-                        acc[1][8 + e] += pb;
-                    }
-                    sum = fmaf(pa, wa[e], fmaf(pb, wb[e], sum));
-                }
+                T* out = const_cast<T*>(row_of<T>(j.out, j.ldo, here, d));
+                store8(out + pl.a, va[n]);
+                store8(out + pl.b, vb[n]);
             }
-            const float m = group_sum<LANES>(sum) * a.inv_d;
-            if (!on) continue;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                va[e] = rstd[n] * (ga[e] * wa[e] - va[e] * m);
-                vb[e] = rstd[n] * (gb[e] * wb[e] - vb[e] * m);
-            }
-            const long long t = t0 + tok[n];
-            T* dx = isq ? static_cast<T*>(a.out_q) + t * a.ldoq + head[n] * a.d
-                        : static_cast<T*>(a.out_k) + t * a.ldok + (head[n] - a.nh) * a.d;
-            store8(dx + pl.a, va);
-            store8(dx + pl.b, vb);
+            here.move(j.group_t, j.group_h, heads);
         }
+        __syncthreads();  // this run's sines have been read, the next one's are there
     }
-    // lanes of the same columns, then the warps, in a fixed order
-    __syncthreads();
-    float* rows = table;  // [warp][2][d]
+    {
+        // lanes of the same columns, then the warps, in a fixed order
+        float* rows = tables;  // [warp][d]
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+        for (int e = 0; e < 8; ++e) {
+            const float2 f = apart(acc[e]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            float v = acc[s][e];
+            for (int h = 0; h < 2; ++h) {
+                float v = h ? f.y : f.x;
 #pragma unroll
-            for (int o = 16; o >= LANES; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (threadIdx.x % 32 < LANES && pl.on)
-                rows[((threadIdx.x / 32) * 2 + s) * a.d + (e < 8 ? pl.a + e : pl.b + e - 8)] = v;
+                for (int o = 16; o >= LANES; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+                if (threadIdx.x % 32 < LANES && pl.on)
+                    rows[threadIdx.x / 32 * d + (e < 4 ? pl.a + 2 * e : pl.b + 2 * e - 8) + h] = v;
+            }
         }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.d; c += kQkThreads) {
-        float v = 0.0f;
-        for (int w = 0; w < WARPS; ++w) v += rows[w * 2 * a.d + c];
-        a.partial[static_cast<long long>(blockIdx.x) * 2 * a.d + c] = v;
+        __syncthreads();
+        for (int c = threadIdx.x; c < d; c += kQkThreads) {
+            float v = 0.0f;
+            for (int w = 0; w < kQkThreads / 32; ++w) v += rows[w * d + c];
+            a.partial[static_cast<long long>(blockIdx.x) * d + c] = v;
+        }
     }
 }
 
-// dgamma = the CTAs' parts added up: 32 columns a CTA, 32 threads a column.
-__global__ void __launch_bounds__(1024) qk_dgamma_kernel(const float* partial, int parts, int d, float* dgamma_q,
-                                                         float* dgamma_k) {
+// dgamma = the CTAs' parts added up: 32 columns a CTA, 32 threads a column.  Columns
+// [0, d) are the queries', whose parts come first, [d, 2 d) the keys'.
+__global__ void __launch_bounds__(1024)
+    qk_dgamma_kernel(const float* partial, int parts_q, int parts, int d, float* dgamma_q, float* dgamma_k) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float s[32][33];
     const int x = threadIdx.x % 32, y = threadIdx.x / 32, c = blockIdx.x * 32 + x;
     float v = 0.0f;
     if (c < 2 * d)
-        for (int i = y; i < parts; i += 32) v += partial[static_cast<long long>(i) * 2 * d + c];
+        for (int i = y + (c < d ? 0 : parts_q); i < (c < d ? parts_q : parts); i += 32)
+            v += partial[static_cast<long long>(i) * d + (c < d ? c : c - d)];
     s[y][x] = v;
     __syncthreads();
     v = s[x][y];
@@ -380,29 +489,25 @@ __global__ void __launch_bounds__(1024) qk_dgamma_kernel(const float* partial, i
     if (x == 0 && col < 2 * d) (col < d ? dgamma_q[col] : dgamma_k[col - d]) = v;
 }
 
-constexpr int kUnitsForward = 4, kUnitsBackward = 2;
+// Pairs a thread holds, and CTAs an SM: what the registers allow with enough loads in
+// flight (backward, 8192 tokens of 40 heads of 128: 61 us; two pairs 65, three CTAs, which
+// spill, 79).
+constexpr int kUnitsForward = 4, kUnitsBackward = 1, kPerSmForward = 4, kPerSmBackward = 2;
 
 int lanes_of(int d) { return d <= 32 ? 2 : d <= 64 ? 4 : d <= 128 ? 8 : 16; }
 
-// Tokens that a run of pairs can touch.
-int most_tokens(int run, int heads) { return (run + heads - 2) / heads + 1; }
-
-QkArgs make_args(const QkNormRope& p) {
-    QkArgs a{};
-    a.q = p.q; a.k = p.k;
-    a.dy_q = p.dy_q; a.dy_k = p.dy_k;
-    a.out_q = p.out_q; a.out_k = p.out_k;
-    a.gamma_q = p.gamma_q; a.gamma_k = p.gamma_k;
-    a.positions = p.positions;
-    a.rstd = p.rstd;
-    a.partial = p.partial;
-    a.ldq = p.ldq; a.ldk = p.ldk; a.ldyq = p.ldyq; a.ldyk = p.ldyk; a.ldoq = p.ldoq; a.ldok = p.ldok;
-    a.heads = p.nh + p.nkv;
-    a.total = static_cast<long long>(p.T) * a.heads;
-    a.T = p.T; a.nh = p.nh; a.d = p.d; a.rot = p.rot;
-    a.eps = p.eps;
-    a.inv_d = 1.0f / static_cast<float>(p.d);
-    return a;
+// CTAs for the queries and the keys: in proportion to their runs, one run each at least.
+void deal_ctas(int T, int nh, int nkv, long long run, int most, int (&ctas)[2]) {
+    const long long q = (1LL * T * nh + run - 1) / run, k = (1LL * T * nkv + run - 1) / run;
+    if (q + k <= most) {
+        ctas[0] = static_cast<int>(q);
+        ctas[1] = static_cast<int>(k);
+        return;
+    }
+    long long c = (q * most + (q + k) / 2) / (q + k);
+    c = c < 1 ? 1 : c > most - 1 ? most - 1 : c;
+    ctas[0] = static_cast<int>(c < q ? c : q);
+    ctas[1] = static_cast<int>(most - c < k ? most - c : k);
 }
 
 QkTurns make_turns(double theta, int rot) {
@@ -415,63 +520,102 @@ QkTurns make_turns(double theta, int rot) {
     return t;
 }
 
-template <typename T, int LANES>
-cudaError_t forward(const QkArgs& a, const QkTurns& turns, cudaStream_t st) {
-    constexpr int run = kUnitsForward * kQkThreads / LANES;
-    const size_t smem = sizeof(float) * static_cast<size_t>(most_tokens(run, a.heads)) * a.rot;
-    return launch_dependent(qk_forward_kernel<T, LANES, kUnitsForward>,
-                            dim3(static_cast<unsigned>((a.total + run - 1) / run)), dim3(kQkThreads), smem, st, a, turns);
+QkJob make_job(const void* x, const void* dy, void* out, const void* gamma, long long ldx, long long lddy, long long ldo,
+               int heads, int first, int ctas, int run, int groups) {
+    QkJob j{x, dy, out, gamma, static_cast<int>(ldx), static_cast<int>(lddy), static_cast<int>(ldo), heads, first};
+    const long long step = 1LL * ctas * run;
+    j.step_t = static_cast<int>(step / heads);
+    j.step_h = static_cast<int>(step % heads);
+    j.group_t = groups / heads;
+    j.group_h = groups % heads;
+    return j;
+}
+
+QkArgs make_args(const QkNormRope& p) {
+    QkArgs a{};
+    const int groups = kQkThreads / lanes_of(p.d), run = kUnitsBackward * groups;
+    deal_ctas(p.T, p.nh, p.nkv, run, kQkSms * kPerSmBackward, a.ctas);
+    a.job[0] = make_job(p.q, p.dy_q, p.out_q, p.gamma_q, p.ldq, p.ldyq, p.ldoq, p.nh, 0, a.ctas[0], run, groups);
+    a.job[1] = make_job(p.k, p.dy_k, p.out_k, p.gamma_k, p.ldk, p.ldyk, p.ldok, p.nkv, p.nh, a.ctas[1], run, groups);
+    a.positions = p.positions;
+    a.rstd = p.rstd;
+    a.partial = p.partial;
+    a.T = p.T;
+    a.all_heads = p.nh + p.nkv;
+    a.d = p.d;
+    a.rot = p.rot;
+    a.eps = p.eps;
+    a.inv_d = 1.0f / static_cast<float>(p.d);
+    return a;
+}
+
+// Shared memory of `tables` tables of sines and cosines: as many tokens as a run can touch.
+size_t table_bytes(int run, int heads, int rot, int tables) {
+    return sizeof(float) * static_cast<size_t>((run + heads - 2) / heads + 1) * rot * tables;
 }
 
 template <typename T, int LANES>
-cudaError_t backward(const QkArgs& a, const QkTurns& turns, int parts, cudaStream_t st) {
+cudaError_t forward_as(const QkArgs& a, const QkTurns& turns, cudaStream_t st) {
+    constexpr int run = kUnitsForward * kQkThreads / LANES;
+    const long long pairs = 1LL * a.T * a.all_heads;
+    return launch_dependent(qk_forward_kernel<T, LANES, kUnitsForward, kPerSmForward>,
+                            dim3(static_cast<unsigned>((pairs + run - 1) / run)), dim3(kQkThreads),
+                            table_bytes(run, a.all_heads, a.rot, 1), st, a, turns);
+}
+
+template <typename T, int LANES>
+cudaError_t backward_as(const QkArgs& a, const QkTurns& turns, cudaStream_t st) {
     constexpr int run = kUnitsBackward * kQkThreads / LANES;
-    const size_t table = static_cast<size_t>(most_tokens(run, a.heads)) * a.rot;
-    const size_t rows = static_cast<size_t>(kQkThreads / 32) * 2 * a.d;
-    return launch_dependent(qk_backward_kernel<T, LANES, kUnitsBackward>, dim3(static_cast<unsigned>(parts)),
-                            dim3(kQkThreads), sizeof(float) * (table > rows ? table : rows), st, a, turns);
+    const int heads = a.job[0].heads < a.job[1].heads ? a.job[0].heads : a.job[1].heads;
+    const size_t tables = table_bytes(run, heads, a.rot, 2), rows = sizeof(float) * (kQkThreads / 32) * a.d;
+    const size_t smem = tables > rows ? tables : rows;
+    auto kern = qk_backward_kernel<T, LANES, kUnitsBackward, kPerSmBackward>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(static_cast<unsigned>(a.ctas[0] + a.ctas[1])), dim3(kQkThreads), smem, st, a,
+                            turns, static_cast<int>(tables / (2 * sizeof(float))));
 }
 
 template <typename T>
-cudaError_t by_lanes(const QkArgs& a, const QkTurns& t, int parts, cudaStream_t st) {
+cudaError_t by_lanes(const QkArgs& a, const QkTurns& t, bool back, cudaStream_t st) {
     switch (lanes_of(a.d)) {
-        case 2: return parts ? backward<T, 2>(a, t, parts, st) : forward<T, 2>(a, t, st);
-        case 4: return parts ? backward<T, 4>(a, t, parts, st) : forward<T, 4>(a, t, st);
-        case 8: return parts ? backward<T, 8>(a, t, parts, st) : forward<T, 8>(a, t, st);
-        default: return parts ? backward<T, 16>(a, t, parts, st) : forward<T, 16>(a, t, st);
+        case 2: return back ? backward_as<T, 2>(a, t, st) : forward_as<T, 2>(a, t, st);
+        case 4: return back ? backward_as<T, 4>(a, t, st) : forward_as<T, 4>(a, t, st);
+        case 8: return back ? backward_as<T, 8>(a, t, st) : forward_as<T, 8>(a, t, st);
+        default: return back ? backward_as<T, 16>(a, t, st) : forward_as<T, 16>(a, t, st);
     }
 }
 
-cudaError_t launch(const QkNormRope& p, int parts, cudaStream_t st) {
-    const QkArgs a = make_args(p);
+cudaError_t launch(const QkNormRope& p, const QkArgs& a, bool back, cudaStream_t st) {
     const QkTurns t = make_turns(p.theta, p.rot);
-    if (p.dtype == TPMLP_BF16) return by_lanes<__nv_bfloat16>(a, t, parts, st);
-    if (p.dtype == TPMLP_FP16) return by_lanes<__half>(a, t, parts, st);
-    return by_lanes<float>(a, t, parts, st);
+    if (p.dtype == TPMLP_BF16) return by_lanes<__nv_bfloat16>(a, t, back, st);
+    if (p.dtype == TPMLP_FP16) return by_lanes<__half>(a, t, back, st);
+    return by_lanes<float>(a, t, back, st);
 }
 
 }  // namespace
 
-int qk_norm_parts(int T, int heads, int d) {
-    const long long run = kUnitsBackward * kQkThreads / lanes_of(d);
-    const long long runs = (static_cast<long long>(T) * heads + run - 1) / run;
-    return static_cast<int>(runs < kQkMaxParts ? runs : kQkMaxParts);
+int qk_norm_parts(int T, int nh, int nkv, int d) {
+    int ctas[2];
+    deal_ctas(T, nh, nkv, kUnitsBackward * kQkThreads / lanes_of(d), kQkSms * kPerSmBackward, ctas);
+    return ctas[0] + ctas[1];
 }
 
 cudaError_t launch_qk_norm_rope_forward(const QkNormRope& p, cudaStream_t st, int* launches) {
-    const cudaError_t e = launch(p, 0, st);
+    const cudaError_t e = launch(p, make_args(p), false, st);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
 
 cudaError_t launch_qk_norm_rope_backward(const QkNormRope& p, float* dgamma_q, float* dgamma_k, cudaStream_t st,
                                          int* launches) {
-    const int parts = qk_norm_parts(p.T, p.nh + p.nkv, p.d);
-    cudaError_t e = launch(p, parts, st);
+    const QkArgs a = make_args(p);
+    cudaError_t e = launch(p, a, true, st);
     if (e != cudaSuccess) return e;
     ++*launches;
-    e = launch_dependent(qk_dgamma_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st, p.partial, parts, p.d, dgamma_q,
-                         dgamma_k);
+    e = launch_dependent(qk_dgamma_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st,
+                         static_cast<const float*>(p.partial), a.ctas[0], a.ctas[0] + a.ctas[1], p.d, dgamma_q, dgamma_k);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
