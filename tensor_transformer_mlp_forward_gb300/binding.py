@@ -9,6 +9,7 @@ library's kernels; there is no other code path.  A missing library raises.
 
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -1121,18 +1122,30 @@ def tp_qk_norm_rope_backward(dQo, dKo, Q, K, gamma_q, gamma_k, positions, rstd, 
 
 # ------------------------------- global gradient norm and clipping
 
-def _tensors(xs, name: str, device: int):
-    """Addresses, sizes and type codes of a list of dense tensors."""
+def _addresses(xs, name: str, device: int):
+    """Addresses of a list of dense tensors on this device, as an array."""
     for i, x in enumerate(xs):
-        if x.get_device() != device or device < 0:
-            raise ValueError(f"{name}[{i}] is on {x.device}, but the current device is cuda:{device}")
-        if x.dtype not in _DTYPES:
-            _dtype_of(x, f"{name}[{i}]")
-        if not x.is_contiguous():
+        if x.get_device() != device or not x.is_contiguous() or device < 0:
+            if x.get_device() != device or device < 0:
+                raise ValueError(f"{name}[{i}] is on {x.device}, but the current device is cuda:{device}")
             raise ValueError(f"{name}[{i}] must be contiguous")
-    n = len(xs)
-    return ((_P * n)(*[x.data_ptr() for x in xs]), (_L * n)(*[x.numel() for x in xs]),
-            (_I * n)(*[_DTYPES[x.dtype] for x in xs]))
+    return array.array("Q", [x.data_ptr() for x in xs])
+
+
+def _tensors(xs, name: str, device: int):
+    """Addresses, sizes and type codes of a list of dense tensors, as arrays."""
+    at = _addresses(xs, name, device)
+    try:
+        codes = array.array("i", [_DTYPES[x.dtype] for x in xs])
+    except KeyError:
+        for i, x in enumerate(xs):
+            _dtype_of(x, f"{name}[{i}]")
+        raise
+    return at, array.array("q", [x.numel() for x in xs]), codes
+
+
+def _at(a) -> int:
+    return a.buffer_info()[0]
 
 
 def _norm_scratch(n: int, norm, workspace, device: int, stream):
@@ -1159,7 +1172,7 @@ def tp_grad_norm(grads, norm=None, workspace=None, stream=None):
     dev = _list_device(grads)
     gp, sizes, types = _tensors(grads, "grads", dev)
     norm, workspace, np_, wp = _norm_scratch(len(grads), norm, workspace, dev, stream)
-    status = lib().tp_grad_norm(gp, sizes, types, len(grads), np_, wp, workspace.numel(), _stream_of(stream, dev))
+    status = lib().tp_grad_norm(_at(gp), _at(sizes), _at(types), len(grads), np_, wp, workspace.numel(), _stream_of(stream, dev))
     if status:
         _check("tp_grad_norm", status)
     return norm
@@ -1175,11 +1188,11 @@ def tp_grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None, st
     gp, sizes, types = _tensors(grads, "grads", dev)
     op = gp
     if out is not grads:
-        if [(x.dtype, x.shape) for x in out] != [(x.dtype, x.shape) for x in grads]:
+        if len(out) != len(grads) or any(x.dtype is not y.dtype or x.shape != y.shape for x, y in zip(out, grads)):
             raise ValueError("out must have the types and shapes of grads")
-        op, _, _ = _tensors(out, "out", dev)
+        op = _addresses(out, "out", dev)
     norm, workspace, np_, wp = _norm_scratch(len(grads), norm, workspace, dev, stream)
-    status = lib().tp_grad_clip(gp, op, sizes, types, len(grads), max_norm, np_, wp, workspace.numel(),
+    status = lib().tp_grad_clip(_at(gp), _at(op), _at(sizes), _at(types), len(grads), max_norm, np_, wp, workspace.numel(),
                                 _stream_of(stream, dev))
     if status:
         _check("tp_grad_clip", status)

@@ -11,8 +11,9 @@
 // device, and a captured call holds its own table.
 //
 // A square of a value above 2^63 overflows fp32 although the norm need not; a second
-// sum, of the values times 2^-64, takes over when the first is not finite.  The
-// partial sums are added in 64 bits.
+// sum, of the values times 2^-64, takes over when the first is not finite.  (A batch of
+// values whose squares stay finite gives the second sum its own sum times 2^-128, so only
+// a batch that overflows is gone through twice.)  The partial sums are added in 64 bits.
 //
 // The clipping pass walks the pieces backwards: the norm's pass has left the last
 // ones in L2.
@@ -33,7 +34,8 @@ constexpr int kClipThreads = 256;
 constexpr int kPieceBytes = 32768;  // eight 16-byte words a thread
 constexpr int kWords = kPieceBytes / 16 / kClipThreads;
 constexpr float kDown = 5.421010862427522e-20f;  // 2^-64
-constexpr double kUpSquared = 3.402823669209385e38;  // 2^128
+constexpr float kDownSquared = 2.938735877055719e-39f;  // 2^-128
+constexpr double kUpSquared = 3.402823669209385e38;     // 2^128
 
 template <int MOST>
 struct Table {
@@ -72,24 +74,70 @@ __device__ __forceinline__ float2 word_pair(uint32_t w, __half) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+__device__ __forceinline__ uint64_t pair_of_word(uint32_t w, __nv_bfloat16) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(w << 16), "r"(w & 0xFFFF0000u));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of_word(uint32_t w, __half) {
+    const float2 f = word_pair(w, __half{});
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(f.x), "f"(f.y));
+    return r;
+}
+
 struct Sums {
-    float plain[4], down[4];
-    __device__ void add(float x, int chain) {
-        plain[chain] = fmaf(x, x, plain[chain]);
-        const float y = x * kDown;
-        down[chain] = fmaf(y, y, down[chain]);
+    float plain, down;
+    // a batch's sum of squares, or, where that is not finite, `again`(2^-64)'s
+    template <typename F>
+    __device__ __forceinline__ void add(float batch, F&& again) {
+        plain += batch;
+        down += batch < INFINITY ? batch * kDownSquared : again();
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void add_word(Sums& s, uint32_t w, int chain) {
-    if constexpr (sizeof(T) == 4) {
-        s.add(__uint_as_float(w), chain);
-    } else {
-        const float2 f = word_pair(w, T{});
-        s.add(f.x, chain);
-        s.add(f.y, (chain + 1) & 3);
+// The sum of the squares of a 16-byte word's values (times 2^-64 where DOWN) in pairs.
+template <typename T, bool DOWN>
+__device__ __forceinline__ void add_squares(uint64_t (&acc)[2], const uint4& w) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint64_t down;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(down) : "f"(kDown));
+#pragma unroll
+    for (int i = 0; i < (sizeof(T) == 4 ? 2 : 4); ++i) {
+        uint64_t x;
+        if constexpr (sizeof(T) == 4)
+            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
+        else
+            x = pair_of_word(v[i], T{});
+        if (DOWN) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(down));
+        asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(acc[i & 1]) : "l"(x));
     }
+}
+
+__device__ __forceinline__ float sum_of(const uint64_t (&acc)[2]) {
+    float a, b, c, d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(acc[0]));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(c), "=f"(d) : "l"(acc[1]));
+    return (a + b) + (c + d);
+}
+
+template <typename T, bool DOWN>
+__device__ __forceinline__ float squares_of(const uint4 (&w)[kWords]) {
+    uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) add_squares<T, DOWN>(acc, w[i]);
+    return sum_of(acc);
+}
+
+template <bool DOWN>
+__device__ __forceinline__ float squares_of(const float (&v)[8]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float x = DOWN ? v[k] * kDown : v[k];
+        sum = fmaf(x, x, sum);
+    }
+    return sum;
 }
 
 template <typename T>
@@ -98,30 +146,28 @@ __device__ __forceinline__ void sum_piece(Sums& s, const T* p, long long n) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     const int here = static_cast<int>(n < PER ? n : PER);
     if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        const uint4* q = reinterpret_cast<const uint4*>(p);
-        const int words = here / VEC;
+        const uint4* q = reinterpret_cast<const uint4*>(p) + threadIdx.x;
         uint4 w[kWords];
+        if (here == PER) {
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            const int at = i * kClipThreads + threadIdx.x;
-            w[i] = at < words ? __ldg(q + at) : make_uint4(0u, 0u, 0u, 0u);
-        }
+            for (int i = 0; i < kWords; ++i) w[i] = __ldg(q + i * kClipThreads);
+        } else {
+            const int words = here / VEC;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            add_word<T>(s, w[i].x, 0);
-            add_word<T>(s, w[i].y, 2);
-            add_word<T>(s, w[i].z, 1);
-            add_word<T>(s, w[i].w, 3);
+            for (int i = 0; i < kWords; ++i)
+                w[i] = i * kClipThreads + static_cast<int>(threadIdx.x) < words ? __ldg(q + i * kClipThreads)
+                                                                               : make_uint4(0u, 0u, 0u, 0u);
+            const int at = words * VEC + threadIdx.x;  // the last, incomplete word
+            float v[8] = {at < here ? wide(p[at]) : 0.0f};
+            s.add(squares_of<false>(v), [&] { return squares_of<true>(v); });
         }
-        const int at = words * VEC + threadIdx.x;
-        if (at < here) s.add(wide(p[at]), 0);
+        s.add(squares_of<T, false>(w), [&] { return squares_of<T, true>(w); });
     } else {
         for (int i = threadIdx.x; i < here; i += 8 * kClipThreads) {
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = i + k * kClipThreads < here ? wide(p[i + k * kClipThreads]) : 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s.add(v[k], k & 3);
+            s.add(squares_of<false>(v), [&] { return squares_of<true>(v); });
         }
     }
 }
@@ -149,6 +195,17 @@ __device__ __forceinline__ void scale_piece(const T* p, T* o, long long n, float
     if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(o)) & 15u) == 0) {
         const int words = here / VEC;
         uint4 w[kWords];
+        if (here == PER) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i * kClipThreads + threadIdx.x);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                __stcs(reinterpret_cast<uint4*>(o) + i * kClipThreads + threadIdx.x,
+                       make_uint4(scale_word<T>(w[i].x, f), scale_word<T>(w[i].y, f), scale_word<T>(w[i].z, f),
+                                  scale_word<T>(w[i].w, f)));
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
             const int at = i * kClipThreads + threadIdx.x;
@@ -189,14 +246,12 @@ __device__ __forceinline__ float cta_sum(float v, float* s) {
 }
 
 template <int MOST>
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, 4)
     grad_squares_kernel(const __grid_constant__ Table<MOST> t, float2* partial) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float scratch[kClipThreads / 32];
-    Sums s;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s.plain[i] = s.down[i] = 0.0f;
+    Sums s{0.0f, 0.0f};
     const unsigned pieces = t.first[t.count];
     for (unsigned c = blockIdx.x; c < pieces; c += gridDim.x) {
         const int i = find_tensor(t, c);
@@ -212,8 +267,8 @@ __global__ void __launch_bounds__(kClipThreads)
             sum_piece(s, static_cast<const __nv_bfloat16*>(t.in[i]) + at * per, t.size[i] - at * per);
         }
     }
-    const float plain = cta_sum((s.plain[0] + s.plain[1]) + (s.plain[2] + s.plain[3]), scratch);
-    const float down = cta_sum((s.down[0] + s.down[1]) + (s.down[2] + s.down[3]), scratch);
+    const float plain = cta_sum(s.plain, scratch);
+    const float down = cta_sum(s.down, scratch);
     if (threadIdx.x == 0) partial[blockIdx.x] = make_float2(plain, down);
 }
 
@@ -253,7 +308,7 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const float2* p
 }
 
 template <int MOST>
-__global__ void __launch_bounds__(kClipThreads, 4)
+__global__ void __launch_bounds__(kClipThreads, 3)
     grad_scale_kernel(const __grid_constant__ Table<MOST> t, const float2* partial, int parts, float max_norm,
                       float* norm) {
     pdl_launch_dependents();
