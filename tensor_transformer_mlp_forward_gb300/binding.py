@@ -970,6 +970,30 @@ def _heads(x, name: str, shape, dtype, device: int):
     raise ValueError(f"{name} cannot be used")
 
 
+def _heads_out(x, name: str, shape, dtype, device: int, like):
+    """x, or a fresh dense tensor, its address, and how far its tokens lie apart."""
+    if x is None:
+        x = torch.empty(shape, dtype=dtype, device=like.device)
+        return x, x.data_ptr(), shape[1] * shape[2]
+    return x, *_heads(x, name, shape, dtype, device)
+
+
+def _dense_out(x, name: str, shape, dtype, device: int, like):
+    """x, or a fresh tensor, and its address."""
+    if x is None:
+        x = torch.empty(shape, dtype=dtype, device=like.device)
+        return x, x.data_ptr()
+    return x, _in(x, name, shape, dtype, device)
+
+
+def _scratch(x, name: str, need: int, dtype, device: int, like):
+    """x, or a fresh tensor of `need` elements, and its address."""
+    if x is None:
+        x = torch.empty(need or 1, dtype=dtype, device=like.device)
+        return x, x.data_ptr()
+    return x, _in(x, name, x.shape, dtype, device)
+
+
 def _packed_shape(Q, K):
     T, nh, d = Q.shape
     nkv = K.shape[1]
@@ -994,22 +1018,13 @@ def tp_attn_packed_forward(Q, K, V, cu_seqlens, scale=None, O=None, lse=None, wo
     cp = _in(cu_seqlens, "cu_seqlens", (nb + 1,), _I32, dev)
     L = lib()
     with _on(stream):
-        if O is None:
-            O = torch.empty((T, nh, d), dtype=_BF16, device=Q.device)
-            op = O.data_ptr()
-        else:
-            op = _in(O, "O", (T, nh, d), _BF16, dev)
-        if lse is None:
-            lse = torch.empty((nh, T), dtype=_F32, device=Q.device)
-            lp = lse.data_ptr()
-        else:
-            lp = _in(lse, "lse", (nh, T), _F32, dev)
-        if workspace is None:
-            need = L.tp_attn_packed_forward_workspace_bytes(nb, T, nh, nkv, d)
-            workspace = torch.empty(need or 1, dtype=_U8, device=Q.device)
+        O, op = _dense_out(O, "O", (T, nh, d), _BF16, dev, Q)
+        lse, lp = _dense_out(lse, "lse", (nh, T), _F32, dev, Q)
+        need = L.tp_attn_packed_forward_workspace_bytes(nb, T, nh, nkv, d) if workspace is None else 0
+        workspace, wp = _scratch(workspace, "workspace", need, _U8, dev, Q)
     status = L.tp_attn_packed_forward(
-        qp, ldq, kp, ldk, vp, ldv, cp, nb, T, nh, nkv, d, d ** -0.5 if scale is None else scale, op, lp,
-        _in(workspace, "workspace", workspace.shape, _U8, dev), workspace.numel(), _stream_of(stream, dev))
+        qp, ldq, kp, ldk, vp, ldv, cp, nb, T, nh, nkv, d, d ** -0.5 if scale is None else scale, op, lp, wp,
+        workspace.numel(), _stream_of(stream, dev))
     if status:
         _check("tp_attn_packed_forward", status)
     return O, lse
@@ -1033,19 +1048,14 @@ def tp_attn_packed_backward(Q, K, V, O, lse, dO, cu_seqlens, scale=None, dQ=None
     cp = _in(cu_seqlens, "cu_seqlens", (nb + 1,), _I32, dev)
     L = lib()
     with _on(stream):
-        dQ = torch.empty(qs, dtype=_BF16, device=Q.device) if dQ is None else dQ
-        dK = torch.empty(ks, dtype=_BF16, device=Q.device) if dK is None else dK
-        dV = torch.empty(ks, dtype=_BF16, device=Q.device) if dV is None else dV
-        if workspace is None:
-            need = L.tp_attn_packed_backward_workspace_bytes(nb, T, nh, nkv, d)
-            workspace = torch.empty(need or 1, dtype=_U8, device=Q.device)
-    dqp, lddq = _heads(dQ, "dQ", qs, _BF16, dev)
-    dkp, lddk = _heads(dK, "dK", ks, _BF16, dev)
-    dvp, lddv = _heads(dV, "dV", ks, _BF16, dev)
+        dQ, dqp, lddq = _heads_out(dQ, "dQ", qs, _BF16, dev, Q)
+        dK, dkp, lddk = _heads_out(dK, "dK", ks, _BF16, dev, Q)
+        dV, dvp, lddv = _heads_out(dV, "dV", ks, _BF16, dev, Q)
+        need = L.tp_attn_packed_backward_workspace_bytes(nb, T, nh, nkv, d) if workspace is None else 0
+        workspace, wp = _scratch(workspace, "workspace", need, _U8, dev, Q)
     status = L.tp_attn_packed_backward(
         qp, ldq, kp, ldk, vp, ldv, op, lp, dop, cp, nb, T, nh, nkv, d, d ** -0.5 if scale is None else scale,
-        dqp, lddq, dkp, lddk, dvp, lddv, _in(workspace, "workspace", workspace.shape, _U8, dev), workspace.numel(),
-        _stream_of(stream, dev))
+        dqp, lddq, dkp, lddk, dvp, lddv, wp, workspace.numel(), _stream_of(stream, dev))
     if status:
         _check("tp_attn_packed_backward", status)
     return dQ, dK, dV
@@ -1069,15 +1079,12 @@ def tp_qk_norm_rope_forward(Q, K, gamma_q, gamma_k, positions, rot=None, theta: 
     gq, gk = _in(gamma_q, "gamma_q", (d,), dt, dev), _in(gamma_k, "gamma_k", (d,), dt, dev)
     pp = _in(positions, "positions", (T,), _I32, dev)
     with _on(stream):
-        Qo = torch.empty(qs, dtype=dt, device=Q.device) if Qo is None else Qo
-        Ko = torch.empty(ks, dtype=dt, device=Q.device) if Ko is None else Ko
-        if rstd is None:
-            rstd = torch.empty((T, nh + nkv), dtype=_F32, device=Q.device)
-    qop, ldqo = _heads(Qo, "Qo", qs, dt, dev)
-    kop, ldko = _heads(Ko, "Ko", ks, dt, dev)
+        Qo, qop, ldqo = _heads_out(Qo, "Qo", qs, dt, dev, Q)
+        Ko, kop, ldko = _heads_out(Ko, "Ko", ks, dt, dev, Q)
+        rstd, rp = _dense_out(rstd, "rstd", (T, nh + nkv), _F32, dev, Q)
     status = lib().tp_qk_norm_rope_forward(
         qp, ldq, kp, ldk, gq, gk, pp, T, nh, nkv, d, d if rot is None else rot, theta, eps, code, qop, ldqo, kop, ldko,
-        _in(rstd, "rstd", (T, nh + nkv), _F32, dev), _stream_of(stream, dev))
+        rp, _stream_of(stream, dev))
     if status:
         _check("tp_qk_norm_rope_forward", status)
     return Qo, Ko, rstd
@@ -1101,20 +1108,16 @@ def tp_qk_norm_rope_backward(dQo, dKo, Q, K, gamma_q, gamma_k, positions, rstd, 
     L = lib()
     need = L.tp_qk_norm_rope_backward_workspace_floats(T, nh, nkv, d)
     with _on(stream):
-        dQ = torch.empty(qs, dtype=dt, device=Q.device) if dQ is None else dQ
-        dK = torch.empty(ks, dtype=dt, device=Q.device) if dK is None else dK
-        dgamma_q = torch.empty(d, dtype=_F32, device=Q.device) if dgamma_q is None else dgamma_q
-        dgamma_k = torch.empty(d, dtype=_F32, device=Q.device) if dgamma_k is None else dgamma_k
-        if partial is None:
-            partial = torch.empty(need or 1, dtype=_F32, device=Q.device)
+        dQ, dqp, lddq = _heads_out(dQ, "dQ", qs, dt, dev, Q)
+        dK, dkp, lddk = _heads_out(dK, "dK", ks, dt, dev, Q)
+        dgamma_q, dgq = _dense_out(dgamma_q, "dgamma_q", (d,), _F32, dev, Q)
+        dgamma_k, dgk = _dense_out(dgamma_k, "dgamma_k", (d,), _F32, dev, Q)
+        partial, sp = _scratch(partial, "partial", need, _F32, dev, Q)
     if partial.numel() < need:
         raise ValueError(f"partial holds {partial.numel()} floats, {need} needed")
-    dqp, lddq = _heads(dQ, "dQ", qs, dt, dev)
-    dkp, lddk = _heads(dK, "dK", ks, dt, dev)
     status = L.tp_qk_norm_rope_backward(
         yq, ldyq, yk, ldyk, qp, ldq, kp, ldk, gq, gk, pp, rp, T, nh, nkv, d, d if rot is None else rot, theta, code,
-        dqp, lddq, dkp, lddk, _in(dgamma_q, "dgamma_q", (d,), _F32, dev), _in(dgamma_k, "dgamma_k", (d,), _F32, dev),
-        _in(partial, "partial", partial.shape, _F32, dev), _stream_of(stream, dev))
+        dqp, lddq, dkp, lddk, dgq, dgk, sp, _stream_of(stream, dev))
     if status:
         _check("tp_qk_norm_rope_backward", status)
     return dQ, dK, dgamma_q, dgamma_k

@@ -495,11 +495,9 @@ unsigned persistent_grid(long long items, int sms) {
 template <int D>
 cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& a,
                        unsigned grid, cudaStream_t st) {
-    auto kern = packed_fwd_kernel<D>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<D>::SMEM);
+    const cudaError_t e = allow_shared<packed_fwd_kernel<D>>(FwdCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(grid), dim3(kFwdThreads), FwdCfg<D>::SMEM, st, q, k, v, a);
+    return launch_dependent(packed_fwd_kernel<D>, dim3(grid), dim3(kFwdThreads), FwdCfg<D>::SMEM, st, q, k, v, a);
 }
 
 }  // namespace

@@ -1053,8 +1053,8 @@ cudaError_t launch_bwd(const CUtensorMap& q128, const CUtensorMap& do128, const 
     constexpr int smem = BwdCfg<D>::SMEM;
     auto kq = packed_dq_kernel<D>;
     auto kk = packed_dkdv_kernel<D>;
-    if ((e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
+    if ((e = allow_shared<packed_dq_kernel<D>>(smem)) != cudaSuccess ||
+        (e = allow_shared<packed_dkdv_kernel<D>>(smem)) != cudaSuccess ||
         (e = launch_dependent(kq, grid(p.nh), dim3(kDqThreads), smem, st, q128, do128, k_s, v_s, a)) != cudaSuccess)
         return e;
     ++*launches;

@@ -9,6 +9,8 @@
 // first, so that the persistent kernels take the heaviest items first.
 #pragma once
 
+#include <atomic>
+
 #include "attn_common.cuh"
 
 namespace tpmlp {
@@ -322,6 +324,20 @@ __device__ __forceinline__ void read_out(const RowsOut& out, int c, uint32_t add
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack_scaled(v[2 * i], v[2 * i + 1], f);
     out.store(c, w);
+}
+
+// Lets a kernel have its dynamic shared memory, once per device.
+template <auto KERNEL>
+cudaError_t allow_shared(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace

@@ -511,9 +511,14 @@ void deal_ctas(int T, int nh, int nkv, long long run, int most, int (&ctas)[2]) 
 }
 
 QkTurns make_turns(double theta, int rot) {
+    // theta^(-2 i / rot) as a product of two powers, for 16 + 8 of them in place of 128
+    // (half of a call's host time), two roundings in place of one
     QkTurns t{};
+    double low[8], high[16];
+    for (int i = 0; i < 8; ++i) low[i] = i < rot / 2 ? std::pow(theta, -2.0 * i / rot) : 0.0;
+    for (int i = 0; 8 * i < rot / 2; ++i) high[i] = std::pow(theta, -16.0 * i / rot) * 0.15915494309189535;  // 1 / (2 pi)
     for (int i = 0; i < rot / 2; ++i) {
-        double f = std::pow(theta, -2.0 * i / rot) * 0.15915494309189535;  // 1 / (2 pi)
+        double f = high[i / 8] * low[i % 8];
         f -= std::floor(f);
         t.f[i] = static_cast<unsigned long long>(f * 18446744073709551616.0);  // f < 1
     }
@@ -549,7 +554,8 @@ QkArgs make_args(const QkNormRope& p) {
     return a;
 }
 
-// Shared memory of `tables` tables of sines and cosines: as many tokens as a run can touch.
+// Shared memory of `tables` tables of sines and cosines: as many tokens as a run can touch
+// (one head of 256 or two of 32 at least: 35 KB at most).
 size_t table_bytes(int run, int heads, int rot, int tables) {
     return sizeof(float) * static_cast<size_t>((run + heads - 2) / heads + 1) * rot * tables;
 }
@@ -568,13 +574,9 @@ cudaError_t backward_as(const QkArgs& a, const QkTurns& turns, cudaStream_t st) 
     constexpr int run = kUnitsBackward * kQkThreads / LANES;
     const int heads = a.job[0].heads < a.job[1].heads ? a.job[0].heads : a.job[1].heads;
     const size_t tables = table_bytes(run, heads, a.rot, 2), rows = sizeof(float) * (kQkThreads / 32) * a.d;
-    const size_t smem = tables > rows ? tables : rows;
-    auto kern = qk_backward_kernel<T, LANES, kUnitsBackward, kPerSmBackward>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(static_cast<unsigned>(a.ctas[0] + a.ctas[1])), dim3(kQkThreads), smem, st, a,
-                            turns, static_cast<int>(tables / (2 * sizeof(float))));
+    return launch_dependent(qk_backward_kernel<T, LANES, kUnitsBackward, kPerSmBackward>,
+                            dim3(static_cast<unsigned>(a.ctas[0] + a.ctas[1])), dim3(kQkThreads),
+                            tables > rows ? tables : rows, st, a, turns, static_cast<int>(tables / (2 * sizeof(float))));
 }
 
 template <typename T>
