@@ -247,6 +247,62 @@ def test_a_long_sequence_of_more_ranks_than_shared_memory_counts():
         assert ((lse[:, t].double().cpu() - torch.logsumexp(z, 0) / math.log(2.0)).abs() <= 2.0 ** -9).all()
 
 
+def test_groups_dealt_to_parts():
+    # 64 query heads on 8: the dK/dV kernel's items are few, and each group's heads go to
+    # parts whose sums are added behind; gradients into parts of one matrix, tokens
+    # outside the sequences left alone
+    cu = [3, 403, 403, 990]
+    T, nh, nkv, d = 1000, 64, 8, 64
+    cpu, (q, k, v, do) = _inputs(T, nh, nkv, d, seed=51)
+    Or, lr, _ = ref.attention(*cpu[:3], cu, d ** -0.5)
+    rows = torch.full((T, (nh + 2 * nkv) * d), 7.0, dtype=BF, device="cuda")
+    g = [rows[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in ((0, nh), (nh, nh + nkv), (nh + nkv, nh + 2 * nkv))]
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    got = binding.tp_attn_packed_backward(q, k, v, Or.to(BF).cuda(), lr.float().cuda(), do, cud, dQ=g[0], dK=g[1],
+                                          dV=g[2])
+    assert binding.last_launch_count() == 4  # delta and plan, dQ, dK and dV, parts
+    _check_backward(got, cpu, Or.to(BF), lr.float(), cpu[3], cu, d ** -0.5)
+    assert (rows[:3] == 7.0).all() and (rows[990:] == 7.0).all()
+
+
+def test_dependent_launch_and_threads_change_nothing():
+    import threading
+
+    cu = torch.tensor(_cu([200, 1, 90, 333, 140]), dtype=torch.int32, device="cuda")
+    sets = [_inputs(764, 8, 2, 128, seed=60 + i)[1] for i in range(3)]
+
+    def run(x):
+        O, lse = binding.tp_attn_packed_forward(*x[:3], cu)
+        return [O, lse, *binding.tp_attn_packed_backward(*x[:3], O, lse, x[3], cu)]
+
+    want = [run(x) for x in sets]
+    old = binding.set_dependent_launch(0)
+    try:
+        assert all(torch.equal(a, b) for x, w in zip(sets, want) for a, b in zip(run(x), w))
+    finally:
+        binding.set_dependent_launch(old)
+    torch.cuda.synchronize()
+    got, bad = [None] * 3, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = run(sets[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 - reported below
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    assert binding.device_status() == 0
+
+
 def test_other_stream_and_graph_with_new_lengths():
     T, nh, nkv, d = 400, 4, 2, 128
     cpu, (q, k, v, do) = _inputs(T, nh, nkv, d, seed=41)

@@ -169,6 +169,17 @@ def test_scratch_sizes(L, nb, T):
     assert L.tp_qk_norm_rope_backward_workspace_floats(T, 8, 2, 100) == 0
 
 
+def test_parts_scratch_is_bounded(L):
+    # groups dealt to parts: their fp32 sums stay near 100 MB whatever the tokens are
+    plain = lambda nb, T, nh: 16 * (T // 128 + nb) + 4 * (T // 128 + 2) + 4 * T * nh + 2048  # noqa: E731
+    for nb, T, nh, nkv in ((1, 128, 16, 1), (1, 8192, 16, 1), (8, 8192, 32, 8), (1, 1 << 20, 64, 1), (3, 20000, 24, 3)):
+        need = L.tp_attn_packed_backward_workspace_bytes(nb, T, nh, nkv, 160)
+        assert plain(nb, T, nh) - 2048 <= need <= plain(nb, T, nh) + 160 * (1 << 20), (nb, T, nh, nkv)
+    # enough items without parts: nothing but the plan and delta
+    assert L.tp_attn_packed_backward_workspace_bytes(1, 1 << 20, 64, 1, 160) <= plain(1, 1 << 20, 64)
+    assert L.tp_attn_packed_backward_workspace_bytes(8, 8192, 16, 16, 160) <= plain(8, 8192, 16)
+
+
 def test_binding_refusals():
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     cu = torch.zeros(2, dtype=torch.int32)
