@@ -609,7 +609,7 @@ int tp_attn_backward(const tpmlp_bf16* dY, const tpmlp_bf16* X, const tpmlp_bf16
  *   P = softmax over each row, O = P V
  *
  * Layout: Q, dQ [T, nh, d], K, V, dK, dV [T, nkv, d] bf16, head by head, whose
- * tokens lie ld* values apart (ld* >= heads * d, a multiple of 8), so that they
+ * tokens lie ld* values apart (heads * d <= ld* < 2^31, a multiple of 8), so that they
  * may be parts of one [T, (nh + 2 nkv) d] projection; O, dO [T, nh, d] dense;
  * lse float32 [nh, T], in the log2 domain as in tp_attn_core_forward;
  * cu_seqlens int32 [nb + 1] in device memory (4-byte aligned): read on the
@@ -622,7 +622,7 @@ int tp_attn_backward(const tpmlp_bf16* dY, const tpmlp_bf16* X, const tpmlp_bf16
  * nh % nkv == 0, d in {64, 96, 128, 160}, scale finite and > 0 (1/sqrt(d) as a
  * rule), (T / 128 + nb) nh < 2^31, T nh <= 2^36.  nb == 0 or T == 0 does nothing.
  * A token's infinities and NaN reach no other sequence; within its own they may
- * reach earlier tokens of its block of 128. */
+ * reach tokens of its block of 128 that do not see it. */
 
 /* Bytes of scratch tp_attn_packed_forward needs (contents on entry do not
  * matter): the list of work items that the call makes on its stream. */
@@ -659,7 +659,7 @@ int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16
  *   a_i = p theta^(-2 i / rot)
  *
  * Q, Qo [T, nh, d] and K, Ko [T, nkv, d] of type `dtype` (tpmlp_dtype) with
- * tokens ld* values apart (ld* >= heads * d, whole 16-byte pieces); gamma_q,
+ * tokens ld* values apart (heads * d <= ld* < 2^31, whole 16-byte pieces); gamma_q,
  * gamma_k [d] of that type, shared by the heads; positions int32 [T] (4-byte
  * aligned, any values); rstd float32 [T, nh + nkv] (queries first), saved for
  * the backward pass.  Statistics and rotation are fp32, angles exact to fp32 at

@@ -995,6 +995,8 @@ def _scratch(x, name: str, need: int, dtype, device: int, like):
 
 
 def _packed_shape(Q, K):
+    if Q.dim() != 3 or K.dim() != 3:
+        raise ValueError(f"Q and K must be [T, heads, d], got {tuple(Q.shape)} and {tuple(K.shape)}")
     T, nh, d = Q.shape
     nkv = K.shape[1]
     if T > _MOST or nh > _MOST or nkv > _MOST:

@@ -976,6 +976,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 for (int c = 0; c < D / 32; ++c) read_out(out, c, chunk(c), w ? a.scale : 1.0f);
             } else {
                 // a part of the group's heads: its fp32 sum
+                const bool wide = (reinterpret_cast<uintptr_t>(a.parts) & 31u) == 0;
                 float* row = a.parts + (((it.part * a.T + first_row + lane) * a.nkv + it.kv_head) * 2 + w) * D;
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];
@@ -987,7 +988,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                             uint32_t u[8];
 #pragma unroll
                             for (int f = 0; f < 8; ++f) u[f] = v[8 * e + f];
-                            store_32(row + 32 * c + 8 * e, u, true);
+                            store_32(row + 32 * c + 8 * e, u, wide);
                         }
                 }
             }

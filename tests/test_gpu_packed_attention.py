@@ -263,6 +263,16 @@ def test_groups_dealt_to_parts():
     assert binding.last_launch_count() == 4  # delta and plan, dQ, dK and dV, parts
     _check_backward(got, cpu, Or.to(BF), lr.float(), cpu[3], cu, d ** -0.5)
     assert (rows[:3] == 7.0).all() and (rows[990:] == 7.0).all()
+    # a workspace, O and gradients that start on 16-byte boundaries only
+    need = binding.lib().tp_attn_packed_backward_workspace_bytes(3, T, nh, nkv, d)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")[16:]
+    odd = [torch.empty(x.numel() + 8, dtype=BF, device="cuda")[8:].view(x.shape) for x in got]
+    again = binding.tp_attn_packed_backward(q, k, v, Or.to(BF).cuda(), lr.float().cuda(), do, cud, dQ=odd[0], dK=odd[1],
+                                            dV=odd[2], workspace=ws)
+    assert all(torch.equal(a[3:990], b[3:990]) for a, b in zip(got, again))
+    O = torch.empty(T * nh * d + 8, dtype=BF, device="cuda")[8:].view(T, nh, d)
+    binding.tp_attn_packed_forward(q, k, v, cud, O=O)
+    assert torch.equal(O[3:990], binding.tp_attn_packed_forward(q, k, v, cud)[0][3:990])
 
 
 def test_dependent_launch_and_threads_change_nothing():
