@@ -29,6 +29,16 @@
 namespace tpmlp {
 namespace {
 
+// The Q tiles have two places where they fit (d = 64), so that the next item's are there
+// when the last product of this one is done.
+template <int D>
+struct PackedFwdCfg : FwdCfg<D> {
+    using F = FwdCfg<D>;
+    static constexpr int QPLACES = 2 * F::FIXED + F::STAGES * F::KVTILE <= 224 * 1024 ? 2 : 1;
+    static constexpr int BARS = 256 + 16;
+    static constexpr int SMEM = 1024 + QPLACES * F::FIXED + F::STAGES * F::KVTILE + BARS;
+};
+
 struct FwdArgs {
     const int4* entries;  // the plan's tiles
     unsigned* plan;       // its header words
@@ -74,19 +84,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                       const __grid_constant__ CUtensorMap tm_k,  // BKV-row boxes
                       const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
     pdl_launch_dependents();  // the next kernel may begin its launch
-    using C = FwdCfg<D>;
+    using C = PackedFwdCfg<D>;
     constexpr int S = C::STAGES;
     constexpr int BKV = C::BKV;
     constexpr int SCH = BKV / 32;  // 32-key chunks of S per key tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    uint8_t* sQ = smem;                   // Q_A, Q_B
-    uint8_t* ring = smem + 2 * C::QTILE;  // K_0, V_0, K_1, V_1, ... of every item in turn
+    constexpr int QP = C::QPLACES;
+    uint8_t* sQ = smem;                   // [QP] x {Q_A, Q_B}
+    uint8_t* ring = smem + QP * 2 * C::QTILE;  // K_0, V_0, K_1, V_1, ... of every item in turn
     uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S * C::KVTILE);
-    uint64_t* q_full = bars;              // the item's Q tiles have landed
-    uint64_t* q_empty = bars + 1;         // the item's last S MMAs have read them
-    uint64_t* kv_full = bars + 2;
+    uint64_t* q_full = bars;              // [QP] the item's Q tiles have landed
+    uint64_t* q_empty = bars + 2;         // [QP] the item's last S MMAs have read them
+    uint64_t* kv_full = bars + 4;
     uint64_t* kv_empty = kv_full + S;
     uint64_t* s_full = kv_empty + S;      // [tile]
     uint64_t* p_full = s_full + 2;        // [tile]
@@ -129,8 +140,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     };
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        for (int i = 0; i < QP; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+        }
         for (int i = 0; i < S; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
@@ -192,15 +205,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const Item it = decode(slot);
                 const int kcol = it.head[0] / a.group * D;
                 // the previous item's S MMAs are done with the Q tiles
-                if (k >= 1 && !thread_wait(q_empty, static_cast<uint32_t>(k - 1) & 1u, abort_flag,
-                                            a.status, 0x412))
+                const int qp = k % QP;
+                if (k >= QP && !thread_wait(&q_empty[qp], static_cast<uint32_t>(k / QP - 1) & 1u, abort_flag, a.status,
+                                            0x412))
                     break;
-                mbar_arrive_expect_tx(q_full, (it.has_b ? 2 : 1) * C::QTILE);
+                mbar_arrive_expect_tx(&q_full[qp], (it.has_b ? 2 : 1) * C::QTILE);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     for (int b = 0; b < C::NB && (x == 0 || it.has_b); ++b)
-                        tma_load_3d(&tm_q, smem_u32(q_full),
-                                    smem_u32(sQ) + x * C::QTILE + b * 128 * kRowBytes,
+                        tma_load_3d(&tm_q, smem_u32(&q_full[qp]),
+                                    smem_u32(sQ) + (2 * qp + x) * C::QTILE + b * 128 * kRowBytes,
                                     it.head[x] * D + 64 * b, it.row0 + it.q0[x], 0);
                 ++q_loads;
                 for (int idx = 0; idx < 2 * it.n_kv; ++idx) {  // K_j = 2j, V_j = 2j + 1
@@ -222,7 +236,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
                 if (!ok) break;
             }
-            if (q_loads > 0) wait_drain(q_full, static_cast<uint32_t>(q_loads - 1) & 1u, a.status, 0x402);
+            for (int k = q_loads > QP ? q_loads - QP : 0; k < q_loads; ++k)
+                wait_drain(&q_full[k % QP], static_cast<uint32_t>(k / QP) & 1u, a.status, 0x402);
             for (int i = 0; i < S; ++i)
                 if (issued & (1u << i)) wait_drain(&kv_full[i], (issued_phase >> i) & 1u, a.status, 0x403);
         }
@@ -242,12 +257,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             };
             int s_left = 0;  // S MMAs of the item still to issue
+            int qp = 0;      // where the item's Q tiles lie
             auto issue_s = [&](int x, int stage) {  // S_x = Q_x K^T
-                warp_mma_scores<D, BKV>(tmem + C::s_col(x), desc_low(smem_u32(sQ) + x * C::QTILE, 16),
+                warp_mma_scores<D, BKV>(tmem + C::s_col(x), desc_low(smem_u32(sQ) + (2 * qp + x) * C::QTILE, 16),
                                         desc_low(smem_u32(ring) + stage * C::KVTILE, 16));
                 warp_commit(&s_full[x]);
                 // the item's last S: once done, the Q tiles may be replaced
-                if (--s_left == 0) warp_commit(q_empty);
+                if (--s_left == 0) warp_commit(&q_empty[qp]);
             };
             // O_x (+)= P_x V: A = P_x from TMEM (packed over S_x's first columns), B = V
             // (MN-major: d along the rows, keys down the box)
@@ -273,7 +289,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 __syncwarp();
                 warp_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
-                if (!warp_wait_both(q_full, static_cast<uint32_t>(k) & 1u, &kv_full[rstage], rphase, abort_flag,
+                qp = k % QP;
+                if (!warp_wait_both(&q_full[qp], static_cast<uint32_t>(k / QP) & 1u, &kv_full[rstage], rphase, abort_flag,
                                       a.status, 0x404))
                     break;
                 tc_fence_after();
@@ -351,6 +368,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int jl = x ? it.last[1] : it.last[0];
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j <= jl; ++j) {
+                const int k0 = j * BKV;
+                // V rows behind the sequence's end, while S is computed
+                if (k0 + BKV > it.len) {
+                    const unsigned v_at = ring0 + 2u * static_cast<unsigned>(j) + 1u;
+                    const int vs = static_cast<int>(v_at % S);
+                    if (!warp_wait(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
+                        ok = false;
+                        break;
+                    }
+                    zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - k0, r, 128);
+                }
                 if (!warp_wait(&s_full[x], static_cast<uint32_t>(gxl + j) & 1u, abort_flag,
                                        a.status, 0x40C + x)) {
                     ok = false;
@@ -364,7 +392,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // chunks of 32 keys: the warp's queries see the first `live`, the last of
                 // those up to the diagonal if that is in this key tile; the rest holds
                 // nothing for any of them
-                const int k0 = j * BKV;
                 const int live = ((first_q - k0) >> 5) + 1;
                 // eight independent max / sum chains: the row is one thread's
                 // work, so its reductions must not be one serial chain
@@ -441,16 +468,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         tmem_wait_st();
                     }
                 }
-                // V rows behind the sequence's end
-                if (k0 + BKV > it.len) {
-                    const unsigned v_at = ring0 + 2u * static_cast<unsigned>(j) + 1u;
-                    const int vs = static_cast<int>(v_at % S);
-                    if (!warp_wait(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
-                        ok = false;
-                        break;
-                    }
-                    zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - k0, r, 128);
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -495,9 +512,9 @@ unsigned persistent_grid(long long items, int sms) {
 template <int D>
 cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const FwdArgs& a,
                        unsigned grid, cudaStream_t st) {
-    const cudaError_t e = allow_shared<packed_fwd_kernel<D>>(FwdCfg<D>::SMEM);
+    const cudaError_t e = allow_shared<packed_fwd_kernel<D>>(PackedFwdCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(packed_fwd_kernel<D>, dim3(grid), dim3(kFwdThreads), FwdCfg<D>::SMEM, st, q, k, v, a);
+    return launch_dependent(packed_fwd_kernel<D>, dim3(grid), dim3(kFwdThreads), PackedFwdCfg<D>::SMEM, st, q, k, v, a);
 }
 
 }  // namespace

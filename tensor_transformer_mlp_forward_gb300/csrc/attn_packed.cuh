@@ -259,10 +259,10 @@ __device__ __forceinline__ void warp_mma_values(uint32_t acc, uint32_t tail, uin
 template <int NB>
 __device__ __forceinline__ void zero_rows(uint32_t tile, int rows, int first, int tid, int threads) {
     const int chunks = (rows - first) * 8;  // 16-byte chunks of a box
-    for (int i = tid; i < NB * chunks; i += threads) {
-        const int b = i / chunks, c = i - b * chunks;
-        st_shared_v4(tile + static_cast<uint32_t>((b * rows + first) * kRowBytes + c * 16), 0u, 0u, 0u, 0u);
-    }
+    for (int c = tid; c < chunks; c += threads)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            st_shared_v4(tile + static_cast<uint32_t>((b * rows + first) * kRowBytes + c * 16), 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
 }
 
