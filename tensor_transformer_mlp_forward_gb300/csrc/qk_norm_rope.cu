@@ -39,7 +39,10 @@
 namespace tpmlp {
 namespace {
 
-constexpr int kQkThreads = 256;
+// Small CTAs wait less at the barrier between a run's sines and their use: 32 and 58 us
+// (forward and backward, 8192 tokens of 40 heads of 128) against 34 and 61 with 256
+// threads.  At least one for each of a token's pairs (rot / 2 <= 128).
+constexpr int kQkThreads = 128;
 
 struct QkTurns {
     unsigned long long f[128];  // per pair: turns a position, times 2^64
@@ -490,9 +493,8 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Pairs a thread holds, and CTAs an SM: what the registers allow with enough loads in
-// flight (backward, 8192 tokens of 40 heads of 128: 61 us; two pairs 65, three CTAs, which
-// spill, 79).
-constexpr int kUnitsForward = 4, kUnitsBackward = 1, kPerSmForward = 4, kPerSmBackward = 2;
+// flight (backward: two pairs 64 us, five CTAs, which spill, 62).
+constexpr int kUnitsForward = 4, kUnitsBackward = 1, kPerSmForward = 8, kPerSmBackward = 4;
 
 int lanes_of(int d) { return d <= 32 ? 2 : d <= 64 ? 4 : d <= 128 ? 8 : 16; }
 
