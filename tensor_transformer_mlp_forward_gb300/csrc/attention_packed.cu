@@ -369,16 +369,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j <= jl; ++j) {
                 const int k0 = j * BKV;
-                // V rows behind the sequence's end, while S is computed
-                if (k0 + BKV > it.len) {
-                    const unsigned v_at = ring0 + 2u * static_cast<unsigned>(j) + 1u;
-                    const int vs = static_cast<int>(v_at % S);
-                    if (!warp_wait(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
-                        ok = false;
-                        break;
-                    }
-                    zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - k0, r, 128);
-                }
                 if (!warp_wait(&s_full[x], static_cast<uint32_t>(gxl + j) & 1u, abort_flag,
                                        a.status, 0x40C + x)) {
                     ok = false;
@@ -387,8 +377,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 tc_fence_after();
                 uint32_t v[SCH][32];
 #pragma unroll
-                for (int c = 0; c < SCH; ++c) tmem_ld32(s_addr + c * 32, v[c]);
-                tmem_wait_ld();
+                for (int c = 0; c < SCH; ++c) warp_tmem_ld32(s_addr + c * 32, v[c]);
+#pragma unroll
+                for (int c = 0; c < SCH; ++c) tmem_loaded(v[c]);
                 // chunks of 32 keys: the warp's queries see the first `live`, the last of
                 // those up to the diagonal if that is in this key tile; the rest holds
                 // nothing for any of them
@@ -431,7 +422,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     for (int c = 0; c < SCH; ++c) {
                         uint32_t pk[16];
                         row_weights(v[c], scale2, neg_m, pk, rs2);
-                        tmem_st16(s_addr + 16 * c, pk);
+                        warp_tmem_st16(s_addr + 16 * c, pk);
                     }
                 } else {
 #pragma unroll
@@ -443,7 +434,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 16; ++i) pk[i] = 0u;
                         }
-                        tmem_st16(s_addr + 16 * c, pk);
+                        warp_tmem_st16(s_addr + 16 * c, pk);
                     }
                 }
                 float rsv[8];
@@ -459,15 +450,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
-                            tmem_ld32(lane_addr + C::o_chunk(x, c), o);
-                            tmem_wait_ld();
+                            warp_tmem_ld32(lane_addr + C::o_chunk(x, c), o);
+                            tmem_loaded(o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st32(lane_addr + C::o_chunk(x, c), o);
+                            warp_tmem_st32(lane_addr + C::o_chunk(x, c), o);
                         }
+                        __syncwarp();
                         tmem_wait_st();
                     }
                 }
+                // V rows behind the sequence's end.  (S of this tile is there, so every load up
+                // to its K has landed and V's phase is the next of its slot: before S, a
+                // warpgroup that has skipped items could take an older phase for it.)
+                if (k0 + BKV > it.len) {
+                    const unsigned v_at = ring0 + 2u * static_cast<unsigned>(j) + 1u;
+                    const int vs = static_cast<int>(v_at % S);
+                    if (!warp_wait(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
+                        ok = false;
+                        break;
+                    }
+                    zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - k0, r, 128);
+                }
+                __syncwarp();
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();

@@ -119,8 +119,9 @@ struct RingSlot {
 template <int HALF>
 __device__ __forceinline__ void tmem_ld_half(uint32_t addr, uint32_t (&v)[HALF / 32][32]) {
 #pragma unroll
-    for (int c = 0; c < HALF / 32; ++c) tmem_ld32(addr + 32 * c, v[c]);
-    tmem_wait_ld();
+    for (int c = 0; c < HALF / 32; ++c) warp_tmem_ld32(addr + 32 * c, v[c]);
+#pragma unroll
+    for (int c = 0; c < HALF / 32; ++c) tmem_loaded(v[c]);
 }
 
 // The same value, or the columns' own (in shared memory, the same for every lane), as
@@ -549,8 +550,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                     } else {
                         score_grads<false>(v[c], p[c], neg_dlt, 0, 0, dd);
                     }
-                    tmem_st16(dp + 16 * c, dd);
+                    warp_tmem_st16(dp + 16 * c, dd);
                 }
+                __syncwarp();
                 tmem_wait_st();
                 tc_fence_before();
                 // K rows behind the sequence's end (S, their first use, is done)
@@ -904,8 +906,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 #pragma unroll
                 for (int c = 0; c < HALF / 32; ++c) {
                     uint32_t v[32];
-                    tmem_ld32(lane_addr + C::kS + w * HALF + 32 * c, v);
-                    tmem_wait_ld();
+                    warp_tmem_ld32(lane_addr + C::kS + w * HALF + 32 * c, v);
+                    tmem_loaded(v);
                     const ColumnValues neg_lse{stat + 32 * c};
                     if (full(c)) {
                         weights<false>(v, scale2, neg_lse, 0, 0, p[c]);
@@ -918,8 +920,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                     uint32_t pp[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) pp[e] = pack_bf16x2(p[c][2 * e], p[c][2 * e + 1]);
-                    tmem_st16(lane_addr + C::kS + w * HALF + 16 * c, pp);
+                    warp_tmem_st16(lane_addr + C::kS + w * HALF + 16 * c, pp);
                 }
+                __syncwarp();
                 tmem_wait_st();
                 tc_fence_before();
                 if (tail) {  // dO rows behind the end
@@ -939,8 +942,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 #pragma unroll
                 for (int c = 0; c < HALF / 32; ++c) {
                     uint32_t v[32], dd[16];
-                    tmem_ld32(lane_addr + C::dp(0) + w * HALF + 32 * c, v);
-                    tmem_wait_ld();
+                    warp_tmem_ld32(lane_addr + C::dp(0) + w * HALF + 32 * c, v);
+                    tmem_loaded(v);
                     const ColumnValues neg_dlt{stat + HALF + 32 * c};
                     if (full(c)) {
                         score_grads<false>(v, p[c], neg_dlt, 0, 0, dd);
@@ -950,8 +953,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                     } else {
                         score_grads<true>(v, p[c], neg_dlt, lo(c), hi(c), dd);
                     }
-                    tmem_st16(lane_addr + C::dp(0) + w * HALF + 16 * c, dd);
+                    warp_tmem_st16(lane_addr + C::dp(0) + w * HALF + 16 * c, dd);
                 }
+                __syncwarp();
                 tmem_wait_st();
                 tc_fence_before();
                 // Q rows behind the end (S^T, their first use, is done)
@@ -980,8 +984,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 float* row = a.parts + (((it.part * a.T + first_row + lane) * a.nkv + it.kv_head) * 2 + w) * D;
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];
-                    tmem_ld32(chunk(c), v);
-                    tmem_wait_ld();
+                    warp_tmem_ld32(chunk(c), v);
+                    tmem_loaded(v);
                     if (lane < it.len - first_key)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {

@@ -251,6 +251,34 @@ __device__ __forceinline__ void warp_mma_values(uint32_t acc, uint32_t tail, uin
     }
 }
 
+// Tensor-memory loads and stores are instructions of the whole warp, and the compiler may
+// leave lanes apart after a branch by lane (a causal mask, a row behind the end): they are
+// brought together first.
+__device__ __forceinline__ void warp_tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    __syncwarp();
+    tmem_ld32(taddr, r);
+}
+__device__ __forceinline__ void warp_tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    __syncwarp();
+    tmem_st32(taddr, r);
+}
+__device__ __forceinline__ void warp_tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    __syncwarp();
+    tmem_st16(taddr, r);
+}
+
+// The end of a wait for tensor-memory loads, with their registers passing through it: what
+// is computed from them cannot be moved in front of the wait.
+__device__ __forceinline__ void tmem_loaded(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+
 // Zeroes rows first .. rows - 1 of an operand tile of NB 64-column boxes in
 // shared memory (a box row is 128 bytes whatever the swizzle does within it),
 // by `threads` threads, and makes the zeros visible to the tensor cores.
@@ -319,8 +347,8 @@ struct RowsOut {
 // Scales and rounds accumulator chunk c (32 columns from `addr` on) and stores it.
 __device__ __forceinline__ void read_out(const RowsOut& out, int c, uint32_t addr, float f) {
     uint32_t v[32], w[16];
-    tmem_ld32(addr, v);  // warp-collective: every lane loads
-    tmem_wait_ld();
+    warp_tmem_ld32(addr, v);  // warp-collective: every lane loads
+    tmem_loaded(v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack_scaled(v[2 * i], v[2 * i + 1], f);
     out.store(c, w);

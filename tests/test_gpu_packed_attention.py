@@ -247,6 +247,28 @@ def test_a_long_sequence_of_more_ranks_than_shared_memory_counts():
         assert ((lse[:, t].double().cpu() - torch.logsumexp(z, 0) / math.log(2.0)).abs() <= 2.0 ** -9).all()
 
 
+@pytest.mark.parametrize("nh,nkv,d", [(5, 5, 64), (5, 5, 128), (3, 3, 160), (4, 2, 64)])
+def test_ragged_batches_many_times(nh, nkv, d):
+    # long and short documents in turn, more items than SMs: warps that skip items run
+    # ahead of those that do not
+    g = torch.Generator().manual_seed(nh + d)
+    lens = [int(n) for n in torch.randint(0, 400, (70,), generator=g)]
+    cu = _cu(lens)
+    cpu, (q, k, v, do) = _inputs(cu[-1], nh, nkv, d, seed=71)
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    O, lse = binding.tp_attn_packed_forward(q, k, v, cud)
+    _check_forward(O, lse, cpu, cu, d ** -0.5)
+    Or, lr, _ = ref.attention(*cpu[:3], cu, d ** -0.5)
+    o, l32 = Or.to(BF), lr.float()
+    grads = binding.tp_attn_packed_backward(q, k, v, o.cuda(), l32.cuda(), do, cud)
+    _check_backward(grads, cpu, o, l32, cpu[3], cu, d ** -0.5)
+    for _ in range(40):
+        again = binding.tp_attn_packed_forward(q, k, v, cud)
+        assert torch.equal(again[0], O) and torch.equal(again[1], lse)
+        again = binding.tp_attn_packed_backward(q, k, v, o.cuda(), l32.cuda(), do, cud)
+        assert all(torch.equal(a, b) for a, b in zip(again, grads))
+
+
 def test_groups_dealt_to_parts():
     # 64 query heads on 8: the dK/dV kernel's items are few, and each group's heads go to
     # parts whose sums are added behind; gradients into parts of one matrix, tokens
