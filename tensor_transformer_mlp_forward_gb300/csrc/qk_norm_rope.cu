@@ -494,7 +494,9 @@ __global__ void __launch_bounds__(1024)
 
 // Pairs a thread holds, and CTAs an SM: what the registers allow with enough loads in
 // flight (backward: two pairs 64 us, five CTAs, which spill, 62).
-constexpr int kUnitsForward = 4, kUnitsBackward = 1, kPerSmForward = 8, kPerSmBackward = 4;
+template <typename T>
+constexpr int kUnitsForward = sizeof(T) == 4 ? 2 : 4;
+constexpr int kUnitsBackward = 1, kPerSmForward = 8, kPerSmBackward = 4;
 
 int lanes_of(int d) { return d <= 32 ? 2 : d <= 64 ? 4 : d <= 128 ? 8 : 16; }
 
@@ -557,16 +559,16 @@ QkArgs make_args(const QkNormRope& p) {
 }
 
 // Shared memory of `tables` tables of sines and cosines: as many tokens as a run can touch
-// (one head of 256 or two of 32 at least: 35 KB at most).
+// (18 KB at most).
 size_t table_bytes(int run, int heads, int rot, int tables) {
     return sizeof(float) * static_cast<size_t>((run + heads - 2) / heads + 1) * rot * tables;
 }
 
 template <typename T, int LANES>
 cudaError_t forward_as(const QkArgs& a, const QkTurns& turns, cudaStream_t st) {
-    constexpr int run = kUnitsForward * kQkThreads / LANES;
+    constexpr int run = kUnitsForward<T> * kQkThreads / LANES;
     const long long pairs = 1LL * a.T * a.all_heads;
-    return launch_dependent(qk_forward_kernel<T, LANES, kUnitsForward, kPerSmForward>,
+    return launch_dependent(qk_forward_kernel<T, LANES, kUnitsForward<T>, kPerSmForward>,
                             dim3(static_cast<unsigned>((pairs + run - 1) / run)), dim3(kQkThreads),
                             table_bytes(run, a.all_heads, a.rot, 1), st, a, turns);
 }
