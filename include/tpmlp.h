@@ -619,7 +619,7 @@ int tp_attn_backward(const tpmlp_bf16* dY, const tpmlp_bf16* X, const tpmlp_bf16
  * write nothing and set the device status word to TPMLP_ERR_SHAPE.
  *
  * Rules (else TPMLP_ERR_SHAPE): 0 <= nb, T <= 2^30, nh >= 1, nkv >= 1,
- * nh % nkv == 0, d in {64, 96, 128, 160}, scale finite and > 0 (1/sqrt(d) as a
+ * nh % nkv == 0, d in {64, 96, 128, 160}, 0 < scale <= 2e38 (1/sqrt(d) as a
  * rule), (T / 128 + nb) nh < 2^31, T nh <= 2^36.  nb == 0 or T == 0 does nothing.
  * A token's infinities and NaN reach no other sequence; within its own they may
  * reach tokens of its block of 128 that do not see it. */
@@ -662,9 +662,9 @@ int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16
  * tokens ld* values apart (heads * d <= ld* < 2^31, whole 16-byte pieces); gamma_q,
  * gamma_k [d] of that type, shared by the heads; positions int32 [T] (4-byte
  * aligned, any values); rstd float32 [T, nh + nkv] (queries first), saved for
- * the backward pass.  Statistics and rotation are fp32, angles exact to fp32 at
- * any position.  Rules (else TPMLP_ERR_SHAPE): 0 <= T <= 2^30, nh, nkv >= 1,
- * d % 16 == 0, 32 <= d <= 256, rot % 16 == 0, 0 <= rot <= d, 0 < theta <= 1e300,
+ * the backward pass.  Statistics and rotation are fp32, the angles as near as in
+ * 64 bits at any position.  Rules (else TPMLP_ERR_SHAPE): 0 <= T <= 2^30, nh, nkv >= 1,
+ * d % 16 == 0, 32 <= d <= 256, rot % 16 == 0, 0 <= rot <= d, 1 <= theta <= 1e300,
  * eps finite and > 0, T (nh + nkv) <= 2^36. */
 int tp_qk_norm_rope_forward(const void* Q, long long ldq, const void* K, long long ldk,
                             const void* gamma_q, const void* gamma_k, const int* positions, int T,
@@ -693,7 +693,7 @@ int tp_qk_norm_rope_backward(const void* dQo, long long lddqo, const void* dKo, 
 /* ---------------------------------------------------------------------- */
 
 /* n tensors (n <= 2^20): grads[i] points to sizes[i] dense values (0 <= sizes[i]
- * <= 2^40) of type dtypes[i] (tpmlp_dtype) in device memory, aligned to its type
+ * <= 2^40, 2^43 in all) of type dtypes[i] (tpmlp_dtype) in device memory, aligned to its type
  * only (tensors on 16-byte boundaries are the fast ones); the three arrays are
  * host memory and free once the call returns.
  *
@@ -803,8 +803,9 @@ int tpmlp_device_status(void);
 /* Reads and clears the site code of the first bounded wait that gave up on
  * the current device since the last read: 0 if none; otherwise a code that
  * names the kernel and the wait (0x1nn attention forward, 0x2nn attention dQ,
- * 0x3nn attention dK/dV, 0x4nn, 0x5nn and 0x6nn the same of packed attention; the GEMM kernels record none).  Synchronises the
- * device.  A failed read returns minus the status code. */
+ * 0x3nn attention dK/dV, 0x4nn, 0x5nn and 0x6nn the same of packed attention;
+ * the GEMM kernels record none).  Synchronises the device.  A failed read
+ * returns minus the status code. */
 int tpmlp_device_wait_site(void);
 
 /* Number of kernels the last successful call on the calling thread

@@ -1004,6 +1004,21 @@ def _packed_shape(Q, K):
     return T, nh, nkv, d
 
 
+def _sequences(cu_seqlens) -> int:
+    nb = cu_seqlens.numel() - 1
+    if nb > _MOST:
+        _too_large(nb=nb)
+    return nb
+
+
+def _rotated(rot, d: int) -> int:
+    if rot is None:
+        return d
+    if not 0 <= rot <= d:
+        raise ValueError(f"rot must be from 0 to d = {d}, got {rot}")
+    return rot
+
+
 def tp_attn_packed_forward(Q, K, V, cu_seqlens, scale=None, O=None, lse=None, workspace=None, stream=None):
     """O [T, nh, d] (bf16) and lse [nh, T] (float32, log2 domain) of causal
     attention over packed sequences: sequence i owns tokens cu_seqlens[i] to
@@ -1016,7 +1031,7 @@ def tp_attn_packed_forward(Q, K, V, cu_seqlens, scale=None, O=None, lse=None, wo
     qp, ldq = _heads(Q, "Q", (T, nh, d), _BF16, dev)
     kp, ldk = _heads(K, "K", (T, nkv, d), _BF16, dev)
     vp, ldv = _heads(V, "V", (T, nkv, d), _BF16, dev)
-    nb = cu_seqlens.numel() - 1
+    nb = _sequences(cu_seqlens)
     cp = _in(cu_seqlens, "cu_seqlens", (nb + 1,), _I32, dev)
     L = lib()
     with _on(stream):
@@ -1046,7 +1061,7 @@ def tp_attn_packed_backward(Q, K, V, O, lse, dO, cu_seqlens, scale=None, dQ=None
     vp, ldv = _heads(V, "V", ks, _BF16, dev)
     op, dop = _in(O, "O", qs, _BF16, dev), _in(dO, "dO", qs, _BF16, dev)
     lp = _in(lse, "lse", (nh, T), _F32, dev)
-    nb = cu_seqlens.numel() - 1
+    nb = _sequences(cu_seqlens)
     cp = _in(cu_seqlens, "cu_seqlens", (nb + 1,), _I32, dev)
     L = lib()
     with _on(stream):
@@ -1085,7 +1100,7 @@ def tp_qk_norm_rope_forward(Q, K, gamma_q, gamma_k, positions, rot=None, theta: 
         Ko, kop, ldko = _heads_out(Ko, "Ko", ks, dt, dev, Q)
         rstd, rp = _dense_out(rstd, "rstd", (T, nh + nkv), _F32, dev, Q)
     status = lib().tp_qk_norm_rope_forward(
-        qp, ldq, kp, ldk, gq, gk, pp, T, nh, nkv, d, d if rot is None else rot, theta, eps, code, qop, ldqo, kop, ldko,
+        qp, ldq, kp, ldk, gq, gk, pp, T, nh, nkv, d, _rotated(rot, d), theta, eps, code, qop, ldqo, kop, ldko,
         rp, _stream_of(stream, dev))
     if status:
         _check("tp_qk_norm_rope_forward", status)
@@ -1118,7 +1133,7 @@ def tp_qk_norm_rope_backward(dQo, dKo, Q, K, gamma_q, gamma_k, positions, rstd, 
     if partial.numel() < need:
         raise ValueError(f"partial holds {partial.numel()} floats, {need} needed")
     status = L.tp_qk_norm_rope_backward(
-        yq, ldyq, yk, ldyk, qp, ldq, kp, ldk, gq, gk, pp, rp, T, nh, nkv, d, d if rot is None else rot, theta, code,
+        yq, ldyq, yk, ldyk, qp, ldq, kp, ldk, gq, gk, pp, rp, T, nh, nkv, d, _rotated(rot, d), theta, code,
         dqp, lddq, dkp, lddk, dgq, dgk, sp, _stream_of(stream, dev))
     if status:
         _check("tp_qk_norm_rope_backward", status)

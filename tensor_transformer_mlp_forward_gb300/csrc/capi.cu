@@ -2290,7 +2290,7 @@ constexpr long long kMostTokens = 1LL << 30;
 
 int check_packed(int nb, int T, int nh, int nkv, int d, float scale) {
     if (nb < 0 || T < 0 || nb > kMostTokens || T > kMostTokens || nh < 1 || nkv < 1 || nh % nkv != 0 ||
-        !attn_head_dim_ok(d) || !(scale > 0.0f) || scale > 3.0e38f)
+        !attn_head_dim_ok(d) || !(scale > 0.0f) || scale > 2.0e38f)  // times log2(e) in fp32 too
         return TPMLP_ERR_SHAPE;
     if (1LL * nh * d >= (1LL << 31) || (T / 128 + 1LL * nb) * nh >= (1LL << 31) || 1LL * T * nh > (1LL << 36))
         return TPMLP_ERR_SHAPE;
@@ -2437,7 +2437,7 @@ namespace {
 
 int check_qk(int T, int nh, int nkv, int d, int rot, double theta, int dtype) {
     if (T < 0 || T > kMostTokens || nh < 1 || nkv < 1 || d < 32 || d > 256 || d % 16 != 0 || rot < 0 || rot > d ||
-        rot % 16 != 0 || !(theta > 0.0) || theta > 1e300 || (dtype != TPMLP_BF16 && dtype != TPMLP_FP16 && dtype != TPMLP_FP32))
+        rot % 16 != 0 || !(theta >= 1.0) || theta > 1e300 || (dtype != TPMLP_BF16 && dtype != TPMLP_FP16 && dtype != TPMLP_FP32))
         return TPMLP_ERR_SHAPE;
     if ((1LL * nh + nkv) * d >= (1LL << 31) || 1LL * T * (1LL * nh + nkv) > (1LL << 36)) return TPMLP_ERR_SHAPE;
     return TPMLP_OK;
@@ -2523,15 +2523,19 @@ namespace tpmlp {
 namespace {
 
 constexpr int kMostGrads = 1 << 20;
+constexpr long long kMostGradValues = 1LL << 43;  // of all tensors: the kernels count pieces of 32 KB in 32 bits
 
 int check_grads(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes, int n,
                 bool clip) {
     if (n < 0 || n > kMostGrads) return TPMLP_ERR_SHAPE;
     if (n > 0 && (any_null(grads, sizes, dtypes) || (clip && out == nullptr))) return TPMLP_ERR_NULL;
+    long long all = 0;
     for (int i = 0; i < n; ++i) {
         if (sizes[i] < 0 || sizes[i] > (1LL << 40) ||
             (dtypes[i] != TPMLP_BF16 && dtypes[i] != TPMLP_FP16 && dtypes[i] != TPMLP_FP32))
             return TPMLP_ERR_SHAPE;
+        all += sizes[i];
+        if (all > kMostGradValues) return TPMLP_ERR_SHAPE;
         if (sizes[i] == 0) continue;
         if (grads[i] == nullptr || (clip && out[i] == nullptr)) return TPMLP_ERR_NULL;
         const uintptr_t mask = dtypes[i] == TPMLP_FP32 ? 3u : 1u;

@@ -349,16 +349,14 @@ struct Part {
     int grid, partial;  // CTAs, and the first one's partial sum
 };
 
-// The part of the list that starts at tensor `i`: up to kLargeTable tensors and less
-// than 2^31 pieces.
+// The part of the list that starts at tensor `i`: up to kLargeTable tensors (their
+// pieces fit 32 bits: the caller has checked the values of all).
 Part part_at(const long long* sizes, const int* dtypes, int n, int i, int partial) {
     Part p{i, 0, 0u, 0, partial};
     long long pieces = 0;
     for (; i < n && p.count < kLargeTable; ++i, ++p.count) {
         const long long bytes = sizes[i] * (dtypes[i] == TPMLP_FP32 ? 4 : 2);
-        const long long more = (bytes + kPieceBytes - 1) / kPieceBytes;
-        if (p.count > 0 && pieces + more >= (1LL << 31)) break;
-        pieces += more;
+        pieces += (bytes + kPieceBytes - 1) / kPieceBytes;
     }
     p.pieces = static_cast<unsigned>(pieces);
     p.grid = static_cast<int>(pieces < kClipCtas ? pieces : kClipCtas);
@@ -402,10 +400,8 @@ cudaError_t scale(const void* const* in, void* const* out, const long long* size
 }  // namespace
 
 long long grad_partials(int n) {
-    // a part ends at kLargeTable tensors, or where the next tensor would be its
-    // 2^31st piece (64 TB), which no device holds
     const long long parts = (static_cast<long long>(n) + kLargeTable - 1) / kLargeTable;
-    return (parts + 1) * kClipCtas;
+    return (parts > 0 ? parts : 1) * kClipCtas;
 }
 
 cudaError_t launch_grad_clip(const void* const* in, void* const* out, const long long* sizes, const int* dtypes, int n,

@@ -74,7 +74,7 @@ def test_attention_refusals(L):
                                          ldk, P, 256, ws, n, N)
 
     for kw in (dict(nb=-1), dict(T=-1), dict(nh=0), dict(nkv=0), dict(nkv=3), dict(d=80), dict(d=0), dict(sc=0.0),
-               dict(sc=-1.0), dict(sc=NAN), dict(sc=INF), dict(lq=504), dict(lq=516), dict(lk=255), dict(lk=-256),
+               dict(sc=-1.0), dict(sc=NAN), dict(sc=INF), dict(sc=2.5e38), dict(lq=504), dict(lq=516), dict(lk=255), dict(lk=-256),
                dict(T=(1 << 30) + 1), dict(nb=(1 << 30) + 1), dict(nb=1 << 30)):
         assert fwd(**kw) == S, kw
     for kw in (dict(q=N), dict(k=N), dict(cu=N), dict(o=N), dict(lse=N)):
@@ -108,7 +108,7 @@ def test_qk_refusals(L):
 
     for kw in (dict(T=-1), dict(nh=0), dict(nkv=0), dict(d=120, rot=64), dict(d=16, rot=16), dict(d=272), dict(rot=136),
                dict(rot=8), dict(rot=-16), dict(th=0.0), dict(th=NAN), dict(th=INF), dict(eps=0.0), dict(eps=NAN),
-               dict(eps=INF), dict(dt=3), dict(dt=-1), dict(lq=511), dict(lq=516), dict(lk=128), dict(lqo=500)):
+               dict(th=0.5), dict(th=5e-324), dict(eps=INF), dict(dt=3), dict(dt=-1), dict(lq=511), dict(lq=516), dict(lk=128), dict(lqo=500)):
         assert fwd(**kw) == S, kw
     for kw in (dict(q=N), dict(gq=N), dict(pos=N), dict(qo=N), dict(rstd=N)):
         assert fwd(**kw) == NU, kw
@@ -137,6 +137,9 @@ def test_clip_refusals(L):
     assert _clip(L, [a], [b], [-1], [0]) == S
     assert _clip(L, [a], [b], [(1 << 40) + 1], [0]) == S
     assert _clip(L, [a], [b], [8], [3]) == S
+    many = [1 << 40] * 9  # more values than the kernels count pieces of
+    assert L.tp_grad_norm((ctypes.c_void_p * 9)(*[a] * 9), (ctypes.c_longlong * 9)(*many), (ctypes.c_int * 9)(), 9, P, P,
+                          1 << 40, N) == S
     assert _clip(L, [0], [b], [8], [0]) == NU
     assert _clip(L, [a], [0], [8], [0]) == NU
     assert _clip(L, [a], [b], [8], [0], norm=N) == NU
@@ -189,5 +192,12 @@ def test_binding_refusals():
         binding.tp_qk_norm_rope_forward(x, x, x[0, 0], x[0, 0], cu)
     with pytest.raises(ValueError, match="must be bfloat16"):
         binding.tp_qk_norm_rope_forward(x.double(), x, x[0, 0], x[0, 0], cu)
+    for rot in (-16, 80, (1 << 32) + 16):  # the last is 16 in 32 bits
+        with pytest.raises(ValueError, match="rot must be from 0 to d = 64"):
+            binding._rotated(rot, 64)
+    assert [binding._rotated(r, 64) for r in (None, 0, 48, 64)] == [64, 0, 48, 64]
+    huge = torch.empty(1, dtype=torch.int32).expand((1 << 32) + 2)  # 1 sequence in 32 bits
+    with pytest.raises(ValueError, match="nb"):
+        binding._sequences(huge)
     with pytest.raises(ValueError, match="grads\\[0\\] is on cpu"):
         binding.tp_grad_norm([x])
