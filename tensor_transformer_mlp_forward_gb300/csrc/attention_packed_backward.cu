@@ -13,7 +13,11 @@
 //   packed_dq_kernel    items: (128 queries, head); streams the K and V tiles.
 //   packed_dkdv_kernel  items: (128 keys, key/value head); streams the Q and dO
 //                       tiles of every head of the group.
-// P and dS are rounded to bf16 where they become operands of the next product.
+// P and dS are rounded to bf16 where they become operands of the next product, and dS
+// of a sequence's first 128 tokens in two parts, dS = hi + lo, each with a product of its
+// own.  Over many keys the roundings average out; a gradient that is one or two terms (a
+// sequence of two tokens: dQ_1 = dS_10 K_0 + dS_11 K_1) has the whole of one, 2^-8, which
+// made batches of short sequences up to twice as far off as the rounding of the result.
 //
 // Tiles are 128 x 128 (128 x 64 for d = 160, whose accumulators leave tensor memory
 // no more): with N = 128 an MMA of two shared-memory operands reads them at exactly
@@ -177,6 +181,28 @@ __device__ __forceinline__ void score_grads(const uint32_t (&v)[32], const float
         }
         dd[i / 2] = pack_bf16x2(x[0], x[1]);
         dd[i / 2 + 1] = pack_bf16x2(x[2], x[3]);
+    }
+}
+
+// The same in two parts, each packed: dS rounded, and what that leaves.
+template <typename Delta>
+__device__ __forceinline__ void score_grads_two(const uint32_t (&v)[32], const float (&p)[32], Delta neg_dlt, int lo,
+                                                int hi, uint32_t (&dd)[16], uint32_t (&rest)[16]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const ulonglong2 l = neg_dlt(i / 4);
+        float x[4];
+        f32x2_split(mul_f32x2(f32x2(p[i], p[i + 1]), add_f32x2(pair_of(v, i), l.x)), x[0], x[1]);
+        f32x2_split(mul_f32x2(f32x2(p[i + 2], p[i + 3]), add_f32x2(pair_of(v, i + 2), l.y)), x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i + e < lo || i + e >= hi) x[e] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const uint32_t w = pack_bf16x2(x[e], x[e + 1]);
+            dd[(i + e) / 2] = w;
+            rest[(i + e) / 2] = pack_bf16x2(x[e] - __uint_as_float(w << 16), x[e + 1] - __uint_as_float(w & 0xFFFF0000u));
+        }
     }
 }
 
@@ -460,6 +486,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                         tc_fence_after();
                         warp_mma_values<D, BS, HALF>(tmem + C::kDQ, tmem + C::kDQTail, tmem + C::dp(b),
                                       desc_low(smem_u32(sK) + ks.at * C::STREAM, BS * kRowBytes), j > 0);
+                        if (it.q0 == 0)  // dS's second part
+                            warp_mma_values<D, BS, HALF>(tmem + C::kDQ, tmem + C::kDQTail, tmem + C::dp(b) + HALF / 2,
+                                      desc_low(smem_u32(sK) + ks.at * C::STREAM, BS * kRowBytes), true);
                         warp_commit(&ds_used[b]);
                         warp_commit(&k_empty[ks.at]);
                     }
@@ -545,6 +574,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                     if (c >= live) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) dd[i] = 0u;
+                        if (it.q0 == 0) warp_tmem_st16(dp + HALF / 2 + 16 * c, dd);
+                    } else if (it.q0 == 0) {  // the second part goes behind the first of the whole half
+                        uint32_t rest[16];
+                        score_grads_two(v[c], p[c], neg_dlt, 0, c == live - 1 ? lane + 1 : 32, dd, rest);
+                        warp_tmem_st16(dp + HALF / 2 + 16 * c, rest);
                     } else if (c == live - 1) {
                         score_grads<true>(v[c], p[c], neg_dlt, 0, lane + 1, dd);
                     } else {
@@ -784,7 +818,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             // the tile whose gradient product is still to be issued
             int last_q = 0, last_o = 0, last_k = -1;
             uint32_t last_o_phase = 0;
-            bool last_first = false, last_final = false;
+            bool last_first = false, last_final = false, last_two = false;
             auto issue_grad = [&]() {
                 if (last_k < 0 || !ok) return;
                 const uint32_t parity = static_cast<uint32_t>(g - 1) & 1u;
@@ -799,6 +833,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 // dV += P^T dO, dK += dS^T Q
                 const uint32_t rows = first ? smem_u32(sdO) + last_o * C::STREAM : smem_u32(sQ) + last_q * C::STREAM;
                 warp_mma_values<D, BS, HALF>(acc, tail, tile, desc_low(rows, BS * kRowBytes), !last_first);
+                if (last_two)  // dS's second part
+                    warp_mma_values<D, BS, HALF>(acc, tail, tile + HALF / 2, desc_low(rows, BS * kRowBytes), true);
                 warp_commit(first ? &do_empty[last_o] : &q_empty[last_q]);
                 if (last_final) warp_commit(grad_done);
                 last_k = -1;
@@ -811,6 +847,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 __syncwarp();
                 warp_arrive(&item_empty[slot]);
                 if (it.len == 0) break;
+                int i = 0;  // the tile of its head
                 for (int n = 0; n < it.tiles; ++n) {
                     uint64_t* full = first ? &q_full[qs.at] : &do_full[os.at];
                     const uint32_t phase = first ? qs.phase : os.phase;
@@ -837,6 +874,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                     last_k = k;
                     last_first = n == 0;
                     last_final = n == it.tiles - 1;
+                    last_two = !first && (it.i0 + i) * BS < 128;
+                    if (++i == it.nq) i = 0;
                     ++g;
                     qs.next();
                     os.next();
@@ -881,11 +920,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 const int q0 = (it.i0 + i) * BS + w * HALF;  // first query of this half
                 const int valid = it.len - (it.i0 + i) * BS;  // queries of the tile inside the sequence
                 const bool tail = valid < BS;
+                const bool two = (it.i0 + i) * BS < 128;  // dS in two parts
                 // chunks of 32 queries: all of them see the warp's keys (full), none does or
                 // none is inside the sequence (dead), or those in [lo, hi)
                 auto full = [&](int c) { return q0 + 32 * c > first_key && q0 + 32 * c + 32 <= it.len; };
                 auto dead = [&](int c) { return q0 + 32 * c < first_key || q0 + 32 * c >= it.len; };
-                auto lo = [&](int c) { return q0 + 32 * c == first_key ? lane : 0; };
+                auto lo = [&](int c) { return q0 + 32 * c == first_key ? lane : q0 + 32 * c < first_key ? 32 : 0; };
                 auto hi = [&](int c) { return it.len - q0 - 32 * c; };
                 float* stat = stats + ((g & 1) * 2 + w) * 2 * HALF;
                 if (r < 2 * HALF) stat[r] = stat_n;
@@ -939,21 +979,37 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                     break;
                 }
                 tc_fence_after();
+                const uint32_t dp = lane_addr + C::dp(0) + w * HALF;
+                if (two) {
+                    uint32_t rest[HALF / 32][16];
 #pragma unroll
-                for (int c = 0; c < HALF / 32; ++c) {
-                    uint32_t v[32], dd[16];
-                    warp_tmem_ld32(lane_addr + C::dp(0) + w * HALF + 32 * c, v);
-                    tmem_loaded(v);
-                    const ColumnValues neg_dlt{stat + HALF + 32 * c};
-                    if (full(c)) {
-                        score_grads<false>(v, p[c], neg_dlt, 0, 0, dd);
-                    } else if (dead(c)) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) dd[e] = 0u;
-                    } else {
-                        score_grads<true>(v, p[c], neg_dlt, lo(c), hi(c), dd);
+                    for (int c = 0; c < HALF / 32; ++c) {
+                        uint32_t v[32], dd[16];
+                        warp_tmem_ld32(dp + 32 * c, v);
+                        tmem_loaded(v);
+                        score_grads_two(v, p[c], ColumnValues{stat + HALF + 32 * c}, lo(c), hi(c), dd, rest[c]);
+                        warp_tmem_st16(dp + 16 * c, dd);
                     }
-                    warp_tmem_st16(lane_addr + C::dp(0) + w * HALF + 16 * c, dd);
+                    // over the end of the half, which has all been read now
+#pragma unroll
+                    for (int c = 0; c < HALF / 32; ++c) warp_tmem_st16(dp + HALF / 2 + 16 * c, rest[c]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < HALF / 32; ++c) {
+                        uint32_t v[32], dd[16];
+                        warp_tmem_ld32(dp + 32 * c, v);
+                        tmem_loaded(v);
+                        const ColumnValues neg_dlt{stat + HALF + 32 * c};
+                        if (full(c)) {
+                            score_grads<false>(v, p[c], neg_dlt, 0, 0, dd);
+                        } else if (dead(c)) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) dd[e] = 0u;
+                        } else {
+                            score_grads<true>(v, p[c], neg_dlt, lo(c), hi(c), dd);
+                        }
+                        warp_tmem_st16(dp + 16 * c, dd);
+                    }
                 }
                 __syncwarp();
                 tmem_wait_st();

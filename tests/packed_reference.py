@@ -33,10 +33,11 @@ def attention(Q, K, V, cu, scale):
     return O, lse, A
 
 
-def attention_backward(Q, K, V, O, lse, dO, cu, scale):
+def attention_backward(Q, K, V, O, lse, dO, cu, scale, two=False):
     """dQ, dK, dV from the saved O and lse, and a bound of the errors of each: its
     operands P and dS are rounded to bf16 (half a step each), dP, delta and the
-    exponents to fp32 (sums of d <= 160 terms), the result to bf16."""
+    exponents to fp32 (sums of d <= 160 terms), the result to bf16.  two: dS is held
+    in two bf16 parts, of which the second's rounding is 2^-8 of 2^-8 off."""
     Q, K, V, O, dO, lse = (x.double() for x in (Q, K, V, O, dO, lse))
     T, nh, d = Q.shape
     g = nh // K.shape[1]
@@ -50,7 +51,7 @@ def attention_backward(Q, K, V, O, lse, dO, cu, scale):
             delta = (do * O[a:b, j]).sum(1, keepdim=True)
             ds = p * (do @ v.t() - delta)
             # |dS| as rounded, and the fp32 error of dP - delta
-            e = half * ds.abs() + wide * p * (do.abs() @ v.abs().t() + (do * O[a:b, j]).abs().sum(1, keepdim=True))
+            e = (2.0 ** -16 + 2.0 ** -12 if two else half) * ds.abs() + wide * p * (do.abs() @ v.abs().t() + (do * O[a:b, j]).abs().sum(1, keepdim=True))
             out[0][a:b, j] = ds @ k * scale
             tol[0][a:b, j] = e @ k.abs() * scale
             out[1][a:b, j // g] += ds.t() @ q * scale

@@ -269,6 +269,24 @@ def test_ragged_batches_many_times(nh, nkv, d):
         assert all(torch.equal(a, b) for a, b in zip(again, grads))
 
 
+@pytest.mark.parametrize("lens,nh,nkv,d", [([2, 1, 2, 3, 0, 2, 1], 4, 2, 64), ([2], 1, 1, 128), ([5, 2, 9, 64, 127, 128, 3], 6, 2, 96),
+                                           ([2, 4, 65, 128, 1, 100], 3, 3, 160), ([3, 128, 40, 2], 16, 1, 128)])
+def test_short_sequences_keep_dS_in_two_parts(lens, nh, nkv, d):
+    # where a gradient is one or two terms, dS's rounding alone would be as large as the
+    # result's: within 128 tokens of a sequence's start nothing of it may be left
+    cu = _cu(lens)
+    cpu, (q, k, v, do) = _inputs(cu[-1], nh, nkv, d, seed=17 + d)
+    Or, lr, _ = ref.attention(*cpu[:3], cu, d ** -0.5)
+    o, l32 = Or.to(BF), lr.float()
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    got = binding.tp_attn_packed_backward(q, k, v, o.cuda(), l32.cuda(), do, cud)
+    want, tol = ref.attention_backward(*cpu[:3], o, l32, cpu[3], cu, d ** -0.5, two=True)
+    for name, x, w, t in list(zip(("dQ", "dK"), got, want, tol)):
+        err = (x.double().cpu() - w).abs()
+        assert (err <= t).all(), (name, (err - t).max())
+        assert (err.norm() <= 1.1 * (w.to(BF).double() - w).norm() + 2.0 ** -12 * w.norm())
+
+
 def test_groups_dealt_to_parts():
     # 64 query heads on 8: the dK/dV kernel's items are few, and each group's heads go to
     # parts whose sums are added behind; gradients into parts of one matrix, tokens
