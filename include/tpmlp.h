@@ -664,7 +664,7 @@ int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16
  * aligned, any values); rstd float32 [T, nh + nkv] (queries first), saved for
  * the backward pass.  Statistics and rotation are fp32, the angles as near as in
  * 64 bits at any position.  Rules (else TPMLP_ERR_SHAPE): 0 <= T <= 2^30, nh, nkv >= 1,
- * d % 16 == 0, 32 <= d <= 256, rot % 16 == 0, 0 <= rot <= d, 1 <= theta <= 1e300,
+ * d % 16 == 0, 32 <= d <= 256, rot % 16 == 0, 0 <= rot <= d, 1e-300 <= theta <= 1e300,
  * eps finite and > 0, T (nh + nkv) <= 2^36. */
 int tp_qk_norm_rope_forward(const void* Q, long long ldq, const void* K, long long ldk,
                             const void* gamma_q, const void* gamma_k, const int* positions, int T,

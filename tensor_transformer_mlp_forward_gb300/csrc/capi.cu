@@ -2437,7 +2437,7 @@ namespace {
 
 int check_qk(int T, int nh, int nkv, int d, int rot, double theta, int dtype) {
     if (T < 0 || T > kMostTokens || nh < 1 || nkv < 1 || d < 32 || d > 256 || d % 16 != 0 || rot < 0 || rot > d ||
-        rot % 16 != 0 || !(theta >= 1.0) || theta > 1e300 || (dtype != TPMLP_BF16 && dtype != TPMLP_FP16 && dtype != TPMLP_FP32))
+        rot % 16 != 0 || !(theta >= 1e-300) || theta > 1e300 || (dtype != TPMLP_BF16 && dtype != TPMLP_FP16 && dtype != TPMLP_FP32))
         return TPMLP_ERR_SHAPE;
     if ((1LL * nh + nkv) * d >= (1LL << 31) || 1LL * T * (1LL * nh + nkv) > (1LL << 36)) return TPMLP_ERR_SHAPE;
     return TPMLP_OK;

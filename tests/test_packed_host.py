@@ -108,7 +108,7 @@ def test_qk_refusals(L):
 
     for kw in (dict(T=-1), dict(nh=0), dict(nkv=0), dict(d=120, rot=64), dict(d=16, rot=16), dict(d=272), dict(rot=136),
                dict(rot=8), dict(rot=-16), dict(th=0.0), dict(th=NAN), dict(th=INF), dict(eps=0.0), dict(eps=NAN),
-               dict(th=0.5), dict(th=5e-324), dict(eps=INF), dict(dt=3), dict(dt=-1), dict(lq=511), dict(lq=516), dict(lk=128), dict(lqo=500)):
+               dict(th=1e-301), dict(th=5e-324), dict(eps=INF), dict(dt=3), dict(dt=-1), dict(lq=511), dict(lq=516), dict(lk=128), dict(lqo=500)):
         assert fwd(**kw) == S, kw
     for kw in (dict(q=N), dict(gq=N), dict(pos=N), dict(qo=N), dict(rstd=N)):
         assert fwd(**kw) == NU, kw
