@@ -480,9 +480,18 @@ __global__ void __launch_bounds__(1024)
     __shared__ float s[32][33];
     const int x = threadIdx.x % 32, y = threadIdx.x / 32, c = blockIdx.x * 32 + x;
     float v = 0.0f;
-    if (c < 2 * d)
-        for (int i = y + (c < d ? 0 : parts_q); i < (c < d ? parts_q : parts); i += 32)
-            v += partial[static_cast<long long>(i) * d + (c < d ? c : c - d)];
+    if (c < 2 * d) {
+        const float* column = partial + (c < d ? c : c - d);
+        const int end = c < d ? parts_q : parts;
+        // eight parts on their way at a time
+        for (int i = y + (c < d ? 0 : parts_q); i < end; i += 8 * 32) {
+            float w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = i + 32 * k < end ? column[static_cast<long long>(i + 32 * k) * d] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += w[k];
+        }
+    }
     s[y][x] = v;
     __syncthreads();
     v = s[x][y];
