@@ -483,20 +483,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
-            if (!ok || !warp_wait(&o_full[x], static_cast<uint32_t>(taken) & 1u, abort_flag,
-                                          a.status, 0x410 + x)) {
+            if (!ok) break;
+            // while the last P V runs
+            const float inv = 1.0f / l;
+            if (q < it.len) a.lse[head * a.T + it.row0 + q] = m + lg2(l);
+            const RowsOut out(a.O, static_cast<long long>(a.nh) * D, static_cast<long long>(it.row0) + first_q, head * D,
+                              it.len - first_q);
+            if (!warp_wait(&o_full[x], static_cast<uint32_t>(taken) & 1u, abort_flag, a.status, 0x410 + x)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const float inv = 1.0f / l;
-            const bool q_ok = q < it.len;
-            const long long tok = static_cast<long long>(it.row0) + q;
-            const RowsOut out(a.O, static_cast<long long>(a.nh) * D, static_cast<long long>(it.row0) + first_q, head * D,
-                              it.len - first_q);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) read_out(out, c, lane_addr + C::o_chunk(x, c), inv);
-            if (q_ok) a.lse[head * a.T + tok] = m + lg2(l);
             // O_x is in registers or on its way to memory: the MMA may reuse it
             tc_fence_before();
             __syncwarp();
