@@ -34,13 +34,18 @@
 namespace tpmlp {
 namespace {
 
+// 8 softmax warps, the producer's, the MMAs', and one that zeroes V's rows behind the
+// sequences' ends as soon as they land (left to the softmax warps, that waited for V and
+// for its own stores between the scores and P V).
+constexpr int kPackedFwdThreads = 352;
+
 // The Q tiles have two places where they fit (d = 64), so that the next item's are there
 // when the last product of this one is done.
 template <int D>
 struct PackedFwdCfg : FwdCfg<D> {
     using F = FwdCfg<D>;
     static constexpr int QPLACES = 2 * F::FIXED + F::STAGES * F::KVTILE <= 224 * 1024 ? 2 : 1;
-    static constexpr int BARS = 256 + 16;
+    static constexpr int BARS = 384;
     static constexpr int SMEM = 1024 + QPLACES * F::FIXED + F::STAGES * F::KVTILE + BARS;
 };
 
@@ -84,7 +89,7 @@ __device__ __forceinline__ void row_weights(const uint32_t (&v)[32], uint64_t sc
 }
 
 template <int D>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kPackedFwdThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,  // 128-row boxes
                       const __grid_constant__ CUtensorMap tm_k,  // BKV-row boxes
                       const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
@@ -110,7 +115,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t* o_free = o_full + 2;       // [tile] the softmax warps have read O_x out
     uint64_t* item_full = o_free + 2;     // [2]
     uint64_t* item_empty = item_full + 2; // [2]
-    uint64_t* drain = item_empty + 2;
+    uint64_t* v_clean = item_empty + 2;   // [4] V's rows behind the end are zeros (ends in turn)
+    uint64_t* v_issued = v_clean + 4;     // [4] the load of such a V has been started
+    uint64_t* drain = v_issued + 4;
+    static_assert((4 + 2 * S + 12 + 8 + 1) * 8 + 8 * 4 + 8 <= C::BARS, "barrier space");
     int* items = reinterpret_cast<int*>(drain + 1);  // [2] x {first row, length, tile, head}
     uint32_t* misc = reinterpret_cast<uint32_t*>(items + 8);
     volatile uint32_t* abort_flag = misc + 1;
@@ -119,7 +127,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     struct Item {
         int row0, len, n_kv;
         int q0[2], head[2];
-        bool has_b;
+        bool has_b, ends;  // ends: the last key tile reaches behind the sequence's end
         int last[2];  // last key tile each query tile sees
     };
     auto decode = [&](int slot) {
@@ -141,6 +149,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) it.last[x] = (min(it.q0[x] + 128, it.len) - 1) / BKV;
         it.n_kv = it.has_b ? it.last[1] + 1 : it.last[0] + 1;
+        it.ends = it.n_kv * BKV > it.len;
         return it;
     };
 
@@ -159,7 +168,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&o_full[x], 1);
             mbar_init(&o_free[x], 4);
             mbar_init(&item_full[x], 1);
-            mbar_init(&item_empty[x], 9);  // the MMA thread and the 8 softmax warps
+            mbar_init(&item_empty[x], 10);  // the MMA thread, the 8 softmax warps and V's
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&v_clean[i], 1);
+            mbar_init(&v_issued[i], 1);
         }
         mbar_init(drain, 1);
         misc[1] = 0u;
@@ -186,6 +199,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             int q_loads = 0;
+            unsigned ends = 0;
             bool ok = true;
             for (int k = 0;; ++k) {
                 const int slot = k & 1;
@@ -240,6 +254,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                 }
                 if (!ok) break;
+                if (it.ends) mbar_arrive(&v_issued[ends++ % 4]);
             }
             for (int k = q_loads > QP ? q_loads - QP : 0; k < q_loads; ++k)
                 wait_drain(&q_full[k % QP], static_cast<uint32_t>(k / QP) & 1u, a.status, 0x402);
@@ -261,6 +276,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     rphase ^= 1u;
                 }
             };
+            unsigned ends = 0;  // items so far whose V has rows behind the end
             int s_left = 0;  // S MMAs of the item still to issue
             int qp = 0;      // where the item's Q tiles lie
             auto issue_s = [&](int x, int stage) {  // S_x = Q_x K^T
@@ -313,9 +329,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     next();
                     const bool more = j + 1 < it.n_kv;
                     const int kn = rstage;
-                    ok = more ? warp_wait_both(&kv_full[vs], vp, &kv_full[kn], rphase, abort_flag, a.status, 0x408)
-                              : warp_wait(&kv_full[vs], vp, abort_flag, a.status, 0x409);
-                    if (more) next();
+                    if (more) {
+                        ok = warp_wait_both(&kv_full[vs], vp, &kv_full[kn], rphase, abort_flag, a.status, 0x408);
+                        next();
+                    } else if (it.ends) {
+                        // (warp 10 is at most two items ahead: four barriers tell its ends apart)
+                        ok = warp_wait_both(&kv_full[vs], vp, &v_clean[ends % 4], ends / 4 & 1u, abort_flag, a.status,
+                                            0x409);
+                        ++ends;
+                    } else {
+                        ok = warp_wait(&kv_full[vs], vp, abort_flag, a.status, 0x409);
+                    }
                     if (!ok) break;
                     if (j <= it.last[0]) {
                         wait_p(0, j);
@@ -345,6 +369,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) wait_drain(drain, 0, a.status, 0x40B);
         }
         __syncwarp();
+    } else if (warp == 10) {
+        // -------------------- zeroes of V's rows behind the sequences' ends
+        unsigned ends = 0, ring_at = 0;  // of the items so far
+        for (int k = 0;; ++k) {
+            const int slot = k & 1;
+            if (!warp_wait(&item_full[slot], static_cast<uint32_t>(k >> 1) & 1u, abort_flag, a.status, 0x417)) break;
+            const Item it = decode(slot);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[slot]);
+            if (it.len == 0) break;
+            ring_at += 2u * static_cast<unsigned>(it.n_kv);
+            if (!it.ends) continue;
+            const unsigned v_at = ring_at - 1u;  // the last V
+            const int vs = static_cast<int>(v_at % S);
+            // its load first: from then on the slot is in V's phase, and stays in it until
+            // V is used, for which this warp's word is needed
+            if (!warp_wait(&v_issued[ends % 4], ends / 4 & 1u, abort_flag, a.status, 0x418) ||
+                !warp_wait(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414))
+                break;
+            zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - (it.n_kv - 1) * BKV, lane, 32);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_clean[ends % 4]);
+            ++ends;
+        }
+        __syncwarp();
     } else {
         // -------------------------------------------------- softmax warps
         const int x = warp >> 2;               // tile: 0 = A, 1 = B
@@ -353,7 +402,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t s_addr = lane_addr + C::s_col(x);
         int gxl = 0;  // this tile's S / P V MMAs over the items so far
         int taken = 0;         // items this tile has taken part in
-        unsigned ring_at = 0;  // ring entries of the items so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int slot = k & 1;
@@ -364,8 +412,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             if (it.len == 0) break;
-            const unsigned ring0 = ring_at;  // ring entry of the item's K_0
-            ring_at += 2u * static_cast<unsigned>(it.n_kv);
             if (x == 1 && !it.has_b) continue;  // no B tile in this item
             const int first_q = (x ? it.q0[1] : it.q0[0]) + (warp & 3) * 32;  // the warp's
             const int q = first_q + lane;
@@ -465,18 +511,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         tmem_wait_st();
                     }
                 }
-                // V rows behind the sequence's end.  (S of this tile is there, so every load up
-                // to its K has landed and V's phase is the next of its slot: before S, a
-                // warpgroup that has skipped items could take an older phase for it.)
-                if (k0 + BKV > it.len) {
-                    const unsigned v_at = ring0 + 2u * static_cast<unsigned>(j) + 1u;
-                    const int vs = static_cast<int>(v_at % S);
-                    if (!warp_wait(&kv_full[vs], (v_at / S) & 1u, abort_flag, a.status, 0x414)) {
-                        ok = false;
-                        break;
-                    }
-                    zero_rows<C::NB>(smem_u32(ring) + vs * C::KVTILE, BKV, it.len - k0, r, 128);
-                }
                 __syncwarp();
                 tmem_wait_st();
                 tc_fence_before();
@@ -523,7 +557,7 @@ cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtenso
                        unsigned grid, cudaStream_t st) {
     const cudaError_t e = allow_shared<packed_fwd_kernel<D>>(PackedFwdCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(packed_fwd_kernel<D>, dim3(grid), dim3(kFwdThreads), PackedFwdCfg<D>::SMEM, st, q, k, v, a);
+    return launch_dependent(packed_fwd_kernel<D>, dim3(grid), dim3(kPackedFwdThreads), PackedFwdCfg<D>::SMEM, st, q, k, v, a);
 }
 
 }  // namespace
