@@ -22,7 +22,8 @@
 // Long sequences are bound by the tensor cores and the softmax between their products
 // (16384 tokens, 16 heads on 2 of 128: 661-690 us, 1600-1660 TFLOP/s), short ones by an
 // item's chain of load, S, softmax, P V and store (8 x 1024 tokens, 32 heads on 8 of 128:
-// 70-73 us; 37 sequences in 8191 tokens, 20 heads of 64: 46-48 us).
+// 70.5 us; 37 sequences in 8191 tokens, 20 heads of 64: 48 us).  For the latter neither a
+// deeper ring (50.9 against 49.3 us) nor a second place for O (49.7 against 48.6) helped.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,8 +36,8 @@ namespace tpmlp {
 namespace {
 
 // 8 softmax warps, the producer's, the MMAs', and one that zeroes V's rows behind the
-// sequences' ends as soon as they land (left to the softmax warps, that waited for V and
-// for its own stores between the scores and P V).
+// sequences' ends as soon as they land (left to the softmax warps, that was a wait for V
+// and for stores between the scores and P V: 72.4 us for 8 x 1024 tokens against 70.5).
 constexpr int kPackedFwdThreads = 352;
 
 // The Q tiles have two places where they fit (d = 64), so that the next item's are there
@@ -397,7 +398,6 @@ __global__ void __launch_bounds__(kPackedFwdThreads, 1)
     } else {
         // -------------------------------------------------- softmax warps
         const int x = warp >> 2;               // tile: 0 = A, 1 = B
-        const int r = threadIdx.x & 127;       // row of the tile = TMEM lane
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t s_addr = lane_addr + C::s_col(x);
         int gxl = 0;  // this tile's S / P V MMAs over the items so far
