@@ -1,0 +1,51 @@
+"""Packed attention at the ends of what its inputs may hold (GB300)."""
+
+import math
+
+import pytest
+import torch
+
+from tensor_transformer_mlp_forward_gb300 import binding
+from tests import packed_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+# scores of -inf in whole key tiles (128 keys, 64 at d = 160): of keys that are -inf, and of
+# finite ones whose products leave fp32 (in 64 bits they are finite and weigh nothing)
+@pytest.mark.parametrize("fill", [-math.inf, -3e38])
+@pytest.mark.parametrize("nh,nkv,d,n", [(4, 2, 64, 128), (3, 3, 64, 256), (2, 1, 128, 256), (3, 1, 96, 130), (5, 5, 128, 128),
+                                        (4, 2, 160, 64), (3, 3, 160, 200)])
+def test_first_keys_of_no_weight(nh, nkv, d, n, fill):
+    cu, T = [0, 37, 457, 462], 462
+    g = torch.Generator().manual_seed(n + d)
+    q = (torch.randn(T, nh, d, generator=g).abs() + 0.1).to(BF)  # every product with `fill` has its sign
+    k, v = (torch.randn(T, nkv, d, generator=g).to(BF) for _ in range(2))
+    do = torch.randn(T, nh, d, generator=g).to(BF)
+    k[cu[1]:cu[1] + n] = fill
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    O, lse = binding.tp_attn_packed_forward(q.cuda(), k.cuda(), v.cuda(), cud)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    rows = torch.ones(T, dtype=torch.bool)
+    rows[cu[1]:cu[1] + n] = False  # these see no other keys
+    Or, lr, A = ref.attention(q, k, v, cu, d ** -0.5)
+    Or, lr, A = Or[rows], lr[:, rows], A[rows]
+    assert torch.isfinite(Or).all() and torch.isfinite(lr).all()
+    # P rounded to bf16, O rounded to bf16, exponents of sums of d <= 160 terms in fp32:
+    # d 2^-24 times sum |q k| scale log2(e) < 24 is below 2^-12
+    tol = 2.0 ** -8 * (1 + 2.0 ** -6) * (A + Or.abs()) + 2.0 ** -11 * A
+    assert ((O.double().cpu()[rows] - Or).abs() <= tol).all()
+    assert ((lse.double().cpu()[:, rows] - lr).abs() <= 2.0 ** -11 + 2.0 ** -21 * lr.abs()).all()
+    if fill == -math.inf:
+        # rows without a finite score have no softmax
+        assert torch.isnan(O.cpu()[~rows].float()).all()
+        return
+    # dQ of the other rows (dK and dV sum over all of them)
+    Oall, lall, _ = ref.attention(q, k, v, cu, d ** -0.5)
+    o, l32 = Oall.to(BF), lall.float()
+    dQ, _, _ = binding.tp_attn_packed_backward(q.cuda(), k.cuda(), v.cuda(), o.cuda(), l32.cuda(), do.cuda(), cud)
+    (want, _, _), (t, _, _) = ref.attention_backward(q, k, v, o, l32, do, cu, d ** -0.5)
+    assert torch.isfinite(want[rows]).all()
+    assert ((dQ.double().cpu() - want).abs() <= t)[rows].all()
