@@ -796,7 +796,7 @@ int tpmlp_last_cuda_error(void);
 /* Reads and clears the device status word of the current device: TPMLP_OK,
  * TPMLP_ERR_DEVICE_TIMEOUT if a bounded wait in a kernel gave up since the last
  * read, or TPMLP_ERR_SHAPE if the offsets of a packed batch were out of order or
- * range.  Synchronises the device. Returns TPMLP_ERR_LAUNCH if the read
+ * range (a timeout goes before that).  Synchronises the device. Returns TPMLP_ERR_LAUNCH if the read
  * itself fails. */
 int tpmlp_device_status(void);
 

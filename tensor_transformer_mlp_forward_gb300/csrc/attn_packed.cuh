@@ -74,7 +74,7 @@ __device__ __forceinline__ void plan_block(const int* __restrict__ cu, int nb, i
     if (s_bad) {
         if (tid == 0) {
             head[kPlanWork0] = head[kPlanWork1] = head[kPlanCount] = 0u;
-            atomicExch(status, kStatusShape);
+            atomicCAS(status, 0, kStatusShape);  // a timeout that nobody has read yet stays
         }
         return;
     }

@@ -49,3 +49,16 @@ def test_first_keys_of_no_weight(nh, nkv, d, n, fill):
     (want, _, _), (t, _, _) = ref.attention_backward(q, k, v, o, l32, do, cu, d ** -0.5)
     assert torch.isfinite(want[rows]).all()
     assert ((dQ.double().cpu() - want).abs() <= t)[rows].all()
+
+
+def test_bad_offsets_leave_an_earlier_timeout():
+    x = torch.zeros(100, 2, 64, dtype=BF, device="cuda")
+    bad = torch.tensor([0, 50, 40, 90], dtype=torch.int32, device="cuda")
+    assert binding.device_status() == binding.TPMLP_OK
+    # a wait that gives up after 2 ms, whose status is not read
+    assert binding.lib().tpmlp_selftest_bounded_wait(2000, torch.cuda.current_stream().cuda_stream) == binding.TPMLP_OK
+    binding.tp_attn_packed_forward(x, x, x, bad)
+    assert binding.device_status() == binding.TPMLP_ERR_DEVICE_TIMEOUT
+    binding.tp_attn_packed_forward(x, x, x, bad)
+    assert binding.device_status() == binding.TPMLP_ERR_SHAPE
+    assert binding.device_status() == binding.TPMLP_OK
