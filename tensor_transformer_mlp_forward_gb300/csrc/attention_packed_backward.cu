@@ -89,6 +89,8 @@ struct BwdArgs {
     unsigned* plan;
     int nh, nkv, group;
     int split;           // parts of a group's heads (dK/dV kernel)
+    int part_heads;      // a part's heads; the first part_more parts have one more
+    int part_more;
     float* parts;        // [split][T][nkv][dV, dK][d] where split > 1
     long long T;
     float scale, scale2;
@@ -669,10 +671,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         it.k0 = p[2] * 128;
         it.kv_head = p[3] / a.split;
         it.part = p[3] - it.kv_head * a.split;
-        it.head = it.kv_head * a.group + it.part * (a.group / a.split);
+        it.head = it.kv_head * a.group + it.part * a.part_heads + min(it.part, a.part_more);
         it.i0 = it.k0 / BS;                         // first query tile that sees the keys
         it.nq = (it.len + BS - 1) / BS - it.i0;     // query tiles of each head
-        it.tiles = it.nq * (a.group / a.split);
+        it.tiles = it.nq * (a.part_heads + (it.part < a.part_more));
         return it;
     };
 
@@ -1142,14 +1144,19 @@ cudaError_t launch_bwd(const CUtensorMap& q128, const CUtensorMap& do128, const 
 // groups of 16 heads of 128 on one key/value head took 250 us (8 x 1024 tokens) and
 // 1688 us (one sequence of 8192), in parts 144 and 585; two parts where the items were
 // 256 cost 15 % at 8 x 1024 tokens (their sums go through memory) and gained 5 % at 8192.
-// The sums are at most some 100 MB, whatever T.
+// Parts of one size where less than twice as many give that, and their sums stay in
+// bounds: split T nkv <= kPartRows, 75 MB at d = 160, which the fewest parts always
+// keep ((items + wanted - 1) / items parts of 128 items rows, items < wanted).
 int packed_attn_split(int nb, int T, int nh, int nkv) {
-    constexpr long long wanted = 3 * 152 / 2;
+    constexpr long long wanted = 3 * 152 / 2, kPartRows = 2 * wanted * 128;
     const int group = nh / nkv;
     const long long items = ((static_cast<long long>(T) + 127) / 128 + nb / 2) * nkv;  // half a tile each lost to ends
-    for (int s = 1; s < group; ++s)
-        if (group % s == 0 && items * s >= wanted) return s;
-    return group;
+    if (items >= wanted) return 1;
+    const int fewest = static_cast<int>((wanted + items - 1) / items);
+    if (fewest >= group) return group;
+    for (int s = fewest; s < 2 * fewest && s <= group; ++s)
+        if (group % s == 0 && 1LL * s * T * nkv <= kPartRows) return s;
+    return fewest;
 }
 
 int packed_attn_stream_rows(int d) { return d <= 128 ? 128 : 64; }
@@ -1170,6 +1177,8 @@ cudaError_t launch_packed_backward(const CUtensorMap& q128, const CUtensorMap& d
     a.lse = p.lse_in;
     a.delta = p.delta;
     a.split = packed_attn_split(p.nb, p.T, p.nh, p.nkv);
+    a.part_heads = a.group / a.split;
+    a.part_more = a.group % a.split;
     a.parts = p.parts;
     a.dQ = p.dQ;
     a.dK = p.dK;

@@ -62,3 +62,36 @@ def test_bad_offsets_leave_an_earlier_timeout():
     binding.tp_attn_packed_forward(x, x, x, bad)
     assert binding.device_status() == binding.TPMLP_ERR_SHAPE
     assert binding.device_status() == binding.TPMLP_OK
+
+
+def _cu(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+# groups of 5, 7 and 13 heads in 2 and 6 parts, of unequal size
+@pytest.mark.parametrize("nb,nh,nkv,d", [(20, 40, 8, 64), (40, 21, 3, 128), (40, 13, 1, 160), (40, 13, 1, 96)])
+def test_groups_dealt_to_unequal_parts(nb, nh, nkv, d):
+    g = torch.Generator().manual_seed(nh + d)
+    lens = [int(n) for n in torch.randint(0, 130, (nb,), generator=g)]
+    cu = _cu(lens)
+    T = cu[-1] + 3
+    q, k, v, do = (torch.randn(T, n, d, generator=g).to(BF) for n in (nh, nkv, nkv, nh))
+    Or, lr, _ = ref.attention(q, k, v, cu, d ** -0.5)
+    o, l32 = Or.to(BF), lr.float()
+    gpu = [x.cuda() for x in (q, k, v, o, l32, do)]
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    out = [torch.full((T, n, d), 7.0, dtype=BF, device="cuda") for n in (nh, nkv, nkv)]
+    got = binding.tp_attn_packed_backward(*gpu, cud, dQ=out[0], dK=out[1], dV=out[2])
+    assert binding.last_launch_count() == 4  # delta and plan, dQ, dK and dV, parts
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    want, tol = ref.attention_backward(q, k, v, o, l32, do, cu, d ** -0.5)
+    for name, x, w, t in zip(("dQ", "dK", "dV"), got, want, tol):
+        err = (x.double().cpu() - w).abs()[:cu[-1]]
+        assert (err <= t[:cu[-1]]).all(), (name, (err - t[:cu[-1]]).max())
+        assert (x[cu[-1]:] == 7.0).all()
+    again = binding.tp_attn_packed_backward(*gpu, cud)
+    assert all(torch.equal(a[:cu[-1]], b[:cu[-1]]) for a, b in zip(got, again))

@@ -1,0 +1,29 @@
+"""The scratch of packed attention and of the norms and rotation over all batches, on a
+host without a GPU."""
+
+import pytest
+
+from tensor_transformer_mlp_forward_gb300 import binding, build
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return binding.lib()
+
+
+def _base(nb, T, nh):
+    """The plan and delta."""
+    return 16 * (T // 128 + nb) + 4 * (T // 128 + 2) + 4 * T * nh + 2048
+
+
+@pytest.mark.parametrize("nkv", [1, 2, 3, 4, 8, 16])
+@pytest.mark.parametrize("group", [2, 3, 4, 5, 7, 8, 13, 16, 17, 71, 113])
+def test_parts_scratch_is_bounded_for_every_group(L, group, nkv):
+    # the parts' fp32 sums: at most 2 * 228 * 128 rows of dK and dV
+    d = 160
+    for tiles in sorted({1, 2, 7, 30, 57, 75, 76, 113, 114, 200, 226, 227, 228, 300}):
+        for T in (128 * (tiles // nkv + 1) - 1, 128 * max(tiles // nkv, 1)):
+            for nb in (1, 2, 30):
+                need = L.tp_attn_packed_backward_workspace_bytes(nb, T, group * nkv, nkv, d)
+                assert need <= _base(nb, T, group * nkv) + 2 * 228 * 128 * 2 * d * 4, (nb, T)
