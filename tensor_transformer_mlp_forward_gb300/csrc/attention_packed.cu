@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kPackedFwdThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) rs2[kk] = 0ull;  // (0.0f, 0.0f)
                 // (a row whose scores so far are all -inf: weights of 0, not of -inf + inf)
-                const float from = m == -INFINITY ? 0.0f : m;
+                const float from = fmaxf(m, -3.4e38f);
                 const uint64_t scale2 = f32x2(a.scale2, a.scale2), neg_m = f32x2(-from, -from);
                 // P_x, packed bf16, over the first columns of S_x (already read)
                 if (live > SCH) {
