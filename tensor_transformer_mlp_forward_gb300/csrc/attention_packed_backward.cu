@@ -1151,7 +1151,7 @@ int packed_attn_split(int nb, int T, int nh, int nkv) {
     constexpr long long wanted = 3 * 152 / 2, kPartRows = 2 * wanted * 128;
     const int group = nh / nkv;
     const long long items = ((static_cast<long long>(T) + 127) / 128 + nb / 2) * nkv;  // half a tile each lost to ends
-    if (items >= wanted) return 1;
+    if (items >= wanted || items == 0) return 1;
     const int fewest = static_cast<int>((wanted + items - 1) / items);
     if (fewest >= group) return group;
     for (int s = fewest; s < 2 * fewest && s <= group; ++s)

@@ -27,3 +27,10 @@ def test_parts_scratch_is_bounded_for_every_group(L, group, nkv):
             for nb in (1, 2, 30):
                 need = L.tp_attn_packed_backward_workspace_bytes(nb, T, group * nkv, nkv, d)
                 assert need <= _base(nb, T, group * nkv) + 2 * 228 * 128 * 2 * d * 4, (nb, T)
+
+
+@pytest.mark.parametrize("nb", [0, 1, 2, 9])
+def test_scratch_of_no_tokens(L, nb):
+    assert 0 < L.tp_attn_packed_backward_workspace_bytes(nb, 0, 8, 2, 128) < 1 << 20
+    assert 0 < L.tp_attn_packed_forward_workspace_bytes(nb, 0, 8, 2, 128) < 1 << 20
+    assert L.tp_qk_norm_rope_backward_workspace_floats(0, 8, 2, 128) == 0
