@@ -625,7 +625,9 @@ int tp_attn_backward(const tpmlp_bf16* dY, const tpmlp_bf16* X, const tpmlp_bf16
  * reach tokens of its block of 128 that do not see it. */
 
 /* Bytes of scratch tp_attn_packed_forward needs (contents on entry do not
- * matter): the list of work items that the call makes on its stream. */
+ * matter): the list of work items that the call makes on its stream.  What a batch
+ * needs serves every batch of no more sequences and tokens too (for the backward
+ * pass as well), so a program may size it for its largest. */
 size_t tp_attn_packed_forward_workspace_bytes(int nb, int T, int nh, int nkv, int d);
 
 int tp_attn_packed_forward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16* K, long long ldk,

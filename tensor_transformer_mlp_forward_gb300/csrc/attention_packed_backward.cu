@@ -1146,17 +1146,26 @@ cudaError_t launch_bwd(const CUtensorMap& q128, const CUtensorMap& do128, const 
 // 256 cost 15 % at 8 x 1024 tokens (their sums go through memory) and gained 5 % at 8192.
 // Parts of one size where less than twice as many give that, and their sums stay in
 // bounds: split T nkv <= kPartRows, 75 MB at d = 160, which the fewest parts always
-// keep ((items + wanted - 1) / items parts of 128 items rows, items < wanted).
+// keep ((items + kPartItems - 1) / items parts of 128 items rows, items < kPartItems).
+constexpr long long kPartItems = 3 * 152 / 2, kPartRows = 2 * kPartItems * 128;
+
 int packed_attn_split(int nb, int T, int nh, int nkv) {
-    constexpr long long wanted = 3 * 152 / 2, kPartRows = 2 * wanted * 128;
     const int group = nh / nkv;
     const long long items = ((static_cast<long long>(T) + 127) / 128 + nb / 2) * nkv;  // half a tile each lost to ends
-    if (items >= wanted || items == 0) return 1;
-    const int fewest = static_cast<int>((wanted + items - 1) / items);
+    if (items >= kPartItems || items == 0) return 1;
+    const int fewest = static_cast<int>((kPartItems + items - 1) / items);
     if (fewest >= group) return group;
     for (int s = fewest; s < 2 * fewest && s <= group; ++s)
         if (group % s == 0 && 1LL * s * T * nkv <= kPartRows) return s;
     return fewest;
+}
+
+int packed_attn_parts_tokens(int nh, int nkv) {
+    return nh == nkv ? 0 : static_cast<int>((kPartItems - 1) / nkv * 128);
+}
+
+long long packed_attn_parts_rows(int T, int nh) {
+    return 1LL * T * nh < kPartRows ? 1LL * T * nh : kPartRows;
 }
 
 int packed_attn_stream_rows(int d) { return d <= 128 ? 128 : 64; }

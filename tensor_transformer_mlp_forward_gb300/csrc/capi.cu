@@ -2302,24 +2302,31 @@ bool row_stride_ok(long long ld, long long cols, int multiple) {
 }
 
 // Header words, entries, ranks; behind them the backward pass's delta and the sums of
-// parts of a group's heads.
+// parts of a group's heads.  The fewer tokens, the more parts: the backward pass's total
+// is what the neediest batch of up to nb sequences and T tokens takes, so that scratch for
+// a program's largest batch serves all of them.
 struct PackedLayout {
     size_t entries, ranks, delta, parts, total;
 };
 
 PackedLayout packed_layout(int nb, int T, int nh, int nkv, int d, bool backward) {
-    const size_t tiles = static_cast<size_t>(T) / 128;
-    PackedLayout L;
-    L.entries = 256;
-    L.ranks = align256(L.entries + sizeof(int4) * (tiles + nb));
-    L.delta = align256(L.ranks + sizeof(int) * (tiles + 2));
-    if (!backward) {
-        L.total = L.delta;
+    auto front = [&](int tokens) {
+        const size_t tiles = static_cast<size_t>(tokens) / 128;
+        PackedLayout L;
+        L.entries = 256;
+        L.ranks = align256(L.entries + sizeof(int4) * (tiles + nb));
+        L.delta = align256(L.ranks + sizeof(int) * (tiles + 2));
+        L.parts = align256(L.delta + sizeof(float) * static_cast<size_t>(tokens) * nh);
         return L;
+    };
+    PackedLayout L = front(T);
+    L.total = backward ? L.parts : L.delta;
+    if (!backward) return L;
+    const int most = std::min(T, packed_attn_parts_tokens(nh, nkv));  // with parts
+    if (most > 0) {
+        const size_t rows = static_cast<size_t>(packed_attn_parts_rows(most, nh));
+        L.total = std::max(L.total, front(most).parts + align256(sizeof(float) * 2 * d * rows));
     }
-    const size_t split = static_cast<size_t>(packed_attn_split(nb, T, nh, nkv));
-    L.parts = align256(L.delta + sizeof(float) * static_cast<size_t>(T) * nh);
-    L.total = L.parts + (split > 1 ? align256(sizeof(float) * split * T * nkv * 2 * d) : 0);
     return L;
 }
 

@@ -225,6 +225,10 @@ cudaError_t launch_packed_forward(const CUtensorMap& q, const CUtensorMap& k, co
 // the dK/dV kernel (the other operands' boxes have 128).
 int packed_attn_stream_rows(int d);
 int packed_attn_split(int nb, int T, int nh, int nkv);
+// Bounds of the parts for batches of any sequences: the most tokens with which a group
+// is dealt to more than one, and the most rows (split T nkv) with up to T tokens.
+int packed_attn_parts_tokens(int nh, int nkv);
+long long packed_attn_parts_rows(int T, int nh);
 cudaError_t launch_packed_backward(const CUtensorMap& q128, const CUtensorMap& do128, const CUtensorMap& k128,
                                    const CUtensorMap& v128, const CUtensorMap& q_stream,
                                    const CUtensorMap& do_stream, const CUtensorMap& k_stream,

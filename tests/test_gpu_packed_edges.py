@@ -95,3 +95,28 @@ def test_groups_dealt_to_unequal_parts(nb, nh, nkv, d):
         assert (x[cu[-1]:] == 7.0).all()
     again = binding.tp_attn_packed_backward(*gpu, cud)
     assert all(torch.equal(a[:cu[-1]], b[:cu[-1]]) for a, b in zip(got, again))
+
+
+def test_scratch_of_the_largest_batch_serves_the_smaller_ones():
+    nh, nkv, d = 16, 4, 160
+    need = binding.lib().tp_attn_packed_backward_workspace_bytes(23, 6007, nh, nkv, d)
+    room = torch.full((need + 4096,), 90, dtype=torch.uint8, device="cuda")
+    for nb, T in ((23, 6007), (10, 6007), (10, 5000), (1, 3000), (2, 1)):
+        g = torch.Generator(device="cuda").manual_seed(T)
+        q, k, v, do = (torch.randn(T, n, d, generator=g, device="cuda").to(BF) for n in (nh, nkv, nkv, nh))
+        cu = (torch.arange(nb + 1, device="cuda") * T // nb).int()
+        O, lse = binding.tp_attn_packed_forward(q, k, v, cu, workspace=room[:need])
+        a = binding.tp_attn_packed_backward(q, k, v, O, lse, do, cu, workspace=room[:need])
+        b = binding.tp_attn_packed_backward(q, k, v, O, lse, do, cu)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert (room[need:] == 90).all() and binding.device_status() == 0
+    with pytest.raises(binding.TpMlpError):
+        binding.tp_attn_packed_backward(q, k, v, O, lse, do, cu, workspace=room[:64])
+
+
+def test_a_batch_without_tokens():
+    e = torch.empty(0, 4, 64, dtype=BF, device="cuda")
+    cu = torch.zeros(2, dtype=torch.int32, device="cuda")
+    O, lse = binding.tp_attn_packed_forward(e, e[:, :2], e[:, :2], cu)
+    dQ, dK, dV = binding.tp_attn_packed_backward(e, e[:, :2], e[:, :2], O, lse, e, cu)
+    assert dQ.shape == (0, 4, 64) and dK.shape == dV.shape == (0, 2, 64)

@@ -34,3 +34,22 @@ def test_scratch_of_no_tokens(L, nb):
     assert 0 < L.tp_attn_packed_backward_workspace_bytes(nb, 0, 8, 2, 128) < 1 << 20
     assert 0 < L.tp_attn_packed_forward_workspace_bytes(nb, 0, 8, 2, 128) < 1 << 20
     assert L.tp_qk_norm_rope_backward_workspace_floats(0, 8, 2, 128) == 0
+
+
+@pytest.mark.parametrize("nh,nkv,d", [(16, 4, 160), (32, 8, 128), (16, 1, 64), (28, 4, 128), (71, 1, 64), (20, 20, 64),
+                                      (456, 228, 64), (454, 227, 64)])
+def test_scratch_never_shrinks_with_the_batch(L, nh, nkv, d):
+    # a program that sizes its scratch for its largest batch may run any smaller one
+    Ts = sorted({0, 1, 127, 128, 129, 1000, 2000, 3585, 5000, 6007, 7295, 7296, 7297, 8191, 8192, 14591, 14592, 14593,
+                 29055, 29056, 29057, 29183, 29184, 29185, 40000, 1 << 17, 1 << 20})
+    nbs = [1, 2, 3, 7, 10, 23, 57, 100, 300, 455, 456, 457, 5000]
+    for f in (lambda nb, T: L.tp_attn_packed_forward_workspace_bytes(nb, T, nh, nkv, d),
+              lambda nb, T: L.tp_attn_packed_backward_workspace_bytes(nb, T, nh, nkv, d)):
+        for nb in nbs:
+            sizes = [f(nb, T) for T in Ts]
+            assert sizes == sorted(sizes), nb
+        for T in Ts:
+            sizes = [f(nb, T) for nb in nbs]
+            assert sizes == sorted(sizes), T
+    sizes = [L.tp_qk_norm_rope_backward_workspace_floats(T, nh, nkv, d) for T in Ts]
+    assert sizes == sorted(sizes)
