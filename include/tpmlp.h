@@ -701,8 +701,8 @@ int tp_qk_norm_rope_backward(const void* dQo, long long lddqo, const void* dKo, 
  *
  *   norm = sqrt(sum over all tensors and values of g^2)     (float32, device)
  *
- * The sum runs in a fixed order.  Squares above the float32 range are kept in
- * range; a norm below 2^-63 may read as less than it is.  An infinite or NaN
+ * The sum runs in a fixed order.  Squares outside the float32 range are kept in
+ * range, so the norm may lie anywhere in it.  An infinite or NaN
  * gradient gives an infinite or NaN norm.  workspace: tp_grad_workspace_bytes(n)
  * bytes, 16-byte aligned. */
 size_t tp_grad_workspace_bytes(int n);

@@ -2588,12 +2588,12 @@ int check_outputs_apart(const void* const* grads, void* const* out, const long l
 int grad_clip(const void* const* grads, void* const* out, const long long* sizes, const int* dtypes, int n,
               float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
     if (any_null(norm)) return TPMLP_ERR_NULL;
-    if (workspace == nullptr || workspace_bytes < sizeof(float2) * static_cast<size_t>(grad_partials(n)))
+    if (workspace == nullptr || workspace_bytes < sizeof(double) * static_cast<size_t>(grad_partials(n)))
         return TPMLP_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(norm) & 3u) || !aligned16(workspace)) return TPMLP_ERR_ALIGN;
     DeviceInfo dev;
     if (int rc = enter(dev)) return rc;
-    const cudaError_t e = launch_grad_clip(grads, out, sizes, dtypes, n, max_norm, norm, static_cast<float2*>(workspace),
+    const cudaError_t e = launch_grad_clip(grads, out, sizes, dtypes, n, max_norm, norm, static_cast<double*>(workspace),
                                            static_cast<cudaStream_t>(stream), &t_last_launches);
     return e == cudaSuccess ? TPMLP_OK : fail_cuda(e);
 }
@@ -2603,7 +2603,7 @@ int grad_clip(const void* const* grads, void* const* out, const long long* sizes
 
 TPMLP_API size_t tp_grad_workspace_bytes(int n) {
     if (n < 0 || n > kMostGrads) return 0;
-    return sizeof(float2) * static_cast<size_t>(grad_partials(n));
+    return sizeof(double) * static_cast<size_t>(grad_partials(n));
 }
 
 TPMLP_API int tp_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes, int n, float* norm,

@@ -10,10 +10,11 @@
 // table of tensors travels in the kernels' parameters: nothing is copied to the
 // device, and a captured call holds its own table.
 //
-// A square of a value above 2^63 overflows fp32 although the norm need not; a second
-// sum, of the values times 2^-64, takes over when the first is not finite.  (A batch of
-// values whose squares stay finite gives the second sum its own sum times 2^-128, so only
-// a batch that overflows is gone through twice.)  The partial sums are added in 64 bits.
+// A square above 2^63 overflows fp32, one below 2^-75 is lost, although the norm need
+// not be: beside the sum of the squares run those of the values times 2^-64 and times
+// 2^100, of which a CTA takes the one that its sum calls for.  (A batch whose squares
+// stay in range adds its own sum times 2^-128 and 2^200 to them, so only a batch outside
+// is gone through again.)  The CTAs' sums are added in 64 bits.
 //
 // The clipping pass walks the pieces backwards: the norm's pass has left the last
 // ones in L2.
@@ -35,9 +36,11 @@ namespace {
 constexpr int kClipThreads = 256;
 constexpr int kPieceBytes = 32768;  // eight 16-byte words a thread
 constexpr int kWords = kPieceBytes / 16 / kClipThreads;
-constexpr float kDown = 5.421010862427522e-20f;  // 2^-64
+constexpr float kDown = 5.421010862427522e-20f;   // 2^-64
+constexpr float kUp = 1.2676506002282294e30f;      // 2^100
 constexpr float kDownSquared = 2.938735877055719e-39f;  // 2^-128
-constexpr double kUpSquared = 3.402823669209385e38;     // 2^128
+constexpr float kLow = 7.888609052210118e-31f;     // 2^-100: a batch's sum below it goes through again
+constexpr float kLowSum = 8.271806125530277e-25f;  // 2^-80: a CTA's
 
 template <int MOST>
 struct Table {
@@ -88,22 +91,26 @@ __device__ __forceinline__ uint64_t pair_of_word(uint32_t w, __half) {
     return r;
 }
 
+enum Scale { kAsIs, kScaleDown, kScaleUp };
+
 struct Sums {
-    float plain, down;
-    // a batch's sum of squares, or, where that is not finite, `again`(2^-64)'s
+    float plain, down, up;
+    // a batch's sum of squares, and it or what `squares` gives for the scaled values
     template <typename F>
-    __device__ __forceinline__ void add(float batch, F&& again) {
+    __device__ __forceinline__ void add(F&& squares) {
+        const float batch = squares(std::integral_constant<Scale, kAsIs>{});
         plain += batch;
-        down += batch < INFINITY ? batch * kDownSquared : again();
+        down += batch < INFINITY ? batch * kDownSquared : squares(std::integral_constant<Scale, kScaleDown>{});
+        up += batch < kLow ? squares(std::integral_constant<Scale, kScaleUp>{}) : batch * kUp * kUp;
     }
 };
 
-// The sum of the squares of a 16-byte word's values (times 2^-64 where DOWN) in pairs.
-template <typename T, bool DOWN>
+// The sum of the squares of a 16-byte word's (scaled) values in pairs.
+template <typename T, Scale SCALE>
 __device__ __forceinline__ void add_squares(uint64_t (&acc)[2], const uint4& w) {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-    uint64_t down;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(down) : "f"(kDown));
+    uint64_t factor;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(factor) : "f"(SCALE == kScaleDown ? kDown : kUp));
 #pragma unroll
     for (int i = 0; i < (sizeof(T) == 4 ? 2 : 4); ++i) {
         uint64_t x;
@@ -111,7 +118,7 @@ __device__ __forceinline__ void add_squares(uint64_t (&acc)[2], const uint4& w) 
             asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
         else
             x = pair_of_word(v[i], T{});
-        if (DOWN) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(down));
+        if (SCALE != kAsIs) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(factor));
         asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(acc[i & 1]) : "l"(x));
     }
 }
@@ -123,20 +130,20 @@ __device__ __forceinline__ float sum_of(const uint64_t (&acc)[2]) {
     return (a + b) + (c + d);
 }
 
-template <typename T, bool DOWN>
+template <typename T, Scale SCALE>
 __device__ __forceinline__ float squares_of(const uint4 (&w)[kWords]) {
     uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) add_squares<T, DOWN>(acc, w[i]);
+    for (int i = 0; i < kWords; ++i) add_squares<T, SCALE>(acc, w[i]);
     return sum_of(acc);
 }
 
-template <bool DOWN>
+template <Scale SCALE>
 __device__ __forceinline__ float squares_of(const float (&v)[8]) {
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float x = DOWN ? v[k] * kDown : v[k];
+        const float x = SCALE == kAsIs ? v[k] : v[k] * (SCALE == kScaleDown ? kDown : kUp);
         sum = fmaf(x, x, sum);
     }
     return sum;
@@ -161,15 +168,15 @@ __device__ __forceinline__ void sum_piece(Sums& s, const T* p, long long n) {
                                                                                : make_uint4(0u, 0u, 0u, 0u);
             const int at = words * VEC + threadIdx.x;  // the last, incomplete word
             float v[8] = {at < here ? wide(p[at]) : 0.0f};
-            s.add(squares_of<false>(v), [&] { return squares_of<true>(v); });
+            s.add([&](auto scale) { return squares_of<decltype(scale)::value>(v); });
         }
-        s.add(squares_of<T, false>(w), [&] { return squares_of<T, true>(w); });
+        s.add([&](auto scale) { return squares_of<T, decltype(scale)::value>(w); });
     } else {
         for (int i = threadIdx.x; i < here; i += 8 * kClipThreads) {
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = i + k * kClipThreads < here ? wide(p[i + k * kClipThreads]) : 0.0f;
-            s.add(squares_of<false>(v), [&] { return squares_of<true>(v); });
+            s.add([&](auto scale) { return squares_of<decltype(scale)::value>(v); });
         }
     }
 }
@@ -249,11 +256,11 @@ __device__ __forceinline__ float cta_sum(float v, float* s) {
 
 template <int MOST>
 __global__ void __launch_bounds__(kClipThreads, 4)
-    grad_squares_kernel(const __grid_constant__ Table<MOST> t, float2* partial) {
+    grad_squares_kernel(const __grid_constant__ Table<MOST> t, double* partial) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float scratch[kClipThreads / 32];
-    Sums s{0.0f, 0.0f};
+    Sums s{0.0f, 0.0f, 0.0f};
     const unsigned pieces = t.first[t.count];
     for (unsigned c = blockIdx.x; c < pieces; c += gridDim.x) {
         const int i = find_tensor(t, c);
@@ -271,38 +278,27 @@ __global__ void __launch_bounds__(kClipThreads, 4)
     }
     const float plain = cta_sum(s.plain, scratch);
     const float down = cta_sum(s.down, scratch);
-    if (threadIdx.x == 0) partial[blockIdx.x] = make_float2(plain, down);
+    const float up = cta_sum(s.up, scratch);
+    if (threadIdx.x == 0)
+        partial[blockIdx.x] = isinf(plain) ? down * 0x1p128 : plain < kLowSum ? up * 0x1p-200 : plain;
 }
 
 // The norm from the partial sums, the same bits in every CTA that computes it.
-__device__ __forceinline__ float norm_of(const float2* partial, int parts) {
-    __shared__ double sp[kClipThreads / 32], sd[kClipThreads / 32];
-    double p = 0.0, d = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kClipThreads) {
-        const float2 v = partial[i];
-        p += v.x;
-        d += v.y;
-    }
+__device__ __forceinline__ float norm_of(const double* partial, int parts) {
+    __shared__ double sums[kClipThreads / 32];
+    double p = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kClipThreads) p += partial[i];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        p += __shfl_xor_sync(0xFFFFFFFFu, p, o);
-        d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-    }
-    if (threadIdx.x % 32 == 0) {
-        sp[threadIdx.x / 32] = p;
-        sd[threadIdx.x / 32] = d;
-    }
+    for (int o = 16; o > 0; o >>= 1) p += __shfl_xor_sync(0xFFFFFFFFu, p, o);
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = p;
     __syncthreads();
-    p = d = 0.0;
+    p = 0.0;
 #pragma unroll
-    for (int w = 0; w < kClipThreads / 32; ++w) {
-        p += sp[w];
-        d += sd[w];
-    }
-    return static_cast<float>(sqrt(isinf(p) ? d * kUpSquared : p));
+    for (int w = 0; w < kClipThreads / 32; ++w) p += sums[w];
+    return static_cast<float>(sqrt(p));
 }
 
-__global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const float2* partial, int parts, float* norm) {
+__global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const double* partial, int parts, float* norm) {
     pdl_launch_dependents();
     pdl_wait();
     const float n = norm_of(partial, parts);
@@ -311,7 +307,7 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const float2* p
 
 template <int MOST>
 __global__ void __launch_bounds__(kClipThreads, 3)
-    grad_scale_kernel(const __grid_constant__ Table<MOST> t, const float2* partial, int parts, float max_norm,
+    grad_scale_kernel(const __grid_constant__ Table<MOST> t, const double* partial, int parts, float max_norm,
                       float* norm) {
     pdl_launch_dependents();
     pdl_wait();
@@ -386,7 +382,7 @@ Table<MOST> make_table(const void* const* in, void* const* out, const long long*
 }
 
 template <int MOST>
-cudaError_t squares(const void* const* in, const long long* sizes, const int* dtypes, const Part& p, float2* partial,
+cudaError_t squares(const void* const* in, const long long* sizes, const int* dtypes, const Part& p, double* partial,
                     cudaStream_t st) {
     return launch_dependent(grad_squares_kernel<MOST>, dim3(p.grid), dim3(kClipThreads), 0, st,
                             make_table<MOST>(in, nullptr, sizes, dtypes, p), partial + p.partial);
@@ -394,7 +390,7 @@ cudaError_t squares(const void* const* in, const long long* sizes, const int* dt
 
 template <int MOST>
 cudaError_t scale(const void* const* in, void* const* out, const long long* sizes, const int* dtypes, const Part& p,
-                  const float2* partial, int parts, float max_norm, float* norm, cudaStream_t st) {
+                  const double* partial, int parts, float max_norm, float* norm, cudaStream_t st) {
     return launch_dependent(grad_scale_kernel<MOST>, dim3(p.grid), dim3(kClipThreads), 0, st,
                             make_table<MOST>(in, out, sizes, dtypes, p), partial, parts, max_norm, norm);
 }
@@ -407,7 +403,7 @@ long long grad_partials(int n) {
 }
 
 cudaError_t launch_grad_clip(const void* const* in, void* const* out, const long long* sizes, const int* dtypes, int n,
-                             float max_norm, float* norm, float2* partial, cudaStream_t st, int* launches) {
+                             float max_norm, float* norm, double* partial, cudaStream_t st, int* launches) {
     int parts = 0;
     cudaError_t e;
     for (int i = 0; i < n;) {
@@ -421,7 +417,7 @@ cudaError_t launch_grad_clip(const void* const* in, void* const* out, const long
         parts += p.grid;
     }
     if (out == nullptr || parts == 0) {
-        e = launch_dependent(grad_norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const float2*>(partial),
+        e = launch_dependent(grad_norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const double*>(partial),
                              parts, norm);
         if (e == cudaSuccess) ++*launches;
         return e;

@@ -255,11 +255,11 @@ cudaError_t launch_qk_norm_rope_backward(const QkNormRope& p, float* dgamma_q, f
                                          int* launches);
 
 // Global gradient norm, and clipping where `out` is given (grad_clip.cu).  The
-// arrays are host memory; `partial` holds grad_partials(n) float2.
+// arrays are host memory; `partial` holds grad_partials(n) doubles.
 constexpr int kClipCtas = 912;  // CTAs of a launch: 6 on each of 152 SMs
 long long grad_partials(int n);
 cudaError_t launch_grad_clip(const void* const* in, void* const* out, const long long* sizes, const int* dtypes, int n,
-                             float max_norm, float* norm, float2* partial, cudaStream_t st, int* launches);
+                             float max_norm, float* norm, double* partial, cudaStream_t st, int* launches);
 
 // `grid` is the number of work units wanted (CTAs, or CTA pairs when PAIR).
 // With static units it is clipped to what can be resident at once, so the
