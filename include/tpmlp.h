@@ -664,8 +664,8 @@ int tp_attn_packed_backward(const tpmlp_bf16* Q, long long ldq, const tpmlp_bf16
  * tokens ld* values apart (heads * d <= ld* < 2^31, whole 16-byte pieces); gamma_q,
  * gamma_k [d] of that type, shared by the heads; positions int32 [T] (4-byte
  * aligned, any values); rstd float32 [T, nh + nkv] (queries first), saved for
- * the backward pass.  Statistics and rotation are fp32, the angles as near as in
- * 64 bits at any position.  Rules (else TPMLP_ERR_SHAPE): 0 <= T <= 2^30, nh, nkv >= 1,
+ * the backward pass.  Statistics and rotation are fp32; the angles are right to
+ * 2^-33 of a turn at any position (theta >= 1e-10) before they are rounded to it.  Rules (else TPMLP_ERR_SHAPE): 0 <= T <= 2^30, nh, nkv >= 1,
  * d % 16 == 0, 32 <= d <= 256, rot % 16 == 0, 0 <= rot <= d, 1e-300 <= theta <= 1e300,
  * eps finite and > 0, T (nh + nkv) <= 2^36. */
 int tp_qk_norm_rope_forward(const void* Q, long long ldq, const void* K, long long ldk,

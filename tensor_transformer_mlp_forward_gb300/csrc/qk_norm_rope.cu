@@ -12,8 +12,8 @@
 //   dx = rstd (g gamma - xhat mean(g gamma xhat))
 //
 // Angles: theta^(-2i/rot) / 2 pi turns a position as a 64-bit fixed-point fraction
-// f; p f modulo 2^64 is the angle's fraction of a turn, exact but for f's rounding
-// (2^-53 relative), so far positions lose nothing to the size of p.  The nearest
+// f, right to 2^-64; p f modulo 2^64 is the angle's fraction of a turn, right to
+// 2^-64 |p| <= 2^-33, well below fp32's last bit of an eighth of a turn.  The nearest
 // quarter turn comes off as an integer, and the rest (at most an eighth of a turn)
 // is rounded to fp32 once.
 //
@@ -523,17 +523,46 @@ void deal_ctas(int T, int nh, int nkv, long long run, int most, int (&ctas)[2]) 
     ctas[1] = static_cast<int>(most - c < k ? most - c : k);
 }
 
+// Numbers of some 106 bits as sums of two doubles: products and sums whose rounding is
+// caught exactly (Dekker 1971, with a fused multiply-add).
+struct Wide {
+    double hi, lo;
+};
+Wide fast_sum(double a, double b) {  // |a| >= |b|
+    const double s = a + b;
+    return {s, b - (s - a)};
+}
+Wide times(Wide a, Wide b) {
+    const double p = a.hi * b.hi;
+    return fast_sum(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+
+// |x| modulo 1, times 2^64
+unsigned long long fraction(double x) {
+    return static_cast<unsigned long long>(std::nearbyint((x - std::floor(x)) * 0x1p64));
+}
+
+// theta^(-2 i / rot) / 2 pi modulo 1, as powers of r = theta^(-1 / n), n = rot / 2, in 106
+// bits: from pow's r by one Newton step towards theta r^n = 1.
 QkTurns make_turns(double theta, int rot) {
-    // theta^(-2 i / rot) as a product of two powers, for 16 + 8 of them in place of 128
-    // (half of a call's host time), two roundings in place of one
     QkTurns t{};
-    double low[8], high[16];
-    for (int i = 0; i < 8; ++i) low[i] = i < rot / 2 ? std::pow(theta, -2.0 * i / rot) : 0.0;
-    for (int i = 0; 8 * i < rot / 2; ++i) high[i] = std::pow(theta, -16.0 * i / rot) * 0.15915494309189535;  // 1 / (2 pi)
-    for (int i = 0; i < rot / 2; ++i) {
-        double f = high[i / 8] * low[i % 8];
-        f -= std::floor(f);
-        t.f[i] = static_cast<unsigned long long>(f * 18446744073709551616.0);  // f < 1
+    const int n = rot / 2;
+    if (n == 0) return t;
+    const double r0 = std::pow(theta, -1.0 / n);
+    Wide all{theta, 0.0}, square{r0, 0.0};
+    for (int m = n; m > 0; m >>= 1) {
+        if (m & 1) all = times(all, square);
+        if (m > 1) square = times(square, square);
+    }
+    const Wide r = fast_sum(r0, -r0 * (((all.hi - 1.0) + all.lo) / n));
+    // 16 + 8 powers, then products of two
+    Wide low[9], high{0.15915494309189535, -9.839338337591243e-18};  // 1 / (2 pi)
+    low[0] = {1.0, 0.0};
+    for (int i = 1; i < 9; ++i) low[i] = times(low[i - 1], r);
+    for (int i = 0; i < n; ++i) {
+        const Wide f = times(high, low[i % 8]);
+        t.f[i] = fraction(f.hi) + (f.lo < 0.0 ? 0ull - fraction(-f.lo) : fraction(f.lo));
+        if (i % 8 == 7) high = times(high, low[8]);
     }
     return t;
 }
