@@ -160,21 +160,24 @@ __device__ __forceinline__ void store8(T* p, const uint64_t (&v)[4]) {
     }
 }
 
-// cos and sin of 2 pi (p f / 2^64 mod 1).
-// In the 16-bit types by the fast sine and cosine, whose error on an eighth of a turn
-// (2^-21) is nothing beside the rounding of the result.
-template <bool FAST>
+// cos and sin of 2 pi (p f / 2^64 mod 1), the rest behind the nearest quarter turn
+// rounded to fp32 once, whatever its size.  For the 16-bit types by Taylor's series, whose
+// first missing terms are below 2^-21 and 2^-25 at an eighth of a turn and fall with the
+// angle, so small sines keep all of their digits: backward, 58 us where sincospi takes 60
+// (8192 tokens of 40 heads of 128).
+template <bool SERIES>
 __device__ __forceinline__ float2 turn(int p, unsigned long long f) {
     const unsigned long long a = static_cast<unsigned long long>(static_cast<long long>(p)) * f;
     const unsigned long long quarter = (a + (1ull << 61)) >> 62;  // nearest quarter turn, modulo 4
     const long long rest = static_cast<long long>(a - (quarter << 62));  // +- 2^61
-    // in half turns, for cospi and sinpi
-    const float x = static_cast<float>(static_cast<int>(rest >> 31)) * 4.656612873077393e-10f * 0.5f;
     float s, c;
-    if constexpr (FAST)
-        __sincosf(x * 3.14159265358979f, &s, &c);
-    else
-        sincospif(x, &s, &c);
+    if constexpr (SERIES) {
+        const float r = __ll2float_rn(rest) * (3.14159265358979f * 0x1p-63f), r2 = r * r;
+        s = fmaf(r * r2, fmaf(r2, fmaf(r2, -1.0f / 5040.0f, 1.0f / 120.0f), -1.0f / 6.0f), r);
+        c = fmaf(r2, fmaf(r2, fmaf(r2, fmaf(r2, 1.0f / 40320.0f, -1.0f / 720.0f), 1.0f / 24.0f), -0.5f), 1.0f);
+    } else {
+        sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);  // half turns
+    }
     const bool swap = quarter & 1ull;
     const float cc = swap ? s : c, ss = swap ? c : s;
     const unsigned q = static_cast<unsigned>(quarter) & 3u;
@@ -208,10 +211,10 @@ struct TurnsOf {
         if (tok >= per) tok = 1 << 30;  // beyond every run
     }
     // cos and sin of the tokens [t0, t0 + tokens) into shared memory, [token][2][rot / 2]
-    template <bool FAST>
+    template <bool SERIES>
     __device__ __forceinline__ void fill(float* table, const int* positions, int t0, int tokens, int rot) const {
         for (int t = tok; t < tokens; t += per) {
-            const float2 cs = turn<FAST>(__ldg(positions + t0 + t), f);
+            const float2 cs = turn<SERIES>(__ldg(positions + t0 + t), f);
             table[t * rot + j] = cs.x;
             table[t * rot + rot / 2 + j] = cs.y;
         }
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kQkThreads, PER_SM)
     pdl_wait();
     extern __shared__ __align__(16) float table[];
     constexpr int GROUPS = kQkThreads / LANES, RUN = GROUPS * UNITS;
-    constexpr bool FAST = sizeof(T) == 2;
+    constexpr bool SERIES = sizeof(T) == 2;
     const int heads = a.all_heads, nh = a.job[0].heads, d = a.d;
     const int u = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     const Place pl = place_of(u, d, a.rot);
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kQkThreads, PER_SM)
         }
         from.move(group_t, group_h, heads);
     }
-    mine.fill<FAST>(table, a.positions, t0, min(t0 + (h0 + RUN - 1) / heads, a.T - 1) - t0 + 1, a.rot);
+    mine.fill<SERIES>(table, a.positions, t0, min(t0 + (h0 + RUN - 1) / heads, a.T - 1) - t0 + 1, a.rot);
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < UNITS; ++n) {
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kQkThreads, PER_SM)
     pdl_wait();
     extern __shared__ __align__(16) float tables[];
     constexpr int GROUPS = kQkThreads / LANES, RUN = GROUPS * UNITS;
-    constexpr bool FAST = sizeof(T) == 2;
+    constexpr bool SERIES = sizeof(T) == 2;
     const bool keys = static_cast<int>(blockIdx.x) >= a.ctas[0];
     const QkJob& j = a.job[keys];
     const int heads = j.heads, d = a.d;
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kQkThreads, PER_SM)
         }
     };
     auto fill = [&](int k) {
-        mine.fill<FAST>(tables + (k & 1) * table_floats, a.positions, at0.t, min(last.t, a.T - 1) - at0.t + 1, a.rot);
+        mine.fill<SERIES>(tables + (k & 1) * table_floats, a.positions, at0.t, min(last.t, a.T - 1) - at0.t + 1, a.rot);
     };
     load(at);
     fill(0);

@@ -58,3 +58,21 @@ def test_far_positions(d, rot, theta, first):
     x[..., :rot // 2] *= first
     got, want, size = _rotated(x, FAR, rot, theta)
     assert ((got - want).abs() <= ABSOLUTE * size).all()
+
+
+@pytest.mark.parametrize("dt,half", [(torch.float32, 2.0 ** -24), (torch.float16, 2.0 ** -11), (torch.bfloat16, 2.0 ** -8)])
+@pytest.mark.parametrize("d,rot,theta", [(256, 256, 1e6), (128, 64, 1e4)])
+def test_small_angles_keep_their_digits(dt, half, d, rot, theta):
+    # a value that is the sine of its angle alone, angles from 1e-6 on
+    positions = (0, 1, -1, 2, 3, 7, 100, -1000, 65537)
+    x = torch.ones(len(positions), 1, d, dtype=dt)
+    x[..., :rot // 2] = 0.0
+    got, want, size = _rotated(x, positions, rot, theta)
+    # the angle's rounding and the result's product, 2^-24 each, the sine's two last bits
+    # (2^-22 of it), and the frequency's 2^-64 of a turn (with the reduction's, twice);
+    # then the result's own, half a step of a normal value or of the smallest one
+    slack = 2 * 2.0 ** -24 + 2.0 ** -22
+    tiny = {torch.float32: 2.0 ** -150, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}[dt]
+    bound = (half * (1 + 2.0 ** -10) + slack) * want.abs() + tiny
+    bound += size * (4 * math.pi * 2.0 ** -64 * torch.tensor(positions).abs().double())[:, None]
+    assert ((got - want).abs() <= bound).all()
