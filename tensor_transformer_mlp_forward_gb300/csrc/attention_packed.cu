@@ -583,12 +583,12 @@ cudaError_t launch_packed_forward(const CUtensorMap& q, const CUtensorMap& k, co
     const int tile = a.pair_heads ? 128 : 256;
     // the plan's scans cross the CTA's warps: few of them where there is little to plan
     // (a prompt of one token: 12.0 us of device time with 1024 threads, 9.9 with 256)
-    const unsigned planners = p.T / tile + p.nb <= 512 ? 256 : 1024;
+    const unsigned planners = packed_attn_entries(p.nb, p.T, tile) <= 512 ? 256 : 1024;
     cudaError_t e = launch_dependent(packed_plan_kernel, dim3(1), dim3(planners), 0, st, p.cu_seqlens, p.nb, p.T, tile,
                                      p.entries, p.plan, p.ranks, p.status);
     if (e != cudaSuccess) return e;
     ++*launches;
-    const unsigned grid = persistent_grid((static_cast<long long>(p.T) / tile + p.nb) * a.units, p.sms);
+    const unsigned grid = persistent_grid(packed_attn_entries(p.nb, p.T, tile) * a.units, p.sms);
     switch (d) {
         case 64: e = launch_fwd<64>(q, k, v, a, grid, st); break;
         case 96: e = launch_fwd<96>(q, k, v, a, grid, st); break;

@@ -1112,7 +1112,7 @@ cudaError_t launch_bwd(const CUtensorMap& q128, const CUtensorMap& do128, const 
                                      p.plan, p.ranks, p.status);
     if (e != cudaSuccess) return e;
     ++*launches;
-    const long long most = static_cast<long long>(p.T) / 128 + p.nb;  // entries at most
+    const long long most = packed_attn_entries(p.nb, p.T, 128);
     auto grid = [&](long long heads) {
         return dim3(static_cast<unsigned>(most * heads < p.sms ? most * heads : p.sms));
     };

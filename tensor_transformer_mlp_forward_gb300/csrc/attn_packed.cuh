@@ -45,7 +45,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
 }
 
 // One CTA (whole warps).  entries: {first row, length, rank - 1, tiles of the
-// sequence}; `ranks` holds T / tile + 2 words, used beyond kPlanShared ranks.
+// sequence}, packed_attn_entries(nb, T, tile) at most; `ranks` holds
+// packed_attn_ranks(T) words, used beyond kPlanShared ranks.
 // Offsets that leave [0, T] or fall make an empty list and set the device
 // status word.
 __device__ __forceinline__ void plan_block(const int* __restrict__ cu, int nb, int T, int tile,

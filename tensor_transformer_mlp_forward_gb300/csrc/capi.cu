@@ -2292,7 +2292,7 @@ int check_packed(int nb, int T, int nh, int nkv, int d, float scale) {
     if (nb < 0 || T < 0 || nb > kMostTokens || T > kMostTokens || nh < 1 || nkv < 1 || nh % nkv != 0 ||
         !attn_head_dim_ok(d) || !(scale > 0.0f) || scale > 2.0e38f)  // times log2(e) in fp32 too
         return TPMLP_ERR_SHAPE;
-    if (1LL * nh * d >= (1LL << 31) || (T / 128 + 1LL * nb) * nh >= (1LL << 31) || 1LL * T * nh > (1LL << 36))
+    if (1LL * nh * d >= (1LL << 31) || packed_attn_entries(nb, T, 128) * nh >= (1LL << 31) || 1LL * T * nh > (1LL << 36))
         return TPMLP_ERR_SHAPE;
     return TPMLP_OK;
 }
@@ -2311,11 +2311,10 @@ struct PackedLayout {
 
 PackedLayout packed_layout(int nb, int T, int nh, int nkv, int d, bool backward) {
     auto front = [&](int tokens) {
-        const size_t tiles = static_cast<size_t>(tokens) / 128;
         PackedLayout L;
         L.entries = 256;
-        L.ranks = align256(L.entries + sizeof(int4) * (tiles + nb));
-        L.delta = align256(L.ranks + sizeof(int) * (tiles + 2));
+        L.ranks = align256(L.entries + sizeof(int4) * static_cast<size_t>(packed_attn_entries(nb, tokens, 128)));
+        L.delta = align256(L.ranks + sizeof(int) * static_cast<size_t>(packed_attn_ranks(tokens)));
         L.parts = align256(L.delta + sizeof(float) * static_cast<size_t>(tokens) * nh);
         return L;
     };

@@ -199,13 +199,20 @@ cudaError_t launch_attn_backward(const CUtensorMap& tm_qkv128, const CUtensorMap
 // Packed causal attention with grouped heads (attention_packed.cu,
 // attention_packed_backward.cu): Q [T, nh, d], K, V [T, nkv, d] through 3-D maps
 // {columns, T, 1} with 64-column boxes.  Head dims 64, 96, 128, 160.
+//
+// Tiles of a plan at most: a sequence of n tokens has n / tile whole ones, all sequences
+// together no more than T / tile, and each one more that its end cuts.
+inline long long packed_attn_entries(int nb, int T, int tile) { return T / tile + 1LL * nb; }
+// Counters of the plan's ranks 0 .. T / 128 + 1 (a sequence's tiles at most).
+inline int packed_attn_ranks(int T) { return T / 128 + 2; }
+
 struct PackedAttn {
     const int* cu_seqlens;       // [nb + 1], device
     int nb, T, nh, nkv, sms;
     float scale;
-    int4* entries;               // scratch: the plan (packed_attn_entries(nb, T, .) int4,
-    unsigned* plan;              // 4 header words, T / 128 + 2 ranks)
-    int* ranks;
+    int4* entries;               // scratch: the plan, packed_attn_entries(nb, T, 128) tiles,
+    unsigned* plan;              // 4 header words
+    int* ranks;                  // and packed_attn_ranks(T) counters
     __nv_bfloat16* O;            // forward: [T, nh, d]
     float* lse;                  // forward: [nh, T], log2 domain
     const __nv_bfloat16* O_in;   // backward: the forward's O and lse, and dO [T, nh, d]
