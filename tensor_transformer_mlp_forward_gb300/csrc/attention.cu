@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (x == 1 && !it.has_b) continue;  // no B tile in this item
             const int q = it.q0 + 128 * x + r;
             const int jl = it.last[x];
-            float m = -INFINITY, l = 0.0f;
+            // (finite: scores that are all -inf so far weigh 2^-inf, not 2^(-inf + inf))
+            float m = -3.4e38f, l = 0.0f;
             for (int j = 0; j <= jl; ++j) {
                 if (!warp_wait_bounded(&s_full[x], static_cast<uint32_t>(gxl + j) & 1u, abort_flag,
                                        a.status, 0x10C + x)) {
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // keys in this tile are all masked (rows past the sequence end
                 // in a 64-key tile) keeps its reference.
                 const float m_new = fmaxf(m, mx * a.scale2);
-                const bool move = (j == 0 && m_new > -INFINITY) || m_new > m + kRescaleLog2;
+                const bool move = j == 0 || m_new > m + kRescaleLog2;
                 const float alpha = move ? ex2(m - m_new) : 1.0f;
                 if (move) m = m_new;
                 uint64_t rs2[4];
