@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kPackedFwdThreads, 1)
             const int q = first_q + lane;
             const int head = x ? it.head[1] : it.head[0];
             const int jl = x ? it.last[1] : it.last[0];
-            float m = -INFINITY, l = 0.0f;
+            // (finite: scores that are all -inf so far weigh 2^-inf, not 2^(-inf + inf))
+            float m = -3.4e38f, l = 0.0f;
             for (int j = 0; j <= jl; ++j) {
                 const int k0 = j * BKV;
                 if (!warp_wait(&s_full[x], static_cast<uint32_t>(gxl + j) & 1u, abort_flag,
@@ -460,15 +461,13 @@ __global__ void __launch_bounds__(kPackedFwdThreads, 1)
                 // more than 2^8, so the O rescale below is rare.  A row whose
                 // keys in this tile are all masked keeps its reference.
                 const float m_new = fmaxf(m, mx * a.scale2);
-                const bool move = (j == 0 && m_new > -INFINITY) || m_new > m + kRescaleLog2;
+                const bool move = j == 0 || m_new > m + kRescaleLog2;
                 const float alpha = move ? ex2(m - m_new) : 1.0f;
                 if (move) m = m_new;
                 uint64_t rs2[4];
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) rs2[kk] = 0ull;  // (0.0f, 0.0f)
-                // (a row whose scores so far are all -inf: weights of 0, not of -inf + inf)
-                const float from = fmaxf(m, -3.4e38f);
-                const uint64_t scale2 = f32x2(a.scale2, a.scale2), neg_m = f32x2(-from, -from);
+                const uint64_t scale2 = f32x2(a.scale2, a.scale2), neg_m = f32x2(-m, -m);
                 // P_x, packed bf16, over the first columns of S_x (already read)
                 if (live > SCH) {
 #pragma unroll
