@@ -622,7 +622,8 @@ int tp_attn_backward(const tpmlp_bf16* dY, const tpmlp_bf16* X, const tpmlp_bf16
  * nh % nkv == 0, d in {64, 96, 128, 160}, 0 < scale <= 2e38 (1/sqrt(d) as a
  * rule), (T / 128 + nb) nh < 2^31, T nh <= 2^36.  nb == 0 or T == 0 does nothing.
  * A token's infinities and NaN reach no other sequence; within its own they may
- * reach tokens of its block of 128 that do not see it. */
+ * reach tokens of its block of 128 that do not see it.  A token all of whose scores are
+ * -inf has no softmax: O is NaN, lse -inf. */
 
 /* Bytes of scratch tp_attn_packed_forward needs (contents on entry do not
  * matter): the list of work items that the call makes on its stream.  What a batch
@@ -713,7 +714,7 @@ int tp_grad_norm(const void* const* grads, const long long* sizes, const int* dt
  * types.  out[i] may be grads[i] (clipped in place); otherwise no output may
  * share memory with another tensor (TPMLP_ERR_SHAPE, as max_norm that is not
  * > 0).  A NaN norm makes every output NaN; an infinite one zeroes the finite
- * values. */
+ * values (with an infinite max_norm too, every output is NaN). */
 int tp_grad_clip(const void* const* grads, void* const* out, const long long* sizes,
                  const int* dtypes, int n, float max_norm, float* norm, void* workspace,
                  size_t workspace_bytes, void* stream);

@@ -1025,7 +1025,9 @@ def tp_attn_packed_forward(Q, K, V, cu_seqlens, scale=None, O=None, lse=None, wo
     cu_seqlens[i + 1] - 1 (int32, on the device).  Q [T, nh, d], K, V [T, nkv,
     d] may be parts of one projection's rows; query head j reads head j // (nh
     // nkv) of K and V.  scale: 1 / sqrt(d) unless given.  Tokens in no
-    sequence are left as they are (in a fresh O: uninitialised)."""
+    sequence are left as they are (in a fresh O: uninitialised), and all of them
+    where the offsets fall or leave [0, T]: they are read on the device, so only
+    device_status() tells."""
     T, nh, nkv, d = _packed_shape(Q, K)
     dev = _device_of(Q)
     qp, ldq = _heads(Q, "Q", (T, nh, d), _BF16, dev)
@@ -1052,7 +1054,9 @@ def tp_attn_packed_backward(Q, K, V, O, lse, dO, cu_seqlens, scale=None, dQ=None
     """dQ [T, nh, d], dK, dV [T, nkv, d] (bf16) of tp_attn_packed_forward given
     dO; dK and dV are summed over the query heads that share them.  dQ, dK and
     dV may be parts of one gradient's rows.  Tokens in no sequence are left as
-    they are (in fresh outputs: uninitialised)."""
+    they are (in fresh outputs: uninitialised), and all of them where the offsets
+    fall or leave [0, T] (device_status()).  A workspace of the size for the
+    largest batch serves every one of no more sequences and tokens."""
     T, nh, nkv, d = _packed_shape(Q, K)
     dev = _device_of(Q)
     qs, ks = (T, nh, d), (T, nkv, d)

@@ -8,8 +8,9 @@
 //
 // in one pass over the keys with a running maximum and sum, in the log2 domain
 // (u = scale log2(e) q.k, P = 2^(u - m) / l, lse = m + log2(l)).  S, l and O are
-// fp32; P is rounded to bf16 where it becomes an operand of P V, which the
-// rounding of O to bf16 covers.
+// fp32; P is rounded to bf16 where it becomes an operand of P V, as the tensor cores
+// take it beside a bf16 V.  That leaves O 1.2 to 1.35 times as far from 64 bits (in the
+// 2-norm) as its own rounding to bf16 alone.
 //
 // The kernel is that of attention.cu (two 128-query tiles A and B in ping-pong,
 // S and O in tensor memory, P written back over S as the A operand of P V) with
@@ -20,9 +21,9 @@
 // both busy; else two adjacent tiles of one head.
 //
 // Long sequences are bound by the tensor cores and the softmax between their products
-// (16384 tokens, 16 heads on 2 of 128: 661-690 us, 1600-1660 TFLOP/s), short ones by an
+// (16384 tokens, 16 heads on 2 of 128: 641-690 us, 1590-1710 TFLOP/s), short ones by an
 // item's chain of load, S, softmax, P V and store (8 x 1024 tokens, 32 heads on 8 of 128:
-// 70.5 us; 37 sequences in 8191 tokens, 20 heads of 64: 48 us).  For the latter neither a
+// 70.7 us; 37 sequences in 8191 tokens, 20 heads of 64: 48 to 50 us).  For the latter neither a
 // deeper ring (50.9 against 49.3 us) nor a second place for O (49.7 against 48.6) helped.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -54,3 +54,9 @@ def test_sizes_of_every_kind_together():
         small[77] = bad
         got = float(binding.tp_grad_norm([small]))
         assert math.isnan(got) if math.isnan(bad) else math.isinf(got)
+
+
+def test_an_infinite_norm_and_an_infinite_limit():
+    grads = [torch.ones(5000, dtype=BF, device="cuda"), torch.full((3,), math.inf, device="cuda")]
+    norm, out = binding.tp_grad_clip(grads, math.inf)
+    assert math.isinf(float(norm)) and all(torch.isnan(x.float()).all() for x in out)

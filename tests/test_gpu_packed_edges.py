@@ -40,7 +40,7 @@ def test_first_keys_of_no_weight(nh, nkv, d, n, fill):
     assert ((lse.double().cpu()[:, rows] - lr).abs() <= 2.0 ** -11 + 2.0 ** -21 * lr.abs()).all()
     if fill == -math.inf:
         # rows without a finite score have no softmax
-        assert torch.isnan(O.cpu()[~rows].float()).all()
+        assert torch.isnan(O.cpu()[~rows].float()).all() and (lse.cpu()[:, ~rows] == -math.inf).all()
         return
     # dQ of the other rows (dK and dV sum over all of them)
     Oall, lall, _ = ref.attention(q, k, v, cu, d ** -0.5)
